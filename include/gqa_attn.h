@@ -65,7 +65,8 @@ typedef enum {
     GQA_ERR_UNSUPPORTED = 2,   /* D not 128 or 256, Hkv not dividing Hq,
                                   Hq > 64, page not a power of
                                   two in [8, 256], query_rows * Hq / Hkv > 48 (E4M3 tail),
-                                  Hq / Hkv > 16 (sparse) */
+                                  Hq / Hkv > 16 (sparse), batch > 1024, Hkv * D > 1024
+                                  (block index, selection), max_sel > 2048 */
     GQA_ERR_WORKSPACE = 3,     /* no workspace registered, or it is too small */
     GQA_ERR_CUDA = 4           /* a CUDA runtime call or kernel launch failed */
 } gqa_status;
@@ -74,7 +75,7 @@ typedef enum {
 #define GQA_DEVERR_WAIT_TIMEOUT 0x1u  /* a pipeline wait exceeded its limit; output invalid */
 #define GQA_DEVERR_BAD_BLOCK_ID 0x2u  /* sel_idx held an id < 0 or past the row's own block */
 #define GQA_DEVERR_BAD_PAGE_ID  0x4u  /* a block-table entry was < 0 or >= num_pages */
-#define GQA_DEVERR_BAD_CTX_LEN  0x8u  /* a device-side ctx_len was < query_rows or > max_ctx_len */
+#define GQA_DEVERR_BAD_CTX_LEN  0x8u  /* a device-side ctx_len was < its rows or > max_ctx_len */
 #define GQA_DEVERR_DUP_BLOCK_ID 0x10u /* sel_idx held an id an earlier position of its row holds */
 
 /* Dense causal prefill [P1, Purpose].
@@ -245,11 +246,148 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
                                 int ctx_len, int query_rows, int Hq, int Hkv, int D, float scale,
                                 void* out, struct CUstream_st* stream);
 
+/* ---- Filling, reading back and searching the paged cache ----------------
+ *
+ * Rows of a step.  The cache write, cache read and block index entry points
+ * take the rows of a batch, packed one sequence behind the other:
+ *   row_starts    device int32 [batch + 1], ascending: sequence b owns rows
+ *                 row_starts[b] .. row_starts[b + 1] - 1 (n_b rows, 0 allowed).
+ *                 NULL: tokens / batch rows each (batch must divide tokens).
+ *   ctx_lens_dev  device int32 [batch]: the context length including these
+ *                 rows, so row j of sequence b sits at position
+ *                 ctx_lens[b] - n_b + j.  Read when the kernel runs (as
+ *                 row_starts and the tables), so a captured graph replays as
+ *                 the contexts grow.
+ *   block_tables  [batch, table_stride] int32 physical page ids;
+ *                 table_stride * page >= max_ctx_len.
+ *   tokens        rows of the launch.  Rows in front of row_starts[0] or from
+ *                 row_starts[batch] on are padding: nothing is read or written
+ *                 for them.
+ * A sequence whose context length is below n_b or above max_ctx_len is left
+ * out whole and flags GQA_DEVERR_BAD_CTX_LEN.  A block-table entry outside
+ * [0, num_pages) flags GQA_DEVERR_BAD_PAGE_ID; nothing is stored for its
+ * tokens (a read gives zeros).  Two rows must not name the same cached token
+ * (sequences that share pages): which of the two is kept is not defined.
+ * 1 <= batch <= 1024; num_pages * page < 2^31; head sizes, groupings and
+ * pages as for the attention.  None needs a workspace. */
+
+/* Types of 16-bit floats. */
+#define GQA_DTYPE_F16 0
+#define GQA_DTYPE_BF16 1
+
+/* Cache write: per-head RMS norm and position rotation of a step's queries
+ * and keys, and K and V stored into the paged E4M3 cache, in one launch.
+ *   q, k, v       [tokens, Hq | Hkv | Hkv, D] of `dtype`, D contiguous, tokens
+ *                 and heads *_token_stride / *_head_stride elements apart
+ *                 (multiples of 8), so views of one fused projection go in as
+ *                 they are.  q may be NULL (with q_out): only K and V.
+ *   q_weight, k_weight  [D] of `dtype`, 16-byte aligned: y = x /
+ *                 sqrt(mean(x^2) + eps) * weight over each head.  NULL: no norm
+ *                 of that tensor.  eps finite, >= 0.
+ *   inv_freq      device fp32 [rot_dim / 2]: pair i of the first rot_dim
+ *                 values turns by the angle position * inv_freq[i].  rot_dim:
+ *                 0 (inv_freq unused) or a multiple of 16 up to D.
+ *   interleaved   0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
+ *   q_out         [tokens, Hq, D] fp16, contiguous
+ *   kcache/vcache [num_pages, page, Hkv, D] E4M3 codes: round to nearest even
+ *                 of the value times the fp32 reciprocal of kscale / vscale
+ *                 (device fp32, > 0), +-448 beyond the range, NaN stays NaN.
+ * Norm, angle (to 2^-40 of a turn at any position) and rotation in 32 bits,
+ * one rounding at the end.  q_out and the caches must not overlap q, k or v. */
+int gqa_cache_write_e4m3(const void* q, const void* k, const void* v, int dtype,
+                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const void* q_weight, const void* k_weight, float eps,
+                         const float* inv_freq, int rot_dim, int interleaved,
+                         const float* kscale, const float* vscale, const int32_t* block_tables,
+                         int table_stride, int num_pages, int page, const int32_t* row_starts,
+                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                         int Hq, int Hkv, int D, void* q_out, uint8_t* kcache, uint8_t* vcache,
+                         struct CUstream_st* stream);
+
+/* The same over an fp16 cache: kcache/vcache [num_pages, page, Hkv, D] fp16,
+ * no scales. */
+int gqa_cache_write(const void* q, const void* k, const void* v, int dtype,
+                    int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                    const void* q_weight, const void* k_weight, float eps,
+                    const float* inv_freq, int rot_dim, int interleaved,
+                    const int32_t* block_tables, int table_stride, int num_pages, int page,
+                    const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
+                    int batch, int tokens, int Hq, int Hkv, int D, void* q_out, void* kcache,
+                    void* vcache, struct CUstream_st* stream);
+
+/* Cache read: the cached tokens the rows stand for, as dense rows (the K / V
+ * of gqa_attn_prefill for one sequence).  k_out, v_out [tokens, Hkv, D] fp16 =
+ * decode(code) * scale, rounded to nearest fp16. */
+int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
+                        const float* vscale, const int32_t* block_tables, int table_stride,
+                        int num_pages, int page, const int32_t* row_starts,
+                        const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                        int Hkv, int D, void* k_out, void* v_out, struct CUstream_st* stream);
+
+/* The same rows as they are: elem_bytes = 2 for an fp16 cache, 1 for E4M3
+ * codes (the K / V of gqa_attn_prefill_e4m3).  k_out, v_out [tokens, Hkv, D]
+ * of the cache's type. */
+int gqa_cache_read(const void* kcache, const void* vcache, int elem_bytes,
+                   const int32_t* block_tables, int table_stride, int num_pages, int page,
+                   const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
+                   int batch, int tokens, int Hkv, int D, void* k_out, void* v_out,
+                   struct CUstream_st* stream);
+
+/* Block index: the summary of every 4-token block that a row of this step
+ * finishes (a row at a position 4b + 3), from the cache's keys.
+ *   s[g, d] = (k0 + k1) + (k2 + k3) in 32 bits over the block's four tokens
+ *   (codes of an E4M3 cache), A = max |s|;
+ *   index[block, g, d] = rint(s * (127 / A)),
+ *   index_scale[block] = A * (kscale / 508)   (kscale = 1 for an fp16 cache),
+ * so that code * scale is about the block's mean key.  A block whose sums are
+ * all zero or not all finite gets zero codes and a zero scale.
+ *   index         [num_pages, page / 4, Hkv, D] int8
+ *   index_scale   [num_pages, page / 4] fp32
+ * Hkv * D <= 1024. */
+int gqa_block_index_e4m3(const uint8_t* kcache, const float* kscale, const int32_t* block_tables,
+                         int table_stride, int num_pages, int page, const int32_t* row_starts,
+                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                         int Hkv, int D, int8_t* index, float* index_scale,
+                         struct CUstream_st* stream);
+int gqa_block_index(const void* kcache, const int32_t* block_tables, int table_stride,
+                    int num_pages, int page, const int32_t* row_starts,
+                    const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                    int Hkv, int D, int8_t* index, float* index_scale,
+                    struct CUstream_st* stream);
+
+/* Block selection: the sel_idx / sel_cnt of gqa_attn_sparse_blocks for the
+ * query_rows last positions of one sequence, by the block index.
+ *   q             [query_rows, Hq, D] fp16; S[g, d] = sum of q over the query
+ *                 heads of KV head g (exact, rounded once to 32 bits); codes
+ *                 c = rint(S * (127 / max |S|)) per row (zero codes for a row
+ *                 that holds an infinity or NaN)
+ *   score(row, b) = (sum over g, d of c * index[b]) * index_scale[b]: a whole
+ *                 number, exact, times the scale in 32 bits.  A NaN score
+ *                 counts below all others.
+ * Row i at position p = ctx_len - query_rows + i sees blocks 0 .. p / 4.  It
+ * takes min(max_sel, p / 4 + 1) of them: always the first n_first and the last
+ * n_last (its own among them, n_last >= 1), and the best scores of the others,
+ * equal scores by the lower id.  sel_idx [query_rows, max_sel] holds the ids in
+ * ascending order, then -1; sel_cnt [query_rows] their number.  Only blocks
+ * finished before the row are scored.
+ * n_first + n_last <= max_sel <= 2048; Hkv * D <= 1024; num_pages * page <
+ * 2^31.  Block-table entries outside the cache read page 0 and flag
+ * GQA_DEVERR_BAD_PAGE_ID.  Workspace: gqa_workspace_bytes(
+ * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hq, D). */
+int gqa_select_blocks(const void* q, const int8_t* index, const float* index_scale,
+                      const int32_t* block_table, int num_pages, int page, int ctx_len,
+                      int query_rows, int Hq, int Hkv, int D, int max_sel, int n_first,
+                      int n_last, int32_t* sel_idx, int32_t* sel_cnt,
+                      struct CUstream_st* stream);
+
 /* Workspace kinds for gqa_workspace_bytes. */
 #define GQA_KIND_PREFILL 0
 #define GQA_KIND_PAGED_E4M3 1
 #define GQA_KIND_SPARSE 2
 #define GQA_KIND_PAGED_E4M3_BATCH 3   /* ctx_or_kv = number of sequences */
+#define GQA_KIND_SELECT_BLOCKS 4
 
 /* Bytes of workspace an entry point of `kind` needs for the given shape on
  * the current device (query_rows = Q or the tail/row count, ctx_or_kv = KV or

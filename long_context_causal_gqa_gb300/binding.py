@@ -30,6 +30,9 @@ KIND_PREFILL = 0
 KIND_PAGED_E4M3 = 1
 KIND_SPARSE = 2
 KIND_PAGED_E4M3_BATCH = 3
+KIND_SELECT_BLOCKS = 4
+DTYPE_F16 = 0
+DTYPE_BF16 = 1
 DEVERR_WAIT_TIMEOUT = 0x1
 DEVERR_BAD_BLOCK_ID = 0x2
 DEVERR_BAD_PAGE_ID = 0x4
@@ -41,6 +44,8 @@ EXPORTED = ("gqa_attn_prefill", "gqa_attn_prefill_e4m3", "gqa_attn_paged_e4m3", 
             "gqa_attn_paged_e4m3_batch",
             "gqa_attn_paged_e4m3_noalloc",
             "gqa_attn_sparse_blocks", "gqa_attn_sparse_blocks_e4m3",
+            "gqa_cache_write_e4m3", "gqa_cache_write", "gqa_cache_read_e4m3", "gqa_cache_read",
+            "gqa_block_index_e4m3", "gqa_block_index", "gqa_select_blocks",
             "gqa_workspace_bytes", "gqa_set_workspace", "gqa_get_device_error",
             "gqa_check_wait_limit", "gqa_prefill_sm_pairs", "gqa_status_string")
 
@@ -86,6 +91,25 @@ def load():
             lib.gqa_attn_sparse_blocks_e4m3.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I,
                                                         I, I, I, F, P, P]
             lib.gqa_attn_sparse_blocks_e4m3.restype = I
+            L = ctypes.c_int64
+            lib.gqa_cache_write_e4m3.argtypes = [P, P, P, I, L, L, L, L, L, L, P, P, F, P, I, I,
+                                                 P, P, P, I, I, I, P, P, I, I, I, I, I, I, P, P,
+                                                 P, P]
+            lib.gqa_cache_write_e4m3.restype = I
+            lib.gqa_cache_write.argtypes = [P, P, P, I, L, L, L, L, L, L, P, P, F, P, I, I, P, I,
+                                            I, I, P, P, I, I, I, I, I, I, P, P, P, P]
+            lib.gqa_cache_write.restype = I
+            lib.gqa_cache_read_e4m3.argtypes = [P, P, P, P, P, I, I, I, P, P, I, I, I, I, I, P,
+                                                P, P]
+            lib.gqa_cache_read_e4m3.restype = I
+            lib.gqa_cache_read.argtypes = [P, P, I, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
+            lib.gqa_cache_read.restype = I
+            lib.gqa_block_index_e4m3.argtypes = [P, P, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
+            lib.gqa_block_index_e4m3.restype = I
+            lib.gqa_block_index.argtypes = [P, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
+            lib.gqa_block_index.restype = I
+            lib.gqa_select_blocks.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P]
+            lib.gqa_select_blocks.restype = I
             lib.gqa_workspace_bytes.argtypes = [I, I, I, I, I]
             lib.gqa_workspace_bytes.restype = Z
             lib.gqa_set_workspace.argtypes = [I, P, Z]
@@ -340,3 +364,259 @@ def sparse_blocks_e4m3(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tens
                                                 float(scale), _ptr(out), _stream_ptr(stream))
     _check(st, "gqa_attn_sparse_blocks_e4m3")
     return out
+
+
+# ---- the cache write, cache read, block index and block selection ----------
+#
+# These run once a layer and step beside a single small kernel, so their
+# wrappers keep to what costs little on the host: plain integers instead of
+# ctypes objects, and no device switch when the tensors' device is current.
+
+def _refuse(what: str):
+    raise GQAError(GQA_ERR_INVALID_ARG, what)
+
+
+def _want(name: str, t, dtype, dev, dims: int):
+    """A contiguous CUDA tensor of the given type, device and dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims:
+        _refuse(f"{name} must be a {dims}-dimensional {dtype} tensor")
+    if t.device != dev:
+        _refuse(f"{name} must be on {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """One library call on the tensors' device and the given (or current) stream."""
+    idx = dev.index
+    if torch.cuda.current_device() != idx:
+        with torch.cuda.device(idx):
+            return _call(fn, dev, stream, *args)
+    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
+    st = fn(*args, s)
+    if st != GQA_OK:
+        raise GQAError(st, fn.__name__)
+
+
+def _device_of(t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse("tensors must be CUDA tensors")
+    return t.device
+
+
+def _pages(kcache, vcache, dtype, dev):
+    """Pointers of the two caches and their [pages, page, Hkv, D]."""
+    kp, vp = _want("kcache", kcache, dtype, dev, 4), _want("vcache", vcache, dtype, dev, 4)
+    if kcache.shape != vcache.shape:
+        _refuse("kcache and vcache must have the same shape")
+    return kp, vp, kcache.shape
+
+
+def _one_scale(name, t, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.numel() != 1 \
+            or t.device != dev:
+        _refuse(f"{name} must be a one-element fp32 tensor on {dev}")
+    return t.data_ptr()
+
+
+def _rows(block_tables, ctx_lens_dev, row_starts, dev):
+    """(tables, stride, row_starts, ctx_lens, batch) of the rows' sequences."""
+    bt = _want("block_tables", block_tables, torch.int32, dev, 2)
+    cl = _want("ctx_lens_dev", ctx_lens_dev, torch.int32, dev, 1)
+    batch, stride = block_tables.shape
+    if ctx_lens_dev.shape[0] != batch:
+        _refuse("one context length and table row per sequence")
+    rs = None
+    if row_starts is not None:
+        rs = _want("row_starts", row_starts, torch.int32, dev, 1)
+        if row_starts.shape[0] != batch + 1:
+            _refuse("row_starts must hold batch + 1 starts")
+    return bt, stride, rs, cl, batch
+
+
+def _cache_write(q, k, v, kcache, vcache, scales, block_tables, ctx_lens_dev, max_ctx_len,
+                 q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out, stream):
+    lib = load()
+    dev = _device_of(k)
+    dtype = k.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        _refuse("k must be fp16 or bf16")
+    kp, vp, (num_pages, page, Hkv, D) = _pages(
+        kcache, vcache, torch.float16 if scales is None else torch.uint8, dev)
+    tokens = k.shape[0]
+    strides = []
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is None:
+            strides += [0, 0]
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev \
+                or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != D or t.stride(2) != 1:
+            _refuse(f"{name} must be [tokens, heads, D] like k, with D contiguous")
+        strides += t.stride()[:2]
+    if k.shape[1] != Hkv or v.shape[1] != Hkv:
+        _refuse("k and v must have the cache's KV heads")
+    Hq = Hkv
+    qp = op = None
+    if q is not None:
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((tokens, Hq, D), dtype=torch.float16, device=dev)
+        qp, op = q.data_ptr(), _want("q_out", q_out, torch.float16, dev, 3)
+        if q_out.shape != q.shape:
+            _refuse("q_out must have q's shape")
+    elif q_out is not None:
+        _refuse("q_out without q")
+    weights = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        weights.append(None if w is None else _want(name, w, dtype, dev, 1))
+        if w is not None and w.shape[0] != D:
+            _refuse(f"{name} must hold D weights")
+    fp = rot = 0
+    if inv_freq is not None:
+        fp = _want("inv_freq", inv_freq, torch.float32, dev, 1)
+        rot = 2 * inv_freq.shape[0]
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
+    head = (qp, k.data_ptr(), v.data_ptr(), DTYPE_F16 if dtype is torch.float16 else DTYPE_BF16,
+            *strides, *weights, eps, fp, rot, 1 if interleaved else 0)
+    tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hq, Hkv, D, op, kp,
+            vp)
+    if scales is None:
+        _call(lib.gqa_cache_write, dev, stream, *head, *tail)
+    else:
+        _call(lib.gqa_cache_write_e4m3, dev, stream, *head,
+              _one_scale("kscale", scales[0], dev), _one_scale("vscale", scales[1], dev), *tail)
+    return q_out
+
+
+def cache_write_e4m3(q, k, v, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev,
+                     max_ctx_len, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                     interleaved=False, row_starts=None, q_out=None, stream=None):
+    """Norm, rotation and store of a step's rows into an E4M3 cache
+    (gqa_cache_write_e4m3): q [T,Hq,D] (or None), k/v [T,Hkv,D] fp16 or bf16,
+    views of a fused projection included; caches [pages,page,Hkv,D] uint8;
+    block_tables [B, stride], ctx_lens_dev [B], row_starts [B+1] int32.
+    Returns q_out [T,Hq,D] fp16 (None without q)."""
+    return _cache_write(q, k, v, kcache, vcache, (kscale, vscale), block_tables, ctx_lens_dev,
+                        max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts,
+                        q_out, stream)
+
+
+def cache_write(q, k, v, kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len, q_weight=None,
+                k_weight=None, eps=1e-6, inv_freq=None, interleaved=False, row_starts=None,
+                q_out=None, stream=None):
+    """cache_write_e4m3 over an fp16 cache (caches [pages,page,Hkv,D] fp16, no scales)."""
+    return _cache_write(q, k, v, kcache, vcache, None, block_tables, ctx_lens_dev, max_ctx_len,
+                        q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out,
+                        stream)
+
+
+def _cache_read(kcache, vcache, scales, block_tables, ctx_lens_dev, max_ctx_len, tokens,
+                row_starts, k_out, v_out, stream):
+    lib = load()
+    dev = _device_of(kcache)
+    dtype = kcache.dtype
+    if dtype is not torch.uint8 and (scales is not None or dtype is not torch.float16):
+        _refuse("caches must be uint8 codes" + ("" if scales else " or fp16"))
+    kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache, dtype, dev)
+    out_type = dtype if scales is None else torch.float16
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty((tokens, Hkv, D), dtype=out_type, device=dev)
+        _want(name, t, out_type, dev, 3)
+        if t.shape != (tokens, Hkv, D):
+            _refuse(f"{name} must be [tokens, Hkv, D]")
+        outs.append(t)
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
+    tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hkv, D,
+            outs[0].data_ptr(), outs[1].data_ptr())
+    if scales is None:
+        _call(lib.gqa_cache_read, dev, stream, kp, vp, kcache.element_size(), *tail)
+    else:
+        _call(lib.gqa_cache_read_e4m3, dev, stream, kp, vp, _one_scale("kscale", scales[0], dev),
+              _one_scale("vscale", scales[1], dev), *tail)
+    return outs[0], outs[1]
+
+
+def cache_read_e4m3(kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
+                    tokens, row_starts=None, k_out=None, v_out=None, stream=None):
+    """The cached tokens of a batch's rows as dense fp16 K, V [tokens,Hkv,D]
+    (gqa_cache_read_e4m3); the last tokens / B (or row_starts') of each context."""
+    return _cache_read(kcache, vcache, (kscale, vscale), block_tables, ctx_lens_dev, max_ctx_len,
+                       tokens, row_starts, k_out, v_out, stream)
+
+
+def cache_read(kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len, tokens, row_starts=None,
+               k_out=None, v_out=None, stream=None):
+    """The same rows in the cache's own type: fp16, or E4M3 codes (uint8)."""
+    return _cache_read(kcache, vcache, None, block_tables, ctx_lens_dev, max_ctx_len, tokens,
+                       row_starts, k_out, v_out, stream)
+
+
+def _block_index(kcache, kscale, e4m3, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
+                 index_scale, row_starts, stream):
+    lib = load()
+    dev = _device_of(kcache)
+    kp = _want("kcache", kcache, torch.uint8 if e4m3 else torch.float16, dev, 4)
+    num_pages, page, Hkv, D = kcache.shape
+    ip = _want("index", index, torch.int8, dev, 4)
+    sp = _want("index_scale", index_scale, torch.float32, dev, 2)
+    if index.shape != (num_pages, page // 4, Hkv, D) or index_scale.shape != index.shape[:2]:
+        _refuse("index must be [pages, page / 4, Hkv, D], index_scale [pages, page / 4]")
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
+    tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hkv, D, ip, sp)
+    if e4m3:
+        _call(lib.gqa_block_index_e4m3, dev, stream, kp, _one_scale("kscale", kscale, dev),
+              *tail)
+    else:
+        _call(lib.gqa_block_index, dev, stream, kp, *tail)
+
+
+def block_index_e4m3(kcache, kscale, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
+                     index_scale, row_starts=None, stream=None):
+    """Summaries of the 4-token blocks that a step's rows finish
+    (gqa_block_index_e4m3), into index [pages,page/4,Hkv,D] int8 and
+    index_scale [pages,page/4] fp32."""
+    _block_index(kcache, kscale, True, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
+                 index_scale, row_starts, stream)
+
+
+def block_index(kcache, block_tables, ctx_lens_dev, max_ctx_len, tokens, index, index_scale,
+                row_starts=None, stream=None):
+    """block_index_e4m3 over an fp16 cache."""
+    _block_index(kcache, None, False, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
+                 index_scale, row_starts, stream)
+
+
+def select_blocks(q, index, index_scale, block_table, ctx_len, max_sel, n_first=0, n_last=1,
+                  sel_idx=None, sel_cnt=None, stream=None):
+    """The blocks each of the last rows of one sequence attends
+    (gqa_select_blocks): q [rows,Hq,D] fp16, the sequence's block index and
+    block_table [pages of ctx_len] int32.  Returns sel_idx [rows,max_sel] and
+    sel_cnt [rows], as sparse_blocks takes them."""
+    lib = load()
+    dev = _device_of(q)
+    qp = _want("q", q, torch.float16, dev, 3)
+    ip = _want("index", index, torch.int8, dev, 4)
+    sp = _want("index_scale", index_scale, torch.float32, dev, 2)
+    bt = _want("block_table", block_table, torch.int32, dev, 1)
+    rows, Hq, D = q.shape
+    num_pages, ppb, Hkv, _ = index.shape
+    if index.shape[3] != D or index_scale.shape != index.shape[:2]:
+        _refuse("index must be [pages, page / 4, Hkv, D], index_scale [pages, page / 4]")
+    if block_table.shape[0] * ppb * 4 < ctx_len:
+        _refuse("block_table must cover ctx_len")
+    if sel_idx is None:
+        sel_idx = torch.empty((rows, max_sel), dtype=torch.int32, device=dev)
+    if sel_cnt is None:
+        sel_cnt = torch.empty((rows,), dtype=torch.int32, device=dev)
+    xp = _want("sel_idx", sel_idx, torch.int32, dev, 2)
+    cp = _want("sel_cnt", sel_cnt, torch.int32, dev, 1)
+    if sel_idx.shape != (rows, max_sel) or sel_cnt.shape != (rows,):
+        _refuse("sel_idx must be [rows, max_sel], sel_cnt [rows]")
+    with torch.cuda.device(dev):
+        ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D), dev)
+    _call(lib.gqa_select_blocks, dev, stream, qp, ip, sp, bt, num_pages, ppb * 4, ctx_len, rows,
+          Hq, Hkv, D, max_sel, n_first, n_last, xp, cp)
+    return sel_idx, sel_cnt

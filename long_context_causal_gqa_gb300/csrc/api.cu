@@ -208,6 +208,71 @@ int sparse_common(const void* q, const void* kcache, const void* vcache, const f
                          stream);
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// What the cache write, cache read and block index check of their rows and
+// pages.
+int rows_check(const CacheRows& r, int Hq, int Hkv, int D) {
+    if (!r.block_tables || !r.ctx_lens_dev) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(r.block_tables) || !aligned4(r.ctx_lens_dev) || !aligned4(r.row_starts))
+        return GQA_ERR_INVALID_ARG;
+    if (r.tokens < 1 || r.batch < 1 || r.num_pages < 1 || r.max_ctx_len < 1 || r.table_stride < 1)
+        return GQA_ERR_INVALID_ARG;
+    if (!family_ok(Hq, Hkv, D) || !page_ok(r.page) || r.batch > kMaxTailBatch)
+        return GQA_ERR_UNSUPPORTED;
+    if ((long long)r.num_pages * r.page > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if ((long long)r.max_ctx_len > (long long)r.num_pages * r.page ||
+        (long long)r.max_ctx_len > (long long)r.table_stride * r.page)
+        return GQA_ERR_INVALID_ARG;
+    if (!r.row_starts && r.tokens % r.batch) return GQA_ERR_INVALID_ARG;
+    return GQA_OK;
+}
+
+int write_common(const CacheRows& r, const CacheWriteArgs& a, cudaStream_t stream) {
+    if (!a.x[1] || !a.x[2] || !a.kcache || !a.vcache || !a.x[0] != !a.q_out)
+        return GQA_ERR_INVALID_ARG;
+    if (a.e4m3 && (!a.kscale || !a.vscale || !aligned4(a.kscale) || !aligned4(a.vscale)))
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(a.x[0]) || !aligned16(a.x[1]) || !aligned16(a.x[2]) || !aligned16(a.q_out) ||
+        !aligned16(a.kcache) || !aligned16(a.vcache) || !aligned16(a.q_weight) ||
+        !aligned16(a.k_weight))
+        return GQA_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (a.token_stride[i] % 8 || a.head_stride[i] % 8) return GQA_ERR_INVALID_ARG;
+    if (a.dtype != GQA_DTYPE_F16 && a.dtype != GQA_DTYPE_BF16) return GQA_ERR_UNSUPPORTED;
+    if (!isfinite(a.eps) || a.eps < 0.f) return GQA_ERR_INVALID_ARG;
+    if (a.rot_dim < 0 || (a.rot_dim > 0 && (!a.inv_freq || !aligned4(a.inv_freq))))
+        return GQA_ERR_INVALID_ARG;
+    const int rc = rows_check(r, a.Hq, a.Hkv, a.D);
+    if (rc != GQA_OK) return rc;
+    if (a.rot_dim > a.D || a.rot_dim % 16) return GQA_ERR_UNSUPPORTED;
+    return cache_write_launch(r, a, stream);
+}
+
+int read_common(const CacheRows& r, const void* kcache, const void* vcache, const float* kscale,
+                const float* vscale, int elem_bytes, int Hkv, int D, void* k_out, void* v_out,
+                cudaStream_t stream) {
+    if (!kcache || !vcache || !k_out || !v_out) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(kcache) || !aligned16(vcache) || !aligned16(k_out) || !aligned16(v_out))
+        return GQA_ERR_INVALID_ARG;
+    if (elem_bytes != 1 && elem_bytes != 2) return GQA_ERR_UNSUPPORTED;
+    const int rc = rows_check(r, Hkv, Hkv, D);
+    if (rc != GQA_OK) return rc;
+    return cache_read_launch(r, kcache, vcache, kscale, vscale, Hkv * D * elem_bytes, k_out,
+                             v_out, stream);
+}
+
+int index_common(const CacheRows& r, const void* kcache, const float* kscale, int Hkv, int D,
+                 int8_t* index, float* index_scale, cudaStream_t stream) {
+    if (!kcache || !index || !index_scale) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(kcache) || !aligned16(index) || !aligned4(index_scale))
+        return GQA_ERR_INVALID_ARG;
+    const int rc = rows_check(r, Hkv, Hkv, D);
+    if (rc != GQA_OK) return rc;
+    if (Hkv * D > kMaxIndexWidth) return GQA_ERR_UNSUPPORTED;
+    return block_index_launch(r, kcache, kscale, Hkv * D, index, index_scale, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -346,6 +411,109 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
                          stream);
 }
 
+int gqa_cache_write_e4m3(const void* q, const void* k, const void* v, int dtype,
+                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const void* q_weight, const void* k_weight, float eps,
+                         const float* inv_freq, int rot_dim, int interleaved,
+                         const float* kscale, const float* vscale, const int32_t* block_tables,
+                         int table_stride, int num_pages, int page, const int32_t* row_starts,
+                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                         int Hq, int Hkv, int D, void* q_out, uint8_t* kcache, uint8_t* vcache,
+                         struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    const CacheWriteArgs a = {{q, k, v}, {q_token_stride, k_token_stride, v_token_stride},
+                              {q_head_stride, k_head_stride, v_head_stride}, dtype, q_weight,
+                              k_weight, eps, inv_freq, rot_dim, interleaved, true, kscale,
+                              vscale, Hq, Hkv, D, q_out, kcache, vcache};
+    return write_common(r, a, stream);
+}
+
+int gqa_cache_write(const void* q, const void* k, const void* v, int dtype,
+                    int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                    const void* q_weight, const void* k_weight, float eps,
+                    const float* inv_freq, int rot_dim, int interleaved,
+                    const int32_t* block_tables, int table_stride, int num_pages, int page,
+                    const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
+                    int batch, int tokens, int Hq, int Hkv, int D, void* q_out, void* kcache,
+                    void* vcache, struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    const CacheWriteArgs a = {{q, k, v}, {q_token_stride, k_token_stride, v_token_stride},
+                              {q_head_stride, k_head_stride, v_head_stride}, dtype, q_weight,
+                              k_weight, eps, inv_freq, rot_dim, interleaved, false, nullptr,
+                              nullptr, Hq, Hkv, D, q_out, kcache, vcache};
+    return write_common(r, a, stream);
+}
+
+int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
+                        const float* vscale, const int32_t* block_tables, int table_stride,
+                        int num_pages, int page, const int32_t* row_starts,
+                        const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                        int Hkv, int D, void* k_out, void* v_out, struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    if (!kscale || !vscale || !aligned4(kscale) || !aligned4(vscale)) return GQA_ERR_INVALID_ARG;
+    return read_common(r, kcache, vcache, kscale, vscale, 1, Hkv, D, k_out, v_out, stream);
+}
+
+int gqa_cache_read(const void* kcache, const void* vcache, int elem_bytes,
+                   const int32_t* block_tables, int table_stride, int num_pages, int page,
+                   const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
+                   int batch, int tokens, int Hkv, int D, void* k_out, void* v_out,
+                   struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    return read_common(r, kcache, vcache, nullptr, nullptr, elem_bytes, Hkv, D, k_out, v_out,
+                       stream);
+}
+
+int gqa_block_index_e4m3(const uint8_t* kcache, const float* kscale, const int32_t* block_tables,
+                         int table_stride, int num_pages, int page, const int32_t* row_starts,
+                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                         int Hkv, int D, int8_t* index, float* index_scale,
+                         struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    if (!kscale || !aligned4(kscale)) return GQA_ERR_INVALID_ARG;
+    return index_common(r, kcache, kscale, Hkv, D, index, index_scale, stream);
+}
+
+int gqa_block_index(const void* kcache, const int32_t* block_tables, int table_stride,
+                    int num_pages, int page, const int32_t* row_starts,
+                    const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                    int Hkv, int D, int8_t* index, float* index_scale,
+                    struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    return index_common(r, kcache, nullptr, Hkv, D, index, index_scale, stream);
+}
+
+int gqa_select_blocks(const void* q, const int8_t* index, const float* index_scale,
+                      const int32_t* block_table, int num_pages, int page, int ctx_len,
+                      int query_rows, int Hq, int Hkv, int D, int max_sel, int n_first,
+                      int n_last, int32_t* sel_idx, int32_t* sel_cnt,
+                      struct CUstream_st* stream) {
+    if (!q || !index || !index_scale || !block_table || !sel_idx || !sel_cnt)
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(index) || !aligned4(index_scale) || !aligned4(block_table) ||
+        !aligned4(sel_idx) || !aligned4(sel_cnt))
+        return GQA_ERR_INVALID_ARG;
+    if (query_rows < 1 || ctx_len < query_rows || num_pages < 1 || max_sel < 1 || n_first < 0 ||
+        n_last < 1 || (long long)n_first + n_last > max_sel)
+        return GQA_ERR_INVALID_ARG;
+    if (!family_ok(Hq, Hkv, D) || !page_ok(page) || Hkv * D > kMaxIndexWidth ||
+        max_sel > kMaxSelect)
+        return GQA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if ((long long)ctx_len > (long long)num_pages * page) return GQA_ERR_INVALID_ARG;
+    return select_blocks_launch(q, index, index_scale, block_table, num_pages, page, ctx_len,
+                                query_rows, Hq, Hkv, D, max_sel, n_first, n_last, sel_idx,
+                                sel_cnt, stream);
+}
+
 size_t gqa_workspace_bytes(int kind, int query_rows, int ctx_or_kv, int Hq, int D) {
     if ((D != kHeadDim && D != 128) || query_rows < 1 || ctx_or_kv < 1) return 0;
     if (Hq < 1 || Hq > kMaxHeads) return 0;
@@ -366,6 +534,9 @@ size_t gqa_workspace_bytes(int kind, int query_rows, int ctx_or_kv, int Hq, int 
             return paged_e4m3_workspace_bytes(query_rows * Hq, ctx_or_kv, di->num_sms, D);
         case GQA_KIND_SPARSE:
             return kWorkspaceCounterBytes;
+        case GQA_KIND_SELECT_BLOCKS:
+            return select_blocks_workspace_bytes(
+                query_rows, ctx_or_kv, Hq * D < kMaxIndexWidth ? Hq * D : kMaxIndexWidth);
         default:
             return 0;
     }

@@ -137,6 +137,49 @@ int sparse_launch(const void* q, const void* kcache, const void* vcache, const f
                   int page, int ctx_len, int rows, int Hq, int Hkv, int Dh, float scale,
                   void* out, cudaStream_t stream);
 
+// The rows of a step and where they sit in the paged cache (the cache write,
+// cache read and block index entry points).
+struct CacheRows {
+    const int32_t* block_tables;
+    const int32_t* row_starts;   // null: tokens / batch rows a sequence
+    const int32_t* ctx_lens_dev;
+    int table_stride, num_pages, page, max_ctx_len, batch, tokens;
+};
+
+struct CacheWriteArgs {
+    const void* x[3];            // q (or null), k, v
+    long long token_stride[3], head_stride[3];
+    int dtype;
+    const void *q_weight, *k_weight;
+    float eps;
+    const float* inv_freq;
+    int rot_dim, interleaved;
+    bool e4m3;
+    const float *kscale, *vscale;
+    int Hq, Hkv, D;
+    void *q_out, *kcache, *vcache;
+};
+
+int cache_write_launch(const CacheRows& r, const CacheWriteArgs& a, cudaStream_t stream);
+// kscale / vscale: null to copy the cached rows as they are (row_bytes of K
+// and V per token), else E4M3 codes to fp16.
+int cache_read_launch(const CacheRows& r, const void* kcache, const void* vcache,
+                      const float* kscale, const float* vscale, int row_bytes, void* k_out,
+                      void* v_out, cudaStream_t stream);
+// kscale: null for an fp16 cache.  width = Hkv * D.
+int block_index_launch(const CacheRows& r, const void* kcache, const float* kscale, int width,
+                       int8_t* index, float* index_scale, cudaStream_t stream);
+
+constexpr int kMaxIndexWidth = 1024;   // Hkv * D of the block index
+constexpr int kMaxSelect = 2048;       // blocks kept per row by the block selection
+
+int select_blocks_launch(const void* q, const int8_t* index, const float* index_scale,
+                         const int32_t* block_table, int num_pages, int page, int ctx_len,
+                         int rows, int Hq, int Hkv, int D, int max_sel, int n_first, int n_last,
+                         int32_t* sel_idx, int32_t* sel_cnt, cudaStream_t stream);
+// width = Hkv * D.
+size_t select_blocks_workspace_bytes(int rows, int ctx_len, int width);
+
 // Bytes at the start of every workspace reserved for merge counters.
 constexpr size_t kWorkspaceCounterBytes = 4096;
 
