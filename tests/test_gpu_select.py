@@ -59,6 +59,14 @@ CASES = [
     (130, 20011, 16, 5, 1, 128, 64, 0, 1),
     (1, 100003, 16, 6, 1, 256, 2000, 0, 1),
     (700, 700, 16, 6, 1, 256, 12, 1, 3),        # from the first position on
+    # Many blocks for what is taken: candidates by the bound of a sample.
+    (33, 9001, 16, 6, 1, 256, 64, 0, 1),
+    (300, 12007, 32, 8, 2, 128, 20, 2, 3),
+    (257, 9002, 16, 8, 4, 256, 9, 0, 2),        # width 1024
+    (40, 16390, 64, 6, 6, 128, 200, 17, 30),
+    (130, 9999, 256, 1, 1, 128, 3, 1, 1),
+    (60, 40001, 16, 6, 1, 256, 600, 0, 1),
+    (2500, 2500 + 7000, 16, 2, 1, 128, 32, 1, 1),
 ]
 
 
@@ -70,10 +78,10 @@ def test_select_matches_the_definition(cuda_lib, case):
     assert cuda_lib.device_error() == 0
 
 
-@pytest.mark.parametrize("rows", [1, 7, 40, 200])
+@pytest.mark.parametrize("rows,ctx", [(1, 4000), (7, 4000), (40, 4000), (200, 4000), (70, 10000)])
 @pytest.mark.parametrize("kind", ["equal", "few", "zero_scale", "zero_query", "two_values"])
-def test_ties_go_to_the_lowest_id(cuda_lib, rows, kind):
-    ctx, page = 4000, 16
+def test_ties_go_to_the_lowest_id(cuda_lib, rows, ctx, kind):
+    page = 16
     q, index, scale, table = make(rows, rows, ctx, page, 6, 1, 256)
     if kind == "equal":        # every block the same summary
         index[:] = index[0, 0]
@@ -93,10 +101,10 @@ def test_ties_go_to_the_lowest_id(cuda_lib, rows, kind):
     check(cuda_lib, q, index, scale, table, page, ctx, 50, 1, 2)
 
 
-@pytest.mark.parametrize("rows", [2, 150])
-def test_extreme_values(cuda_lib, rows):
+@pytest.mark.parametrize("rows,ctx", [(2, 3000), (150, 3000), (50, 12000)])
+def test_extreme_values(cuda_lib, rows, ctx):
     """Largest codes, huge / tiny / infinite / NaN scales, infinite and NaN queries."""
-    ctx, page = 3000, 16
+    page = 16
     q, index, scale, table = make(3, rows, ctx, page, 8, 4, 256)
     index[1] = 127
     index[2] = -127
@@ -115,11 +123,11 @@ def test_extreme_values(cuda_lib, rows):
     check(cuda_lib, q, index, scale, table, page, ctx, 30, 0, 1)
 
 
-@pytest.mark.parametrize("rows", [3, 200])
-def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows):
+@pytest.mark.parametrize("rows,ctx", [(3, 2002), (200, 2002), (100, 11002)])
+def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows, ctx):
     """What lies at or behind a row's own block, and in pages nobody names,
     changes nothing (a step's later rows write their blocks' summaries first)."""
-    ctx, page = 2002, 16
+    page = 16
     q, index, scale, table = make(8, rows, ctx, page, 6, 1, 256)
     a = run(cuda_lib, q, index, scale, table, ctx, 40, 1, 2)
     nb = (ctx + 3) // 4
@@ -137,6 +145,28 @@ def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows):
     # Row by row: a later row's blocks do not reach an earlier one.
     c = run(cuda_lib, q[:1], index, scale, table, ctx - rows + 1, 40, 1, 2)
     assert torch.equal(a[0][:1], c[0]) and first_own + 1 >= int(c[0].max()) + 1
+
+
+@pytest.mark.parametrize("kind", ["most_nan", "clustered", "rising"])
+def test_scores_that_defeat_the_sample(cuda_lib, kind):
+    """Fewer numbers than are taken, all the best in one stretch, scores that
+    rise with the position: rows whose candidates run out or do not fit."""
+    rows, ctx, page = 64, 12000, 16
+    q, index, scale, table = make(17, rows, ctx, page, 6, 1, 256)
+    b = torch.arange(ctx // 4)
+    at = table[b * 4 // page].long(), b % (page // 4)
+    if kind == "most_nan":
+        scale[at] = torch.where(b % 300 == 5, 1.0, float("nan"))
+    elif kind == "clustered":
+        q = q.abs()
+        index[at[0], at[1]] = torch.where((b >= 1000) & (b < 1500), 100, 1)[:, None, None].to(
+            torch.int8).expand(-1, 1, 256)
+        scale[at] = 1 + b.float() * 1e-4
+    else:
+        q = q.abs()
+        index[:] = 3
+        scale[at] = 1 + b.float()
+    check(cuda_lib, q, index, scale, table, page, ctx, 60, 1, 2)
 
 
 def test_rows_do_not_depend_on_the_launch(cuda_lib):
