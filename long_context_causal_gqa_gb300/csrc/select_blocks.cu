@@ -9,15 +9,16 @@
 // The selection is therefore a function of the inputs alone, whatever the
 // path, the split or the other rows of the call.
 //
-// Few rows: every block's scores by dp4a straight from the int8 index, then
-// one CTA a row finds the best.  More rows: the tensor cores (dot_kernel).
-// With many blocks, writing rows x blocks scores and reading them back would
-// cost several times the products themselves, so only every 8th block's are
-// written; the k-th best of those bounds the k-th best of all from below
-// (bound_kernel), and the other blocks' products are compared with that bound
-// as they leave the tensor memory, keeping about 7 k candidates a row.  One
-// CTA a row then takes the best of the candidates (best_kernel).  A row whose
-// candidates do not fit (thousands of equal scores) is searched block by block.
+// Few rows: every block's scores by dp4a straight from the int8 index.  More
+// rows: the tensor cores (dot_kernel).  With many blocks, writing rows x blocks
+// scores and reading them back would cost several times the products
+// themselves.  So every 8th block's products are taken first, of which only
+// maxima over small groups are kept; the k-th best of those is a lower bound
+// of the row's k-th best score (k blocks reach it), found by bound_kernel.  The
+// products of all blocks are then compared with the bound as they leave the
+// tensor memory, and about 9 k of them stay as candidates.  Either way one CTA
+// a row takes the best of what is left (best_of).  A row whose candidates do
+// not fit (thousands of equal scores) is searched block by block (scan_best).
 #include <atomic>
 #include <cuda_fp16.h>
 
@@ -28,23 +29,22 @@
 namespace gqa {
 namespace select {
 
-constexpr int STRIDE = 8;   // every STRIDE-th block is in the sample
+constexpr int STRIDE = 4;   // every STRIDE-th block is in the sample
 
-// Columns of the score products: all blocks in order, the sampled blocks
-// (0, 8, 16, ...), or the rest in order.
-enum Order { ALL = 0, SAMPLE = 1, REST = 2 };
+// What dot_kernel does with its products: keep all scores, keep the maxima of
+// groups of the sampled blocks' (columns 0, 1, ... are blocks 0, 8, 16, ...),
+// or keep the candidates.
+enum Mode { SCORES = 0, MAXIMA = 1, CANDIDATES = 2 };
 
-template <int ORDER>
+// Block of a column, and the columns whose block is below hi.
+template <int MODE>
 __host__ __device__ __forceinline__ int col_block(int c) {
-    return ORDER == ALL ? c : ORDER == SAMPLE ? c * STRIDE
-                                              : c / (STRIDE - 1) * STRIDE + c % (STRIDE - 1) + 1;
+    return MODE == MAXIMA ? c * STRIDE : c;
 }
-// Columns whose block is below hi (a prefix in each order).
-template <int ORDER>
+template <int MODE>
 __host__ __device__ __forceinline__ int cols_below(int hi) {
     if (hi <= 0) return 0;
-    const int s = (hi + STRIDE - 1) / STRIDE;
-    return ORDER == ALL ? hi : ORDER == SAMPLE ? s : hi - s;
+    return MODE == MAXIMA ? (hi + STRIDE - 1) / STRIDE : hi;
 }
 
 // What a row takes: blocks below n_first and from hi on always, `need` of the
@@ -69,7 +69,8 @@ __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t u = __float_as_uint(f + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-constexpr uint32_t kOrderedMinusInf = 0x007fffffu;
+// A bound that nothing reaches (a comparison with NaN is false).
+#define kNoBound __int_as_float(0x7fffffff)
 
 struct IndexView {
     const int8_t* index;
@@ -105,9 +106,8 @@ __device__ __forceinline__ uint2 codes_half4(uint32_t w) {
 
 // ------------------------------------------------------------ query codes
 // codes[row, g * D + d] = rint(S * 127 / max |S|), S = sum of q over the query
-// heads of KV head g.  fp16 values are whole multiples of 2^-24 below 2^41 of
-// them, so the sums are exact as 64-bit whole numbers; S is rounded to 32 bits
-// once.  A row with an infinity or NaN gets codes of zero.  One warp a row.
+// heads of KV head g, exact and rounded to 32 bits once.  A row with an
+// infinity or NaN gets codes of zero.  One warp a row, 8 values a lane.
 struct CodeParams {
     const __half* q;
     int rows, Hq, D, group, width;
@@ -115,92 +115,128 @@ struct CodeParams {
     __half* codes16;   // the same codes as fp16 (null: not wanted)
 };
 
-__device__ __forceinline__ void query_codes(const CodeParams& P, int row, int lane) {
-    float s[8][4];
+// Each fp16 value x is split at 2^-6: x + kSplit has a last place of 2^-6 for
+// every |x| < 65536, so its bits, as whole numbers, add up the upper parts (at
+// most 64 of 2^22), and the lower parts are multiples of 2^-24 of at most 2^-7,
+// whose sum stays exact in 32 bits.
+constexpr float kSplit = 196608.f;   // 1.5 * 2^17
+constexpr int kSplitBits = 0x48400000;
+
+__device__ __forceinline__ void query_codes(const CodeParams& P, int row, int lane,
+                                            uint2 (&w)[4]) {
+    float s[4][8];
     float most = 0.f;
     bool fine = true;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c * 128 >= P.width) break;
-        const int g = c * 128 / P.D;
-        const __half* src = P.q + ((long long)row * P.Hq + g * P.group) * P.D +
-                            (c * 128 - g * P.D) + lane * 4;
-        long long sum[4] = {0, 0, 0, 0};
-        for (int h = 0; h < P.group; ++h) {
-            const uint2 u = *reinterpret_cast<const uint2*>(src + (long long)h * P.D);
-            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-            const float f[4] = {f0.x, f0.y, f1.x, f1.y};
+    for (int c = 0; c < 4; ++c) {
+        const int e = c * 256 + lane * 8;
+        if (c * 256 >= P.width) break;
+        if (e >= P.width) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                fine = fine && fabsf(f[j]) <= 65504.f;
-                sum[j] += __float2ll_rn(f[j] * 16777216.f);
+            for (int j = 0; j < 8; ++j) s[c][j] = 0.f;
+            continue;
+        }
+        const int g = e / P.D;
+        const __half* src = P.q + ((long long)row * P.Hq + g * P.group) * P.D + (e - g * P.D);
+        int upper[8];
+        float lower[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            upper[j] = 0;
+            lower[j] = 0.f;
+        }
+#pragma unroll 4
+        for (int h = 0; h < P.group; ++h) {
+            const uint4 u = *reinterpret_cast<const uint4*>(src + (long long)h * P.D);
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[j / 2]));
+                const float x = j & 1 ? f.y : f.x;
+                fine = fine && fabsf(x) <= 65504.f;
+                const float t = __fadd_rn(x, kSplit);
+                upper[j] += __float_as_int(t) - kSplitBits;
+                lower[j] += __fsub_rn(x, __fsub_rn(t, kSplit));
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s[c][j] = __ll2float_rn(sum[j]);
+        for (int j = 0; j < 8; ++j) {
+            // In units of 2^-24, exact; one rounding to 32 bits.
+            const long long sum = ((long long)upper[j] << 18) + (int)(lower[j] * 16777216.f);
+            s[c][j] = __ll2float_rn(sum) * (1.f / 16777216.f);
             most = fmaxf(most, fabsf(s[c][j]));
         }
     }
     fine = __all_sync(0xffffffffu, fine);
     most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
     fine = fine && most > 0.f;
-    // The sums carry a factor 2^24, as `most` does: the codes see their ratio.
-    const float inv = fine ? 127.f / (most * (1.f / 16777216.f)) : 0.f;
+    const float inv = fine ? 127.f / most : 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c * 128 >= P.width) break;
-        uint32_t w = 0;
+    for (int c = 0; c < 4; ++c) {
+        if (c * 256 >= P.width) break;
+        uint32_t x[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int code =
-                fine ? (int)rintf(__fmul_rn(s[c][j] * (1.f / 16777216.f), inv)) : 0;
-            w |= (uint32_t)(code & 0xff) << (8 * j);
+        for (int j = 0; j < 8; ++j) {
+            const int code = fine ? (int)rintf(__fmul_rn(s[c][j], inv)) : 0;
+            x[j / 4] |= (uint32_t)(code & 0xff) << (8 * (j % 4));
         }
-        const long long at = (long long)row * P.width + c * 128 + lane * 4;
-        *reinterpret_cast<uint32_t*>(P.codes + at) = w;
-        if (P.codes16) *reinterpret_cast<uint2*>(P.codes16 + at) = codes_half4(w);
+        w[c] = make_uint2(x[0], x[1]);
     }
 }
 
-// The index's columns as the tensor cores read them: fp16 codes in column
-// order and the columns' scales.
+__device__ __forceinline__ void store_codes(const CodeParams& P, int row, int lane,
+                                            const uint2 (&w)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int e = c * 256 + lane * 8;
+        if (e >= P.width) break;
+        const long long at = (long long)row * P.width + e;
+        *reinterpret_cast<uint2*>(P.codes + at) = w[c];
+        if (P.codes16) {
+            const uint2 a = codes_half4(w[c].x), b = codes_half4(w[c].y);
+            *reinterpret_cast<uint4*>(P.codes16 + at) = make_uint4(a.x, a.y, b.x, b.y);
+        }
+    }
+}
+
+// The index's blocks in order as the tensor cores read them: fp16 codes, the
+// blocks' scales, and the sampled blocks' scales again.
 struct ExpandParams {
     IndexView V;
-    int n_first_cols;    // columns of the first map (ALL or SAMPLE)
-    int n_rest_cols;     // columns of the REST map (0 when all are in the first)
-    bool sampled;
-    __half* first;
-    __half* rest;
-    float* first_scale;
-    float* rest_scale;
+    int n;
+    __half* cols;
+    float* scale;
+    float* sample_scale;   // null: no sample
 };
 
 // The first `code_ctas` CTAs make query codes (8 rows each), the others
-// expand columns (16 codes a thread).
+// expand blocks (16 codes a thread).
 __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const ExpandParams E,
                                                       int code_ctas) {
     if ((int)blockIdx.x < code_ctas) {
-        const int row = blockIdx.x * 8 + threadIdx.x / 32;
-        if (row < C.rows) query_codes(C, row, threadIdx.x % 32);
+        const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+        if (row >= C.rows) return;
+        uint2 w[4];
+        query_codes(C, row, lane, w);
+        store_codes(C, row, lane, w);
         return;
     }
     const int per_col = E.V.width / 16;
     const long long i = (long long)(blockIdx.x - code_ctas) * 256 + threadIdx.x;
-    const int c = (int)(i / per_col), part = (int)(i - (long long)c * per_col);
-    if (c >= E.n_first_cols + E.n_rest_cols) return;
-    const bool rest = c >= E.n_first_cols;
-    const int col = rest ? c - E.n_first_cols : c;
-    const int b = rest ? col_block<REST>(col) : E.sampled ? col_block<SAMPLE>(col) : col;
+    const int b = (int)(i / per_col), part = (int)(i - (long long)b * per_col);
+    if (b >= E.n) return;
     const long long block = physical_block(E.V, b);
     const uint4 w = *reinterpret_cast<const uint4*>(E.V.index + block * E.V.width + part * 16);
-    __half* dst = (rest ? E.rest : E.first) + (long long)col * E.V.width + part * 16;
+    __half* dst = E.cols + (long long)b * E.V.width + part * 16;
     const uint2 x = codes_half4(w.x), y = codes_half4(w.y), z = codes_half4(w.z),
                 u = codes_half4(w.w);
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(x.x, x.y, y.x, y.y);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(z.x, z.y, u.x, u.y);
-    if (part == 0) (rest ? E.rest_scale : E.first_scale)[col] = E.V.scale[block];
+    if (part == 0) {
+        const float s = E.V.scale[block];
+        E.scale[b] = s;
+        if (E.sample_scale && b % STRIDE == 0) E.sample_scale[b / STRIDE] = s;
+    }
 }
 
 // ------------------------------------------------------------ products
@@ -218,6 +254,7 @@ constexpr int CHUNK_BYTES = 128 * 128;       // 128 rows x 64 fp16
 constexpr int RES_CHUNKS = 4;                // row chunks kept (width 256)
 constexpr int EPI_WARPS = 8;
 constexpr int DOT_THREADS = 32 * (2 + EPI_WARPS);
+constexpr int SCALE_BYTES = EPI_WARPS * 128 * 4;   // a warp's columns' scales
 constexpr uint32_t DOT_TMEM = 512;
 constexpr uint32_t IDESC = idesc_f16_f32(256, TILE, false, false);
 
@@ -227,7 +264,8 @@ struct DotCfg {
     static constexpr int SLOT_BYTES = RESIDENT ? CHUNK_BYTES : 2 * CHUNK_BYTES;
     static constexpr int ROW_BYTES = RESIDENT ? RES_CHUNKS * CHUNK_BYTES : 0;
     static constexpr int NUM_BARS = 2 * SLOTS + 7;
-    static constexpr int SMEM = 1024 + ROW_BYTES + SLOTS * SLOT_BYTES + NUM_BARS * 8 + 16;
+    static constexpr int SMEM = 1024 + ROW_BYTES + SLOTS * SLOT_BYTES + SCALE_BYTES +
+                                NUM_BARS * 8 + 16;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -238,22 +276,23 @@ struct DotParams {
     int G;                     // pairs
     long long total;           // (row tile, column tile) products
     int pos0;                  // position of the first row
-    int max_sel, n_first, n_last;
+    int n_first, n_last;
     const float* scale;        // per column, allocated to a multiple of TILE
-    float* scores;             // ALL, SAMPLE: [rows, stride]
+    float* scores;             // SCORES, MAXIMA: [rows, stride]
     long long stride;
-    const float* bound;        // REST: per row
-    uint2* list;               // REST: (score, column) [rows][segs][2][cap]
-    int* counts;               // REST: entries found [rows][segs][2]
+    int log2_group;            // MAXIMA: columns of a group, 1 to 8
+    const float* bound;        // CANDIDATES: per row
+    uint2* list;               // CANDIDATES: (score, block) [rows][segs][2][cap]
+    int* counts;               // CANDIDATES: entries [rows][segs][2], -1: too many
     int segs, cap;
     unsigned* err;
 };
 
-template <int ORDER>
+template <int MODE>
 __host__ __device__ __forceinline__ int col_tiles(const DotParams& P, int rt) {
     const int last = min(rt * PAIR_ROWS + PAIR_ROWS, P.rows) - 1;
     const int hi = ((P.pos0 + last) >> 2) + 1 - P.n_last;
-    return (cols_below<ORDER>(hi) + TILE - 1) / TILE;
+    return (cols_below<MODE>(hi) + TILE - 1) / TILE;
 }
 // The pair that computes product x of the row-tile-major order, and the first
 // product of pair p.
@@ -265,7 +304,7 @@ __host__ __device__ __forceinline__ int pair_of(const DotParams& P, long long x)
 }
 
 // A pair's products as runs of column tiles [jb, je) of one row tile.
-template <int ORDER>
+template <int MODE>
 struct Runs {
     long long pos, end, cum;
     int rt;
@@ -275,7 +314,7 @@ struct Runs {
         cum = 0;
         rt = 0;
         while (rt < P.row_tiles) {
-            const int n = col_tiles<ORDER>(P, rt);
+            const int n = col_tiles<MODE>(P, rt);
             if (cum + n > pos) break;
             cum += n;
             ++rt;
@@ -284,8 +323,8 @@ struct Runs {
     // seg: this run's number among its row tile's runs.
     __device__ bool next(const DotParams& P, int pair, int& t, int& jb, int& je, int& seg) {
         if (pos >= end) return false;
-        int n = col_tiles<ORDER>(P, rt);
-        while (n == 0) n = col_tiles<ORDER>(P, ++rt);
+        int n = col_tiles<MODE>(P, rt);
+        while (n == 0) n = col_tiles<MODE>(P, ++rt);
         t = rt;
         jb = (int)(pos - cum);
         je = (int)min((long long)n, end - cum);
@@ -305,7 +344,21 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
                  : "memory");
 }
 
-template <int ORDER, bool RESIDENT>
+// Stores (v, block) and moves on if v >= bound: predicated, since in nearly
+// every column some lane of the warp has a candidate and a branch would run
+// its body each time.
+__device__ __forceinline__ void keep_candidate(uint2*& to, float v, float bound, int block) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ge.f32 p, %1, %2;\n\t"
+        "@p st.global.v2.b32 [%0], {%3, %4};\n\t"
+        "@p add.u64 %0, %0, 8;\n\t}"
+        : "+l"(to)
+        : "f"(v), "f"(bound), "r"(__float_as_uint(v)), "r"(block)
+        : "memory");
+}
+
+template <int MODE, bool RESIDENT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DOT_THREADS, 1)
 dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
            const DotParams P) {
@@ -315,15 +368,15 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t s_rows = base;
     const uint32_t s_ring = base + C::ROW_BYTES;
-    const uint32_t bars = s_ring + C::SLOTS * C::SLOT_BYTES;
+    const uint32_t bars = s_ring + C::SLOTS * C::SLOT_BYTES + SCALE_BYTES;
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (C::SLOTS + s); };
     const uint32_t rows_full = bars + 8 * (2 * C::SLOTS), rows_empty = rows_full + 8;
     auto tfull = [&](int i) { return rows_full + 16 + 8 * i; };    // products in buffer i
     auto tempty = [&](int i) { return rows_full + 32 + 8 * i; };   // buffer i read out
     const uint32_t drain = rows_full + 48;
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(base_ptr + C::ROW_BYTES +
-                                                     C::SLOTS * C::SLOT_BYTES + C::NUM_BARS * 8);
+    float* s_scale = reinterpret_cast<float*>(base_ptr + C::ROW_BYTES + C::SLOTS * C::SLOT_BYTES);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(s_scale + SCALE_BYTES / 4 + C::NUM_BARS * 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -354,7 +407,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
 
-    Runs<ORDER> runs;
+    Runs<MODE> runs;
     runs.init(P, pair);
     int rt, jb, je, seg;
     if (warp == 0) {
@@ -443,6 +496,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
         const int half = (warp - 2) >> 2;      // which 128 columns of a tile
         const int quarter = warp & 3;          // TMEM lanes this warp may read
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+        float4* const my_scale = reinterpret_cast<float4*>(s_scale + (warp - 2) * 128);
         uint32_t t = 0;
         bool ok = true;
         while (ok && runs.next(P, pair, rt, jb, je, seg)) {
@@ -451,32 +505,36 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             const bool valid = row < P.rows;
             const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;     // this row's scored blocks end
             const int hi0 = ((P.pos0 + row0) >> 2) + 1 - P.n_last;   // the warp's smallest
-            const float bound = ORDER == REST ? (valid ? P.bound[row] : INFINITY) : 0.f;
+            float bound = MODE == CANDIDATES && valid ? P.bound[row] : kNoBound;
             const long long at = (((long long)row * P.segs + seg) * 2 + half);
-            uint2* list = ORDER == REST ? P.list + at * P.cap : nullptr;
-            int found = 0;
-            const int last = P.cap - 1;
+            uint2* const list = MODE == CANDIDATES ? P.list + at * P.cap : nullptr;
+            uint2* const full32 = list + (P.cap - 32);   // room for 32 more up to here
+            uint2* to = list;
+            bool over = false;
+            // The tile's scales: four a lane, loaded a tile ahead, then shared by
+            // the warp.
+            const float4* scale4 =
+                reinterpret_cast<const float4*>(P.scale + jb * TILE + half * 128) + lane;
+            float4 ahead = __ldg(scale4);
             for (int j = jb; j < je; ++j, ++t) {
+                __syncwarp();
+                my_scale[lane] = ahead;
+                if (j + 1 < je) ahead = __ldg(scale4 += TILE / 4);
+                __syncwarp();
                 ok = mbar_wait(tfull(t & 1), (t >> 1) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const int col0 = j * TILE + half * 128;
+                // Two tensor-memory loads in flight.
+                uint32_t r[2][32];
+                tmem_ld32(t_lane + (t & 1) * TILE, r[0]);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    uint32_t r[32];
-                    tmem_ld32(t_lane + (t & 1) * TILE + g * 32, r);
+                    const int c0 = col0 + g * 32;
+                    tmem_ld_wait<32>(r[g & 1]);
+                    if (g < 3) tmem_ld32(t_lane + (t & 1) * TILE + (g + 1) * 32, r[(g + 1) & 1]);
                     float sc[32];
-                    const float4* src = reinterpret_cast<const float4*>(P.scale + col0 + g * 32);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 f = __ldg(src + i);
-                        sc[4 * i] = f.x;
-                        sc[4 * i + 1] = f.y;
-                        sc[4 * i + 2] = f.z;
-                        sc[4 * i + 3] = f.w;
-                    }
-                    tmem_ld_wait<32>(r);
                     if (g == 3) {
                         // The buffer is read out.
                         tc_fence_before();
@@ -484,37 +542,67 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                         if (lane == 0) pairs::remote_arrive(pairs::leader_addr(tempty(t & 1)));
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        sc[i] = __fmul_rn(__uint_as_float(r[i]), sc[i]);
-                    const int c0 = col0 + g * 32;
-                    if (ORDER != REST) {
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = my_scale[g * 8 + i];
+                        sc[4 * i] = __fmul_rn(__uint_as_float(r[g & 1][4 * i]), f.x);
+                        sc[4 * i + 1] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 1]), f.y);
+                        sc[4 * i + 2] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 2]), f.z);
+                        sc[4 * i + 3] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 3]), f.w);
+                    }
+                    if (MODE == SCORES) {
                         if (valid) {
                             float* dst = P.scores + row * P.stride + c0;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
                         }
-                    } else {
-                        const bool whole = col_block<ORDER>(c0) >= P.n_first &&
-                                           col_block<ORDER>(c0 + 31) < hi0;
-                        if (!whole) {
-                            // A tile on the rows' own blocks, or on the first ones.
+                        continue;
+                    }
+                    if (col_block<MODE>(c0) < P.n_first || col_block<MODE>(c0 + 31) >= hi0) {
+                        // Columns on the rows' own blocks, behind them, or on the
+                        // first ones: not scored.
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int b = col_block<ORDER>(c0 + i);
-                                if (b < P.n_first || b >= hi) sc[i] = __int_as_float(0x7fc00000);
-                            }
+                        for (int i = 0; i < 32; ++i) {
+                            const int b = col_block<MODE>(c0 + i);
+                            if (b < P.n_first || b >= hi) sc[i] = -INFINITY;
+                        }
+                    }
+                    if (MODE == MAXIMA) {
+                        if (!valid) continue;
+                        float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
+                        // fmaxf drops a NaN; a group of nothing else stays below -inf's key.
+                        if (P.log2_group == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
+                            continue;
+                        }
+                        float m[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) m[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
+                        if (P.log2_group == 1) {
+                            store8(dst, m);
+                            store8(dst + 8, m + 8);
+                            continue;
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (sc[i] >= bound) {
-                                list[min(found, last)] =
-                                    make_uint2(__float_as_uint(sc[i]), (uint32_t)(c0 + i));
-                                ++found;
-                            }
+                        for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
+                        if (P.log2_group == 2) {
+                            store8(dst, m);
+                            continue;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
+                        *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
+                        continue;
                     }
+                    if (to > full32) {
+                        over = true;
+                        bound = kNoBound;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) keep_candidate(to, sc[i], bound, c0 + i);
                 }
             }
-            if (ORDER == REST && valid) P.counts[at] = found;
+            if (MODE == CANDIDATES && valid) P.counts[at] = over ? -1 : (int)(to - list);
         }
     }
 
@@ -535,61 +623,89 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     }
 }
 
-// Few rows: eight lanes read one block's codes (16 bytes at a time) and take
-// its dots with up to SMALL_ROWS rows.
-constexpr int SMALL_ROWS = 8;
+// ------------------------------------------------------------ few rows
+// Every CTA makes the codes of its (up to 8) rows itself, which costs less
+// than a launch of its own; a warp then takes 8 blocks at a time, eight lanes
+// reading one block's codes 16 bytes each, and keeps the scores and their
+// maximum over the scored ones.
+constexpr int FEW_TILE = 8;
 
-struct SmallParams {
+struct FewParams {
+    CodeParams C;
     IndexView V;
-    const int8_t* codes;
-    int rows;
     int n;                       // blocks
+    int pos0, n_first, n_last;
     float* scores;               // [rows, stride]
     long long stride;
+    float* maxima;               // [rows, stride / 8]
 };
 
-__global__ void __launch_bounds__(256) score_small_kernel(const SmallParams P) {
-    __shared__ __align__(16) int8_t s_q[SMALL_ROWS][kMaxIndexWidth];
+__global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
+    __shared__ __align__(16) uint2 s_q[FEW_TILE][kMaxIndexWidth / 8];
     const int width = P.V.width;
-    const int r0 = blockIdx.y * SMALL_ROWS;
-    const int nr = min(SMALL_ROWS, P.rows - r0);
-    for (int i = threadIdx.x; i < SMALL_ROWS * width / 16; i += 256) {
-        const int r = i / (width / 16), c = i - r * (width / 16);
-        reinterpret_cast<uint4*>(s_q[r])[c] =
-            r < nr ? *reinterpret_cast<const uint4*>(P.codes + (long long)(r0 + r) * width + c * 16)
-                   : make_uint4(0, 0, 0, 0);
+    const int r0 = blockIdx.y * FEW_TILE;
+    const int nr = min(FEW_TILE, P.C.rows - r0);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (warp < nr) {
+        uint2 w[4];
+        query_codes(P.C, r0 + warp, lane, w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c * 256 + lane * 8 < width) s_q[warp][c * 32 + lane] = w[c];
+        if (blockIdx.x == 0) store_codes(P.C, r0 + warp, lane, w);
     }
     __syncthreads();
-    const int lane = threadIdx.x % 8;
-    for (int b0 = blockIdx.x * 32; b0 < P.n; b0 += gridDim.x * 32) {
-        const int b = b0 + threadIdx.x / 8;
-        const bool live = b < P.n;
-        const long long block = physical_block(P.V, live ? b : b0);
-        const uint4* src = reinterpret_cast<const uint4*>(P.V.index + block * width);
-        int dot[SMALL_ROWS];
+    const int sub = lane / 8, part = lane % 8;
+    for (int b0 = (blockIdx.x * 8 + warp) * 8; b0 < P.n; b0 += gridDim.x * 64) {
+        // This lane's blocks: b0 + sub and b0 + 4 + sub.
+        const uint4* src[2];
+        float scale[2];
 #pragma unroll
-        for (int r = 0; r < SMALL_ROWS; ++r) dot[r] = 0;
-        for (int c = lane; c < width / 16; c += 8) {
-            const uint4 k = src[c];
+        for (int i = 0; i < 2; ++i) {
+            const long long block = physical_block(P.V, min(b0 + 4 * i + sub, P.n - 1));
+            src[i] = reinterpret_cast<const uint4*>(P.V.index + block * width);
+            scale[i] = P.V.scale[block];
+        }
+        int dot[2][FEW_TILE];
 #pragma unroll
-            for (int r = 0; r < SMALL_ROWS; ++r) {
+        for (int r = 0; r < FEW_TILE; ++r) dot[0][r] = dot[1][r] = 0;
+#pragma unroll 2
+        for (int c = part; c < width / 16; c += 8) {
+            const uint4 k0 = src[0][c], k1 = src[1][c];
+#pragma unroll
+            for (int r = 0; r < FEW_TILE; ++r) {
                 if (r >= nr) break;
                 const uint4 x = reinterpret_cast<const uint4*>(s_q[r])[c];
-                dot[r] = __dp4a((int)k.x, (int)x.x, dot[r]);
-                dot[r] = __dp4a((int)k.y, (int)x.y, dot[r]);
-                dot[r] = __dp4a((int)k.z, (int)x.z, dot[r]);
-                dot[r] = __dp4a((int)k.w, (int)x.w, dot[r]);
+                dot[0][r] = __dp4a((int)k0.x, (int)x.x, dot[0][r]);
+                dot[1][r] = __dp4a((int)k1.x, (int)x.x, dot[1][r]);
+                dot[0][r] = __dp4a((int)k0.y, (int)x.y, dot[0][r]);
+                dot[1][r] = __dp4a((int)k1.y, (int)x.y, dot[1][r]);
+                dot[0][r] = __dp4a((int)k0.z, (int)x.z, dot[0][r]);
+                dot[1][r] = __dp4a((int)k1.z, (int)x.z, dot[1][r]);
+                dot[0][r] = __dp4a((int)k0.w, (int)x.w, dot[0][r]);
+                dot[1][r] = __dp4a((int)k1.w, (int)x.w, dot[1][r]);
             }
         }
-        const float scale = P.V.scale[block];
 #pragma unroll
-        for (int r = 0; r < SMALL_ROWS; ++r) {
+        for (int r = 0; r < FEW_TILE; ++r) {
             if (r >= nr) break;
-            int d = dot[r];
-            d += __shfl_xor_sync(0xffffffffu, d, 4);
-            d += __shfl_xor_sync(0xffffffffu, d, 2);
-            d += __shfl_xor_sync(0xffffffffu, d, 1);
-            if (lane == 0 && live) P.scores[(r0 + r) * P.stride + b] = __fmul_rn((float)d, scale);
+            const int row = r0 + r;
+            const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;
+            float most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                int d = dot[i][r];
+                d += __shfl_xor_sync(0xffffffffu, d, 4);
+                d += __shfl_xor_sync(0xffffffffu, d, 2);
+                d += __shfl_xor_sync(0xffffffffu, d, 1);
+                const int b = b0 + 4 * i + sub;
+                const float v = __fmul_rn((float)d, scale[i]);
+                if (part == 0 && b < P.n) P.scores[row * P.stride + b] = v;
+                if (b >= P.n_first && b < hi) most = fmaxf(most, v);
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+            if (lane == 0) P.maxima[row * (P.stride / 8) + b0 / 8] = most;
         }
     }
 }
@@ -602,111 +718,215 @@ struct PickParams {
     int32_t* sel_cnt;
 };
 
-// Largest digit d of a 256-bin histogram with at least *left entries in bins
-// >= d; *left becomes what is left to take from bin d.  One warp; the result
-// in every lane.
-__device__ __forceinline__ int pick_digit(const int* hist, int lane, int* left) {
-    // Lane l holds bins 255 - 8 l .. 248 - 8 l, highest first.
-    int c[8], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - 8 * lane - i];
-        sum += c[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, incl >= *left);
-    const int who = m ? __ffs(m) - 1 : 31;
-    int rest = *left - (incl - sum), d = 255 - 8 * lane;
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (rest > c[i] && 255 - 8 * lane - i == d) {
-            rest -= c[i];
-            --d;
-        }
-    *left = __shfl_sync(0xffffffffu, rest, who);
-    return __shfl_sync(0xffffffffu, d, who);
+// Candidates as whole numbers, higher is better: the score's order, then the
+// lower id.
+using Key = unsigned long long;
+__device__ __forceinline__ Key make_key(float score, int b) {
+    return ((Key)ordered(score) << 32) | (0xffffffffu - (uint32_t)b);
 }
 
-struct ScanShared {
-    int hist[256];
-    uint32_t prefix;
-    int need;
-    int above[32], equal[32];
+constexpr int WINDOW = 65536;    // block ids of one pass of the ordered output
+
+template <int THREADS>
+struct BestShared {
+    static constexpr int LOG2_BINS = THREADS <= 512 ? 9 : 10;
+    static constexpr int BINS = 1 << LOG2_BINS;
+    int hist[BINS];
+    Key most[32], least[32];
+    int sums[32];
+    int digit, left, count;
+    int total, bad;
 };
 
-// The best blocks of one row by its scores, one after the other (score(b) for
-// lo <= b < hi): the key of the last one taken is found eight bits at a time,
-// then one pass over the blocks in order writes those above it and the first
-// of those equal to it.  Called by all threads of a CTA.
-template <int THREADS, typename Score>
-__device__ void scan_best(const RowRange& R, const Score& score, int32_t* out, ScanShared& S) {
+// Inclusive prefix sum over the CTA's threads; two barriers.
+template <int THREADS>
+__device__ __forceinline__ int cta_scan(int v, int* sums) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
+    __syncthreads();
+    return v + before;
+}
+
+// The need-th largest of key[0 .. total), 1 <= need <= total, all keys
+// different, as a lower limit that exactly `need` keys reach.  Counts over BINS
+// equal parts of the keys' range, then of the part that holds it, until what
+// is in the part is taken whole.
+template <int THREADS>
+__device__ Key need_th(const Key* key, int total, int need, BestShared<THREADS>& S) {
+    constexpr int LOG2_BINS = BestShared<THREADS>::LOG2_BINS, BINS = 1 << LOG2_BINS;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    Key most = 0, least = ~0ull;
+    for (int i = tid; i < total; i += THREADS) {
+        most = max(most, key[i]);
+        least = min(least, key[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    if (lane == 0) {
+        S.most[warp] = most;
+        S.least[warp] = least;
+    }
+    __syncthreads();
+    most = S.most[lane % (THREADS / 32)];
+    least = S.least[lane % (THREADS / 32)];
+#pragma unroll
+    for (int o = THREADS / 64; o; o >>= 1) {
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    Key lo = least, width = most - least;   // keys of interest: [lo, lo + width]
+    for (;;) {
+        const int shift =
+            width >> LOG2_BINS ? 64 - LOG2_BINS - __clzll((long long)width) : 0;
+        constexpr int PER = BINS / THREADS;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) S.hist[tid * PER + i] = 0;
+        __syncthreads();
+        for (int i = tid; i < total; i += THREADS) {
+            const Key k = key[i] - lo;      // below lo: wraps to beyond width
+            if (k <= width) atomicAdd(&S.hist[(int)(k >> shift)], 1);
+        }
+        __syncthreads();
+        // Thread t holds bins from the top down.
+        int c[PER], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            c[i] = S.hist[BINS - 1 - tid * PER - i];
+            sum += c[i];
+        }
+        int before = cta_scan<THREADS>(sum, S.sums) - sum;
+        if (before < need && need <= before + sum) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (before < need && need <= before + c[i]) {
+                    S.digit = BINS - 1 - tid * PER - i;
+                    S.left = need - before;
+                    S.count = c[i];
+                }
+                before += c[i];
+            }
+        }
+        __syncthreads();
+        lo += (Key)S.digit << shift;
+        need = S.left;
+        if (S.count == need) return lo;
+        width = ((Key)1 << shift) - 1;
+        __syncthreads();
+    }
+}
+
+// Writes the taken blocks in ascending order: those below R.lo, those from
+// R.hi on, and the R.need best of key[0 .. total).  total >= R.need.  bits: room
+// for one per id of a window.
+template <int THREADS>
+__device__ void best_of(const RowRange& R, const Key* key, int total, int32_t* out,
+                        uint32_t* bits, BestShared<THREADS>& S) {
+    const int tid = threadIdx.x;
+    Key limit = 0;
+    if (R.need > 0) limit = need_th<THREADS>(key, total, R.need, S);
+    int done = 0;    // ids written
+    for (int w0 = 0; w0 < R.n_vis; w0 += WINDOW) {
+        const int ids = min(WINDOW, R.n_vis - w0), words = (ids + 31) / 32;
+        __syncthreads();
+        for (int i = tid; i < words; i += THREADS) {
+            // Blocks always taken: ids below lo or from hi on.
+            uint32_t m = 0;
+            const int id = w0 + i * 32;
+            if (id < R.lo) m |= R.lo - id >= 32 ? 0xffffffffu : (1u << (R.lo - id)) - 1;
+            if (id + 32 > R.hi) m |= id >= R.hi ? 0xffffffffu : ~((1u << (R.hi - id)) - 1);
+            if (id + 32 > R.n_vis) m &= (1u << (R.n_vis - id)) - 1;
+            bits[i] = m;
+        }
+        __syncthreads();
+        if (R.need > 0)
+            for (int i = tid; i < total; i += THREADS) {
+                const Key k = key[i];
+                const uint32_t id = 0xffffffffu - (uint32_t)k - (uint32_t)w0;
+                if (k >= limit && id < (uint32_t)ids) atomicOr(&bits[id / 32], 1u << (id % 32));
+            }
+        __syncthreads();
+        // Thread t writes the ids of its stretch of words.
+        const int per = (words + THREADS - 1) / THREADS;
+        const int a = min(tid * per, words), b = min(a + per, words);
+        int n = 0;
+        for (int i = a; i < b; ++i) n += __popc(bits[i]);
+        const int upto = cta_scan<THREADS>(n, S.sums);
+        int at = done + upto - n;
+        for (int i = a; i < b; ++i)
+            for (uint32_t m = bits[i]; m; m &= m - 1) out[at++] = w0 + i * 32 + __ffs(m) - 1;
+        if (tid == THREADS - 1) S.count = upto;
+        __syncthreads();
+        done += S.count;
+    }
+}
+
+// The best blocks of one row by its scores, one after the other (score(b) for
+// lo <= b < hi), whatever their number: the key of the last one taken is found
+// eight bits at a time, then one pass over the blocks in order writes those
+// above it and the first of those equal to it.
+template <int THREADS, typename Score>
+__device__ void scan_best(const RowRange& R, const Score& score, int32_t* out,
+                          BestShared<THREADS>& S) {
+    const int tid = threadIdx.x;
     uint32_t prefix = 0;
     int need = R.need;
-    if (need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += THREADS) S.hist[i] = 0;
-            __syncthreads();
-            for (int b = R.lo + tid; b < R.hi; b += THREADS) {
-                const uint32_t k = ordered(score(b));
-                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                    atomicAdd(&S.hist[(k >> shift) & 255], 1);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                int left = need;
-                const int d = pick_digit(S.hist, lane, &left);
-                if (lane == 0) {
-                    S.need = left;
-                    S.prefix = prefix | ((uint32_t)d << shift);
-                }
-            }
-            __syncthreads();
-            prefix = S.prefix;
-            need = S.need;
+    for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
+        __syncthreads();
+        for (int i = tid; i < 256; i += THREADS) S.hist[i] = 0;
+        __syncthreads();
+        for (int b = R.lo + tid; b < R.hi; b += THREADS) {
+            const uint32_t k = ordered(score(b));
+            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+                atomicAdd(&S.hist[(k >> shift) & 255], 1);
         }
-    } else {
-        prefix = 0xffffffffu;
+        __syncthreads();
+        // Thread t holds bins 255 - 2 t and 254 - 2 t.
+        const int c0 = tid < 128 ? S.hist[255 - 2 * tid] : 0;
+        const int c1 = tid < 128 ? S.hist[254 - 2 * tid] : 0;
+        const int before = cta_scan<THREADS>(c0 + c1, S.sums) - c0 - c1;
+        if (before < need && need <= before + c0 + c1) {
+            const bool second = need > before + c0;
+            S.digit = 255 - 2 * tid - second;
+            S.left = need - before - (second ? c0 : 0);
+        }
+        __syncthreads();
+        prefix |= (uint32_t)S.digit << shift;
+        need = S.left;
     }
     // need = how many of the blocks with key == prefix are taken (lowest ids).
-    int n_above = 0, n_equal = 0;   // so far, in blocks below b0
+    int done = 0, equals = 0;    // ids written, equal keys met
     for (int b0 = 0; b0 < R.n_vis; b0 += THREADS) {
         const int b = b0 + tid;
         bool above = false, equal = false;
         if (b < R.n_vis) {
             if (b < R.lo || b >= R.hi) above = true;
-            else {
+            else if (R.need > 0) {
                 const uint32_t k = ordered(score(b));
                 above = k > prefix;
-                equal = k == prefix && need > 0;
+                equal = k == prefix;
             }
         }
-        const uint32_t ma = __ballot_sync(0xffffffffu, above);
-        const uint32_t me = __ballot_sync(0xffffffffu, equal);
-        if (lane == 0) {
-            S.above[warp] = __popc(ma);
-            S.equal[warp] = __popc(me);
+        const int e = equals + cta_scan<THREADS>(equal, S.sums);
+        const bool take = above || (equal && e <= need);
+        const int at = done + cta_scan<THREADS>(take, S.sums);
+        if (take) out[at - 1] = b;
+        if (tid == THREADS - 1) {
+            S.left = e;
+            S.count = at;
         }
         __syncthreads();
-        int a = n_above, e = n_equal;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) {
-                a += S.above[w];
-                e += S.equal[w];
-            }
-            n_above += S.above[w];
-            n_equal += S.equal[w];
-        }
-        const uint32_t below = (1u << lane) - 1;
-        a += __popc(ma & below);
-        e += __popc(me & below);
-        if (above || (equal && e < need)) out[a + min(e, need)] = b;
-        __syncthreads();
+        equals = S.left;
+        done = S.count;
     }
 }
 
@@ -721,264 +941,265 @@ __device__ __forceinline__ bool write_plain(const PickParams& P, const RowRange&
     return true;
 }
 
-// One CTA a row, from all its scores.
+// One CTA a row, from all its scores: all of them as candidates if they fit;
+// else, with the maxima of each 8 (of more together if they are many), the
+// scores that reach the need-th best maximum.
+struct ScorePick {
+    PickParams K;
+    const float* scores;
+    long long stride;
+    const float* maxima;     // [rows, stride / 8], null: none
+    int room, room_groups;   // keys a CTA holds of candidates and of maxima
+};
+
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) pick_kernel(const PickParams P, const float* scores,
-                                                       long long stride) {
-    __shared__ ScanShared S;
-    const int row = blockIdx.x;
-    const RowRange R = row_range(P.pos0 + row, P.max_sel, P.n_first, P.n_last);
-    int32_t* out = P.sel_idx + (long long)row * P.max_sel;
-    if (write_plain(P, R, row, out)) return;
-    const float* s = scores + row * stride;
+__global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
+    extern __shared__ Key s_key[];   // [room], [room_groups], then the ids' bits
+    __shared__ BestShared<THREADS> S;
+    Key* groups = s_key + P.room;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(groups + P.room_groups);
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
+    int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
+    if (write_plain(P.K, R, row, out)) return;
+    const float* s = P.scores + row * P.stride;
+    const int n = R.hi - R.lo;
+    if (R.need == 0 || n <= P.room) {
+        const int total = R.need ? n : 0;
+#pragma unroll 4
+        for (int i = tid; i < total; i += THREADS) s_key[i] = make_key(s[R.lo + i], R.lo + i);
+        __syncthreads();
+        best_of<THREADS>(R, s_key, total, out, bits, S);
+        return;
+    }
+    if (P.maxima) {
+        const int g8 = (R.hi + 7) / 8;
+        const int per = (g8 + P.room_groups - 1) / P.room_groups;
+        const int n_groups = (g8 + per - 1) / per;
+        const float* m = P.maxima + row * (P.stride / 8);
+        if (per == 1) {
+#pragma unroll 8
+            for (int g = tid; g < n_groups; g += THREADS) groups[g] = make_key(m[g], g);
+        } else {
+            for (int g = tid; g < n_groups; g += THREADS) {
+                float most = -INFINITY;
+#pragma unroll 4
+                for (int i = g * per; i < min(g * per + per, g8); ++i) most = fmaxf(most, m[i]);
+                groups[g] = make_key(most, g);
+            }
+        }
+        if (tid == 0) S.total = S.count = 0;
+        __syncthreads();
+        if (n_groups >= R.need) {
+            const uint32_t bound = (uint32_t)(need_th<THREADS>(groups, n_groups, R.need, S) >> 32);
+            // The groups that reach the bound, one behind the other (S.bad: their
+            // number), in place of the groups' keys.
+            __syncthreads();
+            int mine = 0;
+            for (int g = tid; g < n_groups; g += THREADS) mine += (uint32_t)(groups[g] >> 32) >= bound;
+            const int upto = cta_scan<THREADS>(mine, S.sums);
+            if (tid == THREADS - 1) S.bad = upto;
+            int* const reach = reinterpret_cast<int*>(s_key);   // room >= need groups, see below
+            int at = upto - mine;
+            for (int g = tid; g < n_groups; g += THREADS)
+                if ((uint32_t)(groups[g] >> 32) >= bound) {
+                    if (at < 2 * P.room) reach[at] = g;
+                    ++at;
+                }
+            __syncthreads();
+            const int n_reach = S.bad;
+            if (n_reach <= P.room_groups && n_reach <= 2 * P.room) {
+                // Their list moves behind, where the groups' keys were.
+                int* const list = reinterpret_cast<int*>(groups);
+                for (int i = tid; i < n_reach; i += THREADS) list[i] = reach[i];
+                __syncthreads();
+                const int each = per * 8;
+                for (int i = tid; i < n_reach * each; i += THREADS) {
+                    const int b = list[i / each] * each + i % each;
+                    if (b < R.lo || b >= R.hi) continue;
+                    const float v = s[b];
+                    if (v == v && ordered(v) >= bound) {
+                        const int to = atomicAdd(&S.total, 1);
+                        if (to < P.room) s_key[to] = make_key(v, b);
+                    }
+                }
+                __syncthreads();
+                const int total = S.total;
+                if (total >= R.need && total <= P.room) {
+                    best_of<THREADS>(R, s_key, total, out, bits, S);
+                    return;
+                }
+            }
+        }
+    }
     scan_best<THREADS>(R, [&](int b) { return s[b]; }, out, S);
 }
 
 // ------------------------------------------------------------ the bound
 struct BoundParams {
-    const float* scores;     // the sampled blocks' [rows, stride]
+    const float* maxima;     // of the sampled blocks' groups [rows, stride]
     long long stride;
+    int log2_group;
+    int rows;
     int pos0, max_sel, n_first, n_last;
     float* bound;            // per row
-    uint2* list;             // (score, column) of the sample's own candidates [rows][cap]
-    int* counts;             // their number; -1: too many, the row is searched block by block
-    int cap;
 };
 
-// A lower bound on the need-th best score, from the sample: the leading 22 bits
-// of the sample's need-th best (11 bits at a time), -inf if the sample is
-// smaller than need, +inf for a row that needs none.
+constexpr int BOUND_HELD = 32;    // maxima a lane keeps in registers
+constexpr int BOUND_STEPS = 20;
+
+// One warp a row: a number that at least `need` group maxima, so at least
+// `need` of the row's scores, reach: a limit that exactly the need largest
+// reach, or close below the need-th largest (halving the range of their order
+// at most 20 times).  The smallest finite number if there are too few; none for
+// a row that needs none.
 __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
-    __shared__ int s_hist[2048];
-    __shared__ int s_sum[8];
-    __shared__ int s_digit, s_left, s_count;
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (row >= P.rows) return;
     const RowRange R = row_range(P.pos0 + row, P.max_sel, P.n_first, P.n_last);
     if (R.need == 0) {
-        if (tid == 0) {
-            P.bound[row] = INFINITY;
-            P.counts[row] = 0;
-        }
+        if (lane == 0) P.bound[row] = kNoBound;
         return;
     }
-    const float* s = P.scores + row * P.stride;
-    const int c0 = (R.lo + STRIDE - 1) / STRIDE, c1 = cols_below<SAMPLE>(R.hi);
-    uint32_t prefix = 0;
-    if (c1 - c0 >= R.need) {
-        int need = R.need;
-        for (int shift = 21; shift >= 10; shift -= 11) {
-            for (int i = tid; i < 2048; i += 256) s_hist[i] = 0;
-            __syncthreads();
-            for (int c = c0 + tid; c < c1; c += 256) {
-                const uint32_t k = ordered(s[c]);
-                if (shift == 21 || (k >> 21) == (prefix >> 21))
-                    atomicAdd(&s_hist[(k >> shift) & 2047], 1);
-            }
-            __syncthreads();
-            // Thread t holds bins 2047 - 8 t .. 2040 - 8 t, highest first.
-            int cnt[8], sum = 0;
+    const float* m = P.maxima + row * P.stride;
+    const int cols = cols_below<MAXIMA>(R.hi);
+    // (at least 1: one maximum is read whether it counts or not)
+    const int n = max((cols + (1 << P.log2_group) - 1) >> P.log2_group, 1);
+    // Maxima that are not numbers above -inf count for nothing (key 0).
+    auto key_of = [&](int i) {
+        const float v = m[min(i, n - 1)];
+        return i < n && v > -INFINITY ? ordered(v) : 0u;
+    };
+    uint32_t held[BOUND_HELD];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cnt[i] = s_hist[2047 - 8 * tid - i];
-                sum += cnt[i];
-            }
-            int incl = sum;
+    for (int i = 0; i < BOUND_HELD; ++i) held[i] = key_of(i * 32 + lane);
+    const bool more = n > BOUND_HELD * 32;
+    auto count = [&](uint32_t key) {
+        int c = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) s_sum[warp] = incl;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) incl += s_sum[w];
-            int before = incl - sum;
-            if (before < need && need <= incl) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (before < need && need <= before + cnt[i]) {
-                        s_digit = 2047 - 8 * tid - i;
-                        s_left = need - before;
-                    }
-                    before += cnt[i];
-                }
-            }
-            __syncthreads();
-            prefix |= (uint32_t)s_digit << shift;
-            need = s_left;
+        for (int i = 0; i < BOUND_HELD; ++i) c += held[i] >= key;
+        if (more)
+            for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) c += key_of(i) >= key;
+        return (int)__reduce_add_sync(0xffffffffu, c);
+    };
+    uint32_t most = 0, least = 0xffffffffu;
+    auto see = [&](uint32_t k) {
+        if (k) {
+            most = max(most, k);
+            least = min(least, k);
         }
-    }
-    float bound = -INFINITY;
-    if (prefix > kOrderedMinusInf)
-        bound = __uint_as_float(prefix & 0x80000000u ? prefix & 0x7fffffffu : ~prefix);
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    uint2* list = P.list + (long long)row * P.cap;
-    for (int c = c0 + tid; c < c1; c += 256) {
-        const float v = s[c];
-        if (v >= bound) {
-            const int i = atomicAdd(&s_count, 1);
-            if (i < P.cap) list[i] = make_uint2(__float_as_uint(v), (uint32_t)c);
+    };
+#pragma unroll
+    for (int i = 0; i < BOUND_HELD; ++i) see(held[i]);
+    if (more)
+        for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) see(key_of(i));
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    float bound = -3.402823466e38f;
+    if (most && count(least) >= R.need) {
+        // At least need maxima reach lo; fewer reach lo + width + 1.
+        uint32_t lo = least, width = most - least;
+        for (int i = 0; i < BOUND_STEPS && width; ++i) {
+            const uint32_t step = width / 2 + 1;
+            const int c = count(lo + step);
+            if (c >= R.need) {
+                lo += step;
+                width = c == R.need ? 0 : width - step;
+            } else {
+                width = step - 1;
+            }
         }
+        bound = __uint_as_float(lo & 0x80000000u ? lo & 0x7fffffffu : ~lo);
     }
-    __syncthreads();
-    if (tid == 0) {
-        const bool fits = s_count <= P.cap;
-        P.bound[row] = fits ? bound : INFINITY;
-        P.counts[row] = fits ? s_count : -1;
-    }
+    if (lane == 0) P.bound[row] = bound;
 }
 
 // ------------------------------------------------------------ best of the candidates
 struct BestParams {
     PickParams K;
-    DotParams D;             // the REST products' (lists, counts, schedule)
-    const uint2* list;       // the sample's
-    const int* counts;
-    int cap;
+    DotParams D;             // the products' lists and schedule
     int room;                // candidates a CTA holds
     IndexView V;             // for rows searched block by block
     const int8_t* codes;
 };
 
-constexpr int BEST_THREADS = 256;
+constexpr int BEST_THREADS = 128;
+constexpr int MAX_LISTS = 2 * 80;   // two a run; a row tile's runs are at most the pairs
 
 __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) {
-    extern __shared__ unsigned long long s_key[];   // [room]
-    __shared__ ScanShared S;
-    __shared__ int s_total, s_bad, s_count;
-    __shared__ unsigned long long s_prefix;
-    __shared__ int s_ids[kMaxSelect];
+    extern __shared__ Key s_key[];   // [room], then the ids' bits
+    __shared__ BestShared<BEST_THREADS> S;
+    __shared__ int s_n[MAX_LISTS], s_at[MAX_LISTS];
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
     if (write_plain(P.K, R, row, out)) return;
-    if (tid == 0) {
-        s_total = s_bad = 0;
-        s_count = 0;
-    }
+    if (tid == 0) S.total = S.bad = 0;
     __syncthreads();
     if (R.need > 0) {
         // Runs of this row's row tile.
         const int rt = row / PAIR_ROWS;
         long long cum = 0;
-        for (int t = 0; t < rt; ++t) cum += col_tiles<REST>(P.D, t);
-        const int nt = col_tiles<REST>(P.D, rt);
-        const int runs =
-            nt ? pair_of(P.D, cum + nt - 1) - pair_of(P.D, cum) + 1 : 0;
-        // A warp per list: the sample's, then two per run.
-        for (int l = warp; l < 1 + 2 * runs; l += BEST_THREADS / 32) {
-            const long long at = (long long)row * P.D.segs * 2 + (l - 1);
-            const int n = l == 0 ? P.counts[row] : P.D.counts[at];
-            const int cap = l == 0 ? P.cap : P.D.cap;
-            if (n < 0 || n > cap) {
-                s_bad = 1;
-                continue;
-            }
-            const uint2* src = l == 0 ? P.list + (long long)row * P.cap : P.D.list + at * cap;
-            int to = 0;
-            if (lane == 0) to = atomicAdd(&s_total, n);
-            to = __shfl_sync(0xffffffffu, to, 0);
-            if (to + n > P.room) {
-                s_bad = 1;
-                continue;
-            }
-            for (int i = lane; i < n; i += 32) {
-                const uint2 e = src[i];
-                const uint32_t b = l == 0 ? (uint32_t)col_block<SAMPLE>((int)e.y)
-                                          : (uint32_t)col_block<REST>((int)e.y);
-                // Higher is better: the score's order, then the lower id.
-                s_key[to + i] =
-                    ((unsigned long long)ordered(__uint_as_float(e.x)) << 32) | (0xffffffffu - b);
-            }
+        for (int t = 0; t < rt; ++t) cum += col_tiles<CANDIDATES>(P.D, t);
+        const int nt = col_tiles<CANDIDATES>(P.D, rt);
+        const int runs = nt ? pair_of(P.D, cum + nt - 1) - pair_of(P.D, cum) + 1 : 0;
+        const int lists = 2 * runs;
+        const long long at = (long long)row * P.D.segs * 2;
+        for (int l = tid; l < lists; l += BEST_THREADS) {
+            const int n = P.D.counts[at + l];
+            const bool bad = n < 0 || n > P.D.cap;
+            const int to = bad ? 0 : atomicAdd(&S.total, n);
+            if (bad || to + n > P.room) S.bad = 1;
+            s_n[l] = n;
+            s_at[l] = to;
         }
+        __syncthreads();
+        // A warp per list.
+        if (!S.bad)
+            for (int l = warp; l < lists; l += BEST_THREADS / 32) {
+                const uint2* src = P.D.list + (at + l) * P.D.cap;
+                const int n = s_n[l];
+                Key* to = s_key + s_at[l];
+#pragma unroll 4
+                for (int i = lane; i < n; i += 32) {
+                    const uint2 e = src[i];
+                    to[i] = make_key(__uint_as_float(e.x), (int)e.y);
+                }
+            }
     }
     __syncthreads();
-    const int total = s_total;
-    if (s_bad || total < R.need) {
-        // Searched block by block; a row of zero codes needs no products.
-        __syncthreads();
-        const uint4* q = reinterpret_cast<const uint4*>(P.codes + (long long)row * P.V.width);
-        bool any = false;
-        for (int i = tid; i < P.V.width / 16; i += BEST_THREADS) {
-            const uint4 u = q[i];
-            any = any || (u.x | u.y | u.z | u.w);
-        }
-        const bool zero = !__syncthreads_or(any);
-        scan_best<BEST_THREADS>(
-            R,
-            [&](int b) {
-                const long long block = physical_block(P.V, b);
-                int dot = 0;
-                if (!zero) {
-                    const uint4* k =
-                        reinterpret_cast<const uint4*>(P.V.index + block * P.V.width);
-                    for (int i = 0; i < P.V.width / 16; ++i) {
-                        const uint4 x = q[i], y = k[i];
-                        dot = __dp4a((int)x.x, (int)y.x, dot);
-                        dot = __dp4a((int)x.y, (int)y.y, dot);
-                        dot = __dp4a((int)x.z, (int)y.z, dot);
-                        dot = __dp4a((int)x.w, (int)y.w, dot);
-                    }
-                }
-                return __fmul_rn((float)dot, P.V.scale[block]);
-            },
-            out, S);
+    const int total = S.total;
+    if (!S.bad && total >= R.need) {
+        best_of<BEST_THREADS>(R, s_key, total, out, reinterpret_cast<uint32_t*>(s_key + P.room),
+                              S);
         return;
     }
-    // The need-th best key, eight bits at a time, until the keys that share
-    // the bits found are all taken.
-    unsigned long long prefix = 0;
-    int need = R.need;
-    for (int shift = 56; need > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += BEST_THREADS) S.hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < total; i += BEST_THREADS) {
-            const unsigned long long k = s_key[i];
-            if (shift == 56 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&S.hist[(int)(k >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            int left = need;
-            const int d = pick_digit(S.hist, lane, &left);
-            if (lane == 0) {
-                // All of bin d taken: what is above or in it is the answer.
-                S.need = S.hist[d] == left ? 0 : left;
-                s_prefix = prefix | ((unsigned long long)d << shift);
-            }
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = S.need;
-        __syncthreads();
+    // Searched block by block; a row of zero codes needs no products.
+    const uint4* q = reinterpret_cast<const uint4*>(P.codes + (long long)row * P.V.width);
+    bool any = false;
+    for (int i = tid; i < P.V.width / 16; i += BEST_THREADS) {
+        const uint4 u = q[i];
+        any = any || (u.x | u.y | u.z | u.w);
     }
-    for (int i = tid; i < total; i += BEST_THREADS) {
-        const unsigned long long k = s_key[i];
-        if (R.need > 0 && k >= prefix)
-            s_ids[atomicAdd(&s_count, 1)] = (int)(0xffffffffu - (uint32_t)k);
-    }
-    __syncthreads();
-    // The blocks that are always taken, and room for a power of two.
-    for (int i = tid; i < R.lo; i += BEST_THREADS) s_ids[R.need + i] = i;
-    for (int i = tid; i < R.n_vis - R.hi; i += BEST_THREADS) s_ids[R.need + R.lo + i] = R.hi + i;
-    int pow2 = 1;
-    while (pow2 < R.take) pow2 <<= 1;
-    for (int i = R.take + tid; i < pow2; i += BEST_THREADS) s_ids[i] = 0x7fffffff;
-    // Ids ascending: bitonic sort.
-    for (int k = 2; k <= pow2; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            __syncthreads();
-            for (int i = tid; i < pow2 / 2; i += BEST_THREADS) {
-                const int a = (i / j) * 2 * j + i % j, b = a + j;
-                const int x = s_ids[a], y = s_ids[b];
-                if ((x > y) == ((a & k) == 0)) {
-                    s_ids[a] = y;
-                    s_ids[b] = x;
+    const bool zero = !__syncthreads_or(any);
+    scan_best<BEST_THREADS>(
+        R,
+        [&](int b) {
+            const long long block = physical_block(P.V, b);
+            int dot = 0;
+            if (!zero) {
+                const uint4* k = reinterpret_cast<const uint4*>(P.V.index + block * P.V.width);
+                for (int i = 0; i < P.V.width / 16; ++i) {
+                    const uint4 x = q[i], y = k[i];
+                    dot = __dp4a((int)x.x, (int)y.x, dot);
+                    dot = __dp4a((int)x.y, (int)y.y, dot);
+                    dot = __dp4a((int)x.z, (int)y.z, dot);
+                    dot = __dp4a((int)x.w, (int)y.w, dot);
                 }
             }
-        }
-    __syncthreads();
-    for (int i = tid; i < R.take; i += BEST_THREADS) out[i] = s_ids[i];
+            return __fmul_rn((float)dot, P.V.scale[block]);
+        },
+        out, S);
 }
 
 // ------------------------------------------------------------ host side
@@ -990,35 +1211,35 @@ constexpr int FEW_ROWS = 32;
 // Below this many blocks, or this many per block taken, all scores are kept.
 constexpr int SAMPLE_MIN_BLOCKS = 2048;
 constexpr int SAMPLE_MIN_RATIO = 16;
-constexpr size_t SCORE_BYTES = 128ull << 20;   // scores held at once
+constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 256ull << 20;    // candidates held at once
+constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
+
+bool sampled(int n, int max_sel) {
+    return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel;
+}
 
 // Where a call keeps what in the workspace.  Every area grows with the rows
-// and the blocks, so the size for a context's last block holds for any n_last
-// and max_sel.
+// and the blocks and is sized for any max_sel, so the size for a context's
+// last block holds for every call on it.
 struct Layout {
-    long long stride;         // scores of a row
+    long long stride;         // scores (or sampled columns) of a row
     int chunk;                // most rows of a launch, by the scores
-    size_t codes, scores, codes16, cols, first_scale, rest_scale, bound, scounts, counts, list;
+    size_t codes, scores, maxima, codes16, cols, scale, sample_scale, bound, counts, list;
     size_t counts_bytes, list_bytes, bytes;
 };
 
-size_t list_row_bytes(int segs, int cap, int cap_sample) {
-    return ((size_t)segs * 2 * cap + cap_sample) * 8;
-}
+size_t list_row_bytes(int segs, int cap) { return (size_t)segs * 2 * cap * 8; }
 int list_cap(int max_sel, long long tiles_per_pair) {
-    const long long most = tiles_per_pair * (TILE / 2);
-    return (int)(most < 4 * max_sel + 64 ? most : 4 * max_sel + 64);
-}
-int sample_cap(int max_sel, int n_sample) {
-    return n_sample < 2 * max_sel + 64 ? n_sample : 2 * max_sel + 64;
+    const long long most = tiles_per_pair * (TILE / 2), want = 4 * max_sel + 64;
+    return (int)(most < want ? most : want);
 }
 
-// n: blocks scored; n_first: columns whose scores are kept (n, or the sample).
-Layout layout(int rows, int n, int n_first, int width, int pairs) {
+// n: blocks scored; kept: scores kept of a row (n, or the sample's).
+Layout layout(int rows, int n, int kept, int width, int pairs) {
     Layout L = {};
     const bool few = rows <= FEW_ROWS;
-    L.stride = round_up(n_first > 0 ? n_first : 1, TILE);
+    L.stride = round_up(kept > 0 ? kept : 1, TILE);
     const size_t row_bytes = (size_t)L.stride * 4;
     size_t at = kWorkspaceCounterBytes;
     auto take = [&](size_t bytes) {
@@ -1034,28 +1255,24 @@ Layout layout(int rows, int n, int n_first, int width, int pairs) {
         L.chunk = (int)(scores / row_bytes / PAIR_ROWS) * PAIR_ROWS;
     L.codes = take((size_t)rows * width);
     L.scores = take(scores);
-    if (!few) {
+    if (few) {
+        L.maxima = take(scores / 8);
+    } else {
         L.codes16 = take((size_t)rows * width * 2);
         L.cols = take((size_t)n * width * 2);
-        L.first_scale = take(row_bytes);
-        L.rest_scale = take((size_t)round_up(n, TILE) * 4);
+        L.scale = take((size_t)round_up(n, TILE) * 4);
+        L.sample_scale = take((size_t)round_up(n, TILE) * 4);
         L.bound = take(rows_up * 4);
-        L.scounts = take(rows_up * 4);
         L.counts_bytes = ((size_t)PAIR_ROWS * pairs + 2 * rows_up) * 2 * 4;
         L.counts = take(L.counts_bytes);
         // One row tile fits with any max_sel.
         const long long tiles = (round_up(n, TILE) / TILE + pairs - 1) / pairs + 1;
-        const size_t one = PAIR_ROWS * list_row_bytes(pairs, list_cap(kMaxSelect, tiles),
-                                                      sample_cap(kMaxSelect, n_first));
+        const size_t one = PAIR_ROWS * list_row_bytes(pairs, list_cap(kMaxSelect, tiles));
         L.list_bytes = one > LIST_BYTES ? one : LIST_BYTES;
         L.list = take(L.list_bytes);
     }
     L.bytes = at;
     return L;
-}
-
-bool sampled(int n, int max_sel) {
-    return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel;
 }
 
 // Pairs that can be resident at once (both SMs of a pair in one GPC).
@@ -1065,7 +1282,7 @@ int max_pairs(const DeviceInfo* di) {
         const int c = cached[di->device].load(std::memory_order_relaxed);
         if (c) return c;
     }
-    if (ensure_smem_limit(reinterpret_cast<const void*>(dot_kernel<ALL, true>),
+    if (ensure_smem_limit(reinterpret_cast<const void*>(dot_kernel<SCORES, true>),
                           DotCfg<true>::SMEM) != GQA_OK)
         return 0;
     cudaLaunchConfig_t cfg = {};
@@ -1080,26 +1297,28 @@ int max_pairs(const DeviceInfo* di) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, dot_kernel<ALL, true>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, dot_kernel<SCORES, true>, &cfg) != cudaSuccess ||
+        n < 1) {
         cudaGetLastError();
         return 0;
     }
     if (n > di->num_sms / 2) n = di->num_sms / 2;
+    if (n > MAX_LISTS / 2) n = MAX_LISTS / 2;
     if (di->device < 64) cached[di->device].store(n, std::memory_order_relaxed);
     return n;
 }
 
 // The schedule of a launch's products: pairs and, per row tile, the most runs.
-template <int ORDER>
+template <int MODE>
 void schedule(DotParams& D, int pairs) {
     D.row_tiles = (D.rows + PAIR_ROWS - 1) / PAIR_ROWS;
     D.total = 0;
-    for (int t = 0; t < D.row_tiles; ++t) D.total += col_tiles<ORDER>(D, t);
+    for (int t = 0; t < D.row_tiles; ++t) D.total += col_tiles<MODE>(D, t);
     D.G = (int)(D.total < pairs ? D.total : pairs);
     D.segs = 1;
     long long cum = 0;
     for (int t = 0; t < D.row_tiles && D.total > 0; ++t) {
-        const int n = col_tiles<ORDER>(D, t);
+        const int n = col_tiles<MODE>(D, t);
         if (n > 0) {
             const int s = pair_of(D, cum + n - 1) - pair_of(D, cum) + 1;
             if (s > D.segs) D.segs = s;
@@ -1108,25 +1327,52 @@ void schedule(DotParams& D, int pairs) {
     }
 }
 
-template <int ORDER>
-int launch_dots(const __half* rows16, const __half* cols, int n_cols, const DotParams& D,
+// cols: [blocks, width]; the columns of MAXIMA are its every STRIDE-th row.
+template <int MODE>
+int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams& D,
                 cudaStream_t stream) {
     if (D.total == 0) return GQA_OK;
-    const int width = D.chunks * 64;
+    const int width = D.chunks * 64, skip = MODE == MAXIMA ? STRIDE : 1;
     CUtensorMap tr, tc;
     if (!make_map_2d_f16(&tr, rows16, D.rows, width, width, CTA_ROWS, 64) ||
-        !make_map_2d_f16(&tc, cols, n_cols, width, width, CTA_ROWS, 64))
+        !make_map_2d_f16(&tc, cols, cols_below<MODE>(n), width, (uint64_t)width * skip, CTA_ROWS,
+                         64))
         return GQA_ERR_CUDA;
     const bool resident = D.chunks <= RES_CHUNKS;
     const int smem = resident ? DotCfg<true>::SMEM : DotCfg<false>::SMEM;
-    auto* kernel = resident ? dot_kernel<ORDER, true> : dot_kernel<ORDER, false>;
+    auto* kernel = resident ? dot_kernel<MODE, true> : dot_kernel<MODE, false>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem) != GQA_OK)
         return GQA_ERR_CUDA;
     kernel<<<2 * D.G, DOT_THREADS, smem, stream>>>(tr, tc, D);
     return GQA_OK;
 }
 
-constexpr int BEST_SMEM = 200 << 10;
+// The bits of the block ids a launch's rows see, one window at a time.
+size_t bits_bytes(const PickParams& K, int rows) {
+    const int ids = ((K.pos0 + rows - 1) >> 2) + 1;
+    return (size_t)((ids < WINDOW ? ids : WINDOW) + 31) / 32 * 4;
+}
+
+// room: candidates; groups: maxima.
+template <int THREADS>
+int launch_pick(const PickParams& K, int rows, const float* scores, long long stride,
+                const float* maxima, int n, cudaStream_t stream) {
+    ScorePick P = {K, scores, stride, maxima, 0, 0};
+    int want = 12 * K.max_sel + 1024;
+    const int most = PICK_SMEM / 8;
+    if (maxima) {
+        P.room_groups = 8192 < (n + 7) / 8 ? 8192 : (n + 7) / 8;
+        P.room = want < most - P.room_groups ? want : most - P.room_groups;
+    } else {
+        P.room = n < most ? n : most;
+    }
+    if (ensure_smem_limit(reinterpret_cast<const void*>(pick_kernel<THREADS>),
+                          PICK_SMEM + WINDOW / 8) != GQA_OK)
+        return GQA_ERR_CUDA;
+    const size_t smem = (size_t)(P.room + P.room_groups) * 8 + bits_bytes(K, rows);
+    pick_kernel<THREADS><<<rows, THREADS, smem, stream>>>(P);
+    return GQA_OK;
+}
 
 }  // namespace select
 
@@ -1136,9 +1382,7 @@ size_t select_blocks_workspace_bytes(int rows, int ctx_len, int width) {
     const int pairs = di ? max_pairs(di) : 0;
     if (pairs < 1) return 0;
     const int n = (ctx_len - 1) / 4 + 1;
-    const size_t all = layout(rows, n, n, width, pairs).bytes;
-    const size_t some = layout(rows, n, cols_below<SAMPLE>(n), width, pairs).bytes;
-    return all > some ? all : some;
+    return layout(rows, n, n, width, pairs).bytes;
 }
 
 int select_blocks_launch(const void* q, const int8_t* index, const float* index_scale,
@@ -1154,10 +1398,10 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     int n = ((ctx_len - 1) >> 2) + 1 - n_last;
     if (n <= n_first) n = 0;   // nothing to score
     const bool sample = !few && sampled(n, max_sel);
-    const int n_kept = sample ? cols_below<SAMPLE>(n) : n;
+    const int kept = sample ? cols_below<MAXIMA>(n) : n;
     const int pairs = max_pairs(di);
     if (pairs < 1) return GQA_ERR_CUDA;
-    const Layout L = layout(rows, n, n_kept, width, pairs);
+    const Layout L = layout(rows, n, kept, width, pairs);
     void* ws;
     size_t ws_bytes;
     current_workspace(&ws, &ws_bytes);
@@ -1168,100 +1412,93 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     const IndexView V = {index, index_scale, block_table, num_pages,
                          __builtin_ctz((unsigned)page) - 2, width, di->err_word};
     CodeParams C = {static_cast<const __half*>(q), rows, Hq, D, Hq / Hkv, width, codes, nullptr};
-    const int code_ctas = (rows + 7) / 8;
     const int pos0 = ctx_len - rows;
     PickParams K = {pos0, max_sel, n_first, n_last, sel_idx, sel_cnt};
+    int rc = GQA_OK;
     if (few) {
+        float* maxima = reinterpret_cast<float*>(w + L.maxima);
         if (n > 0) {
-            prepare_kernel<<<code_ctas, 256, 0, stream>>>(C, ExpandParams{}, code_ctas);
-            const SmallParams S = {V, codes, rows, n, scores, L.stride};
-            const int tiles = (n + 31) / 32, cap = di->num_sms * 8;
-            const dim3 grid(tiles < cap ? tiles : cap, (rows + SMALL_ROWS - 1) / SMALL_ROWS);
-            score_small_kernel<<<grid, 256, 0, stream>>>(S);
+            const FewParams F = {C, V, n, pos0, n_first, n_last, scores, L.stride, maxima};
+            const int tiles = (n + 63) / 64, cap = di->num_sms * 4;
+            const dim3 grid(tiles < cap ? tiles : cap, (rows + FEW_TILE - 1) / FEW_TILE);
+            score_few_kernel<<<grid, 256, 0, stream>>>(F);
         }
-        pick_kernel<1024><<<rows, 1024, 0, stream>>>(K, scores, L.stride);
+        rc = launch_pick<1024>(K, rows, scores, L.stride, maxima, n, stream);
+        if (rc != GQA_OK) return rc;
         return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
     }
     __half* codes16 = reinterpret_cast<__half*>(w + L.codes16);
-    __half* first = reinterpret_cast<__half*>(w + L.cols);
-    float* first_scale = reinterpret_cast<float*>(w + L.first_scale);
-    float* rest_scale = reinterpret_cast<float*>(w + L.rest_scale);
+    __half* cols = reinterpret_cast<__half*>(w + L.cols);
+    float* scale = reinterpret_cast<float*>(w + L.scale);
+    float* sample_scale = reinterpret_cast<float*>(w + L.sample_scale);
     C.codes16 = codes16;
-    const ExpandParams E = {V, n_kept, n - n_kept, sample, first, first + (size_t)n_kept * width,
-                            first_scale, rest_scale};
     if (n > 0) {
+        const ExpandParams E = {V, n, cols, scale, sample ? sample_scale : nullptr};
+        const int code_ctas = (rows + 7) / 8;
         const long long threads = (long long)n * (width / 16);
-        const long long ctas = code_ctas + (threads + 255) / 256;
-        prepare_kernel<<<(unsigned)ctas, 256, 0, stream>>>(C, E, code_ctas);
+        prepare_kernel<<<(unsigned)(code_ctas + (threads + 255) / 256), 256, 0, stream>>>(
+            C, E, code_ctas);
     }
-    if (sample && ensure_smem_limit(reinterpret_cast<const void*>(best_kernel), BEST_SMEM) != GQA_OK)
+    if (sample && ensure_smem_limit(reinterpret_cast<const void*>(best_kernel),
+                                    PICK_SMEM + WINDOW / 8) != GQA_OK)
         return GQA_ERR_CUDA;
     int step = L.chunk;
     for (int r0 = 0; r0 < rows; r0 += step) {
         DotParams P = {};
+        P.rows = rows - r0 < step ? rows - r0 : step;
         P.chunks = width / 64;
         P.pos0 = pos0 + r0;
-        P.max_sel = max_sel;
         P.n_first = n_first;
         P.n_last = n_last;
-        P.scale = first_scale;
         P.scores = scores;
         P.stride = L.stride;
         P.err = di->err_word;
-        DotParams R = P;     // the REST products
-        const int cap_sample = sample_cap(max_sel, n_kept);
-        // Fewer rows a launch if their candidate lists would not fit.
-        for (;;) {
-            P.rows = R.rows = rows - r0 < step ? rows - r0 : step;
-            if (!sample) break;
-            schedule<REST>(R, pairs);
-            R.cap = R.G > 0 ? list_cap(max_sel, (R.total + R.G - 1) / R.G) : 1;
-            if (R.rows * list_row_bytes(R.segs, R.cap, cap_sample) <= L.list_bytes &&
-                (size_t)R.rows * R.segs * 2 * 4 <= L.counts_bytes)
-                break;
-            if (step <= PAIR_ROWS) return GQA_ERR_WORKSPACE;   // does not happen: see layout()
-            step = round_up(R.rows, PAIR_ROWS) - PAIR_ROWS;
-        }
         K.pos0 = pos0 + r0;
         K.sel_idx = sel_idx + (size_t)r0 * max_sel;
         K.sel_cnt = sel_cnt + r0;
         const __half* rows16 = codes16 + (size_t)r0 * width;
-        int rc;
         if (!sample) {
-            schedule<ALL>(P, pairs);
-            if (n == 0) P.total = 0;
-            rc = launch_dots<ALL>(rows16, first, n_kept, P, stream);
+            P.scale = scale;
+            schedule<SCORES>(P, pairs);
+            if (n > 0) rc = launch_dots<SCORES>(rows16, cols, n, P, stream);
+            if (rc == GQA_OK)
+                rc = launch_pick<256>(K, P.rows, scores, L.stride, nullptr, n, stream);
             if (rc != GQA_OK) return rc;
-            pick_kernel<256><<<P.rows, 256, 0, stream>>>(K, scores, L.stride);
             continue;
         }
-        schedule<SAMPLE>(P, pairs);
-        rc = launch_dots<SAMPLE>(rows16, first, n_kept, P, stream);
+        DotParams R = P;     // the candidates' products
+        // Fewer rows a launch if their candidate lists would not fit.
+        for (;;) {
+            schedule<CANDIDATES>(R, pairs);
+            R.cap = R.G > 0 ? list_cap(max_sel, (R.total + R.G - 1) / R.G) : 32;
+            if (R.rows * list_row_bytes(R.segs, R.cap) <= L.list_bytes &&
+                (size_t)R.rows * R.segs * 2 * 4 <= L.counts_bytes)
+                break;
+            if (R.rows <= PAIR_ROWS) return GQA_ERR_WORKSPACE;   // layout() leaves room for these
+            step = round_up(R.rows, PAIR_ROWS) - PAIR_ROWS;
+            P.rows = R.rows = step;
+        }
+        P.scale = sample_scale;
+        // Groups as large as leave four times as many maxima as blocks taken.
+        while (P.log2_group < 3 && (kept >> (P.log2_group + 1)) >= 4 * max_sel) ++P.log2_group;
+        P.stride = L.stride >> P.log2_group;
+        schedule<MAXIMA>(P, pairs);
+        rc = launch_dots<MAXIMA>(rows16, cols, n, P, stream);
         if (rc != GQA_OK) return rc;
         float* bound = reinterpret_cast<float*>(w + L.bound);
-        int* scounts = reinterpret_cast<int*>(w + L.scounts);
-        uint2* slist = reinterpret_cast<uint2*>(w + L.list);
-        const BoundParams B = {scores, L.stride, K.pos0, max_sel, n_first, n_last,
-                               bound, slist, scounts, cap_sample};
-        bound_kernel<<<P.rows, 256, 0, stream>>>(B);
-        R.scale = rest_scale;
-        R.scores = nullptr;
+        const BoundParams B = {scores, P.stride, P.log2_group, P.rows, K.pos0, max_sel, n_first,
+                               n_last, bound};
+        bound_kernel<<<(P.rows + 7) / 8, 256, 0, stream>>>(B);
+        R.scale = scale;
         R.bound = bound;
-        R.list = slist + (size_t)R.rows * cap_sample;
+        R.list = reinterpret_cast<uint2*>(w + L.list);
         R.counts = reinterpret_cast<int*>(w + L.counts);
-        rc = launch_dots<REST>(rows16, E.rest, E.n_rest_cols, R, stream);
+        rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
-        BestParams T = {};
-        T.K = K;
-        T.D = R;
-        T.list = slist;
-        T.counts = scounts;
-        T.cap = cap_sample;
-        T.room = 12 * max_sel + 1024;
-        if (T.room > BEST_SMEM / 8) T.room = BEST_SMEM / 8;
-        T.V = V;
-        T.codes = codes + (size_t)r0 * width;
-        best_kernel<<<R.rows, BEST_THREADS, (size_t)T.room * 8, stream>>>(T);
+        BestParams T = {K, R, 12 * max_sel + 512, V, codes + (size_t)r0 * width};
+        if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
+        best_kernel<<<R.rows, BEST_THREADS, (size_t)T.room * 8 + bits_bytes(K, R.rows), stream>>>(
+            T);
     }
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
