@@ -62,10 +62,10 @@ __device__ __forceinline__ RowRange row_range(int pos, int max_sel, int n_first,
     return r;
 }
 
-// A float's order as whole numbers; NaN below everything.  Adding zero makes
-// the two zeros one.
+// A float's order as whole numbers above 0; NaN, as 1, below everything.  Adding
+// zero makes the two zeros one.
 __device__ __forceinline__ uint32_t ordered(float f) {
-    if (f != f) return 0;
+    if (f != f) return 1;
     const uint32_t u = __float_as_uint(f + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -122,13 +122,15 @@ struct CodeParams {
 constexpr float kSplit = 196608.f;   // 1.5 * 2^17
 constexpr int kSplitBits = 0x48400000;
 
+// CHUNKS: 256-wide pieces of a row.
+template <int CHUNKS>
 __device__ __forceinline__ void query_codes(const CodeParams& P, int row, int lane,
-                                            uint2 (&w)[4]) {
-    float s[4][8];
+                                            uint2 (&w)[CHUNKS]) {
+    float s[CHUNKS][8];
     float most = 0.f;
     bool fine = true;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < CHUNKS; ++c) {
         const int e = c * 256 + lane * 8;
         if (c * 256 >= P.width) break;
         if (e >= P.width) {
@@ -172,7 +174,7 @@ __device__ __forceinline__ void query_codes(const CodeParams& P, int row, int la
     fine = fine && most > 0.f;
     const float inv = fine ? 127.f / most : 0.f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < CHUNKS; ++c) {
         if (c * 256 >= P.width) break;
         uint32_t x[2] = {0, 0};
 #pragma unroll
@@ -184,10 +186,11 @@ __device__ __forceinline__ void query_codes(const CodeParams& P, int row, int la
     }
 }
 
+template <int CHUNKS>
 __device__ __forceinline__ void store_codes(const CodeParams& P, int row, int lane,
-                                            const uint2 (&w)[4]) {
+                                            const uint2 (&w)[CHUNKS]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < CHUNKS; ++c) {
         const int e = c * 256 + lane * 8;
         if (e >= P.width) break;
         const long long at = (long long)row * P.width + e;
@@ -210,32 +213,47 @@ struct ExpandParams {
 };
 
 // The first `code_ctas` CTAs make query codes (8 rows each), the others
-// expand blocks (16 codes a thread).
+// expand EXPAND_PASSES x (256 / (width / 16)) blocks, 16 codes a thread and
+// pass, all passes' loads in flight together.
+constexpr int EXPAND_PASSES = 4;
+
+template <int CHUNKS>
 __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const ExpandParams E,
                                                       int code_ctas) {
     if ((int)blockIdx.x < code_ctas) {
         const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
         if (row >= C.rows) return;
-        uint2 w[4];
-        query_codes(C, row, lane, w);
-        store_codes(C, row, lane, w);
+        uint2 w[CHUNKS];
+        query_codes<CHUNKS>(C, row, lane, w);
+        store_codes<CHUNKS>(C, row, lane, w);
         return;
     }
-    const int per_col = E.V.width / 16;
-    const long long i = (long long)(blockIdx.x - code_ctas) * 256 + threadIdx.x;
-    const int b = (int)(i / per_col), part = (int)(i - (long long)b * per_col);
-    if (b >= E.n) return;
-    const long long block = physical_block(E.V, b);
-    const uint4 w = *reinterpret_cast<const uint4*>(E.V.index + block * E.V.width + part * 16);
-    __half* dst = E.cols + (long long)b * E.V.width + part * 16;
-    const uint2 x = codes_half4(w.x), y = codes_half4(w.y), z = codes_half4(w.z),
-                u = codes_half4(w.w);
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(x.x, x.y, y.x, y.y);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(z.x, z.y, u.x, u.y);
-    if (part == 0) {
-        const float s = E.V.scale[block];
-        E.scale[b] = s;
-        if (E.sample_scale && b % STRIDE == 0) E.sample_scale[b / STRIDE] = s;
+    const int per_block = E.V.width / 16, at_once = 256 / per_block;
+    const int mine = threadIdx.x / per_block, part = threadIdx.x - mine * per_block;
+    if (mine >= at_once) return;
+    const int b0 = (blockIdx.x - code_ctas) * at_once * EXPAND_PASSES + mine;
+    long long block[EXPAND_PASSES];
+    uint4 w[EXPAND_PASSES];
+#pragma unroll
+    for (int i = 0; i < EXPAND_PASSES; ++i)
+        block[i] = physical_block(E.V, min(b0 + i * at_once, E.n - 1));
+#pragma unroll
+    for (int i = 0; i < EXPAND_PASSES; ++i)
+        w[i] = *reinterpret_cast<const uint4*>(E.V.index + block[i] * E.V.width + part * 16);
+#pragma unroll
+    for (int i = 0; i < EXPAND_PASSES; ++i) {
+        const int b = b0 + i * at_once;
+        if (b >= E.n) break;
+        __half* dst = E.cols + (long long)b * E.V.width + part * 16;
+        const uint2 x = codes_half4(w[i].x), y = codes_half4(w[i].y), z = codes_half4(w[i].z),
+                    u = codes_half4(w[i].w);
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(x.x, x.y, y.x, y.y);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(z.x, z.y, u.x, u.y);
+        if (part == 0) {
+            const float s = E.V.scale[block[i]];
+            E.scale[b] = s;
+            if (E.sample_scale && b % STRIDE == 0) E.sample_scale[b / STRIDE] = s;
+        }
     }
 }
 
@@ -245,27 +263,33 @@ __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const 
 // M = 256, N = 256 UMMA stream issued by the even CTA into two tensor-memory
 // buffers.  Up to width 256 a pair keeps its rows' codes in shared memory for
 // all its tiles; beyond, they stream with the columns.  Warp 0 loads, warp 1
-// issues, warps 2..9 take the products: each thread one row and half of a
-// tile's columns.
+// issues, the others take the products: each thread one row and a quarter of a
+// tile's columns.  (With two warps a scheduler instead of four, each waiting on
+// its own chain of compares and stores, the products waited for them: 63
+// instead of ~TBD~ us over 4096 x 32000.)
 constexpr int CTA_ROWS = 128;
 constexpr int PAIR_ROWS = 256;
 constexpr int TILE = 256;                    // columns of a tile
 constexpr int CHUNK_BYTES = 128 * 128;       // 128 rows x 64 fp16
 constexpr int RES_CHUNKS = 4;                // row chunks kept (width 256)
-constexpr int EPI_WARPS = 8;
+constexpr int PARTS = 2;                     // warpgroups that share a tile's columns
+constexpr int PART = TILE / PARTS;
+constexpr int EPI_WARPS = 4 * PARTS;
 constexpr int DOT_THREADS = 32 * (2 + EPI_WARPS);
-constexpr int SCALE_BYTES = EPI_WARPS * 128 * 4;   // a warp's columns' scales
+constexpr int SCALE_BYTES = EPI_WARPS * PART * 4;   // a warp's columns' scales
+constexpr int DUMP_WORDS = 36;                      // 32 products of a row, 16-byte aligned
+constexpr int DUMP_BYTES = EPI_WARPS * 32 * DUMP_WORDS * 4;
 constexpr uint32_t DOT_TMEM = 512;
 constexpr uint32_t IDESC = idesc_f16_f32(256, TILE, false, false);
 
 template <bool RESIDENT>
 struct DotCfg {
-    static constexpr int SLOTS = RESIDENT ? 8 : 6;
+    static constexpr int SLOTS = RESIDENT ? 7 : 5;
     static constexpr int SLOT_BYTES = RESIDENT ? CHUNK_BYTES : 2 * CHUNK_BYTES;
     static constexpr int ROW_BYTES = RESIDENT ? RES_CHUNKS * CHUNK_BYTES : 0;
     static constexpr int NUM_BARS = 2 * SLOTS + 7;
     static constexpr int SMEM = 1024 + ROW_BYTES + SLOTS * SLOT_BYTES + SCALE_BYTES +
-                                NUM_BARS * 8 + 16;
+                                DUMP_BYTES + NUM_BARS * 8 + 16;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -282,8 +306,8 @@ struct DotParams {
     long long stride;
     int log2_group;            // MAXIMA: columns of a group, 1 to 8
     const float* bound;        // CANDIDATES: per row
-    uint2* list;               // CANDIDATES: (score, block) [rows][segs][2][cap]
-    int* counts;               // CANDIDATES: entries [rows][segs][2], -1: too many
+    uint2* list;               // CANDIDATES: (score, block) [rows][segs][PARTS][cap]
+    int* counts;               // CANDIDATES: entries [rows][segs][PARTS], -1: too many
     int segs, cap;
     unsigned* err;
 };
@@ -344,18 +368,11 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
                  : "memory");
 }
 
-// Stores (v, block) and moves on if v >= bound: predicated, since in nearly
-// every column some lane of the warp has a candidate and a branch would run
-// its body each time.
-__device__ __forceinline__ void keep_candidate(uint2*& to, float v, float bound, int block) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ge.f32 p, %1, %2;\n\t"
-        "@p st.global.v2.b32 [%0], {%3, %4};\n\t"
-        "@p add.u64 %0, %0, 8;\n\t}"
-        : "+l"(to)
-        : "f"(v), "f"(bound), "r"(__float_as_uint(v)), "r"(block)
-        : "memory");
+// max(a, b, c); a NaN gives way to a number.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 template <int MODE, bool RESIDENT>
@@ -368,7 +385,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t s_rows = base;
     const uint32_t s_ring = base + C::ROW_BYTES;
-    const uint32_t bars = s_ring + C::SLOTS * C::SLOT_BYTES + SCALE_BYTES;
+    const uint32_t bars = s_ring + C::SLOTS * C::SLOT_BYTES + SCALE_BYTES + DUMP_BYTES;
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (C::SLOTS + s); };
     const uint32_t rows_full = bars + 8 * (2 * C::SLOTS), rows_empty = rows_full + 8;
@@ -376,7 +393,8 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     auto tempty = [&](int i) { return rows_full + 32 + 8 * i; };   // buffer i read out
     const uint32_t drain = rows_full + 48;
     float* s_scale = reinterpret_cast<float*>(base_ptr + C::ROW_BYTES + C::SLOTS * C::SLOT_BYTES);
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(s_scale + SCALE_BYTES / 4 + C::NUM_BARS * 2);
+    float* s_dump = s_scale + SCALE_BYTES / 4;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(s_dump + DUMP_BYTES / 4 + C::NUM_BARS * 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -493,10 +511,12 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
         }
     } else {
         // ------------------------------------------------------------ scores
-        const int half = (warp - 2) >> 2;      // which 128 columns of a tile
+        const int part = (warp - 2) >> 2;      // which columns of a tile
         const int quarter = warp & 3;          // TMEM lanes this warp may read
-        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
-        float4* const my_scale = reinterpret_cast<float4*>(s_scale + (warp - 2) * 128);
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + part * PART;
+        float* const my_scale = s_scale + (warp - 2) * PART;
+        float* const my_dump = s_dump + ((warp - 2) * 32 + lane) * DUMP_WORDS;
+        static_assert(PART == 128, "four columns a lane");
         uint32_t t = 0;
         bool ok = true;
         while (ok && runs.next(P, pair, rt, jb, je, seg)) {
@@ -505,104 +525,142 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             const bool valid = row < P.rows;
             const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;     // this row's scored blocks end
             const int hi0 = ((P.pos0 + row0) >> 2) + 1 - P.n_last;   // the warp's smallest
-            float bound = MODE == CANDIDATES && valid ? P.bound[row] : kNoBound;
-            const long long at = (((long long)row * P.segs + seg) * 2 + half);
+            const float bound = MODE == CANDIDATES && valid ? P.bound[row] : kNoBound;
+            // Just below the bound, so that the sign of one fused multiply-add
+            // lets every score that reaches the bound through (and few others).
+            const float below = nextafterf(bound, -INFINITY);
+            uint32_t open = bound == bound ? 0xffffffffu : 0u;
+            const long long at = ((long long)row * P.segs + seg) * PARTS + part;
             uint2* const list = MODE == CANDIDATES ? P.list + at * P.cap : nullptr;
-            uint2* const full32 = list + (P.cap - 32);   // room for 32 more up to here
-            uint2* to = list;
-            bool over = false;
-            // The tile's scales: four a lane, loaded a tile ahead, then shared by
+            int n = 0;
+            // The columns' scales: four a lane, loaded a tile ahead, then shared by
             // the warp.
             const float4* scale4 =
-                reinterpret_cast<const float4*>(P.scale + jb * TILE + half * 128) + lane;
+                reinterpret_cast<const float4*>(P.scale + jb * TILE + part * PART) + lane;
             float4 ahead = __ldg(scale4);
             for (int j = jb; j < je; ++j, ++t) {
                 __syncwarp();
-                my_scale[lane] = ahead;
+                reinterpret_cast<float4*>(my_scale)[lane] = ahead;
                 if (j + 1 < je) ahead = __ldg(scale4 += TILE / 4);
                 __syncwarp();
                 ok = mbar_wait(tfull(t & 1), (t >> 1) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const int col0 = j * TILE + half * 128;
+                const int col0 = j * TILE + part * PART;
                 // Two tensor-memory loads in flight.
                 uint32_t r[2][32];
                 tmem_ld32(t_lane + (t & 1) * TILE, r[0]);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < PART / 32; ++g) {
                     const int c0 = col0 + g * 32;
-                    tmem_ld_wait<32>(r[g & 1]);
-                    if (g < 3) tmem_ld32(t_lane + (t & 1) * TILE + (g + 1) * 32, r[(g + 1) & 1]);
-                    float sc[32];
-                    if (g == 3) {
+                    uint32_t (&d)[32] = r[g & 1];
+                    tmem_ld_wait<32>(d);
+                    if (g + 1 < PART / 32)
+                        tmem_ld32(t_lane + (t & 1) * TILE + (g + 1) * 32, r[(g + 1) & 1]);
+                    else {
                         // The buffer is read out.
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) pairs::remote_arrive(pairs::leader_addr(tempty(t & 1)));
                     }
+                    const float4* sc4 = reinterpret_cast<const float4*>(my_scale + g * 32);
+                    // Columns on the rows' own blocks, behind them, or on the first
+                    // ones, are not scored.
+                    const bool edge =
+                        col_block<MODE>(c0) < P.n_first || col_block<MODE>(c0 + 31) >= hi0;
+                    if (MODE == CANDIDATES) {
+                        uint32_t under = 0;    // signs of score - bound, column i in bit i
+#pragma unroll
+                        for (int i = 7; i >= 0; --i) {
+                            const float4 f = sc4[i];
+                            const float s[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int k = 3; k >= 0; --k)
+                                under = __funnelshift_l(
+                                    __float_as_uint(fmaf(__uint_as_float(d[4 * i + k]), s[k],
+                                                         -below)),
+                                    under, 1);
+                        }
+                        uint32_t m = ~under & open;
+                        if (edge) {
+                            const int a = min(max(P.n_first - c0, 0), 32);
+                            const int b = min(max(hi - c0, 0), 32);
+                            m &= (b == 32 ? 0xffffffffu : (1u << b) - 1) &
+                                 (a == 32 ? 0u : 0xffffffffu << a);
+                        }
+                        if (!__any_sync(0xffffffffu, m)) continue;
+                        if (n + 32 > P.cap) {
+                            open = m = 0;    // no room: the row is searched block by block
+                            n = -1;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(my_dump)[i] =
+                                make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+                        // Each lane reads its own row's products only.
+                        while (m) {
+                            const int i = __ffs(m) - 1;
+                            m &= m - 1;
+                            const float v = __fmul_rn(my_dump[i], my_scale[g * 32 + i]);
+                            if (v >= bound) list[n++] = make_uint2(__float_as_uint(v), c0 + i);
+                        }
+                        continue;
+                    }
+                    float sc[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 f = my_scale[g * 8 + i];
-                        sc[4 * i] = __fmul_rn(__uint_as_float(r[g & 1][4 * i]), f.x);
-                        sc[4 * i + 1] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 1]), f.y);
-                        sc[4 * i + 2] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 2]), f.z);
-                        sc[4 * i + 3] = __fmul_rn(__uint_as_float(r[g & 1][4 * i + 3]), f.w);
+                        const float4 f = sc4[i];
+                        sc[4 * i] = __fmul_rn(__uint_as_float(d[4 * i]), f.x);
+                        sc[4 * i + 1] = __fmul_rn(__uint_as_float(d[4 * i + 1]), f.y);
+                        sc[4 * i + 2] = __fmul_rn(__uint_as_float(d[4 * i + 2]), f.z);
+                        sc[4 * i + 3] = __fmul_rn(__uint_as_float(d[4 * i + 3]), f.w);
                     }
+                    float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
                     if (MODE == SCORES) {
                         if (valid) {
-                            float* dst = P.scores + row * P.stride + c0;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
                         }
                         continue;
                     }
-                    if (col_block<MODE>(c0) < P.n_first || col_block<MODE>(c0 + 31) >= hi0) {
-                        // Columns on the rows' own blocks, behind them, or on the
-                        // first ones: not scored.
+                    if (edge) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int b = col_block<MODE>(c0 + i);
                             if (b < P.n_first || b >= hi) sc[i] = -INFINITY;
                         }
                     }
-                    if (MODE == MAXIMA) {
-                        if (!valid) continue;
-                        float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
-                        // fmaxf drops a NaN; a group of nothing else stays below -inf's key.
-                        if (P.log2_group == 0) {
+                    // Maxima drop a NaN; a group of nothing else counts for nothing.
+                    if (!valid) continue;
+                    if (P.log2_group == 3) {
+                        float m[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
-                            continue;
+                        for (int i = 0; i < 4; ++i) {
+                            const float* x = sc + 8 * i;
+                            m[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]),
+                                         fmaxf(x[6], x[7]));
                         }
+                        *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
+                    } else if (P.log2_group == 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
+                    } else {
                         float m[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) m[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
                         if (P.log2_group == 1) {
                             store8(dst, m);
                             store8(dst + 8, m + 8);
-                            continue;
-                        }
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
-                        if (P.log2_group == 2) {
+                            for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
                             store8(dst, m);
-                            continue;
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
-                        *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
-                        continue;
                     }
-                    if (to > full32) {
-                        over = true;
-                        bound = kNoBound;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) keep_candidate(to, sc[i], bound, c0 + i);
                 }
             }
-            if (MODE == CANDIDATES && valid) P.counts[at] = over ? -1 : (int)(to - list);
+            if (MODE == CANDIDATES && valid) P.counts[at] = n;
         }
     }
 
@@ -640,6 +698,7 @@ struct FewParams {
     float* maxima;               // [rows, stride / 8]
 };
 
+template <int CHUNKS>
 __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     __shared__ __align__(16) uint2 s_q[FEW_TILE][kMaxIndexWidth / 8];
     const int width = P.V.width;
@@ -647,12 +706,11 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     const int nr = min(FEW_TILE, P.C.rows - r0);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (warp < nr) {
-        uint2 w[4];
-        query_codes(P.C, r0 + warp, lane, w);
+        uint2 w[CHUNKS];
+        query_codes<CHUNKS>(P.C, r0 + warp, lane, w);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < CHUNKS; ++c)
             if (c * 256 + lane * 8 < width) s_q[warp][c * 32 + lane] = w[c];
-        if (blockIdx.x == 0) store_codes(P.C, r0 + warp, lane, w);
     }
     __syncthreads();
     const int sub = lane / 8, part = lane % 8;
@@ -718,21 +776,17 @@ struct PickParams {
     int32_t* sel_cnt;
 };
 
-// Candidates as whole numbers, higher is better: the score's order, then the
-// lower id.
-using Key = unsigned long long;
-__device__ __forceinline__ Key make_key(float score, int b) {
-    return ((Key)ordered(score) << 32) | (0xffffffffu - (uint32_t)b);
-}
-
 constexpr int WINDOW = 65536;    // block ids of one pass of the ordered output
+__host__ __device__ __forceinline__ int bits_words(int ids) {
+    return ((ids < WINDOW ? ids : WINDOW) + 127) / 128 * 4;
+}
 
 template <int THREADS>
 struct BestShared {
     static constexpr int LOG2_BINS = THREADS <= 512 ? 9 : 10;
     static constexpr int BINS = 1 << LOG2_BINS;
     int hist[BINS];
-    Key most[32], least[32];
+    uint32_t most[32], least[32];
     int sums[32];
     int digit, left, count;
     int total, bad;
@@ -754,47 +808,32 @@ __device__ __forceinline__ int cta_scan(int v, int* sums) {
     return v + before;
 }
 
-// The need-th largest of key[0 .. total), 1 <= need <= total, all keys
-// different, as a lower limit that exactly `need` keys reach.  Counts over BINS
-// equal parts of the keys' range, then of the part that holds it, until what
-// is in the part is taken whole.
-template <int THREADS>
-__device__ Key need_th(const Key* key, int total, int need, BestShared<THREADS>& S) {
+// A limit for the `need` largest of key(0) .. key(total - 1), 1 <= need <=
+// total, keys above 0: those above it are taken, and `equals` of those equal to
+// it.
+// Counts over BINS equal parts of the keys' range, then of the part that holds
+// the need-th largest, until what is in the part is taken whole.  No key is
+// outside [least, most].
+struct Limit {
+    uint32_t key;
+    int equals;
+};
+
+template <int THREADS, typename KeyOf>
+__device__ Limit need_th(const KeyOf& key, int total, int need, uint32_t least, uint32_t most,
+                         BestShared<THREADS>& S) {
     constexpr int LOG2_BINS = BestShared<THREADS>::LOG2_BINS, BINS = 1 << LOG2_BINS;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    Key most = 0, least = ~0ull;
-    for (int i = tid; i < total; i += THREADS) {
-        most = max(most, key[i]);
-        least = min(least, key[i]);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-    }
-    if (lane == 0) {
-        S.most[warp] = most;
-        S.least[warp] = least;
-    }
-    __syncthreads();
-    most = S.most[lane % (THREADS / 32)];
-    least = S.least[lane % (THREADS / 32)];
-#pragma unroll
-    for (int o = THREADS / 64; o; o >>= 1) {
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-    }
-    Key lo = least, width = most - least;   // keys of interest: [lo, lo + width]
+    const int tid = threadIdx.x;
+    uint32_t lo = least, width = most - least;   // keys of interest: [lo, lo + width]
     for (;;) {
-        const int shift =
-            width >> LOG2_BINS ? 64 - LOG2_BINS - __clzll((long long)width) : 0;
+        const int shift = width >> LOG2_BINS ? 32 - LOG2_BINS - __clz((int)width) : 0;
         constexpr int PER = BINS / THREADS;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) S.hist[tid * PER + i] = 0;
+        for (int i = 0; i < PER; ++i) S.hist[tid + i * THREADS] = 0;
         __syncthreads();
         for (int i = tid; i < total; i += THREADS) {
-            const Key k = key[i] - lo;      // below lo: wraps to beyond width
-            if (k <= width) atomicAdd(&S.hist[(int)(k >> shift)], 1);
+            const uint32_t k = key(i) - lo;      // below lo: wraps to beyond width
+            if (k <= width) atomicAdd(&S.hist[k >> shift], 1);
         }
         __syncthreads();
         // Thread t holds bins from the top down.
@@ -817,53 +856,93 @@ __device__ Key need_th(const Key* key, int total, int need, BestShared<THREADS>&
             }
         }
         __syncthreads();
-        lo += (Key)S.digit << shift;
+        lo += (uint32_t)S.digit << shift;
         need = S.left;
-        if (S.count == need) return lo;
-        width = ((Key)1 << shift) - 1;
+        if (S.count == need) return {lo - 1, 0};
+        if (shift == 0) return {lo, need};
+        width = (1u << shift) - 1;
         __syncthreads();
     }
 }
 
+// The smallest and the largest key.
+template <int THREADS, typename KeyOf>
+__device__ void range_of(const KeyOf& key, int total, uint32_t* least, uint32_t* most,
+                         BestShared<THREADS>& S) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    uint32_t a = ~0u, b = 0;
+    for (int i = tid; i < total; i += THREADS) {
+        const uint32_t k = key(i);
+        a = min(a, k);
+        b = max(b, k);
+    }
+    a = __reduce_min_sync(0xffffffffu, a);
+    b = __reduce_max_sync(0xffffffffu, b);
+    if (lane == 0) {
+        S.least[warp] = a;
+        S.most[warp] = b;
+    }
+    __syncthreads();
+    *least = __reduce_min_sync(0xffffffffu, S.least[lane % (THREADS / 32)]);
+    *most = __reduce_max_sync(0xffffffffu, S.most[lane % (THREADS / 32)]);
+}
+
 // Writes the taken blocks in ascending order: those below R.lo, those from
-// R.hi on, and the R.need best of key[0 .. total).  total >= R.need.  bits: room
-// for one per id of a window.
+// R.hi on, and the R.need best of the candidates (key[i] > 0 and within [least,
+// most], id[i]), i < total, equal keys by the lower id.  total >= R.need.  bits:
+// room for one per id of a window, in whole uint4.
 template <int THREADS>
-__device__ void best_of(const RowRange& R, const Key* key, int total, int32_t* out,
-                        uint32_t* bits, BestShared<THREADS>& S) {
+__device__ void best_of(const RowRange& R, const uint32_t* key, const int* id, int total,
+                        uint32_t least, uint32_t most, int32_t* out, uint32_t* bits,
+                        BestShared<THREADS>& S) {
     const int tid = threadIdx.x;
-    Key limit = 0;
-    if (R.need > 0) limit = need_th<THREADS>(key, total, R.need, S);
+    Limit limit = {0, 0};
+    uint32_t last = ~0u;   // of the equal keys, those with ~id above this
+    if (R.need > 0) {
+        limit = need_th<THREADS>([&](int i) { return key[i]; }, total, R.need, least, most, S);
+        if (limit.equals > 0) {
+            __syncthreads();
+            // ~id: the lowest ids largest; the others' 1 is below every ~id.
+            last = need_th<THREADS>(
+                       [&](int i) { return key[i] == limit.key ? ~(uint32_t)id[i] : 1u; }, total,
+                       limit.equals, 1u, ~0u, S)
+                       .key;
+        }
+    }
     int done = 0;    // ids written
     for (int w0 = 0; w0 < R.n_vis; w0 += WINDOW) {
-        const int ids = min(WINDOW, R.n_vis - w0), words = (ids + 31) / 32;
+        const uint32_t ids = (uint32_t)min(WINDOW, R.n_vis - w0);
+        const int quads = (int)(ids + 127) / 128;
+        uint4* bits4 = reinterpret_cast<uint4*>(bits);
+        for (int i = tid; i < quads; i += THREADS) bits4[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        for (int i = tid; i < words; i += THREADS) {
-            // Blocks always taken: ids below lo or from hi on.
-            uint32_t m = 0;
-            const int id = w0 + i * 32;
-            if (id < R.lo) m |= R.lo - id >= 32 ? 0xffffffffu : (1u << (R.lo - id)) - 1;
-            if (id + 32 > R.hi) m |= id >= R.hi ? 0xffffffffu : ~((1u << (R.hi - id)) - 1);
-            if (id + 32 > R.n_vis) m &= (1u << (R.n_vis - id)) - 1;
-            bits[i] = m;
-        }
-        __syncthreads();
+        auto mark = [&](int b) {
+            const uint32_t i = (uint32_t)b - (uint32_t)w0;
+            if (i < ids) atomicOr(&bits[i / 32], 1u << (i % 32));
+        };
+        for (int b = tid; b < R.lo; b += THREADS) mark(b);
+        for (int b = R.hi + tid; b < R.n_vis; b += THREADS) mark(b);
         if (R.need > 0)
             for (int i = tid; i < total; i += THREADS) {
-                const Key k = key[i];
-                const uint32_t id = 0xffffffffu - (uint32_t)k - (uint32_t)w0;
-                if (k >= limit && id < (uint32_t)ids) atomicOr(&bits[id / 32], 1u << (id % 32));
+                const uint32_t k = key[i];
+                if (k > limit.key || (k == limit.key && ~(uint32_t)id[i] > last)) mark(id[i]);
             }
         __syncthreads();
         // Thread t writes the ids of its stretch of words.
-        const int per = (words + THREADS - 1) / THREADS;
-        const int a = min(tid * per, words), b = min(a + per, words);
+        const int per = (quads + THREADS - 1) / THREADS;
+        const int a = min(tid * per, quads), b = min(a + per, quads);
         int n = 0;
-        for (int i = a; i < b; ++i) n += __popc(bits[i]);
+        for (int i = a; i < b; ++i) {
+            const uint4 u = bits4[i];
+            n += __popc(u.x) + __popc(u.y) + __popc(u.z) + __popc(u.w);
+        }
         const int upto = cta_scan<THREADS>(n, S.sums);
         int at = done + upto - n;
-        for (int i = a; i < b; ++i)
-            for (uint32_t m = bits[i]; m; m &= m - 1) out[at++] = w0 + i * 32 + __ffs(m) - 1;
+        if (n)
+            for (int i = 4 * a; i < 4 * b; ++i)
+                for (uint32_t m = bits[i]; m; m &= m - 1)
+                    out[at++] = w0 + i * 32 + __ffs(m) - 1;
+        if (w0 + WINDOW >= R.n_vis) break;
         if (tid == THREADS - 1) S.count = upto;
         __syncthreads();
         done += S.count;
@@ -949,27 +1028,37 @@ struct ScorePick {
     const float* scores;
     long long stride;
     const float* maxima;     // [rows, stride / 8], null: none
-    int room, room_groups;   // keys a CTA holds of candidates and of maxima
+    int words, room, room_groups, room_reach;   // what a CTA holds, see pick_kernel
 };
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
-    extern __shared__ Key s_key[];   // [room], [room_groups], then the ids' bits
+    // The ids' bits [words], candidates' keys and ids [room] each, maxima's keys
+    // [room_groups], the groups that reach the limit [room_reach].
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ BestShared<THREADS> S;
-    Key* groups = s_key + P.room;
-    uint32_t* bits = reinterpret_cast<uint32_t*>(groups + P.room_groups);
+    uint32_t* bits = s_key;
+    uint32_t* const key = bits + P.words;
+    int* const id = reinterpret_cast<int*>(key + P.room);
+    uint32_t* groups = key + 2 * P.room;
+    int* const reach = reinterpret_cast<int*>(groups + P.room_groups);
     const int row = blockIdx.x, tid = threadIdx.x;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
     if (write_plain(P.K, R, row, out)) return;
     const float* s = P.scores + row * P.stride;
     const int n = R.hi - R.lo;
+    uint32_t least, most;
     if (R.need == 0 || n <= P.room) {
         const int total = R.need ? n : 0;
 #pragma unroll 4
-        for (int i = tid; i < total; i += THREADS) s_key[i] = make_key(s[R.lo + i], R.lo + i);
+        for (int i = tid; i < total; i += THREADS) {
+            key[i] = ordered(s[R.lo + i]);
+            id[i] = R.lo + i;
+        }
         __syncthreads();
-        best_of<THREADS>(R, s_key, total, out, bits, S);
+        range_of<THREADS>([&](int i) { return key[i]; }, total, &least, &most, S);
+        best_of<THREADS>(R, key, id, total, least, most, out, bits, S);
         return;
     }
     if (P.maxima) {
@@ -979,54 +1068,49 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
         const float* m = P.maxima + row * (P.stride / 8);
         if (per == 1) {
 #pragma unroll 8
-            for (int g = tid; g < n_groups; g += THREADS) groups[g] = make_key(m[g], g);
+            for (int g = tid; g < n_groups; g += THREADS) groups[g] = ordered(m[g]);
         } else {
             for (int g = tid; g < n_groups; g += THREADS) {
                 float most = -INFINITY;
 #pragma unroll 4
                 for (int i = g * per; i < min(g * per + per, g8); ++i) most = fmaxf(most, m[i]);
-                groups[g] = make_key(most, g);
+                groups[g] = ordered(most);
             }
         }
-        if (tid == 0) S.total = S.count = 0;
+        if (tid == 0) S.total = S.bad = 0;
         __syncthreads();
         if (n_groups >= R.need) {
-            const uint32_t bound = (uint32_t)(need_th<THREADS>(groups, n_groups, R.need, S) >> 32);
-            // The groups that reach the bound, one behind the other (S.bad: their
-            // number), in place of the groups' keys.
-            __syncthreads();
-            int mine = 0;
-            for (int g = tid; g < n_groups; g += THREADS) mine += (uint32_t)(groups[g] >> 32) >= bound;
-            const int upto = cta_scan<THREADS>(mine, S.sums);
-            if (tid == THREADS - 1) S.bad = upto;
-            int* const reach = reinterpret_cast<int*>(s_key);   // room >= need groups, see below
-            int at = upto - mine;
+            // need groups, so need scores, reach the limit.
+            auto key_of = [&](int i) { return groups[i]; };
+            range_of<THREADS>(key_of, n_groups, &least, &most, S);
+            const Limit limit = need_th<THREADS>(key_of, n_groups, R.need, least, most, S);
+            const uint32_t bound = limit.equals ? limit.key : limit.key + 1;
+            // The groups that reach it, then their scores that do.
             for (int g = tid; g < n_groups; g += THREADS)
-                if ((uint32_t)(groups[g] >> 32) >= bound) {
-                    if (at < 2 * P.room) reach[at] = g;
-                    ++at;
+                if (groups[g] >= bound) {
+                    const int at = atomicAdd(&S.bad, 1);
+                    if (at < P.room_reach) reach[at] = g;
                 }
             __syncthreads();
-            const int n_reach = S.bad;
-            if (n_reach <= P.room_groups && n_reach <= 2 * P.room) {
-                // Their list moves behind, where the groups' keys were.
-                int* const list = reinterpret_cast<int*>(groups);
-                for (int i = tid; i < n_reach; i += THREADS) list[i] = reach[i];
-                __syncthreads();
-                const int each = per * 8;
+            const int n_reach = S.bad, each = per * 8;
+            if (n_reach <= P.room_reach) {
                 for (int i = tid; i < n_reach * each; i += THREADS) {
-                    const int b = list[i / each] * each + i % each;
+                    const int b = reach[i / each] * each + i % each;
                     if (b < R.lo || b >= R.hi) continue;
-                    const float v = s[b];
-                    if (v == v && ordered(v) >= bound) {
+                    const uint32_t k = ordered(s[b]);
+                    if (k >= bound && k > 1) {   // (1: a NaN)
                         const int to = atomicAdd(&S.total, 1);
-                        if (to < P.room) s_key[to] = make_key(v, b);
+                        if (to < P.room) {
+                            key[to] = k;
+                            id[to] = b;
+                        }
                     }
                 }
                 __syncthreads();
                 const int total = S.total;
                 if (total >= R.need && total <= P.room) {
-                    best_of<THREADS>(R, s_key, total, out, bits, S);
+                    // (no maximum is above `most`, so no score is)
+                    best_of<THREADS>(R, key, id, total, bound, most, out, bits, S);
                     return;
                 }
             }
@@ -1046,14 +1130,46 @@ struct BoundParams {
 };
 
 constexpr int BOUND_HELD = 32;    // maxima a lane keeps in registers
-constexpr int BOUND_STEPS = 20;
+
+// Of a histogram's 256 bins the largest with at least *left entries in it and
+// above; *left becomes what is left to take from it.  One warp, *left at most
+// all entries.
+__device__ __forceinline__ int pick_bin(const int* hist, int lane, int* left) {
+    // Lane l holds bins 255 - 8 l .. 248 - 8 l, highest first.
+    const int4* h = reinterpret_cast<const int4*>(hist + 248 - 8 * lane);
+    const int4 low = h[0], high = h[1];
+    const int c[8] = {high.w, high.z, high.y, high.x, low.w, low.z, low.y, low.x};
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += c[i];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    int bin = 255 - 8 * lane, rest = *left - (upto - sum);
+    bool open = true;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        open = open && rest > c[i];
+        if (open) {
+            rest -= c[i];
+            --bin;
+        }
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, upto >= *left)) - 1;
+    *left = __shfl_sync(0xffffffffu, rest, who);
+    return __shfl_sync(0xffffffffu, bin, who);
+}
 
 // One warp a row: a number that at least `need` group maxima, so at least
-// `need` of the row's scores, reach: a limit that exactly the need largest
-// reach, or close below the need-th largest (halving the range of their order
-// at most 20 times).  The smallest finite number if there are too few; none for
-// a row that needs none.
+// `need` of the row's scores, reach: the need-th largest maximum to one part
+// in 2^16 of their order's range, from below, by two counts over 256 parts.
+// The smallest finite number if there are too few maxima; none for a row that
+// needs none.
 __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
+    __shared__ __align__(16) int s_hist[8][256];
     const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (row >= P.rows) return;
     const RowRange R = row_range(P.pos0 + row, P.max_sel, P.n_first, P.n_last);
@@ -1073,41 +1189,40 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
     uint32_t held[BOUND_HELD];
 #pragma unroll
     for (int i = 0; i < BOUND_HELD; ++i) held[i] = key_of(i * 32 + lane);
-    const bool more = n > BOUND_HELD * 32;
-    auto count = [&](uint32_t key) {
-        int c = 0;
+    auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < BOUND_HELD; ++i) c += held[i] >= key;
-        if (more)
-            for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) c += key_of(i) >= key;
-        return (int)__reduce_add_sync(0xffffffffu, c);
+        for (int i = 0; i < BOUND_HELD; ++i) f(held[i]);
+        for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) f(key_of(i));
     };
     uint32_t most = 0, least = 0xffffffffu;
-    auto see = [&](uint32_t k) {
-        if (k) {
-            most = max(most, k);
-            least = min(least, k);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < BOUND_HELD; ++i) see(held[i]);
-    if (more)
-        for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) see(key_of(i));
+    int some = 0;
+    each([&](uint32_t k) {
+        most = max(most, k);
+        least = min(least, k ? k : 0xffffffffu);
+        some += k != 0;
+    });
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
+    some = (int)__reduce_add_sync(0xffffffffu, some);
     float bound = -3.402823466e38f;
-    if (most && count(least) >= R.need) {
-        // At least need maxima reach lo; fewer reach lo + width + 1.
+    if (some >= R.need) {
+        int* hist = s_hist[threadIdx.x / 32];
         uint32_t lo = least, width = most - least;
-        for (int i = 0; i < BOUND_STEPS && width; ++i) {
-            const uint32_t step = width / 2 + 1;
-            const int c = count(lo + step);
-            if (c >= R.need) {
-                lo += step;
-                width = c == R.need ? 0 : width - step;
-            } else {
-                width = step - 1;
-            }
+        int left = R.need;
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+            const int shift = width >> 8 ? 24 - __clz((int)width) : 0;
+            __syncwarp();
+            reinterpret_cast<int4*>(hist)[lane] = make_int4(0, 0, 0, 0);
+            reinterpret_cast<int4*>(hist)[lane + 32] = make_int4(0, 0, 0, 0);
+            __syncwarp();
+            each([&](uint32_t k) {
+                if (k - lo <= width) atomicAdd(&hist[(k - lo) >> shift], 1);
+            });
+            __syncwarp();
+            lo += (uint32_t)pick_bin(hist, lane, &left) << shift;
+            if (shift == 0) break;
+            width = (1u << shift) - 1;
         }
         bound = __uint_as_float(lo & 0x80000000u ? lo & 0x7fffffffu : ~lo);
     }
@@ -1115,36 +1230,42 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
 }
 
 // ------------------------------------------------------------ best of the candidates
+constexpr int MAX_ROW_TILES = 256;   // of a launch
+struct RunTable {
+    uint8_t runs[MAX_ROW_TILES];     // of each row tile
+};
+
 struct BestParams {
     PickParams K;
     DotParams D;             // the products' lists and schedule
-    int room;                // candidates a CTA holds
+    RunTable T;
+    const float* bound;
+    int words, room;         // what a CTA holds
     IndexView V;             // for rows searched block by block
     const int8_t* codes;
 };
 
 constexpr int BEST_THREADS = 128;
-constexpr int MAX_LISTS = 2 * 80;   // two a run; a row tile's runs are at most the pairs
+constexpr int MAX_LISTS = PARTS * 80;   // a row tile's runs are at most the pairs
 
 __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) {
-    extern __shared__ Key s_key[];   // [room], then the ids' bits
+    // The ids' bits [words], candidates' keys and ids [room] each.
+    extern __shared__ __align__(16) uint32_t s_bits[];
     __shared__ BestShared<BEST_THREADS> S;
     __shared__ int s_n[MAX_LISTS], s_at[MAX_LISTS];
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
     if (write_plain(P.K, R, row, out)) return;
+    uint32_t* const key = s_bits + P.words;
+    int* const id = reinterpret_cast<int*>(key + P.room);
     if (tid == 0) S.total = S.bad = 0;
+    if (tid < 32) S.most[tid] = 0;
     __syncthreads();
     if (R.need > 0) {
-        // Runs of this row's row tile.
-        const int rt = row / PAIR_ROWS;
-        long long cum = 0;
-        for (int t = 0; t < rt; ++t) cum += col_tiles<CANDIDATES>(P.D, t);
-        const int nt = col_tiles<CANDIDATES>(P.D, rt);
-        const int runs = nt ? pair_of(P.D, cum + nt - 1) - pair_of(P.D, cum) + 1 : 0;
-        const int lists = 2 * runs;
-        const long long at = (long long)row * P.D.segs * 2;
+        const int runs = P.T.runs[row / PAIR_ROWS];
+        const int lists = PARTS * runs;
+        const long long at = (long long)row * P.D.segs * PARTS;
         for (int l = tid; l < lists; l += BEST_THREADS) {
             const int n = P.D.counts[at + l];
             const bool bad = n < 0 || n > P.D.cap;
@@ -1154,24 +1275,31 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
             s_at[l] = to;
         }
         __syncthreads();
-        // A warp per list.
+        // Eight lanes a list.
+        uint32_t most = 0;
         if (!S.bad)
-            for (int l = warp; l < lists; l += BEST_THREADS / 32) {
+            for (int l = tid / 8; l < lists; l += BEST_THREADS / 8) {
                 const uint2* src = P.D.list + (at + l) * P.D.cap;
-                const int n = s_n[l];
-                Key* to = s_key + s_at[l];
+                const int n = s_n[l], to = s_at[l];
 #pragma unroll 4
-                for (int i = lane; i < n; i += 32) {
+                for (int i = tid % 8; i < n; i += 8) {
                     const uint2 e = src[i];
-                    to[i] = make_key(__uint_as_float(e.x), (int)e.y);
+                    const uint32_t k = ordered(__uint_as_float(e.x));
+                    key[to + i] = k;
+                    id[to + i] = (int)e.y;
+                    most = max(most, k);
                 }
             }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) S.most[warp] = most;
     }
     __syncthreads();
     const int total = S.total;
     if (!S.bad && total >= R.need) {
-        best_of<BEST_THREADS>(R, s_key, total, out, reinterpret_cast<uint32_t*>(s_key + P.room),
-                              S);
+        // Every candidate reaches the bound.
+        const uint32_t least = R.need ? ordered(P.bound[row]) : 0;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, S.most[lane % (BEST_THREADS / 32)]);
+        best_of<BEST_THREADS>(R, key, id, total, least, most, out, s_bits, S);
         return;
     }
     // Searched block by block; a row of zero codes needs no products.
@@ -1229,9 +1357,9 @@ struct Layout {
     size_t counts_bytes, list_bytes, bytes;
 };
 
-size_t list_row_bytes(int segs, int cap) { return (size_t)segs * 2 * cap * 8; }
+size_t list_row_bytes(int segs, int cap) { return (size_t)segs * PARTS * cap * 8; }
 int list_cap(int max_sel, long long tiles_per_pair) {
-    const long long most = tiles_per_pair * (TILE / 2), want = 4 * max_sel + 64;
+    const long long most = tiles_per_pair * PART, want = 4 * max_sel + 64;
     return (int)(most < want ? most : want);
 }
 
@@ -1250,9 +1378,9 @@ Layout layout(int rows, int n, int kept, int width, int pairs) {
     const size_t rows_up = few ? rows : round_up(rows, PAIR_ROWS);
     size_t scores = SCORE_BYTES > PAIR_ROWS * row_bytes ? SCORE_BYTES : PAIR_ROWS * row_bytes;
     if (rows_up * row_bytes < scores) scores = rows_up * row_bytes;
-    L.chunk = rows;
+    L.chunk = rows < PAIR_ROWS * MAX_ROW_TILES ? rows : PAIR_ROWS * MAX_ROW_TILES;
     if (!few && scores / row_bytes < rows_up)
-        L.chunk = (int)(scores / row_bytes / PAIR_ROWS) * PAIR_ROWS;
+        L.chunk = min(L.chunk, (int)(scores / row_bytes / PAIR_ROWS) * PAIR_ROWS);
     L.codes = take((size_t)rows * width);
     L.scores = take(scores);
     if (few) {
@@ -1263,7 +1391,7 @@ Layout layout(int rows, int n, int kept, int width, int pairs) {
         L.scale = take((size_t)round_up(n, TILE) * 4);
         L.sample_scale = take((size_t)round_up(n, TILE) * 4);
         L.bound = take(rows_up * 4);
-        L.counts_bytes = ((size_t)PAIR_ROWS * pairs + 2 * rows_up) * 2 * 4;
+        L.counts_bytes = ((size_t)PAIR_ROWS * pairs + 2 * rows_up) * PARTS * 4;
         L.counts = take(L.counts_bytes);
         // One row tile fits with any max_sel.
         const long long tiles = (round_up(n, TILE) / TILE + pairs - 1) / pairs + 1;
@@ -1303,26 +1431,25 @@ int max_pairs(const DeviceInfo* di) {
         return 0;
     }
     if (n > di->num_sms / 2) n = di->num_sms / 2;
-    if (n > MAX_LISTS / 2) n = MAX_LISTS / 2;
+    if (n > MAX_LISTS / PARTS) n = MAX_LISTS / PARTS;
     if (di->device < 64) cached[di->device].store(n, std::memory_order_relaxed);
     return n;
 }
 
 // The schedule of a launch's products: pairs and, per row tile, the most runs.
 template <int MODE>
-void schedule(DotParams& D, int pairs) {
+void schedule(DotParams& D, int pairs, RunTable* table = nullptr) {
     D.row_tiles = (D.rows + PAIR_ROWS - 1) / PAIR_ROWS;
     D.total = 0;
     for (int t = 0; t < D.row_tiles; ++t) D.total += col_tiles<MODE>(D, t);
     D.G = (int)(D.total < pairs ? D.total : pairs);
     D.segs = 1;
     long long cum = 0;
-    for (int t = 0; t < D.row_tiles && D.total > 0; ++t) {
+    for (int t = 0; t < D.row_tiles; ++t) {
         const int n = col_tiles<MODE>(D, t);
-        if (n > 0) {
-            const int s = pair_of(D, cum + n - 1) - pair_of(D, cum) + 1;
-            if (s > D.segs) D.segs = s;
-        }
+        const int s = n > 0 ? pair_of(D, cum + n - 1) - pair_of(D, cum) + 1 : 0;
+        if (s > D.segs) D.segs = s;
+        if (table) table->runs[t] = (uint8_t)s;
         cum += n;
     }
 }
@@ -1347,29 +1474,24 @@ int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams
     return GQA_OK;
 }
 
-// The bits of the block ids a launch's rows see, one window at a time.
-size_t bits_bytes(const PickParams& K, int rows) {
-    const int ids = ((K.pos0 + rows - 1) >> 2) + 1;
-    return (size_t)((ids < WINDOW ? ids : WINDOW) + 31) / 32 * 4;
-}
-
 // room: candidates; groups: maxima.
 template <int THREADS>
 int launch_pick(const PickParams& K, int rows, const float* scores, long long stride,
                 const float* maxima, int n, cudaStream_t stream) {
-    ScorePick P = {K, scores, stride, maxima, 0, 0};
+    ScorePick P = {K, scores, stride, maxima, bits_words(((K.pos0 + rows - 1) >> 2) + 1), 0, 0, 0};
     int want = 12 * K.max_sel + 1024;
     const int most = PICK_SMEM / 8;
     if (maxima) {
-        P.room_groups = 8192 < (n + 7) / 8 ? 8192 : (n + 7) / 8;
-        P.room = want < most - P.room_groups ? want : most - P.room_groups;
+        P.room_groups = 16384 < (n + 7) / 8 ? 16384 : (n + 7) / 8;
+        P.room = want < most - P.room_groups / 2 ? want : most - P.room_groups / 2;
+        P.room_reach = 2 * K.max_sel + 256;
     } else {
         P.room = n < most ? n : most;
     }
     if (ensure_smem_limit(reinterpret_cast<const void*>(pick_kernel<THREADS>),
-                          PICK_SMEM + WINDOW / 8) != GQA_OK)
+                          PICK_SMEM + (2 * kMaxSelect + 256) * 4 + WINDOW / 8) != GQA_OK)
         return GQA_ERR_CUDA;
-    const size_t smem = (size_t)(P.room + P.room_groups) * 8 + bits_bytes(K, rows);
+    const size_t smem = (size_t)P.room * 8 + (P.words + P.room_groups + P.room_reach) * 4;
     pick_kernel<THREADS><<<rows, THREADS, smem, stream>>>(P);
     return GQA_OK;
 }
@@ -1421,7 +1543,8 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
             const FewParams F = {C, V, n, pos0, n_first, n_last, scores, L.stride, maxima};
             const int tiles = (n + 63) / 64, cap = di->num_sms * 4;
             const dim3 grid(tiles < cap ? tiles : cap, (rows + FEW_TILE - 1) / FEW_TILE);
-            score_few_kernel<<<grid, 256, 0, stream>>>(F);
+            if (width <= 256) score_few_kernel<1><<<grid, 256, 0, stream>>>(F);
+            else score_few_kernel<4><<<grid, 256, 0, stream>>>(F);
         }
         rc = launch_pick<1024>(K, rows, scores, L.stride, maxima, n, stream);
         if (rc != GQA_OK) return rc;
@@ -1435,9 +1558,10 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     if (n > 0) {
         const ExpandParams E = {V, n, cols, scale, sample ? sample_scale : nullptr};
         const int code_ctas = (rows + 7) / 8;
-        const long long threads = (long long)n * (width / 16);
-        prepare_kernel<<<(unsigned)(code_ctas + (threads + 255) / 256), 256, 0, stream>>>(
-            C, E, code_ctas);
+        const int a_cta = 256 / (width / 16) * EXPAND_PASSES;
+        const int ctas = code_ctas + (n + a_cta - 1) / a_cta;
+        if (width <= 256) prepare_kernel<1><<<ctas, 256, 0, stream>>>(C, E, code_ctas);
+        else prepare_kernel<4><<<ctas, 256, 0, stream>>>(C, E, code_ctas);
     }
     if (sample && ensure_smem_limit(reinterpret_cast<const void*>(best_kernel),
                                     PICK_SMEM + WINDOW / 8) != GQA_OK)
@@ -1467,12 +1591,13 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
             continue;
         }
         DotParams R = P;     // the candidates' products
+        RunTable table;
         // Fewer rows a launch if their candidate lists would not fit.
         for (;;) {
-            schedule<CANDIDATES>(R, pairs);
+            schedule<CANDIDATES>(R, pairs, &table);
             R.cap = R.G > 0 ? list_cap(max_sel, (R.total + R.G - 1) / R.G) : 32;
             if (R.rows * list_row_bytes(R.segs, R.cap) <= L.list_bytes &&
-                (size_t)R.rows * R.segs * 2 * 4 <= L.counts_bytes)
+                (size_t)R.rows * R.segs * PARTS * 4 <= L.counts_bytes)
                 break;
             if (R.rows <= PAIR_ROWS) return GQA_ERR_WORKSPACE;   // layout() leaves room for these
             step = round_up(R.rows, PAIR_ROWS) - PAIR_ROWS;
@@ -1495,10 +1620,10 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         R.counts = reinterpret_cast<int*>(w + L.counts);
         rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
-        BestParams T = {K, R, 12 * max_sel + 512, V, codes + (size_t)r0 * width};
+        BestParams T = {K, R, table, bound, bits_words(((K.pos0 + R.rows - 1) >> 2) + 1),
+                        12 * max_sel + 512, V, codes + (size_t)r0 * width};
         if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
-        best_kernel<<<R.rows, BEST_THREADS, (size_t)T.room * 8 + bits_bytes(K, R.rows), stream>>>(
-            T);
+        best_kernel<<<R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4, stream>>>(T);
     }
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
