@@ -29,6 +29,17 @@
 namespace gqa {
 namespace select {
 
+// Each kernel of a call but the first is a programmatic dependent of the one
+// before: it is launched while that runs, and waits for its end (so for the end
+// of all before) ahead of its first read or write of global memory.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 constexpr int STRIDE = 4;   // every STRIDE-th block is in the sample
 
 // What dot_kernel does with its products: keep all scores, keep the maxima of
@@ -220,6 +231,7 @@ constexpr int EXPAND_PASSES = 4;
 template <int CHUNKS>
 __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const ExpandParams E,
                                                       int code_ctas) {
+    let_next_launch();
     if ((int)blockIdx.x < code_ctas) {
         const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
         if (row >= C.rows) return;
@@ -272,7 +284,7 @@ constexpr int PAIR_ROWS = 256;
 constexpr int TILE = 256;                    // columns of a tile
 constexpr int CHUNK_BYTES = 128 * 128;       // 128 rows x 64 fp16
 constexpr int RES_CHUNKS = 4;                // row chunks kept (width 256)
-constexpr int PARTS = 2;                     // warpgroups that share a tile's columns
+constexpr int PARTS = 4;                     // warpgroups that share a tile's columns
 constexpr int PART = TILE / PARTS;
 constexpr int EPI_WARPS = 4 * PARTS;
 constexpr int DOT_THREADS = 32 * (2 + EPI_WARPS);
@@ -284,7 +296,7 @@ constexpr uint32_t IDESC = idesc_f16_f32(256, TILE, false, false);
 
 template <bool RESIDENT>
 struct DotCfg {
-    static constexpr int SLOTS = RESIDENT ? 7 : 5;
+    static constexpr int SLOTS = RESIDENT ? (PARTS == 4 ? 5 : 7) : (PARTS == 4 ? 4 : 5);
     static constexpr int SLOT_BYTES = RESIDENT ? CHUNK_BYTES : 2 * CHUNK_BYTES;
     static constexpr int ROW_BYTES = RESIDENT ? RES_CHUNKS * CHUNK_BYTES : 0;
     static constexpr int NUM_BARS = 2 * SLOTS + 7;
@@ -424,6 +436,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
     pairs::cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
+    wait_for_previous();
 
     Runs<MODE> runs;
     runs.init(P, pair);
@@ -516,7 +529,6 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + part * PART;
         float* const my_scale = s_scale + (warp - 2) * PART;
         float* const my_dump = s_dump + ((warp - 2) * 32 + lane) * DUMP_WORDS;
-        static_assert(PART == 128, "four columns a lane");
         uint32_t t = 0;
         bool ok = true;
         while (ok && runs.next(P, pair, rt, jb, je, seg)) {
@@ -533,14 +545,15 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             const long long at = ((long long)row * P.segs + seg) * PARTS + part;
             uint2* const list = MODE == CANDIDATES ? P.list + at * P.cap : nullptr;
             int n = 0;
-            // The columns' scales: four a lane, loaded a tile ahead, then shared by
-            // the warp.
-            const float4* scale4 =
-                reinterpret_cast<const float4*>(P.scale + jb * TILE + part * PART) + lane;
+            // The columns' scales: four a lane (of the first PART / 4), loaded a tile
+            // ahead, then shared by the warp.
+            const float4* scale4 = reinterpret_cast<const float4*>(P.scale + jb * TILE +
+                                                                   part * PART) +
+                                   lane % (PART / 4);
             float4 ahead = __ldg(scale4);
             for (int j = jb; j < je; ++j, ++t) {
                 __syncwarp();
-                reinterpret_cast<float4*>(my_scale)[lane] = ahead;
+                if (lane < PART / 4) reinterpret_cast<float4*>(my_scale)[lane] = ahead;
                 if (j + 1 < je) ahead = __ldg(scale4 += TILE / 4);
                 __syncwarp();
                 ok = mbar_wait(tfull(t & 1), (t >> 1) & 1, abort_flag, P.err);
@@ -548,17 +561,13 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
                 const int col0 = j * TILE + part * PART;
-                // Two tensor-memory loads in flight.
-                uint32_t r[2][32];
-                tmem_ld32(t_lane + (t & 1) * TILE, r[0]);
 #pragma unroll
                 for (int g = 0; g < PART / 32; ++g) {
                     const int c0 = col0 + g * 32;
-                    uint32_t (&d)[32] = r[g & 1];
+                    uint32_t d[32];
+                    tmem_ld32(t_lane + (t & 1) * TILE + g * 32, d);
                     tmem_ld_wait<32>(d);
-                    if (g + 1 < PART / 32)
-                        tmem_ld32(t_lane + (t & 1) * TILE + (g + 1) * 32, r[(g + 1) & 1]);
-                    else {
+                    if (g + 1 == PART / 32) {
                         // The buffer is read out.
                         tc_fence_before();
                         __syncwarp();
@@ -701,6 +710,7 @@ struct FewParams {
 template <int CHUNKS>
 __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     __shared__ __align__(16) uint2 s_q[FEW_TILE][kMaxIndexWidth / 8];
+    let_next_launch();
     const int width = P.V.width;
     const int r0 = blockIdx.y * FEW_TILE;
     const int nr = min(FEW_TILE, P.C.rows - r0);
@@ -1045,6 +1055,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
     const int row = blockIdx.x, tid = threadIdx.x;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
+    wait_for_previous();
     if (write_plain(P.K, R, row, out)) return;
     const float* s = P.scores + row * P.stride;
     const int n = R.hi - R.lo;
@@ -1171,6 +1182,7 @@ __device__ __forceinline__ int pick_bin(const int* hist, int lane, int* left) {
 __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
     __shared__ __align__(16) int s_hist[8][256];
     const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    wait_for_previous();
     if (row >= P.rows) return;
     const RowRange R = row_range(P.pos0 + row, P.max_sel, P.n_first, P.n_last);
     if (R.need == 0) {
@@ -1256,6 +1268,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
+    wait_for_previous();
     if (write_plain(P.K, R, row, out)) return;
     uint32_t* const key = s_bits + P.words;
     int* const id = reinterpret_cast<int*>(key + P.room);
@@ -1275,21 +1288,33 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
             s_at[l] = to;
         }
         __syncthreads();
-        // Eight lanes a list.
+        // A warp per list; the loads of four lists in flight together.
         uint32_t most = 0;
-        if (!S.bad)
-            for (int l = tid / 8; l < lists; l += BEST_THREADS / 8) {
-                const uint2* src = P.D.list + (at + l) * P.D.cap;
-                const int n = s_n[l], to = s_at[l];
-#pragma unroll 4
-                for (int i = tid % 8; i < n; i += 8) {
-                    const uint2 e = src[i];
-                    const uint32_t k = ordered(__uint_as_float(e.x));
-                    key[to + i] = k;
-                    id[to + i] = (int)e.y;
-                    most = max(most, k);
+        if (!S.bad) {
+            auto keep = [&](int i, const uint2& e) {
+                const uint32_t k = ordered(__uint_as_float(e.x));
+                key[i] = k;
+                id[i] = (int)e.y;
+                most = max(most, k);
+            };
+            constexpr int WARPS = BEST_THREADS / 32, TOGETHER = 4;
+            for (int l0 = warp; l0 < lists; l0 += WARPS * TOGETHER) {
+                uint2 e[TOGETHER];
+#pragma unroll
+                for (int u = 0; u < TOGETHER; ++u) {
+                    const int l = l0 + u * WARPS;
+                    if (l < lists && lane < s_n[l]) e[u] = P.D.list[(at + l) * P.D.cap + lane];
+                }
+#pragma unroll
+                for (int u = 0; u < TOGETHER; ++u) {
+                    const int l = l0 + u * WARPS;
+                    if (l >= lists) break;
+                    if (lane < s_n[l]) keep(s_at[l] + lane, e[u]);
+                    for (int i = lane + 32; i < s_n[l]; i += 32)
+                        keep(s_at[l] + i, P.D.list[(at + l) * P.D.cap + i]);
                 }
             }
+        }
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) S.most[warp] = most;
     }
@@ -1343,6 +1368,23 @@ constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 256ull << 20;    // candidates held at once
 constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
 
+// A launch as a programmatic dependent of the kernel before it on the stream.
+template <typename... Params, typename... Args>
+bool launch_next(void (*kernel)(Params...), int grid, int threads, size_t smem,
+                 cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 bool sampled(int n, int max_sel) {
     return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel;
 }
@@ -1359,7 +1401,7 @@ struct Layout {
 
 size_t list_row_bytes(int segs, int cap) { return (size_t)segs * PARTS * cap * 8; }
 int list_cap(int max_sel, long long tiles_per_pair) {
-    const long long most = tiles_per_pair * PART, want = 4 * max_sel + 64;
+    const long long most = tiles_per_pair * PART, want = 8 * max_sel / PARTS + 64;
     return (int)(most < want ? most : want);
 }
 
@@ -1470,8 +1512,8 @@ int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams
     auto* kernel = resident ? dot_kernel<MODE, true> : dot_kernel<MODE, false>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem) != GQA_OK)
         return GQA_ERR_CUDA;
-    kernel<<<2 * D.G, DOT_THREADS, smem, stream>>>(tr, tc, D);
-    return GQA_OK;
+    return launch_next(kernel, 2 * D.G, DOT_THREADS, smem, stream, tr, tc, D) ? GQA_OK
+                                                                             : GQA_ERR_CUDA;
 }
 
 // room: candidates; groups: maxima.
@@ -1492,8 +1534,8 @@ int launch_pick(const PickParams& K, int rows, const float* scores, long long st
                           PICK_SMEM + (2 * kMaxSelect + 256) * 4 + WINDOW / 8) != GQA_OK)
         return GQA_ERR_CUDA;
     const size_t smem = (size_t)P.room * 8 + (P.words + P.room_groups + P.room_reach) * 4;
-    pick_kernel<THREADS><<<rows, THREADS, smem, stream>>>(P);
-    return GQA_OK;
+    return launch_next(pick_kernel<THREADS>, rows, THREADS, smem, stream, P) ? GQA_OK
+                                                                             : GQA_ERR_CUDA;
 }
 
 }  // namespace select
@@ -1613,7 +1655,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         float* bound = reinterpret_cast<float*>(w + L.bound);
         const BoundParams B = {scores, P.stride, P.log2_group, P.rows, K.pos0, max_sel, n_first,
                                n_last, bound};
-        bound_kernel<<<(P.rows + 7) / 8, 256, 0, stream>>>(B);
+        if (!launch_next(bound_kernel, (P.rows + 7) / 8, 256, 0, stream, B)) return GQA_ERR_CUDA;
         R.scale = scale;
         R.bound = bound;
         R.list = reinterpret_cast<uint2*>(w + L.list);
@@ -1621,9 +1663,11 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
         BestParams T = {K, R, table, bound, bits_words(((K.pos0 + R.rows - 1) >> 2) + 1),
-                        12 * max_sel + 512, V, codes + (size_t)r0 * width};
+                        10 * max_sel + 512, V, codes + (size_t)r0 * width};
         if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
-        best_kernel<<<R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4, stream>>>(T);
+        if (!launch_next(best_kernel, R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4,
+                         stream, T))
+            return GQA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
