@@ -292,30 +292,28 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
  *   kcache/vcache [num_pages, page, Hkv, D] E4M3 codes: round to nearest even
  *                 of the value times the fp32 reciprocal of kscale / vscale
  *                 (device fp32, > 0), +-448 beyond the range, NaN stays NaN.
- * Norm, angle (to 2^-40 of a turn at any position) and rotation in 32 bits,
- * one rounding at the end.  q_out and the caches must not overlap q, k or v. */
-int gqa_cache_write_e4m3(const void* q, const void* k, const void* v, int dtype,
-                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
-                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
-                         const void* q_weight, const void* k_weight, float eps,
-                         const float* inv_freq, int rot_dim, int interleaved,
-                         const float* kscale, const float* vscale, const int32_t* block_tables,
-                         int table_stride, int num_pages, int page, const int32_t* row_starts,
-                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
-                         int Hq, int Hkv, int D, void* q_out, uint8_t* kcache, uint8_t* vcache,
-                         struct CUstream_st* stream);
+ * Norm and rotation in 32 bits (cos and sin to 2^-20, of an angle kept to
+ * 2^-20 at any position), one rounding at the end.  q_out and the caches must
+ * not overlap q, k or v. */
+typedef struct {
+    const void *q, *k, *v;
+    const void *q_weight, *k_weight;
+    const float* inv_freq;
+    const float *kscale, *vscale;      /* unused by gqa_cache_write */
+    const int32_t *block_tables, *row_starts, *ctx_lens_dev;
+    void *q_out, *kcache, *vcache;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+        v_head_stride;
+    int32_t dtype, rot_dim, interleaved;
+    float eps;
+    int32_t table_stride, num_pages, page, max_ctx_len, batch, tokens, Hq, Hkv, D;
+} gqa_cache_write_args;
+
+int gqa_cache_write_e4m3(const gqa_cache_write_args* args, struct CUstream_st* stream);
 
 /* The same over an fp16 cache: kcache/vcache [num_pages, page, Hkv, D] fp16,
  * no scales. */
-int gqa_cache_write(const void* q, const void* k, const void* v, int dtype,
-                    int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
-                    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
-                    const void* q_weight, const void* k_weight, float eps,
-                    const float* inv_freq, int rot_dim, int interleaved,
-                    const int32_t* block_tables, int table_stride, int num_pages, int page,
-                    const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
-                    int batch, int tokens, int Hq, int Hkv, int D, void* q_out, void* kcache,
-                    void* vcache, struct CUstream_st* stream);
+int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream);
 
 /* Cache read: the cached tokens the rows stand for, as dense rows (the K / V
  * of gqa_attn_prefill for one sequence).  k_out, v_out [tokens, Hkv, D] fp16 =

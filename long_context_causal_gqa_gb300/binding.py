@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -59,6 +60,7 @@ class GQAError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 _ws = {}  # device index -> torch.uint8 tensor registered as workspace
+_outgrown = []  # workspaces replaced by larger ones: captured graphs may still use them
 
 
 def load():
@@ -91,14 +93,9 @@ def load():
             lib.gqa_attn_sparse_blocks_e4m3.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I,
                                                         I, I, I, F, P, P]
             lib.gqa_attn_sparse_blocks_e4m3.restype = I
-            L = ctypes.c_int64
-            lib.gqa_cache_write_e4m3.argtypes = [P, P, P, I, L, L, L, L, L, L, P, P, F, P, I, I,
-                                                 P, P, P, I, I, I, P, P, I, I, I, I, I, I, P, P,
-                                                 P, P]
-            lib.gqa_cache_write_e4m3.restype = I
-            lib.gqa_cache_write.argtypes = [P, P, P, I, L, L, L, L, L, L, P, P, F, P, I, I, P, I,
-                                            I, I, P, P, I, I, I, I, I, I, P, P, P, P]
-            lib.gqa_cache_write.restype = I
+            for f in (lib.gqa_cache_write_e4m3, lib.gqa_cache_write):
+                f.argtypes = [ctypes.c_char_p, P]
+                f.restype = I
             lib.gqa_cache_read_e4m3.argtypes = [P, P, P, P, P, I, I, I, P, P, I, I, I, I, I, P,
                                                 P, P]
             lib.gqa_cache_read_e4m3.restype = I
@@ -169,7 +166,12 @@ def ensure_workspace(nbytes: int, device=None) -> torch.Tensor:
     cur = _ws.get(idx)
     if cur is None or cur.numel() < nbytes:
         torch.cuda.synchronize(idx)
-        buf = torch.empty(max(int(nbytes), 4096), dtype=torch.uint8, device=f"cuda:{idx}")
+        size = max(int(nbytes), 4096)
+        if cur is not None:
+            # Half as much again at least, so that the ones kept stay few.
+            _outgrown.append(cur)
+            size = max(size, cur.numel() * 3 // 2)
+        buf = torch.empty(size, dtype=torch.uint8, device=f"cuda:{idx}")
         _check(load().gqa_set_workspace(idx, _ptr(buf), buf.numel()), "gqa_set_workspace")
         _ws[idx] = buf
         cur = buf
@@ -370,31 +372,50 @@ def sparse_blocks_e4m3(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tens
 #
 # These run once a layer and step beside a single small kernel, so their
 # wrappers keep to what costs little on the host: plain integers instead of
-# ctypes objects, and no device switch when the tensors' device is current.
+# ctypes objects, no device switch when the tensors' device is current, and one
+# look at each property of a tensor that is as it should be.
+
+# gqa_cache_write_args, in the C compiler's layout.
+_WRITE_ARGS = struct.Struct("@14P6q3if9i4x")
+
 
 def _refuse(what: str):
     raise GQAError(GQA_ERR_INVALID_ARG, what)
 
 
-def _want(name: str, t, dtype, dev, dims: int):
-    """A contiguous CUDA tensor of the given type, device and dimensions."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims:
-        _refuse(f"{name} must be a {dims}-dimensional {dtype} tensor")
-    if t.device != dev:
-        _refuse(f"{name} must be on {dev}" if t.is_cuda else f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
-    return t.data_ptr()
+def _want(name: str, t, dtype, idx, dims: int):
+    """Pointer of a contiguous CUDA tensor of the given type, device and dimensions."""
+    try:
+        if t.dtype is dtype and t.get_device() == idx and t.dim() == dims and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(f"{name} must be a contiguous {dims}-dimensional {dtype} tensor on cuda:{idx}")
 
 
-def _call(fn, dev, stream, *args):
+def _heads(name: str, t, dtype, idx, tokens, D):
+    """Heads and strides of a [tokens, heads, D] tensor with D contiguous."""
+    try:
+        if t.dtype is dtype and t.get_device() == idx and t.dim() == 3:
+            n, heads, d = t.shape
+            a, b, c = t.stride()
+            if n == tokens and d == D and c == 1:
+                return heads, a, b
+    except AttributeError:
+        pass
+    _refuse(f"{name} must be [tokens, heads, D] like k, with D contiguous")
+
+
+def _call(fn, idx, stream, *args):
     """One library call on the tensors' device and the given (or current) stream."""
-    idx = dev.index
-    if torch.cuda.current_device() != idx:
+    if torch._C._cuda_getDevice() != idx:
         with torch.cuda.device(idx):
-            return _call(fn, dev, stream, *args)
-    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
-    st = fn(*args, s)
+            return _call(fn, idx, stream, *args)
+    if stream is not None:
+        stream = stream.cuda_stream
+    else:
+        stream = torch._C._cuda_getCurrentRawStream(idx)
+    st = fn(*args, stream)
     if st != GQA_OK:
         raise GQAError(st, fn.__name__)
 
@@ -402,90 +423,96 @@ def _call(fn, dev, stream, *args):
 def _device_of(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse("tensors must be CUDA tensors")
-    return t.device
+    return t.get_device()
 
 
-def _pages(kcache, vcache, dtype, dev):
+def _scale(name, t, idx):
+    try:
+        if t.dtype is torch.float32 and t.numel() == 1 and t.get_device() == idx:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(f"{name} must be a one-element fp32 tensor on cuda:{idx}")
+
+
+def _pages(kcache, vcache, dtype, idx):
     """Pointers of the two caches and their [pages, page, Hkv, D]."""
-    kp, vp = _want("kcache", kcache, dtype, dev, 4), _want("vcache", vcache, dtype, dev, 4)
-    if kcache.shape != vcache.shape:
+    kp = _want("kcache", kcache, dtype, idx, 4)
+    vp = _want("vcache", vcache, dtype, idx, 4)
+    shape = kcache.shape
+    if vcache.shape != shape:
         _refuse("kcache and vcache must have the same shape")
-    return kp, vp, kcache.shape
+    return kp, vp, shape
 
 
-def _one_scale(name, t, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.numel() != 1 \
-            or t.device != dev:
-        _refuse(f"{name} must be a one-element fp32 tensor on {dev}")
-    return t.data_ptr()
-
-
-def _rows(block_tables, ctx_lens_dev, row_starts, dev):
+def _rows(block_tables, ctx_lens_dev, row_starts, idx):
     """(tables, stride, row_starts, ctx_lens, batch) of the rows' sequences."""
-    bt = _want("block_tables", block_tables, torch.int32, dev, 2)
-    cl = _want("ctx_lens_dev", ctx_lens_dev, torch.int32, dev, 1)
+    bt = _want("block_tables", block_tables, torch.int32, idx, 2)
+    cl = _want("ctx_lens_dev", ctx_lens_dev, torch.int32, idx, 1)
     batch, stride = block_tables.shape
-    if ctx_lens_dev.shape[0] != batch:
+    if ctx_lens_dev.numel() != batch:
         _refuse("one context length and table row per sequence")
-    rs = None
+    rs = 0
     if row_starts is not None:
-        rs = _want("row_starts", row_starts, torch.int32, dev, 1)
-        if row_starts.shape[0] != batch + 1:
+        rs = _want("row_starts", row_starts, torch.int32, idx, 1)
+        if row_starts.numel() != batch + 1:
             _refuse("row_starts must hold batch + 1 starts")
     return bt, stride, rs, cl, batch
 
 
-def _cache_write(q, k, v, kcache, vcache, scales, block_tables, ctx_lens_dev, max_ctx_len,
-                 q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out, stream):
-    lib = load()
-    dev = _device_of(k)
+def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ctx_lens_dev,
+                 max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out,
+                 stream):
+    lib = load() if _lib is None else _lib
+    idx = _device_of(k)
     dtype = k.dtype
-    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+    if dtype is torch.float16:
+        kind = DTYPE_F16
+    elif dtype is torch.bfloat16:
+        kind = DTYPE_BF16
+    else:
         _refuse("k must be fp16 or bf16")
-    kp, vp, (num_pages, page, Hkv, D) = _pages(
-        kcache, vcache, torch.float16 if scales is None else torch.uint8, dev)
-    tokens = k.shape[0]
-    strides = []
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is None:
-            strides += [0, 0]
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev \
-                or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != D or t.stride(2) != 1:
-            _refuse(f"{name} must be [tokens, heads, D] like k, with D contiguous")
-        strides += t.stride()[:2]
-    if k.shape[1] != Hkv or v.shape[1] != Hkv:
+    kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache,
+                                               torch.uint8 if e4m3 else torch.float16, idx)
+    tokens = len(k)
+    hk, kt, kh = _heads("k", k, dtype, idx, tokens, D)
+    hv, vt, vh = _heads("v", v, dtype, idx, tokens, D)
+    if hk != Hkv or hv != Hkv:
         _refuse("k and v must have the cache's KV heads")
-    Hq = Hkv
-    qp = op = None
     if q is not None:
-        Hq = q.shape[1]
+        Hq, qt, qh = _heads("q", q, dtype, idx, tokens, D)
         if q_out is None:
-            q_out = torch.empty((tokens, Hq, D), dtype=torch.float16, device=dev)
-        qp, op = q.data_ptr(), _want("q_out", q_out, torch.float16, dev, 3)
+            q_out = torch.empty((tokens, Hq, D), dtype=torch.float16, device=k.device)
+        qp, op = q.data_ptr(), _want("q_out", q_out, torch.float16, idx, 3)
         if q_out.shape != q.shape:
             _refuse("q_out must have q's shape")
-    elif q_out is not None:
-        _refuse("q_out without q")
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        weights.append(None if w is None else _want(name, w, dtype, dev, 1))
-        if w is not None and w.shape[0] != D:
-            _refuse(f"{name} must hold D weights")
-    fp = rot = 0
-    if inv_freq is not None:
-        fp = _want("inv_freq", inv_freq, torch.float32, dev, 1)
-        rot = 2 * inv_freq.shape[0]
-    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
-    head = (qp, k.data_ptr(), v.data_ptr(), DTYPE_F16 if dtype is torch.float16 else DTYPE_BF16,
-            *strides, *weights, eps, fp, rot, 1 if interleaved else 0)
-    tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hq, Hkv, D, op, kp,
-            vp)
-    if scales is None:
-        _call(lib.gqa_cache_write, dev, stream, *head, *tail)
+    elif q_out is None:
+        Hq, qt, qh, qp, op = Hkv, 0, 0, 0, 0
     else:
-        _call(lib.gqa_cache_write_e4m3, dev, stream, *head,
-              _one_scale("kscale", scales[0], dev), _one_scale("vscale", scales[1], dev), *tail)
+        _refuse("q_out without q")
+    qw = kw = fp = rot = ks = vs = 0
+    if q_weight is not None:
+        qw = _want("q_weight", q_weight, dtype, idx, 1)
+        if q_weight.numel() != D:
+            _refuse("q_weight must hold D weights")
+    if k_weight is not None:
+        kw = _want("k_weight", k_weight, dtype, idx, 1)
+        if k_weight.numel() != D:
+            _refuse("k_weight must hold D weights")
+    if inv_freq is not None:
+        fp = _want("inv_freq", inv_freq, torch.float32, idx, 1)
+        rot = 2 * inv_freq.numel()
+    if e4m3:
+        ks, vs = _scale("kscale", kscale, idx), _scale("vscale", vscale, idx)
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
+    try:
+        args = _WRITE_ARGS.pack(qp, k.data_ptr(), v.data_ptr(), qw, kw, fp, ks, vs, bt, rs, cl,
+                                op, kp, vp, qt, qh, kt, kh, vt, vh, kind, rot,
+                                1 if interleaved else 0, eps, stride, num_pages, page,
+                                max_ctx_len, batch, tokens, Hq, Hkv, D)
+    except (struct.error, OverflowError, TypeError) as e:
+        _refuse(str(e))
+    _call(lib.gqa_cache_write_e4m3 if e4m3 else lib.gqa_cache_write, idx, stream, args)
     return q_out
 
 
@@ -497,80 +524,91 @@ def cache_write_e4m3(q, k, v, kcache, vcache, kscale, vscale, block_tables, ctx_
     views of a fused projection included; caches [pages,page,Hkv,D] uint8;
     block_tables [B, stride], ctx_lens_dev [B], row_starts [B+1] int32.
     Returns q_out [T,Hq,D] fp16 (None without q)."""
-    return _cache_write(q, k, v, kcache, vcache, (kscale, vscale), block_tables, ctx_lens_dev,
-                        max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts,
-                        q_out, stream)
+    return _cache_write(q, k, v, kcache, vcache, kscale, vscale, True, block_tables,
+                        ctx_lens_dev, max_ctx_len, q_weight, k_weight, eps, inv_freq,
+                        interleaved, row_starts, q_out, stream)
 
 
 def cache_write(q, k, v, kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len, q_weight=None,
                 k_weight=None, eps=1e-6, inv_freq=None, interleaved=False, row_starts=None,
                 q_out=None, stream=None):
     """cache_write_e4m3 over an fp16 cache (caches [pages,page,Hkv,D] fp16, no scales)."""
-    return _cache_write(q, k, v, kcache, vcache, None, block_tables, ctx_lens_dev, max_ctx_len,
-                        q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out,
-                        stream)
+    return _cache_write(q, k, v, kcache, vcache, None, None, False, block_tables, ctx_lens_dev,
+                        max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts,
+                        q_out, stream)
 
 
-def _cache_read(kcache, vcache, scales, block_tables, ctx_lens_dev, max_ctx_len, tokens,
-                row_starts, k_out, v_out, stream):
-    lib = load()
-    dev = _device_of(kcache)
+def _out_rows(name, t, tokens, Hkv, D, dtype, idx):
+    if t is None:
+        return torch.empty((tokens, Hkv, D), dtype=dtype, device=idx), None
+    p = _want(name, t, dtype, idx, 3)
+    if t.shape != (tokens, Hkv, D):
+        _refuse(f"{name} must be [tokens, Hkv, D]")
+    return t, p
+
+
+def _cache_read(kcache, vcache, kscale, vscale, e4m3, block_tables, ctx_lens_dev, max_ctx_len,
+                tokens, row_starts, k_out, v_out, stream):
+    lib = load() if _lib is None else _lib
+    idx = _device_of(kcache)
     dtype = kcache.dtype
-    if dtype is not torch.uint8 and (scales is not None or dtype is not torch.float16):
-        _refuse("caches must be uint8 codes" + ("" if scales else " or fp16"))
-    kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache, dtype, dev)
-    out_type = dtype if scales is None else torch.float16
-    outs = []
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty((tokens, Hkv, D), dtype=out_type, device=dev)
-        _want(name, t, out_type, dev, 3)
-        if t.shape != (tokens, Hkv, D):
-            _refuse(f"{name} must be [tokens, Hkv, D]")
-        outs.append(t)
-    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
+    if dtype is not torch.uint8 and (e4m3 or dtype is not torch.float16):
+        _refuse("caches must be uint8 codes" + ("" if e4m3 else " or fp16"))
+    kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache, dtype, idx)
+    out_type = torch.float16 if e4m3 else dtype
+    k_out, ko = _out_rows("k_out", k_out, tokens, Hkv, D, out_type, idx)
+    v_out, vo = _out_rows("v_out", v_out, tokens, Hkv, D, out_type, idx)
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
     tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hkv, D,
-            outs[0].data_ptr(), outs[1].data_ptr())
-    if scales is None:
-        _call(lib.gqa_cache_read, dev, stream, kp, vp, kcache.element_size(), *tail)
+            ko or k_out.data_ptr(), vo or v_out.data_ptr())
+    if e4m3:
+        _call(lib.gqa_cache_read_e4m3, idx, stream, kp, vp, _scale("kscale", kscale, idx),
+              _scale("vscale", vscale, idx), *tail)
     else:
-        _call(lib.gqa_cache_read_e4m3, dev, stream, kp, vp, _one_scale("kscale", scales[0], dev),
-              _one_scale("vscale", scales[1], dev), *tail)
-    return outs[0], outs[1]
+        _call(lib.gqa_cache_read, idx, stream, kp, vp, 1 if dtype is torch.uint8 else 2, *tail)
+    return k_out, v_out
 
 
 def cache_read_e4m3(kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
                     tokens, row_starts=None, k_out=None, v_out=None, stream=None):
     """The cached tokens of a batch's rows as dense fp16 K, V [tokens,Hkv,D]
     (gqa_cache_read_e4m3); the last tokens / B (or row_starts') of each context."""
-    return _cache_read(kcache, vcache, (kscale, vscale), block_tables, ctx_lens_dev, max_ctx_len,
-                       tokens, row_starts, k_out, v_out, stream)
+    return _cache_read(kcache, vcache, kscale, vscale, True, block_tables, ctx_lens_dev,
+                       max_ctx_len, tokens, row_starts, k_out, v_out, stream)
 
 
 def cache_read(kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len, tokens, row_starts=None,
                k_out=None, v_out=None, stream=None):
     """The same rows in the cache's own type: fp16, or E4M3 codes (uint8)."""
-    return _cache_read(kcache, vcache, None, block_tables, ctx_lens_dev, max_ctx_len, tokens,
-                       row_starts, k_out, v_out, stream)
+    return _cache_read(kcache, vcache, None, None, False, block_tables, ctx_lens_dev,
+                       max_ctx_len, tokens, row_starts, k_out, v_out, stream)
+
+
+def _index_pointers(index, index_scale, idx):
+    """Pointers of a block index and its [pages, page / 4, Hkv, D]."""
+    ip = _want("index", index, torch.int8, idx, 4)
+    sp = _want("index_scale", index_scale, torch.float32, idx, 2)
+    shape = index.shape
+    if index_scale.shape != shape[:2]:
+        _refuse("index must be [pages, page / 4, Hkv, D], index_scale [pages, page / 4]")
+    return ip, sp, shape
 
 
 def _block_index(kcache, kscale, e4m3, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
                  index_scale, row_starts, stream):
-    lib = load()
-    dev = _device_of(kcache)
-    kp = _want("kcache", kcache, torch.uint8 if e4m3 else torch.float16, dev, 4)
+    lib = load() if _lib is None else _lib
+    idx = _device_of(kcache)
+    kp = _want("kcache", kcache, torch.uint8 if e4m3 else torch.float16, idx, 4)
     num_pages, page, Hkv, D = kcache.shape
-    ip = _want("index", index, torch.int8, dev, 4)
-    sp = _want("index_scale", index_scale, torch.float32, dev, 2)
-    if index.shape != (num_pages, page // 4, Hkv, D) or index_scale.shape != index.shape[:2]:
+    ip, sp, shape = _index_pointers(index, index_scale, idx)
+    if shape != (num_pages, page // 4, Hkv, D):
         _refuse("index must be [pages, page / 4, Hkv, D], index_scale [pages, page / 4]")
-    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, dev)
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
     tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hkv, D, ip, sp)
     if e4m3:
-        _call(lib.gqa_block_index_e4m3, dev, stream, kp, _one_scale("kscale", kscale, dev),
-              *tail)
+        _call(lib.gqa_block_index_e4m3, idx, stream, kp, _scale("kscale", kscale, idx), *tail)
     else:
-        _call(lib.gqa_block_index, dev, stream, kp, *tail)
+        _call(lib.gqa_block_index, idx, stream, kp, *tail)
 
 
 def block_index_e4m3(kcache, kscale, block_tables, ctx_lens_dev, max_ctx_len, tokens, index,
@@ -595,28 +633,30 @@ def select_blocks(q, index, index_scale, block_table, ctx_len, max_sel, n_first=
     (gqa_select_blocks): q [rows,Hq,D] fp16, the sequence's block index and
     block_table [pages of ctx_len] int32.  Returns sel_idx [rows,max_sel] and
     sel_cnt [rows], as sparse_blocks takes them."""
-    lib = load()
-    dev = _device_of(q)
-    qp = _want("q", q, torch.float16, dev, 3)
-    ip = _want("index", index, torch.int8, dev, 4)
-    sp = _want("index_scale", index_scale, torch.float32, dev, 2)
-    bt = _want("block_table", block_table, torch.int32, dev, 1)
+    lib = load() if _lib is None else _lib
+    idx = _device_of(q)
+    qp = _want("q", q, torch.float16, idx, 3)
+    ip, sp, (num_pages, ppb, Hkv, d) = _index_pointers(index, index_scale, idx)
+    bt = _want("block_table", block_table, torch.int32, idx, 1)
     rows, Hq, D = q.shape
-    num_pages, ppb, Hkv, _ = index.shape
-    if index.shape[3] != D or index_scale.shape != index.shape[:2]:
-        _refuse("index must be [pages, page / 4, Hkv, D], index_scale [pages, page / 4]")
-    if block_table.shape[0] * ppb * 4 < ctx_len:
+    if d != D:
+        _refuse("q and index must have the same head size")
+    if block_table.numel() * ppb * 4 < ctx_len:
         _refuse("block_table must cover ctx_len")
     if sel_idx is None:
-        sel_idx = torch.empty((rows, max_sel), dtype=torch.int32, device=dev)
+        sel_idx = torch.empty((rows, max_sel), dtype=torch.int32, device=idx)
     if sel_cnt is None:
-        sel_cnt = torch.empty((rows,), dtype=torch.int32, device=dev)
-    xp = _want("sel_idx", sel_idx, torch.int32, dev, 2)
-    cp = _want("sel_cnt", sel_cnt, torch.int32, dev, 1)
-    if sel_idx.shape != (rows, max_sel) or sel_cnt.shape != (rows,):
+        sel_cnt = torch.empty((rows,), dtype=torch.int32, device=idx)
+    xp = _want("sel_idx", sel_idx, torch.int32, idx, 2)
+    cp = _want("sel_cnt", sel_cnt, torch.int32, idx, 1)
+    if sel_idx.shape != (rows, max_sel) or sel_cnt.numel() != rows:
         _refuse("sel_idx must be [rows, max_sel], sel_cnt [rows]")
-    with torch.cuda.device(dev):
-        ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D), dev)
-    _call(lib.gqa_select_blocks, dev, stream, qp, ip, sp, bt, num_pages, ppb * 4, ctx_len, rows,
-          Hq, Hkv, D, max_sel, n_first, n_last, xp, cp)
+    args = (qp, ip, sp, bt, num_pages, ppb * 4, ctx_len, rows, Hq, Hkv, D, max_sel, n_first,
+            n_last, xp, cp)
+    ws = _ws.get(idx)
+    if ws is None or torch._C._cuda_getDevice() != idx or \
+            ws.numel() < lib.gqa_workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D):
+        with torch.cuda.device(idx):
+            ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D), idx)
+    _call(lib.gqa_select_blocks, idx, stream, *args)
     return sel_idx, sel_cnt

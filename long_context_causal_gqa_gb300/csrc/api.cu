@@ -228,17 +228,21 @@ int rows_check(const CacheRows& r, int Hq, int Hkv, int D) {
     return GQA_OK;
 }
 
-int write_common(const CacheRows& r, const CacheWriteArgs& a, cudaStream_t stream) {
-    if (!a.x[1] || !a.x[2] || !a.kcache || !a.vcache || !a.x[0] != !a.q_out)
+int write_common(const gqa_cache_write_args* args, bool e4m3, cudaStream_t stream) {
+    if (!args) return GQA_ERR_INVALID_ARG;
+    const gqa_cache_write_args& a = *args;
+    const CacheRows r = {a.block_tables, a.row_starts, a.ctx_lens_dev, a.table_stride,
+                         a.num_pages, a.page, a.max_ctx_len, a.batch, a.tokens};
+    if (!a.k || !a.v || !a.kcache || !a.vcache || !a.q != !a.q_out) return GQA_ERR_INVALID_ARG;
+    if (e4m3 && (!a.kscale || !a.vscale || !aligned4(a.kscale) || !aligned4(a.vscale)))
         return GQA_ERR_INVALID_ARG;
-    if (a.e4m3 && (!a.kscale || !a.vscale || !aligned4(a.kscale) || !aligned4(a.vscale)))
-        return GQA_ERR_INVALID_ARG;
-    if (!aligned16(a.x[0]) || !aligned16(a.x[1]) || !aligned16(a.x[2]) || !aligned16(a.q_out) ||
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) ||
         !aligned16(a.kcache) || !aligned16(a.vcache) || !aligned16(a.q_weight) ||
         !aligned16(a.k_weight))
         return GQA_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i)
-        if (a.token_stride[i] % 8 || a.head_stride[i] % 8) return GQA_ERR_INVALID_ARG;
+    if ((a.q_token_stride | a.q_head_stride | a.k_token_stride | a.k_head_stride |
+         a.v_token_stride | a.v_head_stride) & 7)
+        return GQA_ERR_INVALID_ARG;
     if (a.dtype != GQA_DTYPE_F16 && a.dtype != GQA_DTYPE_BF16) return GQA_ERR_UNSUPPORTED;
     if (!isfinite(a.eps) || a.eps < 0.f) return GQA_ERR_INVALID_ARG;
     if (a.rot_dim < 0 || (a.rot_dim > 0 && (!a.inv_freq || !aligned4(a.inv_freq))))
@@ -246,7 +250,7 @@ int write_common(const CacheRows& r, const CacheWriteArgs& a, cudaStream_t strea
     const int rc = rows_check(r, a.Hq, a.Hkv, a.D);
     if (rc != GQA_OK) return rc;
     if (a.rot_dim > a.D || a.rot_dim % 16) return GQA_ERR_UNSUPPORTED;
-    return cache_write_launch(r, a, stream);
+    return cache_write_launch(r, a, e4m3, stream);
 }
 
 int read_common(const CacheRows& r, const void* kcache, const void* vcache, const float* kscale,
@@ -411,41 +415,12 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
                          stream);
 }
 
-int gqa_cache_write_e4m3(const void* q, const void* k, const void* v, int dtype,
-                         int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
-                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
-                         const void* q_weight, const void* k_weight, float eps,
-                         const float* inv_freq, int rot_dim, int interleaved,
-                         const float* kscale, const float* vscale, const int32_t* block_tables,
-                         int table_stride, int num_pages, int page, const int32_t* row_starts,
-                         const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
-                         int Hq, int Hkv, int D, void* q_out, uint8_t* kcache, uint8_t* vcache,
-                         struct CUstream_st* stream) {
-    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
-                         page, max_ctx_len, batch, tokens};
-    const CacheWriteArgs a = {{q, k, v}, {q_token_stride, k_token_stride, v_token_stride},
-                              {q_head_stride, k_head_stride, v_head_stride}, dtype, q_weight,
-                              k_weight, eps, inv_freq, rot_dim, interleaved, true, kscale,
-                              vscale, Hq, Hkv, D, q_out, kcache, vcache};
-    return write_common(r, a, stream);
+int gqa_cache_write_e4m3(const gqa_cache_write_args* args, struct CUstream_st* stream) {
+    return write_common(args, true, stream);
 }
 
-int gqa_cache_write(const void* q, const void* k, const void* v, int dtype,
-                    int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
-                    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
-                    const void* q_weight, const void* k_weight, float eps,
-                    const float* inv_freq, int rot_dim, int interleaved,
-                    const int32_t* block_tables, int table_stride, int num_pages, int page,
-                    const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
-                    int batch, int tokens, int Hq, int Hkv, int D, void* q_out, void* kcache,
-                    void* vcache, struct CUstream_st* stream) {
-    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
-                         page, max_ctx_len, batch, tokens};
-    const CacheWriteArgs a = {{q, k, v}, {q_token_stride, k_token_stride, v_token_stride},
-                              {q_head_stride, k_head_stride, v_head_stride}, dtype, q_weight,
-                              k_weight, eps, inv_freq, rot_dim, interleaved, false, nullptr,
-                              nullptr, Hq, Hkv, D, q_out, kcache, vcache};
-    return write_common(r, a, stream);
+int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream) {
+    return write_common(args, false, stream);
 }
 
 int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,

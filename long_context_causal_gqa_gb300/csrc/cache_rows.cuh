@@ -37,34 +37,11 @@ __device__ __forceinline__ void load_row_starts(const RowMap& m, int* s_starts) 
         for (int i = threadIdx.x; i <= m.batch; i += blockDim.x) s_starts[i] = m.row_starts[i];
 }
 
-// Position of `row` in its sequence and its token row in the cache.  Returns
-// pos = -1 for a padding row (behind the last sequence) and for a row whose
-// sequence has a context length outside [its rows, max_ctx] (flagged); slot =
-// -1 if the page table's entry is outside the cache (flagged).
-__device__ __forceinline__ void locate_row(const RowMap& m, const int* s_starts, int row,
-                                           int* pos, long long* slot) {
-    *pos = -1;
-    *slot = -1;
-    int b, j, n;
-    if (m.row_starts) {
-        // The last start <= row (empty sequences share a start with the next).
-        int lo = 0, hi = m.batch + 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_starts[mid] <= row) lo = mid + 1;
-            else hi = mid;
-        }
-        b = lo - 1;
-        if (b < 0 || b >= m.batch) return;
-        const int first = s_starts[b];
-        if (first < 0 || s_starts[b + 1] <= row) return;   // starts that do not ascend
-        j = row - first;
-        n = s_starts[b + 1] - first;
-    } else {
-        b = m.rows_per_seq.div(row);
-        n = m.rows_per_seq.d;
-        j = row - b * n;
-    }
+// Row j of the n rows of sequence b: its position and its token row in the
+// cache, slot = -1 if the page table's entry is outside the cache (flagged, as
+// is a context length outside [n, max_ctx]: pos = -1).
+__device__ __forceinline__ void locate_in_sequence(const RowMap& m, int b, int j, int n, int* pos,
+                                                   long long* slot) {
     const int ctx = m.ctx_lens[b];
     if (ctx < n || ctx > m.max_ctx) {
         atomicOr(m.err, kErrBadCtxLen);
@@ -78,6 +55,32 @@ __device__ __forceinline__ void locate_row(const RowMap& m, const int* s_starts,
         return;
     }
     *slot = ((long long)id << m.log2_page) + (p & ((1 << m.log2_page) - 1));
+}
+
+// Position of `row` in its sequence and its token row in the cache, -1 each for
+// a padding row (in front of the first sequence or behind the last).  One
+// thread, the starts in shared memory.
+__device__ __forceinline__ void locate_row(const RowMap& m, const int* s_starts, int row,
+                                           int* pos, long long* slot) {
+    *pos = -1;
+    *slot = -1;
+    if (!m.row_starts) {
+        const int b = m.rows_per_seq.div(row), n = m.rows_per_seq.d;
+        locate_in_sequence(m, b, row - b * n, n, pos, slot);
+        return;
+    }
+    // The last start <= row (empty sequences share a start with the next).
+    int lo = 0, hi = m.batch + 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_starts[mid] <= row) lo = mid + 1;
+        else hi = mid;
+    }
+    const int b = lo - 1;
+    if (b < 0 || b >= m.batch) return;
+    const int first = s_starts[b], end = s_starts[b + 1];
+    if (first < 0 || end <= row) return;   // starts that do not ascend
+    locate_in_sequence(m, b, row - first, end - first, pos, slot);
 }
 
 }  // namespace gqa

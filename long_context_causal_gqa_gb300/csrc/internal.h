@@ -146,21 +146,9 @@ struct CacheRows {
     int table_stride, num_pages, page, max_ctx_len, batch, tokens;
 };
 
-struct CacheWriteArgs {
-    const void* x[3];            // q (or null), k, v
-    long long token_stride[3], head_stride[3];
-    int dtype;
-    const void *q_weight, *k_weight;
-    float eps;
-    const float* inv_freq;
-    int rot_dim, interleaved;
-    bool e4m3;
-    const float *kscale, *vscale;
-    int Hq, Hkv, D;
-    void *q_out, *kcache, *vcache;
-};
-
-int cache_write_launch(const CacheRows& r, const CacheWriteArgs& a, cudaStream_t stream);
+// e4m3: the caches hold codes (a.kscale, a.vscale), else fp16.
+int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e4m3,
+                       cudaStream_t stream);
 // kscale / vscale: null to copy the cached rows as they are (row_bytes of K
 // and V per token), else E4M3 codes to fp16.
 int cache_read_launch(const CacheRows& r, const void* kcache, const void* vcache,

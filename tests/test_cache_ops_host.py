@@ -21,6 +21,21 @@ def lib():
     return binding.load()
 
 
+WRITE_FIELDS = [(n, ctypes.c_void_p) for n in
+                ("q", "k", "v", "qw", "kw", "freq", "ks", "vs", "bt", "starts", "ctx", "out", "kc",
+                 "vc")] + \
+               [(n, ctypes.c_int64) for n in ("qt", "qh", "kt", "kh", "vt", "vh")] + \
+               [("dtype", ctypes.c_int32), ("rot", ctypes.c_int32), ("inter", ctypes.c_int32),
+                ("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in
+                ("stride", "pages", "page", "max_ctx", "batch", "tokens", "Hq", "Hkv", "D")]
+
+
+class WriteArgs(ctypes.Structure):
+    """gqa_cache_write_args."""
+    _fields_ = WRITE_FIELDS
+
+
 def _write(lib, e4m3=True, **kw):
     a = dict(q=FAKE, k=FAKE, v=FAKE, dtype=0, qt=2048, qh=256, kt=2048, kh=256, vt=2048, vh=256,
              qw=FAKE, kw=FAKE, eps=1e-6, freq=FAKE, rot=64, inter=0, ks=FAKE, vs=FAKE, bt=FAKE,
@@ -28,13 +43,23 @@ def _write(lib, e4m3=True, **kw):
              Hq=6, Hkv=1, D=256, out=FAKE, kc=FAKE, vc=FAKE)
     assert not set(kw) - set(a)
     a.update(kw)
-    head = [a[x] for x in ("q", "k", "v", "dtype", "qt", "qh", "kt", "kh", "vt", "vh", "qw", "kw",
-                           "eps", "freq", "rot", "inter")]
-    scales = [a["ks"], a["vs"]] if e4m3 else []
-    tail = [a[x] for x in ("bt", "stride", "pages", "page", "starts", "ctx", "max_ctx", "batch",
-                           "tokens", "Hq", "Hkv", "D", "out", "kc", "vc")]
+    args = WriteArgs()
+    for name, x in a.items():
+        setattr(args, name, x)
     fn = lib.gqa_cache_write_e4m3 if e4m3 else lib.gqa_cache_write
-    return fn(*head, *scales, *tail, None)
+    return fn(bytes(args), None)
+
+
+def test_write_arguments_have_the_c_layout(lib):
+    """The binding packs gqa_cache_write_args itself: same size as the structure
+    the C compiler lays out."""
+    assert binding._WRITE_ARGS.size == ctypes.sizeof(WriteArgs)
+    packed = binding._WRITE_ARGS.pack(*range(1, 24), 0.5, *range(30, 39))
+    args = WriteArgs.from_buffer_copy(packed)
+    assert args.q == 1 and args.vc == 14 and args.vh == 20 and args.inter == 23
+    assert args.eps == 0.5 and args.stride == 30 and args.D == 38
+    assert lib.gqa_cache_write_e4m3(None, None) == INVALID
+    assert lib.gqa_cache_write(None, None) == INVALID
 
 
 ROW_REFUSALS = [
