@@ -13,8 +13,6 @@ namespace gqa {
 namespace cacheops {
 
 constexpr int THREADS = 256;
-constexpr int WRITE_WARPS = 16;         // write warps an SM is given before heads are shared out
-
 // 1 / (2 pi) as the sum of two floats.
 constexpr double kInvTwoPi = 0.15915494309189533577;
 constexpr float kInvTwoPiHi = (float)kInvTwoPi;
@@ -37,9 +35,8 @@ struct WriteParams {
     void* vcache;
     int nq;                      // query heads handled (0 without q)
     int hkv;
-    FastDiv shares;              // warps a token's heads are shared out to
-    int heads_per_share;
-    int tokens_per_warp;         // 1 if the heads are shared out
+    FastDiv by_pairs;
+    int tile;                    // tokens per CTA
 };
 
 // Two floats as one operand of the packed 32-bit operations.
@@ -106,220 +103,208 @@ __device__ __forceinline__ float2 turn(int pos, float hi, float lo) {
     return make_float2(__cosf(angle), __sinf(angle));
 }
 
-// A warp takes some tokens, one after the other, or when there are few a share
-// of one token's heads.  It finds all its tokens' cache rows at once (a lane
-// each), and always has the next WRITE_AHEAD heads' loads in flight while it
-// works on the present ones.  It computes the cos and sin of its lanes' own
-// pairs once for all heads of a token.  No thread waits for another warp.
-// (Tokens of a CTA sharing addresses and cos / sin through shared memory kept
-// 8000 rows at 21 us whatever the tile, and so did a warp for each token with
-// all loads in front: in both the loads of a warp and its work took turns.)
+// A CTA takes up to four tokens and a share of their heads.  Groups of DH / 8
+// lanes take one head of all its tokens at a time: the tokens' loads, sums,
+// products and stores run side by side (one token's head after the other, each
+// waiting for its own sum of squares, took 22 us for 8000 rows however they were
+// shared out), the next head's loads are in flight meanwhile, and a head's
+// weights serve all tokens.  The cos and sin of the tokens' pairs are computed
+// once for all heads, in shared memory, while the first loads are on their way.
 //
-// y = x / sqrt(mean(x^2) + eps) * w and the rotation in 32 bits; one rounding
-// at the end (fp16 for q, the cache's type for K and V).
+// y = x / sqrt(mean(x^2) + eps) * w and the rotation in 32 bits, two products
+// an instruction; one rounding at the end (fp16 for q, the cache's type for K
+// and V).
 //
-// DH / 8 lanes take a head (two heads a warp at DH = 128), each lane two runs of
-// four values: in the rotated part both members of four pairs, so no value
-// crosses lanes.  Pairs (i, i + rot / 2): runs 4 l and rot / 2 + 4 l; pairs
-// (2 i, 2 i + 1), and the values that do not turn: runs 8 l and 8 l + 4.
-constexpr int WRITE_AHEAD = 4;
+// A lane holds two runs of four values: in the rotated part both members of
+// four pairs, so no value crosses lanes.  Pairs (i, i + rot / 2): runs 4 l and
+// rot / 2 + 4 l; pairs (2 i, 2 i + 1), and the values that do not turn: runs 8 l
+// and 8 l + 4.
+constexpr int UNIT = 4;                 // tokens of a unit
 constexpr int WRITE_THREADS = 128;
+constexpr int WRITE_CTAS = 5;           // resident on an SM
+constexpr int MAX_ROT_PAIRS = 128;      // rotated pairs of a head (rot_dim <= 256)
 
 template <int DH, bool E4M3, bool BF16>
-__global__ void __launch_bounds__(WRITE_THREADS) write_kernel(const WriteParams P) {
+__global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const WriteParams P) {
     constexpr int LANES = DH / 8;
-    constexpr int GROUPS = 32 / LANES;     // heads a warp takes at once
-    constexpr int AHEAD = WRITE_AHEAD;
+    constexpr int GROUPS = WRITE_THREADS / LANES;
     __shared__ int s_starts[kRowsMaxBatch + 1];
-    const int warp = blockIdx.x * (WRITE_THREADS / 32) + threadIdx.x / 32;
-    const int part = P.shares.div(warp), share = warp - part * P.shares.d;
-    const int token0 = part * P.tokens_per_warp;
-    const int n_tokens = min(P.tokens_per_warp, P.rows.tokens - token0);
-    const int wlane = threadIdx.x % 32, lane = wlane % LANES, group = wlane / LANES;
+    __shared__ int s_pos[UNIT];
+    __shared__ long long s_cache[UNIT];    // element offset of the token, -1: none
+    __shared__ __align__(16) float s_cos[UNIT][MAX_ROT_PAIRS];
+    __shared__ __align__(16) float s_sin[UNIT][MAX_ROT_PAIRS];
+    const int t0 = blockIdx.x * P.tile;
+    const int nt = min(P.tile, P.rows.tokens - t0);
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    // The lanes of this group within the warp.
+    const uint32_t mates = LANES == 32 ? 0xffffffffu : 0xffffu << (16 * (group & 1));
     const bool turns = lane < P.pairs / 4;
     const bool split = turns && !P.interleaved;
     const int run0 = split ? lane * 4 : lane * 8;
     const int run1 = split ? P.pairs + lane * 4 : lane * 8 + 4;
     const int k0 = P.nq, v0 = k0 + P.hkv, heads = v0 + P.hkv;   // heads: q, then K, then V
-    const int h0 = share * P.heads_per_share, h1 = min(h0 + P.heads_per_share, heads);
+    // This group's heads.
+    const int groups = gridDim.y * GROUPS, per = (heads + groups - 1) / groups;
+    int head = (blockIdx.y * GROUPS + group) * per;
+    const int head_end = min(head + per, heads);
 
-    // The loads walk the tokens, and in each the heads of this group of lanes (h0
-    // + group, + GROUPS, ...), AHEAD at a time: where the next one's values are,
-    // up to the last head of its kind.
-    int load_token = token0, load_i = 0, load_h = h0 + group, load_end = 0;
-    const uint16_t* src = nullptr;
-    long long src_step = 0;
-    auto load = [&](uint2 (&raw)[AHEAD][2]) {
-        if (load_token >= token0 + n_tokens) return;
+    struct Place {
+        int kind, in_kind;
+    };
+    auto place = [&](int h) {
+        Place p;
+        p.kind = h < k0 ? 0 : h < v0 ? 1 : 2;
+        p.in_kind = h - (p.kind == 0 ? 0 : p.kind == 1 ? k0 : v0);
+        return p;
+    };
+    auto load = [&](const Place& p, uint2 (&raw)[UNIT][2]) {
+        const long long step = P.token_stride[p.kind];
+        const uint16_t* y = P.x[p.kind] + t0 * step + p.in_kind * P.head_stride[p.kind];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            if (load_h >= h1) break;
-            if (load_h >= load_end) {
-                const int kind = load_h < k0 ? 0 : load_h < v0 ? 1 : 2;
-                const int begin = kind == 0 ? 0 : kind == 1 ? k0 : v0;
-                load_end = kind == 0 ? k0 : kind == 1 ? v0 : heads;
-                src = P.x[kind] + load_token * P.token_stride[kind] +
-                      (load_h - begin) * P.head_stride[kind];
-                src_step = GROUPS * P.head_stride[kind];
-            }
-            raw[u][0] = *reinterpret_cast<const uint2*>(src + run0);
-            raw[u][1] = *reinterpret_cast<const uint2*>(src + run1);
-            src += src_step;
-            load_h += GROUPS;
-        }
-        load_i += AHEAD * GROUPS;
-        if (load_i >= h1 - h0) {
-            ++load_token;
-            load_i = 0;
-            load_h = h0 + group;
-            load_end = 0;
+        for (int i = 0; i < UNIT; ++i) {
+            if (i >= nt) break;
+            raw[i][0] = *reinterpret_cast<const uint2*>(y + run0);
+            raw[i][1] = *reinterpret_cast<const uint2*>(y + run1);
+            y += step;
         }
     };
-    uint2 next[AHEAD][2];
-    load(next);
+    uint2 next[UNIT][2];
+    Place at_next = place(head);
+    if (head < head_end) load(at_next, next);
 
     if (P.rows.row_starts) {
         load_row_starts(P.rows, s_starts);
         __syncthreads();
     }
-    if (n_tokens <= 0) return;
-    int my_pos = -1;             // lane i: token token0 + i
-    long long my_slot = -1;
-    if (wlane < n_tokens) locate_row(P.rows, s_starts, token0 + wlane, &my_pos, &my_slot);
-    const float inv[2] = {E4M3 ? 1.f / *P.kscale : 1.f, E4M3 ? 1.f / *P.vscale : 1.f};
-    float4 freq = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (turns) {
-        freq.x = P.inv_freq[lane * 4];
-        freq.y = P.inv_freq[lane * 4 + 1];
-        freq.z = P.inv_freq[lane * 4 + 2];
-        freq.w = P.inv_freq[lane * 4 + 3];
+    if (threadIdx.x < nt) {
+        long long slot;
+        locate_row(P.rows, s_starts, t0 + threadIdx.x, &s_pos[threadIdx.x], &slot);
+        s_cache[threadIdx.x] = slot < 0 ? -1 : slot * (P.hkv * DH);
     }
-
-    for (int i_token = 0; i_token < n_tokens; ++i_token) {
-    const int token = token0 + i_token;
-    const int pos = __shfl_sync(0xffffffffu, my_pos, i_token);
-    const long long slot = __shfl_sync(0xffffffffu, my_slot, i_token);
-    Pair c[2], s[2];     // cos and sin of pairs 4 l .. 4 l + 3
-    if (turns) {
-        float cs[4], sn[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float f = i == 0 ? freq.x : i == 1 ? freq.y : i == 2 ? freq.z : freq.w;
+    const float kinv = E4M3 ? 1.f / *P.kscale : 1.f, vinv = E4M3 ? 1.f / *P.vscale : 1.f;
+    __syncthreads();
+    if (P.pairs) {
+        for (int i = threadIdx.x; i < nt * P.pairs; i += WRITE_THREADS) {
+            const int t = P.by_pairs.div(i), j = i - t * P.pairs;
+            const float f = P.inv_freq[j];
             const float hi = __fmul_rn(f, kInvTwoPiHi);
             const float lo = __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -hi));
-            const float2 t = turn(max(pos, 0), hi, lo);
-            cs[i] = t.x;
-            sn[i] = t.y;
+            const float2 cs = turn(max(s_pos[t], 0), hi, lo);
+            s_cos[t][j] = cs.x;
+            s_sin[t][j] = cs.y;
         }
-        c[0] = pack(cs[0], cs[1]);
-        c[1] = pack(cs[2], cs[3]);
-        s[0] = pack(sn[0], sn[1]);
-        s[1] = pack(sn[2], sn[3]);
+        __syncthreads();
     }
 
-    // The head at hand: its kind until `end`, that kind's weights (or 1 / scale
-    // for V), and where it goes.
-    int h = h0 + group, end = 0, kind = 0;
-    bool norm = false, store = true;
-    float scale = 1.f;
+    int weights_of = -1;     // the kind w belongs to
     Pair w[4];
-    uint8_t* out = nullptr;
-    long long out_step = 0;
-    const int warp_end = h1 - h0;
-    // Every lane of a warp takes the same number of heads (the shuffles need it);
-    // one past the last is not stored.
-    for (int i0 = 0; i0 < warp_end; i0 += AHEAD * GROUPS) {
-        uint2 raw[AHEAD][2];
+    for (; head < head_end; ++head) {
+        const Place p = at_next;
+        Pair x[UNIT][4];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            raw[u][0] = next[u][0];
-            raw[u][1] = next[u][1];
+        for (int i = 0; i < UNIT; ++i) {
+            x[i][0] = unpack16<BF16>(next[i][0].x);
+            x[i][1] = unpack16<BF16>(next[i][0].y);
+            x[i][2] = unpack16<BF16>(next[i][1].x);
+            x[i][3] = unpack16<BF16>(next[i][1].y);
         }
-        load(next);
-        if (pos < 0) continue;
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            if (i0 + u * GROUPS >= warp_end) break;
-            if (h >= end) {
-                kind = h < k0 ? 0 : h < v0 ? 1 : 2;
-                end = kind == 0 ? k0 : kind == 1 ? v0 : heads;
-                const int head = h - (kind == 0 ? 0 : kind == 1 ? k0 : v0);
-                if (kind == 0) {
-                    out = reinterpret_cast<uint8_t*>(P.q_out +
-                                                     ((long long)token * P.nq + head) * DH);
-                    out_step = GROUPS * DH * 2;
-                } else {
-                    constexpr int SIZE = E4M3 ? 1 : 2;
-                    out = static_cast<uint8_t*>(kind == 1 ? P.kcache : P.vcache) +
-                          (slot * P.hkv + head) * (DH * SIZE);
-                    out_step = GROUPS * DH * SIZE;
-                    scale = inv[kind - 1];
-                }
-                store = h < h1 && (kind == 0 || slot >= 0);
-                const uint16_t* weight = kind < 2 ? P.weight[kind] : nullptr;
-                norm = weight != nullptr;
-                if (norm) {
-                    const uint2 a = *reinterpret_cast<const uint2*>(weight + run0);
-                    const uint2 b = *reinterpret_cast<const uint2*>(weight + run1);
-                    w[0] = unpack16<BF16>(a.x);
-                    w[1] = unpack16<BF16>(a.y);
-                    w[2] = unpack16<BF16>(b.x);
-                    w[3] = unpack16<BF16>(b.y);
-                }
+        if (head + 1 < head_end) {
+            at_next = place(head + 1);
+            load(at_next, next);
+        }
+        const uint16_t* weight = p.kind < 2 ? P.weight[p.kind] : nullptr;
+        if (weight) {
+            if (weights_of != p.kind) {
+                const uint2 a = *reinterpret_cast<const uint2*>(weight + run0);
+                const uint2 b = *reinterpret_cast<const uint2*>(weight + run1);
+                w[0] = unpack16<BF16>(a.x);
+                w[1] = unpack16<BF16>(a.y);
+                w[2] = unpack16<BF16>(b.x);
+                w[3] = unpack16<BF16>(b.y);
+                weights_of = p.kind;
             }
-            Pair x[4] = {unpack16<BF16>(raw[u][0].x), unpack16<BF16>(raw[u][0].y),
-                         unpack16<BF16>(raw[u][1].x), unpack16<BF16>(raw[u][1].y)};
-            if (i0 + u * GROUPS + h0 < v0) {      // (not all V)
-                Pair sq = mul2(x[0], x[0]);
+            float ss[UNIT];
 #pragma unroll
-                for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+            for (int i = 0; i < UNIT; ++i) {
+                Pair sq = mul2(x[i][0], x[i][0]);
+#pragma unroll
+                for (int k = 1; k < 4; ++k) sq = fma2(x[i][k], x[i][k], sq);
                 const float2 halves = unpack(sq);
-                float ss = halves.x + halves.y;
+                ss[i] = halves.x + halves.y;
+            }
 #pragma unroll
-                for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (norm) {
-                    const float r = rsqrtf(ss * (1.f / DH) + P.eps);
-                    const Pair rr = pack(r, r);
+            for (int o = LANES / 2; o; o >>= 1)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(x[i], rr), w[i]);
-                }
-                if (turns && kind < 2) {
-                    if (split) {
+                for (int i = 0; i < UNIT; ++i) ss[i] += __shfl_xor_sync(mates, ss[i], o);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const Pair a = x[i], b = x[2 + i];
-                            // (the sign of a packed operand is one bit each)
-                            const Pair minus_s = s[i] ^ 0x8000000080000000ull;
-                            x[i] = fma2(b, minus_s, mul2(a, c[i]));
-                            x[2 + i] = fma2(a, s[i], mul2(b, c[i]));
-                        }
-                    } else {
+            for (int i = 0; i < UNIT; ++i) {
+                const float r = rsqrtf(ss[i] * (1.f / DH) + P.eps);
+                const Pair rr = pack(r, r);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 ab = unpack(x[i]);
-                            const float2 c2 = unpack(c[i / 2]), s2 = unpack(s[i / 2]);
-                            const float ci = i & 1 ? c2.y : c2.x, si = i & 1 ? s2.y : s2.x;
-                            x[i] = pack(ab.x * ci - ab.y * si, ab.y * ci + ab.x * si);
-                        }
+                for (int k = 0; k < 4; ++k) x[i][k] = mul2(mul2(x[i][k], rr), w[k]);
+            }
+        }
+        if (turns && p.kind < 2) {
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i) {
+                // (past the last token: whatever is there, for values that go nowhere)
+                const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[i][lane * 4]);
+                const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[i][lane * 4]);
+                if (split) {
+                    const Pair c[2] = {pack(c4.x, c4.y), pack(c4.z, c4.w)};
+                    const Pair s[2] = {pack(s4.x, s4.y), pack(s4.z, s4.w)};
+                    const Pair m[2] = {pack(-s4.x, -s4.y), pack(-s4.z, -s4.w)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const Pair a = x[i][k], b = x[i][2 + k];
+                        x[i][k] = fma2(b, m[k], mul2(a, c[k]));
+                        x[i][2 + k] = fma2(a, s[k], mul2(b, c[k]));
+                    }
+                } else {
+                    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 ab = unpack(x[i][k]);
+                        x[i][k] = pack(ab.x * c[k] - ab.y * s[k], ab.y * c[k] + ab.x * s[k]);
                     }
                 }
             }
-            h += GROUPS;
-            uint8_t* const to = out;
-            out += out_step;
-            if (!store || h - GROUPS >= h1) continue;
-            if (E4M3 && kind > 0) {
-                const Pair f = pack(scale, scale);
+        }
+        if (p.kind == 0) {
+            __half* to = P.q_out + ((long long)t0 * P.nq + p.in_kind) * DH;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], f);
-                *reinterpret_cast<uint32_t*>(to + run0) = to_e4m3x2(x[0]) | to_e4m3x2(x[1]) << 16;
-                *reinterpret_cast<uint32_t*>(to + run1) = to_e4m3x2(x[2]) | to_e4m3x2(x[3]) << 16;
+            for (int i = 0; i < UNIT; ++i) {
+                if (i < nt && s_pos[i] >= 0) {
+                    *reinterpret_cast<uint2*>(to + run0) =
+                        make_uint2(to_half2(x[i][0]), to_half2(x[i][1]));
+                    *reinterpret_cast<uint2*>(to + run1) =
+                        make_uint2(to_half2(x[i][2]), to_half2(x[i][3]));
+                }
+                to += P.nq * DH;
+            }
+            continue;
+        }
+        void* const cache = p.kind == 1 ? P.kcache : P.vcache;
+        const float f = p.kind == 1 ? kinv : vinv;
+        const Pair ff = pack(f, f);
+#pragma unroll
+        for (int i = 0; i < UNIT; ++i) {
+            if (i >= nt || s_cache[i] < 0) continue;
+            const long long at = s_cache[i] + p.in_kind * DH;
+            if (E4M3) {
+                uint8_t* to = static_cast<uint8_t*>(cache) + at;
+                *reinterpret_cast<uint32_t*>(to + run0) =
+                    to_e4m3x2(mul2(x[i][0], ff)) | to_e4m3x2(mul2(x[i][1], ff)) << 16;
+                *reinterpret_cast<uint32_t*>(to + run1) =
+                    to_e4m3x2(mul2(x[i][2], ff)) | to_e4m3x2(mul2(x[i][3], ff)) << 16;
             } else {
-                *reinterpret_cast<uint2*>(to + 2 * run0) = make_uint2(to_half2(x[0]), to_half2(x[1]));
-                *reinterpret_cast<uint2*>(to + 2 * run1) = make_uint2(to_half2(x[2]), to_half2(x[3]));
+                __half* to = static_cast<__half*>(cache) + at;
+                *reinterpret_cast<uint2*>(to + run0) =
+                    make_uint2(to_half2(x[i][0]), to_half2(x[i][1]));
+                *reinterpret_cast<uint2*>(to + run1) =
+                    make_uint2(to_half2(x[i][2]), to_half2(x[i][3]));
             }
         }
-    }
     }
 }
 
@@ -556,7 +541,7 @@ RowMap make_rows(const CacheRows& r, const DeviceInfo* di) {
 }
 
 template <int DH, bool E4M3>
-void launch_write(const WriteParams& P, bool bf16, int grid, cudaStream_t stream) {
+void launch_write(const WriteParams& P, bool bf16, dim3 grid, cudaStream_t stream) {
     if (bf16) write_kernel<DH, E4M3, true><<<grid, WRITE_THREADS, 0, stream>>>(P);
     else write_kernel<DH, E4M3, false><<<grid, WRITE_THREADS, 0, stream>>>(P);
 }
@@ -591,22 +576,16 @@ int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e
     P.vcache = a.vcache;
     P.nq = a.q ? a.Hq : 0;
     P.hkv = a.Hkv;
-    // About as many warps as the device holds: few tokens share out their heads
-    // (at most one for each head, or pair of heads at D = 128, that a warp takes
-    // at once), many go several to a warp.
-    const int heads = P.nq + 2 * P.hkv, at_once = 256 / a.D;
-    const int warps = di->num_sms * WRITE_WARPS;
-    int shares = (heads + at_once - 1) / at_once;
-    const int full = (warps + r.tokens - 1) / r.tokens;
-    if (shares > full) shares = full;
-    P.heads_per_share = (heads + shares - 1) / shares;
-    P.heads_per_share = (P.heads_per_share + at_once - 1) / at_once * at_once;
-    shares = (heads + P.heads_per_share - 1) / P.heads_per_share;
-    P.shares = make_fastdiv(shares);
-    const int per = shares > 1 ? 1 : (r.tokens + warps - 1) / warps;
-    P.tokens_per_warp = per < 32 ? per : 32;
-    const long long parts = (r.tokens + P.tokens_per_warp - 1) / P.tokens_per_warp;
-    const int grid = (int)((parts * shares + WRITE_THREADS / 32 - 1) / (WRITE_THREADS / 32));
+    P.by_pairs = make_fastdiv(P.pairs > 0 ? P.pairs : 1);
+    // Few tokens go one to a CTA; their heads are shared out as far as that keeps
+    // all CTAs resident at once.
+    const int heads = P.nq + 2 * P.hkv, groups = WRITE_THREADS * 8 / a.D;
+    const long long resident = (long long)di->num_sms * WRITE_CTAS;
+    P.tile = (long long)r.tokens * heads <= resident * groups ? 1 : UNIT;
+    const int tiles = (r.tokens + P.tile - 1) / P.tile;
+    long long shares = (heads + groups - 1) / groups;
+    if (shares > resident / tiles) shares = resident / tiles > 0 ? resident / tiles : 1;
+    const dim3 grid(tiles, (unsigned)shares);
     const bool bf16 = a.dtype == GQA_DTYPE_BF16;
     if (e4m3) {
         if (a.D == 256) launch_write<256, true>(P, bf16, grid, stream);
