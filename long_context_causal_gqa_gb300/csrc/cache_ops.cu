@@ -392,6 +392,7 @@ struct IndexParams {
     int8_t* index;
     float* index_scale;
     int width;             // Hkv * D, a multiple of 128, at most 1024
+    int rows_per_warp;
 };
 
 // Eight keys' values of 16 (fp16) or 8 (E4M3) bytes.
@@ -433,8 +434,8 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 }
 
 // Summaries of the 4-token blocks whose last token is a row of this step.  A
-// warp takes 32 rows, a lane each to find the blocks they finish, then block
-// after block: 8 values a lane of each 256 (CHUNKS of them), the keys of
+// warp takes rows_per_warp rows (32, or 8 when there are few), a lane each to
+// find the blocks they finish, then block after block: 8 values a lane of each 256 (CHUNKS of them), the keys of
 // TOGETHER blocks in flight together.  The sums, the largest magnitude and the
 // codes follow fixed 32-bit operations, so the codes are the same wherever and
 // in whatever batch a block is summarised.
@@ -449,10 +450,10 @@ __global__ void __launch_bounds__(INDEX_THREADS) index_kernel(const IndexParams 
         __syncthreads();
     }
     const int lane = threadIdx.x % 32;
-    const int row = blockIdx.x * INDEX_THREADS + threadIdx.x;
+    const int row = (blockIdx.x * (INDEX_THREADS / 32) + threadIdx.x / 32) * P.rows_per_warp + lane;
     int pos = -1;
     long long slot = -1;
-    if (row < P.rows.tokens) locate_row(P.rows, s_starts, row, &pos, &slot);
+    if (lane < P.rows_per_warp && row < P.rows.tokens) locate_row(P.rows, s_starts, row, &pos, &slot);
     const float unit = E4M3 ? *P.kscale / 508.f : 1.f / 508.f;
     uint32_t ends = __ballot_sync(0xffffffffu, (pos & 3) == 3 && slot >= 0);
     while (ends) {
@@ -632,7 +633,9 @@ int block_index_launch(const CacheRows& r, const void* kcache, const float* ksca
     P.index = index;
     P.index_scale = index_scale;
     P.width = width;
-    const int grid = (r.tokens + INDEX_THREADS - 1) / INDEX_THREADS;
+    P.rows_per_warp = r.tokens <= di->num_sms * 128 ? 8 : 32;
+    const int a_cta = INDEX_THREADS / 32 * P.rows_per_warp;
+    const int grid = (r.tokens + a_cta - 1) / a_cta;
     if (kscale) launch_index<true>(P, grid, stream);
     else launch_index<false>(P, grid, stream);
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;

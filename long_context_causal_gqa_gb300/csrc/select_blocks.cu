@@ -80,6 +80,10 @@ __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t u = __float_as_uint(f + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
 // A bound that nothing reaches (a comparison with NaN is false).
 #define kNoBound __int_as_float(0x7fffffff)
 
@@ -691,11 +695,11 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------ few rows
-// Every CTA makes the codes of its (up to 8) rows itself, which costs less
-// than a launch of its own; a warp then takes 8 blocks at a time, eight lanes
-// reading one block's codes 16 bytes each, and keeps the scores and their
-// maximum over the scored ones.
-constexpr int FEW_TILE = 8;
+// Every CTA makes the codes of its rows itself, which costs less than a launch
+// of its own, with its first blocks' codes already on their way.  Eight lanes
+// read one block's codes, 16 bytes each at a time; a warp takes 4 * PER blocks
+// together and keeps the scores and, over each 8 blocks, the largest scored one.
+constexpr int FEW_TILE = 8;      // most rows of a CTA
 
 struct FewParams {
     CodeParams C;
@@ -707,14 +711,34 @@ struct FewParams {
     float* maxima;               // [rows, stride / 8]
 };
 
-template <int CHUNKS>
+// NR: rows of a CTA, 1 or FEW_TILE.
+template <int CHUNKS, int NR>
 __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
-    __shared__ __align__(16) uint2 s_q[FEW_TILE][kMaxIndexWidth / 8];
+    constexpr int PER = CHUNKS == 1 && NR == 1 ? 4 : 2;
+    constexpr int STEPS = CHUNKS * 2;          // 128 codes each
+    __shared__ __align__(16) uint2 s_q[NR][CHUNKS * 32];
     let_next_launch();
-    const int width = P.V.width;
-    const int r0 = blockIdx.y * FEW_TILE;
-    const int nr = min(FEW_TILE, P.C.rows - r0);
+    const int width = P.V.width, steps = width / 128;
+    const int r0 = blockIdx.y * NR;
+    const int nr = NR == 1 ? 1 : min(NR, P.C.rows - r0);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int sub = lane / 8, part = lane % 8;
+    uint4 k[PER][STEPS];
+    float scale[PER];
+    // This lane's blocks: b0 + 4 i + sub.
+    auto fetch = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const long long block = physical_block(P.V, min(b0 + 4 * i + sub, P.n - 1));
+            const uint4* src = reinterpret_cast<const uint4*>(P.V.index + block * width) + part;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                if (s < steps) k[i][s] = src[s * 8];
+            scale[i] = P.V.scale[block];
+        }
+    };
+    int b0 = (blockIdx.x * 8 + warp) * (4 * PER);
+    if (b0 < P.n) fetch(b0);
     if (warp < nr) {
         uint2 w[CHUNKS];
         query_codes<CHUNKS>(P.C, r0 + warp, lane, w);
@@ -723,59 +747,63 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
             if (c * 256 + lane * 8 < width) s_q[warp][c * 32 + lane] = w[c];
     }
     __syncthreads();
-    const int sub = lane / 8, part = lane % 8;
-    for (int b0 = (blockIdx.x * 8 + warp) * 8; b0 < P.n; b0 += gridDim.x * 64) {
-        // This lane's blocks: b0 + sub and b0 + 4 + sub.
-        const uint4* src[2];
-        float scale[2];
+    while (b0 < P.n) {
+        int dot[PER][NR];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const long long block = physical_block(P.V, min(b0 + 4 * i + sub, P.n - 1));
-            src[i] = reinterpret_cast<const uint4*>(P.V.index + block * width);
-            scale[i] = P.V.scale[block];
-        }
-        int dot[2][FEW_TILE];
+        for (int r = 0; r < NR; ++r) {
 #pragma unroll
-        for (int r = 0; r < FEW_TILE; ++r) dot[0][r] = dot[1][r] = 0;
-#pragma unroll 2
-        for (int c = part; c < width / 16; c += 8) {
-            const uint4 k0 = src[0][c], k1 = src[1][c];
+            for (int i = 0; i < PER; ++i) dot[i][r] = 0;
+            if (r >= nr) break;
 #pragma unroll
-            for (int r = 0; r < FEW_TILE; ++r) {
-                if (r >= nr) break;
-                const uint4 x = reinterpret_cast<const uint4*>(s_q[r])[c];
-                dot[0][r] = __dp4a((int)k0.x, (int)x.x, dot[0][r]);
-                dot[1][r] = __dp4a((int)k1.x, (int)x.x, dot[1][r]);
-                dot[0][r] = __dp4a((int)k0.y, (int)x.y, dot[0][r]);
-                dot[1][r] = __dp4a((int)k1.y, (int)x.y, dot[1][r]);
-                dot[0][r] = __dp4a((int)k0.z, (int)x.z, dot[0][r]);
-                dot[1][r] = __dp4a((int)k1.z, (int)x.z, dot[1][r]);
-                dot[0][r] = __dp4a((int)k0.w, (int)x.w, dot[0][r]);
-                dot[1][r] = __dp4a((int)k1.w, (int)x.w, dot[1][r]);
+            for (int s = 0; s < STEPS; ++s) {
+                if (s >= steps) break;
+                const uint4 x = reinterpret_cast<const uint4*>(s_q[r])[s * 8 + part];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    dot[i][r] = __dp4a((int)k[i][s].x, (int)x.x, dot[i][r]);
+                    dot[i][r] = __dp4a((int)k[i][s].y, (int)x.y, dot[i][r]);
+                    dot[i][r] = __dp4a((int)k[i][s].z, (int)x.z, dot[i][r]);
+                    dot[i][r] = __dp4a((int)k[i][s].w, (int)x.w, dot[i][r]);
+                }
             }
         }
 #pragma unroll
-        for (int r = 0; r < FEW_TILE; ++r) {
+        for (int r = 0; r < NR; ++r) {
             if (r >= nr) break;
             const int row = r0 + r;
             const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;
-            float most = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                int d = dot[i][r];
-                d += __shfl_xor_sync(0xffffffffu, d, 4);
-                d += __shfl_xor_sync(0xffffffffu, d, 2);
-                d += __shfl_xor_sync(0xffffffffu, d, 1);
-                const int b = b0 + 4 * i + sub;
-                const float v = __fmul_rn((float)d, scale[i]);
-                if (part == 0 && b < P.n) P.scores[row * P.stride + b] = v;
-                if (b >= P.n_first && b < hi) most = fmaxf(most, v);
+            for (int i = 0; i < PER; i += 2) {
+                float most = -INFINITY;
+#pragma unroll
+                for (int j = i; j < i + 2; ++j) {
+                    int d = dot[j][r];
+                    d += __shfl_xor_sync(0xffffffffu, d, 4);
+                    d += __shfl_xor_sync(0xffffffffu, d, 2);
+                    d += __shfl_xor_sync(0xffffffffu, d, 1);
+                    const int b = b0 + 4 * j + sub;
+                    const float v = __fmul_rn((float)d, scale[j]);
+                    if (part == 0 && b < P.n) P.scores[row * P.stride + b] = v;
+                    if (b >= P.n_first && b < hi) most = fmaxf(most, v);
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+                if (lane == 0) P.maxima[row * (P.stride / 8) + b0 / 8 + i / 2] = most;
             }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-            if (lane == 0) P.maxima[row * (P.stride / 8) + b0 / 8] = most;
         }
+        b0 += gridDim.x * 8 * (4 * PER);
+        if (b0 < P.n) fetch(b0);
     }
+}
+
+template <int CHUNKS>
+void launch_score_few(const FewParams& F, const DeviceInfo* di, cudaStream_t stream) {
+    const bool one = F.C.rows == 1;
+    const int a_cta = 8 * 4 * (CHUNKS == 1 && one ? 4 : 2);
+    const int tiles = (F.n + a_cta - 1) / a_cta, cap = di->num_sms * 4;
+    const dim3 grid(tiles < cap ? tiles : cap, one ? 1 : (F.C.rows + FEW_TILE - 1) / FEW_TILE);
+    if (one) score_few_kernel<CHUNKS, 1><<<grid, 256, 0, stream>>>(F);
+    else score_few_kernel<CHUNKS, FEW_TILE><<<grid, 256, 0, stream>>>(F);
 }
 
 // ------------------------------------------------------------ the best blocks
@@ -818,31 +846,55 @@ __device__ __forceinline__ int cta_scan(int v, int* sums) {
     return v + before;
 }
 
-// A limit for the `need` largest of key(0) .. key(total - 1), 1 <= need <=
-// total, keys above 0: those above it are taken, and `equals` of those equal to
-// it.
-// Counts over BINS equal parts of the keys' range, then of the part that holds
-// the need-th largest, until what is in the part is taken whole.  No key is
-// outside [least, most].
+// The smallest and the largest of key[0 .. total), all above 0.
+template <int THREADS>
+__device__ void range_of(const uint32_t* key, int total, uint32_t* least, uint32_t* most,
+                         BestShared<THREADS>& S) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t a = ~0u, b = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < total; i += THREADS) {
+        const uint32_t k = key[i];
+        a = min(a, k);
+        b = max(b, k);
+    }
+    a = __reduce_min_sync(0xffffffffu, a);
+    b = __reduce_max_sync(0xffffffffu, b);
+    if (lane == 0) {
+        S.least[warp] = a;
+        S.most[warp] = b;
+    }
+    __syncthreads();
+    *least = __reduce_min_sync(0xffffffffu, S.least[lane % (THREADS / 32)]);
+    *most = __reduce_max_sync(0xffffffffu, S.most[lane % (THREADS / 32)]);
+}
+
+// A limit for the `need` largest of key[0 .. total), 1 <= need <= those in
+// [least, most] (0: not to be counted; none is above most): those above the
+// limit are taken, and `equals` of those equal to it.  Counts over BINS equal
+// parts of the keys' range, then of the part that holds the need-th largest,
+// until what is in the part is taken whole.
 struct Limit {
     uint32_t key;
     int equals;
 };
 
-template <int THREADS, typename KeyOf>
-__device__ Limit need_th(const KeyOf& key, int total, int need, uint32_t least, uint32_t most,
-                         BestShared<THREADS>& S) {
+template <int THREADS>
+__device__ __forceinline__ Limit need_th(const uint32_t* key, int total, int need, uint32_t least,
+                                         uint32_t most, BestShared<THREADS>& S) {
     constexpr int LOG2_BINS = BestShared<THREADS>::LOG2_BINS, BINS = 1 << LOG2_BINS;
     const int tid = threadIdx.x;
     uint32_t lo = least, width = most - least;   // keys of interest: [lo, lo + width]
+#pragma unroll 1
     for (;;) {
         const int shift = width >> LOG2_BINS ? 32 - LOG2_BINS - __clz((int)width) : 0;
         constexpr int PER = BINS / THREADS;
 #pragma unroll
         for (int i = 0; i < PER; ++i) S.hist[tid + i * THREADS] = 0;
         __syncthreads();
+#pragma unroll 1
         for (int i = tid; i < total; i += THREADS) {
-            const uint32_t k = key(i) - lo;      // below lo: wraps to beyond width
+            const uint32_t k = key[i] - lo;      // below lo: wraps to beyond width
             if (k <= width) atomicAdd(&S.hist[k >> shift], 1);
         }
         __syncthreads();
@@ -870,53 +922,46 @@ __device__ Limit need_th(const KeyOf& key, int total, int need, uint32_t least, 
         need = S.left;
         if (S.count == need) return {lo - 1, 0};
         if (shift == 0) return {lo, need};
-        width = (1u << shift) - 1;
+        // (the last part may end beyond `most`: no key is there, but 0 would be)
+        width = min((1u << shift) - 1, most - lo);
         __syncthreads();
     }
 }
 
-// The smallest and the largest key.
-template <int THREADS, typename KeyOf>
-__device__ void range_of(const KeyOf& key, int total, uint32_t* least, uint32_t* most,
-                         BestShared<THREADS>& S) {
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    uint32_t a = ~0u, b = 0;
-    for (int i = tid; i < total; i += THREADS) {
-        const uint32_t k = key(i);
-        a = min(a, k);
-        b = max(b, k);
-    }
-    a = __reduce_min_sync(0xffffffffu, a);
-    b = __reduce_max_sync(0xffffffffu, b);
-    if (lane == 0) {
-        S.least[warp] = a;
-        S.most[warp] = b;
-    }
-    __syncthreads();
-    *least = __reduce_min_sync(0xffffffffu, S.least[lane % (THREADS / 32)]);
-    *most = __reduce_max_sync(0xffffffffu, S.most[lane % (THREADS / 32)]);
+// The same as a function, for a kernel that runs once on one SM and pays more
+// for each instruction's first fetch than for executing it.
+template <int THREADS>
+__device__ __noinline__ Limit need_th_called(const uint32_t* key, int total, int need,
+                                             uint32_t least, uint32_t most,
+                                             BestShared<THREADS>& S) {
+    return need_th<THREADS>(key, total, need, least, most, S);
 }
 
 // Writes the taken blocks in ascending order: those below R.lo, those from
-// R.hi on, and the R.need best of the candidates (key[i] > 0 and within [least,
-// most], id[i]), i < total, equal keys by the lower id.  total >= R.need.  bits:
-// room for one per id of a window, in whole uint4.
-template <int THREADS>
-__device__ void best_of(const RowRange& R, const uint32_t* key, const int* id, int total,
-                        uint32_t least, uint32_t most, int32_t* out, uint32_t* bits,
-                        BestShared<THREADS>& S) {
+// R.hi on, and the R.need best of the candidates (key[i] within [least, most],
+// id[i]), i < total, equal keys by the lower id; key[] does not outlast the
+// call.  total >= R.need.  bits: room for one per id of a window, in whole uint4.
+template <int THREADS, bool CALLED>
+__device__ __forceinline__ void best_of(const RowRange& R, uint32_t* key, const int* id, int total,
+                                        uint32_t least, uint32_t most, int32_t* out,
+                                        uint32_t* bits, BestShared<THREADS>& S) {
     const int tid = threadIdx.x;
-    Limit limit = {0, 0};
-    uint32_t last = ~0u;   // of the equal keys, those with ~id above this
+    uint32_t limit = 0;     // keys above it are taken
     if (R.need > 0) {
-        limit = need_th<THREADS>([&](int i) { return key[i]; }, total, R.need, least, most, S);
-        if (limit.equals > 0) {
+        Limit l = CALLED ? need_th_called<THREADS>(key, total, R.need, least, most, S)
+                         : need_th<THREADS>(key, total, R.need, least, most, S);
+        limit = l.key;
+        if (l.equals > 0) {
+            // Of the equal ones the lowest ids: on with keys that fall with the id,
+            // the larger ones above all of them and the smaller ones 0.
             __syncthreads();
-            // ~id: the lowest ids largest; the others' 1 is below every ~id.
-            last = need_th<THREADS>(
-                       [&](int i) { return key[i] == limit.key ? ~(uint32_t)id[i] : 1u; }, total,
-                       limit.equals, 1u, ~0u, S)
-                       .key;
+#pragma unroll 1
+            for (int i = tid; i < total; i += THREADS) {
+                const uint32_t k = key[i];
+                key[i] = k > limit ? ~0u : k == limit ? ~1u - (uint32_t)id[i] : 0u;
+            }
+            __syncthreads();
+            limit = need_th_called<THREADS>(key, total, l.equals, 1u, ~1u, S).key;
         }
     }
     int done = 0;    // ids written
@@ -933,10 +978,9 @@ __device__ void best_of(const RowRange& R, const uint32_t* key, const int* id, i
         for (int b = tid; b < R.lo; b += THREADS) mark(b);
         for (int b = R.hi + tid; b < R.n_vis; b += THREADS) mark(b);
         if (R.need > 0)
-            for (int i = tid; i < total; i += THREADS) {
-                const uint32_t k = key[i];
-                if (k > limit.key || (k == limit.key && ~(uint32_t)id[i] > last)) mark(id[i]);
-            }
+#pragma unroll 1
+            for (int i = tid; i < total; i += THREADS)
+                if (key[i] > limit) mark(id[i]);
         __syncthreads();
         // Thread t writes the ids of its stretch of words.
         const int per = (quads + THREADS - 1) / THREADS;
@@ -1032,7 +1076,10 @@ __device__ __forceinline__ bool write_plain(const PickParams& P, const RowRange&
 
 // One CTA a row, from all its scores: all of them as candidates if they fit;
 // else, with the maxima of each 8 (of more together if they are many), the
-// scores that reach the need-th best maximum.
+// scores that reach the need-th best maximum.  For one row this kernel runs once
+// on one SM, where fetching its instructions takes longer than executing them:
+// its loops stay loops (256 threads with the maxima unrolled into registers took
+// 20 us where these take TBD).
 struct ScorePick {
     PickParams K;
     const float* scores;
@@ -1059,20 +1106,18 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
     if (write_plain(P.K, R, row, out)) return;
     const float* s = P.scores + row * P.stride;
     const int n = R.hi - R.lo;
-    uint32_t least, most;
+    int total = -1;          // candidates
+    uint32_t least = 1, most = 1;
     if (R.need == 0 || n <= P.room) {
-        const int total = R.need ? n : 0;
+        total = R.need ? n : 0;
 #pragma unroll 4
         for (int i = tid; i < total; i += THREADS) {
             key[i] = ordered(s[R.lo + i]);
             id[i] = R.lo + i;
         }
         __syncthreads();
-        range_of<THREADS>([&](int i) { return key[i]; }, total, &least, &most, S);
-        best_of<THREADS>(R, key, id, total, least, most, out, bits, S);
-        return;
-    }
-    if (P.maxima) {
+        range_of<THREADS>(key, total, &least, &most, S);
+    } else if (P.maxima) {
         const int g8 = (R.hi + 7) / 8;
         const int per = (g8 + P.room_groups - 1) / P.room_groups;
         const int n_groups = (g8 + per - 1) / per;
@@ -1082,21 +1127,34 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
             for (int g = tid; g < n_groups; g += THREADS) groups[g] = ordered(m[g]);
         } else {
             for (int g = tid; g < n_groups; g += THREADS) {
-                float most = -INFINITY;
-#pragma unroll 4
-                for (int i = g * per; i < min(g * per + per, g8); ++i) most = fmaxf(most, m[i]);
-                groups[g] = ordered(most);
+                float top = -INFINITY;
+                for (int i = g * per; i < min(g * per + per, g8); ++i) top = fmaxf(top, m[i]);
+                groups[g] = ordered(top);
             }
         }
         if (tid == 0) S.total = S.bad = 0;
         __syncthreads();
         if (n_groups >= R.need) {
+            range_of<THREADS>(groups, n_groups, &least, &most, S);
+            // A quarter of the largest bounds the need-th largest from below as a
+            // rule, and leaves a range of two octaves.  (Over the whole range, in
+            // which most keys are those of tiny numbers, nearly all maxima would be
+            // counted in a few of the parts, one after the other.)
+            const uint32_t cut = ordered(0.25f * from_ordered(most));
+            int reach_cut = 0;
+#pragma unroll 1
+            for (int g = tid; g < n_groups; g += THREADS) reach_cut += groups[g] >= cut;
+            reach_cut = cta_scan<THREADS>(reach_cut, S.sums);
+            if (tid == THREADS - 1) S.count = reach_cut;
+            __syncthreads();
+            if (S.count >= R.need && cut > least && cut <= most) least = cut;
+            __syncthreads();
             // need groups, so need scores, reach the limit.
-            auto key_of = [&](int i) { return groups[i]; };
-            range_of<THREADS>(key_of, n_groups, &least, &most, S);
-            const Limit limit = need_th<THREADS>(key_of, n_groups, R.need, least, most, S);
+            const Limit limit =
+                need_th_called<THREADS>(groups, n_groups, R.need, least, most, S);
             const uint32_t bound = limit.equals ? limit.key : limit.key + 1;
             // The groups that reach it, then their scores that do.
+#pragma unroll 1
             for (int g = tid; g < n_groups; g += THREADS)
                 if (groups[g] >= bound) {
                     const int at = atomicAdd(&S.bad, 1);
@@ -1105,6 +1163,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
             __syncthreads();
             const int n_reach = S.bad, each = per * 8;
             if (n_reach <= P.room_reach) {
+#pragma unroll 1
                 for (int i = tid; i < n_reach * each; i += THREADS) {
                     const int b = reach[i / each] * each + i % each;
                     if (b < R.lo || b >= R.hi) continue;
@@ -1118,16 +1177,14 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
                     }
                 }
                 __syncthreads();
-                const int total = S.total;
-                if (total >= R.need && total <= P.room) {
-                    // (no maximum is above `most`, so no score is)
-                    best_of<THREADS>(R, key, id, total, bound, most, out, bits, S);
-                    return;
-                }
+                total = S.total;
+                if (total < R.need || total > P.room) total = -1;
+                least = bound;   // (no maximum is above `most`, so no score is)
             }
         }
     }
-    scan_best<THREADS>(R, [&](int b) { return s[b]; }, out, S);
+    if (total >= 0) best_of<THREADS, true>(R, key, id, total, least, most, out, bits, S);
+    else scan_best<THREADS>(R, [&](int b) { return s[b]; }, out, S);
 }
 
 // ------------------------------------------------------------ the bound
@@ -1234,9 +1291,9 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
             __syncwarp();
             lo += (uint32_t)pick_bin(hist, lane, &left) << shift;
             if (shift == 0) break;
-            width = (1u << shift) - 1;
+            width = min((1u << shift) - 1, most - lo);
         }
-        bound = __uint_as_float(lo & 0x80000000u ? lo & 0x7fffffffu : ~lo);
+        bound = from_ordered(lo);
     }
     if (lane == 0) P.bound[row] = bound;
 }
@@ -1324,7 +1381,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
         // Every candidate reaches the bound.
         const uint32_t least = R.need ? ordered(P.bound[row]) : 0;
         const uint32_t most = __reduce_max_sync(0xffffffffu, S.most[lane % (BEST_THREADS / 32)]);
-        best_of<BEST_THREADS>(R, key, id, total, least, most, out, s_bits, S);
+        best_of<BEST_THREADS, false>(R, key, id, total, least, most, out, s_bits, S);
         return;
     }
     // Searched block by block; a row of zero codes needs no products.
@@ -1516,14 +1573,13 @@ int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams
                                                                              : GQA_ERR_CUDA;
 }
 
-// room: candidates; groups: maxima.
 template <int THREADS>
 int launch_pick(const PickParams& K, int rows, const float* scores, long long stride,
                 const float* maxima, int n, cudaStream_t stream) {
     ScorePick P = {K, scores, stride, maxima, bits_words(((K.pos0 + rows - 1) >> 2) + 1), 0, 0, 0};
-    int want = 12 * K.max_sel + 1024;
     const int most = PICK_SMEM / 8;
     if (maxima) {
+        const int want = 12 * K.max_sel + 1024;
         P.room_groups = 16384 < (n + 7) / 8 ? 16384 : (n + 7) / 8;
         P.room = want < most - P.room_groups / 2 ? want : most - P.room_groups / 2;
         P.room_reach = 2 * K.max_sel + 256;
@@ -1583,10 +1639,8 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         float* maxima = reinterpret_cast<float*>(w + L.maxima);
         if (n > 0) {
             const FewParams F = {C, V, n, pos0, n_first, n_last, scores, L.stride, maxima};
-            const int tiles = (n + 63) / 64, cap = di->num_sms * 4;
-            const dim3 grid(tiles < cap ? tiles : cap, (rows + FEW_TILE - 1) / FEW_TILE);
-            if (width <= 256) score_few_kernel<1><<<grid, 256, 0, stream>>>(F);
-            else score_few_kernel<4><<<grid, 256, 0, stream>>>(F);
+            if (width <= 256) launch_score_few<1>(F, di, stream);
+            else launch_score_few<4>(F, di, stream);
         }
         rc = launch_pick<1024>(K, rows, scores, L.stride, maxima, n, stream);
         if (rc != GQA_OK) return rc;

@@ -99,6 +99,7 @@ def test_ties_go_to_the_lowest_id(cuda_lib, rows, ctx, kind):
         scale.view(-1)[::3] = 2.0
         q = q.abs()
     check(cuda_lib, q, index, scale, table, page, ctx, 50, 1, 2)
+    check(cuda_lib, q, index, scale, table, page, ctx, 9, 0, 1)   # id 0 among the equal ones
 
 
 @pytest.mark.parametrize("rows,ctx", [(2, 3000), (150, 3000), (50, 12000)])
