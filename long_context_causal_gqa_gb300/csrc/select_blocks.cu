@@ -12,13 +12,22 @@
 // Few rows: every block's scores by dp4a straight from the int8 index.  More
 // rows: the tensor cores (dot_kernel).  With many blocks, writing rows x blocks
 // scores and reading them back would cost several times the products
-// themselves.  So every 8th block's products are taken first, of which only
+// themselves.  So every 2^s-th block's products are taken first, of which only
 // maxima over small groups are kept; the k-th best of those is a lower bound
 // of the row's k-th best score (k blocks reach it), found by bound_kernel.  The
 // products of all blocks are then compared with the bound as they leave the
-// tensor memory, and about 9 k of them stay as candidates.  Either way one CTA
-// a row takes the best of what is left (best_of).  A row whose candidates do
-// not fit (thousands of equal scores) is searched block by block (scan_best).
+// tensor memory, and a little over 2^s k of them stay as candidates.  Either way
+// one CTA a row takes the best of what is left (best_of).  A row whose candidates
+// do not fit (thousands of equal scores) is searched block by block (scan_best).
+//
+// What bounds it: 4096 rows over 32000 blocks of width 256 are 67 GFLOP, 35 us
+// of the tensor cores; the call takes 119 us: query and index codes 11, the
+// sample (every 4th block) 21, its bounds 10, the candidates 55, the best of
+// them 30, overlapping a little.  Of the candidates' 55 the products alone are
+// 44 (loads and products without the epilogue's compares).  One row over 65472
+// blocks reads 17 MB, 2.5 us; it takes 17.7 us, of which 12 are the pick on one
+// SM, a chain of barriers and dependent loads; the call's host side takes 22.
+#include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
 
@@ -40,23 +49,24 @@ __device__ __forceinline__ void let_next_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-constexpr int STRIDE = 4;   // every STRIDE-th block is in the sample
-
 // What dot_kernel does with its products: keep all scores, keep the maxima of
-// groups of the sampled blocks' (columns 0, 1, ... are blocks 0, 8, 16, ...),
-// or keep the candidates.
+// groups of the sampled blocks', or keep the candidates.
 enum Mode { SCORES = 0, MAXIMA = 1, CANDIDATES = 2 };
 
-// Block of a column, and the columns whose block is below hi.
-template <int MODE>
-__host__ __device__ __forceinline__ int col_block(int c) {
-    return MODE == MAXIMA ? c * STRIDE : c;
-}
-template <int MODE>
-__host__ __device__ __forceinline__ int cols_below(int hi) {
-    if (hi <= 0) return 0;
-    return MODE == MAXIMA ? (hi + STRIDE - 1) / STRIDE : hi;
-}
+// The sample: every 2^skip-th block, in eight stretches of `per`.  Eight columns
+// in a row are one block of each stretch, column 8 i + g number g * per + i, so
+// that a group's blocks lie far apart: neighbours score alike, and a group of
+// them would count the best of a good neighbourhood once instead of eight times.
+struct Sample {
+    int skip, per;
+    __host__ __device__ int cols() const { return 8 * per; }
+    // Sampled blocks below hi.
+    __device__ int below(int hi) const { return hi <= 0 ? 0 : (hi + (1 << skip) - 1) >> skip; }
+    __device__ int col_of(int number) const {
+        const int g = number / per;
+        return 8 * (number - g * per) + g;
+    }
+};
 
 // What a row takes: blocks below n_first and from hi on always, `need` of the
 // scored blocks [n_first, hi).
@@ -225,6 +235,7 @@ struct ExpandParams {
     __half* cols;
     float* scale;
     float* sample_scale;   // null: no sample
+    Sample sample;
 };
 
 // The first `code_ctas` CTAs make query codes (8 rows each), the others
@@ -268,7 +279,8 @@ __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const 
         if (part == 0) {
             const float s = E.V.scale[block[i]];
             E.scale[b] = s;
-            if (E.sample_scale && b % STRIDE == 0) E.sample_scale[b / STRIDE] = s;
+            if (E.sample_scale && (b & ((1 << E.sample.skip) - 1)) == 0)
+                E.sample_scale[E.sample.col_of(b >> E.sample.skip)] = s;
         }
     }
 }
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const 
 // issues, the others take the products: each thread one row and a quarter of a
 // tile's columns.  (With two warps a scheduler instead of four, each waiting on
 // its own chain of compares and stores, the products waited for them: 63
-// instead of ~TBD~ us over 4096 x 32000.)
+// instead of 55 us over 4096 x 32000.)
 constexpr int CTA_ROWS = 128;
 constexpr int PAIR_ROWS = 256;
 constexpr int TILE = 256;                    // columns of a tile
@@ -320,19 +332,28 @@ struct DotParams {
     const float* scale;        // per column, allocated to a multiple of TILE
     float* scores;             // SCORES, MAXIMA: [rows, stride]
     long long stride;
+    Sample sample;             // MAXIMA
     int log2_group;            // MAXIMA: columns of a group, 1 to 8
     const float* bound;        // CANDIDATES: per row
-    uint2* list;               // CANDIDATES: (score, block) [rows][segs][PARTS][cap]
-    int* counts;               // CANDIDATES: entries [rows][segs][PARTS], -1: too many
-    int segs, cap;
+    // CANDIDATES: (score, block) [runs][tile_rows][PARTS][cap], and their numbers
+    // [runs][tile_rows][PARTS], -1: too many.  A run is what a pair computes of a
+    // row tile; pair p's of row tile t is number p + t.
+    uint2* list;
+    int* counts;
+    int tile_rows, cap;
     unsigned* err;
+    __host__ __device__ int runs() const { return G + row_tiles; }
+    __device__ long long list_at(int run, int row) const {
+        return ((long long)run * tile_rows + row % PAIR_ROWS) * PARTS;
+    }
 };
 
 template <int MODE>
 __host__ __device__ __forceinline__ int col_tiles(const DotParams& P, int rt) {
+    if (MODE == MAXIMA) return (P.sample.cols() + TILE - 1) / TILE;
     const int last = min(rt * PAIR_ROWS + PAIR_ROWS, P.rows) - 1;
     const int hi = ((P.pos0 + last) >> 2) + 1 - P.n_last;
-    return (cols_below<MODE>(hi) + TILE - 1) / TILE;
+    return hi <= 0 ? 0 : (hi + TILE - 1) / TILE;
 }
 // The pair that computes product x of the row-tile-major order, and the first
 // product of pair p.
@@ -360,15 +381,13 @@ struct Runs {
             ++rt;
         }
     }
-    // seg: this run's number among its row tile's runs.
-    __device__ bool next(const DotParams& P, int pair, int& t, int& jb, int& je, int& seg) {
+    __device__ bool next(const DotParams& P, int& t, int& jb, int& je) {
         if (pos >= end) return false;
         int n = col_tiles<MODE>(P, rt);
         while (n == 0) n = col_tiles<MODE>(P, ++rt);
         t = rt;
         jb = (int)(pos - cum);
         je = (int)min((long long)n, end - cum);
-        seg = pair - pair_of(P, cum);
         pos = cum + je;
         if (je == n) {
             cum += n;
@@ -389,6 +408,70 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// The scores of 32 columns (products d times scales) of one row from column c0
+// on, or the maxima of their groups.  hi, hi0: the end of the blocks scored in
+// this row and in the warp's first.
+template <int MODE>
+__device__ __forceinline__ void keep_scores(const DotParams& P, const uint32_t (&d)[32],
+                                            const float4* scale4, int row, int c0, int hi,
+                                            int hi0, bool valid) {
+    float sc[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = scale4[i];
+        sc[4 * i] = __fmul_rn(__uint_as_float(d[4 * i]), f.x);
+        sc[4 * i + 1] = __fmul_rn(__uint_as_float(d[4 * i + 1]), f.y);
+        sc[4 * i + 2] = __fmul_rn(__uint_as_float(d[4 * i + 2]), f.z);
+        sc[4 * i + 3] = __fmul_rn(__uint_as_float(d[4 * i + 3]), f.w);
+    }
+    float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
+    if (MODE == SCORES) {
+        if (!valid) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
+        return;
+    }
+    // Blocks that are not scored count for nothing.
+    const int i0 = c0 / 8;
+    if (i0 < P.sample.below(P.n_first) || i0 + 7 * P.sample.per + 3 >= P.sample.below(hi0)) {
+        int a = P.sample.below(P.n_first) - i0, b = P.sample.below(hi) - i0;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < a || i >= b) sc[8 * i + g] = -INFINITY;
+            a -= P.sample.per;
+            b -= P.sample.per;
+        }
+    }
+    if (!valid) return;
+    // Maxima drop a NaN; a group of nothing else counts for nothing.
+    if (P.log2_group == 3) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* x = sc + 8 * i;
+            m[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+        }
+        *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
+    } else if (P.log2_group == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
+    } else {
+        float m[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
+        if (P.log2_group == 1) {
+            store8(dst, m);
+            store8(dst + 8, m + 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
+            store8(dst, m);
+        }
+    }
 }
 
 template <int MODE, bool RESIDENT>
@@ -444,7 +527,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
 
     Runs<MODE> runs;
     runs.init(P, pair);
-    int rt, jb, je, seg;
+    int rt, jb, je;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         // Completions of both CTAs' halves land on the even CTA's barriers.
@@ -452,7 +535,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             uint32_t n = 0;     // slots filled
             int run = 0;
             bool ok = true;
-            while (ok && runs.next(P, pair, rt, jb, je, seg)) {
+            while (ok && runs.next(P, rt, jb, je)) {
                 const int row0 = rt * PAIR_ROWS + CTA_ROWS * (int)rank;
                 if (RESIDENT) {
                     ok = mbar_wait(rows_empty, (run & 1) ^ 1, abort_flag, P.err);
@@ -470,8 +553,11 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                         if (leader) mbar_arrive_expect_tx(full(s), 2 * C::SLOT_BYTES);
                         const uint32_t bar = pairs::leader_addr(full(s));
                         const uint32_t dst = s_ring + s * C::SLOT_BYTES;
-                        pairs::tma_load_2d(dst, &tm_cols, bar, c * 64,
-                                           j * TILE + CTA_ROWS * (int)rank);
+                        const int col0 = j * TILE + CTA_ROWS * (int)rank;
+                        if (MODE == MAXIMA)
+                            pairs::tma_load_3d(dst, &tm_cols, bar, c * 64, 0, col0 / 8);
+                        else
+                            pairs::tma_load_2d(dst, &tm_cols, bar, c * 64, col0);
                         if (!RESIDENT)
                             pairs::tma_load_2d(dst + CHUNK_BYTES, &tm_rows, bar, c * 64, row0);
                     }
@@ -492,7 +578,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             uint32_t n = 0, t = 0;
             int run = 0;
             bool ok = true;
-            while (ok && runs.next(P, pair, rt, jb, je, seg)) {
+            while (ok && runs.next(P, rt, jb, je)) {
                 if (RESIDENT) {
                     ok = mbar_wait(rows_full, run & 1, abort_flag, P.err);
                     if (!ok) break;
@@ -535,7 +621,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
         float* const my_dump = s_dump + ((warp - 2) * 32 + lane) * DUMP_WORDS;
         uint32_t t = 0;
         bool ok = true;
-        while (ok && runs.next(P, pair, rt, jb, je, seg)) {
+        while (ok && runs.next(P, rt, jb, je)) {
             const int row0 = rt * PAIR_ROWS + CTA_ROWS * (int)rank + quarter * 32;
             const int row = row0 + lane;
             const bool valid = row < P.rows;
@@ -546,7 +632,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             // lets every score that reaches the bound through (and few others).
             const float below = nextafterf(bound, -INFINITY);
             uint32_t open = bound == bound ? 0xffffffffu : 0u;
-            const long long at = ((long long)row * P.segs + seg) * PARTS + part;
+            const long long at = P.list_at(pair + rt, row) + part;
             uint2* const list = MODE == CANDIDATES ? P.list + at * P.cap : nullptr;
             int n = 0;
             // The columns' scales: four a lane (of the first PART / 4), loaded a tile
@@ -578,11 +664,10 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                         if (lane == 0) pairs::remote_arrive(pairs::leader_addr(tempty(t & 1)));
                     }
                     const float4* sc4 = reinterpret_cast<const float4*>(my_scale + g * 32);
-                    // Columns on the rows' own blocks, behind them, or on the first
-                    // ones, are not scored.
-                    const bool edge =
-                        col_block<MODE>(c0) < P.n_first || col_block<MODE>(c0 + 31) >= hi0;
-                    if (MODE == CANDIDATES) {
+                    if constexpr (MODE == CANDIDATES) {
+                        // Columns on the rows' own blocks, behind them, or on the first
+                        // ones, are not scored.
+                        const bool edge = c0 < P.n_first || c0 + 32 > hi0;
                         uint32_t under = 0;    // signs of score - bound, column i in bit i
 #pragma unroll
                         for (int i = 7; i >= 0; --i) {
@@ -618,58 +703,8 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                             const float v = __fmul_rn(my_dump[i], my_scale[g * 32 + i]);
                             if (v >= bound) list[n++] = make_uint2(__float_as_uint(v), c0 + i);
                         }
-                        continue;
-                    }
-                    float sc[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 f = sc4[i];
-                        sc[4 * i] = __fmul_rn(__uint_as_float(d[4 * i]), f.x);
-                        sc[4 * i + 1] = __fmul_rn(__uint_as_float(d[4 * i + 1]), f.y);
-                        sc[4 * i + 2] = __fmul_rn(__uint_as_float(d[4 * i + 2]), f.z);
-                        sc[4 * i + 3] = __fmul_rn(__uint_as_float(d[4 * i + 3]), f.w);
-                    }
-                    float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
-                    if (MODE == SCORES) {
-                        if (valid) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
-                        }
-                        continue;
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int b = col_block<MODE>(c0 + i);
-                            if (b < P.n_first || b >= hi) sc[i] = -INFINITY;
-                        }
-                    }
-                    // Maxima drop a NaN; a group of nothing else counts for nothing.
-                    if (!valid) continue;
-                    if (P.log2_group == 3) {
-                        float m[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float* x = sc + 8 * i;
-                            m[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]),
-                                         fmaxf(x[6], x[7]));
-                        }
-                        *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
-                    } else if (P.log2_group == 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
                     } else {
-                        float m[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) m[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
-                        if (P.log2_group == 1) {
-                            store8(dst, m);
-                            store8(dst + 8, m + 8);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[2 * i], m[2 * i + 1]);
-                            store8(dst, m);
-                        }
+                        keep_scores<MODE>(P, d, sc4, row, c0, hi, hi0, valid);
                     }
                 }
             }
@@ -1079,7 +1114,7 @@ __device__ __forceinline__ bool write_plain(const PickParams& P, const RowRange&
 // scores that reach the need-th best maximum.  For one row this kernel runs once
 // on one SM, where fetching its instructions takes longer than executing them:
 // its loops stay loops (256 threads with the maxima unrolled into registers took
-// 20 us where these take TBD).
+// 20 us where these take 17.7, with the scores).
 struct ScorePick {
     PickParams K;
     const float* scores;
@@ -1191,7 +1226,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
 struct BoundParams {
     const float* maxima;     // of the sampled blocks' groups [rows, stride]
     long long stride;
-    int log2_group;
+    int groups;              // of a row
     int rows;
     int pos0, max_sel, n_first, n_last;
     float* bound;            // per row
@@ -1247,20 +1282,30 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
         return;
     }
     const float* m = P.maxima + row * P.stride;
-    const int cols = cols_below<MAXIMA>(R.hi);
-    // (at least 1: one maximum is read whether it counts or not)
-    const int n = max((cols + (1 << P.log2_group) - 1) >> P.log2_group, 1);
+    const int n = P.groups;
     // Maxima that are not numbers above -inf count for nothing (key 0).
+    // (-0 below +0 here: a bound of either lets both through.)
     auto key_of = [&](int i) {
         const float v = m[min(i, n - 1)];
-        return i < n && v > -INFINITY ? ordered(v) : 0u;
+        const uint32_t u = __float_as_uint(v);
+        return i < n && v > -INFINITY ? u ^ ((uint32_t)((int)u >> 31) | 0x80000000u) : 0u;
     };
     uint32_t held[BOUND_HELD];
 #pragma unroll
-    for (int i = 0; i < BOUND_HELD; ++i) held[i] = key_of(i * 32 + lane);
+    for (int i = 0; i < BOUND_HELD; ++i) held[i] = 0;
+#pragma unroll
+    for (int c = 0; c < BOUND_HELD; c += 8) {
+        if (c * 32 >= n) break;
+#pragma unroll
+        for (int i = c; i < c + 8; ++i) held[i] = key_of(i * 32 + lane);
+    }
     auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < BOUND_HELD; ++i) f(held[i]);
+        for (int c = 0; c < BOUND_HELD; c += 8) {
+            if (c * 32 >= n) break;
+#pragma unroll
+            for (int i = c; i < c + 8; ++i) f(held[i]);
+        }
         for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) f(key_of(i));
     };
     uint32_t most = 0, least = 0xffffffffu;
@@ -1301,7 +1346,7 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
 // ------------------------------------------------------------ best of the candidates
 constexpr int MAX_ROW_TILES = 256;   // of a launch
 struct RunTable {
-    uint8_t runs[MAX_ROW_TILES];     // of each row tile
+    uint8_t first[MAX_ROW_TILES], runs[MAX_ROW_TILES];   // pairs of each row tile
 };
 
 struct BestParams {
@@ -1315,7 +1360,8 @@ struct BestParams {
 };
 
 constexpr int BEST_THREADS = 128;
-constexpr int MAX_LISTS = PARTS * 80;   // a row tile's runs are at most the pairs
+constexpr int MAX_PAIRS = 80;
+constexpr int MAX_LISTS = PARTS * MAX_PAIRS;   // a row tile's runs are at most the pairs
 
 __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) {
     // The ids' bits [words], candidates' keys and ids [room] each.
@@ -1333,11 +1379,13 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
     if (tid < 32) S.most[tid] = 0;
     __syncthreads();
     if (R.need > 0) {
-        const int runs = P.T.runs[row / PAIR_ROWS];
-        const int lists = PARTS * runs;
-        const long long at = (long long)row * P.D.segs * PARTS;
+        const int rt = row / PAIR_ROWS;
+        const int lists = PARTS * P.T.runs[rt];
+        const long long at = P.D.list_at(P.T.first[rt] + rt, row);
+        const long long run_step = (long long)P.D.tile_rows * PARTS;
+        // List l is run l / PARTS of the row tile, part l % PARTS.
         for (int l = tid; l < lists; l += BEST_THREADS) {
-            const int n = P.D.counts[at + l];
+            const int n = P.D.counts[at + l / PARTS * run_step + l % PARTS];
             const bool bad = n < 0 || n > P.D.cap;
             const int to = bad ? 0 : atomicAdd(&S.total, n);
             if (bad || to + n > P.room) S.bad = 1;
@@ -1345,7 +1393,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
             s_at[l] = to;
         }
         __syncthreads();
-        // A warp per list; the loads of four lists in flight together.
+        // A warp per part; the loads of four lists in flight together.
         uint32_t most = 0;
         if (!S.bad) {
             auto keep = [&](int i, const uint2& e) {
@@ -1354,21 +1402,25 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
                 id[i] = (int)e.y;
                 most = max(most, k);
             };
-            constexpr int WARPS = BEST_THREADS / 32, TOGETHER = 4;
-            for (int l0 = warp; l0 < lists; l0 += WARPS * TOGETHER) {
+            constexpr int TOGETHER = 4;
+            static_assert(BEST_THREADS / 32 == PARTS, "a warp per part");
+            const long long step = run_step * P.D.cap;
+            const uint2* list = P.D.list + (at + warp) * P.D.cap + lane;
+            for (int l0 = warp; l0 < lists; l0 += PARTS * TOGETHER, list += step * TOGETHER) {
                 uint2 e[TOGETHER];
+                int n[TOGETHER];
 #pragma unroll
                 for (int u = 0; u < TOGETHER; ++u) {
-                    const int l = l0 + u * WARPS;
-                    if (l < lists && lane < s_n[l]) e[u] = P.D.list[(at + l) * P.D.cap + lane];
+                    const int l = l0 + u * PARTS;
+                    n[u] = l < lists ? s_n[l] - lane : 0;    // this lane's and those behind
+                    if (n[u] > 0) e[u] = list[u * step];
                 }
 #pragma unroll
                 for (int u = 0; u < TOGETHER; ++u) {
-                    const int l = l0 + u * WARPS;
-                    if (l >= lists) break;
-                    if (lane < s_n[l]) keep(s_at[l] + lane, e[u]);
-                    for (int i = lane + 32; i < s_n[l]; i += 32)
-                        keep(s_at[l] + i, P.D.list[(at + l) * P.D.cap + i]);
+                    if (n[u] <= 0) continue;
+                    const int to = s_at[l0 + u * PARTS] + lane;
+                    keep(to, e[u]);
+                    for (int i = 32; i < n[u]; i += 32) keep(to + i, list[u * step + i]);
                 }
             }
         }
@@ -1416,14 +1468,22 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
-// Calls of up to this many rows take the dp4a path.
+// Calls of up to this many rows take the dp4a path: over 8192 blocks 32 rows take
+// 20 us by it and 30 us by the tensor cores, over 65472 blocks 64 and 68 us; 64
+// rows 27 and 30 us, 109 and 69 us.
 constexpr int FEW_ROWS = 32;
-// Below this many blocks, or this many per block taken, all scores are kept.
-constexpr int SAMPLE_MIN_BLOCKS = 2048;
-constexpr int SAMPLE_MIN_RATIO = 16;
 constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
-constexpr size_t LIST_BYTES = 256ull << 20;    // candidates held at once
+constexpr size_t LIST_BYTES = 1024ull << 20;   // candidates held at once
 constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
+
+// More rows: a sample where the scores are many, or more of a row than its CTA
+// holds, and few of the blocks are taken.  All scores and a sample, in us, 128
+// blocks taken: 4096 x 2048 54 and 54, 1024 x 8192 56 and 42, 4096 x 4096 79 and
+// 62, 4096 x 32000 2890 and 119; 512 taken: 512 x 8192 42 and 47; an 8th of the
+// blocks taken: 4096 x 4096 86 and 94, 8192 204 and 184, 16384 857 and 382.
+constexpr long long SAMPLE_MIN_SCORES = 6 << 20;
+constexpr int SAMPLE_MIN_BLOCKS = 2048;
+constexpr int SAMPLE_MIN_RATIO = 8;            // blocks per block taken
 
 // A launch as a programmatic dependent of the kernel before it on the stream.
 template <typename... Params, typename... Args>
@@ -1442,8 +1502,39 @@ bool launch_next(void (*kernel)(Params...), int grid, int threads, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-bool sampled(int n, int max_sel) {
-    return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel;
+bool sampled(int rows, int n, int max_sel) {
+    return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel &&
+           ((long long)rows * n >= SAMPLE_MIN_SCORES || n > PICK_SMEM / 8);
+}
+
+// The sample's products cost n / 2^skip columns and leave about 2^skip candidates
+// per block taken, so it thins out with n / max_sel: at 32 skips of 0 and 1 take
+// 103 and 136 us (4096 x 8192), at 64 76 and 72 (4096 x 8192), at 128 skips of 1
+// and 2 89 and 91 (4096 x 16384), at 250 141 and 121 (4096 x 32000), at 511 skips
+// of 2 and 3 204 and 197, at 1023 198 and 175 (4096 x 65472).
+constexpr int MAX_SKIP = 3;
+constexpr int SKIP_RATIO[MAX_SKIP + 1] = {SAMPLE_MIN_RATIO, 48, 160, 700};
+// The last stretch of a sample may end this many blocks behind the last one.
+constexpr int SAMPLE_PAD = 8 << MAX_SKIP;
+
+Sample sample_of(int n, int max_sel) {
+    int skip = 0;
+    while (skip < MAX_SKIP && n / SKIP_RATIO[skip + 1] >= max_sel) ++skip;
+    const int sampled = ((n - 1) >> skip) + 1;
+    return {skip, (sampled + 7) / 8};
+}
+// Groups as large as leave four times as many maxima as blocks taken.
+int sample_group(const Sample& S, int max_sel) {
+    int g = 0;
+    while (g < 3 && (S.cols() >> (g + 1)) >= 4 * max_sel) ++g;
+    return g;
+}
+// max_sel << skip of a call on n blocks is at most this.
+int most_expected(int n) {
+    int most = 0;
+    for (int s = 0; s <= MAX_SKIP; ++s)
+        most = std::max(most, std::min((int)kMaxSelect, n / SKIP_RATIO[s]) << s);
+    return most;
 }
 
 // Where a call keeps what in the workspace.  Every area grows with the rows
@@ -1452,21 +1543,27 @@ bool sampled(int n, int max_sel) {
 struct Layout {
     long long stride;         // scores (or sampled columns) of a row
     int chunk;                // most rows of a launch, by the scores
-    size_t codes, scores, maxima, codes16, cols, scale, sample_scale, bound, counts, list;
-    size_t counts_bytes, list_bytes, bytes;
+    size_t codes, scores, maxima, codes16, cols, scale, sample_scale, bound, list;
+    size_t list_bytes, bytes;
 };
 
-size_t list_row_bytes(int segs, int cap) { return (size_t)segs * PARTS * cap * 8; }
-int list_cap(int max_sel, long long tiles_per_pair) {
-    const long long most = tiles_per_pair * PART, want = 8 * max_sel / PARTS + 64;
+// Entries of a list when max_sel << skip candidates of a row are expected: all of
+// them, and half as many again, may be in one run, even over its parts.
+int list_cap(int expected, long long tiles_per_pair) {
+    const long long most = tiles_per_pair * PART, want = 3ll * expected / 2 / PARTS + 64;
     return (int)(most < want ? most : want);
 }
+// Lists of `rows` rows' products over `tiles` column tiles, and their numbers.
+size_t list_bytes(int runs, int tile_rows, int cap) {
+    return (size_t)runs * tile_rows * PARTS * (cap * sizeof(uint2) + sizeof(int));
+}
 
-// n: blocks scored; kept: scores kept of a row (n, or the sample's).
-Layout layout(int rows, int n, int kept, int width, int pairs) {
+// n: blocks scored; kept: columns of which a row's scores or, of 2^log2_group
+// together, maxima are kept.
+Layout layout(int rows, int n, int kept, int log2_group, int width, int pairs) {
     Layout L = {};
     const bool few = rows <= FEW_ROWS;
-    L.stride = round_up(kept > 0 ? kept : 1, TILE);
+    L.stride = round_up(kept > 0 ? kept : 1, TILE) >> log2_group;
     const size_t row_bytes = (size_t)L.stride * 4;
     size_t at = kWorkspaceCounterBytes;
     auto take = [&](size_t bytes) {
@@ -1486,16 +1583,19 @@ Layout layout(int rows, int n, int kept, int width, int pairs) {
         L.maxima = take(scores / 8);
     } else {
         L.codes16 = take((size_t)rows * width * 2);
-        L.cols = take((size_t)n * width * 2);
+        L.cols = take((size_t)(n + SAMPLE_PAD) * width * 2);
         L.scale = take((size_t)round_up(n, TILE) * 4);
-        L.sample_scale = take((size_t)round_up(n, TILE) * 4);
+        L.sample_scale = take((size_t)round_up(n + SAMPLE_PAD, TILE) * 4);
         L.bound = take(rows_up * 4);
-        L.counts_bytes = ((size_t)PAIR_ROWS * pairs + 2 * rows_up) * PARTS * 4;
-        L.counts = take(L.counts_bytes);
-        // One row tile fits with any max_sel.
-        const long long tiles = (round_up(n, TILE) / TILE + pairs - 1) / pairs + 1;
-        const size_t one = PAIR_ROWS * list_row_bytes(pairs, list_cap(kMaxSelect, tiles));
-        L.list_bytes = one > LIST_BYTES ? one : LIST_BYTES;
+        // For any max_sel: all rows together, or as many row tiles as LIST_BYTES hold.
+        auto lists = [&](int row_tiles) {
+            const long long total = (long long)row_tiles * (round_up(n, TILE) / TILE);
+            const int G = (int)std::min<long long>(std::max(total, 1ll), pairs);
+            return list_bytes(G + row_tiles, std::min(rows, PAIR_ROWS),
+                              list_cap(most_expected(n), (total + G - 1) / G));
+        };
+        L.list_bytes = std::min(lists(std::min((int)(rows_up / PAIR_ROWS), MAX_ROW_TILES)),
+                                std::max(LIST_BYTES, lists(1)));
         L.list = take(L.list_bytes);
     }
     L.bytes = at;
@@ -1530,39 +1630,43 @@ int max_pairs(const DeviceInfo* di) {
         return 0;
     }
     if (n > di->num_sms / 2) n = di->num_sms / 2;
-    if (n > MAX_LISTS / PARTS) n = MAX_LISTS / PARTS;
+    if (n > MAX_PAIRS) n = MAX_PAIRS;
     if (di->device < 64) cached[di->device].store(n, std::memory_order_relaxed);
     return n;
 }
 
-// The schedule of a launch's products: pairs and, per row tile, the most runs.
+// The schedule of a launch's products, and each row tile's runs.
 template <int MODE>
 void schedule(DotParams& D, int pairs, RunTable* table = nullptr) {
     D.row_tiles = (D.rows + PAIR_ROWS - 1) / PAIR_ROWS;
     D.total = 0;
     for (int t = 0; t < D.row_tiles; ++t) D.total += col_tiles<MODE>(D, t);
     D.G = (int)(D.total < pairs ? D.total : pairs);
-    D.segs = 1;
+    if (!table) return;
     long long cum = 0;
     for (int t = 0; t < D.row_tiles; ++t) {
         const int n = col_tiles<MODE>(D, t);
-        const int s = n > 0 ? pair_of(D, cum + n - 1) - pair_of(D, cum) + 1 : 0;
-        if (s > D.segs) D.segs = s;
-        if (table) table->runs[t] = (uint8_t)s;
+        table->first[t] = table->runs[t] = 0;
+        if (n > 0) {
+            table->first[t] = (uint8_t)pair_of(D, cum);
+            table->runs[t] = (uint8_t)(pair_of(D, cum + n - 1) - table->first[t] + 1);
+        }
         cum += n;
     }
 }
 
-// cols: [blocks, width]; the columns of MAXIMA are its every STRIDE-th row.
+// cols: [blocks, width].
 template <int MODE>
 int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams& D,
                 cudaStream_t stream) {
     if (D.total == 0) return GQA_OK;
-    const int width = D.chunks * 64, skip = MODE == MAXIMA ? STRIDE : 1;
+    const int width = D.chunks * 64;
     CUtensorMap tr, tc;
-    if (!make_map_2d_f16(&tr, rows16, D.rows, width, width, CTA_ROWS, 64) ||
-        !make_map_2d_f16(&tc, cols, cols_below<MODE>(n), width, (uint64_t)width * skip, CTA_ROWS,
-                         64))
+    const uint64_t step = (uint64_t)width * 2 << D.sample.skip;   // bytes, MAXIMA
+    if (!make_map_2d_f16(&tr, rows16, D.rows, width, width, CTA_ROWS, 64)) return GQA_ERR_CUDA;
+    if (MODE == MAXIMA ? !make_map_3d_f16(&tc, cols, width, 8, D.sample.per, step * D.sample.per,
+                                          step, CTA_ROWS / 8, 8)
+                       : !make_map_2d_f16(&tc, cols, n, width, width, CTA_ROWS, 64))
         return GQA_ERR_CUDA;
     const bool resident = D.chunks <= RES_CHUNKS;
     const int smem = resident ? DotCfg<true>::SMEM : DotCfg<false>::SMEM;
@@ -1602,7 +1706,7 @@ size_t select_blocks_workspace_bytes(int rows, int ctx_len, int width) {
     const int pairs = di ? max_pairs(di) : 0;
     if (pairs < 1) return 0;
     const int n = (ctx_len - 1) / 4 + 1;
-    return layout(rows, n, n, width, pairs).bytes;
+    return layout(rows, n, n, 0, width, pairs).bytes;
 }
 
 int select_blocks_launch(const void* q, const int8_t* index, const float* index_scale,
@@ -1617,11 +1721,13 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     // Blocks below the last row's always-taken ones.
     int n = ((ctx_len - 1) >> 2) + 1 - n_last;
     if (n <= n_first) n = 0;   // nothing to score
-    const bool sample = !few && sampled(n, max_sel);
-    const int kept = sample ? cols_below<MAXIMA>(n) : n;
+    const bool sample = !few && sampled(rows, n, max_sel);
+    const Sample S = sample ? sample_of(n, max_sel) : Sample{};
+    const int log2_group = sample ? sample_group(S, max_sel) : 0;
+    const int kept = sample ? S.cols() : n;
     const int pairs = max_pairs(di);
     if (pairs < 1) return GQA_ERR_CUDA;
-    const Layout L = layout(rows, n, kept, width, pairs);
+    const Layout L = layout(rows, n, kept, log2_group, width, pairs);
     void* ws;
     size_t ws_bytes;
     current_workspace(&ws, &ws_bytes);
@@ -1652,7 +1758,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     float* sample_scale = reinterpret_cast<float*>(w + L.sample_scale);
     C.codes16 = codes16;
     if (n > 0) {
-        const ExpandParams E = {V, n, cols, scale, sample ? sample_scale : nullptr};
+        const ExpandParams E = {V, n, cols, scale, sample ? sample_scale : nullptr, S};
         const int code_ctas = (rows + 7) / 8;
         const int a_cta = 256 / (width / 16) * EXPAND_PASSES;
         const int ctas = code_ctas + (n + a_cta - 1) / a_cta;
@@ -1691,33 +1797,33 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         // Fewer rows a launch if their candidate lists would not fit.
         for (;;) {
             schedule<CANDIDATES>(R, pairs, &table);
-            R.cap = R.G > 0 ? list_cap(max_sel, (R.total + R.G - 1) / R.G) : 32;
-            if (R.rows * list_row_bytes(R.segs, R.cap) <= L.list_bytes &&
-                (size_t)R.rows * R.segs * PARTS * 4 <= L.counts_bytes)
-                break;
+            R.tile_rows = R.rows < PAIR_ROWS ? R.rows : PAIR_ROWS;
+            R.cap = R.G > 0 ? list_cap(max_sel << S.skip, (R.total + R.G - 1) / R.G) : 32;
+            if (list_bytes(R.runs(), R.tile_rows, R.cap) <= L.list_bytes) break;
             if (R.rows <= PAIR_ROWS) return GQA_ERR_WORKSPACE;   // layout() leaves room for these
             step = round_up(R.rows, PAIR_ROWS) - PAIR_ROWS;
             P.rows = R.rows = step;
         }
         P.scale = sample_scale;
-        // Groups as large as leave four times as many maxima as blocks taken.
-        while (P.log2_group < 3 && (kept >> (P.log2_group + 1)) >= 4 * max_sel) ++P.log2_group;
-        P.stride = L.stride >> P.log2_group;
+        P.sample = S;
+        P.log2_group = log2_group;
         schedule<MAXIMA>(P, pairs);
         rc = launch_dots<MAXIMA>(rows16, cols, n, P, stream);
         if (rc != GQA_OK) return rc;
         float* bound = reinterpret_cast<float*>(w + L.bound);
-        const BoundParams B = {scores, P.stride, P.log2_group, P.rows, K.pos0, max_sel, n_first,
+        const BoundParams B = {scores, P.stride, kept >> log2_group, P.rows, K.pos0, max_sel, n_first,
                                n_last, bound};
         if (!launch_next(bound_kernel, (P.rows + 7) / 8, 256, 0, stream, B)) return GQA_ERR_CUDA;
         R.scale = scale;
         R.bound = bound;
         R.list = reinterpret_cast<uint2*>(w + L.list);
-        R.counts = reinterpret_cast<int*>(w + L.counts);
+        R.counts = reinterpret_cast<int*>(
+            R.list + (size_t)R.runs() * R.tile_rows * PARTS * R.cap);
         rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
         BestParams T = {K, R, table, bound, bits_words(((K.pos0 + R.rows - 1) >> 2) + 1),
-                        10 * max_sel + 512, V, codes + (size_t)r0 * width};
+                        3 * (max_sel << S.skip) / 2 + 2 * max_sel + 256, V,
+                        codes + (size_t)r0 * width};
         if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
         if (!launch_next(best_kernel, R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4,
                          stream, T))

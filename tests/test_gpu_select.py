@@ -59,7 +59,6 @@ CASES = [
     (130, 20011, 16, 5, 1, 128, 64, 0, 1),
     (1, 100003, 16, 6, 1, 256, 2000, 0, 1),
     (700, 700, 16, 6, 1, 256, 12, 1, 3),        # from the first position on
-    # Many blocks for what is taken: candidates by the bound of a sample.
     (33, 9001, 16, 6, 1, 256, 64, 0, 1),
     (300, 12007, 32, 8, 2, 128, 20, 2, 3),
     (257, 9002, 16, 8, 4, 256, 9, 0, 2),        # width 1024
@@ -67,6 +66,16 @@ CASES = [
     (130, 9999, 256, 1, 1, 128, 3, 1, 1),
     (60, 40001, 16, 6, 1, 256, 600, 0, 1),
     (2500, 2500 + 7000, 16, 2, 1, 128, 32, 1, 1),
+    # Many scores and many blocks for what is taken: candidates by the bound of a
+    # sample, of every block to every eighth.
+    (2000, 13001, 16, 6, 1, 128, 32, 1, 1),
+    (33, 98405, 16, 6, 1, 256, 64, 0, 1),
+    (257, 98402, 32, 8, 4, 256, 200, 17, 30),   # width 1024
+    (40, 99999, 64, 6, 6, 128, 9, 1, 1),
+    (64, 110001, 16, 1, 1, 128, 2048, 5, 9),
+    (300, 100001, 256, 2, 1, 128, 600, 0, 1),
+    (35, 120001, 8, 4, 1, 128, 1, 0, 1),
+    (47, 100003, 16, 6, 1, 256, 500, 250, 249),
 ]
 
 
@@ -78,7 +87,7 @@ def test_select_matches_the_definition(cuda_lib, case):
     assert cuda_lib.device_error() == 0
 
 
-@pytest.mark.parametrize("rows,ctx", [(1, 4000), (7, 4000), (40, 4000), (200, 4000), (70, 10000)])
+@pytest.mark.parametrize("rows,ctx", [(1, 4000), (7, 4000), (40, 4000), (200, 4000), (70, 10000), (40, 99000)])
 @pytest.mark.parametrize("kind", ["equal", "few", "zero_scale", "zero_query", "two_values"])
 def test_ties_go_to_the_lowest_id(cuda_lib, rows, ctx, kind):
     page = 16
@@ -102,7 +111,7 @@ def test_ties_go_to_the_lowest_id(cuda_lib, rows, ctx, kind):
     check(cuda_lib, q, index, scale, table, page, ctx, 9, 0, 1)   # id 0 among the equal ones
 
 
-@pytest.mark.parametrize("rows,ctx", [(2, 3000), (150, 3000), (50, 12000)])
+@pytest.mark.parametrize("rows,ctx", [(2, 3000), (150, 3000), (50, 12000), (34, 99000)])
 def test_extreme_values(cuda_lib, rows, ctx):
     """Largest codes, huge / tiny / infinite / NaN scales, infinite and NaN queries."""
     page = 16
@@ -124,7 +133,7 @@ def test_extreme_values(cuda_lib, rows, ctx):
     check(cuda_lib, q, index, scale, table, page, ctx, 30, 0, 1)
 
 
-@pytest.mark.parametrize("rows,ctx", [(3, 2002), (200, 2002), (100, 11002)])
+@pytest.mark.parametrize("rows,ctx", [(3, 2002), (200, 2002), (100, 11002), (100, 98502)])
 def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows, ctx):
     """What lies at or behind a row's own block, and in pages nobody names,
     changes nothing (a step's later rows write their blocks' summaries first)."""
@@ -148,11 +157,13 @@ def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows, ctx):
     assert torch.equal(a[0][:1], c[0]) and first_own + 1 >= int(c[0].max()) + 1
 
 
-@pytest.mark.parametrize("kind", ["most_nan", "clustered", "rising"])
-def test_scores_that_defeat_the_sample(cuda_lib, kind):
+@pytest.mark.parametrize("ctx", [12000, 100000])
+@pytest.mark.parametrize("kind", ["most_nan", "clustered", "rising", "walk"])
+def test_scores_that_defeat_the_sample(cuda_lib, kind, ctx):
     """Fewer numbers than are taken, all the best in one stretch, scores that
-    rise with the position: rows whose candidates run out or do not fit."""
-    rows, ctx, page = 64, 12000, 16
+    rise with the position, neighbours that are all but equal: rows whose
+    candidates run out or do not fit."""
+    rows, page = 64, 16
     q, index, scale, table = make(17, rows, ctx, page, 6, 1, 256)
     b = torch.arange(ctx // 4)
     at = table[b * 4 // page].long(), b % (page // 4)
@@ -163,6 +174,11 @@ def test_scores_that_defeat_the_sample(cuda_lib, kind):
         index[at[0], at[1]] = torch.where((b >= 1000) & (b < 1500), 100, 1)[:, None, None].to(
             torch.int8).expand(-1, 1, 256)
         scale[at] = 1 + b.float() * 1e-4
+    elif kind == "walk":
+        g = torch.Generator().manual_seed(5)
+        walk = torch.randn(len(b), 1, 256, generator=g).cumsum(0) * 2
+        index[at] = (walk - walk.mean(0)).clamp(-127, 127).to(torch.int8)
+        scale[at] = 1.0
     else:
         q = q.abs()
         index[:] = 3
