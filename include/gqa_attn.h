@@ -317,7 +317,8 @@ int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream
 
 /* Cache read: the cached tokens the rows stand for, as dense rows (the K / V
  * of gqa_attn_prefill for one sequence).  k_out, v_out [tokens, Hkv, D] fp16 =
- * decode(code) * scale, rounded to nearest fp16. */
+ * decode(code) * scale in 32 bits, rounded to nearest fp16.  Sequences may share
+ * pages. */
 int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
                         const float* vscale, const int32_t* block_tables, int table_stride,
                         int num_pages, int page, const int32_t* row_starts,

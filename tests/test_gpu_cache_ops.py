@@ -301,6 +301,32 @@ def test_cache_read(cuda_lib, case, kind):
             assert torch.equal(out[:rows].cpu().view(torch.uint8), want.view(torch.uint8))
 
 
+def test_sequences_that_share_pages(cuda_lib):
+    """Two sequences with the same table read the same tokens and summarise the
+    same blocks."""
+    dev = torch.device("cuda")
+    c = make_case(5, 2, 24, 40, 16, 1, 128, True, ragged=False)
+    c["tables"][1] = c["tables"][0]
+    c["lens"], c["max_ctx"] = [21, 30], 30
+    tables, lens, _ = device_rows(c)
+    kc, vc = (x.to(dev) for x in c["caches"])
+    k, v = cuda_lib.cache_read(kc, vc, tables, lens, 30, 24)
+    assert torch.equal(k[18 - 9:12], k[12:15]) and torch.equal(v[18 - 9:12], v[12:15])
+    s = torch.tensor([0.5], device=dev)
+    got = []
+    for last in (1, 2):     # the second sequence alone, then both
+        index = torch.zeros(c["pages"], 4, 1, 128, dtype=torch.int8, device=dev)
+        scale = torch.zeros(c["pages"], 4, device=dev)
+        cuda_lib.block_index_e4m3(kc, s, tables[2 - last:].contiguous(), lens[2 - last:].contiguous(),
+                                  30, 12 * last, index, scale)
+        got.append((index, scale))
+    assert cuda_lib.device_error() == 0
+    both, alone = got[1][1].view(-1), got[0][1].view(-1)
+    assert torch.equal(both[alone != 0], alone[alone != 0])
+    # Positions 11, 15, 19 of the first; 19, 23, 27 of the second.
+    assert int((both != 0).sum()) == 5 and int((alone != 0).sum()) == 3
+
+
 INDEXES = [(1, 4, 4, 8, 1, 128, 0, False), (16, 64, 200, 16, 1, 256, 0, False),
            (5, 130, 90, 32, 2, 256, 6, True), (3, 4500, 3000, 64, 2, 128, 3, True),
            (6, 100, 300, 256, 4, 256, 0, True), (2, 40, 60, 16, 7, 128, 0, True),

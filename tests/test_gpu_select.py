@@ -274,3 +274,37 @@ def test_needs_its_workspace(cuda_lib):
     assert st == cuda_lib.GQA_ERR_WORKSPACE
     if keep is not None:
         cuda_lib.register_workspace(keep)
+
+
+def test_workspace_of_a_longer_context_is_no_smaller(cuda_lib):
+    """A workspace sized for the last block of a context serves every call on it."""
+    for rows in (1, 32, 33, 300, 4096):
+        sizes = [cuda_lib.workspace_bytes(cuda_lib.KIND_SELECT_BLOCKS, rows, c)
+                 for c in sorted({rows, rows + 1, 5000, 8191, 8200, 33000, 98300, 98400, 261888,
+                                  3000000}) if c >= rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_captured_call_outlives_a_growing_workspace(cuda_lib):
+    """A later call that needs a larger workspace leaves a captured one its own."""
+    dev = torch.device("cuda")
+    ctx = 20001
+    q, index, scale, table = (x.to(dev) for x in make(4, 400, ctx, 16, 6, 1, 256))
+    want = cuda_lib.select_blocks(q, index, scale, table, ctx, 32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sel, cnt = cuda_lib.select_blocks(q, index, scale, table, ctx, 32)
+    before = cuda_lib.ensure_workspace(1)
+    cuda_lib.ensure_workspace(before.numel() + 1)
+    assert cuda_lib.ensure_workspace(1).data_ptr() != before.data_ptr()
+    # What memory the allocator has to give is taken and filled.
+    rest = [torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=dev) for _ in range(24)]
+    for _ in range(2):
+        other = cuda_lib.select_blocks(q, index, scale, table, ctx, 32)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, other, (sel, cnt)):
+            assert torch.equal(a, b) and torch.equal(a, c)
+    del rest
+    assert cuda_lib.device_error() == 0
