@@ -293,7 +293,8 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
  *                 of the value times the fp32 reciprocal of kscale / vscale
  *                 (device fp32, > 0), +-448 beyond the range, NaN stays NaN.
  * Norm and rotation in 32 bits (cos and sin to 2^-20, of an angle kept to
- * 2^-20 at any position), one rounding at the end.  q_out and the caches must
+ * 2^-20 at any position), one rounding at the end; a head's sum of squares has to
+ * stay within 32 bits' range.  q_out and the caches must
  * not overlap q, k or v. */
 typedef struct {
     const void *q, *k, *v;
@@ -374,7 +375,8 @@ int gqa_block_index(const void* kcache, const int32_t* block_tables, int table_s
  * n_first + n_last <= max_sel <= 2048; Hkv * D <= 1024; num_pages * page <
  * 2^31.  Block-table entries outside the cache read page 0 and flag
  * GQA_DEVERR_BAD_PAGE_ID.  Workspace: gqa_workspace_bytes(
- * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hq, D). */
+ * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hq, D), for any max_sel, and for
+ * any shorter context; about 1.1 GB for 4096 rows of a 261888-token context. */
 int gqa_select_blocks(const void* q, const int8_t* index, const float* index_scale,
                       const int32_t* block_table, int num_pages, int page, int ctx_len,
                       int query_rows, int Hq, int Hkv, int D, int max_sel, int n_first,
