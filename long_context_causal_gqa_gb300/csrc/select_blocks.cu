@@ -1720,7 +1720,9 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     const bool few = rows <= FEW_ROWS;
     // Blocks below the last row's always-taken ones.
     int n = ((ctx_len - 1) >> 2) + 1 - n_last;
-    if (n <= n_first) n = 0;   // nothing to score
+    // Nothing to score: no block is left, every row takes all it sees, or only the
+    // first and last ones.
+    if (n <= n_first || n + n_last <= max_sel || n_first + n_last == max_sel) n = 0;
     const bool sample = !few && sampled(rows, n, max_sel);
     const Sample S = sample ? sample_of(n, max_sel) : Sample{};
     const int log2_group = sample ? sample_group(S, max_sel) : 0;
