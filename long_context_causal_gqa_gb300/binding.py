@@ -645,18 +645,26 @@ def select_blocks(q, index, index_scale, block_table, ctx_len, max_sel, n_first=
         _refuse("block_table must cover ctx_len")
     if sel_idx is None:
         sel_idx = torch.empty((rows, max_sel), dtype=torch.int32, device=idx)
+        xp = sel_idx.data_ptr()
+    else:
+        xp = _want("sel_idx", sel_idx, torch.int32, idx, 2)
+        if sel_idx.shape != (rows, max_sel):
+            _refuse("sel_idx must be [rows, max_sel]")
     if sel_cnt is None:
         sel_cnt = torch.empty((rows,), dtype=torch.int32, device=idx)
-    xp = _want("sel_idx", sel_idx, torch.int32, idx, 2)
-    cp = _want("sel_cnt", sel_cnt, torch.int32, idx, 1)
-    if sel_idx.shape != (rows, max_sel) or sel_cnt.numel() != rows:
-        _refuse("sel_idx must be [rows, max_sel], sel_cnt [rows]")
+        cp = sel_cnt.data_ptr()
+    else:
+        cp = _want("sel_cnt", sel_cnt, torch.int32, idx, 1)
+        if sel_cnt.numel() != rows:
+            _refuse("sel_cnt must be [rows]")
     args = (qp, ip, sp, bt, num_pages, ppb * 4, ctx_len, rows, Hq, Hkv, D, max_sel, n_first,
             n_last, xp, cp)
-    ws = _ws.get(idx)
-    if ws is None or torch._C._cuda_getDevice() != idx or \
-            ws.numel() < lib.gqa_workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D):
+    try:
+        _call(lib.gqa_select_blocks, idx, stream, *args)
+    except GQAError as e:
+        if e.status != GQA_ERR_WORKSPACE:
+            raise
         with torch.cuda.device(idx):
             ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D), idx)
-    _call(lib.gqa_select_blocks, idx, stream, *args)
+        _call(lib.gqa_select_blocks, idx, stream, *args)
     return sel_idx, sel_cnt
