@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
+#include <numeric>
 
 #include "internal.h"
 #include "pair_mma.cuh"
@@ -53,20 +54,25 @@ __device__ __forceinline__ void let_next_launch() {
 // groups of the sampled blocks', or keep the candidates.
 enum Mode { SCORES = 0, MAXIMA = 1, CANDIDATES = 2 };
 
-// The sample: every 2^skip-th block, in eight stretches of `per`.  Eight columns
-// in a row are one block of each stretch, column 8 i + g number g * per + i, so
-// that a group's blocks lie far apart: neighbours score alike, and a group of
-// them would count the best of a good neighbourhood once instead of eight times.
+// The sample: one block of every 2^skip, at a place that varies without a period
+// (every 4th block may be the only good ones, or none of them), in an order that
+// puts neighbours in different groups: neighbours score alike, and a group of them
+// would count the best of a good neighbourhood once instead of eight times.
 struct Sample {
-    int skip, per;
-    __host__ __device__ int cols() const { return 8 * per; }
-    // Sampled blocks below hi.
-    __device__ int below(int hi) const { return hi <= 0 ? 0 : (hi + (1 << skip) - 1) >> skip; }
-    __device__ int col_of(int number) const {
-        const int g = number / per;
-        return 8 * (number - g * per) + g;
+    int skip;
+    int count;       // sampled blocks
+    int cols;        // columns: count up to a multiple of 8
+    uint32_t step;   // between the columns of blocks sampled one after the other,
+                     // without a common divisor with cols
+    // The block sampled as number x < count, of n.
+    __device__ int block(int x, int n) const {
+        return min((x << skip) + (int)__umulhi((uint32_t)x * 0x9e3779b1u, 1u << skip), n - 1);
+    }
+    __device__ int column(int x) const {
+        return (int)((unsigned long long)x * step % (uint32_t)cols);
     }
 };
+constexpr int NO_BLOCK = 0x7fffffff;    // behind every row
 
 // What a row takes: blocks below n_first and from hi on always, `need` of the
 // scored blocks [n_first, hi).
@@ -227,15 +233,19 @@ __device__ __forceinline__ void store_codes(const CodeParams& P, int row, int la
     }
 }
 
-// The index's blocks in order as the tensor cores read them: fp16 codes, the
-// blocks' scales, and the sampled blocks' scales again.
+// The index's blocks in order as the tensor cores read them, fp16 codes and the
+// blocks' scales, and the sampled ones again.
 struct ExpandParams {
     IndexView V;
     int n;
     __half* cols;
     float* scale;
-    float* sample_scale;   // null: no sample
+    // The sample's columns: codes, scales and blocks (null: no sample).
+    __half* sample_cols;
+    float* sample_scale;
+    int* sample_block;
     Sample sample;
+    int n_first;           // blocks below are not scored
 };
 
 // The first `code_ctas` CTAs make query codes (8 rows each), the others
@@ -276,12 +286,19 @@ __global__ void __launch_bounds__(256) prepare_kernel(const CodeParams C, const 
                     u = codes_half4(w[i].w);
         reinterpret_cast<uint4*>(dst)[0] = make_uint4(x.x, x.y, y.x, y.y);
         reinterpret_cast<uint4*>(dst)[1] = make_uint4(z.x, z.y, u.x, u.y);
-        if (part == 0) {
-            const float s = E.V.scale[block[i]];
-            E.scale[b] = s;
-            if (E.sample_scale && (b & ((1 << E.sample.skip) - 1)) == 0)
-                E.sample_scale[E.sample.col_of(b >> E.sample.skip)] = s;
-        }
+        const float s = part == 0 ? E.V.scale[block[i]] : 0.f;
+        if (part == 0) E.scale[b] = s;
+        const Sample& S = E.sample;
+        if (!E.sample_cols || b != S.block(b >> S.skip, E.n)) continue;
+        const int col = S.column(b >> S.skip);
+        dst = E.sample_cols + (long long)col * E.V.width + part * 16;
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(x.x, x.y, y.x, y.y);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(z.x, z.y, u.x, u.y);
+        if (part) continue;
+        E.sample_scale[col] = s;
+        E.sample_block[col] = b < E.n_first ? NO_BLOCK : b;
+        if (b >> S.skip == S.count - 1)      // the columns left over
+            for (int c = S.count; c < S.cols; ++c) E.sample_block[S.column(c)] = NO_BLOCK;
     }
 }
 
@@ -332,8 +349,9 @@ struct DotParams {
     const float* scale;        // per column, allocated to a multiple of TILE
     float* scores;             // SCORES, MAXIMA: [rows, stride]
     long long stride;
-    Sample sample;             // MAXIMA
-    int log2_group;            // MAXIMA: columns of a group, 1 to 8
+    int cols;                  // MAXIMA: columns
+    const int* block;          // MAXIMA: their blocks, allocated like scale
+    int log2_group;            // MAXIMA: columns of a group, 2 to 8
     const float* bound;        // CANDIDATES: per row
     // CANDIDATES: (score, block) [runs][tile_rows][PARTS][cap], and their numbers
     // [runs][tile_rows][PARTS], -1: too many.  A run is what a pair computes of a
@@ -350,7 +368,7 @@ struct DotParams {
 
 template <int MODE>
 __host__ __device__ __forceinline__ int col_tiles(const DotParams& P, int rt) {
-    if (MODE == MAXIMA) return (P.sample.cols() + TILE - 1) / TILE;
+    if (MODE == MAXIMA) return (P.cols + TILE - 1) / TILE;
     const int last = min(rt * PAIR_ROWS + PAIR_ROWS, P.rows) - 1;
     const int hi = ((P.pos0 + last) >> 2) + 1 - P.n_last;
     return hi <= 0 ? 0 : (hi + TILE - 1) / TILE;
@@ -410,14 +428,9 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
-// The scores of 32 columns (products d times scales) of one row from column c0
-// on, or the maxima of their groups.  hi, hi0: the end of the blocks scored in
-// this row and in the warp's first.
-template <int MODE>
-__device__ __forceinline__ void keep_scores(const DotParams& P, const uint32_t (&d)[32],
-                                            const float4* scale4, int row, int c0, int hi,
-                                            int hi0, bool valid) {
-    float sc[32];
+// The scores of 32 columns: products d times scales.
+__device__ __forceinline__ void scores_of(const uint32_t (&d)[32], const float4* scale4,
+                                          float (&sc)[32]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float4 f = scale4[i];
@@ -426,29 +439,23 @@ __device__ __forceinline__ void keep_scores(const DotParams& P, const uint32_t (
         sc[4 * i + 2] = __fmul_rn(__uint_as_float(d[4 * i + 2]), f.z);
         sc[4 * i + 3] = __fmul_rn(__uint_as_float(d[4 * i + 3]), f.w);
     }
-    float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
-    if (MODE == SCORES) {
-        if (!valid) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
-        return;
-    }
+}
+
+// The maxima of groups of 2^log2_group of 32 columns' scores, for the blocks below hi.
+__device__ __forceinline__ void store_maxima(float (&sc)[32], const int4* block4, int hi,
+                                             int log2_group, float* dst, bool valid) {
     // Blocks that are not scored count for nothing.
-    const int i0 = c0 / 8;
-    if (i0 < P.sample.below(P.n_first) || i0 + 7 * P.sample.per + 3 >= P.sample.below(hi0)) {
-        int a = P.sample.below(P.n_first) - i0, b = P.sample.below(hi) - i0;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < a || i >= b) sc[8 * i + g] = -INFINITY;
-            a -= P.sample.per;
-            b -= P.sample.per;
-        }
+    for (int i = 0; i < 8; ++i) {
+        const int4 b = block4[i];
+        if (b.x >= hi) sc[4 * i] = -INFINITY;
+        if (b.y >= hi) sc[4 * i + 1] = -INFINITY;
+        if (b.z >= hi) sc[4 * i + 2] = -INFINITY;
+        if (b.w >= hi) sc[4 * i + 3] = -INFINITY;
     }
     if (!valid) return;
     // Maxima drop a NaN; a group of nothing else counts for nothing.
-    if (P.log2_group == 3) {
+    if (log2_group == 3) {
         float m[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -456,14 +463,11 @@ __device__ __forceinline__ void keep_scores(const DotParams& P, const uint32_t (
             m[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
         }
         *reinterpret_cast<float4*>(dst) = make_float4(m[0], m[1], m[2], m[3]);
-    } else if (P.log2_group == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
     } else {
         float m[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
-        if (P.log2_group == 1) {
+        if (log2_group == 1) {
             store8(dst, m);
             store8(dst + 8, m + 8);
         } else {
@@ -553,11 +557,8 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                         if (leader) mbar_arrive_expect_tx(full(s), 2 * C::SLOT_BYTES);
                         const uint32_t bar = pairs::leader_addr(full(s));
                         const uint32_t dst = s_ring + s * C::SLOT_BYTES;
-                        const int col0 = j * TILE + CTA_ROWS * (int)rank;
-                        if (MODE == MAXIMA)
-                            pairs::tma_load_3d(dst, &tm_cols, bar, c * 64, 0, col0 / 8);
-                        else
-                            pairs::tma_load_2d(dst, &tm_cols, bar, c * 64, col0);
+                        pairs::tma_load_2d(dst, &tm_cols, bar, c * 64,
+                                           j * TILE + CTA_ROWS * (int)rank);
                         if (!RESIDENT)
                             pairs::tma_load_2d(dst + CHUNK_BYTES, &tm_rows, bar, c * 64, row0);
                     }
@@ -619,6 +620,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + part * PART;
         float* const my_scale = s_scale + (warp - 2) * PART;
         float* const my_dump = s_dump + ((warp - 2) * 32 + lane) * DUMP_WORDS;
+        int* const my_block = reinterpret_cast<int*>(s_dump) + (warp - 2) * PART;   // MAXIMA
         uint32_t t = 0;
         bool ok = true;
         while (ok && runs.next(P, rt, jb, je)) {
@@ -635,16 +637,20 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             const long long at = P.list_at(pair + rt, row) + part;
             uint2* const list = MODE == CANDIDATES ? P.list + at * P.cap : nullptr;
             int n = 0;
-            // The columns' scales: four a lane (of the first PART / 4), loaded a tile
-            // ahead, then shared by the warp.
-            const float4* scale4 = reinterpret_cast<const float4*>(P.scale + jb * TILE +
-                                                                   part * PART) +
-                                   lane % (PART / 4);
-            float4 ahead = __ldg(scale4);
+            // The columns' scales: four a lane of the first half, loaded a tile ahead,
+            // then shared by the warp; of the sample the blocks, by the other half.
+            static_assert(PART == 64, "half a warp's float4");
+            const bool half = MODE == MAXIMA && lane >= 16;
+            const void* const cols = half ? static_cast<const void*>(P.block) : P.scale;
+            const uint4* src = static_cast<const uint4*>(cols) + (jb * TILE + part * PART) / 4 +
+                               lane % 16;
+            uint4* const dst4 = reinterpret_cast<uint4*>(half ? my_block : (int*)my_scale) +
+                                lane % 16;
+            uint4 ahead = __ldg(src);
             for (int j = jb; j < je; ++j, ++t) {
                 __syncwarp();
-                if (lane < PART / 4) reinterpret_cast<float4*>(my_scale)[lane] = ahead;
-                if (j + 1 < je) ahead = __ldg(scale4 += TILE / 4);
+                if (lane < 16 || half) *dst4 = ahead;
+                if (j + 1 < je) ahead = __ldg(src += TILE / 4);
                 __syncwarp();
                 ok = mbar_wait(tfull(t & 1), (t >> 1) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
@@ -704,7 +710,16 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                             if (v >= bound) list[n++] = make_uint2(__float_as_uint(v), c0 + i);
                         }
                     } else {
-                        keep_scores<MODE>(P, d, sc4, row, c0, hi, hi0, valid);
+                        float sc[32];
+                        scores_of(d, sc4, sc);
+                        float* dst = P.scores + row * P.stride + (c0 >> P.log2_group);
+                        if constexpr (MODE == MAXIMA) {
+                            store_maxima(sc, reinterpret_cast<const int4*>(my_block + g * 32), hi,
+                                         P.log2_group, dst, valid);
+                        } else if (valid) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) store8(dst + 8 * i, sc + 8 * i);
+                        }
                     }
                 }
             }
@@ -1514,19 +1529,23 @@ bool sampled(int rows, int n, int max_sel) {
 // of 2 and 3 204 and 197, at 1023 198 and 175 (4096 x 65472).
 constexpr int MAX_SKIP = 3;
 constexpr int SKIP_RATIO[MAX_SKIP + 1] = {SAMPLE_MIN_RATIO, 48, 160, 700};
-// The last stretch of a sample may end this many blocks behind the last one.
-constexpr int SAMPLE_PAD = 8 << MAX_SKIP;
+static_assert(SAMPLE_MIN_RATIO >= 8 && 48 >= 8 << 1 && 160 >= 8 << 2 && 700 >= 8 << 3,
+              "eight columns of a sample per block taken");
 
 Sample sample_of(int n, int max_sel) {
     int skip = 0;
     while (skip < MAX_SKIP && n / SKIP_RATIO[skip + 1] >= max_sel) ++skip;
-    const int sampled = ((n - 1) >> skip) + 1;
-    return {skip, (sampled + 7) / 8};
+    Sample S = {skip, ((n - 1) >> skip) + 1, 0, 0};
+    S.cols = round_up(S.count, 8);
+    S.step = (uint32_t)(S.cols * 0.618034);
+    while (std::gcd(S.step, (uint32_t)S.cols) != 1) ++S.step;
+    return S;
 }
-// Groups as large as leave four times as many maxima as blocks taken.
+// Groups as large as leave four times as many maxima as blocks taken (of two at
+// least: a sample has eight columns per block taken).
 int sample_group(const Sample& S, int max_sel) {
-    int g = 0;
-    while (g < 3 && (S.cols() >> (g + 1)) >= 4 * max_sel) ++g;
+    int g = 1;
+    while (g < 3 && (S.cols >> (g + 1)) >= 4 * max_sel) ++g;
     return g;
 }
 // max_sel << skip of a call on n blocks is at most this.
@@ -1543,7 +1562,8 @@ int most_expected(int n) {
 struct Layout {
     long long stride;         // scores (or sampled columns) of a row
     int chunk;                // most rows of a launch, by the scores
-    size_t codes, scores, maxima, codes16, cols, scale, sample_scale, bound, list;
+    size_t codes, scores, maxima, codes16, cols, scale, sample_cols, sample_scale, sample_block,
+        bound, list;
     size_t list_bytes, bytes;
 };
 
@@ -1583,9 +1603,11 @@ Layout layout(int rows, int n, int kept, int log2_group, int width, int pairs) {
         L.maxima = take(scores / 8);
     } else {
         L.codes16 = take((size_t)rows * width * 2);
-        L.cols = take((size_t)(n + SAMPLE_PAD) * width * 2);
+        L.cols = take((size_t)n * width * 2);
         L.scale = take((size_t)round_up(n, TILE) * 4);
-        L.sample_scale = take((size_t)round_up(n + SAMPLE_PAD, TILE) * 4);
+        L.sample_cols = take((size_t)(n + 8) * width * 2);
+        L.sample_scale = take((size_t)round_up(n + 8, TILE) * 4);
+        L.sample_block = take((size_t)round_up(n + 8, TILE) * 4);
         L.bound = take(rows_up * 4);
         // For any max_sel: all rows together, or as many row tiles as LIST_BYTES hold.
         auto lists = [&](int row_tiles) {
@@ -1655,18 +1677,15 @@ void schedule(DotParams& D, int pairs, RunTable* table = nullptr) {
     }
 }
 
-// cols: [blocks, width].
+// cols: [n, width].
 template <int MODE>
 int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams& D,
                 cudaStream_t stream) {
     if (D.total == 0) return GQA_OK;
     const int width = D.chunks * 64;
     CUtensorMap tr, tc;
-    const uint64_t step = (uint64_t)width * 2 << D.sample.skip;   // bytes, MAXIMA
-    if (!make_map_2d_f16(&tr, rows16, D.rows, width, width, CTA_ROWS, 64)) return GQA_ERR_CUDA;
-    if (MODE == MAXIMA ? !make_map_3d_f16(&tc, cols, width, 8, D.sample.per, step * D.sample.per,
-                                          step, CTA_ROWS / 8, 8)
-                       : !make_map_2d_f16(&tc, cols, n, width, width, CTA_ROWS, 64))
+    if (!make_map_2d_f16(&tr, rows16, D.rows, width, width, CTA_ROWS, 64) ||
+        !make_map_2d_f16(&tc, cols, n, width, width, CTA_ROWS, 64))
         return GQA_ERR_CUDA;
     const bool resident = D.chunks <= RES_CHUNKS;
     const int smem = resident ? DotCfg<true>::SMEM : DotCfg<false>::SMEM;
@@ -1726,7 +1745,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     const bool sample = !few && sampled(rows, n, max_sel);
     const Sample S = sample ? sample_of(n, max_sel) : Sample{};
     const int log2_group = sample ? sample_group(S, max_sel) : 0;
-    const int kept = sample ? S.cols() : n;
+    const int kept = sample ? S.cols : n;
     const int pairs = max_pairs(di);
     if (pairs < 1) return GQA_ERR_CUDA;
     const Layout L = layout(rows, n, kept, log2_group, width, pairs);
@@ -1757,10 +1776,13 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     __half* codes16 = reinterpret_cast<__half*>(w + L.codes16);
     __half* cols = reinterpret_cast<__half*>(w + L.cols);
     float* scale = reinterpret_cast<float*>(w + L.scale);
+    __half* sample_cols = reinterpret_cast<__half*>(w + L.sample_cols);
     float* sample_scale = reinterpret_cast<float*>(w + L.sample_scale);
+    int* sample_block = reinterpret_cast<int*>(w + L.sample_block);
     C.codes16 = codes16;
     if (n > 0) {
-        const ExpandParams E = {V, n, cols, scale, sample ? sample_scale : nullptr, S};
+        const ExpandParams E = {V, n, cols, scale, sample ? sample_cols : nullptr, sample_scale,
+                                sample_block, S, n_first};
         const int code_ctas = (rows + 7) / 8;
         const int a_cta = 256 / (width / 16) * EXPAND_PASSES;
         const int ctas = code_ctas + (n + a_cta - 1) / a_cta;
@@ -1807,10 +1829,11 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
             P.rows = R.rows = step;
         }
         P.scale = sample_scale;
-        P.sample = S;
+        P.cols = S.cols;
+        P.block = sample_block;
         P.log2_group = log2_group;
         schedule<MAXIMA>(P, pairs);
-        rc = launch_dots<MAXIMA>(rows16, cols, n, P, stream);
+        rc = launch_dots<MAXIMA>(rows16, sample_cols, S.cols, P, stream);
         if (rc != GQA_OK) return rc;
         float* bound = reinterpret_cast<float*>(w + L.bound);
         const BoundParams B = {scores, P.stride, kept >> log2_group, P.rows, K.pos0, max_sel, n_first,
