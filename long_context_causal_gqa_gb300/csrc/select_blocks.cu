@@ -30,7 +30,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
-#include <numeric>
 
 #include "internal.h"
 #include "pair_mma.cuh"
@@ -62,14 +61,24 @@ struct Sample {
     int skip;
     int count;       // sampled blocks
     int cols;        // columns: count up to a multiple of 8
-    uint32_t step;   // between the columns of blocks sampled one after the other,
-                     // without a common divisor with cols
+    uint32_t mask;   // 2^bits - 1 >= cols - 1
+    int half;        // half the bits
     // The block sampled as number x < count, of n.
     __device__ int block(int x, int n) const {
         return min((x << skip) + (int)__umulhi((uint32_t)x * 0x9e3779b1u, 1u << skip), n - 1);
     }
-    __device__ int column(int x) const {
-        return (int)((unsigned long long)x * step % (uint32_t)cols);
+    // Column of number x < cols: the numbers of the mask's bits mixed by steps that
+    // can each be undone (odd factors, from the golden ratio and the root of two),
+    // again and again until the result is below cols.
+    __host__ __device__ int column(int x) const {
+        uint32_t y = (uint32_t)x;
+        do {
+            y = y * 0x9e3779b1u & mask;
+            y ^= y >> half;
+            y = y * 0x6a09e667u & mask;
+            y ^= y >> half;
+        } while (y >= (uint32_t)cols);
+        return (int)y;
     }
 };
 constexpr int NO_BLOCK = 0x7fffffff;    // behind every row
@@ -694,7 +703,7 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                                  (a == 32 ? 0u : 0xffffffffu << a);
                         }
                         if (!__any_sync(0xffffffffu, m)) continue;
-                        if (n + 32 > P.cap) {
+                        if (n + __popc(m) > P.cap) {
                             open = m = 0;    // no room: the row is searched block by block
                             n = -1;
                         }
@@ -1247,8 +1256,6 @@ struct BoundParams {
     float* bound;            // per row
 };
 
-constexpr int BOUND_HELD = 32;    // maxima a lane keeps in registers
-
 // Of a histogram's 256 bins the largest with at least *left entries in it and
 // above; *left becomes what is left to take from it.  One warp, *left at most
 // all entries.
@@ -1281,47 +1288,85 @@ __device__ __forceinline__ int pick_bin(const int* hist, int lane, int* left) {
     return __shfl_sync(0xffffffffu, bin, who);
 }
 
-// One warp a row: a number that at least `need` group maxima, so at least
-// `need` of the row's scores, reach: the need-th largest maximum to one part
-// in 2^16 of their order's range, from below, by two counts over 256 parts.
-// The smallest finite number if there are too few maxima; none for a row that
-// needs none.
+// A number that at least `need` group maxima, so at least `need` of the row's
+// scores, reach: the need-th largest maximum to one part in 2^15 (neighbours score
+// alike: hundreds more would reach one a percent lower), from below, by counts over
+// 256 parts of the keys' range, then of the part it is in.  The smallest finite
+// number if there are too few maxima; none for a row that needs none.
+//
+// WARPS a row: one, eight rows a CTA, up to 1024 maxima, which its lanes hold; a CTA
+// of eight for more (2000 maxima of 4096 rows: 39 us, 67 with one warp).
+constexpr int BOUND_ONE_WARP = 1024;
+
+template <int WARPS>
 __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
-    __shared__ __align__(16) int s_hist[8][256];
-    const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int T = 32 * WARPS, ROWS = 8 / WARPS;
+    constexpr int HELD = WARPS == 1 ? BOUND_ONE_WARP / 32 : 16;    // keys a lane holds
+    __shared__ __align__(16) int s_hist[ROWS][256];
+    __shared__ uint32_t s_part[3][8];
+    const int row = blockIdx.x * ROWS + threadIdx.x / T, tid = threadIdx.x % T;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto sync = [] {
+        if (WARPS == 1) __syncwarp();
+        else __syncthreads();
+    };
+    // One value from all of the row's threads.
+    auto greatest = [&](uint32_t v, int slot) {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (WARPS == 1) return v;
+        if (lane == 0) s_part[slot][warp] = v;
+        __syncthreads();
+        return __reduce_max_sync(0xffffffffu, s_part[slot][lane % 8]);
+    };
+    auto total = [&](int v, int slot) {
+        v = (int)__reduce_add_sync(0xffffffffu, v);
+        if (WARPS == 1) return v;
+        if (lane == 0) s_part[slot][warp] = (uint32_t)v;
+        __syncthreads();
+        return (int)__reduce_add_sync(0xffffffffu, lane < 8 ? s_part[slot][lane] : 0u);
+    };
     wait_for_previous();
     if (row >= P.rows) return;
     const RowRange R = row_range(P.pos0 + row, P.max_sel, P.n_first, P.n_last);
     if (R.need == 0) {
-        if (lane == 0) P.bound[row] = kNoBound;
+        if (tid == 0) P.bound[row] = kNoBound;
         return;
     }
     const float* m = P.maxima + row * P.stride;
     const int n = P.groups;
-    // Maxima that are not numbers above -inf count for nothing (key 0).
-    // (-0 below +0 here: a bound of either lets both through.)
+    // Maxima that are not numbers above -inf count for nothing (key 0).  (-0 below
+    // +0 here: a bound of either lets both through.)
     auto key_of = [&](int i) {
         const float v = m[min(i, n - 1)];
         const uint32_t u = __float_as_uint(v);
         return i < n && v > -INFINITY ? u ^ ((uint32_t)((int)u >> 31) | 0x80000000u) : 0u;
     };
-    uint32_t held[BOUND_HELD];
+    uint32_t held[HELD];
 #pragma unroll
-    for (int i = 0; i < BOUND_HELD; ++i) held[i] = 0;
+    for (int i = 0; i < HELD; ++i) held[i] = 0;
 #pragma unroll
-    for (int c = 0; c < BOUND_HELD; c += 8) {
-        if (c * 32 >= n) break;
+    for (int c = 0; c < HELD; c += 8) {
+        if (c * T >= n) break;
 #pragma unroll
-        for (int i = c; i < c + 8; ++i) held[i] = key_of(i * 32 + lane);
+        for (int i = c; i < c + 8; ++i) held[i] = key_of(i * T + tid);
     }
     auto each = [&](auto f) {
 #pragma unroll
-        for (int c = 0; c < BOUND_HELD; c += 8) {
-            if (c * 32 >= n) break;
+        for (int c = 0; c < HELD; c += 8) {
+            if (c * T >= n) break;
 #pragma unroll
             for (int i = c; i < c + 8; ++i) f(held[i]);
         }
-        for (int i = BOUND_HELD * 32 + lane; i < n; i += 32) f(key_of(i));
+        if constexpr (WARPS > 1) {
+#pragma unroll 1
+            for (int i0 = HELD * T; i0 < n; i0 += 4 * T) {
+                uint32_t k[4];     // loads in flight together
+#pragma unroll
+                for (int u = 0; u < 4; ++u) k[u] = key_of(i0 + u * T + tid);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) f(k[u]);
+            }
+        }
     };
     uint32_t most = 0, least = 0xffffffffu;
     int some = 0;
@@ -1330,32 +1375,32 @@ __global__ void __launch_bounds__(256) bound_kernel(const BoundParams P) {
         least = min(least, k ? k : 0xffffffffu);
         some += k != 0;
     });
-    most = __reduce_max_sync(0xffffffffu, most);
-    least = __reduce_min_sync(0xffffffffu, least);
-    some = (int)__reduce_add_sync(0xffffffffu, some);
+    most = greatest(most, 0);
+    least = ~greatest(~least, 1);
+    some = total(some, 2);
     float bound = -3.402823466e38f;
     if (some >= R.need) {
-        int* hist = s_hist[threadIdx.x / 32];
+        int* hist = s_hist[ROWS == 1 ? 0 : warp];
         uint32_t lo = least, width = most - least;
         int left = R.need;
 #pragma unroll 1
-        for (int level = 0; level < 2; ++level) {
+        for (;;) {
             const int shift = width >> 8 ? 24 - __clz((int)width) : 0;
-            __syncwarp();
-            reinterpret_cast<int4*>(hist)[lane] = make_int4(0, 0, 0, 0);
-            reinterpret_cast<int4*>(hist)[lane + 32] = make_int4(0, 0, 0, 0);
-            __syncwarp();
+            sync();
+            for (int i = tid; i < 64; i += T)
+                reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+            sync();
             each([&](uint32_t k) {
                 if (k - lo <= width) atomicAdd(&hist[(k - lo) >> shift], 1);
             });
-            __syncwarp();
+            sync();
             lo += (uint32_t)pick_bin(hist, lane, &left) << shift;
-            if (shift == 0) break;
+            if (shift <= 8) break;
             width = min((1u << shift) - 1, most - lo);
         }
         bound = from_ordered(lo);
     }
-    if (lane == 0) P.bound[row] = bound;
+    if (tid == 0) P.bound[row] = bound;
 }
 
 // ------------------------------------------------------------ best of the candidates
@@ -1466,6 +1511,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
             int dot = 0;
             if (!zero) {
                 const uint4* k = reinterpret_cast<const uint4*>(P.V.index + block * P.V.width);
+#pragma unroll 8
                 for (int i = 0; i < P.V.width / 16; ++i) {
                     const uint4 x = q[i], y = k[i];
                     dot = __dp4a((int)x.x, (int)y.x, dot);
@@ -1535,10 +1581,11 @@ static_assert(SAMPLE_MIN_RATIO >= 8 && 48 >= 8 << 1 && 160 >= 8 << 2 && 700 >= 8
 Sample sample_of(int n, int max_sel) {
     int skip = 0;
     while (skip < MAX_SKIP && n / SKIP_RATIO[skip + 1] >= max_sel) ++skip;
-    Sample S = {skip, ((n - 1) >> skip) + 1, 0, 0};
+    Sample S = {skip, ((n - 1) >> skip) + 1, 0, 1, 1};
     S.cols = round_up(S.count, 8);
-    S.step = (uint32_t)(S.cols * 0.618034);
-    while (std::gcd(S.step, (uint32_t)S.cols) != 1) ++S.step;
+    int bits = 1;
+    for (; S.mask < (uint32_t)S.cols - 1; S.mask = 2 * S.mask + 1) ++bits;
+    S.half = bits / 2;
     return S;
 }
 // Groups as large as leave four times as many maxima as blocks taken (of two at
@@ -1567,10 +1614,10 @@ struct Layout {
     size_t list_bytes, bytes;
 };
 
-// Entries of a list when max_sel << skip candidates of a row are expected: all of
-// them, and half as many again, may be in one run, even over its parts.
+// Entries of a list when max_sel << skip candidates of a row are expected: twice as
+// many may be in one run, even over its parts.
 int list_cap(int expected, long long tiles_per_pair) {
-    const long long most = tiles_per_pair * PART, want = 3ll * expected / 2 / PARTS + 64;
+    const long long most = tiles_per_pair * PART, want = 2ll * expected / PARTS + 64;
     return (int)(most < want ? most : want);
 }
 // Lists of `rows` rows' products over `tiles` column tiles, and their numbers.
@@ -1838,7 +1885,10 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         float* bound = reinterpret_cast<float*>(w + L.bound);
         const BoundParams B = {scores, P.stride, kept >> log2_group, P.rows, K.pos0, max_sel, n_first,
                                n_last, bound};
-        if (!launch_next(bound_kernel, (P.rows + 7) / 8, 256, 0, stream, B)) return GQA_ERR_CUDA;
+        if (!(B.groups <= BOUND_ONE_WARP
+                  ? launch_next(bound_kernel<1>, (P.rows + 7) / 8, 256, 0, stream, B)
+                  : launch_next(bound_kernel<8>, P.rows, 256, 0, stream, B)))
+            return GQA_ERR_CUDA;
         R.scale = scale;
         R.bound = bound;
         R.list = reinterpret_cast<uint2*>(w + L.list);
@@ -1847,7 +1897,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
         BestParams T = {K, R, table, bound, bits_words(((K.pos0 + R.rows - 1) >> 2) + 1),
-                        3 * (max_sel << S.skip) / 2 + 2 * max_sel + 256, V,
+                        2 * (max_sel << S.skip) + max_sel + 256, V,
                         codes + (size_t)r0 * width};
         if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
         if (!launch_next(best_kernel, R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4,
