@@ -376,7 +376,7 @@ int gqa_block_index(const void* kcache, const int32_t* block_tables, int table_s
  * 2^31.  Block-table entries outside the cache read page 0 and flag
  * GQA_DEVERR_BAD_PAGE_ID.  Workspace: gqa_workspace_bytes(
  * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hq, D), for any max_sel, and for
- * any shorter context; about 1.1 GB for 4096 rows of a 261888-token context. */
+ * any shorter context; about 1.5 GB for 4096 rows of a 261888-token context. */
 int gqa_select_blocks(const void* q, const int8_t* index, const float* index_scale,
                       const int32_t* block_table, int num_pages, int page, int ctx_len,
                       int query_rows, int Hq, int Hkv, int D, int max_sel, int n_first,

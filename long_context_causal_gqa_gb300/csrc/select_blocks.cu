@@ -12,7 +12,7 @@
 // Few rows: every block's scores by dp4a straight from the int8 index.  More
 // rows: the tensor cores (dot_kernel).  With many blocks, writing rows x blocks
 // scores and reading them back would cost several times the products
-// themselves.  So every 2^s-th block's products are taken first, of which only
+// themselves.  So one block's products of every 2^s are taken first, of which only
 // maxima over small groups are kept; the k-th best of those is a lower bound
 // of the row's k-th best score (k blocks reach it), found by bound_kernel.  The
 // products of all blocks are then compared with the bound as they leave the
@@ -21,8 +21,8 @@
 // do not fit (thousands of equal scores) is searched block by block (scan_best).
 //
 // What bounds it: 4096 rows over 32000 blocks of width 256 are 67 GFLOP, 35 us
-// of the tensor cores; the call takes 119 us: query and index codes 11, the
-// sample (every 4th block) 21, its bounds 10, the candidates 55, the best of
+// of the tensor cores; the call takes 120 us: query and index codes 11, the
+// sample (a block of four) 22, its bounds 11, the candidates 55, the best of
 // them 30, overlapping a little.  Of the candidates' 55 the products alone are
 // 44 (loads and products without the epilogue's compares).  One row over 65472
 // blocks reads 17 MB, 2.5 us; it takes 17.7 us, of which 12 are the pick on one
@@ -1496,7 +1496,8 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
         best_of<BEST_THREADS, false>(R, key, id, total, least, most, out, s_bits, S);
         return;
     }
-    // Searched block by block; a row of zero codes needs no products.
+    // Searched block by block; a row of zero codes, and blocks with a scale of zero
+    // (an index not filled yet), need no products.
     const uint4* q = reinterpret_cast<const uint4*>(P.codes + (long long)row * P.V.width);
     bool any = false;
     for (int i = tid; i < P.V.width / 16; i += BEST_THREADS) {
@@ -1508,8 +1509,9 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
         R,
         [&](int b) {
             const long long block = physical_block(P.V, b);
+            const float scale = P.V.scale[block];
             int dot = 0;
-            if (!zero) {
+            if (!zero && scale != 0.f) {
                 const uint4* k = reinterpret_cast<const uint4*>(P.V.index + block * P.V.width);
 #pragma unroll 8
                 for (int i = 0; i < P.V.width / 16; ++i) {
@@ -1520,7 +1522,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
                     dot = __dp4a((int)x.w, (int)y.w, dot);
                 }
             }
-            return __fmul_rn((float)dot, P.V.scale[block]);
+            return __fmul_rn((float)dot, scale);
         },
         out, S);
 }
@@ -1540,7 +1542,7 @@ constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
 // More rows: a sample where the scores are many, or more of a row than its CTA
 // holds, and few of the blocks are taken.  All scores and a sample, in us, 128
 // blocks taken: 4096 x 2048 54 and 54, 1024 x 8192 56 and 42, 4096 x 4096 79 and
-// 62, 4096 x 32000 2890 and 119; 512 taken: 512 x 8192 42 and 47; an 8th of the
+// 62, 4096 x 32000 2890 and 120; 512 taken: 512 x 8192 42 and 47; an 8th of the
 // blocks taken: 4096 x 4096 86 and 94, 8192 204 and 184, 16384 857 and 382.
 constexpr long long SAMPLE_MIN_SCORES = 6 << 20;
 constexpr int SAMPLE_MIN_BLOCKS = 2048;
