@@ -158,7 +158,7 @@ def test_unfinished_and_unused_blocks_do_not_matter(cuda_lib, rows, ctx):
 
 
 @pytest.mark.parametrize("ctx", [12000, 100000])
-@pytest.mark.parametrize("kind", ["most_nan", "clustered", "rising", "walk"])
+@pytest.mark.parametrize("kind", ["most_nan", "clustered", "rising", "walk", "period"])
 def test_scores_that_defeat_the_sample(cuda_lib, kind, ctx):
     """Fewer numbers than are taken, all the best in one stretch, scores that
     rise with the position, neighbours that are all but equal: rows whose
@@ -174,6 +174,8 @@ def test_scores_that_defeat_the_sample(cuda_lib, kind, ctx):
         index[at[0], at[1]] = torch.where((b >= 1000) & (b < 1500), 100, 1)[:, None, None].to(
             torch.int8).expand(-1, 1, 256)
         scale[at] = 1 + b.float() * 1e-4
+    elif kind == "period":     # three of four blocks beat the fourth
+        scale[at] = torch.where(b % 4 == 0, 0.1, 1.0) * scale[at]
     elif kind == "walk":
         g = torch.Generator().manual_seed(5)
         walk = torch.randn(len(b), 1, 256, generator=g).cumsum(0) * 2
@@ -212,15 +214,22 @@ def test_bad_pages_read_page_zero(cuda_lib, rows):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-@pytest.mark.parametrize("rows,ctx", [(4096, 8192), (1000, 65537), (3, 1000001)])
-def test_large_calls_sampled_rows(cuda_lib, rows, ctx):
+@pytest.mark.parametrize("rows,ctx,Hq,D,max_sel", [
+    (4096, 8192, 6, 256, 128), (1000, 65537, 6, 256, 128), (3, 1000001, 6, 256, 128),
+    (20000, 20003, 1, 128, 700),     # more scores than are held at once
+    (30000, 40001, 1, 128, 1240),    # more maxima
+    (13100, 330001, 1, 128, 512),    # more candidates
+    (70000, 70001, 1, 128, 128),     # more rows than a launch takes
+])
+def test_large_calls_sampled_rows(cuda_lib, rows, ctx, Hq, D, max_sel):
     page = 16
-    q, index, scale, table = make(rows, rows, ctx, page, 6, 1, 256)
-    sel, cnt = run(cuda_lib, q, index, scale, table, ctx, 128, 2, 3)
-    pick = sorted({0, 1, 2, 63, 64, 127, 128, rows // 2, rows - 2, rows - 1} & set(range(rows)))
+    q, index, scale, table = make(rows, rows, ctx, page, Hq, 1, D)
+    sel, cnt = run(cuda_lib, q, index, scale, table, ctx, max_sel, 2, 3)
+    pick = sorted({0, 1, 2, 63, 64, 127, 128, 6143, 6144, 6400, 11263, 11264, 65535, 65536,
+                   rows // 2, rows - 2, rows - 1} & set(range(rows)))
     for r in pick:
         end = ctx - rows + r + 1
-        s, c = ref.select(q[r:r + 1], index, scale, table, page, end, 128, 2, 3)
+        s, c = ref.select(q[r:r + 1], index, scale, table, page, end, max_sel, 2, 3)
         assert np.array_equal(sel[r].cpu().numpy(), s[0]) and int(cnt[r]) == c[0]
     # Every row: ids ascending, distinct and visible.
     d = sel.long()
