@@ -428,8 +428,11 @@ __device__ __forceinline__ float add_half(uint16_t h, float c) {
     asm("add.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(h), "f"(c));
     return d;
 }
-// (a + b) + (c + d) of four fp16 values in 32 bits.
+// (a + b) + (c + d) of four fp16 values in 32 bits; of E4M3 values, whose sums are
+// exact in any order (20 bits from 2^-9 up), one after the other.
+template <bool E4M3>
 __device__ __forceinline__ float sum4(uint16_t a, uint16_t b, uint16_t c, uint16_t d) {
+    if (E4M3) return add_half(d, add_half(c, add_half(b, __half2float(__ushort_as_half(a)))));
     return __fadd_rn(add_half(b, __half2float(__ushort_as_half(a))),
                      add_half(d, __half2float(__ushort_as_half(c))));
 }
@@ -448,8 +451,8 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // in whatever batch a block is summarised.
 //
 // Bound by the keys' bytes: 261888 E4M3 rows of 256 are 84 MB with what is
-// written, 12.4 us at the copy rate, and take 16.7 us (5.0 TB/s; 2, 4 or 8 blocks
-// together 16.9, 16.7 and 18.4 us).
+// written, 12.4 us at the copy rate, and take 16.2 us (5.2 TB/s; 2 or 8 blocks
+// together, 16 rows a warp or other CTAs are no faster).
 constexpr int INDEX_THREADS = 128;
 
 template <bool E4M3, int CHUNKS>
@@ -497,8 +500,8 @@ __global__ void __launch_bounds__(INDEX_THREADS) index_kernel(const IndexParams 
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t x0 = k[b][c][0].pair(j), x1 = k[b][c][1].pair(j),
                                    x2 = k[b][c][2].pair(j), x3 = k[b][c][3].pair(j);
-                    s[c][2 * j] = sum4(x0 & 0xffff, x1 & 0xffff, x2 & 0xffff, x3 & 0xffff);
-                    s[c][2 * j + 1] = sum4(x0 >> 16, x1 >> 16, x2 >> 16, x3 >> 16);
+                    s[c][2 * j] = sum4<E4M3>(x0 & 0xffff, x1 & 0xffff, x2 & 0xffff, x3 & 0xffff);
+                    s[c][2 * j + 1] = sum4<E4M3>(x0 >> 16, x1 >> 16, x2 >> 16, x3 >> 16);
                     largest = max3_abs(s[c][2 * j], s[c][2 * j + 1], largest);
                 }
             // As whole numbers magnitudes keep their order, NaN above all.
