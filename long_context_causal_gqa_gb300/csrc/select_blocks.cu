@@ -1539,15 +1539,6 @@ constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 1024ull << 20;   // candidates held at once
 constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
 
-// More rows: a sample where the scores are many, or more of a row than its CTA
-// holds, and few of the blocks are taken.  All scores and a sample, in us, 128
-// blocks taken: 4096 x 2048 54 and 54, 1024 x 8192 56 and 42, 4096 x 4096 79 and
-// 62, 4096 x 32000 2890 and 120; 512 taken: 512 x 8192 42 and 47; an 8th of the
-// blocks taken: 4096 x 4096 86 and 94, 8192 204 and 184, 16384 857 and 382.
-constexpr long long SAMPLE_MIN_SCORES = 6 << 20;
-constexpr int SAMPLE_MIN_BLOCKS = 2048;
-constexpr int SAMPLE_MIN_RATIO = 8;            // blocks per block taken
-
 // A launch as a programmatic dependent of the kernel before it on the stream.
 template <typename... Params, typename... Args>
 bool launch_next(void (*kernel)(Params...), int grid, int threads, size_t smem,
@@ -1565,9 +1556,20 @@ bool launch_next(void (*kernel)(Params...), int grid, int threads, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+// More rows: a sample where the scores are many and few of the blocks are taken, or
+// a row has more blocks than its CTA holds.  All scores and a sample, in us (rows x
+// blocks : taken): 4096 x 2048 : 8 and : 64 48 and 40, 52 and 46; 4096 x 1024 : 16
+// 37 and 39; 512 x 8192 : 128 39 and 35; 284 x 16384 : 64 58 and 37; 1024 x 8192 :
+// 128 56 and 41; 4096 x 32000 : 128 2890 and 120.  Less than 30 blocks per block
+// taken: 4096 x 2048 : 128 54 and 52, 8000 x 2000 : 128 81 and 105, 512 x 8192 : 512
+// 41 and 43; an 8th of the blocks taken: 4096 x 4096 86 and 94, 8192 204 and 184,
+// 16384 857 and 382.
+constexpr int SAMPLE_MIN_RATIO = 8;            // blocks per block taken
 bool sampled(int rows, int n, int max_sel) {
-    return n >= SAMPLE_MIN_BLOCKS && n / SAMPLE_MIN_RATIO >= max_sel &&
-           ((long long)rows * n >= SAMPLE_MIN_SCORES || n > PICK_SMEM / 8);
+    if (n / SAMPLE_MIN_RATIO < max_sel) return false;
+    if (n > PICK_SMEM / 8) return true;
+    const long long scores = (long long)rows * n;
+    return n / 30 >= max_sel ? n >= 1536 && scores >= 4000000 : n >= 4000 && scores >= 16000000;
 }
 
 // The sample's products cost n / 2^skip columns and leave about 2^skip candidates

@@ -69,6 +69,7 @@ CASES = [
     # Many scores and many blocks for what is taken: candidates by the bound of a
     # sample, of every block to every eighth.
     (2000, 13001, 16, 6, 1, 128, 32, 1, 1),
+    (2700, 6203, 16, 2, 1, 128, 2, 0, 1),       # the fewest blocks, spaced widest
     (33, 98405, 16, 6, 1, 256, 64, 0, 1),
     (257, 98402, 32, 8, 4, 256, 200, 17, 30),   # width 1024
     (40, 99999, 64, 6, 6, 128, 9, 1, 1),
