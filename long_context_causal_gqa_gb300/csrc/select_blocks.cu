@@ -807,11 +807,9 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     }
     __syncthreads();
     while (b0 < P.n) {
-        int dot[PER][NR];
+        int dot[PER][NR] = {};
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dot[i][r] = 0;
             if (r >= nr) break;
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
@@ -826,29 +824,53 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
                 }
             }
         }
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            if (r >= nr) break;
-            const int row = r0 + r;
-            const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;
+        if constexpr (NR == 1) {
+            const int hi = ((P.pos0 + r0) >> 2) + 1 - P.n_last;
 #pragma unroll
             for (int i = 0; i < PER; i += 2) {
                 float most = -INFINITY;
 #pragma unroll
                 for (int j = i; j < i + 2; ++j) {
-                    int d = dot[j][r];
+                    int d = dot[j][0];
                     d += __shfl_xor_sync(0xffffffffu, d, 4);
                     d += __shfl_xor_sync(0xffffffffu, d, 2);
                     d += __shfl_xor_sync(0xffffffffu, d, 1);
                     const int b = b0 + 4 * j + sub;
                     const float v = __fmul_rn((float)d, scale[j]);
-                    if (part == 0 && b < P.n) P.scores[row * P.stride + b] = v;
+                    if (part == 0 && b < P.n) P.scores[r0 * P.stride + b] = v;
                     if (b >= P.n_first && b < hi) most = fmaxf(most, v);
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-                if (lane == 0) P.maxima[row * (P.stride / 8) + b0 / 8 + i / 2] = most;
+                if (lane == 0) P.maxima[r0 * (P.stride / 8) + b0 / 8 + i / 2] = most;
             }
+        } else {
+            // The eight lanes exchange halves of the rows, then quarters and single
+            // rows: lane `part` ends up with row `part`'s sums.
+            static_assert(NR == 8 && PER == 2, "a row a lane, eight blocks");
+            const int row = r0 + part;
+            const int hi = ((P.pos0 + row) >> 2) + 1 - P.n_last;
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+#pragma unroll
+                for (int half = NR / 2; half; half /= 2) {
+                    const bool upper = part & half;
+#pragma unroll
+                    for (int r = 0; r < half; ++r) {
+                        const int other = upper ? dot[j][r] : dot[j][r + half];
+                        dot[j][r] = (upper ? dot[j][r + half] : dot[j][r]) +
+                                    __shfl_xor_sync(0xffffffffu, other, half);
+                    }
+                }
+                const int b = b0 + 4 * j + sub;
+                const float v = __fmul_rn((float)dot[j][0], scale[j]);
+                if (part < nr && b < P.n) P.scores[row * P.stride + b] = v;
+                if (b >= P.n_first && b < hi) most = fmaxf(most, v);
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+            if (sub == 0 && part < nr) P.maxima[row * (P.stride / 8) + b0 / 8] = most;
         }
         b0 += gridDim.x * 8 * (4 * PER);
         if (b0 < P.n) fetch(b0);
@@ -1531,10 +1553,15 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
-// Calls of up to this many rows take the dp4a path: over 8192 blocks 32 rows take
-// 20 us by it and 30 us by the tensor cores, over 65472 blocks 64 and 68 us; 64
-// rows 27 and 30 us, 109 and 69 us.
-constexpr int FEW_ROWS = 32;
+// Calls of few rows take the dp4a path.  In us by it and by the tensor cores (rows x
+// blocks, 64 or 128 taken): width 256, 32 x 8192 17 and 22, 40 x 65472 52 and 59, 64
+// x 65472 73 and 60; width 512, 16 x 16384 30 and 35, 24 x 16384 40 and 35; width
+// 1024, 8 x 16384 28 and 43, 16 x 16384 45 and 43.  (A width above the call's own,
+// as the workspace is sized for, never makes it few where the call is not.)
+bool few_rows(int rows, int width) {
+    return (long long)rows * (width > 256 ? width : 256) <= 10240;
+}
+
 constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 1024ull << 20;   // candidates held at once
 constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
@@ -1633,7 +1660,7 @@ size_t list_bytes(int runs, int tile_rows, int cap) {
 // together, maxima are kept.
 Layout layout(int rows, int n, int kept, int log2_group, int width, int pairs) {
     Layout L = {};
-    const bool few = rows <= FEW_ROWS;
+    const bool few = few_rows(rows, width);
     L.stride = round_up(kept > 0 ? kept : 1, TILE) >> log2_group;
     const size_t row_bytes = (size_t)L.stride * 4;
     size_t at = kWorkspaceCounterBytes;
@@ -1791,7 +1818,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
     const DeviceInfo* di = device_info();
     if (!di) return GQA_ERR_CUDA;
     const int width = Hkv * D;
-    const bool few = rows <= FEW_ROWS;
+    const bool few = few_rows(rows, width);
     // Blocks below the last row's always-taken ones.
     int n = ((ctx_len - 1) >> 2) + 1 - n_last;
     // Nothing to score: no block is left, every row takes all it sees, or only the
