@@ -1893,8 +1893,14 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
             P.scale = scale;
             schedule<SCORES>(P, pairs);
             if (n > 0) rc = launch_dots<SCORES>(rows16, cols, n, P, stream);
+            // More threads a row where rows are few, or so long that one or two fill an
+            // SM (rows x blocks, 256 and 1024 threads: 128 x 16384 36 and 25 us, 300 x
+            // 5000 28 and 26, 474 x 10311 63 and 61; 900 x 8192 50 and 63, 200 x 2048
+            // 22 and 25).
+            const bool wide = n >= 4096 && (P.rows <= 2 * di->num_sms || n >= 10000);
             if (rc == GQA_OK)
-                rc = launch_pick<256>(K, P.rows, scores, L.stride, nullptr, n, stream);
+                rc = wide ? launch_pick<1024>(K, P.rows, scores, L.stride, nullptr, n, stream)
+                          : launch_pick<256>(K, P.rows, scores, L.stride, nullptr, n, stream);
             if (rc != GQA_OK) return rc;
             continue;
         }
