@@ -1554,13 +1554,11 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
 // Calls of few rows take the dp4a path.  In us by it and by the tensor cores (rows x
-// blocks, 64 or 128 taken): width 256, 32 x 8192 17 and 22, 40 x 65472 52 and 59, 64
-// x 65472 73 and 60; width 512, 16 x 16384 30 and 35, 24 x 16384 40 and 35; width
-// 1024, 8 x 16384 28 and 43, 16 x 16384 45 and 43.  (A width above the call's own,
-// as the workspace is sized for, never makes it few where the call is not.)
-bool few_rows(int rows, int width) {
-    return (long long)rows * (width > 256 ? width : 256) <= 10240;
-}
+// blocks, 64 or 128 taken): width 256, 8 x 8192 12 and 16, 32 x 8192 17 and 17, 40 x
+// 16384 24 and 22; width 512, 16 x 16384 30 and 24; width 1024, 8 x 16384 28 and 31,
+// 10 x 16384 41 and 32.  (A width above the call's own, as the workspace is sized
+// for, never makes it few where the call is not.)
+bool few_rows(int rows, int width) { return rows <= (width > 256 ? 8 : 32); }
 
 constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 1024ull << 20;   // candidates held at once

@@ -59,11 +59,13 @@ CASES = [
     (130, 20011, 16, 5, 1, 128, 64, 0, 1),
     (1, 100003, 16, 6, 1, 256, 2000, 0, 1),
     (700, 700, 16, 6, 1, 256, 12, 1, 3),        # from the first position on
-    (40, 9003, 16, 6, 1, 256, 30, 1, 2),        # the most rows of the path for few
-    (41, 9003, 16, 6, 1, 256, 30, 1, 2),
-    (10, 5001, 32, 8, 8, 128, 70, 0, 1),
-    (11, 5001, 32, 8, 8, 128, 70, 0, 1),
+    (32, 9003, 16, 6, 1, 256, 30, 1, 2),        # the most rows of the path for few
+    (33, 9003, 16, 6, 1, 256, 30, 1, 2),
+    (8, 5001, 32, 8, 8, 128, 70, 0, 1),
+    (9, 5001, 32, 8, 8, 128, 70, 0, 1),
     (20, 4999, 16, 4, 4, 128, 25, 2, 2),
+    (70, 66001, 16, 2, 1, 128, 1700, 2, 2),     # a row's pick with all scores, long rows
+    (330, 18005, 64, 2, 1, 128, 900, 0, 3),     # and many
     (33, 9001, 16, 6, 1, 256, 64, 0, 1),
     (300, 12007, 32, 8, 2, 128, 20, 2, 3),
     (257, 9002, 16, 8, 4, 256, 9, 0, 2),        # width 1024
