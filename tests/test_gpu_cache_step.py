@@ -193,3 +193,34 @@ def test_side_stream_and_eager_order(cuda_lib):
         got.append((q, c.k, c.v, c.index, c.index_scale, sel, cnt, out))
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Writes, reads and summaries need no workspace: two sequences on two streams
+    at once, over one cache, give what they give one after the other."""
+    dev = torch.device("cuda")
+    g = torch.Generator().manual_seed(9)
+    qkv = [torch.randn(700, 8, 256, generator=g).half().to(dev) for _ in range(2)]
+    got = []
+    for together in (False, True):
+        c = Cache(1600, 16, 1, 256, True, seed=3)
+        tables = [c.table[:50].contiguous().view(1, -1), c.table[50:].contiguous().view(1, -1)]
+        lens = [torch.tensor([n], dtype=torch.int32, device=dev) for n in (700, 790)]
+        streams = [torch.cuda.Stream(), torch.cuda.Stream() if together else None]
+        streams[1] = streams[1] or streams[0]
+        outs = [[torch.zeros(700, 1, 256, dtype=torch.float16, device=dev) for _ in range(2)]
+                + [torch.zeros(700, 6, 256, dtype=torch.float16, device=dev)] for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for x, t, n, s, o in zip(qkv, tables, lens, streams, outs):
+                where = (t, n, 800)
+                cuda_lib.cache_write_e4m3(x[:, :6], x[:, 6:7], x[:, 7:], c.k, c.v, c.ks, c.vs,
+                                          *where, q_out=o[2], stream=s)
+                cuda_lib.block_index_e4m3(c.k, c.ks, *where, 700, c.index, c.index_scale, stream=s)
+                cuda_lib.cache_read_e4m3(c.k, c.v, c.ks, c.vs, *where, 700, k_out=o[0], v_out=o[1],
+                                         stream=s)
+        torch.cuda.synchronize()
+        assert cuda_lib.device_error() == 0
+        got.append([c.k, c.v, c.index, c.index_scale] + outs[0] + outs[1])
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
