@@ -756,8 +756,9 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
 // ------------------------------------------------------------ few rows
 // Every CTA makes the codes of its rows itself, which costs less than a launch
 // of its own, with its first blocks' codes already on their way.  Eight lanes
-// read one block's codes, 16 bytes each at a time; a warp takes 4 * PER blocks
-// together and keeps the scores and, over each 8 blocks, the largest scored one.
+// read one block's codes, 16 bytes each at a time, 256 codes ahead of the products;
+// a warp takes 4 * PER blocks together and keeps the scores and, over each 8 blocks,
+// the largest scored one.
 constexpr int FEW_TILE = 8;      // most rows of a CTA
 
 struct FewParams {
@@ -774,30 +775,37 @@ struct FewParams {
 template <int CHUNKS, int NR>
 __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     constexpr int PER = CHUNKS == 1 && NR == 1 ? 4 : 2;
-    constexpr int STEPS = CHUNKS * 2;          // 128 codes each
     __shared__ __align__(16) uint2 s_q[NR][CHUNKS * 32];
     let_next_launch();
-    const int width = P.V.width, steps = width / 128;
+    const int width = P.V.width, steps = width / 128, chunks = (width + 255) / 256;
     const int r0 = blockIdx.y * NR;
     const int nr = NR == 1 ? 1 : min(NR, P.C.rows - r0);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / 8, part = lane % 8;
-    uint4 k[PER][STEPS];
-    float scale[PER];
-    // This lane's blocks: b0 + 4 i + sub.
-    auto fetch = [&](int b0) {
+    // This lane's blocks: b0 + 4 i + sub; 256 codes of each at a time.
+    const uint4* src[PER];
+    uint4 ahead[PER][2];
+    float scale_ahead[PER];
+    auto point = [&](int b0) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const long long block = physical_block(P.V, min(b0 + 4 * i + sub, P.n - 1));
-            const uint4* src = reinterpret_cast<const uint4*>(P.V.index + block * width) + part;
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s)
-                if (s < steps) k[i][s] = src[s * 8];
-            scale[i] = P.V.scale[block];
+            src[i] = reinterpret_cast<const uint4*>(P.V.index + block * width) + part;
+            scale_ahead[i] = P.V.scale[block];
         }
     };
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (c * 2 + s < steps) ahead[i][s] = src[i][(c * 2 + s) * 8];
+    };
     int b0 = (blockIdx.x * 8 + warp) * (4 * PER);
-    if (b0 < P.n) fetch(b0);
+    if (b0 < P.n) {
+        point(b0);
+        fetch(0);
+    }
     if (warp < nr) {
         uint2 w[CHUNKS];
         query_codes<CHUNKS>(P.C, r0 + warp, lane, w);
@@ -807,20 +815,40 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
     }
     __syncthreads();
     while (b0 < P.n) {
+        const int b_next = b0 + gridDim.x * 8 * (4 * PER);
         int dot[PER][NR] = {};
+        float scale[PER];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            if (r >= nr) break;
+        for (int i = 0; i < PER; ++i) scale[i] = scale_ahead[i];
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            uint4 k[PER][2];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                if (s >= steps) break;
-                const uint4 x = reinterpret_cast<const uint4*>(s_q[r])[s * 8 + part];
+            for (int i = 0; i < PER; ++i)
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    dot[i][r] = __dp4a((int)k[i][s].x, (int)x.x, dot[i][r]);
-                    dot[i][r] = __dp4a((int)k[i][s].y, (int)x.y, dot[i][r]);
-                    dot[i][r] = __dp4a((int)k[i][s].z, (int)x.z, dot[i][r]);
-                    dot[i][r] = __dp4a((int)k[i][s].w, (int)x.w, dot[i][r]);
+                for (int s = 0; s < 2; ++s) k[i][s] = ahead[i][s];
+            // The next codes are on their way during these products.
+            if (c + 1 < chunks) {
+                fetch(c + 1);
+            } else if (b_next < P.n) {
+                point(b_next);
+                fetch(0);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (r >= nr) break;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (c * 2 + s >= steps) break;
+                    const uint4 x =
+                        reinterpret_cast<const uint4*>(s_q[r])[(c * 2 + s) * 8 + part];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        dot[i][r] = __dp4a((int)k[i][s].x, (int)x.x, dot[i][r]);
+                        dot[i][r] = __dp4a((int)k[i][s].y, (int)x.y, dot[i][r]);
+                        dot[i][r] = __dp4a((int)k[i][s].z, (int)x.z, dot[i][r]);
+                        dot[i][r] = __dp4a((int)k[i][s].w, (int)x.w, dot[i][r]);
+                    }
                 }
             }
         }
@@ -872,8 +900,7 @@ __global__ void __launch_bounds__(256) score_few_kernel(const FewParams P) {
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
             if (sub == 0 && part < nr) P.maxima[row * (P.stride / 8) + b0 / 8] = most;
         }
-        b0 += gridDim.x * 8 * (4 * PER);
-        if (b0 < P.n) fetch(b0);
+        b0 = b_next;
     }
 }
 
@@ -1555,8 +1582,8 @@ int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
 // Calls of few rows take the dp4a path.  In us by it and by the tensor cores (rows x
 // blocks, 64 or 128 taken): width 256, 8 x 8192 12 and 16, 32 x 8192 17 and 17, 40 x
-// 16384 24 and 22; width 512, 16 x 16384 30 and 24; width 1024, 8 x 16384 28 and 31,
-// 10 x 16384 41 and 32.  (A width above the call's own, as the workspace is sized
+// 16384 24 and 22; width 512, 32 x 16384 36 and 25; width 1024, 8 x 16384 23 and 31,
+// 16 x 16384 35 and 31.  (A width above the call's own, as the workspace is sized
 // for, never makes it few where the call is not.)
 bool few_rows(int rows, int width) { return rows <= (width > 256 ? 8 : 32); }
 
