@@ -13,6 +13,9 @@ namespace select {
 // scored blocks [n_first, hi).
 struct RowRange {
     int n_vis, take, lo, hi, need;
+    // Of a row that does not take all: take again, from what is at hand (take itself,
+    // kept in a register for the stores' sake, cost best_kernel a stack frame).
+    __device__ __forceinline__ int room() const { return lo + need + n_vis - hi; }
 };
 __device__ __forceinline__ RowRange row_range(int pos, int max_sel, int n_first, int n_last) {
     RowRange r;
@@ -94,7 +97,8 @@ __device__ void range_of(const uint32_t* key, int total, uint32_t* least, uint32
 // [least, most] (0: not to be counted; none is above most): those above the
 // limit are taken, and `equals` of those equal to it.  Counts over BINS equal
 // parts of the keys' range, then of the part that holds the need-th largest,
-// until what is in the part is taken whole.
+// until what is in the part is taken whole.  Where fewer than `need` are in
+// [least, most] all the same (best_of says when), it ends with those.
 struct Limit {
     uint32_t key;
     int equals;
@@ -112,6 +116,10 @@ __device__ __forceinline__ Limit need_th(const uint32_t* key, int total, int nee
         constexpr int PER = BINS / THREADS;
 #pragma unroll
         for (int i = 0; i < PER; ++i) S.hist[tid + i * THREADS] = 0;
+        if (tid == 0) {     // what holds if no bin has the need-th
+            S.digit = 0;
+            S.left = S.count = need;
+        }
         __syncthreads();
 #pragma unroll 1
         for (int i = tid; i < total; i += THREADS) {
@@ -162,6 +170,10 @@ __device__ __noinline__ Limit need_th_called(const uint32_t* key, int total, int
 // R.hi on, and the R.need best of the candidates (key[i] within [least, most],
 // id[i]), i < total, equal keys by the lower id; key[] does not outlast the
 // call.  total >= R.need.  bits: room for one per id of a window, in whole uint4.
+//
+// Keys and limits come from a workspace that a call whose wait ran into its limit
+// (an error is flagged), or another call at the same time, leaves in any state.
+// Then the ids are not the best, but only the row's own R.take places are written.
 template <int THREADS, bool CALLED>
 __device__ __forceinline__ void best_of(const RowRange& R, uint32_t* key, const int* id, int total,
                                         uint32_t least, uint32_t most, int32_t* out,
@@ -215,8 +227,8 @@ __device__ __forceinline__ void best_of(const RowRange& R, uint32_t* key, const 
         int at = done + upto - n;
         if (n)
             for (int i = 4 * a; i < 4 * b; ++i)
-                for (uint32_t m = bits[i]; m; m &= m - 1)
-                    out[at++] = w0 + i * 32 + __ffs(m) - 1;
+                for (uint32_t m = bits[i]; m; m &= m - 1, ++at)
+                    if (at < R.room()) out[at] = w0 + i * 32 + __ffs(m) - 1;
         if (w0 + WINDOW >= R.n_vis) break;
         if (tid == THREADS - 1) S.count = upto;
         __syncthreads();
@@ -227,7 +239,8 @@ __device__ __forceinline__ void best_of(const RowRange& R, uint32_t* key, const 
 // The best blocks of one row by its scores, one after the other (score(b) for
 // lo <= b < hi), whatever their number: the key of the last one taken is found
 // eight bits at a time, then one pass over the blocks in order writes those
-// above it and the first of those equal to it.
+// above it and the first of those equal to it, R.take at most (as in best_of,
+// whatever the scores are from pass to pass).
 template <int THREADS, typename Score>
 __device__ void scan_best(const RowRange& R, const Score& score, int32_t* out,
                           BestShared<THREADS>& S) {
@@ -237,6 +250,10 @@ __device__ void scan_best(const RowRange& R, const Score& score, int32_t* out,
     for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
         __syncthreads();
         for (int i = tid; i < 256; i += THREADS) S.hist[i] = 0;
+        if (tid == 0) {     // what holds if no bin has the need-th
+            S.digit = 0;
+            S.left = need;
+        }
         __syncthreads();
         for (int b = R.lo + tid; b < R.hi; b += THREADS) {
             const uint32_t k = ordered(score(b));
@@ -273,7 +290,7 @@ __device__ void scan_best(const RowRange& R, const Score& score, int32_t* out,
         const int e = equals + cta_scan<THREADS>(equal, S.sums);
         const bool take = above || (equal && e <= need);
         const int at = done + cta_scan<THREADS>(take, S.sums);
-        if (take) out[at - 1] = b;
+        if (take && at <= R.room()) out[at - 1] = b;
         if (tid == THREADS - 1) {
             S.left = e;
             S.count = at;
