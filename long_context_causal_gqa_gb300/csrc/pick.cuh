@@ -43,6 +43,40 @@ __host__ __device__ __forceinline__ int bits_words(int ids) {
     return ((ids < WINDOW ? ids : WINDOW) + 127) / 128 * 4;
 }
 
+// A picking CTA's dynamic shared memory, in 32-bit words from its 16-byte aligned
+// start: the ids' bits [words, in whole uint4], the candidates' keys and ids [room]
+// each, the maxima's keys [room_groups], the groups that reach the limit
+// [room_reach].  Launch and kernel take the places and the size from here.
+struct PickAreas {
+    int words, room, room_groups, room_reach;
+    __host__ __device__ __forceinline__ int key() const { return words; }
+    __host__ __device__ __forceinline__ int id() const { return key() + room; }
+    __host__ __device__ __forceinline__ int groups() const { return id() + room; }
+    __host__ __device__ __forceinline__ int reach() const { return groups() + room_groups; }
+    __host__ __device__ __forceinline__ int bytes() const { return 4 * (reach() + room_reach); }
+};
+constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
+constexpr int PICK_MOST_TAKEN = 2048;
+constexpr int PICK_MOST_BYTES = PICK_SMEM + (2 * PICK_MOST_TAKEN + 256) * 4 + WINDOW / 8;
+constexpr int BEST_MOST_BYTES = PICK_SMEM + WINDOW / 8;
+
+// Of a row that sees n_vis blocks at most, n of them scored: from all its scores, or
+// by their maxima.
+inline PickAreas pick_areas(int n_vis, int n, int max_sel, bool maxima) {
+    const int most = PICK_SMEM / 8;
+    if (!maxima) return {bits_words(n_vis), min(n, most), 0, 0};
+    // Fewer maxima of more blocks, as long as they are many per block taken: one row
+    // of 65470 blocks 17.8 us with 8184 maxima, 17.1 with 4092, and with 512 taken
+    // 19.8 and 20.8.
+    const int groups = min(min(max(16 * max_sel, 4096), 16384), (n + 7) / 8);
+    return {bits_words(n_vis), min(12 * max_sel + 1024, most - (groups + 1) / 2), groups,
+            2 * max_sel + 256};
+}
+// By candidates, `expected` of them.
+inline PickAreas best_areas(int n_vis, int expected, int max_sel) {
+    return {bits_words(n_vis), min(2 * expected + max_sel + 256, PICK_SMEM / 8), 0, 0};
+}
+
 template <int THREADS>
 struct BestShared {
     static constexpr int LOG2_BINS = THREADS <= 512 ? 9 : 10;

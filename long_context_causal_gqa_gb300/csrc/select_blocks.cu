@@ -919,20 +919,18 @@ struct ScorePick {
     const float* scores;
     long long stride;
     const float* maxima;     // [rows, stride / 8], null: none
-    int words, room, room_groups, room_reach;   // what a CTA holds, see pick_kernel
+    PickAreas A;
 };
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
-    // The ids' bits [words], candidates' keys and ids [room] each, maxima's keys
-    // [room_groups], the groups that reach the limit [room_reach].
     extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ BestShared<THREADS> S;
     uint32_t* bits = s_key;
-    uint32_t* const key = bits + P.words;
-    int* const id = reinterpret_cast<int*>(key + P.room);
-    uint32_t* groups = key + 2 * P.room;
-    int* const reach = reinterpret_cast<int*>(groups + P.room_groups);
+    uint32_t* const key = bits + P.A.key();
+    int* const id = reinterpret_cast<int*>(bits + P.A.id());
+    uint32_t* groups = bits + P.A.groups();
+    int* const reach = reinterpret_cast<int*>(bits + P.A.reach());
     const int row = blockIdx.x, tid = threadIdx.x;
     const RowRange R = row_range(P.K.pos0 + row, P.K.max_sel, P.K.n_first, P.K.n_last);
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
@@ -942,7 +940,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
     const int n = R.hi - R.lo;
     int total = -1;          // candidates
     uint32_t least = 1, most = 1;
-    if (R.need == 0 || n <= P.room) {
+    if (R.need == 0 || n <= P.A.room) {
         total = R.need ? n : 0;
 #pragma unroll 4
         for (int i = tid; i < total; i += THREADS) {
@@ -953,7 +951,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
         range_of<THREADS>(key, total, &least, &most, S);
     } else if (P.maxima) {
         const int g8 = (R.hi + 7) / 8;
-        const int per = (g8 + P.room_groups - 1) / P.room_groups;
+        const int per = (g8 + P.A.room_groups - 1) / P.A.room_groups;
         const int n_groups = (g8 + per - 1) / per;
         const float* m = P.maxima + row * (P.stride / 8);
         if (per == 1) {
@@ -992,11 +990,11 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
             for (int g = tid; g < n_groups; g += THREADS)
                 if (groups[g] >= bound) {
                     const int at = atomicAdd(&S.bad, 1);
-                    if (at < P.room_reach) reach[at] = g;
+                    if (at < P.A.room_reach) reach[at] = g;
                 }
             __syncthreads();
             const int n_reach = S.bad, each = per * 8;
-            if (n_reach <= P.room_reach) {
+            if (n_reach <= P.A.room_reach) {
 #pragma unroll 1
                 for (int i = tid; i < n_reach * each; i += THREADS) {
                     const int b = reach[i / each] * each + i % each;
@@ -1004,7 +1002,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
                     const uint32_t k = ordered(s[b]);
                     if (k >= bound && k > 1) {   // (1: a NaN)
                         const int to = atomicAdd(&S.total, 1);
-                        if (to < P.room) {
+                        if (to < P.A.room) {
                             key[to] = k;
                             id[to] = b;
                         }
@@ -1012,7 +1010,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const ScorePick P) {
                 }
                 __syncthreads();
                 total = S.total;
-                if (total < R.need || total > P.room) total = -1;
+                if (total < R.need || total > P.A.room) total = -1;
                 least = bound;   // (no maximum is above `most`, so no score is)
             }
         }
@@ -1189,7 +1187,7 @@ struct BestParams {
     DotParams D;             // the products' lists and schedule
     RunTable T;
     const float* bound;
-    int words, room;         // what a CTA holds
+    PickAreas A;
     IndexView V;             // for rows searched block by block
     const int8_t* codes;
 };
@@ -1199,7 +1197,6 @@ constexpr int MAX_PAIRS = 80;
 constexpr int MAX_LISTS = PARTS * MAX_PAIRS;   // a row tile's runs are at most the pairs
 
 __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) {
-    // The ids' bits [words], candidates' keys and ids [room] each.
     extern __shared__ __align__(16) uint32_t s_bits[];
     __shared__ BestShared<BEST_THREADS> S;
     __shared__ int s_n[MAX_LISTS], s_at[MAX_LISTS];
@@ -1208,8 +1205,8 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
     int32_t* out = P.K.sel_idx + (long long)row * P.K.max_sel;
     wait_for_previous();
     if (write_plain(P.K, R, row, out)) return;
-    uint32_t* const key = s_bits + P.words;
-    int* const id = reinterpret_cast<int*>(key + P.room);
+    uint32_t* const key = s_bits + P.A.key();
+    int* const id = reinterpret_cast<int*>(s_bits + P.A.id());
     if (tid == 0) S.total = S.bad = 0;
     if (tid < 32) S.most[tid] = 0;
     __syncthreads();
@@ -1223,7 +1220,7 @@ __global__ void __launch_bounds__(BEST_THREADS) best_kernel(const BestParams P) 
             const int n = P.D.counts[at + l / PARTS * run_step + l % PARTS];
             const bool bad = n < 0 || n > P.D.cap;
             const int to = bad ? 0 : atomicAdd(&S.total, n);
-            if (bad || to + n > P.room) S.bad = 1;
+            if (bad || to + n > P.A.room) S.bad = 1;
             s_n[l] = n;
             s_at[l] = to;
         }
@@ -1315,7 +1312,6 @@ bool few_rows(int rows, int width) { return rows <= (width > 256 ? 8 : 32); }
 
 constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
 constexpr size_t LIST_BYTES = 1024ull << 20;   // candidates held at once
-constexpr int PICK_SMEM = 192 << 10;           // most keys of a CTA, in bytes
 
 // A launch as a programmatic dependent of the kernel before it on the stream.
 template <typename... Params, typename... Args>
@@ -1528,26 +1524,15 @@ int launch_dots(const __half* rows16, const __half* cols, int n, const DotParams
 template <int THREADS>
 int launch_pick(const PickParams& K, int rows, const float* scores, long long stride,
                 const float* maxima, int n, cudaStream_t stream) {
-    ScorePick P = {K, scores, stride, maxima, bits_words(((K.pos0 + rows - 1) >> 2) + 1), 0, 0, 0};
-    const int most = PICK_SMEM / 8;
-    if (maxima) {
-        const int want = 12 * K.max_sel + 1024;
-        // Fewer maxima of more blocks, as long as they are many per block taken: one
-        // row of 65470 blocks 17.8 us with 8184 maxima, 17.1 with 4092, and with 512
-        // taken 19.8 and 20.8.
-        const int groups = std::min(std::max(16 * K.max_sel, 4096), 16384);
-        P.room_groups = std::min(groups, (n + 7) / 8);
-        P.room = want < most - P.room_groups / 2 ? want : most - P.room_groups / 2;
-        P.room_reach = 2 * K.max_sel + 256;
-    } else {
-        P.room = n < most ? n : most;
-    }
-    if (ensure_smem_limit(reinterpret_cast<const void*>(pick_kernel<THREADS>),
-                          PICK_SMEM + (2 * kMaxSelect + 256) * 4 + WINDOW / 8) != GQA_OK)
+    static_assert(PICK_MOST_TAKEN == kMaxSelect, "room for the groups that are reached");
+    const ScorePick P = {K, scores, stride, maxima,
+                         pick_areas(((K.pos0 + rows - 1) >> 2) + 1, n, K.max_sel, maxima)};
+    if (ensure_smem_limit(reinterpret_cast<const void*>(pick_kernel<THREADS>), PICK_MOST_BYTES) !=
+        GQA_OK)
         return GQA_ERR_CUDA;
-    const size_t smem = (size_t)P.room * 8 + (P.words + P.room_groups + P.room_reach) * 4;
-    return launch_next(pick_kernel<THREADS>, rows, THREADS, smem, stream, P) ? GQA_OK
-                                                                             : GQA_ERR_CUDA;
+    return launch_next(pick_kernel<THREADS>, rows, THREADS, P.A.bytes(), stream, P)
+               ? GQA_OK
+               : GQA_ERR_CUDA;
 }
 
 }  // namespace select
@@ -1623,7 +1608,7 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
         else prepare_kernel<4><<<ctas, 256, 0, stream>>>(C, E, code_ctas);
     }
     if (sample && ensure_smem_limit(reinterpret_cast<const void*>(best_kernel),
-                                    PICK_SMEM + WINDOW / 8) != GQA_OK)
+                                    BEST_MOST_BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
     int step = L.chunk;
     for (int r0 = 0; r0 < rows; r0 += step) {
@@ -1688,12 +1673,11 @@ int select_blocks_launch(const void* q, const int8_t* index, const float* index_
             R.list + (size_t)R.runs() * R.tile_rows * PARTS * R.cap);
         rc = launch_dots<CANDIDATES>(rows16, cols, n, R, stream);
         if (rc != GQA_OK) return rc;
-        BestParams T = {K, R, table, bound, bits_words(((K.pos0 + R.rows - 1) >> 2) + 1),
-                        2 * (max_sel << S.skip) + max_sel + 256, V,
-                        codes + (size_t)r0 * width};
-        if (T.room > PICK_SMEM / 8) T.room = PICK_SMEM / 8;
-        if (!launch_next(best_kernel, R.rows, BEST_THREADS, (size_t)T.room * 8 + T.words * 4,
-                         stream, T))
+        const BestParams T = {
+            K, R, table, bound,
+            best_areas(((K.pos0 + R.rows - 1) >> 2) + 1, max_sel << S.skip, max_sel), V,
+            codes + (size_t)r0 * width};
+        if (!launch_next(best_kernel, R.rows, BEST_THREADS, T.A.bytes(), stream, T))
             return GQA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;

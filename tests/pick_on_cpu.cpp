@@ -6,8 +6,11 @@
 // kind 0: best_of over n / 2 keys, then their ids.  kind 1: scan_best over n
 // scores as bits.  kind 2: scan_best, n / 2 scores for the passes that look for the
 // limit, the others for the pass that writes.  room: ids the output has room for;
-// fill: what the shared memory holds before the call.
-// stdout: a line per case: the output's room + n_vis words (-7: not written).
+// fill: what the shared memory holds before the call.  kind 3: no call, but the
+// areas of a CTA for n_vis blocks seen, `total` scored, `take` taken, by maxima if
+// lo, by hi candidates if hi.
+// stdout: a line per case: the output's room + n_vis words (-7: not written), or of
+// the areas the places, the size, the rooms and the most a kernel is launched with.
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -167,6 +170,14 @@ int main() {
             long u;
             if (scanf("%ld", &u) != 1) return 2;
             x = (uint32_t)u;
+        }
+        if (c.kind == 3) {
+            const PickAreas A = c.R.hi ? best_areas(c.R.n_vis, c.R.hi, c.R.take)
+                                       : pick_areas(c.R.n_vis, c.total, c.R.take, c.R.lo);
+            printf("%d %d %d %d %d %d %d %d %d %d\n", A.key(), A.id(), A.groups(), A.reach(),
+                   A.bytes(), A.room, A.room_groups, A.room_reach,
+                   c.R.hi ? BEST_MOST_BYTES : PICK_MOST_BYTES, (int)sizeof(BestShared<1024>));
+            continue;
         }
         c.out.assign(c.room + c.R.n_vis, -7);
         c.bits.resize(bits_words(c.R.n_vis) / 4);

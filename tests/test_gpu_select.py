@@ -325,3 +325,13 @@ def test_captured_call_outlives_a_growing_workspace(cuda_lib):
             assert torch.equal(a, b) and torch.equal(a, c)
     del rest
     assert cuda_lib.device_error() == 0
+
+
+@pytest.mark.parametrize("rows,ctx", [(1, 300000), (3, 300004), (8, 300036)])
+def test_most_blocks_of_a_long_context(cuda_lib, rows, ctx):
+    """The largest max_sel over contexts whose maxima are an odd number or an even
+    one: a row's keys, maxima and bits fill its CTA's shared memory."""
+    page = 32
+    q, index, scale, table = make(ctx, rows, ctx, page, 6, 1, 256)
+    check(cuda_lib, q, index, scale, table, page, ctx, 2048, 1, 1)
+    assert cuda_lib.device_error() == 0

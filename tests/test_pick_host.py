@@ -148,3 +148,28 @@ def test_scores_that_change_stay_in_the_row(pick):
                           *map(bits, a), *map(bits, b)])
     for c, g in zip(cases, pick(cases)):
         assert all(x == UNWRITTEN for x in g[c[2]:]), c[:12]
+
+
+def test_areas_fit_what_is_launched(pick):
+    """The places of a CTA's shared memory follow one another, the ids' bits in whole
+    16-byte words, and end within the bytes of the launch, whatever the call."""
+    rnd = random.Random(7)
+    cases = []
+    for n_vis in (1, 2, 127, 128, 129, 4096, 24576, 24577, 65536, 65537, 250001, 2 ** 29):
+        for take in (1, 2, 33, 128, 1500, 2048):
+            for n in {0, 1, n_vis // 2, n_vis - 1, rnd.randint(0, n_vis)}:
+                cases += [(n_vis, take, n, 0, 0), (n_vis, take, n, 1, 0)]
+            cases += [(n_vis, take, 0, 0, take << s) for s in range(4)]
+    lines = pick([[3, n_vis, take, maxima, expected, 0, 0, n, 0, 0, 0, 0]
+                  for n_vis, take, n, maxima, expected in cases])
+    for (n_vis, take, n, maxima, expected), line in zip(cases, lines):
+        key, ident, groups, reach, size, room, room_groups, room_reach, most, static = line
+        assert key % 4 == 0 and 32 * key >= min(n_vis, 65536)
+        assert min(room, room_groups, room_reach) >= 0
+        assert ident == key + room and groups == ident + room and reach == groups + room_groups
+        assert size == 4 * (reach + room_reach) <= most
+        # Beside the kernels' own shared memory (at most this and two lists of 320).
+        assert most + static + 2 * 320 * 4 <= 232448
+        if maxima:
+            assert room >= take and room_reach >= take
+            assert room_groups == 0 if n == 0 else 0 < room_groups <= (n + 7) // 8
