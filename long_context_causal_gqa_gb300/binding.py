@@ -160,22 +160,42 @@ def workspace_bytes(kind: int, query_rows: int, ctx_or_kv: int, Hq: int = 6, D: 
 
 
 def ensure_workspace(nbytes: int, device=None) -> torch.Tensor:
-    """Make sure the device's registered workspace holds at least nbytes."""
+    """Make sure the device's registered workspace holds at least nbytes.  A
+    workspace that a larger one replaces is kept, for graphs captured with it
+    (see release_outgrown)."""
     dev = torch.device(device if device is not None else "cuda")
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
     cur = _ws.get(idx)
     if cur is None or cur.numel() < nbytes:
         torch.cuda.synchronize(idx)
-        size = max(int(nbytes), 4096)
+        need = size = max(int(nbytes), 4096)
         if cur is not None:
             # Half as much again at least, so that the ones kept stay few.
-            _outgrown.append(cur)
-            size = max(size, cur.numel() * 3 // 2)
-        buf = torch.empty(size, dtype=torch.uint8, device=f"cuda:{idx}")
+            size = max(need, cur.numel() * 3 // 2)
+        try:
+            buf = torch.empty(size, dtype=torch.uint8, device=f"cuda:{idx}")
+        except torch.cuda.OutOfMemoryError:
+            if size == need:
+                raise
+            buf = torch.empty(need, dtype=torch.uint8, device=f"cuda:{idx}")
         _check(load().gqa_set_workspace(idx, _ptr(buf), buf.numel()), "gqa_set_workspace")
+        if cur is not None:
+            _outgrown.append(cur)
         _ws[idx] = buf
         cur = buf
     return cur
+
+
+def release_outgrown(device=None) -> int:
+    """Free the workspaces of a device that larger ones have replaced, and
+    return their bytes.  A graph captured with one of them must not be replayed
+    afterwards: capture it again, or keep them."""
+    dev = torch.device(device if device is not None else "cuda")
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    torch.cuda.synchronize(idx)
+    mine = [b for b in _outgrown if b.device.index == idx]
+    _outgrown[:] = [b for b in _outgrown if b.device.index != idx]
+    return sum(b.numel() for b in mine)
 
 
 def register_workspace(buf: torch.Tensor):
