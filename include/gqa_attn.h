@@ -375,8 +375,9 @@ int gqa_block_index(const void* kcache, const int32_t* block_tables, int table_s
  * n_first + n_last <= max_sel <= 2048; Hkv * D <= 1024; num_pages * page <
  * 2^31.  Block-table entries outside the cache read page 0 and flag
  * GQA_DEVERR_BAD_PAGE_ID.  Workspace: gqa_workspace_bytes(
- * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hq, D), for any max_sel, and for
- * any shorter context; about 1.5 GB for 4096 rows of a 261888-token context. */
+ * GQA_KIND_SELECT_BLOCKS, query_rows, ctx_len, Hkv, D), for any max_sel, and for
+ * any shorter context: about 1.3 GB for 4096 rows of a 261888-token context with one KV
+ * head of 256.  (With Hq in Hkv's place it holds for any Hkv dividing Hq.) */
 int gqa_select_blocks(const void* q, const int8_t* index, const float* index_scale,
                       const int32_t* block_table, int num_pages, int page, int ctx_len,
                       int query_rows, int Hq, int Hkv, int D, int max_sel, int n_first,

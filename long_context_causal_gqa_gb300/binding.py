@@ -685,6 +685,7 @@ def select_blocks(q, index, index_scale, block_table, ctx_len, max_sel, n_first=
         if e.status != GQA_ERR_WORKSPACE:
             raise
         with torch.cuda.device(idx):
-            ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hq, D), idx)
+            # (by the heads its size goes by: those of the index)
+            ensure_workspace(workspace_bytes(KIND_SELECT_BLOCKS, rows, ctx_len, Hkv, D), idx)
         _call(lib.gqa_select_blocks, idx, stream, *args)
     return sel_idx, sel_cnt

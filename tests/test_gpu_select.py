@@ -335,3 +335,31 @@ def test_most_blocks_of_a_long_context(cuda_lib, rows, ctx):
     q, index, scale, table = make(ctx, rows, ctx, page, 6, 1, 256)
     check(cuda_lib, q, index, scale, table, page, ctx, 2048, 1, 1)
     assert cuda_lib.device_error() == 0
+
+
+@pytest.mark.parametrize("rows,ctx,Hq,Hkv,D,max_sel", [
+    (1, 9001, 6, 1, 256, 64), (20, 9001, 8, 1, 128, 64), (32, 70001, 6, 1, 256, 128),
+    (300, 9001, 6, 1, 256, 64), (9, 9001, 8, 4, 128, 512), (257, 70001, 12, 2, 128, 128),
+    (2500, 40001, 6, 1, 256, 128)])
+def test_workspace_goes_by_the_heads_of_the_index(cuda_lib, monkeypatch, rows, ctx, Hq, Hkv, D,
+                                                  max_sel):
+    """The wrapper asks for what the index's own width takes, and that is enough."""
+    q, index, scale, table = make(ctx, rows, ctx, 16, Hq, Hkv, D)
+    want, _ = run(cuda_lib, q, index, scale, table, ctx, max_sel, 1, 2)
+    keep, asked = cuda_lib.ensure_workspace(1), []
+    none = torch.empty(4096, dtype=torch.uint8, device="cuda")
+
+    def ensure(n, device=None):
+        asked.append(n)
+        cuda_lib.register_workspace(torch.empty(n, dtype=torch.uint8, device="cuda"))
+
+    monkeypatch.setattr(cuda_lib, "ensure_workspace", ensure)
+    cuda_lib.register_workspace(none)
+    try:
+        got, _ = run(cuda_lib, q, index, scale, table, ctx, max_sel, 1, 2)
+    finally:
+        cuda_lib.register_workspace(keep)
+    assert asked == [cuda_lib.workspace_bytes(cuda_lib.KIND_SELECT_BLOCKS, rows, ctx, Hkv, D)]
+    assert asked[0] <= cuda_lib.workspace_bytes(cuda_lib.KIND_SELECT_BLOCKS, rows, ctx, Hq, D)
+    assert torch.equal(got, want)
+    assert cuda_lib.device_error() == 0
