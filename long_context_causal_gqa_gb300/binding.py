@@ -5,9 +5,13 @@ current CUDA stream to the C ABI declared in ``include/gqa_attn.h``; all of the
 attention runs in the library's CUDA kernels.  There is no fallback: if the
 library is missing or a call fails, a ``GQAError`` is raised.
 
-Workspace: the prefill and paged-E4M3 entry points keep split partials in a
-workspace registered per device.  ``ensure_workspace`` allocates it with torch
-(outside the C calls) and registers it; the wrappers call it for you.
+Workspace: the prefill, paged-E4M3 and block-selection entry points keep what
+they need in between in a workspace registered per device.  ``ensure_workspace``
+allocates it with torch (outside the C calls) and registers it; the wrappers call
+it for you.  Calls that share it must not overlap on the GPU.
+
+Streams: a call runs on ``stream`` (a torch stream), or on the current one.
+Outputs that a call allocates belong to the stream it runs on.
 """
 
 from __future__ import annotations
@@ -141,6 +145,20 @@ def _ptr(t: torch.Tensor):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory of an output, from the stream that writes it.  (From the current
+    stream's it could still be in use by that stream's earlier work.)  Freed, it is
+    not given out again before what the current stream does with it until then."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _need_cuda(*ts):
     dev = None
     for t in ts:
@@ -238,7 +256,7 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float = 1.
     Q, Hq, D = q.shape
     KV, Hkv, _ = k.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         ensure_workspace(workspace_bytes(KIND_PREFILL, Q, KV, Hq, D), dev)
@@ -257,7 +275,7 @@ def prefill_e4m3(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kscale: torc
     Q, Hq, D = q.shape
     KV, Hkv, _ = k.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         ensure_workspace(workspace_bytes(KIND_PREFILL, Q, KV, Hq, D), dev)
@@ -278,7 +296,7 @@ def paged_e4m3(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
     R, Hq, D = q.shape
     num_pages, page, Hkv, _ = kcache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         ensure_workspace(workspace_bytes(KIND_PAGED_E4M3, R, ctx_len, Hq, D), dev)
@@ -303,7 +321,7 @@ def paged_e4m3_devctx(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tenso
     R, Hq, D = q.shape
     num_pages, page, Hkv, _ = kcache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         ensure_workspace(workspace_bytes(KIND_PAGED_E4M3, R, max_ctx_len, Hq, D), dev)
@@ -330,7 +348,7 @@ def paged_e4m3_batch(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor
         raise GQAError(GQA_ERR_INVALID_ARG, "one context length and table row per sequence")
     num_pages, page, Hkv, _ = kcache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         ensure_workspace(workspace_bytes(KIND_PAGED_E4M3_BATCH, R, B, Hq, D), dev)
@@ -353,7 +371,7 @@ def sparse_blocks(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
     num_pages, page, Hkv, _ = kcache.shape
     max_sel = sel_idx.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         st = load().gqa_attn_sparse_blocks(_ptr(q), _ptr(kcache), _ptr(vcache),
@@ -376,7 +394,7 @@ def sparse_blocks_e4m3(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tens
     num_pages, page, Hkv, _ = kcache.shape
     max_sel = sel_idx.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out)
     with torch.cuda.device(dev):
         st = load().gqa_attn_sparse_blocks_e4m3(_ptr(q), _ptr(kcache), _ptr(vcache),
@@ -502,7 +520,7 @@ def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ct
     if q is not None:
         Hq, qt, qh = _heads("q", q, dtype, idx, tokens, D)
         if q_out is None:
-            q_out = torch.empty((tokens, Hq, D), dtype=torch.float16, device=k.device)
+            q_out = _empty((tokens, Hq, D), torch.float16, k.device, stream)
         qp, op = q.data_ptr(), _want("q_out", q_out, torch.float16, idx, 3)
         if q_out.shape != q.shape:
             _refuse("q_out must have q's shape")
@@ -558,9 +576,9 @@ def cache_write(q, k, v, kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len
                         q_out, stream)
 
 
-def _out_rows(name, t, tokens, Hkv, D, dtype, idx):
+def _out_rows(name, t, tokens, Hkv, D, dtype, idx, stream):
     if t is None:
-        return torch.empty((tokens, Hkv, D), dtype=dtype, device=idx), None
+        return _empty((tokens, Hkv, D), dtype, idx, stream), None
     p = _want(name, t, dtype, idx, 3)
     if t.shape != (tokens, Hkv, D):
         _refuse(f"{name} must be [tokens, Hkv, D]")
@@ -576,8 +594,8 @@ def _cache_read(kcache, vcache, kscale, vscale, e4m3, block_tables, ctx_lens_dev
         _refuse("caches must be uint8 codes" + ("" if e4m3 else " or fp16"))
     kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache, dtype, idx)
     out_type = torch.float16 if e4m3 else dtype
-    k_out, ko = _out_rows("k_out", k_out, tokens, Hkv, D, out_type, idx)
-    v_out, vo = _out_rows("v_out", v_out, tokens, Hkv, D, out_type, idx)
+    k_out, ko = _out_rows("k_out", k_out, tokens, Hkv, D, out_type, idx, stream)
+    v_out, vo = _out_rows("v_out", v_out, tokens, Hkv, D, out_type, idx, stream)
     bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
     tail = (bt, stride, num_pages, page, rs, cl, max_ctx_len, batch, tokens, Hkv, D,
             ko or k_out.data_ptr(), vo or v_out.data_ptr())
@@ -664,14 +682,14 @@ def select_blocks(q, index, index_scale, block_table, ctx_len, max_sel, n_first=
     if block_table.numel() * ppb * 4 < ctx_len:
         _refuse("block_table must cover ctx_len")
     if sel_idx is None:
-        sel_idx = torch.empty((rows, max_sel), dtype=torch.int32, device=idx)
+        sel_idx = _empty((rows, max_sel), torch.int32, idx, stream)
         xp = sel_idx.data_ptr()
     else:
         xp = _want("sel_idx", sel_idx, torch.int32, idx, 2)
         if sel_idx.shape != (rows, max_sel):
             _refuse("sel_idx must be [rows, max_sel]")
     if sel_cnt is None:
-        sel_cnt = torch.empty((rows,), dtype=torch.int32, device=idx)
+        sel_cnt = _empty((rows,), torch.int32, idx, stream)
         cp = sel_cnt.data_ptr()
     else:
         cp = _want("sel_cnt", sel_cnt, torch.int32, idx, 1)
