@@ -623,6 +623,8 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
             int n = 0;
             // The columns' scales: four a lane of the first half, loaded a tile ahead,
             // then shared by the warp; of the sample the blocks, by the other half.
+            // (Ordinary loads: the kernel before writes them while this one may run
+            // already, so they are not read-only for its lifetime.)
             static_assert(PART == 64, "half a warp's float4");
             const bool half = MODE == MAXIMA && lane >= 16;
             const void* const cols = half ? static_cast<const void*>(P.block) : P.scale;
@@ -630,11 +632,11 @@ dot_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ 
                                lane % 16;
             uint4* const dst4 = reinterpret_cast<uint4*>(half ? my_block : (int*)my_scale) +
                                 lane % 16;
-            uint4 ahead = __ldg(src);
+            uint4 ahead = *src;
             for (int j = jb; j < je; ++j, ++t) {
                 __syncwarp();
                 if (lane < 16 || half) *dst4 = ahead;
-                if (j + 1 < je) ahead = __ldg(src += TILE / 4);
+                if (j + 1 < je) ahead = *(src += TILE / 4);
                 __syncwarp();
                 ok = mbar_wait(tfull(t & 1), (t >> 1) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);

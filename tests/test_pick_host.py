@@ -173,3 +173,13 @@ def test_areas_fit_what_is_launched(pick):
         if maxima:
             assert room >= take and room_reach >= take
             assert room_groups == 0 if n == 0 else 0 < room_groups <= (n + 7) // 8
+
+
+def test_no_read_only_loads_in_dependent_kernels():
+    """The selection's kernels start before the kernel ahead of them has ended, so
+    what it writes is not read-only for their lifetime: no load says that it is."""
+    path = os.path.join(HERE, "..", "long_context_causal_gqa_gb300", "csrc")
+    for name in ("select_blocks.cu", "pick.cuh", "pair_mma.cuh"):
+        with open(os.path.join(path, name)) as f:
+            text = f.read()
+        assert not [w for w in ("__ldg", "global.nc", "__restrict__") if w in text], name
