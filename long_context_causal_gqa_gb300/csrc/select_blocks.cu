@@ -313,7 +313,7 @@ constexpr uint32_t IDESC = idesc_f16_f32(256, TILE, false, false);
 
 template <bool RESIDENT>
 struct DotCfg {
-    static constexpr int SLOTS = RESIDENT ? (PARTS == 4 ? 5 : 7) : (PARTS == 4 ? 4 : 5);
+    static constexpr int SLOTS = RESIDENT ? 5 : 4;
     static constexpr int SLOT_BYTES = RESIDENT ? CHUNK_BYTES : 2 * CHUNK_BYTES;
     static constexpr int ROW_BYTES = RESIDENT ? RES_CHUNKS * CHUNK_BYTES : 0;
     static constexpr int NUM_BARS = 2 * SLOTS + 7;
