@@ -132,7 +132,8 @@ __device__ void range_of(const uint32_t* key, int total, uint32_t* least, uint32
 // limit are taken, and `equals` of those equal to it.  Counts over BINS equal
 // parts of the keys' range, then of the part that holds the need-th largest,
 // until what is in the part is taken whole.  Where fewer than `need` are in
-// [least, most] all the same (best_of says when), it ends with those.
+// [least, most] all the same (best_of says when), the limit is any: each part is
+// narrower than the last, so it ends as soon.
 struct Limit {
     uint32_t key;
     int equals;
@@ -150,10 +151,6 @@ __device__ __forceinline__ Limit need_th(const uint32_t* key, int total, int nee
         constexpr int PER = BINS / THREADS;
 #pragma unroll
         for (int i = 0; i < PER; ++i) S.hist[tid + i * THREADS] = 0;
-        if (tid == 0) {     // what holds if no bin has the need-th
-            S.digit = 0;
-            S.left = S.count = need;
-        }
         __syncthreads();
 #pragma unroll 1
         for (int i = tid; i < total; i += THREADS) {
@@ -259,10 +256,10 @@ __device__ __forceinline__ void best_of(const RowRange& R, uint32_t* key, const 
         }
         const int upto = cta_scan<THREADS>(n, S.sums);
         int at = done + upto - n;
-        if (n)
+        if (n && at + n <= R.room())
             for (int i = 4 * a; i < 4 * b; ++i)
-                for (uint32_t m = bits[i]; m; m &= m - 1, ++at)
-                    if (at < R.room()) out[at] = w0 + i * 32 + __ffs(m) - 1;
+                for (uint32_t m = bits[i]; m; m &= m - 1)
+                    out[at++] = w0 + i * 32 + __ffs(m) - 1;
         if (w0 + WINDOW >= R.n_vis) break;
         if (tid == THREADS - 1) S.count = upto;
         __syncthreads();
@@ -284,10 +281,6 @@ __device__ void scan_best(const RowRange& R, const Score& score, int32_t* out,
     for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
         __syncthreads();
         for (int i = tid; i < 256; i += THREADS) S.hist[i] = 0;
-        if (tid == 0) {     // what holds if no bin has the need-th
-            S.digit = 0;
-            S.left = need;
-        }
         __syncthreads();
         for (int b = R.lo + tid; b < R.hi; b += THREADS) {
             const uint32_t k = ordered(score(b));
