@@ -261,13 +261,17 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
  *   block_tables  [batch, table_stride] int32 physical page ids;
  *                 table_stride * page >= max_ctx_len.
  *   tokens        rows of the launch.  Rows in front of row_starts[0] or from
- *                 row_starts[batch] on are padding: nothing is read or written
- *                 for them.
+ *                 row_starts[batch] on are padding: nothing is written for
+ *                 them, and whatever they hold has no effect.  (Their q, k and
+ *                 v may be loaded all the same, so all `tokens` rows have to be
+ *                 there.)
  * A sequence whose context length is below n_b or above max_ctx_len is left
- * out whole and flags GQA_DEVERR_BAD_CTX_LEN.  A block-table entry outside
- * [0, num_pages) flags GQA_DEVERR_BAD_PAGE_ID; nothing is stored for its
- * tokens (a read gives zeros).  Two rows must not name the same cached token
- * (sequences that share pages): which of the two is kept is not defined.
+ * out whole (as padding) and flags GQA_DEVERR_BAD_CTX_LEN.  Outputs keep what
+ * they held for rows that are left out.  A block-table entry outside
+ * [0, num_pages) flags GQA_DEVERR_BAD_PAGE_ID; nothing is stored into the cache
+ * or the index for its tokens (their q_out is written, a read gives zeros).
+ * Two rows must not name the same cached token (sequences that share pages):
+ * which of the two is kept is not defined.
  * 1 <= batch <= 1024; num_pages * page < 2^31; head sizes, groupings and
  * pages as for the attention.  None needs a workspace. */
 

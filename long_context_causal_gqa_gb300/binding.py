@@ -561,7 +561,9 @@ def cache_write_e4m3(q, k, v, kcache, vcache, kscale, vscale, block_tables, ctx_
     (gqa_cache_write_e4m3): q [T,Hq,D] (or None), k/v [T,Hkv,D] fp16 or bf16,
     views of a fused projection included; caches [pages,page,Hkv,D] uint8;
     block_tables [B, stride], ctx_lens_dev [B], row_starts [B+1] int32.
-    Returns q_out [T,Hq,D] fp16 (None without q)."""
+    Returns q_out [T,Hq,D] fp16 (None without q); rows that belong to no
+    sequence, or to one whose context length is refused, are left as they were
+    (in a q_out allocated here: not initialised)."""
     return _cache_write(q, k, v, kcache, vcache, kscale, vscale, True, block_tables,
                         ctx_lens_dev, max_ctx_len, q_weight, k_weight, eps, inv_freq,
                         interleaved, row_starts, q_out, stream)
@@ -610,7 +612,9 @@ def _cache_read(kcache, vcache, kscale, vscale, e4m3, block_tables, ctx_lens_dev
 def cache_read_e4m3(kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
                     tokens, row_starts=None, k_out=None, v_out=None, stream=None):
     """The cached tokens of a batch's rows as dense fp16 K, V [tokens,Hkv,D]
-    (gqa_cache_read_e4m3); the last tokens / B (or row_starts') of each context."""
+    (gqa_cache_read_e4m3); the last tokens / B (or row_starts') of each context.
+    Rows that belong to no sequence, or to one whose context length is refused,
+    are left as they were (in outputs allocated here: not initialised)."""
     return _cache_read(kcache, vcache, kscale, vscale, True, block_tables, ctx_lens_dev,
                        max_ctx_len, tokens, row_starts, k_out, v_out, stream)
 
