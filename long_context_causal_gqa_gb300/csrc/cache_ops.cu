@@ -464,11 +464,13 @@ __global__ void __launch_bounds__(INDEX_THREADS) index_kernel(const IndexParams 
         __syncthreads();
     }
     const int lane = threadIdx.x % 32;
-    const int row = (blockIdx.x * (INDEX_THREADS / 32) + threadIdx.x / 32) * P.rows_per_warp + lane;
+    // (unsigned: the last CTA's rows may pass 2^31)
+    const uint32_t row =
+        (blockIdx.x * (INDEX_THREADS / 32) + threadIdx.x / 32) * P.rows_per_warp + lane;
     int pos = -1;
     long long slot = -1;
-    if (lane < P.rows_per_warp && row < P.rows.tokens)
-        locate_row(P.rows, s_starts, row, &pos, &slot);
+    if (lane < P.rows_per_warp && row < (uint32_t)P.rows.tokens)
+        locate_row(P.rows, s_starts, (int)row, &pos, &slot);
     const float unit = E4M3 ? *P.kscale / 508.f : 1.f / 508.f;
     uint32_t ends = __ballot_sync(0xffffffffu, (pos & 3) == 3 && slot >= 0);
     while (ends) {
@@ -655,7 +657,7 @@ int block_index_launch(const CacheRows& r, const void* kcache, const float* ksca
     // rows 2.6 instead of 3.6; many make as many warps anyway.
     P.rows_per_warp = r.tokens <= di->num_sms * 128 ? 8 : 32;
     const int a_cta = INDEX_THREADS / 32 * P.rows_per_warp;
-    const int grid = (r.tokens + a_cta - 1) / a_cta;
+    const int grid = (r.tokens - 1) / a_cta + 1;
     if (kscale) launch_index<true>(P, grid, stream);
     else launch_index<false>(P, grid, stream);
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;

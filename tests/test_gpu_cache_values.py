@@ -171,3 +171,25 @@ def test_infinities_and_nan(cuda_lib, interleaved):
                 tol = 2.0 ** -11 * np.abs(y) + 2.0 ** -25 + bound(m, 3 + j, freq.cpu().numpy(),
                                                                   rot, interleaved)
                 assert (np.abs(g - y)[fine] <= tol[fine]).all()
+
+
+def test_index_of_the_most_rows(cuda_lib):
+    """2^31 - 2 rows: 1023 sequences that share their pages."""
+    dev = torch.device("cuda")
+    batch, ctx, page, D = 1023, 2099202, 256, 128
+    pages = -(-ctx // page)
+    assert batch * ctx == 2 ** 31 - 2
+    kc = torch.randint(0, 120, (pages, page, 1, D), dtype=torch.uint8, device=dev)
+    s = torch.tensor([0.02], device=dev)
+    tables = torch.arange(pages, dtype=torch.int32, device=dev).repeat(batch, 1)
+    lens = torch.full((batch,), ctx, dtype=torch.int32, device=dev)
+    got = []
+    for n in (1, batch):
+        index = torch.zeros(pages, page // 4, 1, D, dtype=torch.int8, device=dev)
+        scale = torch.zeros(pages, page // 4, device=dev)
+        cuda_lib.block_index_e4m3(kc, s, tables[:n].contiguous(), lens[:n].contiguous(), ctx,
+                                  n * ctx, index, scale)
+        got.append((index, scale))
+    assert cuda_lib.device_error() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert int((got[1][1] > 0).sum()) == ctx // 4
