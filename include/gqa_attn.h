@@ -296,10 +296,11 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
  *   kcache/vcache [num_pages, page, Hkv, D] E4M3 codes: round to nearest even
  *                 of the value times the fp32 reciprocal of kscale / vscale
  *                 (device fp32, > 0), +-448 beyond the range, NaN stays NaN.
- * Norm and rotation in 32 bits (cos and sin to 2^-20, of an angle kept to
- * 2^-20 at any position), one rounding at the end; a head's sum of squares has to
- * stay within 32 bits' range.  q_out and the caches must
- * not overlap q, k or v. */
+ * Norm and rotation in 32 bits, one rounding at the end; a head's sum of squares
+ * has to stay within 32 bits' range.  q_out becomes an infinity beyond fp16's
+ * range.  cos and sin are those of position * inv_freq to
+ * 2^-20 + |position * inv_freq| * 2^-45, from position 2^24 on to 2^-18 + the
+ * same.  q_out and the caches must not overlap q, k or v. */
 typedef struct {
     const void *q, *k, *v;
     const void *q_weight, *k_weight;
@@ -317,7 +318,7 @@ typedef struct {
 int gqa_cache_write_e4m3(const gqa_cache_write_args* args, struct CUstream_st* stream);
 
 /* The same over an fp16 cache: kcache/vcache [num_pages, page, Hkv, D] fp16,
- * no scales. */
+ * no scales; K and V become infinities beyond fp16's range, NaN stays NaN. */
 int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream);
 
 /* Cache read: the cached tokens the rows stand for, as dense rows (the K / V

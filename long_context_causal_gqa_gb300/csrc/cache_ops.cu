@@ -77,10 +77,14 @@ __device__ __forceinline__ uint32_t to_e4m3x2(Pair p) {
     return __nv_cvt_float2_to_fp8x2(unpack(p), __NV_SATFINITE, __NV_E4M3);
 }
 
-// cos and sin of position * frequency, as a fraction of a turn: the product
-// position * frequency / (2 pi) is formed to about 48 bits (two floats and
-// the product's own rounding error), so that far positions keep their angle;
-// then the hardware's approximations (error below 2^-20 within half a turn).
+// cos and sin of position * frequency, as a fraction of a turn: frequency / (2 pi)
+// as hi + lo, to 1.5 2^-47 of it, and the products' own rounding errors, whose
+// fractions are taken before they are added, so that far positions keep their
+// angle.  Then the hardware's approximations: within half a turn 2^-21.4 for the
+// sine and 2^-21.2 for the cosine, and 2^-21.8 of the angle's product with 2 pi.
+// With the sums' roundings (2^-25 of a turn; 5 2^-24 with a high part) the results
+// hold to 2^-20 + |position * frequency| 2^-45, from position 2^24 on to 2^-18 and
+// the same.
 __device__ __forceinline__ float2 turn(int pos, float hi, float lo) {
     // Parts of at most 24 bits, each exact as a float.
     const int low = pos & 0xffffff, high = pos - low;
@@ -113,7 +117,8 @@ __device__ __forceinline__ float2 turn(int pos, float hi, float lo) {
 //
 // y = x / sqrt(mean(x^2) + eps) * w and the rotation in 32 bits, two products
 // an instruction; one rounding at the end (fp16 for q, the cache's type for K
-// and V).
+// and V).  The root is rsqrtf, to 2 units in the last place of 32 bits; codes are
+// those of the product with the scale's rounded reciprocal.
 //
 // 8000 rows of 6 + 1 + 1 heads of 256 into an E4M3 cache move 61 MB, 9.0 us at the
 // copy rate, and take 16.9 us (a plain copy of the same buffers, 11.7): between
@@ -595,8 +600,11 @@ int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e
     P.nq = a.q ? a.Hq : 0;
     P.hkv = a.Hkv;
     P.by_pairs = make_fastdiv(P.pairs > 0 ? P.pairs : 1);
-    // Few tokens go one to a CTA; their heads are shared out as far as that keeps
-    // all CTAs resident at once (8000 rows: 16.9 us, 18.2 with all heads in one).
+    // Few tokens go one to a CTA, and while all CTAs are resident at once the heads
+    // are shared out among more of them (6 + 1 + 1 heads of 256: 400 rows 3.5 us,
+    // 4.0 with a unit's heads in one CTA, 1500 rows 4.7 and 5.1; 16 + 4 + 4 heads:
+    // 400 rows 4.4 and 7.5).  Of many tokens a CTA takes all heads of its unit (8000
+    // rows: 2000 CTAs, 760 of them at once).
     const int heads = P.nq + 2 * P.hkv, groups = WRITE_THREADS * 8 / a.D;
     const long long resident = (long long)di->num_sms * WRITE_CTAS;
     P.tile = (long long)r.tokens * heads <= resident * groups ? 1 : UNIT;

@@ -1308,8 +1308,10 @@ int round_up(int n, int m) { return (n + m - 1) / m * m; }
 // Calls of few rows take the dp4a path.  In us by it and by the tensor cores (rows x
 // blocks, 64 or 128 taken): width 256, 8 x 8192 12 and 16, 32 x 8192 17 and 17, 40 x
 // 16384 24 and 22; width 512, 32 x 16384 36 and 25; width 1024, 8 x 16384 23 and 31,
-// 16 x 16384 35 and 31.  (A width above the call's own, as the workspace is sized
-// for, never makes it few where the call is not.)
+// 16 x 16384 35 and 31.  Over the longest contexts: width 256, 8 x 65472 22 and 56,
+// 32 x 65472 45 and 58; width 512, 8 x 65472 31 and 85; width 1024, 8 x 50000 44 and
+// 108.  (A width above the call's own, as the workspace is sized for, never makes it
+// few where the call is not.)
 bool few_rows(int rows, int width) { return rows <= (width > 256 ? 8 : 32); }
 
 constexpr size_t SCORE_BYTES = 128ull << 20;   // scores or maxima held at once
