@@ -25,7 +25,7 @@
 // sample (a block of four) 22, its bounds 11, the candidates 55, the best of
 // them 30, overlapping a little.  Of the candidates' 55 the products alone are
 // 44 (loads and products without the epilogue's compares).  One row over 65472
-// blocks reads 17 MB, 2.5 us; it takes 16.7 us, of which 11 are the pick on one
+// blocks reads 17 MB, 2.5 us; it takes 16.8 us, of which 11 are the pick on one
 // SM, a chain of barriers and dependent loads; the call's host side takes 22.
 #include <algorithm>
 #include <atomic>
