@@ -203,6 +203,33 @@ int gqa_attn_paged_e4m3_noalloc(const void* q, const uint8_t* kcache, const uint
                                 int ctx_len, int query_rows, int Hq, int Hkv, int D,
                                 float scale, void* out, struct CUstream_st* stream);
 
+/* Tails of a batch over a 4-bit cache, all of the context or a sliding window and
+ * first tokens that stay visible ("sinks").
+ *   q, out        [batch, query_rows, Hq, D] fp16; query_rows * Hq / Hkv <= 48
+ *   kcache/vcache [num_pages, Hkv, page, 9 D / 16] uint8, as gqa_cache_write_fp4 writes
+ *                 them; kscale/vscale device fp32, > 0, 4-byte aligned
+ *   block_tables  [batch, table_stride] int32; table_stride * page >= max_ctx_len
+ *   ctx_lens_dev  device int32 [batch], read when the kernels run; values below 0 or
+ *                 above max_ctx_len are clamped and flag GQA_DEVERR_BAD_CTX_LEN
+ *   window        0: none.  W >= 1: the row at position p sees the keys j <= p with
+ *                 j > p - W or j < sinks (sinks >= 0, unused without a window)
+ * Row r of sequence b sits at position ctx_lens[b] - query_rows + r.  A row that sees no
+ * key (a context shorter than query_rows, or of no tokens) gets zeros.  Block-table
+ * entries of pages that no row sees are not read; others outside the cache read page 0
+ * and flag GQA_DEVERR_BAD_PAGE_ID.  Keys that a row does not see have no effect on it,
+ * whatever their bytes (NaN scales included).
+ * 1 <= batch <= 1024; num_pages * page < 2^31.  FP32 accumulation; cached values enter the
+ * products exactly, P rounded to fp16.  The visible tiles of all sequences and KV
+ * heads are divided equally between the SMs on the device, and what is cut is joined
+ * in a fixed order by a second kernel.  Workspace: gqa_workspace_bytes(
+ * GQA_KIND_PAGED_FP4, query_rows, any, Hq, D), for any batch and context. */
+int gqa_attn_paged_fp4(const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                       const float* kscale, const float* vscale, const int32_t* block_tables,
+                       int table_stride, int num_pages, int page, const int32_t* ctx_lens_dev,
+                       int max_ctx_len, int batch, int query_rows, int Hq, int Hkv, int D,
+                       float scale, int window, int sinks, void* out,
+                       struct CUstream_st* stream);
+
 /* Selected-block sparse paged prefill [P3, Changes].
  *   q            [query_rows, Hq, D] fp16
  *   kcache/vcache [num_pages, page, Hkv, D] fp16, page a power of two in
@@ -321,6 +348,18 @@ int gqa_cache_write_e4m3(const gqa_cache_write_args* args, struct CUstream_st* s
  * no scales; K and V become infinities beyond fp16's range, NaN stays NaN. */
 int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream);
 
+/* The same over a 4-bit cache.  A row of one token and KV head is D / 2 bytes of
+ * E2M1 codes (value 2 i in the low nibble of byte i) and behind them D / 16 E4M3
+ * scales, one for each 16 values; a value is e2m1(code) * e4m3(scale) * the tensor's
+ * fp32 scale (kscale / vscale).
+ *   kcache/vcache [num_pages, Hkv, page, 9 D / 16] uint8: heads in front of tokens,
+ *                 so that a page of one head is one contiguous run
+ * With u = value * (fp32 reciprocal of kscale / vscale) and A = max |u| over a block of
+ * 16: scale = e4m3(A / 6), codes = e2m1(u / scale), both to nearest even, +-448 and +-6
+ * beyond the range; codes of zero where the scale is zero.  A block with a NaN gets
+ * the NaN scale and zero codes, so all of it reads as NaN. */
+int gqa_cache_write_fp4(const gqa_cache_write_args* args, struct CUstream_st* stream);
+
 /* Cache read: the cached tokens the rows stand for, as dense rows (the K / V
  * of gqa_attn_prefill for one sequence).  k_out, v_out [tokens, Hkv, D] fp16 =
  * decode(code) * scale in 32 bits, rounded to nearest fp16.  Sequences may share
@@ -339,6 +378,15 @@ int gqa_cache_read(const void* kcache, const void* vcache, int elem_bytes,
                    const int32_t* row_starts, const int32_t* ctx_lens_dev, int max_ctx_len,
                    int batch, int tokens, int Hkv, int D, void* k_out, void* v_out,
                    struct CUstream_st* stream);
+
+/* The same rows of a 4-bit cache (layout as for gqa_cache_write_fp4) as dense fp16
+ * rows: k_out, v_out [tokens, Hkv, D] = e2m1(code) * e4m3(scale), exact, times kscale /
+ * vscale in 32 bits, rounded to nearest fp16. */
+int gqa_cache_read_fp4(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
+                       const float* vscale, const int32_t* block_tables, int table_stride,
+                       int num_pages, int page, const int32_t* row_starts,
+                       const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                       int Hkv, int D, void* k_out, void* v_out, struct CUstream_st* stream);
 
 /* Block index: the summary of every 4-token block that a row of this step
  * finishes (a row at a position 4b + 3), from the cache's keys.
@@ -395,6 +443,7 @@ int gqa_select_blocks(const void* q, const int8_t* index, const float* index_sca
 #define GQA_KIND_SPARSE 2
 #define GQA_KIND_PAGED_E4M3_BATCH 3   /* ctx_or_kv = number of sequences */
 #define GQA_KIND_SELECT_BLOCKS 4
+#define GQA_KIND_PAGED_FP4 5          /* ctx_or_kv unused */
 
 /* Bytes of workspace an entry point of `kind` needs for the given shape on
  * the current device (query_rows = Q or the tail/row count, ctx_or_kv = KV or

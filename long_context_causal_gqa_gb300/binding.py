@@ -36,6 +36,7 @@ KIND_PAGED_E4M3 = 1
 KIND_SPARSE = 2
 KIND_PAGED_E4M3_BATCH = 3
 KIND_SELECT_BLOCKS = 4
+KIND_PAGED_FP4 = 5
 DTYPE_F16 = 0
 DTYPE_BF16 = 1
 DEVERR_WAIT_TIMEOUT = 0x1
@@ -51,6 +52,7 @@ EXPORTED = ("gqa_attn_prefill", "gqa_attn_prefill_e4m3", "gqa_attn_paged_e4m3", 
             "gqa_attn_sparse_blocks", "gqa_attn_sparse_blocks_e4m3",
             "gqa_cache_write_e4m3", "gqa_cache_write", "gqa_cache_read_e4m3", "gqa_cache_read",
             "gqa_block_index_e4m3", "gqa_block_index", "gqa_select_blocks",
+            "gqa_cache_write_fp4", "gqa_cache_read_fp4", "gqa_attn_paged_fp4",
             "gqa_workspace_bytes", "gqa_set_workspace", "gqa_get_device_error",
             "gqa_check_wait_limit", "gqa_prefill_sm_pairs", "gqa_status_string")
 
@@ -97,12 +99,17 @@ def load():
             lib.gqa_attn_sparse_blocks_e4m3.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I,
                                                         I, I, I, F, P, P]
             lib.gqa_attn_sparse_blocks_e4m3.restype = I
-            for f in (lib.gqa_cache_write_e4m3, lib.gqa_cache_write):
+            for f in (lib.gqa_cache_write_e4m3, lib.gqa_cache_write, lib.gqa_cache_write_fp4):
                 f.argtypes = [ctypes.c_char_p, P]
                 f.restype = I
             lib.gqa_cache_read_e4m3.argtypes = [P, P, P, P, P, I, I, I, P, P, I, I, I, I, I, P,
                                                 P, P]
             lib.gqa_cache_read_e4m3.restype = I
+            lib.gqa_cache_read_fp4.argtypes = lib.gqa_cache_read_e4m3.argtypes
+            lib.gqa_cache_read_fp4.restype = I
+            lib.gqa_attn_paged_fp4.argtypes = [P, P, P, P, P, P, I, I, I, P, I, I, I, I, I, I, F,
+                                               I, I, P, P]
+            lib.gqa_attn_paged_fp4.restype = I
             lib.gqa_cache_read.argtypes = [P, P, I, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
             lib.gqa_cache_read.restype = I
             lib.gqa_block_index_e4m3.argtypes = [P, P, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
@@ -458,6 +465,20 @@ def _call(fn, idx, stream, *args):
         raise GQAError(st, fn.__name__)
 
 
+def _call_with_workspace(fn, idx, stream, args, kind, *shape):
+    """The call; where the workspace is too small for it, again with one that is not."""
+    try:
+        _call(fn, idx, stream, *args)
+    except ctypes.ArgumentError as e:
+        _refuse(str(e))
+    except GQAError as e:
+        if e.status != GQA_ERR_WORKSPACE:
+            raise
+        with torch.cuda.device(idx):
+            ensure_workspace(workspace_bytes(kind, *shape), idx)
+        _call(fn, idx, stream, *args)
+
+
 def _device_of(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse("tensors must be CUDA tensors")
@@ -498,7 +519,15 @@ def _rows(block_tables, ctx_lens_dev, row_starts, idx):
     return bt, stride, rs, cl, batch
 
 
-def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ctx_lens_dev,
+def _fp4_pages(kcache, vcache, idx):
+    """Pointers of two 4-bit caches [pages, Hkv, page, 9 D / 16] and (pages, page, Hkv, D)."""
+    kp, vp, (num_pages, Hkv, page, row) = _pages(kcache, vcache, torch.uint8, idx)
+    if row % 9:
+        _refuse("a row of a 4-bit cache must have 9 D / 16 bytes")
+    return kp, vp, (num_pages, page, Hkv, row // 9 * 16)
+
+
+def _cache_write(q, k, v, kcache, vcache, kscale, vscale, bits, block_tables, ctx_lens_dev,
                  max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts, q_out,
                  stream):
     lib = load() if _lib is None else _lib
@@ -510,8 +539,11 @@ def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ct
         kind = DTYPE_BF16
     else:
         _refuse("k must be fp16 or bf16")
-    kp, vp, (num_pages, page, Hkv, D) = _pages(kcache, vcache,
-                                               torch.uint8 if e4m3 else torch.float16, idx)
+    if bits == 4:
+        kp, vp, (num_pages, page, Hkv, D) = _fp4_pages(kcache, vcache, idx)
+    else:
+        kp, vp, (num_pages, page, Hkv, D) = _pages(
+            kcache, vcache, torch.uint8 if bits == 8 else torch.float16, idx)
     tokens = len(k)
     hk, kt, kh = _heads("k", k, dtype, idx, tokens, D)
     hv, vt, vh = _heads("v", v, dtype, idx, tokens, D)
@@ -540,7 +572,7 @@ def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ct
     if inv_freq is not None:
         fp = _want("inv_freq", inv_freq, torch.float32, idx, 1)
         rot = 2 * inv_freq.numel()
-    if e4m3:
+    if bits < 16:
         ks, vs = _scale("kscale", kscale, idx), _scale("vscale", vscale, idx)
     bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
     try:
@@ -550,7 +582,8 @@ def _cache_write(q, k, v, kcache, vcache, kscale, vscale, e4m3, block_tables, ct
                                 max_ctx_len, batch, tokens, Hq, Hkv, D)
     except (struct.error, OverflowError, TypeError) as e:
         _refuse(str(e))
-    _call(lib.gqa_cache_write_e4m3 if e4m3 else lib.gqa_cache_write, idx, stream, args)
+    _call(lib.gqa_cache_write if bits == 16 else
+          lib.gqa_cache_write_e4m3 if bits == 8 else lib.gqa_cache_write_fp4, idx, stream, args)
     return q_out
 
 
@@ -564,7 +597,7 @@ def cache_write_e4m3(q, k, v, kcache, vcache, kscale, vscale, block_tables, ctx_
     Returns q_out [T,Hq,D] fp16 (None without q); rows that belong to no
     sequence, or to one whose context length is refused, are left as they were
     (in a q_out allocated here: not initialised)."""
-    return _cache_write(q, k, v, kcache, vcache, kscale, vscale, True, block_tables,
+    return _cache_write(q, k, v, kcache, vcache, kscale, vscale, 8, block_tables,
                         ctx_lens_dev, max_ctx_len, q_weight, k_weight, eps, inv_freq,
                         interleaved, row_starts, q_out, stream)
 
@@ -573,7 +606,17 @@ def cache_write(q, k, v, kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len
                 k_weight=None, eps=1e-6, inv_freq=None, interleaved=False, row_starts=None,
                 q_out=None, stream=None):
     """cache_write_e4m3 over an fp16 cache (caches [pages,page,Hkv,D] fp16, no scales)."""
-    return _cache_write(q, k, v, kcache, vcache, None, None, False, block_tables, ctx_lens_dev,
+    return _cache_write(q, k, v, kcache, vcache, None, None, 16, block_tables, ctx_lens_dev,
+                        max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts,
+                        q_out, stream)
+
+
+def cache_write_fp4(q, k, v, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev,
+                    max_ctx_len, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                    interleaved=False, row_starts=None, q_out=None, stream=None):
+    """cache_write_e4m3 into a 4-bit cache (gqa_cache_write_fp4): caches
+    [pages,Hkv,page,9*D/16] uint8, E2M1 codes with an E4M3 scale for every 16."""
+    return _cache_write(q, k, v, kcache, vcache, kscale, vscale, 4, block_tables, ctx_lens_dev,
                         max_ctx_len, q_weight, k_weight, eps, inv_freq, interleaved, row_starts,
                         q_out, stream)
 
@@ -624,6 +667,62 @@ def cache_read(kcache, vcache, block_tables, ctx_lens_dev, max_ctx_len, tokens, 
     """The same rows in the cache's own type: fp16, or E4M3 codes (uint8)."""
     return _cache_read(kcache, vcache, None, None, False, block_tables, ctx_lens_dev,
                        max_ctx_len, tokens, row_starts, k_out, v_out, stream)
+
+
+def cache_read_fp4(kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
+                   tokens, row_starts=None, k_out=None, v_out=None, stream=None):
+    """cache_read_e4m3 of a 4-bit cache (caches [pages,Hkv,page,9*D/16] uint8)."""
+    lib = load() if _lib is None else _lib
+    idx = _device_of(kcache)
+    kp, vp, (num_pages, page, Hkv, D) = _fp4_pages(kcache, vcache, idx)
+    k_out, ko = _out_rows("k_out", k_out, tokens, Hkv, D, torch.float16, idx, stream)
+    v_out, vo = _out_rows("v_out", v_out, tokens, Hkv, D, torch.float16, idx, stream)
+    bt, stride, rs, cl, batch = _rows(block_tables, ctx_lens_dev, row_starts, idx)
+    _call(lib.gqa_cache_read_fp4, idx, stream, kp, vp, _scale("kscale", kscale, idx),
+          _scale("vscale", vscale, idx), bt, stride, num_pages, page, rs, cl, max_ctx_len, batch,
+          tokens, Hkv, D, ko or k_out.data_ptr(), vo or v_out.data_ptr())
+    return k_out, v_out
+
+
+# ---- tails over a 4-bit cache, and attention with a sliding window ---------------
+
+
+def _tails(fn, kind, q, idx, pages, pointers, kscale, vscale, block_tables, ctx_lens_dev,
+           max_ctx_len, scale, window, sinks, out, stream):
+    """A batch's tails: one library call, or two where the workspace has to grow first."""
+    num_pages, page, Hkv, D = pages
+    qp = _want("q", q, torch.float16, idx, 4)
+    B, R, Hq, d = q.shape
+    if d != D:
+        _refuse("q and the caches must have the same head size")
+    bt, stride, _, cl, batch = _rows(block_tables, ctx_lens_dev, None, idx)
+    if batch != B:
+        _refuse("one context length and table row per sequence")
+    if out is None:
+        out = _empty(q.shape, torch.float16, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _want("out", out, torch.float16, idx, 4)
+        if out.shape != q.shape:
+            _refuse("out must have q's shape")
+    args = (qp, *pointers, _scale("kscale", kscale, idx), _scale("vscale", vscale, idx), bt,
+            stride, num_pages, page, cl, max_ctx_len, B, R, Hq, Hkv, D, scale,
+            0 if window is None else window, sinks, op)
+    _call_with_workspace(fn, idx, stream, args, kind, R, B, Hq, D)
+    return out
+
+
+def paged_fp4(q, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
+              scale=1.0 / 16, window=None, sinks=0, out=None, stream=None):
+    """Tails of a batch over a 4-bit cache (gqa_attn_paged_fp4): q [B,R,Hq,D] fp16, caches
+    [pages,Hkv,page,9*D/16] uint8, block_tables [B, stride] and ctx_lens_dev [B] int32.
+    window: a row sees its last `window` positions (its own among them) and the first
+    `sinks` tokens; None: the whole context."""
+    lib = load() if _lib is None else _lib
+    idx = _device_of(q)
+    kp, vp, pages = _fp4_pages(kcache, vcache, idx)
+    return _tails(lib.gqa_attn_paged_fp4, KIND_PAGED_FP4, q, idx, pages, (kp, vp), kscale, vscale,
+                  block_tables, ctx_lens_dev, max_ctx_len, scale, window, sinks, out, stream)
 
 
 def _index_pointers(index, index_scale, idx):

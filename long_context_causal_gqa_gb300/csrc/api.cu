@@ -228,13 +228,15 @@ int rows_check(const CacheRows& r, int Hq, int Hkv, int D) {
     return GQA_OK;
 }
 
-int write_common(const gqa_cache_write_args* args, bool e4m3, cudaStream_t stream) {
+// cache_bits: 16 (fp16), 8 (E4M3 codes) or 4 (E2M1 codes with E4M3 scales).
+int write_common(const gqa_cache_write_args* args, int cache_bits, cudaStream_t stream) {
     if (!args) return GQA_ERR_INVALID_ARG;
     const gqa_cache_write_args& a = *args;
     const CacheRows r = {a.block_tables, a.row_starts, a.ctx_lens_dev, a.table_stride,
                          a.num_pages, a.page, a.max_ctx_len, a.batch, a.tokens};
     if (!a.k || !a.v || !a.kcache || !a.vcache || !a.q != !a.q_out) return GQA_ERR_INVALID_ARG;
-    if (e4m3 && (!a.kscale || !a.vscale || !aligned4(a.kscale) || !aligned4(a.vscale)))
+    if (cache_bits < 16 &&
+        (!a.kscale || !a.vscale || !aligned4(a.kscale) || !aligned4(a.vscale)))
         return GQA_ERR_INVALID_ARG;
     if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) ||
         !aligned16(a.kcache) || !aligned16(a.vcache) || !aligned16(a.q_weight) ||
@@ -250,7 +252,7 @@ int write_common(const gqa_cache_write_args* args, bool e4m3, cudaStream_t strea
     const int rc = rows_check(r, a.Hq, a.Hkv, a.D);
     if (rc != GQA_OK) return rc;
     if (a.rot_dim > a.D || a.rot_dim % 16) return GQA_ERR_UNSUPPORTED;
-    return cache_write_launch(r, a, e4m3, stream);
+    return cache_write_launch(r, a, cache_bits, stream);
 }
 
 int read_common(const CacheRows& r, const void* kcache, const void* vcache, const float* kscale,
@@ -275,6 +277,29 @@ int index_common(const CacheRows& r, const void* kcache, const float* kscale, in
     if (rc != GQA_OK) return rc;
     if (Hkv * D > kMaxIndexWidth) return GQA_ERR_UNSUPPORTED;
     return block_index_launch(r, kcache, kscale, Hkv * D, index, index_scale, stream);
+}
+
+// What the tails of a batch with a window, or over a 4-bit cache, check.
+int batch_check(const void* q, const void* kcache, const void* vcache, const float* kscale,
+                const float* vscale, const int32_t* block_tables, int table_stride,
+                int num_pages, int page, const int32_t* ctx_lens_dev, int max_ctx_len, int batch,
+                int query_rows, int Hq, int Hkv, int D, float scale, const void* out) {
+    if (!q || !kcache || !vcache || !kscale || !vscale || !block_tables || !ctx_lens_dev || !out)
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(out) ||
+        !aligned4(kscale) || !aligned4(vscale) || !aligned4(block_tables) ||
+        !aligned4(ctx_lens_dev))
+        return GQA_ERR_INVALID_ARG;
+    if (query_rows < 1 || max_ctx_len < 1 || num_pages < 1 || batch < 1 || table_stride < 1 ||
+        !scale_ok(scale))
+        return GQA_ERR_INVALID_ARG;
+    if (!tail_family_ok(Hq, Hkv, D, query_rows) || !page_ok(page) || batch > kMaxTailBatch)
+        return GQA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if ((long long)max_ctx_len > (long long)num_pages * page ||
+        (long long)max_ctx_len > (long long)table_stride * page)
+        return GQA_ERR_INVALID_ARG;
+    return GQA_OK;
 }
 
 }  // namespace
@@ -416,11 +441,47 @@ int gqa_attn_sparse_blocks_e4m3(const void* q, const uint8_t* kcache, const uint
 }
 
 int gqa_cache_write_e4m3(const gqa_cache_write_args* args, struct CUstream_st* stream) {
-    return write_common(args, true, stream);
+    return write_common(args, 8, stream);
 }
 
 int gqa_cache_write(const gqa_cache_write_args* args, struct CUstream_st* stream) {
-    return write_common(args, false, stream);
+    return write_common(args, 16, stream);
+}
+
+int gqa_cache_write_fp4(const gqa_cache_write_args* args, struct CUstream_st* stream) {
+    return write_common(args, 4, stream);
+}
+
+int gqa_cache_read_fp4(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
+                       const float* vscale, const int32_t* block_tables, int table_stride,
+                       int num_pages, int page, const int32_t* row_starts,
+                       const int32_t* ctx_lens_dev, int max_ctx_len, int batch, int tokens,
+                       int Hkv, int D, void* k_out, void* v_out, struct CUstream_st* stream) {
+    const CacheRows r = {block_tables, row_starts, ctx_lens_dev, table_stride, num_pages,
+                         page, max_ctx_len, batch, tokens};
+    if (!kcache || !vcache || !k_out || !v_out || !kscale || !vscale) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(kcache) || !aligned16(vcache) || !aligned16(k_out) || !aligned16(v_out) ||
+        !aligned4(kscale) || !aligned4(vscale))
+        return GQA_ERR_INVALID_ARG;
+    const int rc = rows_check(r, Hkv, Hkv, D);
+    if (rc != GQA_OK) return rc;
+    return cache_read_fp4_launch(r, kcache, vcache, kscale, vscale, Hkv, D, k_out, v_out, stream);
+}
+
+int gqa_attn_paged_fp4(const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                       const float* kscale, const float* vscale, const int32_t* block_tables,
+                       int table_stride, int num_pages, int page, const int32_t* ctx_lens_dev,
+                       int max_ctx_len, int batch, int query_rows, int Hq, int Hkv, int D,
+                       float scale, int window, int sinks, void* out,
+                       struct CUstream_st* stream) {
+    const int rc = batch_check(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                               num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq,
+                               Hkv, D, scale, out);
+    if (rc != GQA_OK) return rc;
+    if (window < 0 || sinks < 0) return GQA_ERR_INVALID_ARG;
+    return paged_fp4_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                            num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq, Hkv,
+                            D, scale, window, sinks, out, stream);
 }
 
 int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
@@ -499,6 +560,10 @@ size_t gqa_workspace_bytes(int kind, int query_rows, int ctx_or_kv, int Hq, int 
     if (kind == GQA_KIND_PAGED_E4M3_BATCH) {   // ctx_or_kv = number of sequences
         if (query_rows > kMaxTailPackedRows || ctx_or_kv > kMaxTailBatch) return 0;
         return paged_e4m3_batch_workspace_bytes(query_rows * Hq, ctx_or_kv, di->num_sms, D);
+    }
+    if (kind == GQA_KIND_PAGED_FP4) {
+        if (query_rows > kMaxTailPackedRows) return 0;
+        return paged_fp4_workspace_bytes(query_rows * Hq, di->num_sms, D);
     }
     if (ctx_or_kv < query_rows) return 0;
     switch (kind) {

@@ -4,10 +4,12 @@
 // the block index (an int8 summary of every finished 4-token block).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <type_traits>
 
 #include "cache_rows.cuh"
+#include "fp4_rows.cuh"
 
 namespace gqa {
 namespace cacheops {
@@ -76,6 +78,31 @@ __device__ __forceinline__ uint32_t to_half2(Pair p) {
 __device__ __forceinline__ uint32_t to_e4m3x2(Pair p) {
     return __nv_cvt_float2_to_fp8x2(unpack(p), __NV_SATFINITE, __NV_E4M3);
 }
+// The largest magnitude; NaN if there is one.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max4_abs(float a, float b, float c, float d) {
+    return max3_abs(max3_abs(a, b, c), d, 0.f);
+}
+__device__ __forceinline__ float max4_abs(Pair a, Pair b) {
+    const float2 x = unpack(a), y = unpack(b);
+    return max4_abs(x.x, x.y, y.x, y.y);
+}
+// Four values over their block's scale as E2M1 codes, the first in the lowest
+// nibble: round to nearest even, +-6 beyond the range; zeros for a scale of zero or
+// NaN.  (A true quotient: values and scales have few bits, so that many quotients lie
+// half way between two codes, where the product with a reciprocal may go either way.)
+__device__ __forceinline__ uint32_t to_e2m1x4(Pair a, Pair b, float s) {
+    const float2 x = unpack(a), y = unpack(b);
+    if (!(s > 0.f)) return 0;
+    return __nv_cvt_float2_to_fp4x2(make_float2(x.x / s, x.y / s), __NV_E2M1, cudaRoundNearest) |
+           (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(y.x / s, y.y / s), __NV_E2M1,
+                                              cudaRoundNearest)
+               << 8;
+}
 
 // cos and sin of position * frequency, as a fraction of a turn: frequency / (2 pi)
 // as hi + lo, to 1.5 2^-47 of it, and the products' own rounding errors, whose
@@ -134,7 +161,10 @@ constexpr int WRITE_THREADS = 128;
 constexpr int WRITE_CTAS = 5;           // resident on an SM
 constexpr int MAX_ROT_PAIRS = 128;      // rotated pairs of a head (rot_dim <= 256)
 
-template <int DH, bool E4M3, bool BF16>
+// What the cache holds.
+enum Cache { F16, E4M3, FP4 };
+
+template <int DH, Cache KIND, bool BF16>
 __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const WriteParams P) {
     constexpr int LANES = DH / 8;
     constexpr int GROUPS = WRITE_THREADS / LANES;
@@ -143,6 +173,8 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
     __shared__ long long s_cache[UNIT];    // element offset of the token, -1: none
     __shared__ __align__(16) float s_cos[UNIT][MAX_ROT_PAIRS];
     __shared__ __align__(16) float s_sin[UNIT][MAX_ROT_PAIRS];
+    // FP4: the largest magnitude of every run of four values of a group's head.
+    __shared__ __align__(16) float s_most[KIND == FP4 ? GROUPS : 1][UNIT][DH / 4];
     const int t0 = blockIdx.x * P.tile;
     const int nt = min(P.tile, P.rows.tokens - t0);
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -189,9 +221,17 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
     if (threadIdx.x < nt) {
         long long slot;
         locate_row(P.rows, s_starts, t0 + threadIdx.x, &s_pos[threadIdx.x], &slot);
-        s_cache[threadIdx.x] = slot < 0 ? -1 : slot * (P.hkv * DH);
+        if (KIND == FP4) {
+            // (the row of the first head, the others a page of rows apart)
+            const int lp = P.rows.log2_page;
+            s_cache[threadIdx.x] =
+                slot < 0 ? -1 : ((slot >> lp) * P.hkv << lp) + (slot & ((1 << lp) - 1));
+        } else {
+            s_cache[threadIdx.x] = slot < 0 ? -1 : slot * (P.hkv * DH);
+        }
     }
-    const float kinv = E4M3 ? 1.f / *P.kscale : 1.f, vinv = E4M3 ? 1.f / *P.vscale : 1.f;
+    const float kinv = KIND != F16 ? 1.f / *P.kscale : 1.f;
+    const float vinv = KIND != F16 ? 1.f / *P.vscale : 1.f;
     __syncthreads();
     if (P.pairs) {
         for (int i = threadIdx.x; i < nt * P.pairs; i += WRITE_THREADS) {
@@ -297,11 +337,45 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
         void* const cache = p.kind == 1 ? P.kcache : P.vcache;
         const float f = p.kind == 1 ? kinv : vinv;
         const Pair ff = pack(f, f);
+        if constexpr (KIND == FP4) {
+            // A block of 16 is four runs of up to four lanes, which meet in shared memory.
+            __syncwarp(mates);
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i][k] = mul2(x[i][k], ff);
+                s_most[group][i][run0 / 4] = max4_abs(x[i][0], x[i][1]);
+                s_most[group][i][run1 / 4] = max4_abs(x[i][2], x[i][3]);
+            }
+            __syncwarp(mates);
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i) {
+                if (i >= nt || s_cache[i] < 0) continue;
+                uint8_t* row = static_cast<uint8_t*>(cache) +
+                               (s_cache[i] + ((long long)p.in_kind << P.rows.log2_page)) *
+                                   fp4::row_bytes(DH);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int run = k ? run1 : run0;
+                    const float4 m =
+                        *reinterpret_cast<const float4*>(&s_most[group][i][run / 16 * 4]);
+                    const float most = max4_abs(m.x, m.y, m.z, m.w);
+                    const __nv_fp8_storage_t code =
+                        __nv_cvt_float_to_fp8(most / 6.f, __NV_SATFINITE, __NV_E4M3);
+                    const __half_raw hr = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
+                    const float s = __half2float(*reinterpret_cast<const __half*>(&hr));
+                    *reinterpret_cast<uint16_t*>(row + run / 2) =
+                        (uint16_t)to_e2m1x4(x[i][2 * k], x[i][2 * k + 1], s);
+                    if (run % 16 == 0) row[DH / 2 + run / 16] = code;
+                }
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < UNIT; ++i) {
             if (i >= nt || s_cache[i] < 0) continue;
             const long long at = s_cache[i] + p.in_kind * DH;
-            if (E4M3) {
+            if (KIND == E4M3) {
                 uint8_t* to = static_cast<uint8_t*>(cache) + at;
                 *reinterpret_cast<uint32_t*>(to + run0) =
                     to_e4m3x2(mul2(x[i][0], ff)) | to_e4m3x2(mul2(x[i][1], ff)) << 16;
@@ -397,6 +471,72 @@ __global__ void __launch_bounds__(THREADS) read_kernel(const ReadParams P) {
     }
 }
 
+// Dense fp16 rows of a 4-bit cache: 8 codes a thread, with their block's scale.  code
+// * scale is exact, its product with the tensor's scale rounded to 32 bits, then to
+// fp16.
+template <int DH>
+__global__ void __launch_bounds__(THREADS) read_fp4_kernel(const ReadParams P) {
+    constexpr int A_HEAD = DH / 8;      // pieces of one head's row
+    __shared__ int s_starts[kRowsMaxBatch + 1];
+    __shared__ int s_pos[MAX_READ_TILE];
+    __shared__ long long s_row[MAX_READ_TILE];   // the row of the first head, -1: none
+    const int t0 = blockIdx.x * P.tile;
+    const int nt = min(P.tile, P.rows.tokens - t0);
+    if (P.rows.row_starts) {
+        load_row_starts(P.rows, s_starts);
+        __syncthreads();
+    }
+    if (threadIdx.x < nt) {
+        long long slot;
+        locate_row(P.rows, s_starts, t0 + threadIdx.x, &s_pos[threadIdx.x], &slot);
+        const int lp = P.rows.log2_page, heads = P.chunks.d / A_HEAD;
+        s_row[threadIdx.x] = slot < 0 ? -1 : ((slot >> lp) * heads << lp) + (slot & ((1 << lp) - 1));
+    }
+    const float scale[2] = {*P.scale[0], *P.scale[1]};
+    __syncthreads();
+    const int n = nt * P.chunks.d;
+    for (int i0 = threadIdx.x; i0 < n; i0 += READ_AHEAD * THREADS) {
+        uint32_t in[READ_AHEAD][2];
+        uint8_t unit[READ_AHEAD][2];
+#pragma unroll
+        for (int u = 0; u < READ_AHEAD; ++u) {
+            const int i = i0 + u * THREADS;
+            in[u][0] = in[u][1] = unit[u][0] = unit[u][1] = 0;
+            if (i >= n) continue;
+            const int t = P.chunks.div(i), piece = i - t * P.chunks.d;
+            if (s_row[t] < 0) continue;
+            const int head = piece / A_HEAD, c = piece % A_HEAD;
+            const long long at =
+                (s_row[t] + ((long long)head << P.rows.log2_page)) * fp4::row_bytes(DH);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                in[u][kv] = *reinterpret_cast<const uint32_t*>(P.cache[kv] + at + c * 4);
+                unit[u][kv] = P.cache[kv][at + DH / 2 + c / 2];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < READ_AHEAD; ++u) {
+            const int i = i0 + u * THREADS;
+            if (i >= n) break;
+            if (s_pos[P.chunks.div(i)] < 0) continue;
+            const long long to = ((long long)t0 * P.chunks.d + i) * 16;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                uint32_t h[4];
+                fp4::decode8(in[u][kv], h);
+                const uint32_t s = fp4::scales2(unit[u][kv] * 0x101u);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t e = fp4::mul2(h[k], s);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&e));
+                    h[k] = pack_half2(f.x * scale[kv], f.y * scale[kv]);
+                }
+                *reinterpret_cast<uint4*>(P.out[kv] + to) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+    }
+}
+
 struct IndexParams {
     RowMap rows;
     const uint8_t* kcache;
@@ -440,12 +580,6 @@ __device__ __forceinline__ float sum4(uint16_t a, uint16_t b, uint16_t c, uint16
     if (E4M3) return add_half(d, add_half(c, add_half(b, __half2float(__ushort_as_half(a)))));
     return __fadd_rn(add_half(b, __half2float(__ushort_as_half(a))),
                      add_half(d, __half2float(__ushort_as_half(c))));
-}
-// The largest magnitude; NaN if there is one.
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // Summaries of the 4-token blocks whose last token is a row of this step.  A
@@ -563,15 +697,20 @@ RowMap make_rows(const CacheRows& r, const DeviceInfo* di) {
     return m;
 }
 
-template <int DH, bool E4M3>
-void launch_write(const WriteParams& P, bool bf16, dim3 grid, cudaStream_t stream) {
-    if (bf16) write_kernel<DH, E4M3, true><<<grid, WRITE_THREADS, 0, stream>>>(P);
-    else write_kernel<DH, E4M3, false><<<grid, WRITE_THREADS, 0, stream>>>(P);
+template <Cache KIND>
+void launch_write(const WriteParams& P, int D, bool bf16, dim3 grid, cudaStream_t stream) {
+    if (D == 256) {
+        if (bf16) write_kernel<256, KIND, true><<<grid, WRITE_THREADS, 0, stream>>>(P);
+        else write_kernel<256, KIND, false><<<grid, WRITE_THREADS, 0, stream>>>(P);
+    } else {
+        if (bf16) write_kernel<128, KIND, true><<<grid, WRITE_THREADS, 0, stream>>>(P);
+        else write_kernel<128, KIND, false><<<grid, WRITE_THREADS, 0, stream>>>(P);
+    }
 }
 
 }  // namespace cacheops
 
-int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e4m3,
+int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, int cache_bits,
                        cudaStream_t stream) {
     using namespace cacheops;
     const DeviceInfo* di = device_info();
@@ -613,13 +752,9 @@ int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e
     if (shares > resident / tiles) shares = resident / tiles > 0 ? resident / tiles : 1;
     const dim3 grid(tiles, (unsigned)shares);
     const bool bf16 = a.dtype == GQA_DTYPE_BF16;
-    if (e4m3) {
-        if (a.D == 256) launch_write<256, true>(P, bf16, grid, stream);
-        else launch_write<128, true>(P, bf16, grid, stream);
-    } else {
-        if (a.D == 256) launch_write<256, false>(P, bf16, grid, stream);
-        else launch_write<128, false>(P, bf16, grid, stream);
-    }
+    if (cache_bits == 4) launch_write<FP4>(P, a.D, bf16, grid, stream);
+    else if (cache_bits == 8) launch_write<E4M3>(P, a.D, bf16, grid, stream);
+    else launch_write<F16>(P, a.D, bf16, grid, stream);
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
@@ -646,6 +781,29 @@ int cache_read_launch(const CacheRows& r, const void* kcache, const void* vcache
     const int grid = (r.tokens + P.tile - 1) / P.tile;
     if (kscale) read_kernel<true><<<grid, THREADS, 0, stream>>>(P);
     else read_kernel<false><<<grid, THREADS, 0, stream>>>(P);
+    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+int cache_read_fp4_launch(const CacheRows& r, const void* kcache, const void* vcache,
+                          const float* kscale, const float* vscale, int Hkv, int D, void* k_out,
+                          void* v_out, cudaStream_t stream) {
+    using namespace cacheops;
+    const DeviceInfo* di = device_info();
+    if (!di) return GQA_ERR_CUDA;
+    ReadParams P;
+    P.rows = make_rows(r, di);
+    P.cache[0] = static_cast<const uint8_t*>(kcache);
+    P.cache[1] = static_cast<const uint8_t*>(vcache);
+    P.scale[0] = kscale;
+    P.scale[1] = vscale;
+    P.out[0] = static_cast<uint8_t*>(k_out);
+    P.out[1] = static_cast<uint8_t*>(v_out);
+    P.row_bytes = fp4::row_bytes(D);
+    P.chunks = make_fastdiv(Hkv * D / 8);
+    P.tile = r.tokens <= 2048 ? 8 : 32;
+    const int grid = (r.tokens - 1) / P.tile + 1;
+    if (D == 256) read_fp4_kernel<256><<<grid, THREADS, 0, stream>>>(P);
+    else read_fp4_kernel<128><<<grid, THREADS, 0, stream>>>(P);
     return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 

@@ -129,6 +129,14 @@ int paged_e4m3_noalloc_launch(const void* q, const uint8_t* kcache, const uint8_
                               int R, int Hq, int Hkv, int Dh, float scale, void* out,
                               cudaStream_t stream);
 
+// Tails over a 4-bit cache, one sequence or several, with a window (0: none).
+int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                     const float* kscale, const float* vscale, const int32_t* block_tables,
+                     int table_stride, int num_pages, int page, const int* ctx_lens_dev,
+                     int max_ctx_len, int batch, int R, int Hq, int Hkv, int Dh, float scale,
+                     int window, int sinks, void* out, cudaStream_t stream);
+size_t paged_fp4_workspace_bytes(int nq, int num_sms, int Dh);
+
 // kcache / vcache: fp16 elements, or E4M3 codes with kscale / vscale (device
 // pointers to one fp32 each) when e4m3 is set.
 int sparse_launch(const void* q, const void* kcache, const void* vcache, const float* kscale,
@@ -146,14 +154,19 @@ struct CacheRows {
     int table_stride, num_pages, page, max_ctx_len, batch, tokens;
 };
 
-// e4m3: the caches hold codes (a.kscale, a.vscale), else fp16.
-int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, bool e4m3,
+// cache_bits: 8, E4M3 codes (a.kscale, a.vscale); 4, E2M1 codes with E4M3 scales
+// (the same, rows as in fp4_rows.cuh); 16, fp16.
+int cache_write_launch(const CacheRows& r, const gqa_cache_write_args& a, int cache_bits,
                        cudaStream_t stream);
 // kscale / vscale: null to copy the cached rows as they are (row_bytes of K
 // and V per token), else E4M3 codes to fp16.
 int cache_read_launch(const CacheRows& r, const void* kcache, const void* vcache,
                       const float* kscale, const float* vscale, int row_bytes, void* k_out,
                       void* v_out, cudaStream_t stream);
+// The same of a 4-bit cache.
+int cache_read_fp4_launch(const CacheRows& r, const void* kcache, const void* vcache,
+                          const float* kscale, const float* vscale, int Hkv, int D, void* k_out,
+                          void* v_out, cudaStream_t stream);
 // kscale: null for an fp16 cache.  width = Hkv * D.
 int block_index_launch(const CacheRows& r, const void* kcache, const float* kscale, int width,
                        int8_t* index, float* index_scale, cudaStream_t stream);
