@@ -108,6 +108,21 @@ int gqa_attn_prefill_e4m3(const void* q, const uint8_t* k, const uint8_t* v, con
                           const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int D,
                           float scale, struct CUstream_st* stream);
 
+/* The two prefills with a sliding window and first tokens that stay visible
+ * ("sinks"): the row at position p = KV - Q + i sees the keys j <= p with
+ * j > p - window or j < sinks; window >= 1, sinks >= 0.  Same arguments, layouts and
+ * workspace as without; a window of KV or more hides nothing and gives the other entry
+ * point's result.  Only tiles that some row of a pair tile sees are visited.  Keys that
+ * no row of the call sees (from `sinks` to KV - Q - window) are not read at all; K and V
+ * of the others have to be finite, also for the rows that do not see them. */
+int gqa_attn_prefill_window(const void* q, const void* k, const void* v, void* out, int Q, int KV,
+                            int Hq, int Hkv, int D, float scale, int window, int sinks,
+                            struct CUstream_st* stream);
+int gqa_attn_prefill_e4m3_window(const void* q, const uint8_t* k, const uint8_t* v,
+                                 const float* kscale, const float* vscale, void* out, int Q,
+                                 int KV, int Hq, int Hkv, int D, float scale, int window,
+                                 int sinks, struct CUstream_st* stream);
+
 /* Paged FP8-E4M3 verifier tail [P2, What / Changes].
  *   q            [query_rows, Hq, D] fp16, 1 <= query_rows, query_rows * Hq / Hkv
  *                <= 48 (one launch per KV head packs its query heads x rows;
@@ -174,6 +189,22 @@ int gqa_attn_paged_e4m3_batch(const void* q, const uint8_t* kcache, const uint8_
                               int page, const int32_t* ctx_lens_dev, int max_ctx_len, int batch,
                               int query_rows, int Hq, int Hkv, int D, float scale, void* out,
                               struct CUstream_st* stream);
+
+/* The batched tails with a sliding window and first tokens that stay visible
+ * ("sinks"): the row at position p sees the keys j <= p with j > p - window or
+ * j < sinks; window >= 1, sinks >= 0.  Arguments, layouts and workspace of
+ * gqa_attn_paged_e4m3_batch, any batch from 1 on, except: a context length may be
+ * anything from 0 to max_ctx_len (others are clamped and flag
+ * GQA_DEVERR_BAD_CTX_LEN), and a row that sees no key (a context shorter than
+ * query_rows, or of no tokens) gets zeros.  Only tiles that some row sees are read
+ * (table entries of other pages need not be valid), and keys that no row of a sequence
+ * sees may hold any byte; one that a row sees must not be the E4M3 NaN code. */
+int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                               const float* kscale, const float* vscale,
+                               const int32_t* block_tables, int table_stride, int num_pages,
+                               int page, const int32_t* ctx_lens_dev, int max_ctx_len, int batch,
+                               int query_rows, int Hq, int Hkv, int D, float scale, int window,
+                               int sinks, void* out, struct CUstream_st* stream);
 
 /* Paged FP8-E4M3 verifier tail that allocates nothing (no counterpart in the
  * pages; an addition of this library).  Some callers cannot call cudaMalloc:

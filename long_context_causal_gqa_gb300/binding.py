@@ -53,6 +53,8 @@ EXPORTED = ("gqa_attn_prefill", "gqa_attn_prefill_e4m3", "gqa_attn_paged_e4m3", 
             "gqa_cache_write_e4m3", "gqa_cache_write", "gqa_cache_read_e4m3", "gqa_cache_read",
             "gqa_block_index_e4m3", "gqa_block_index", "gqa_select_blocks",
             "gqa_cache_write_fp4", "gqa_cache_read_fp4", "gqa_attn_paged_fp4",
+            "gqa_attn_paged_e4m3_window", "gqa_attn_prefill_window",
+            "gqa_attn_prefill_e4m3_window",
             "gqa_workspace_bytes", "gqa_set_workspace", "gqa_get_device_error",
             "gqa_check_wait_limit", "gqa_prefill_sm_pairs", "gqa_status_string")
 
@@ -110,6 +112,13 @@ def load():
             lib.gqa_attn_paged_fp4.argtypes = [P, P, P, P, P, P, I, I, I, P, I, I, I, I, I, I, F,
                                                I, I, P, P]
             lib.gqa_attn_paged_fp4.restype = I
+            lib.gqa_attn_paged_e4m3_window.argtypes = lib.gqa_attn_paged_fp4.argtypes
+            lib.gqa_attn_paged_e4m3_window.restype = I
+            lib.gqa_attn_prefill_window.argtypes = [P, P, P, P, I, I, I, I, I, F, I, I, P]
+            lib.gqa_attn_prefill_window.restype = I
+            lib.gqa_attn_prefill_e4m3_window.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, I, I,
+                                                         P]
+            lib.gqa_attn_prefill_e4m3_window.restype = I
             lib.gqa_cache_read.argtypes = [P, P, I, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
             lib.gqa_cache_read.restype = I
             lib.gqa_block_index_e4m3.argtypes = [P, P, P, I, I, I, P, P, I, I, I, I, I, P, P, P]
@@ -723,6 +732,59 @@ def paged_fp4(q, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max
     kp, vp, pages = _fp4_pages(kcache, vcache, idx)
     return _tails(lib.gqa_attn_paged_fp4, KIND_PAGED_FP4, q, idx, pages, (kp, vp), kscale, vscale,
                   block_tables, ctx_lens_dev, max_ctx_len, scale, window, sinks, out, stream)
+
+
+def paged_e4m3_window(q, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len,
+                      window, sinks=0, scale=1.0 / 16, out=None, stream=None):
+    """paged_e4m3_batch with a sliding window (gqa_attn_paged_e4m3_window): a row sees its
+    last `window` positions (its own among them) and the first `sinks` tokens; contexts
+    may be shorter than the rows, whose places in front of the first token give zeros."""
+    lib = load() if _lib is None else _lib
+    idx = _device_of(q)
+    kp, vp, pages = _pages(kcache, vcache, torch.uint8, idx)
+    return _tails(lib.gqa_attn_paged_e4m3_window, KIND_PAGED_E4M3_BATCH, q, idx, pages, (kp, vp),
+                  kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len, scale, window, sinks,
+                  out, stream)
+
+
+def _prefill_window(fn, q, k, v, scales, scale, window, sinks, out, stream):
+    idx = _device_of(q)
+    dtype = torch.uint8 if scales else torch.float16
+    qp, kp, vp = _want("q", q, torch.float16, idx, 3), _want("k", k, dtype, idx, 3), \
+        _want("v", v, dtype, idx, 3)
+    Q, Hq, D = q.shape
+    KV, Hkv, d = k.shape
+    if v.shape != k.shape or d != D:
+        _refuse("k and v must have the same shape, and q's head size")
+    if out is None:
+        out = _empty(q.shape, torch.float16, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _want("out", out, torch.float16, idx, 3)
+        if out.shape != q.shape:
+            _refuse("out must have q's shape")
+    scales = [_scale("kscale" if i == 0 else "vscale", x, idx) for i, x in enumerate(scales)]
+    args = (qp, kp, vp, *scales, op, Q, KV, Hq, Hkv, D, scale, window, sinks)
+    _call_with_workspace(fn, idx, stream, args, KIND_PREFILL, Q, KV, Hq, D)
+    return out
+
+
+def prefill_window(q, k, v, window, sinks=0, scale=1.0 / 16, out=None, stream=None):
+    """Dense causal prefill with a sliding window (gqa_attn_prefill_window): q [Q,Hq,D],
+    k/v [KV,Hkv,D] fp16.  A row sees its last `window` positions (its own among them)
+    and the first `sinks` tokens."""
+    lib = load() if _lib is None else _lib
+    return _prefill_window(lib.gqa_attn_prefill_window, q, k, v, (), scale, window, sinks, out,
+                           stream)
+
+
+def prefill_e4m3_window(q, k, v, kscale, vscale, window, sinks=0, scale=1.0 / 16, out=None,
+                        stream=None):
+    """prefill_window over an E4M3 K/V cache: k/v [KV,Hkv,D] uint8 codes, kscale/vscale
+    one-element fp32 CUDA tensors."""
+    lib = load() if _lib is None else _lib
+    return _prefill_window(lib.gqa_attn_prefill_e4m3_window, q, k, v, (kscale, vscale), scale,
+                           window, sinks, out, stream)
 
 
 def _index_pointers(index, index_scale, idx):

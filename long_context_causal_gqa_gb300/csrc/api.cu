@@ -279,6 +279,21 @@ int index_common(const CacheRows& r, const void* kcache, const float* kscale, in
     return block_index_launch(r, kcache, kscale, Hkv * D, index, index_scale, stream);
 }
 
+int prefill_common(const void* q, const void* k, const void* v, const float* kscale,
+                   const float* vscale, bool e4m3, void* out, int Q, int KV, int Hq, int Hkv,
+                   int D, float scale, int window, int sinks, cudaStream_t stream) {
+    if (!q || !k || !v || !out) return GQA_ERR_INVALID_ARG;
+    if (e4m3 && (!kscale || !vscale || !aligned4(kscale) || !aligned4(vscale)))
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+        return GQA_ERR_INVALID_ARG;
+    if (Q < 1 || KV < 1 || Q > KV || !scale_ok(scale)) return GQA_ERR_INVALID_ARG;
+    if (!family_ok(Hq, Hkv, D)) return GQA_ERR_UNSUPPORTED;
+    if ((long long)Q * Hq > 0x7fffffffLL - 256) return GQA_ERR_INVALID_ARG;
+    return prefill_launch(q, k, v, kscale, vscale, out, Q, KV, Hq, Hkv, D, scale, window, sinks,
+                          stream);
+}
+
 // What the tails of a batch with a window, or over a 4-bit cache, check.
 int batch_check(const void* q, const void* kcache, const void* vcache, const float* kscale,
                 const float* vscale, const int32_t* block_tables, int table_stride,
@@ -308,27 +323,32 @@ extern "C" {
 
 int gqa_attn_prefill(const void* q, const void* k, const void* v, void* out, int Q, int KV,
                      int Hq, int Hkv, int D, float scale, struct CUstream_st* stream) {
-    if (!q || !k || !v || !out) return GQA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
-        return GQA_ERR_INVALID_ARG;
-    if (Q < 1 || KV < 1 || Q > KV || !scale_ok(scale)) return GQA_ERR_INVALID_ARG;
-    if (!family_ok(Hq, Hkv, D)) return GQA_ERR_UNSUPPORTED;
-    if ((long long)Q * Hq > 0x7fffffffLL - 256) return GQA_ERR_INVALID_ARG;
-    return prefill_launch(q, k, v, nullptr, nullptr, out, Q, KV, Hq, Hkv, D, scale, stream);
+    return prefill_common(q, k, v, nullptr, nullptr, false, out, Q, KV, Hq, Hkv, D, scale, 0, 0,
+                          stream);
 }
 
 int gqa_attn_prefill_e4m3(const void* q, const uint8_t* k, const uint8_t* v, const float* kscale,
                           const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int D,
                           float scale, struct CUstream_st* stream) {
-    if (!q || !k || !v || !kscale || !vscale || !out) return GQA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
-        return GQA_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(kscale) | reinterpret_cast<uintptr_t>(vscale)) & 3u)
-        return GQA_ERR_INVALID_ARG;
-    if (Q < 1 || KV < 1 || Q > KV || !scale_ok(scale)) return GQA_ERR_INVALID_ARG;
-    if (!family_ok(Hq, Hkv, D)) return GQA_ERR_UNSUPPORTED;
-    if ((long long)Q * Hq > 0x7fffffffLL - 256) return GQA_ERR_INVALID_ARG;
-    return prefill_launch(q, k, v, kscale, vscale, out, Q, KV, Hq, Hkv, D, scale, stream);
+    return prefill_common(q, k, v, kscale, vscale, true, out, Q, KV, Hq, Hkv, D, scale, 0, 0,
+                          stream);
+}
+
+int gqa_attn_prefill_window(const void* q, const void* k, const void* v, void* out, int Q, int KV,
+                            int Hq, int Hkv, int D, float scale, int window, int sinks,
+                            struct CUstream_st* stream) {
+    if (window < 1 || sinks < 0) return GQA_ERR_INVALID_ARG;
+    return prefill_common(q, k, v, nullptr, nullptr, false, out, Q, KV, Hq, Hkv, D, scale, window,
+                          sinks, stream);
+}
+
+int gqa_attn_prefill_e4m3_window(const void* q, const uint8_t* k, const uint8_t* v,
+                                 const float* kscale, const float* vscale, void* out, int Q,
+                                 int KV, int Hq, int Hkv, int D, float scale, int window,
+                                 int sinks, struct CUstream_st* stream) {
+    if (window < 1 || sinks < 0) return GQA_ERR_INVALID_ARG;
+    return prefill_common(q, k, v, kscale, vscale, true, out, Q, KV, Hq, Hkv, D, scale, window,
+                          sinks, stream);
 }
 
 int gqa_attn_paged_e4m3(const void* q, const uint8_t* kcache, const uint8_t* vcache,
@@ -373,7 +393,25 @@ int gqa_attn_paged_e4m3_batch(const void* q, const uint8_t* kcache, const uint8_
     if ((long long)table_stride * page < (long long)max_ctx_len) return GQA_ERR_INVALID_ARG;
     return paged_e4m3_batch_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
                                    num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows,
-                                   Hq, Hkv, D, scale, out, stream);
+                                   Hq, Hkv, D, scale, 0, 0, out, stream);
+}
+
+int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                               const float* kscale, const float* vscale,
+                               const int32_t* block_tables, int table_stride, int num_pages,
+                               int page, const int32_t* ctx_lens_dev, int max_ctx_len, int batch,
+                               int query_rows, int Hq, int Hkv, int D, float scale, int window,
+                               int sinks, void* out, struct CUstream_st* stream) {
+    const int rc = batch_check(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                               num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq,
+                               Hkv, D, scale, out);
+    if (rc != GQA_OK) return rc;
+    if (window < 1 || sinks < 0) return GQA_ERR_INVALID_ARG;
+    // (beyond the longest context both mean all of it)
+    return paged_e4m3_batch_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                                   num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows,
+                                   Hq, Hkv, D, scale, window < max_ctx_len ? window : max_ctx_len,
+                                   sinks < max_ctx_len ? sinks : max_ctx_len, out, stream);
 }
 
 int gqa_attn_paged_e4m3_devctx(const void* q, const uint8_t* kcache, const uint8_t* vcache,

@@ -99,12 +99,13 @@ int ensure_smem_limit(const void* kernel, int bytes);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Launchers (one per kernel family).  Arguments are validated by the caller.
-// Dh: head size, 256 or 128.
+// Dh: head size, 256 or 128.  window: 0 for none; sinks: first tokens that stay
+// visible with one.
 // kscale / vscale: null for fp16 k / v; device pointers to one fp32 each when
 // k / v hold E4M3 codes.
 int prefill_launch(const void* q, const void* k, const void* v, const float* kscale,
                    const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int Dh,
-                   float scale, cudaStream_t stream);
+                   float scale, int window, int sinks, cudaStream_t stream);
 size_t prefill_workspace_bytes(int Q, int KV, int num_sms);
 int prefill_resident_pairs();   // co-resident two-CTA clusters of the prefill kernel
 
@@ -118,8 +119,8 @@ int paged_e4m3_batch_launch(const void* q, const uint8_t* kcache, const uint8_t*
                             const float* kscale, const float* vscale,
                             const int32_t* block_tables, int table_stride, int num_pages,
                             int page, const int* ctx_lens_dev, int max_ctx_len, int batch,
-                            int R, int Hq, int Hkv, int Dh, float scale, void* out,
-                            cudaStream_t stream);
+                            int R, int Hq, int Hkv, int Dh, float scale, int window, int sinks,
+                            void* out, cudaStream_t stream);
 size_t paged_e4m3_batch_workspace_bytes(int nq, int batch, int num_sms, int Dh);
 
 // Same as paged_e4m3_launch, with the split partials in a static device array.

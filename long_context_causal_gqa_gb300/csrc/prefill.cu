@@ -148,6 +148,8 @@ struct Params {
     float* ws_o;          // [G][2][BM2][DH] unnormalised partial O
     float* ws_ml;         // [G][2][BM2][2] partial (m in log2 units, l)
     unsigned* err;
+    // Windowed kernels only (see WinTiles).
+    int window, sinks, base;
 };
 
 // KV tiles pair tile t needs: up to the last visible key of its last valid row.
@@ -155,6 +157,43 @@ __host__ __device__ inline int kv_tiles(int t, int Q, int KV, int M_total, const
     int last = min(t * BM2 + BM2 - 1, M_total - 1);
     return (KV - Q + grp.div(last)) / BN + 1;
 }
+
+// The tiles pair tile t needs with a window: the row at position p sees the keys
+// j <= p with j > p - window or j < sinks.  Its tiles are first the sinks', from
+// key 0 on, then those of its rows' windows, on a grid that begins at `base`: the
+// first key that any row's window reaches, so that keys no row sees are never read
+// (or 0, where the sinks reach that far, and then the sinks' tiles end where the
+// window's begin).
+struct WinTiles {
+    int sink;    // tiles of sinks
+    int first;   // the window's first tile on its grid
+    int n;       // tiles in all
+    __host__ __device__ int key(int j, int base) const {
+        return j < sink ? j * BN : base + (first + j - sink) * BN;
+    }
+};
+__host__ __device__ inline WinTiles win_tiles(const Params& P, int t) {
+    const int lo = P.KV - P.Q + P.grp.div(t * BM2) + 1;   // (past the first row's own key)
+    const int last = P.KV - P.Q + P.grp.div(min(t * BM2 + BM2 - 1, P.M_total - 1));
+    WinTiles w;
+    w.first = lo > P.window ? (lo - P.window - P.base) / BN : 0;
+    w.sink = (P.sinks + BN - 1) / BN;
+    if (P.base == 0 && w.sink > w.first) w.sink = w.first;
+    w.n = w.sink + (last - P.base) / BN + 1 - w.first;
+    return w;
+}
+template <bool WIN>
+__host__ __device__ inline int tiles_of(const Params& P, int t) {
+    if constexpr (WIN) return win_tiles(P, t).n;
+    else return kv_tiles(t, P.Q, P.KV, P.M_total, P.grp);
+}
+// Maps of the sinks alone (rows past them are zeros).
+template <bool WIN>
+struct SinkMaps {
+    CUtensorMap k, v;
+};
+template <>
+struct SinkMaps<false> {};
 
 __host__ __device__ inline long long pair_begin(long long total, int G, int c) {
     return (long long)c * total / G;
@@ -164,7 +203,7 @@ __host__ __device__ inline long long pair_begin(long long total, int G, int c) {
 // The tile space is heads x num_ptiles pair tiles, head-major; t is the index
 // in it, (hd, lt) its head and pair tile within the head.  With MH false the
 // tile space is one head (packed rows) and hd stays 0.
-template <bool MH>
+template <bool MH, bool WIN>
 struct SegIter {
     long long pos, end, cum;
     int t, hd, lt;
@@ -187,7 +226,7 @@ struct SegIter {
         first = true;
         const int tiles = MH ? P.heads * P.num_ptiles : P.num_ptiles;
         while (t < tiles) {
-            int n = kv_tiles(lt, P.Q, P.KV, P.M_total, P.grp);
+            int n = tiles_of<WIN>(P, lt);
             if (cum + n > pos) break;
             cum += n;
             advance(P);
@@ -198,7 +237,7 @@ struct SegIter {
     __device__ bool next(const Params& P, int& pt, int& head, int& jb, int& je, int& n,
                          bool& is_first) {
         if (pos >= end) return false;
-        n = kv_tiles(lt, P.Q, P.KV, P.M_total, P.grp);
+        n = tiles_of<WIN>(P, lt);
         pt = lt;
         head = hd;
         jb = (int)(pos - cum);
@@ -426,11 +465,13 @@ __device__ __forceinline__ void e4m3x16_f16(const uint4& c, uint4& lo, uint4& hi
 // 3-D maps); otherwise one range of packed rows (2-D maps).  DH: head size,
 // 256 or 128.  F8: K and V are E4M3 codes (read through P.k8 / P.v8; tm_k
 // and tm_v are unused), converted to fp16 in shared memory by four extra
-// warps.
-template <bool MH, int DH, bool F8>
+// warps.  WIN: a sliding window and sinks; the same pipeline over the tiles that
+// win_tiles() names, with two edges to mask.
+template <bool MH, int DH, bool F8, bool WIN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<F8, DH>::NTHREADS, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const Params P) {
+               const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ SinkMaps<WIN> tm_sink, const Params P) {
     static_assert(DH == 256 || DH == 128, "head size");
     constexpr int SLOTS = DH / 128;                 // ring slots per tile, K and V each
     constexpr int QCH = DH / 64;                    // 64-wide chunks of a Q / K row
@@ -503,7 +544,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // The merge kernel may be scheduled now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;");
 
-    SegIter<MH> it;
+    SegIter<MH, WIN> it;
     it.init(P, pair);
     int pt, hd, jb, je, n;
     bool is_first;
@@ -522,6 +563,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             bool ok = true;
             while (ok && it.next(P, pt, hd, jb, je, n, is_first)) {
                 const int kvh = MH ? hd / P.head_group : 0;   // KV head of this segment
+                WinTiles wt{};
+                if constexpr (WIN) wt = win_tiles(P, pt);
                 if (kq) {
                     if (!mbar_wait(BR.qempty(), (seg & 1) ^ 1, abort_flag, P.err)) {
                         ok = false;
@@ -548,22 +591,31 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t fb = BR.full(slot0);
                     if (leader) mbar_arrive_expect_tx(fb, 2 * SLOTS * SLOT_BYTES);
                     const uint32_t fbl = leader_addr(fb);
+                    int key0 = j * BN;
+                    const CUtensorMap *map_k = &tm_k, *map_v = &tm_v;
+                    if constexpr (WIN) {
+                        key0 = wt.key(j, P.base);
+                        if (j < wt.sink) {
+                            map_k = &tm_sink.k;
+                            map_v = &tm_sink.v;
+                        }
+                    }
                     for (int h = 0; h < SLOTS; ++h) {
                         const uint32_t dst = s_ring + (slot0 + h) * SLOT_BYTES;
                         if (kq) {
                             // K: d chunks 2h, 2h + 1 of this CTA's 64 keys
                             for (int cc = 0; cc < 2; ++cc)
-                                tma_load_pair<MH>(dst + cc * HALF_SLOT, &tm_k, fbl,
+                                tma_load_pair<MH>(dst + cc * HALF_SLOT, map_k, fbl,
                                                   (2 * h + cc) * 64, kvh,
-                                                  j * BN + 64 * (int)rank);
+                                                  key0 + 64 * (int)rank);
                         } else {
                             // V: sub-tiles SUBS h .. SUBS h + SUBS - 1 (32 keys)
                             // x this CTA's DH / 2 d
                             for (int ss = 0; ss < SUBS; ++ss)
                                 for (int a = 0; a < VATOMS; ++a)
-                                    tma_load_pair<MH>(dst + ss * SUB_BYTES + a * 4096, &tm_v,
+                                    tma_load_pair<MH>(dst + ss * SUB_BYTES + a * 4096, map_v,
                                                       fbl, (DH / 2) * (int)rank + 64 * a, kvh,
-                                                      j * BN + (SUBS * h + ss) * 32);
+                                                      key0 + (SUBS * h + ss) * 32);
                         }
                     }
                     ++t;
@@ -613,18 +665,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool ok = true;
         while (ok && it.next(P, pt, hd, jb, je, n, is_first)) {
             const int kvh = MH ? hd / P.head_group : 0;
+            WinTiles wt{};
+            if constexpr (WIN) wt = win_tiles(P, pt);
             for (int j = jb; ok && j < je; ++j) {
+                int tile0 = j * BN, limit = P.KV;   // keys from `limit` on are zeros
+                if constexpr (WIN) {
+                    tile0 = wt.key(j, P.base);
+                    if (j < wt.sink && P.base > 0) limit = P.sinks;
+                }
                 uint4 code[SLOTS][PASSES];
 #pragma unroll
                 for (int h = 0; h < SLOTS; ++h) {
                     // K slot h: this CTA's keys j BN + 64 rank + r, d 128 h ..; V slot h:
                     // keys j BN + h (BN / SLOTS) + r, this CTA's d (DH / 2) rank ..
-                    const int key0 = kc ? j * BN + 64 * (int)rank : j * BN + h * (BN / SLOTS);
+                    const int key0 = kc ? tile0 + 64 * (int)rank : tile0 + h * (BN / SLOTS);
                     const int d0 = (kc ? 128 * h : (DH / 2) * (int)rank) + 16 * c;
 #pragma unroll
                     for (int i = 0; i < PASSES; ++i) {
                         const int key = key0 + rbase + i * rpi;
-                        code[h][i] = key < P.KV
+                        code[h][i] = key < limit
                                          ? __ldg(reinterpret_cast<const uint4*>(
                                                codes + (size_t)key * P.kv_rs + kvh * DH + d0))
                                          : make_uint4(0, 0, 0, 0);
@@ -841,7 +900,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int m_row = pt * BM2 + BM * (int)rank + row;
             const bool valid = m_row < P.M_total;
             const int lim = P.KV - P.Q + P.grp.div(m_row);      // last visible key
-            const int j_mask = (P.KV - P.Q + P.grp.div(pt * BM2 + BM * (int)rank) + 1) / BN;
+            const int first_lim = P.KV - P.Q + P.grp.div(pt * BM2 + BM * (int)rank);
+            const int j_mask = (first_lim + 1) / BN;
+            // WIN: the largest limit of this CTA's rows (those past the last row included).
+            WinTiles wt{};
+            int last_lim = 0;
+            if constexpr (WIN) {
+                wt = win_tiles(P, pt);
+                last_lim = P.KV - P.Q + P.grp.div(pt * BM2 + BM * (int)rank + BM - 1);
+            }
             float m_ref = -INFINITY;
             float l = 0.f;
             for (int j = jb; j < je; ++j) {
@@ -859,7 +926,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                               *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
                 tmem_ld_wait<COLS>(sr);
                 float* s = reinterpret_cast<float*>(sr);
-                if (j >= j_mask) {
+                if constexpr (WIN) {
+                    // Both edges: keys past the row's own, and keys in front of its
+                    // window that are no sinks (in a tile of sinks, all that are none).
+                    const int key0 = wt.key(j, P.base);
+                    const bool sink = j < wt.sink;
+                    if (key0 + BN - 1 > first_lim ||
+                        (key0 + BN - 1 >= P.sinks && (sink || key0 <= last_lim - P.window))) {
+                        const int k0 = key0 + COLS * hg;
+                        const int out = sink ? 0x7fffffff : lim - P.window;
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c)
+                            if (k0 + c > lim || (k0 + c <= out && k0 + c >= P.sinks))
+                                s[c] = -INFINITY;
+                    }
+                } else if (j >= j_mask) {
                     const int k0 = j * BN + COLS * hg;
 #pragma unroll
                     for (int c = 0; c < COLS; ++c)
@@ -1083,12 +1164,13 @@ prefill_merge_kernel(const Params P, const __grid_constant__ MergeTasks T) {
 }
 
 // Host side of the schedule: the cut pair tiles and their pieces.
+template <bool WIN>
 static void find_cut_tiles(const Params& P, MergeTasks& T) {
     T.n = 0;
     long long cum = 0;
     int c = 0;  // first pair whose range ends after cum
     for (int t = 0; t < P.heads * P.num_ptiles; ++t) {
-        const int n = kv_tiles(t % P.num_ptiles, P.Q, P.KV, P.M_total, P.grp);
+        const int n = tiles_of<WIN>(P, t % P.num_ptiles);
         const long long t_end = cum + n;
         // pair holding the tile's first iteration
         while (c + 1 < P.G && pair_begin(P.total, P.G, c + 1) <= cum) ++c;
@@ -1124,7 +1206,7 @@ static int max_pairs(int device) {
     int n = 0;
     // All instantiations use one CTA per SM (their shared memory allows no
     // second), so the fp16 kernel's count holds for all.
-    if (cudaOccupancyMaxActiveClusters(&n, prefill_kernel<false, 256, false>, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&n, prefill_kernel<false, 256, false, false>, &cfg) != cudaSuccess ||
         n < 1) {
         cudaGetLastError();
         return 0;
@@ -1135,14 +1217,16 @@ static int max_pairs(int device) {
 }
 
 // One main-kernel launch and, when pair tiles were cut, its merge.
-template <bool MH, int DH, bool F8>
+template <bool MH, int DH, bool F8, bool WIN>
 static int launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                      const Params& P, const MergeTasks& tasks, cudaStream_t stream) {
+                      const SinkMaps<WIN>& ts, const Params& P, const MergeTasks& tasks,
+                      cudaStream_t stream) {
     using C = Cfg<F8, DH>;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill_kernel<MH, DH, F8>),
+    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill_kernel<MH, DH, F8, WIN>),
                           C::SMEM_BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
-    prefill_kernel<MH, DH, F8><<<2 * P.G, C::NTHREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, P);
+    prefill_kernel<MH, DH, F8, WIN>
+        <<<2 * P.G, C::NTHREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, ts, P);
     if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
     if (tasks.n > 0) {
         cudaLaunchConfig_t cfg = {};
@@ -1166,7 +1250,7 @@ static int launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 int prefill_resident_pairs() {
     const DeviceInfo* di = device_info();
     if (!di) return -1;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill::prefill_kernel<false, 256, false>),
+    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill::prefill_kernel<false, 256, false, false>),
                           prefill::Cfg<false, 256>::SMEM_BYTES) != GQA_OK)
         return -1;
     return prefill::max_pairs(di->device);
@@ -1180,14 +1264,17 @@ size_t prefill_workspace_bytes(int Q, int KV, int num_sms) {
     return kWorkspaceCounterBytes + per_pair * pairs + 256;
 }
 
-int prefill_launch(const void* q, const void* k, const void* v, const float* kscale,
-                   const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int Dh,
-                   float scale, cudaStream_t stream) {
-    using namespace prefill;
+namespace prefill {
+
+// The launch of a call with a window (WIN; P.window, P.sinks and P.base set) or without.
+template <bool WIN>
+static int launch(const void* q, const void* k, const void* v, const float* kscale,
+                  const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int Dh,
+                  float scale, int window, int sinks, cudaStream_t stream) {
     const DeviceInfo* di = device_info();
     if (!di) return GQA_ERR_CUDA;
     const bool f8 = kscale != nullptr;   // K / V are E4M3 codes with device-side scales
-    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill_kernel<false, 256, false>),
+    if (ensure_smem_limit(reinterpret_cast<const void*>(prefill_kernel<false, 256, false, false>),
                           Cfg<false, 256>::SMEM_BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
     const int pairs_max = max_pairs(di->device);
@@ -1208,8 +1295,12 @@ int prefill_launch(const void* q, const void* k, const void* v, const float* ksc
     P.M_total = Q * grp;
     P.num_ptiles = (P.M_total + BM2 - 1) / BM2;
     P.ptiles = make_fastdiv(P.num_ptiles);
+    P.window = window;
+    P.sinks = sinks;
+    P.base = KV - Q + 1 > window ? KV - Q + 1 - window : 0;
+    if (sinks > P.base) P.base = 0;
     long long total = 0;
-    for (int t = 0; t < P.num_ptiles; ++t) total += kv_tiles(t, Q, KV, P.M_total, P.grp);
+    for (int t = 0; t < P.num_ptiles; ++t) total += tiles_of<WIN>(P, t);
     total *= P.heads;
     P.total = total;
     int G = pairs_max < di->num_sms / 2 ? pairs_max : di->num_sms / 2;
@@ -1238,36 +1329,62 @@ int prefill_launch(const void* q, const void* k, const void* v, const float* ksc
         P.ws_ml = nullptr;
     }
     MergeTasks tasks;  // passed to the merge kernel by value
-    find_cut_tiles(P, tasks);
+    find_cut_tiles<WIN>(P, tasks);
 
     // E4M3 K / V are read by the converter warps through P.k8 / P.v8; their
     // kernels take the Q map in the K / V map arguments, unused.
     CUtensorMap tq, tk, tv;
+    SinkMaps<WIN> ts;
+    // Keys of the sinks' maps: the sinks alone, or all where they reach the window.
+    const uint64_t sink_keys = P.base > 0 && sinks > 0 ? (uint64_t)sinks : (uint64_t)KV;
     if (packed) {
         if (!make_map_2d_f16(&tq, q, (uint64_t)P.M_total, Dh, Dh, BM, 64)) return GQA_ERR_CUDA;
         if (f8)
-            return Dh == 256 ? launch_one<false, 256, true>(tq, tq, tq, P, tasks, stream)
-                             : launch_one<false, 128, true>(tq, tq, tq, P, tasks, stream);
+            return Dh == 256 ? launch_one<false, 256, true, WIN>(tq, tq, tq, ts, P, tasks, stream)
+                             : launch_one<false, 128, true, WIN>(tq, tq, tq, ts, P, tasks, stream);
         if (!make_map_2d_f16(&tk, k, (uint64_t)KV, Dh, Dh, BN / 2, 64) ||
             !make_map_2d_f16(&tv, v, (uint64_t)KV, Dh, Dh, 32, 64))
             return GQA_ERR_CUDA;
-        return Dh == 256 ? launch_one<false, 256, false>(tq, tk, tv, P, tasks, stream)
-                         : launch_one<false, 128, false>(tq, tk, tv, P, tasks, stream);
+        if constexpr (WIN)
+            if (!make_map_2d_f16(&ts.k, k, sink_keys, Dh, Dh, BN / 2, 64) ||
+                !make_map_2d_f16(&ts.v, v, sink_keys, Dh, Dh, 32, 64))
+                return GQA_ERR_CUDA;
+        return Dh == 256 ? launch_one<false, 256, false, WIN>(tq, tk, tv, ts, P, tasks, stream)
+                         : launch_one<false, 128, false, WIN>(tq, tk, tv, ts, P, tasks, stream);
     }
     const uint64_t row_bytes = 2ull * Dh;
     if (!make_map_3d_f16(&tq, q, Dh, (uint64_t)Hq, (uint64_t)Q, row_bytes,
                          (uint64_t)Hq * row_bytes, BM))
         return GQA_ERR_CUDA;
     if (f8)
-        return Dh == 256 ? launch_one<true, 256, true>(tq, tq, tq, P, tasks, stream)
-                         : launch_one<true, 128, true>(tq, tq, tq, P, tasks, stream);
+        return Dh == 256 ? launch_one<true, 256, true, WIN>(tq, tq, tq, ts, P, tasks, stream)
+                         : launch_one<true, 128, true, WIN>(tq, tq, tq, ts, P, tasks, stream);
     if (!make_map_3d_f16(&tk, k, Dh, (uint64_t)Hkv, (uint64_t)KV, row_bytes,
                          (uint64_t)Hkv * row_bytes, BN / 2) ||
         !make_map_3d_f16(&tv, v, Dh, (uint64_t)Hkv, (uint64_t)KV, row_bytes,
                          (uint64_t)Hkv * row_bytes, 32))
         return GQA_ERR_CUDA;
-    return Dh == 256 ? launch_one<true, 256, false>(tq, tk, tv, P, tasks, stream)
-                     : launch_one<true, 128, false>(tq, tk, tv, P, tasks, stream);
+    if constexpr (WIN)
+        if (!make_map_3d_f16(&ts.k, k, Dh, (uint64_t)Hkv, sink_keys, row_bytes,
+                             (uint64_t)Hkv * row_bytes, BN / 2) ||
+            !make_map_3d_f16(&ts.v, v, Dh, (uint64_t)Hkv, sink_keys, row_bytes,
+                             (uint64_t)Hkv * row_bytes, 32))
+            return GQA_ERR_CUDA;
+    return Dh == 256 ? launch_one<true, 256, false, WIN>(tq, tk, tv, ts, P, tasks, stream)
+                     : launch_one<true, 128, false, WIN>(tq, tk, tv, ts, P, tasks, stream);
+}
+
+}  // namespace prefill
+
+int prefill_launch(const void* q, const void* k, const void* v, const float* kscale,
+                   const float* vscale, void* out, int Q, int KV, int Hq, int Hkv, int Dh,
+                   float scale, int window, int sinks, cudaStream_t stream) {
+    // A window that holds the whole context hides nothing.
+    if (window == 0 || window >= KV)
+        return prefill::launch<false>(q, k, v, kscale, vscale, out, Q, KV, Hq, Hkv, Dh, scale, 0,
+                                      0, stream);
+    return prefill::launch<true>(q, k, v, kscale, vscale, out, Q, KV, Hq, Hkv, Dh, scale, window,
+                                 sinks < KV ? sinks : KV, stream);
 }
 
 }  // namespace gqa
