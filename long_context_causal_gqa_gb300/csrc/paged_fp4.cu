@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "fp4_rows.cuh"
 #include "internal.h"
@@ -554,42 +555,21 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                             c[e] = row[DH / 2 + gid];
                         }
                     }
-                    // Keys no row sees may hold anything: scales of zero.  A key that
-                    // some rows see and others do not must not reach those others even
-                    // if it is NaN (0 * NaN): the rows of one position at a time then.
-                    int passes = 1;
-                    if (edge) {
-                        bool bad = false;
+                    // One pass over the values for all rows (pass < 0), or for the rows of
+                    // one position alone: the others' sums stay as they are.
+                    auto values = [&](auto one, int pass) {
+                        constexpr bool ONE = decltype(one)::value;
+                        uint32_t cc[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
-                            if (key > last || (key < s.lo && key >= P.sinks)) c[e] = 0;
-                            bad |= (c[e] & 0x7f) == 0x7f || (c[e] & 0x7f00) == 0x7f00;
-                        }
-                        if (P.R > 1 && __any_sync(0xffffffffu, bad)) passes = P.R;
-                    }
-                    for (int pass = 0; pass < passes; ++pass) {
-                        uint32_t cc[4], pp[NT][2];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) cc[e] = c[e];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            pp[nt][0] = pf[nt][0];
-                            pp[nt][1] = pf[nt][1];
-                        }
-                        if (passes > 1) {
-                            const int at = s.ctx - P.R + pass;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
+                            cc[e] = c[e];
+                            if constexpr (ONE) {
                                 const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
+                                const int at = s.ctx - P.R + pass;
                                 if (key > at || (P.window > 0 && key <= at - P.window &&
                                                  key >= P.sinks))
                                     cc[e] = 0;
                             }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (min(P.grp.div(row0 + nt * 8 + gid), P.R - 1) != pass)
-                                    pp[nt][0] = pp[nt][1] = 0;
                         }
 #pragma unroll
                         for (int i = 0; i < VW; ++i) {
@@ -611,11 +591,38 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                                 const uint32_t a2 = fp4::mul2(lo1[e], u23);
                                 const uint32_t a3 = fp4::mul2(hi1[e], u23);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816(o[4 * i + e][nt], a0, a1, a2, a3, pp[nt][0],
-                                             pp[nt][1]);
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float(&to)[4] = o[4 * i + e][nt];
+                                    const float kept[4] = {to[0], to[1], to[2], to[3]};
+                                    mma16816(to, a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                                    if constexpr (ONE) {
+#pragma unroll
+                                        for (int x = 0; x < 4; ++x)
+                                            if (pos[nt][x & 1] != s.ctx - P.R + pass)
+                                                to[x] = kept[x];
+                                    }
+                                }
                             }
                         }
+                    };
+                    // Keys no row sees may hold anything: scales of zero.  A key that
+                    // some rows see and others do not must not reach those others even
+                    // if it is NaN (0 * NaN): the rows of one position at a time then.
+                    bool apart = false;
+                    if (edge) {
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
+                            if (key > last || (key < s.lo && key >= P.sinks)) c[e] = 0;
+                            bad |= (c[e] & 0x7f) == 0x7f || (c[e] & 0x7f00) == 0x7f00;
+                        }
+                        apart = P.R > 1 && __any_sync(0xffffffffu, bad);
+                    }
+                    if (!apart) {
+                        values(std::false_type{}, -1);
+                    } else {
+                        for (int pass = 0; pass < P.R; ++pass) values(std::true_type{}, pass);
                     }
                 }
                 __syncwarp();
