@@ -15,17 +15,20 @@
 // * Copies.  One warp brings the pages of a tile (a page of one head is one
 //   contiguous run) into a ring of stages by bulk copies, table entries two tiles
 //   ahead.
-// * Products.  Eight warps take 16 keys of a tile each and never meet before the
-//   end of a piece.  A warp decodes its codes from shared memory straight into the
-//   fragments of m16n8k16 products, keys (for K) or values' places (for V) along M,
-//   packed query rows along N, so eight rows waste nothing: the order of the places
-//   within a product is free, so a lane loads whole words of one key, K's pairs are
-//   a byte's two nibbles and V's pairs come from two keys' nibbles put together.
-//   With the operands in registers nothing decoded goes through shared memory,
-//   which an operand of tcgen05.mma would have to (4 times the codes' bytes, written
-//   and read).
-// * Softmax.  A row's reference moves only when a score passes it by more than 8
-//   (log2 units), so P <= 256 in fp16; each warp keeps its own references.
+// * Products.  Groups of eight warps take a tile each, a warp 16 keys of it for the
+//   scores and a share of D and of the keys for the values, with P going through
+//   shared memory in between.  A warp decodes its codes from shared memory straight
+//   into the fragments of m16n8k16 products, keys (for K) or places of D (for V)
+//   along M, packed query rows along N, so eight rows waste nothing.  The order of the
+//   places within a product is free, so a lane loads whole words of one key: K's pairs
+//   are a byte's two nibbles, V's pairs are put together from two keys' nibbles.
+//   Nothing decoded goes through shared memory, which operands of tcgen05.mma would
+//   have to (four times the codes' bytes, written and read: more than shared memory can
+//   move while the codes arrive).
+// * Softmax.  A group's reference of a row moves only when a score passes it by more
+//   than 8 (log2 units), so P <= 256 in fp16.  A tile's P is computed with the
+//   reference as it stands, and only where some warp's scores passed it (flagged at the
+//   one barrier of a tile) is it moved, and P computed again.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -40,14 +43,7 @@ namespace gqa {
 namespace paged4 {
 
 constexpr int TILE = 128;                  // keys of a tile
-constexpr int NW = 8;                      // warps with products, 16 keys of a tile each
-// And a warpgroup of which one warp copies: at three warps for each quarter of an SM a
-// kernel starts with 168 registers a thread, of which the products take 240 and the
-// copies leave all but 24 (256 * 240 + 128 * 24 = 384 * 168).
-constexpr int THREADS = 32 * NW + 128;
-constexpr int REGS_PRODUCTS = 240, REGS_COPIES = 24;
-constexpr int STAGES = 5;
-constexpr int JOIN_BYTES = 16384;          // the warps' O on their way to one sum
+constexpr int GW = 8;                      // warps of a group, 16 keys of a tile each
 constexpr int MAX_BATCH = 1024;
 constexpr float RESCALE_THRESHOLD = 8.0f;
 
@@ -67,6 +63,8 @@ struct Params {
     int G;                       // ranges (CTAs)
     float* ws_o;                 // [G][2][8 NT][DH]
     float* ws_ml;                // [G][2][8 NT][2]
+    int4* tasks;                 // [G]: what the join has to do (Task)
+    int by_unit;                 // a task for each unit, not for each range
     __half* out;
     unsigned* err;
 };
@@ -91,14 +89,53 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
     return s;
 }
 
-// starts[b] = tiles of the sequences before b, for b = 0 .. batch.  All `N` threads
-// of the CTA (at least 256), with two barriers.
-template <int N>
-__device__ void tile_starts(const Params& P, long long* starts, long long* totals) {
+// A unit cut into several ranges, for the join: its first piece is in slot
+// 2 * range + slot0, the others in the first slots of the ranges behind.  Entry
+// `range` or (by_unit) `unit` of Params::tasks as {unit, range * 2 + slot0, pieces, 0};
+// no pieces: nothing to join.
+
+// Where each sequence's tiles begin among all.  Up to 32 sequences: lane i of every
+// warp holds sequence i, nothing is shared.  More: in shared memory.  (All tiles of all
+// units are fewer than 2^31: the host sees to it.)
+constexpr int LANES = 32;
+struct Seqs {
+    const int* starts;         // [batch + 1], or null
+    int start, tiles, ctx;     // of sequence `lane`
+    int all;                   // tiles of all sequences
+};
+
+__device__ __forceinline__ int scan_warp(int x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += t;
+    }
+    return x;
+}
+
+__device__ __forceinline__ Seqs seqs_small(const Params& P) {
+    Seqs q;
+    const int lane = threadIdx.x & 31;
+    q.starts = nullptr;
+    q.ctx = q.tiles = 0;
+    if (lane < P.batch) {
+        const Span s = span_of(P, P.ctx_lens[lane]);
+        q.ctx = s.ctx;
+        q.tiles = s.tiles;
+    }
+    const int incl = scan_warp(q.tiles);
+    q.start = incl - q.tiles;
+    q.all = __shfl_sync(0xffffffffu, incl, 31);
+    return q;
+}
+
+// starts[b] = tiles of the sequences before b, for b = 0 .. batch.  All threads of the
+// CTA (at least 256), with two barriers.
+__device__ __noinline__ void seqs_large(const Params& P, int* starts, int* totals) {
     constexpr int EACH = MAX_BATCH / 256;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int n[EACH];
-    long long sum = 0, incl = 0;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    int n[EACH], sum = 0, incl = 0;
     if (tid < 256) {
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
@@ -106,17 +143,12 @@ __device__ void tile_starts(const Params& P, long long* starts, long long* total
             n[i] = b < P.batch ? span_of(P, P.ctx_lens[b]).tiles : 0;
             sum += n[i];
         }
-        incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        if (lane == 31) totals[warp] = incl;
+        incl = scan_warp(sum);
+        if ((tid & 31) == 31) totals[warp] = incl;
     }
     __syncthreads();
     if (tid < 256) {
-        long long at = incl - sum;
+        int at = incl - sum;
         for (int w = 0; w < warp; ++w) at += totals[w];
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
@@ -129,59 +161,77 @@ __device__ void tile_starts(const Params& P, long long* starts, long long* total
     __syncthreads();
 }
 
-// Range c of G equal ones over `total` tiles, and the range a tile lies in.
-__device__ __forceinline__ long long range_begin(long long total, int G, int c) {
-    return (long long)c * total / G;
-}
-__device__ __forceinline__ int range_of(long long total, int G, long long pos) {
-    return (int)(((pos + 1) * G - 1) / total);
-}
-
-// The sequence whose tiles hold position pos (units of a sequence are one behind
-// the other, `per` of them).
-__device__ __forceinline__ int sequence_of(const Params& P, const long long* starts, int per,
-                                           long long pos) {
-    int lo = 0, hi = P.batch;   // starts[lo] * per <= pos < starts[hi] * per
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] * per <= pos) lo = mid;
-        else hi = mid;
+// G equal ranges over all tiles of all units (the first `more` one longer).
+struct Ranges {
+    uint32_t each, more;
+    int G;
+    __device__ Ranges(const Params& P, const Seqs& q) {
+        const int total = q.all * (P.hkv * P.groups);
+        G = min(P.G, total);
+        each = G ? (uint32_t)total / (uint32_t)G : 0;
+        more = total - each * G;
     }
-    return lo;
-}
+    __device__ int begin(int c) const { return c * each + min((uint32_t)c, more); }
+    __device__ int of(uint32_t pos) const {
+        const uint32_t front = more * (each + 1);
+        return pos < front ? pos / (each + 1) : more + (pos - front) / each;
+    }
+};
 
-// Walks the pieces (unit, tiles [jb, je)) of one range.
+// Walks the pieces (unit, tiles [jb, je)) of one range.  (All lanes of a warp.)
 struct Pieces {
-    long long pos, end;
-    bool first;
-    int b, h, g;      // sequence, KV head, group of packed rows
-    int jb, je;
-    bool whole;
+    int pos, end;
+    int b, u, h, g;   // sequence, unit within it, its KV head and group of packed rows
+    int jb, je, n;    // tiles of the piece, of the unit
+    bool first;       // the range's first piece
     Span s;
-    __device__ void init(long long begin, long long end_) {
-        pos = begin;
-        end = end_;
-    }
-    __device__ bool next(const Params& P, const long long* starts, long long begin) {
+    __device__ bool whole() const { return jb == 0 && je == n; }
+    __device__ bool next(const Params& P, const Seqs& q, int begin) {
         if (pos >= end) return false;
         const int per = P.hkv * P.groups;
         first = pos == begin;
-        b = sequence_of(P, starts, per, pos);
-        s = span_of(P, P.ctx_lens[b]);
-        // (at most 2^24 tiles of 192 units)
-        const uint32_t off = (uint32_t)(pos - starts[b] * per);
-        const uint32_t n = (uint32_t)(starts[b + 1] - starts[b]);
-        const int u = (int)(off / n);
-        jb = (int)(off - (uint32_t)u * n);
-        const long long left = end - pos;
-        je = (long long)jb + left < (long long)n ? jb + (int)left : (int)n;
-        whole = jb == 0 && je == (int)n;
-        h = u / P.groups;
+        int start, ctx;
+        if (!q.starts) {
+            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start * per <= pos));
+            start = __shfl_sync(0xffffffffu, q.start, b);
+            n = __shfl_sync(0xffffffffu, q.tiles, b);
+            ctx = __shfl_sync(0xffffffffu, q.ctx, b);
+        } else {
+            int lo = 0, hi = P.batch;   // starts[lo] * per <= pos < starts[hi] * per
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (q.starts[mid] * per <= pos) lo = mid;
+                else hi = mid;
+            }
+            b = lo;
+            start = q.starts[lo];
+            n = q.starts[lo + 1] - start;
+            ctx = P.ctx_lens[b];
+        }
+        s = span_of(P, ctx);
+        const int off = pos - start * per;
+        u = per == 1 ? 0 : off / n;
+        jb = off - u * n;
+        je = min(jb + end - pos, n);
+        h = P.groups == 1 ? u : u / P.groups;
         g = u - h * P.groups;
         pos += je - jb;
         return true;
     }
 };
+
+// Wait for a barrier's phase, as mbar_wait, with what a long wait needs out of line.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                       unsigned* err) {
+    return mbar_wait(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     unsigned* err) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_long(bar, parity, abort, err);
+}
 
 __device__ __forceinline__ int tile_key(const Span& s, int j) {
     return (j < s.sink_tiles ? j : s.first_tile + j - s.sink_tiles) * TILE;
@@ -213,88 +263,134 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
     return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 
+// DH: head size; NT: eights of packed rows.
 template <int DH, int NT>
-struct Layout {
+struct Config {
+    // Two groups of eight warps while a warp's sums leave room (four warps for each
+    // quarter of an SM hide the products' latencies: two took twice as long), one for
+    // more rows.  The warpgroup behind them copies.  Registers: what the launch gives
+    // (65536 over the threads, by eights) moved from the copies to the products.
+    static constexpr int NG = NT <= 3 ? 2 : 1;
+    static constexpr int NW = GW * NG;
+    static constexpr int THREADS = 32 * NW + 128;
+    static constexpr int REGS_PRODUCTS = NG == 2 ? 112 : 232;
+    static constexpr int REGS_COPIES = NG == 2 ? 32 : 40;
+    static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
+    static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
+
     static constexpr int ROWB = fp4::row_bytes(DH);
     static constexpr int STAGE = 2 * TILE * ROWB;
     static constexpr int ROWS = 8 * NT;
-    // Query rows in shared memory (NT > 1): a lane's quarter of a row padded by 16
-    // bytes, so that the eight lanes of a load's phase use different banks.
-    static constexpr int QUARTER = DH / 4 * 2 + 16;
-    static constexpr int OFF_RING = 0;
-    static constexpr int OFF_JOIN = OFF_RING + STAGES * STAGE;
-    static constexpr int OFF_Q = OFF_JOIN + JOIN_BYTES;
-    static constexpr int OFF_ML = OFF_Q + (NT > 1 ? ROWS * 4 * QUARTER : 0);
-    static constexpr int OFF_STARTS = OFF_ML + NW * ROWS * 8;
-    static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 8;
-    static constexpr int OFF_BARS = OFF_TOTALS + 8 * 8;
-    static constexpr int OFF_ABORT = OFF_BARS + (2 * STAGES + 1) * 8;
-    static constexpr int BYTES = OFF_ABORT + 16;
-    static_assert(BYTES <= 232448, "shared memory");
+    // V: slices of 64 places, and the shares of a tile's keys that then occupy eight warps.
+    static constexpr int SLICES = DH / 64, SHARES = GW / SLICES;
+    static constexpr int SOURCES = NG * SHARES;    // warps that sum the same places
+    // Query rows: a lane's part of a row so that the eight lanes of a load's phase use
+    // different banks (DH 256: quarters padded by 16 bytes; 128: rows).
+    static constexpr int Q_ROW = DH == 256 ? 4 * 144 : 272;
+    static constexpr int P_ROW = TILE * 2 + 16;    // P^T: rows of 128 keys, padded
+    static constexpr int JOIN_ROW = DH / 4 + 4;    // floats of a row in one round of the join
+
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_P = OFF_Q + ROWS * Q_ROW;                    // [NG][2][ROWS]
+    static constexpr int OFF_JOIN = OFF_P + NG * 2 * ROWS * P_ROW;        // [SOURCES][ROWS]
+    static constexpr int OFF_MAX = OFF_JOIN + SOURCES * ROWS * JOIN_ROW * 4;   // [NW][ROWS]
+    static constexpr int OFF_REF = OFF_MAX + NW * ROWS * 4;               // [NG][ROWS]
+    static constexpr int OFF_STARTS = OFF_REF + NG * ROWS * 4;
+    static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
+    static constexpr int MAX_STAGES = 10;
+    static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
+    static constexpr int OFF_FLAG = OFF_BARS + (2 * MAX_STAGES + NG + 1) * 8;   // [NG][2]
+    static constexpr int OFF_ABORT = OFF_FLAG + NG * 2 * 4;
+    static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
+    // The bytes in flight set the copy rate: all that is left, up to 184 KB.
+    static constexpr int FIT = (232448 - OFF_RING) / STAGE;
+    static constexpr int STAGES = FIT < (DH == 256 ? 5 : 10) ? FIT : (DH == 256 ? 5 : 10);
+    static constexpr int BYTES = OFF_RING + STAGES * STAGE;
+    static_assert(STAGES >= 2 && BYTES <= 232448, "shared memory");
 };
 
+// The k-th place along the products' K of the 16 keys of a warp, for the values: which
+// key it is.  Any order does if P has the same one; these spread the four keys that a
+// quarter of a warp loads words of over the banks (rows 36 or 18 words apart).
+template <int DH>
+__device__ __forceinline__ int key_of(int k) {
+    return DH == 256 ? k : (k & 6) * 2 + (k & 1) + (k >> 3) * 2;
+}
+
 template <int DH, int NT>
-__global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
-    using L = Layout<DH, NT>;
-    constexpr int ROWB = L::ROWB;
-    constexpr int ROWS = L::ROWS;
-    constexpr int MT = DH / 16;         // products along D
+__global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const Params P) {
+    using C = Config<DH, NT>;
+    constexpr int ROWB = C::ROWB, ROWS = C::ROWS, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* join = reinterpret_cast<float*>(smem + L::OFF_JOIN);
-    uint8_t* sq = smem + L::OFF_Q;
-    float* sml = reinterpret_cast<float*>(smem + L::OFF_ML);   // [NW][ROWS][2]
-    long long* starts = reinterpret_cast<long long*>(smem + L::OFF_STARTS);
-    long long* totals = reinterpret_cast<long long*>(smem + L::OFF_TOTALS);
-    const uint32_t bars = smem_u32(smem + L::OFF_BARS);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ABORT);
+    int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
+    int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
+    const uint32_t bars = smem_u32(smem + C::OFF_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (STAGES + s); };
-    const uint32_t meet_bar = bars + 8u * (2 * STAGES);
+    auto group_bar = [&](int g) { return bars + 8u * (2 * STAGES + g); };   // g = NG: all
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), NW);
+            mbar_init(empty(s), GW);
         }
-        mbar_init(meet_bar, NW);
+        for (int g = 0; g < NG; ++g) mbar_init(group_bar(g), GW);
+        mbar_init(group_bar(NG), NW);
+        for (int i = 0; i < NG * 2; ++i) reinterpret_cast<int*>(smem + C::OFF_FLAG)[i] = 0;
         *abort_flag = 0;
         fence_mbar_init();
     }
-    // Nothing of global memory is read or written before the kernel in front has
-    // completed; this kernel's launch overlaps it.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    tile_starts<THREADS>(P, starts, totals);
-    asm volatile("griddepcontrol.launch_dependents;");
-    const long long total = starts[P.batch] * (P.hkv * P.groups);
-    const int G = (int)min((long long)P.G, total);
-    const int cta = blockIdx.x;
-    // Sequences without a key: their rows are zeros.
-    for (int b = cta; b < P.batch; b += gridDim.x) {
-        const int raw = P.ctx_lens[b];
-        if ((raw < 0 || raw > P.max_ctx) && threadIdx.x == 0) atomicOr(P.err, kErrBadCtxLen);
-        if (raw <= 0) {
-            uint4* o = reinterpret_cast<uint4*>(P.out + (long long)b * P.R * P.hq * DH);
-            for (int i = threadIdx.x; i < P.R * P.hq * DH / 8; i += THREADS)
-                o[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    // This CTA's range.  Nothing of global memory is read or written before the kernel in
+    // front has completed; this kernel's launch overlaps it.
+    auto begin_range = [&](Pieces& it, Seqs& seqs) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (P.batch <= LANES) {
+            seqs = seqs_small(P);
+        } else {
+            seqs_large(P, starts, totals);
+            seqs = Seqs{starts, 0, 0, 0, starts[P.batch]};
         }
-    }
-    const bool works = cta < G;
-    const long long begin = works ? range_begin(total, G, cta) : 0;
-    const long long end = works ? range_begin(total, G, cta + 1) : 0;
-    Pieces it;
-    it.init(begin, end);
+        asm volatile("griddepcontrol.launch_dependents;");
+        const Ranges ranges(P, seqs);
+        const bool works = (int)blockIdx.x < ranges.G;
+        it.pos = works ? ranges.begin(blockIdx.x) : 0;
+        it.end = works ? ranges.begin(blockIdx.x + 1) : 0;
+        return ranges;
+    };
+    const int cta = blockIdx.x;
 
     if (warp >= NW) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPIES));
-      if (warp == NW) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
+      Seqs seqs;
+      Pieces it;
+      begin_range(it, seqs);
+      const int begin = it.pos;
+      if (warp == NW + 1) {
+        // ------------------------------------------------------------ what has no tiles
+        // Rows of sequences without a key are zeros; no units of theirs, and no cut
+        // unit for ranges that get no tiles.
+        if (it.pos == it.end && !P.by_unit && lane == 0) P.tasks[cta] = make_int4(0, 0, 0, 0);
+        for (int b = cta; b < P.batch; b += gridDim.x) {
+            const int raw = P.ctx_lens[b];
+            if ((raw < 0 || raw > P.max_ctx) && lane == 0) atomicOr(P.err, kErrBadCtxLen);
+            if (raw > 0) continue;
+            uint4* o = reinterpret_cast<uint4*>(P.out + (long long)b * P.R * P.hq * DH);
+            for (int i = lane; i < P.R * P.hq * DH / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+            if (P.by_unit)
+                for (int u = lane; u < P.hkv * P.groups; u += 32)
+                    P.tasks[b * P.hkv * P.groups + u] = make_int4(0, 0, 0, 0);
+        }
+      } else if (warp == NW) {
         // ------------------------------------------------------------ copies
         // Lanes 0 .. 15 copy K's pages of a tile, 16 .. 31 V's.
         const int kv = lane >> 4, p = lane & 15;
         const int rows = min(P.page, TILE), ppt = TILE / rows;   // rows of a copy, copies of a tile
         uint32_t n = 0;   // tiles so far
         bool ok = true;
-        while (ok && it.next(P, starts, begin)) {
+        while (ok && it.next(P, seqs, begin)) {
             const int pages = (it.s.ctx + P.page - 1) >> P.log2_page;
             const int32_t* table = P.tables + (long long)it.b * P.table_stride;
             auto entry = [&](int j) {
@@ -314,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                 const int st = n % STAGES;
                 int okw = 1;
                 if (lane == 0) {
-                    okw = mbar_wait(empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, P.err);
+                    okw = wait(empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, P.err);
                     if (okw) mbar_arrive_expect_tx(full(st), 2 * copies * rows * ROWB);
                 }
                 ok = __shfl_sync(0xffffffffu, okw, 0);
@@ -322,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                 if (p < copies) {
                     const long long row = ((long long)id * P.hkv + it.h) * P.page +
                                           (key0 & (P.page - 1));
-                    bulk_load(smem_u32(smem) + L::OFF_RING + st * L::STAGE + kv * (TILE * ROWB) +
+                    bulk_load(smem_u32(smem) + C::OFF_RING + st * C::STAGE + kv * (TILE * ROWB) +
                                   p * rows * ROWB,
                               P.cache[kv] + row * ROWB, rows * ROWB, full(st));
                 }
@@ -344,123 +440,131 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
       }
     } else {
         // ------------------------------------------------------------ products
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_PRODUCTS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
+        Seqs seqs;
+        Pieces it;
+        const Ranges ranges = begin_range(it, seqs);
+        const int begin = it.pos;
+        const int group = warp / GW, gwarp = warp % GW;
         const int gid = lane >> 2, t = lane & 3;
-        uint32_t meet_phase = 0;
-        // All warps with products: a barrier that shares the bounded wait.
-        auto meet = [&]() -> bool {
+        const int slice = gwarp % C::SLICES, share = gwarp / C::SLICES;
+        uint8_t* const sq = smem + C::OFF_Q;
+        uint8_t* const sp = smem + C::OFF_P + group * 2 * ROWS * C::P_ROW;
+        float* const smax = reinterpret_cast<float*>(smem + C::OFF_MAX);   // [NW][ROWS]
+        float* const sref = reinterpret_cast<float*>(smem + C::OFF_REF);   // [NG][ROWS]
+        float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+        volatile int* const flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG) + group * 2;
+        uint32_t all_phase = 0, group_phase = 0;
+        // Barriers of all warps with products and of a group, with the bounded wait.
+        auto sync = [&](uint32_t bar, uint32_t& phase) -> bool {
             __syncwarp();
-            if (lane == 0) mbar_arrive(meet_bar);
-            const bool ok = mbar_wait(meet_bar, meet_phase, abort_flag, P.err);
-            meet_phase ^= 1;
+            if (lane == 0) mbar_arrive(bar);
+            const bool ok = wait(bar, phase, abort_flag, P.err);
+            phase ^= 1;
             return __all_sync(0xffffffffu, ok);
         };
+        auto meet = [&]() { return sync(group_bar(NG), all_phase); };
+        auto meet_group = [&]() { return sync(group_bar(group), group_phase); };
         const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
-        const float vscale = *P.scale_dev[1];
-        uint32_t n = 0;
+        uint32_t n = 0;     // tiles of the CTA so far
+        uint32_t mine = 0;  // tiles of the group so far
         bool ok = true;
-        while (ok && it.next(P, starts, begin)) {
+        while (ok && it.next(P, seqs, begin)) {
             const Span s = it.s;
             const int row0 = it.g * ROWS;
-            // Q: the lane's quarter of row gid of each eight (products' B operand).
-            uint32_t qf[NT == 1 ? MT : 1][2];
-            if constexpr (NT == 1) {
-                const bool there = row0 + gid < P.nq;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    P.q + (there ? row_offset(P, it.b, it.h, row0 + gid, DH) : 0) + t * (DH / 4));
-#pragma unroll
-                for (int i = 0; i < MT / 2; ++i) {
-                    const uint4 v = there ? src[i] : make_uint4(0, 0, 0, 0);
-                    qf[2 * i][0] = v.x;
-                    qf[2 * i][1] = v.y;
-                    qf[2 * i + 1][0] = v.z;
-                    qf[2 * i + 1][1] = v.w;
-                }
-            } else {
-                for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
-                    const int r = i / (DH / 8), c = i % (DH / 8);
-                    const uint4 v = row0 + r < P.nq
-                                        ? *reinterpret_cast<const uint4*>(
-                                              P.q + row_offset(P, it.b, it.h, row0 + r, DH) + c * 8)
-                                        : make_uint4(0, 0, 0, 0);
-                    const int quarter = c / (DH / 32);
-                    *reinterpret_cast<uint4*>(sq + (r * 4 + quarter) * L::QUARTER +
-                                              (c % (DH / 32)) * 16) = v;
-                }
-                ok = meet();
-                if (!ok) break;
+            if (threadIdx.x == 0) {
+                // The piece a unit begins with says how it is joined; a range whose last
+                // piece is no cut unit's beginning has none.
+                const int unit = it.b * (P.hkv * P.groups) + it.u;
+                const bool cut = it.jb == 0 && !it.whole();
+                if (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end))
+                    P.tasks[P.by_unit ? unit : cta] =
+                        make_int4(unit, cta * 2 + (it.first ? 0 : 1),
+                                  cut ? ranges.of(it.pos - it.je + it.n - 1) - cta + 1 : 0, 0);
             }
-            // Positions of the lane's packed rows 2 t, 2 t + 1 of each eight.
-            int pos[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    pos[nt][e] = s.ctx - P.R +
-                                 min(P.grp.div(row0 + nt * 8 + 2 * t + e), P.R - 1);
-            float o[MT][NT][4];
-            float mref[NT][2], l[NT][2];
+            for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
+                const int r = i / (DH / 8), c = i % (DH / 8);
+                const uint4 v = row0 + r < P.nq
+                                    ? *reinterpret_cast<const uint4*>(
+                                          P.q + row_offset(P, it.b, it.h, row0 + r, DH) + c * 8)
+                                    : make_uint4(0, 0, 0, 0);
+                const int at = DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
+                *reinterpret_cast<uint4*>(sq + r * C::Q_ROW + at) = v;
+            }
+            ok = meet();
+            if (!ok) break;
+            // Position of packed row r (of this unit's ROWS).
+            auto row_pos = [&](int r) {
+                return s.ctx - P.R + min(P.grp.div(row0 + r), P.R - 1);
+            };
+            auto sees = [&](int at, int key) {
+                return key <= at && (P.window == 0 || key > at - P.window || key < P.sinks);
+            };
+            float o[4][NT][4];              // places 8 gid + 2 i, + 1 of the slice; rows 2 t, 2 t + 1
+            float mref[NT][2], l[NT][2];    // of rows 2 t, 2 t + 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 mref[nt][0] = mref[nt][1] = -INFINITY;
                 l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[m][nt][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
             }
 
-            for (int j = it.jb; j < it.je; ++j) {
+            for (int j = it.jb; j < it.je; ++j, ++n) {
+                if (NG > 1 && n % NG != (uint32_t)group) continue;
                 const int st = n % STAGES;
-                ok = mbar_wait(full(st), (n / STAGES) & 1, abort_flag, P.err);
+                ok = wait(full(st), (n / STAGES) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++n;
-                const int k0 = tile_key(s, j) + warp * 16;
+                const int key0 = tile_key(s, j);
                 const int last = s.ctx - 1;
-                const bool skip = k0 > last || (k0 + 15 < s.lo && k0 >= P.sinks);
-                if (!skip) {
-                    const uint8_t* kst = smem + L::OFF_RING + st * L::STAGE + warp * 16 * ROWB;
-                    const uint8_t* vst = kst + TILE * ROWB;
-                    // Some key of the 16 is hidden from some row.
-                    const bool edge = k0 + 15 > s.ctx - P.R ||
-                                      (P.window > 0 && k0 <= last - P.window && k0 + 15 >= P.sinks);
-                    // ---- scores of keys gid and gid + 8
-                    float sc[NT][4];
+                // Some key of the tile is hidden from some row.
+                const bool edge = key0 + TILE - 1 > s.ctx - P.R ||
+                                  (P.window > 0 && key0 <= last - P.window &&
+                                   key0 + TILE - 1 >= P.sinks);
+                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
+                const uint8_t* vst = kst + TILE * ROWB;
+                uint8_t* const pt = sp + (mine & 1) * ROWS * C::P_ROW;
+                // ---- scores of keys key_of(gid) and key_of(gid + 8) of the warp's 16
+                float sc[NT][4];
+                {
+                    constexpr int CHAINS = NT == 1 ? 2 : 1;   // (sums side by side)
+                    float sd[CHAINS][NT][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int x = 0; x < CHAINS; ++x)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-                    {
-                        constexpr int KW = DH / 32;   // words of a lane and key
-                        uint32_t w[2][KW], u[2][DH / 64];
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sd[x][nt][e] = 0.f;
+                    constexpr int KW = DH / 32;   // words of a lane and key
+                    constexpr int HALF = KW / 2;  // of one load
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t w[2][HALF], u[2][HALF / 2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint8_t* row = kst + (gid + 8 * e) * ROWB;
+                            const uint8_t* row =
+                                kst + (gwarp * 16 + key_of<DH>(gid + 8 * e)) * ROWB;
                             if constexpr (DH == 256) {
-                                const uint4* src = reinterpret_cast<const uint4*>(row + t * 32);
-                                const uint4 x = src[0], y = src[1];
-                                w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
-                                w[e][4] = y.x, w[e][5] = y.y, w[e][6] = y.z, w[e][7] = y.w;
-                                const uint32_t c =
-                                    *reinterpret_cast<const uint32_t*>(row + DH / 2 + t * 4);
-                                const uint32_t c01 = fp4::scales2(c), c23 = fp4::scales2(c >> 16);
-                                u[e][0] = __byte_perm(c01, 0, 0x1010);
-                                u[e][1] = __byte_perm(c01, 0, 0x3232);
-                                u[e][2] = __byte_perm(c23, 0, 0x1010);
-                                u[e][3] = __byte_perm(c23, 0, 0x3232);
-                            } else {
-                                const uint2* src = reinterpret_cast<const uint2*>(row + t * 16);
-                                const uint2 x = src[0], y = src[1];
-                                w[e][0] = x.x, w[e][1] = x.y, w[e][2] = y.x, w[e][3] = y.y;
-                                const uint32_t c = fp4::scales2(
-                                    *reinterpret_cast<const uint16_t*>(row + DH / 2 + t * 2));
+                                const uint4 v =
+                                    *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
+                                w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                                const uint32_t c = fp4::scales2(*reinterpret_cast<const uint16_t*>(
+                                    row + DH / 2 + t * 4 + x * 2));
                                 u[e][0] = __byte_perm(c, 0, 0x1010);
                                 u[e][1] = __byte_perm(c, 0, 0x3232);
+                            } else {
+                                // (places 16 t and 64 + 16 t)
+                                const uint2 v =
+                                    *reinterpret_cast<const uint2*>(row + t * 8 + x * 32);
+                                w[e][0] = v.x, w[e][1] = v.y;
+                                u[e][0] = fp4::scales2(row[DH / 2 + t + x * 4] * 0x101u);
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < KW; ++i) {
+                        for (int i = 0; i < HALF; ++i) {
                             uint32_t a[4], b[4];
                             fp4::decode8(w[0][i], a);
                             fp4::decode8(w[1][i], b);
@@ -471,168 +575,200 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                uint4 qv;
-                                if constexpr (NT == 1)
-                                    qv = make_uint4(qf[2 * i][0], qf[2 * i][1], qf[2 * i + 1][0],
-                                                    qf[2 * i + 1][1]);
-                                else
-                                    qv = *reinterpret_cast<const uint4*>(
-                                        sq + ((nt * 8 + gid) * 4 + t) * L::QUARTER + i * 16);
-                                mma16816(sc[nt], a[0], b[0], a[1], b[1], qv.x, qv.y);
-                                mma16816(sc[nt], a[2], b[2], a[3], b[3], qv.z, qv.w);
+                                const uint4 qv = *reinterpret_cast<const uint4*>(
+                                    sq + (nt * 8 + gid) * C::Q_ROW +
+                                    (DH == 256 ? t * 144 + x * 64 + i * 16
+                                               : t * 32 + x * 128 + i * 16));
+                                mma16816(sd[0][nt], a[0], b[0], a[1], b[1], qv.x, qv.y);
+                                mma16816(sd[CHAINS - 1][nt], a[2], b[2], a[3], b[3], qv.z, qv.w);
                             }
                         }
                     }
-                    bool exceed = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            sc[nt][e] *= sl2;
-                            if (edge) {
-                                const int key = k0 + gid + (e & 2) * 4, at = pos[nt][e & 1];
-                                const bool seen =
-                                    key <= at && (P.window == 0 || key > at - P.window ||
-                                                  key < P.sinks);
-                                if (!seen) sc[nt][e] = -INFINITY;
-                            }
-                            exceed |= sc[nt][e] > mref[nt][e & 1] + RESCALE_THRESHOLD;
-                        }
-                    if (__any_sync(0xffffffffu, exceed)) {
+                        for (int e = 0; e < 4; ++e)
+                            sc[nt][e] = (CHAINS == 2 ? sd[0][nt][e] + sd[CHAINS - 1][nt][e]
+                                                     : sd[0][nt][e]) * sl2;
+                }
+                if (edge) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float f[2];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+                        for (int e = 0; e < 4; ++e)
+                            if (!sees(row_pos(nt * 8 + 2 * t + (e & 1)),
+                                      key0 + gwarp * 16 + key_of<DH>(gid + (e & 2) * 4)))
+                                sc[nt][e] = -INFINITY;
+                }
+                // ---- P by the references as they stand
+                bool exceed = false;
 #pragma unroll
-                                for (int x = 4; x < 32; x <<= 1)
-                                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                                f[e] = 1.f;
-                                if (m > mref[nt][e] + RESCALE_THRESHOLD) {
-                                    f[e] = ex2(mref[nt][e] - m);
-                                    mref[nt][e] = m;
-                                }
-                                l[nt][e] *= f[e];
-                            }
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                o[m][nt][0] *= f[0];
-                                o[m][nt][1] *= f[1];
-                                o[m][nt][2] *= f[0];
-                                o[m][nt][3] *= f[1];
-                            }
-                        }
-                    }
-                    // ---- P, transposed into the second product's B operand: keys
-                    // 2 t, 2 t + 1 (and 8 more) of packed row gid.
-                    uint32_t pf[NT][2];
+                    for (int e = 0; e < 4; ++e)
+                        exceed |= sc[nt][e] > mref[nt][e & 1] + RESCALE_THRESHOLD;
+                if (__any_sync(0xffffffffu, exceed) && lane == 0) flag[mine & 1] = (int)mine + 1;
+                // The P of a strip, transposed: keys 2 t, 2 t + 1 (and 8 more) of packed
+                // row gid.  Returns the rows' sums in ls.
+                auto put_p = [&](float (&ls)[NT][2]) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float m0 = mref[nt][0] == -INFINITY ? 0.f : mref[nt][0];
                         const float m1 = mref[nt][1] == -INFINITY ? 0.f : mref[nt][1];
                         const float p0 = ex2(sc[nt][0] - m0), p1 = ex2(sc[nt][1] - m1);
                         const float p2 = ex2(sc[nt][2] - m0), p3 = ex2(sc[nt][3] - m1);
-                        l[nt][0] += p0 + p2;
-                        l[nt][1] += p1 + p3;
-                        pf[nt][0] = transpose8(pack_half2(p0, p1));
-                        pf[nt][1] = transpose8(pack_half2(p2, p3));
+                        ls[nt][0] = p0 + p2;
+                        ls[nt][1] = p1 + p3;
+                        uint8_t* to = pt + (nt * 8 + gid) * C::P_ROW + (gwarp * 16 + 2 * t) * 2;
+                        *reinterpret_cast<uint32_t*>(to) = transpose8(pack_half2(p0, p1));
+                        *reinterpret_cast<uint32_t*>(to + 16) = transpose8(pack_half2(p2, p3));
                     }
-                    // ---- O += V^T P^T over keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-                    constexpr int VW = DH / 64;   // words of a lane and key
-                    uint32_t w[4][VW];
-                    uint32_t c[4];                // their scales, one byte each 16 values
+                };
+                float ls[NT][2];
+                put_p(ls);
+                // One barrier a tile: P is there, and nobody reads the other buffer, which
+                // the next tile writes, any more (its products are in front of it).
+                ok = meet_group();
+                if (!ok) break;
+                if (flag[mine & 1] == (int)mine + 1) {
+                    // A reference moves: the tile's largest scores of all warps.
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint8_t* row = vst + (2 * t + (e & 1) + (e >> 1) * 8) * ROWB;
-                        if constexpr (DH == 256) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(row + gid * 16);
-                            w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
-                            c[e] = *reinterpret_cast<const uint16_t*>(row + DH / 2 + gid * 2);
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(row + gid * 8);
-                            w[e][0] = x.x, w[e][1] = x.y;
-                            c[e] = row[DH / 2 + gid];
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1)
+                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                            if (gid == 0) smax[warp * ROWS + nt * 8 + 2 * t + e] = m;
+                        }
+                    ok = meet_group();
+                    if (!ok) break;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float* from = smax + group * GW * ROWS + nt * 8 + 2 * t + e;
+                            float m = from[0];
+#pragma unroll
+                            for (int x = 1; x < GW; ++x) m = fmaxf(m, from[x * ROWS]);
+                            f[e] = 1.f;
+                            if (m > mref[nt][e] + RESCALE_THRESHOLD) {
+                                f[e] = ex2(mref[nt][e] - m);
+                                mref[nt][e] = m;
+                            }
+                            l[nt][e] *= f[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[i][nt][0] *= f[0];
+                            o[i][nt][1] *= f[1];
+                            o[i][nt][2] *= f[0];
+                            o[i][nt][3] *= f[1];
                         }
                     }
-                    // One pass over the values for all rows (pass < 0), or for the rows of
-                    // one position alone: the others' sums stay as they are.
-                    auto values = [&](auto one, int pass) {
-                        constexpr bool ONE = decltype(one)::value;
-                        uint32_t cc[4];
+                    put_p(ls);
+                    ok = meet_group();   // (also: the maxima have been read)
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt][0] += ls[nt][0];
+                    l[nt][1] += ls[nt][1];
+                }
+                // ---- O += V^T P^T over the share's keys, 16 at a time
+                constexpr int STEPS = TILE / 16 / C::SHARES;
+                const uint8_t* const vcol = vst + slice * 32 + gid * 4;
+                const uint32_t pick = (gid >> 1) | ((gid >> 1) + 4) << 4;
+                bool apart = false;
+#pragma unroll
+                for (int x = 0; x < STEPS; x += 2) {
+                    uint32_t pf[NT][4];   // B operands of two steps
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t from = smem_u32(pt) + (nt * 8 + (lane & 7)) * C::P_ROW +
+                                              ((share * STEPS + x) * 16 + (lane >> 3) * 8) * 2;
+                        asm volatile(
+                            "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                            : "=r"(pf[nt][0]), "=r"(pf[nt][1]), "=r"(pf[nt][2]), "=r"(pf[nt][3])
+                            : "r"(from)
+                            : "memory");
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int k0 = (share * STEPS + x + y) * 16;
+                        uint32_t w[4], u[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            cc[e] = c[e];
-                            if constexpr (ONE) {
-                                const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
-                                const int at = s.ctx - P.R + pass;
-                                if (key > at || (P.window > 0 && key <= at - P.window &&
-                                                 key >= P.sinks))
-                                    cc[e] = 0;
-                            }
+                            const int k = k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
+                            w[e] = *reinterpret_cast<const uint32_t*>(vcol + k * ROWB);
+                            const uint8_t* sc4 = vst + k * ROWB + DH / 2 + slice * 4;
+                            u[e] = *reinterpret_cast<const uint32_t*>(sc4);
                         }
-#pragma unroll
-                        for (int i = 0; i < VW; ++i) {
-                            // (words 2 k and 2 k + 1 share a scale)
-                            const int sh = DH == 256 ? (i / 2) * 8 : 0;
-                            const uint32_t u01 = fp4::scales2(((cc[0] >> sh) & 0xff) |
-                                                              ((cc[1] >> sh) & 0xff) << 8);
-                            const uint32_t u23 = fp4::scales2(((cc[2] >> sh) & 0xff) |
-                                                              ((cc[3] >> sh) & 0xff) << 8);
-                            uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
-                            fp4::decode8(low_nibbles(w[0][i], w[1][i]), lo0);
-                            fp4::decode8(high_nibbles(w[0][i], w[1][i]), hi0);
-                            fp4::decode8(low_nibbles(w[2][i], w[3][i]), lo1);
-                            fp4::decode8(high_nibbles(w[2][i], w[3][i]), hi1);
+                        uint32_t c01 = __byte_perm(u[0], u[1], pick) & 0xffff;
+                        uint32_t c23 = __byte_perm(u[2], u[3], pick) & 0xffff;
+                        if (edge) {
+                            // Keys no row sees may hold anything: scales of zero.  NaN
+                            // scales of keys that some rows see and others do not are
+                            // zeros too (0 * NaN), and the rows that see them are made NaN
+                            // below.
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const uint32_t a0 = fp4::mul2(lo0[e], u01);
-                                const uint32_t a1 = fp4::mul2(hi0[e], u01);
-                                const uint32_t a2 = fp4::mul2(lo1[e], u23);
-                                const uint32_t a3 = fp4::mul2(hi1[e], u23);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    float(&to)[4] = o[4 * i + e][nt];
-                                    const float kept[4] = {to[0], to[1], to[2], to[3]};
-                                    mma16816(to, a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                                    if constexpr (ONE) {
-#pragma unroll
-                                        for (int x = 0; x < 4; ++x)
-                                            if (pos[nt][x & 1] != s.ctx - P.R + pass)
-                                                to[x] = kept[x];
-                                    }
-                                }
+                                const int key = key0 + k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
+                                uint32_t& c = e < 2 ? c01 : c23;
+                                const uint32_t in = 0x7fu << (e & 1) * 8;
+                                const bool unseen = key > last || (key < s.lo && key >= P.sinks);
+                                const bool nan = (c & in) == in;
+                                if (unseen || nan) c &= ~(0xffu << (e & 1) * 8);
+                                apart |= nan && !unseen;
                             }
                         }
-                    };
-                    // Keys no row sees may hold anything: scales of zero.  A key that
-                    // some rows see and others do not must not reach those others even
-                    // if it is NaN (0 * NaN): the rows of one position at a time then.
-                    bool apart = false;
-                    if (edge) {
-                        bool bad = false;
+                        const uint32_t u01 = fp4::scales2(c01), u23 = fp4::scales2(c23);
+                        uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
+                        fp4::decode8(low_nibbles(w[0], w[1]), lo0);
+                        fp4::decode8(high_nibbles(w[0], w[1]), hi0);
+                        fp4::decode8(low_nibbles(w[2], w[3]), lo1);
+                        fp4::decode8(high_nibbles(w[2], w[3]), hi1);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
-                            if (key > last || (key < s.lo && key >= P.sinks)) c[e] = 0;
-                            bad |= (c[e] & 0x7f) == 0x7f || (c[e] & 0x7f00) == 0x7f00;
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = fp4::mul2(lo0[i], u01);
+                            const uint32_t a1 = fp4::mul2(hi0[i], u01);
+                            const uint32_t a2 = fp4::mul2(lo1[i], u23);
+                            const uint32_t a3 = fp4::mul2(hi1[i], u23);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(o[i][nt], a0, a1, a2, a3, pf[nt][2 * y], pf[nt][2 * y + 1]);
                         }
-                        apart = P.R > 1 && __any_sync(0xffffffffu, bad);
                     }
-                    if (!apart) {
-                        values(std::false_type{}, -1);
-                    } else {
-                        for (int pass = 0; pass < P.R; ++pass) values(std::true_type{}, pass);
+                }
+                if (__any_sync(0xffffffffu, apart)) {
+                    // All places of a lane lie in one block of 16.
+                    uint32_t poison = 0;
+#pragma unroll 1
+                    for (int k = share * STEPS * 16; k < (share + 1) * STEPS * 16; ++k) {
+                        const int key = key0 + k;
+                        if ((vst[k * ROWB + DH / 2 + slice * 4 + (gid >> 1)] & 0x7f) != 0x7f)
+                            continue;
+#pragma unroll
+                        for (int r = 0; r < 2 * NT; ++r)
+                            if (sees(row_pos((r >> 1) * 8 + 2 * t + (r & 1)), key)) poison |= 1u << r;
                     }
+#pragma unroll
+                    for (int r = 0; r < 2 * NT; ++r)
+                        if (poison >> r & 1)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[i][r >> 1][r & 1] = o[i][r >> 1][(r & 1) + 2] = NAN;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(st));
+                ++mine;
             }
             if (!ok) break;
 
             // ---------------------------------------------------------- end of the piece
-            // The warps' references and sums, then their O in a fixed order: warp x
-            // gathers the products [x MT / NW, (x + 1) MT / NW) of all.
+            // Sums of the rows' weights by warp, the groups' references.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -641,261 +777,222 @@ __global__ void __launch_bounds__(THREADS, 1) split_kernel(const Params P) {
                     for (int x = 4; x < 32; x <<= 1)
                         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
                     if (gid == 0) {
-                        float* to = sml + (warp * ROWS + nt * 8 + 2 * t + e) * 2;
-                        to[0] = mref[nt][e];
-                        to[1] = l[nt][e];
+                        smax[warp * ROWS + nt * 8 + 2 * t + e] = l[nt][e];
+                        if (gwarp == 0) sref[group * ROWS + nt * 8 + 2 * t + e] = mref[nt][e];
                     }
                 }
-            ok = meet();
-            if (!ok) break;
-            float M[NT][2], sum[NT][2];
+            // O in four rounds, a quarter of each lane's places each: the sources' shares
+            // go through shared memory and are added in order, in units of the largest
+            // reference.
+            const int slot = cta * 2 + (it.first ? 0 : 1);
+            const bool whole = it.whole();
+#pragma unroll 1
+            for (int r = 0; r < 4; ++r) {
+                float* to = join + (group * C::SHARES + share) * ROWS * C::JOIN_ROW + slice * 16 +
+                            gid * 2;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float* from = sml + (nt * 8 + 2 * t + e) * 2;
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int x = 0; x < NW; ++x) m = fmaxf(m, from[x * ROWS * 2]);
-                    float a = 0.f;
-#pragma unroll
-                    for (int x = 0; x < NW; ++x) {
-                        const float mx = from[x * ROWS * 2];
-                        a += (mx == -INFINITY ? 0.f : ex2(mx - m)) * from[x * ROWS * 2 + 1];
-                    }
-                    M[nt][e] = m;
-                    sum[nt][e] = a;
-                    const float f = mref[nt][e] == -INFINITY ? 0.f : ex2(mref[nt][e] - m);
-#pragma unroll
-                    for (int k = 0; k < MT; ++k) {
-                        o[k][nt][e] *= f;
-                        o[k][nt][e + 2] *= f;
-                    }
-                }
-            constexpr int MINE = MT / NW;                          // products of a target
-            constexpr int PIECE = MINE * NT * 128;                 // floats of one source
-            constexpr int TARGETS = JOIN_BYTES / (NW * PIECE * 4); // of one round
-            static_assert(TARGETS >= 1 && NW % TARGETS == 0, "rounds");
-            float acc[MINE][NT][4];
-#pragma unroll
-            for (int r = 0; r < NW / TARGETS; ++r) {
-                if (r) {
-                    ok = meet();
-                    if (!ok) break;
-                }
-#pragma unroll
-                for (int x = 0; x < TARGETS; ++x)
-#pragma unroll
-                    for (int k = 0; k < MINE; ++k)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float(&v)[4] = o[(r * TARGETS + x) * MINE + k][nt];
-                            *reinterpret_cast<float4*>(join + (x * NW + warp) * PIECE +
-                                                       ((k * NT + nt) * 32 + lane) * 4) =
-                                make_float4(v[0], v[1], v[2], v[3]);
-                        }
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float2*>(to + (nt * 8 + 2 * t + e) * C::JOIN_ROW) =
+                            make_float2(o[0][nt][e], o[0][nt][e + 2]);
                 ok = meet();
                 if (!ok) break;
-                if (warp / TARGETS == r) {
+                for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
+                    const int row = i / (DH / 8), at = i % (DH / 8);   // at: slice, gid
+                    if (row0 + row >= P.nq) break;
+                    float M = sref[row];
 #pragma unroll
-                    for (int k = 0; k < MINE; ++k)
+                    for (int g = 1; g < NG; ++g) M = fmaxf(M, sref[g * ROWS + row]);
+                    float2 a = make_float2(0.f, 0.f);
+                    float sum = 0.f;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int g = 0; g < NG; ++g) {
+                        const float mg = sref[g * ROWS + row];
+                        const float f = mg == -INFINITY ? 0.f : ex2(mg - M);
+                        float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                            for (int x = 0; x < NW; ++x) {
-                                const float4 v = *reinterpret_cast<const float4*>(
-                                    join + ((warp % TARGETS) * NW + x) * PIECE +
-                                    ((k * NT + nt) * 32 + lane) * 4);
-                                a.x += v.x;
-                                a.y += v.y;
-                                a.z += v.z;
-                                a.w += v.w;
-                            }
-                            acc[k][nt][0] = a.x;
-                            acc[k][nt][1] = a.y;
-                            acc[k][nt][2] = a.z;
-                            acc[k][nt][3] = a.w;
+                        for (int x = 0; x < C::SHARES; ++x) {
+                            const float2 y = *reinterpret_cast<const float2*>(
+                                join + ((g * C::SHARES + x) * ROWS + row) * C::JOIN_ROW + at * 2);
+                            v.x += y.x;
+                            v.y += y.y;
                         }
-                }
-            }
-            if (!ok) break;
-            const int slot = cta * 2 + (it.first ? 0 : 1);
+                        float lg = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = nt * 8 + 2 * t + e;
-                    if (row0 + r >= P.nq) continue;
-                    const float inv = sum[nt][e] > 0.f ? vscale / sum[nt][e]
-                                      : isnan(sum[nt][e]) ? NAN : 0.f;
-#pragma unroll
-                    for (int k = 0; k < MINE; ++k) {
-                        // Product i * 4 + x is the places 8 i + 2 x, 8 i + 2 x + 1 of
-                        // every gid's DH / 8.
-                        const int m = warp * MINE + k;
-                        const int d = gid * (DH / 8) + (m / 4) * 8 + (m % 4) * 2;
-                        if (it.whole)
-                            *reinterpret_cast<uint32_t*>(
-                                P.out + row_offset(P, it.b, it.h, row0 + r, DH) + d) =
-                                pack_half2(acc[k][nt][e] * inv, acc[k][nt][e + 2] * inv);
-                        else
-                            *reinterpret_cast<float2*>(P.ws_o + ((long long)slot * ROWS + r) * DH +
-                                                       d) =
-                                make_float2(acc[k][nt][e], acc[k][nt][e + 2]);
+                        for (int x = 0; x < GW; ++x) lg += smax[(g * GW + x) * ROWS + row];
+                        sum = fmaf(f, lg, sum);
+                        a.x = fmaf(f, v.x, a.x);
+                        a.y = fmaf(f, v.y, a.y);
                     }
-                    if (!it.whole && warp == 0 && gid == 0)
-                        *reinterpret_cast<float2*>(P.ws_ml + ((long long)slot * ROWS + r) * 2) =
-                            make_float2(M[nt][e], sum[nt][e]);
+                    const int d = at * 8 + r * 2;
+                    if (whole) {
+                        // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
+                        const float inv = sum == 0.f ? 0.f : *P.scale_dev[1] / sum;
+                        *reinterpret_cast<uint32_t*>(
+                            P.out + row_offset(P, it.b, it.h, row0 + row, DH) + d) =
+                            pack_half2(a.x * inv, a.y * inv);
+                    } else {
+                        *reinterpret_cast<float2*>(
+                            P.ws_o + ((long long)slot * ROWS + row) * DH + d) = a;
+                        if (at == 0 && r == 0)
+                            *reinterpret_cast<float2*>(
+                                P.ws_ml + ((long long)slot * ROWS + row) * 2) = make_float2(M, sum);
+                    }
                 }
-            // (sml and join are written again only behind the next piece's barriers:
-            // sml by warps that may be ahead of this piece's last readers)
-            ok = meet();
+                ok = meet();
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][nt][e] = o[i + 1][nt][e];
+            }
         }
     }
     __syncthreads();
 }
 
-// Joins the partials of the units that lie in several ranges: a block for a
-// packed row of a unit, found by its number (by_unit) or by the first range that
-// begins inside it.  Pieces are added in range order within each of the block's
-// lanes of pieces, which are then added in order.
-constexpr int MERGE_THREADS = 512;
+// Joins the partials of the units that lie in several ranges.  A block of 16 warps
+// takes 128 places of D of one packed row where there are few units, of two rows where
+// there are many (most then have two or three pieces); a row's warps share its pieces
+// out and their sums are added in order.
+constexpr int MERGE_WARPS = 16;
+constexpr int MAX_RANGES = 256;   // 32 pieces a warp where eight share a row
 
-template <int DH, int NT>
-__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const Params P, int by_unit) {
+template <int DH, int NT, int WPR>   // WPR: warps of a row
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P) {
     constexpr int ROWS = 8 * NT;
-    constexpr int LANES = MERGE_THREADS / (DH / 4);   // pieces side by side
-    __shared__ long long starts[MAX_BATCH + 1];
-    __shared__ long long totals[8];
-    __shared__ float w_s[MERGE_THREADS];
-    __shared__ float red[2][MERGE_THREADS / 32];
-    __shared__ float4 part[LANES][DH / 4];
+    __shared__ float4 part[MERGE_WARPS][32];
+    __shared__ float2 top[MERGE_WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (MERGE_WARPS / WPR) + warp / WPR, w = warp % WPR;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    tile_starts<MERGE_THREADS>(P, starts, totals);
+    const int4 task = __ldcg(P.tasks + blockIdx.x);
+    const int pieces = task.z;
+    if (pieces == 0) return;
     const int per = P.hkv * P.groups;
-    const long long total = starts[P.batch] * per;
-    const int G = (int)min((long long)P.G, total);
-    long long unit_start, unit_end;
-    int b, u;
-    if (by_unit) {
-        b = (int)(blockIdx.x / (unsigned)per);
-        u = (int)(blockIdx.x - (unsigned)b * per);
-        const long long n = starts[b + 1] - starts[b];
-        if (n == 0) return;
-        unit_start = starts[b] * per + u * n;
-        unit_end = unit_start + n;
-    } else {
-        const int c = blockIdx.x + 1;
-        if (c >= G) return;
-        const long long pos = range_begin(total, G, c);
-        b = sequence_of(P, starts, per, pos);
-        const uint32_t off = (uint32_t)(pos - starts[b] * per);
-        const uint32_t n = (uint32_t)(starts[b + 1] - starts[b]);
-        u = (int)(off / n);
-        unit_start = starts[b] * per + (long long)u * n;
-        unit_end = unit_start + n;
-        if (unit_start == pos || range_of(total, G, unit_start) != c - 1) return;
-    }
-    const int c0 = range_of(total, G, unit_start), c1 = range_of(total, G, unit_end - 1);
-    if (c0 == c1) return;
+    const int b = task.x / per, u = task.x - b * per;
     const int h = u / P.groups, g = u - h * P.groups;
-    const int r = blockIdx.y;
-    if (g * ROWS + r >= P.nq) return;
-    const int slot0 = range_begin(total, G, c0) == unit_start ? 0 : 1;
-    const int pieces = c1 - c0 + 1;   // at most MERGE_THREADS
+    const bool there = r < ROWS && g * ROWS + r < P.nq;
+    const int d0 = blockIdx.z * 128 + lane * 4;
+    const float vscale = *P.scale_dev[1];
     auto row_of = [&](int i) {
-        return ((long long)(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * ROWS + r;
+        return (i == 0 ? (long long)task.y : (long long)(task.y / 2 + i) * 2) * ROWS + r;
     };
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The warp's pieces w, w + WPR, ...: references and sums, a lane each, and the first O
+    // in flight beside them.
+    constexpr int AHEAD = WPR == MERGE_WARPS ? 10 : 3;
+    const int mine = there && pieces > w ? (pieces - w + WPR - 1) / WPR : 0;
+    const float* from = P.ws_o + d0;
+    float4 o[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < mine)
+            o[i] = __ldcg(reinterpret_cast<const float4*>(from + row_of(w + i * WPR) * DH));
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (tid < pieces) ml = __ldcg(reinterpret_cast<const float2*>(P.ws_ml + row_of(tid) * 2));
+    if (lane < mine) ml = __ldcg(reinterpret_cast<const float2*>(P.ws_ml + row_of(w + lane * WPR) * 2));
     float m = ml.x;
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-    m = red[0][0];
-#pragma unroll
-    for (int x = 1; x < MERGE_THREADS / 32; ++x) m = fmaxf(m, red[0][x]);
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-    w_s[tid] = w;
-    float sum = w * ml.y;
+    // Sums in units of the warp's own largest reference.
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+    float sum = f * ml.y;
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0) red[1][warp] = sum;
-    __syncthreads();
-    const int at = tid % (DH / 4), first = tid / (DH / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = first; i < pieces; i += LANES) {
-        const float4 v =
-            __ldcg(reinterpret_cast<const float4*>(P.ws_o + row_of(i) * DH) + at);
-        const float f = w_s[i];
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-    }
-    part[first][at] = acc;
+    auto add = [&](int i, const float4& v) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        acc.x = fmaf(fi, v.x, acc.x);
+        acc.y = fmaf(fi, v.y, acc.y);
+        acc.z = fmaf(fi, v.z, acc.z);
+        acc.w = fmaf(fi, v.w, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < mine) add(i, o[i]);
+#pragma unroll 4
+    for (int i = AHEAD; i < mine; ++i)
+        add(i, __ldcg(reinterpret_cast<const float4*>(from + row_of(w + i * WPR) * DH)));
+    part[warp][lane] = acc;
+    if (lane == 0) top[warp] = make_float2(m, sum);
     __syncthreads();
-    if (first == 0) {
-        float L = 0.f;
+    if (w || !there) return;
+    float M = m;
 #pragma unroll
-        for (int x = 0; x < MERGE_THREADS / 32; ++x) L += red[1][x];
+    for (int x = 1; x < WPR; ++x) M = fmaxf(M, top[warp + x].x);
+    float total = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int x = 1; x < LANES; ++x) {
-            const float4 v = part[x][at];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-        }
-        const float inv = L > 0.f ? *P.scale_dev[1] / L : isnan(L) ? NAN : 0.f;
-        uint2 v;
-        v.x = pack_half2(acc.x * inv, acc.y * inv);
-        v.y = pack_half2(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * ROWS + r, DH) + at * 4) = v;
+    for (int x = 0; x < WPR; ++x) {
+        const float2 tx = top[warp + x];
+        const float fx = tx.x == -INFINITY ? 0.f : ex2(tx.x - M);
+        const float4 v = part[warp + x][lane];
+        total += fx * tx.y;
+        acc.x = fmaf(fx, v.x, acc.x);
+        acc.y = fmaf(fx, v.y, acc.y);
+        acc.z = fmaf(fx, v.z, acc.z);
+        acc.w = fmaf(fx, v.w, acc.w);
     }
+    const float inv = total == 0.f ? 0.f : vscale / total;
+    uint2 v;
+    v.x = pack_half2(acc.x * inv, acc.y * inv);
+    v.y = pack_half2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * ROWS + r, DH) + d0) = v;
 }
 
 template <int DH, int NT>
 int launch(const Params& P, cudaStream_t stream) {
-    using L = Layout<DH, NT>;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(split_kernel<DH, NT>), L::BYTES) != GQA_OK)
+    using C = Config<DH, NT>;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(split_kernel<DH, NT>), C::BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(P.G);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, split_kernel<DH, NT>, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
-    // A block for each unit or for each cut, whichever are fewer.
-    const long long units = (long long)P.batch * P.hkv * P.groups;
-    const int by_unit = units < P.G - 1;
-    cfg.gridDim = dim3(by_unit ? (unsigned)units : P.G - 1, P.nq < 8 * NT ? P.nq : 8 * NT);
-    cfg.blockDim = dim3(MERGE_THREADS);
+    const int rows = P.nq < 8 * NT ? P.nq : 8 * NT;
+    cfg.blockDim = dim3(MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, merge_kernel<DH, NT>, P, by_unit) != cudaSuccess)
-        return GQA_ERR_CUDA;
-    return GQA_OK;
+    cudaError_t e;
+    if (P.by_unit) {
+        cfg.gridDim = dim3(P.batch * P.hkv * P.groups, rows, DH / 128);
+        e = cudaLaunchKernelEx(&cfg, merge_kernel<DH, NT, MERGE_WARPS>, P);
+    } else {
+        cfg.gridDim = dim3(P.G, (rows + 1) / 2, DH / 128);
+        e = cudaLaunchKernelEx(&cfg, merge_kernel<DH, NT, MERGE_WARPS / 2>, P);
+    }
+    return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
-// Packed rows of a unit: 8, or 16 where there are more.
-int unit_rows(int nq) { return nq <= 8 ? 8 : 16; }
+// Packed rows of a unit: all of a KV head's.
+int unit_rows(int nq) { return nq <= 32 ? (nq + 7) / 8 * 8 : 48; }
+
+template <int DH>
+int launch_rows(const Params& P, cudaStream_t stream) {
+    switch (unit_rows(P.nq)) {
+        case 8: return launch<DH, 1>(P, stream);
+        case 16: return launch<DH, 2>(P, stream);
+        case 24: return launch<DH, 3>(P, stream);
+        case 32: return launch<DH, 4>(P, stream);
+        default: return launch<DH, 6>(P, stream);
+    }
+}
 
 }  // namespace paged4
 
 size_t paged_fp4_workspace_bytes(int nq, int num_sms, int Dh) {
     return kWorkspaceCounterBytes +
-           (size_t)2 * num_sms * paged4::unit_rows(nq) * (Dh + 2) * sizeof(float);
+           (size_t)num_sms * (2 * paged4::unit_rows(nq < 48 ? nq : 48) * (Dh + 2) * sizeof(float) + sizeof(int4));
 }
 
 int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache,
@@ -933,8 +1030,10 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
     P.scale = scale;
     // No more ranges than tiles.
     const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len + TILE - 1LL) / TILE);
+    if (tiles > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
-    if (P.G > MERGE_THREADS) P.G = MERGE_THREADS;
+    if (P.G > MAX_RANGES) P.G = MAX_RANGES;
+    P.by_unit = (long long)batch * Hkv * P.groups < P.G;
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
     void* ws;
@@ -944,8 +1043,8 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
         return GQA_ERR_WORKSPACE;
     P.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWorkspaceCounterBytes);
     P.ws_ml = P.ws_o + (size_t)2 * P.G * rows * Dh;
-    if (Dh == 256) return rows == 8 ? launch<256, 1>(P, stream) : launch<256, 2>(P, stream);
-    return rows == 8 ? launch<128, 1>(P, stream) : launch<128, 2>(P, stream);
+    P.tasks = reinterpret_cast<int4*>(P.ws_ml + (size_t)2 * P.G * rows * 2);
+    return Dh == 256 ? launch_rows<256>(P, stream) : launch_rows<128>(P, stream);
 }
 
 }  // namespace gqa
