@@ -132,7 +132,7 @@ __device__ __forceinline__ Seqs seqs_small(const Params& P) {
 
 // starts[b] = tiles of the sequences before b, for b = 0 .. batch.  All threads of the
 // CTA (at least 256), with two barriers.
-__device__ __noinline__ void seqs_large(const Params& P, int* starts, int* totals) {
+__device__ __forceinline__ void seqs_large(const Params& P, int* starts, int* totals) {
     constexpr int EACH = MAX_BATCH / 256;
     const int tid = threadIdx.x, warp = tid >> 5;
     int n[EACH], sum = 0, incl = 0;
@@ -220,8 +220,8 @@ struct Pieces {
     }
 };
 
-// Wait for a barrier's phase, as mbar_wait, with what a long wait needs out of line.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+// Wait for a barrier's phase, as mbar_wait, a few tries before the clock is read.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
                                        unsigned* err) {
     return mbar_wait(bar, parity, abort, err);
 }
@@ -263,6 +263,151 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
     return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 
+// This CTA's range of the tiles.  Nothing of global memory is read or written before the
+// kernel in front has completed; this kernel's launch overlaps it.
+__device__ __forceinline__ Ranges begin_range(const Params& P, int* starts, int* totals, Pieces& it,
+                                              Seqs& seqs) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (P.batch <= LANES) {
+        seqs = seqs_small(P);
+    } else {
+        seqs_large(P, starts, totals);
+        seqs = Seqs{starts, 0, 0, 0, starts[P.batch]};
+    }
+    asm volatile("griddepcontrol.launch_dependents;");
+    const Ranges ranges(P, seqs);
+    const bool works = (int)blockIdx.x < ranges.G;
+    it.pos = works ? ranges.begin(blockIdx.x) : 0;
+    it.end = works ? ranges.begin(blockIdx.x + 1) : 0;
+    return ranges;
+}
+
+// What has no tiles (one warp): rows of sequences without a key are zeros; no units of
+// theirs, and no cut unit for ranges that get no tiles.
+__device__ __forceinline__ void finish_empty(const Params& P, const Pieces& it, int dh) {
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    if (it.pos == it.end && !P.by_unit && lane == 0) P.tasks[cta] = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int b = cta; b < P.batch; b += gridDim.x) {
+        const int raw = P.ctx_lens[b];
+        if ((raw < 0 || raw > P.max_ctx) && lane == 0) atomicOr(P.err, kErrBadCtxLen);
+        if (raw > 0) continue;
+        uint4* o = reinterpret_cast<uint4*>(P.out + (long long)b * P.R * P.hq * dh);
+#pragma unroll 1
+        for (int i = lane; i < P.R * P.hq * dh / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        if (P.by_unit)
+#pragma unroll 1
+            for (int u = lane; u < P.hkv * P.groups; u += 32)
+                P.tasks[b * P.hkv * P.groups + u] = make_int4(0, 0, 0, 0);
+    }
+}
+
+// The copies (COPY_WARPS warps): the pages of each tile into the ring, a stage freed by
+// its barrier full0 + 8 (STAGES + s).  A bulk copy is an instruction of one lane at a
+// time, about 70 cycles each: the 16 copies of a tile of 16-token pages are shared out
+// among four warps (one warp's took 1100 cycles a tile of head size 128, more than the
+// tile's time at the memory's rate; 62 us for 64 sequences of up to 8192 tokens).
+constexpr int COPY_WARPS = 4;
+
+template <int DH, int STAGES>
+__device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Seqs& seqs,
+                                           uint32_t ring, uint32_t full0, volatile int* abort_flag,
+                                           int warp) {
+    constexpr int ROWB = fp4::row_bytes(DH);
+    const int lane = threadIdx.x & 31;
+    // Rows of a copy, copies of a tile's K (and V); this lane's is of K or V, page p.
+    const int rows = min(P.page, TILE), lppt = max(7 - P.log2_page, 0), ppt = 1 << lppt;
+    const int kv = warp & 1, p = lane * (COPY_WARPS / 2) + (warp >> 1);
+    const uint8_t* const cache = kv ? P.cache[1] : P.cache[0];
+    const uint32_t to = ring + kv * (TILE * ROWB) + p * rows * ROWB;
+    const int begin = it.pos;
+    uint32_t n = 0;   // tiles so far
+    bool ok = true;
+    while (ok && it.next(P, seqs, begin)) {
+        const int pages = (it.s.ctx + P.page - 1) >> P.log2_page;
+        const int32_t* table = P.tables + (long long)it.b * P.table_stride;
+        // Table entries 32 at a time, a lane each, three lots ahead of their use.
+        auto entries = [&](int lot) {
+            const int e = lot * 32 + lane, j = it.jb + (e >> lppt);
+            if (j >= it.je) return 0;
+            const int lp = (tile_key(it.s, j) >> P.log2_page) + (e & (ppt - 1));
+            return lp < pages ? __ldg(table + lp) : 0;
+        };
+        int lot = 0, now = entries(0), next = entries(1), after = entries(2);
+#pragma unroll 1
+        for (int j = it.jb; j < it.je; ++j) {
+            const int e = (j - it.jb) << lppt;
+            if (e >> 5 != lot) {
+                ++lot;
+                now = next;
+                next = after;
+                after = entries(lot + 2);
+            }
+            int id = __shfl_sync(0xffffffffu, now, (e & 31) + (p & (ppt - 1)));
+            const int key0 = tile_key(it.s, j);
+            const int copies = min(ppt, pages - (key0 >> P.log2_page));
+            if (p < copies && (id < 0 || id >= P.num_pages)) {
+                atomicOr(P.err, kErrBadPageId);
+                id = 0;
+            }
+            const uint32_t mine = __popc(__ballot_sync(0xffffffffu, p < copies));
+            const int st = n % STAGES;
+            const uint32_t full = full0 + 8 * st;
+            int okw = 1;
+            if (lane == 0) {
+                okw = wait(full + 8 * STAGES, ((n / STAGES) & 1) ^ 1, abort_flag, P.err);
+                if (okw) mbar_arrive_expect_tx(full, mine * rows * ROWB);
+            }
+            ok = __shfl_sync(0xffffffffu, okw, 0);
+            if (!ok) break;
+            if (p < copies) {
+                const long long row =
+                    ((long long)id * P.hkv + it.h) * P.page + (key0 & (P.page - 1));
+                bulk_load(to + st * (2 * TILE * ROWB), cache + row * ROWB, rows * ROWB, full);
+            }
+            ++n;
+        }
+    }
+    if (!ok && lane == 0) {
+        // Unwind: every copy in flight lands before the CTA exits.
+#pragma unroll 1
+        for (int s = 0; s < STAGES; ++s) {
+            const uint32_t fills = n > (uint32_t)s ? (n - s + STAGES - 1) / STAGES : 0;
+            if (!fills) continue;
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(full0 + 8 * s, (fills - 1) & 1))
+                if (global_timer_ns() - t0 > 100000000ull) break;
+        }
+    }
+}
+
+// How a unit is joined, from the piece it begins with; a range whose last piece is no
+// cut unit's beginning has none to say.  (One thread.)
+__device__ __forceinline__ void write_task(const Params& P, const Pieces& it, const Ranges& ranges) {
+    const int unit = it.b * (P.hkv * P.groups) + it.u, cta = blockIdx.x;
+    const bool cut = it.jb == 0 && !it.whole();
+    if (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end))
+        P.tasks[P.by_unit ? unit : cta] =
+            make_int4(unit, cta * 2 + (it.first ? 0 : 1),
+                      cut ? ranges.of(it.pos - it.je + it.n - 1) - cta + 1 : 0, 0);
+}
+
+// Position of packed row r of a KV head, and whether a row there sees a key.
+__device__ __forceinline__ int row_pos(const Params& P, const Span& s, int r) {
+    return s.ctx - P.R + min(P.grp.div(r), P.R - 1);
+}
+__device__ __forceinline__ bool sees(const Params& P, int at, int key) {
+    return key <= at && (P.window == 0 || key > at - P.window || key < P.sinks);
+}
+// Some key of [key0, key0 + n) is hidden from some row; no row sees the key.
+__device__ __forceinline__ bool has_edge(const Params& P, const Span& s, int key0, int n) {
+    return key0 + n - 1 > s.ctx - P.R ||
+           (P.window > 0 && key0 <= s.ctx - 1 - P.window && key0 + n - 1 >= P.sinks);
+}
+__device__ __forceinline__ bool unseen(const Params& P, const Span& s, int key) {
+    return key >= s.ctx || (key < s.lo && key >= P.sinks);
+}
+
 // DH: head size; NT: eights of packed rows.
 template <int DH, int NT>
 struct Config {
@@ -273,8 +418,8 @@ struct Config {
     static constexpr int NG = NT <= 3 ? 2 : 1;
     static constexpr int NW = GW * NG;
     static constexpr int THREADS = 32 * NW + 128;
-    static constexpr int REGS_PRODUCTS = NG == 2 ? 112 : 232;
-    static constexpr int REGS_COPIES = NG == 2 ? 32 : 40;
+    static constexpr int REGS_PRODUCTS = NG == 2 ? 112 : 224;
+    static constexpr int REGS_COPIES = NG == 2 ? 32 : 56;
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
 
@@ -333,8 +478,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), GW);
+            mbar_init(full(s), COPY_WARPS);
+            mbar_init(empty(s), NW);
         }
         for (int g = 0; g < NG; ++g) mbar_init(group_bar(g), GW);
         mbar_init(group_bar(NG), NW);
@@ -343,107 +488,21 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
         fence_mbar_init();
     }
     __syncthreads();
-    // This CTA's range.  Nothing of global memory is read or written before the kernel in
-    // front has completed; this kernel's launch overlaps it.
-    auto begin_range = [&](Pieces& it, Seqs& seqs) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (P.batch <= LANES) {
-            seqs = seqs_small(P);
-        } else {
-            seqs_large(P, starts, totals);
-            seqs = Seqs{starts, 0, 0, 0, starts[P.batch]};
-        }
-        asm volatile("griddepcontrol.launch_dependents;");
-        const Ranges ranges(P, seqs);
-        const bool works = (int)blockIdx.x < ranges.G;
-        it.pos = works ? ranges.begin(blockIdx.x) : 0;
-        it.end = works ? ranges.begin(blockIdx.x + 1) : 0;
-        return ranges;
-    };
     const int cta = blockIdx.x;
 
     if (warp >= NW) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
       Seqs seqs;
       Pieces it;
-      begin_range(it, seqs);
-      const int begin = it.pos;
-      if (warp == NW + 1) {
-        // ------------------------------------------------------------ what has no tiles
-        // Rows of sequences without a key are zeros; no units of theirs, and no cut
-        // unit for ranges that get no tiles.
-        if (it.pos == it.end && !P.by_unit && lane == 0) P.tasks[cta] = make_int4(0, 0, 0, 0);
-        for (int b = cta; b < P.batch; b += gridDim.x) {
-            const int raw = P.ctx_lens[b];
-            if ((raw < 0 || raw > P.max_ctx) && lane == 0) atomicOr(P.err, kErrBadCtxLen);
-            if (raw > 0) continue;
-            uint4* o = reinterpret_cast<uint4*>(P.out + (long long)b * P.R * P.hq * DH);
-            for (int i = lane; i < P.R * P.hq * DH / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-            if (P.by_unit)
-                for (int u = lane; u < P.hkv * P.groups; u += 32)
-                    P.tasks[b * P.hkv * P.groups + u] = make_int4(0, 0, 0, 0);
-        }
-      } else if (warp == NW) {
-        // ------------------------------------------------------------ copies
-        // Lanes 0 .. 15 copy K's pages of a tile, 16 .. 31 V's.
-        const int kv = lane >> 4, p = lane & 15;
-        const int rows = min(P.page, TILE), ppt = TILE / rows;   // rows of a copy, copies of a tile
-        uint32_t n = 0;   // tiles so far
-        bool ok = true;
-        while (ok && it.next(P, seqs, begin)) {
-            const int pages = (it.s.ctx + P.page - 1) >> P.log2_page;
-            const int32_t* table = P.tables + (long long)it.b * P.table_stride;
-            auto entry = [&](int j) {
-                if (j >= it.je) return 0;
-                const int lp = (tile_key(it.s, j) >> P.log2_page) + p;
-                return p < ppt && lp < pages ? __ldg(table + lp) : 0;
-            };
-            int id = entry(it.jb), id1 = entry(it.jb + 1);
-            for (int j = it.jb; j < it.je; ++j) {
-                const int id2 = entry(j + 2);
-                const int key0 = tile_key(it.s, j);
-                const int copies = min(ppt, pages - (key0 >> P.log2_page));
-                if (p < copies && (id < 0 || id >= P.num_pages)) {
-                    atomicOr(P.err, kErrBadPageId);
-                    id = 0;
-                }
-                const int st = n % STAGES;
-                int okw = 1;
-                if (lane == 0) {
-                    okw = wait(empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, P.err);
-                    if (okw) mbar_arrive_expect_tx(full(st), 2 * copies * rows * ROWB);
-                }
-                ok = __shfl_sync(0xffffffffu, okw, 0);
-                if (!ok) break;
-                if (p < copies) {
-                    const long long row = ((long long)id * P.hkv + it.h) * P.page +
-                                          (key0 & (P.page - 1));
-                    bulk_load(smem_u32(smem) + C::OFF_RING + st * C::STAGE + kv * (TILE * ROWB) +
-                                  p * rows * ROWB,
-                              P.cache[kv] + row * ROWB, rows * ROWB, full(st));
-                }
-                ++n;
-                id = id1;
-                id1 = id2;
-            }
-        }
-        if (!ok && lane == 0) {
-            // Unwind: every copy in flight lands before the CTA exits.
-            for (int s = 0; s < STAGES; ++s) {
-                const uint32_t fills = n > (uint32_t)s ? (n - s + STAGES - 1) / STAGES : 0;
-                if (!fills) continue;
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(full(s), (fills - 1) & 1))
-                    if (global_timer_ns() - t0 > 100000000ull) break;
-            }
-        }
-      }
+      begin_range(P, starts, totals, it, seqs);
+      if (warp == NW) finish_empty(P, it, DH);
+      copy_tiles<DH, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag, warp - NW);
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
         Seqs seqs;
         Pieces it;
-        const Ranges ranges = begin_range(it, seqs);
+        const Ranges ranges = begin_range(P, starts, totals, it, seqs);
         const int begin = it.pos;
         const int group = warp / GW, gwarp = warp % GW;
         const int gid = lane >> 2, t = lane & 3;
@@ -472,16 +531,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
         while (ok && it.next(P, seqs, begin)) {
             const Span s = it.s;
             const int row0 = it.g * ROWS;
-            if (threadIdx.x == 0) {
-                // The piece a unit begins with says how it is joined; a range whose last
-                // piece is no cut unit's beginning has none.
-                const int unit = it.b * (P.hkv * P.groups) + it.u;
-                const bool cut = it.jb == 0 && !it.whole();
-                if (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end))
-                    P.tasks[P.by_unit ? unit : cta] =
-                        make_int4(unit, cta * 2 + (it.first ? 0 : 1),
-                                  cut ? ranges.of(it.pos - it.je + it.n - 1) - cta + 1 : 0, 0);
-            }
+            if (threadIdx.x == 0) write_task(P, it, ranges);
+#pragma unroll 1
             for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
                 const int r = i / (DH / 8), c = i % (DH / 8);
                 const uint4 v = row0 + r < P.nq
@@ -493,13 +544,6 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             }
             ok = meet();
             if (!ok) break;
-            // Position of packed row r (of this unit's ROWS).
-            auto row_pos = [&](int r) {
-                return s.ctx - P.R + min(P.grp.div(row0 + r), P.R - 1);
-            };
-            auto sees = [&](int at, int key) {
-                return key <= at && (P.window == 0 || key > at - P.window || key < P.sinks);
-            };
             float o[4][NT][4];              // places 8 gid + 2 i, + 1 of the slice; rows 2 t, 2 t + 1
             float mref[NT][2], l[NT][2];    // of rows 2 t, 2 t + 1
 #pragma unroll
@@ -513,17 +557,18 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             }
 
             for (int j = it.jb; j < it.je; ++j, ++n) {
-                if (NG > 1 && n % NG != (uint32_t)group) continue;
+                // (Every warp sees every tile land and lets go of it, the other groups' too:
+                // a warp that skipped a phase of a stage could not tell it from the next.)
                 const int st = n % STAGES;
                 ok = wait(full(st), (n / STAGES) & 1, abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if (NG > 1 && n % NG != (uint32_t)group) {
+                    if (lane == 0) mbar_arrive(empty(st));
+                    continue;
+                }
                 const int key0 = tile_key(s, j);
-                const int last = s.ctx - 1;
-                // Some key of the tile is hidden from some row.
-                const bool edge = key0 + TILE - 1 > s.ctx - P.R ||
-                                  (P.window > 0 && key0 <= last - P.window &&
-                                   key0 + TILE - 1 >= P.sinks);
+                const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
                 const uint8_t* vst = kst + TILE * ROWB;
                 uint8_t* const pt = sp + (mine & 1) * ROWS * C::P_ROW;
@@ -596,7 +641,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (!sees(row_pos(nt * 8 + 2 * t + (e & 1)),
+                            if (!sees(P, row_pos(P, s, row0 + nt * 8 + 2 * t + (e & 1)),
                                       key0 + gwarp * 16 + key_of<DH>(gid + (e & 2) * 4)))
                                 sc[nt][e] = -INFINITY;
                 }
@@ -681,7 +726,37 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 constexpr int STEPS = TILE / 16 / C::SHARES;
                 const uint8_t* const vcol = vst + slice * 32 + gid * 4;
                 const uint32_t pick = (gid >> 1) | ((gid >> 1) + 4) << 4;
+                uint32_t c01[STEPS], c23[STEPS];   // scales of a step's pairs of keys
+#pragma unroll
+                for (int x = 0; x < STEPS; ++x) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = *reinterpret_cast<const uint32_t*>(
+                            vst + ((share * STEPS + x) * 16 +
+                                   key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB +
+                            DH / 2 + slice * 4);
+                    c01[x] = __byte_perm(u[0], u[1], pick) & 0xffff;
+                    c23[x] = __byte_perm(u[2], u[3], pick) & 0xffff;
+                }
                 bool apart = false;
+                if (edge) {
+                    // Keys no row sees may hold anything: scales of zero.  NaN scales of
+                    // keys that some rows see and others do not are zeros too (0 * NaN), and
+                    // the rows that see them are made NaN below.
+#pragma unroll
+                    for (int x = 0; x < STEPS; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + (share * STEPS + x) * 16 +
+                                            key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
+                            uint32_t& c = e < 2 ? c01[x] : c23[x];
+                            const uint32_t in = 0x7fu << (e & 1) * 8;
+                            const bool none = unseen(P, s, key), nan = (c & in) == in;
+                            if (none || nan) c &= ~(0xffu << (e & 1) * 8);
+                            apart |= nan && !none;
+                        }
+                }
 #pragma unroll
                 for (int x = 0; x < STEPS; x += 2) {
                     uint32_t pf[NT][4];   // B operands of two steps
@@ -698,33 +773,12 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int k0 = (share * STEPS + x + y) * 16;
-                        uint32_t w[4], u[4];
+                        uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int k = k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
-                            w[e] = *reinterpret_cast<const uint32_t*>(vcol + k * ROWB);
-                            const uint8_t* sc4 = vst + k * ROWB + DH / 2 + slice * 4;
-                            u[e] = *reinterpret_cast<const uint32_t*>(sc4);
-                        }
-                        uint32_t c01 = __byte_perm(u[0], u[1], pick) & 0xffff;
-                        uint32_t c23 = __byte_perm(u[2], u[3], pick) & 0xffff;
-                        if (edge) {
-                            // Keys no row sees may hold anything: scales of zero.  NaN
-                            // scales of keys that some rows see and others do not are
-                            // zeros too (0 * NaN), and the rows that see them are made NaN
-                            // below.
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int key = key0 + k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
-                                uint32_t& c = e < 2 ? c01 : c23;
-                                const uint32_t in = 0x7fu << (e & 1) * 8;
-                                const bool unseen = key > last || (key < s.lo && key >= P.sinks);
-                                const bool nan = (c & in) == in;
-                                if (unseen || nan) c &= ~(0xffu << (e & 1) * 8);
-                                apart |= nan && !unseen;
-                            }
-                        }
-                        const uint32_t u01 = fp4::scales2(c01), u23 = fp4::scales2(c23);
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = *reinterpret_cast<const uint32_t*>(
+                                vcol + (k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB);
+                        const uint32_t u01 = fp4::scales2(c01[x + y]), u23 = fp4::scales2(c23[x + y]);
                         uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
                         fp4::decode8(low_nibbles(w[0], w[1]), lo0);
                         fp4::decode8(high_nibbles(w[0], w[1]), hi0);
@@ -752,7 +806,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                             continue;
 #pragma unroll
                         for (int r = 0; r < 2 * NT; ++r)
-                            if (sees(row_pos((r >> 1) * 8 + 2 * t + (r & 1)), key)) poison |= 1u << r;
+                            if (sees(P, row_pos(P, s, row0 + (r >> 1) * 8 + 2 * t + (r & 1)), key))
+                                poison |= 1u << r;
                     }
 #pragma unroll
                     for (int r = 0; r < 2 * NT; ++r)
@@ -798,6 +853,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                             make_float2(o[0][nt][e], o[0][nt][e + 2]);
                 ok = meet();
                 if (!ok) break;
+#pragma unroll 1
                 for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
                     const int row = i / (DH / 8), at = i % (DH / 8);   // at: slice, gid
                     if (row0 + row >= P.nq) break;
@@ -848,6 +904,395 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[i][nt][e] = o[i + 1][nt][e];
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Up to eight packed rows: every warp by itself, 32 keys of a tile, all of D, with its own
+// references, until the end of a piece.  (P never leaves the warp, and nothing meets in
+// a tile; more rows' sums of all of D do not fit a warp's registers.)
+template <int DH>
+struct Narrow {
+    static constexpr int NG = 2;           // tiles under way
+    static constexpr int KZ = 2;           // sixteens of keys of a warp
+    static constexpr int GW = 8 / KZ;      // warps of a tile
+    static constexpr int NW = NG * GW;
+    static constexpr int THREADS = 32 * NW + 128;
+    static constexpr int REGS_PRODUCTS = 224, REGS_COPIES = 56;
+    static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
+    static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
+    static constexpr int ROWB = fp4::row_bytes(DH);
+    static constexpr int STAGE = 2 * TILE * ROWB;
+    static constexpr int STAGES = DH == 256 ? 5 : 10;   // 184 KB
+    // One round of the join: eight places of every gid, of all warps.
+    static constexpr int JOIN_ROW = 64 + 4;
+    static constexpr int OFF_JOIN = 0;                                   // [NW][8][JOIN_ROW]
+    static constexpr int OFF_ML = OFF_JOIN + NW * 8 * JOIN_ROW * 4;       // [NW][8][2]
+    static constexpr int OFF_STARTS = OFF_ML + NW * 8 * 8;
+    static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
+    static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
+    static constexpr int OFF_ABORT = OFF_BARS + (2 * STAGES + 1) * 8;
+    static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
+    static constexpr int BYTES = OFF_RING + STAGES * STAGE;
+    static_assert(BYTES <= 232448, "shared memory");
+};
+
+template <int DH>
+__global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Params P) {
+    using C = Narrow<DH>;
+    constexpr int ROWB = C::ROWB, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
+    constexpr int MT = DH / 16, KZ = C::KZ;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
+    int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
+    const uint32_t bars = smem_u32(smem + C::OFF_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    const uint32_t meet_bar = bars + 8 * (2 * STAGES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bars + 8 * s, COPY_WARPS);
+            mbar_init(bars + 8 * (STAGES + s), NW);
+        }
+        mbar_init(meet_bar, NW);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (warp >= NW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
+        Seqs seqs;
+        Pieces it;
+        begin_range(P, starts, totals, it, seqs);
+        if (warp == NW) finish_empty(P, it, DH);
+        copy_tiles<DH, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
+                               warp - NW);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
+        Seqs seqs;
+        Pieces it;
+        const Ranges ranges = begin_range(P, starts, totals, it, seqs);
+        const int begin = it.pos;
+        const int group = warp / C::GW, gwarp = warp % C::GW;
+        const int gid = lane >> 2, t = lane & 3;
+        float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+        float* const sml = reinterpret_cast<float*>(smem + C::OFF_ML);
+        uint32_t phase = 0;
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(meet_bar);
+            const bool ok = wait(meet_bar, phase, abort_flag, P.err);
+            phase ^= 1;
+            return __all_sync(0xffffffffu, ok);
+        };
+        const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
+        uint32_t n = 0;     // tiles of the CTA so far
+        bool ok = true;
+        while (ok && it.next(P, seqs, begin)) {
+            const Span s = it.s;
+            if (threadIdx.x == 0) write_task(P, it, ranges);
+            // The lane's places of row gid: the products' B operands.
+            uint4 q[DH / 32];
+            {
+                const bool there = gid < P.nq;
+                const __half* src = P.q + (there ? row_offset(P, it.b, it.h, gid, DH) : 0);
+#pragma unroll
+                for (int i = 0; i < DH / 32; ++i)
+                    q[i] = there ? *reinterpret_cast<const uint4*>(
+                                       src + (DH == 256 ? t * 64 + i * 8
+                                                        : (i >> 1) * 64 + t * 16 + (i & 1) * 8))
+                                 : make_uint4(0, 0, 0, 0);
+            }
+            float o[MT][4];
+            float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+#pragma unroll 1
+            for (int j = it.jb; j < it.je; ++j, ++n) {
+                // (Every warp sees every tile land and lets go of it, the other group's too:
+                // a warp that skipped a phase of a stage could not tell it from the next.)
+                const int st = n % STAGES;
+                ok = wait(bars + 8 * st, (n / STAGES) & 1, abort_flag, P.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (n % NG != (uint32_t)group) {
+                    if (lane == 0) mbar_arrive(bars + 8 * (STAGES + st));
+                    continue;
+                }
+                const int k0 = tile_key(s, j) + gwarp * 16 * KZ;
+                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE + gwarp * 16 * KZ * ROWB;
+                const uint8_t* vst = kst + TILE * ROWB;
+                const bool edge = has_edge(P, s, k0, 16 * KZ);
+                // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
+                float sc[KZ][2][4];
+#pragma unroll
+                for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[z][x][e] = 0.f;
+                constexpr int HALF = DH / 64;   // words of a lane and key in one load
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w[KZ][2][HALF], u[KZ][2][HALF / 2];
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint8_t* row = kst + (z * 16 + key_of<DH>(gid + 8 * e)) * ROWB;
+                            if constexpr (DH == 256) {
+                                const uint4 v =
+                                    *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
+                                w[z][e][0] = v.x, w[z][e][1] = v.y;
+                                w[z][e][2] = v.z, w[z][e][3] = v.w;
+                                const uint32_t c = fp4::scales2(*reinterpret_cast<const uint16_t*>(
+                                    row + DH / 2 + t * 4 + x * 2));
+                                u[z][e][0] = __byte_perm(c, 0, 0x1010);
+                                u[z][e][1] = __byte_perm(c, 0, 0x3232);
+                            } else {
+                                // (places 16 t and 64 + 16 t)
+                                const uint2 v =
+                                    *reinterpret_cast<const uint2*>(row + t * 8 + x * 32);
+                                w[z][e][0] = v.x, w[z][e][1] = v.y;
+                                u[z][e][0] = fp4::scales2(row[DH / 2 + t + x * 4] * 0x101u);
+                            }
+                        }
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+#pragma unroll
+                        for (int z = 0; z < KZ; ++z) {
+                            uint32_t a[4], b[4];
+                            fp4::decode8(w[z][0][i], a);
+                            fp4::decode8(w[z][1][i], b);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                a[e] = fp4::mul2(a[e], u[z][0][i / 2]);
+                                b[e] = fp4::mul2(b[e], u[z][1][i / 2]);
+                            }
+                            const uint4 qv = q[x * HALF + i];
+                            mma16816(sc[z][0], a[0], b[0], a[1], b[1], qv.x, qv.y);
+                            mma16816(sc[z][1], a[2], b[2], a[3], b[3], qv.z, qv.w);
+                        }
+                }
+                float sv[KZ][4];
+#pragma unroll
+                for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sv[z][e] = (sc[z][0][e] + sc[z][1][e]) * sl2;
+                if (edge) {
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!sees(P, row_pos(P, s, 2 * t + (e & 1)),
+                                      k0 + z * 16 + key_of<DH>(gid + (e & 2) * 4)))
+                                sv[z][e] = -INFINITY;
+                }
+                bool exceed = false;
+#pragma unroll
+                for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        exceed |= sv[z][e] > mref[e & 1] + RESCALE_THRESHOLD;
+                if (__any_sync(0xffffffffu, exceed)) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(sv[0][e], sv[0][e + 2]);
+#pragma unroll
+                        for (int z = 1; z < KZ; ++z) m = fmaxf(m, fmaxf(sv[z][e], sv[z][e + 2]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1)
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        f[e] = 1.f;
+                        if (m > mref[e] + RESCALE_THRESHOLD) {
+                            f[e] = ex2(mref[e] - m);
+                            mref[e] = m;
+                        }
+                        l[e] *= f[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        o[i][0] *= f[0];
+                        o[i][1] *= f[1];
+                        o[i][2] *= f[0];
+                        o[i][3] *= f[1];
+                    }
+                }
+                // ---- P, transposed into the second product's B operand
+                uint32_t pf[KZ][2];
+                {
+                    const float m0 = mref[0] == -INFINITY ? 0.f : mref[0];
+                    const float m1 = mref[1] == -INFINITY ? 0.f : mref[1];
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z) {
+                        const float p0 = ex2(sv[z][0] - m0), p1 = ex2(sv[z][1] - m1);
+                        const float p2 = ex2(sv[z][2] - m0), p3 = ex2(sv[z][3] - m1);
+                        l[0] += p0 + p2;
+                        l[1] += p1 + p3;
+                        pf[z][0] = transpose8(pack_half2(p0, p1));
+                        pf[z][1] = transpose8(pack_half2(p2, p3));
+                    }
+                }
+                // ---- O += V^T P^T
+                constexpr int VW = DH / 64;   // words of a lane and key
+                uint32_t c[KZ][4];            // a scale for each 16 values
+#pragma unroll
+                for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint8_t* at =
+                            vst + (z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB +
+                            DH / 2 + gid * (DH / 128);
+                        if constexpr (DH == 256) c[z][e] = *reinterpret_cast<const uint16_t*>(at);
+                        else c[z][e] = *at;
+                    }
+                bool apart = false;
+                if (edge) {
+                    // Keys no row sees may hold anything: scales of zero.  NaN scales of
+                    // keys that some rows see and others do not are zeros too (0 * NaN), and
+                    // the rows that see them are made NaN below.
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
+                            if (unseen(P, s, k0 + k)) c[z][e] = 0;
+#pragma unroll
+                            for (int y = 0; y < DH / 128; ++y)
+                                if ((c[z][e] >> 8 * y & 0x7f) == 0x7f) {
+                                    apart = true;
+                                    c[z][e] &= ~(0xffu << 8 * y);
+                                }
+                        }
+                }
+#pragma unroll
+                for (int z = 0; z < KZ; ++z) {
+                    uint32_t w[4][VW];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint8_t* row =
+                            vst + (z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB;
+                        if constexpr (DH == 256) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(row + gid * 16);
+                            w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(row + gid * 8);
+                            w[e][0] = v.x, w[e][1] = v.y;
+                        }
+                    }
+                    // (words 2 i and 2 i + 1 share a scale)
+                    uint32_t u01[DH / 128], u23[DH / 128];
+#pragma unroll
+                    for (int y = 0; y < DH / 128; ++y) {
+                        u01[y] = fp4::scales2(__byte_perm(c[z][0], c[z][1], y ? 0x0051 : 0x0040));
+                        u23[y] = fp4::scales2(__byte_perm(c[z][2], c[z][3], y ? 0x0051 : 0x0040));
+                    }
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) {
+                        uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
+                        fp4::decode8(low_nibbles(w[0][i], w[1][i]), lo0);
+                        fp4::decode8(high_nibbles(w[0][i], w[1][i]), hi0);
+                        fp4::decode8(low_nibbles(w[2][i], w[3][i]), lo1);
+                        fp4::decode8(high_nibbles(w[2][i], w[3][i]), hi1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mma16816(o[4 * i + e], fp4::mul2(lo0[e], u01[i / 2]),
+                                     fp4::mul2(hi0[e], u01[i / 2]), fp4::mul2(lo1[e], u23[i / 2]),
+                                     fp4::mul2(hi1[e], u23[i / 2]), pf[z][0], pf[z][1]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, apart)) {
+                    uint32_t poison = 0;   // bits: block * 2 + row
+#pragma unroll 1
+                    for (int k = 0; k < 16 * KZ; ++k)
+#pragma unroll
+                        for (int y = 0; y < DH / 128; ++y)
+                            if ((vst[k * ROWB + DH / 2 + gid * (DH / 128) + y] & 0x7f) == 0x7f)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (sees(P, row_pos(P, s, 2 * t + e), k0 + k))
+                                        poison |= 1u << (2 * y + e);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (poison >> (i / 8 * 2 + e) & 1) o[i][e] = o[i][e + 2] = NAN;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + 8 * (STAGES + st));
+            }
+            if (!ok) break;
+
+            // ---------------------------------------------------------- end of the piece
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+                if (gid == 0)
+                    *reinterpret_cast<float2*>(sml + (warp * 8 + 2 * t + e) * 2) =
+                        make_float2(mref[e], l[e]);
+            }
+            // O in rounds of a word of each lane's places: the warps' sums go through shared
+            // memory and are added in order, in units of the largest reference.
+            const int slot = blockIdx.x * 2 + (it.first ? 0 : 1);
+            const bool whole = it.whole();
+#pragma unroll 1
+            for (int r = 0; r < MT / 4; ++r) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float4* to = reinterpret_cast<float4*>(
+                        join + (warp * 8 + 2 * t + e) * C::JOIN_ROW + gid * 8);
+                    to[0] = make_float4(o[0][e], o[0][e + 2], o[1][e], o[1][e + 2]);
+                    to[1] = make_float4(o[2][e], o[2][e + 2], o[3][e], o[3][e + 2]);
+                }
+                ok = meet();
+                if (!ok) break;
+                // A thread's two places: row tid / 32, of gid (tid % 32) / 4.
+                const int row = threadIdx.x >> 5, at = threadIdx.x & 31;
+                if (row < P.nq) {
+                    float2 ml[NW];
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < NW; ++x) {
+                        ml[x] = *reinterpret_cast<const float2*>(sml + (x * 8 + row) * 2);
+                        M = fmaxf(M, ml[x].x);
+                    }
+                    float2 a = make_float2(0.f, 0.f);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < NW; ++x) {
+                        const float f = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - M);
+                        const float2 v = *reinterpret_cast<const float2*>(
+                            join + (x * 8 + row) * C::JOIN_ROW + at * 2);
+                        sum = fmaf(f, ml[x].y, sum);
+                        a.x = fmaf(f, v.x, a.x);
+                        a.y = fmaf(f, v.y, a.y);
+                    }
+                    const int d = (at >> 2) * (DH / 8) + r * 8 + (at & 3) * 2;
+                    if (whole) {
+                        // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
+                        const float inv = sum == 0.f ? 0.f : *P.scale_dev[1] / sum;
+                        *reinterpret_cast<uint32_t*>(P.out + row_offset(P, it.b, it.h, row, DH) + d) =
+                            pack_half2(a.x * inv, a.y * inv);
+                    } else {
+                        *reinterpret_cast<float2*>(P.ws_o + ((long long)slot * 8 + row) * DH + d) = a;
+                        if (at == 0 && r == 0)
+                            *reinterpret_cast<float2*>(P.ws_ml + ((long long)slot * 8 + row) * 2) =
+                                make_float2(M, sum);
+                    }
+                }
+                ok = meet();
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < MT - 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][e] = o[i + 4][e];
             }
         }
     }
@@ -945,8 +1390,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P)
 
 template <int DH, int NT>
 int launch(const Params& P, cudaStream_t stream) {
-    using C = Config<DH, NT>;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(split_kernel<DH, NT>), C::BYTES) != GQA_OK)
+    // (kernel and sizes of one eight of rows, or of more)
+    using C = typename std::conditional<NT == 1, Narrow<DH>, Config<DH, NT == 1 ? 2 : NT>>::type;
+    void (*kernel)(Params);
+    if constexpr (NT == 1) kernel = narrow_kernel<DH>;
+    else kernel = split_kernel<DH, NT>;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), C::BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -958,7 +1407,7 @@ int launch(const Params& P, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, split_kernel<DH, NT>, P) != cudaSuccess) return GQA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
     const int rows = P.nq < 8 * NT ? P.nq : 8 * NT;
     cfg.blockDim = dim3(MERGE_WARPS * 32);
