@@ -302,16 +302,29 @@ __device__ __forceinline__ void finish_empty(const Params& P, const Pieces& it, 
     }
 }
 
-// The copies (COPY_WARPS warps): the pages of each tile into the ring, a stage freed by
-// its barrier full0 + 8 (STAGES + s).  A bulk copy is an instruction of one lane at a
+// Tiles are dealt to the NG groups in turn, tile n to group n % NG as its tile i = n / NG.
+// Its data go to stage n % STAGES of the ring, its barriers are number
+// (n % NG) STAGES + i % STAGES of NG STAGES "full" and as many "empty" ones: a group's
+// own, so that it sees each of their phases (with a barrier for each stage a group would
+// skip the others' phases, and could not tell one it waits for from the one before).
+template <int NG, int STAGES>
+__device__ __forceinline__ uint32_t tile_bar(uint32_t n) {
+    return 8 * ((n % NG) * STAGES + n / NG % STAGES);
+}
+template <int NG, int STAGES>
+__device__ __forceinline__ uint32_t tile_phase(uint32_t n) {
+    return n / NG / STAGES & 1;
+}
+
+// The copies (COPY_WARPS warps): the pages of each tile into the ring.  A bulk copy is an instruction of one lane at a
 // time, about 70 cycles each: the 16 copies of a tile of 16-token pages are shared out
 // among four warps (one warp's took 1100 cycles a tile of head size 128, more than the
 // tile's time at the memory's rate; 62 us for 64 sequences of up to 8192 tokens).
 constexpr int COPY_WARPS = 4;
 
-template <int DH, int STAGES>
+template <int DH, int NG, int STAGES>
 __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Seqs& seqs,
-                                           uint32_t ring, uint32_t full0, volatile int* abort_flag,
+                                           uint32_t ring, uint32_t bars, volatile int* abort_flag,
                                            int warp) {
     constexpr int ROWB = fp4::row_bytes(DH);
     const int lane = threadIdx.x & 31;
@@ -351,11 +364,12 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
                 id = 0;
             }
             const uint32_t mine = __popc(__ballot_sync(0xffffffffu, p < copies));
-            const int st = n % STAGES;
-            const uint32_t full = full0 + 8 * st;
+            const uint32_t full = bars + tile_bar<NG, STAGES>(n);
             int okw = 1;
             if (lane == 0) {
-                okw = wait(full + 8 * STAGES, ((n / STAGES) & 1) ^ 1, abort_flag, P.err);
+                if (n >= STAGES)
+                    okw = wait(bars + 8 * NG * STAGES + tile_bar<NG, STAGES>(n - STAGES),
+                               tile_phase<NG, STAGES>(n - STAGES), abort_flag, P.err);
                 if (okw) mbar_arrive_expect_tx(full, mine * rows * ROWB);
             }
             ok = __shfl_sync(0xffffffffu, okw, 0);
@@ -363,7 +377,7 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
             if (p < copies) {
                 const long long row =
                     ((long long)id * P.hkv + it.h) * P.page + (key0 & (P.page - 1));
-                bulk_load(to + st * (2 * TILE * ROWB), cache + row * ROWB, rows * ROWB, full);
+                bulk_load(to + n % STAGES * (2 * TILE * ROWB), cache + row * ROWB, rows * ROWB, full);
             }
             ++n;
         }
@@ -371,11 +385,9 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
     if (!ok && lane == 0) {
         // Unwind: every copy in flight lands before the CTA exits.
 #pragma unroll 1
-        for (int s = 0; s < STAGES; ++s) {
-            const uint32_t fills = n > (uint32_t)s ? (n - s + STAGES - 1) / STAGES : 0;
-            if (!fills) continue;
+        for (uint32_t m = n > STAGES ? n - STAGES : 0; m < n; ++m) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(full0 + 8 * s, (fills - 1) & 1))
+            while (!mbar_try_wait(bars + tile_bar<NG, STAGES>(m), tile_phase<NG, STAGES>(m)))
                 if (global_timer_ns() - t0 > 100000000ull) break;
         }
     }
@@ -444,7 +456,7 @@ struct Config {
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
     static constexpr int MAX_STAGES = 10;
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
-    static constexpr int OFF_FLAG = OFF_BARS + (2 * MAX_STAGES + NG + 1) * 8;   // [NG][2]
+    static constexpr int OFF_FLAG = OFF_BARS + (2 * NG * MAX_STAGES + NG + 1) * 8;   // [NG][2]
     static constexpr int OFF_ABORT = OFF_FLAG + NG * 2 * 4;
     static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
     // The bytes in flight set the copy rate: all that is left, up to 184 KB.
@@ -471,15 +483,13 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-    auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (STAGES + s); };
-    auto group_bar = [&](int g) { return bars + 8u * (2 * STAGES + g); };   // g = NG: all
+    auto group_bar = [&](int g) { return bars + 8u * (2 * NG * STAGES + g); };   // g = NG: all
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full(s), COPY_WARPS);
-            mbar_init(empty(s), NW);
+        for (int i = 0; i < NG * STAGES; ++i) {
+            mbar_init(bars + 8 * i, COPY_WARPS);
+            mbar_init(bars + 8 * (NG * STAGES + i), GW);
         }
         for (int g = 0; g < NG; ++g) mbar_init(group_bar(g), GW);
         mbar_init(group_bar(NG), NW);
@@ -496,7 +506,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
       Pieces it;
       begin_range(P, starts, totals, it, seqs);
       if (warp == NW) finish_empty(P, it, DH);
-      copy_tiles<DH, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag, warp - NW);
+      copy_tiles<DH, NG, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
+                                 warp - NW);
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
@@ -556,17 +567,15 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
             }
 
-            for (int j = it.jb; j < it.je; ++j, ++n) {
-                // (Every warp sees every tile land and lets go of it, the other groups' too:
-                // a warp that skipped a phase of a stage could not tell it from the next.)
-                const int st = n % STAGES;
-                ok = wait(full(st), (n / STAGES) & 1, abort_flag, P.err);
+            const uint32_t n0 = n;   // the piece's first tile
+            n += it.je - it.jb;
+#pragma unroll 1
+            for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
+                const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
+                const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
+                ok = wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (NG > 1 && n % NG != (uint32_t)group) {
-                    if (lane == 0) mbar_arrive(empty(st));
-                    continue;
-                }
                 const int key0 = tile_key(s, j);
                 const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
@@ -817,7 +826,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                                 o[i][r >> 1][r & 1] = o[i][r >> 1][(r & 1) + 2] = NAN;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty(st));
+                if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
                 ++mine;
             }
             if (!ok) break;
@@ -933,7 +942,7 @@ struct Narrow {
     static constexpr int OFF_STARTS = OFF_ML + NW * 8 * 8;
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
-    static constexpr int OFF_ABORT = OFF_BARS + (2 * STAGES + 1) * 8;
+    static constexpr int OFF_ABORT = OFF_BARS + (2 * NG * STAGES + 1) * 8;
     static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
     static constexpr int BYTES = OFF_RING + STAGES * STAGE;
     static_assert(BYTES <= 232448, "shared memory");
@@ -949,12 +958,12 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-    const uint32_t meet_bar = bars + 8 * (2 * STAGES);
+    const uint32_t meet_bar = bars + 8 * (2 * NG * STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(bars + 8 * s, COPY_WARPS);
-            mbar_init(bars + 8 * (STAGES + s), NW);
+        for (int i = 0; i < NG * STAGES; ++i) {
+            mbar_init(bars + 8 * i, COPY_WARPS);
+            mbar_init(bars + 8 * (NG * STAGES + i), C::GW);
         }
         mbar_init(meet_bar, NW);
         *abort_flag = 0;
@@ -967,8 +976,8 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
         Pieces it;
         begin_range(P, starts, totals, it, seqs);
         if (warp == NW) finish_empty(P, it, DH);
-        copy_tiles<DH, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
-                               warp - NW);
+        copy_tiles<DH, NG, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
+                                   warp - NW);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
         Seqs seqs;
@@ -1012,18 +1021,15 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
+            const uint32_t n0 = n;   // the piece's first tile
+            n += it.je - it.jb;
 #pragma unroll 1
-            for (int j = it.jb; j < it.je; ++j, ++n) {
-                // (Every warp sees every tile land and lets go of it, the other group's too:
-                // a warp that skipped a phase of a stage could not tell it from the next.)
-                const int st = n % STAGES;
-                ok = wait(bars + 8 * st, (n / STAGES) & 1, abort_flag, P.err);
+            for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
+                const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
+                const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
+                ok = wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (n % NG != (uint32_t)group) {
-                    if (lane == 0) mbar_arrive(bars + 8 * (STAGES + st));
-                    continue;
-                }
                 const int k0 = tile_key(s, j) + gwarp * 16 * KZ;
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE + gwarp * 16 * KZ * ROWB;
                 const uint8_t* vst = kst + TILE * ROWB;
@@ -1225,7 +1231,7 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                             if (poison >> (i / 8 * 2 + e) & 1) o[i][e] = o[i][e + 2] = NAN;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars + 8 * (STAGES + st));
+                if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
             }
             if (!ok) break;
 
