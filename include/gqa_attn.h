@@ -250,7 +250,7 @@ int gqa_attn_paged_e4m3_noalloc(const void* q, const uint8_t* kcache, const uint
  * and flag GQA_DEVERR_BAD_PAGE_ID.  Keys that a row does not see have no effect on it,
  * whatever their bytes (NaN scales included).
  * 1 <= batch <= 1024; num_pages * page < 2^31; batch * Hkv * ceil(max_ctx_len / 128) <
- * 2^31 (GQA_ERR_UNSUPPORTED).  FP32 accumulation; cached values enter the
+ * 2^29 (GQA_ERR_UNSUPPORTED).  FP32 accumulation; cached values enter the
  * products exactly, P rounded to fp16.  The visible tiles of all sequences and KV
  * heads are divided equally between the SMs on the device, and what is cut is joined
  * in a fixed order by a second kernel.  Workspace: gqa_workspace_bytes(

@@ -96,12 +96,16 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
 
 // Where each sequence's tiles begin among all.  Up to 32 sequences: lane i of every
 // warp holds sequence i, nothing is shared.  More: in shared memory.  (All tiles of all
-// units are fewer than 2^31: the host sees to it.)
+// units and their LEADs are fewer than 2^31: the host sees to it.)
+//
+// Ranges are equal in tiles and what a piece costs besides: LEAD tiles' time in front of
+// each unit's.  (Sixteen windows of 17 tiles: 22 us without, see below.)
 constexpr int LANES = 32;
+constexpr int LEAD = 3;
 struct Seqs {
     const int* starts;         // [batch + 1], or null
-    int start, tiles, ctx;     // of sequence `lane`
-    int all;                   // tiles of all sequences
+    int start, tiles, ctx;     // of sequence `lane`; tiles with LEAD in front
+    int all;                   // of all sequences
 };
 
 __device__ __forceinline__ int scan_warp(int x) {
@@ -122,7 +126,7 @@ __device__ __forceinline__ Seqs seqs_small(const Params& P) {
     if (lane < P.batch) {
         const Span s = span_of(P, P.ctx_lens[lane]);
         q.ctx = s.ctx;
-        q.tiles = s.tiles;
+        q.tiles = s.tiles ? s.tiles + LEAD : 0;
     }
     const int incl = scan_warp(q.tiles);
     q.start = incl - q.tiles;
@@ -141,6 +145,7 @@ __device__ __forceinline__ void seqs_large(const Params& P, int* starts, int* to
         for (int i = 0; i < EACH; ++i) {
             const int b = tid * EACH + i;
             n[i] = b < P.batch ? span_of(P, P.ctx_lens[b]).tiles : 0;
+            if (n[i]) n[i] += LEAD;
             sum += n[i];
         }
         incl = scan_warp(sum);
@@ -180,27 +185,27 @@ struct Ranges {
 
 // Walks the pieces (unit, tiles [jb, je)) of one range.  (All lanes of a warp.)
 struct Pieces {
-    int pos, end;
+    int pos, end;     // LEADs counted
     int b, u, h, g;   // sequence, unit within it, its KV head and group of packed rows
     int jb, je, n;    // tiles of the piece, of the unit
+    int unit;         // where the unit begins, its LEAD counted
     bool first;       // the range's first piece
     Span s;
     __device__ bool whole() const { return jb == 0 && je == n; }
-    __device__ bool next(const Params& P, const Seqs& q, int begin) {
-        if (pos >= end) return false;
+    // Sets b, u, n, unit and s to the unit that holds position at.
+    __device__ void find(const Params& P, const Seqs& q, int at) {
         const int per = P.hkv * P.groups;
-        first = pos == begin;
         int start, ctx;
         if (!q.starts) {
-            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start * per <= pos));
+            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start * per <= at));
             start = __shfl_sync(0xffffffffu, q.start, b);
             n = __shfl_sync(0xffffffffu, q.tiles, b);
             ctx = __shfl_sync(0xffffffffu, q.ctx, b);
         } else {
-            int lo = 0, hi = P.batch;   // starts[lo] * per <= pos < starts[hi] * per
+            int lo = 0, hi = P.batch;   // starts[lo] * per <= at < starts[hi] * per
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (q.starts[mid] * per <= pos) lo = mid;
+                if (q.starts[mid] * per <= at) lo = mid;
                 else hi = mid;
             }
             b = lo;
@@ -209,28 +214,54 @@ struct Pieces {
             ctx = P.ctx_lens[b];
         }
         s = span_of(P, ctx);
-        const int off = pos - start * per;
-        u = per == 1 ? 0 : off / n;
-        jb = off - u * n;
-        je = min(jb + end - pos, n);
+        u = per == 1 ? 0 : (at - start * per) / n;
+        unit = start * per + u * n;
+        n -= LEAD;
+    }
+    // A boundary in or right behind a LEAD is the unit's beginning.
+    __device__ int boundary(const Params& P, const Seqs& q, int at, int total) {
+        if (at >= total) return total;
+        find(P, q, at);
+        return at <= unit + LEAD ? unit : at;
+    }
+    __device__ bool next(const Params& P, const Seqs& q, int begin) {
+        if (pos >= end) return false;
+        first = pos == begin;
+        find(P, q, pos);
         h = P.groups == 1 ? u : u / P.groups;
         g = u - h * P.groups;
-        pos += je - jb;
+        jb = max(pos - unit - LEAD, 0);
+        je = min(end - unit - LEAD, n);
+        pos = je == n ? unit + LEAD + n : end;
         return true;
     }
 };
 
-// Wait for a barrier's phase, as mbar_wait, a few tries before the clock is read.
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
-                                       unsigned* err) {
-    return mbar_wait(bar, parity, abort, err);
-}
+// Wait for a barrier's phase; bounded as mbar_wait.  After a wait that ran out all others
+// return at once and the warps go on to their end over whatever is there (every address
+// comes from the arguments and the tables), so that the barriers between them, which
+// know no limit, are met by all.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                      unsigned* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 256; ++i)
+    for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
-    return wait_long(bar, parity, abort, err);
+        if (n & 15) continue;
+        if (*abort) return false;
+        const uint64_t now = global_timer_ns();
+        if (!t0) t0 = now;
+        if (now - t0 > kWaitTimeoutNs) {
+            *abort = 1;
+            atomicOr(err, kErrWaitTimeout);
+            return false;
+        }
+    }
+}
+// Barrier `id` of `threads` threads.
+__device__ __forceinline__ void meet(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 __device__ __forceinline__ int tile_key(const Span& s, int j) {
@@ -276,9 +307,12 @@ __device__ __forceinline__ Ranges begin_range(const Params& P, int* starts, int*
     }
     asm volatile("griddepcontrol.launch_dependents;");
     const Ranges ranges(P, seqs);
-    const bool works = (int)blockIdx.x < ranges.G;
-    it.pos = works ? ranges.begin(blockIdx.x) : 0;
-    it.end = works ? ranges.begin(blockIdx.x + 1) : 0;
+    it.pos = it.end = 0;
+    if ((int)blockIdx.x < ranges.G) {
+        const int total = seqs.all * (P.hkv * P.groups);
+        it.pos = it.boundary(P, seqs, ranges.begin(blockIdx.x), total);
+        it.end = it.boundary(P, seqs, ranges.begin(blockIdx.x + 1), total);
+    }
     return ranges;
 }
 
@@ -401,7 +435,7 @@ __device__ __forceinline__ void write_task(const Params& P, const Pieces& it, co
     if (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end))
         P.tasks[P.by_unit ? unit : cta] =
             make_int4(unit, cta * 2 + (it.first ? 0 : 1),
-                      cut ? ranges.of(it.pos - it.je + it.n - 1) - cta + 1 : 0, 0);
+                      cut ? ranges.of(it.unit + LEAD + it.n - 1) - cta + 1 : 0, 0);
 }
 
 // Position of packed row r of a KV head, and whether a row there sees a key.
@@ -456,7 +490,7 @@ struct Config {
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
     static constexpr int MAX_STAGES = 10;
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
-    static constexpr int OFF_FLAG = OFF_BARS + (2 * NG * MAX_STAGES + NG + 1) * 8;   // [NG][2]
+    static constexpr int OFF_FLAG = OFF_BARS + 2 * NG * MAX_STAGES * 8;   // [NG][2]
     static constexpr int OFF_ABORT = OFF_FLAG + NG * 2 * 4;
     static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
     // The bytes in flight set the copy rate: all that is left, up to 184 KB.
@@ -483,7 +517,6 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-    auto group_bar = [&](int g) { return bars + 8u * (2 * NG * STAGES + g); };   // g = NG: all
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -491,8 +524,6 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             mbar_init(bars + 8 * i, COPY_WARPS);
             mbar_init(bars + 8 * (NG * STAGES + i), GW);
         }
-        for (int g = 0; g < NG; ++g) mbar_init(group_bar(g), GW);
-        mbar_init(group_bar(NG), NW);
         for (int i = 0; i < NG * 2; ++i) reinterpret_cast<int*>(smem + C::OFF_FLAG)[i] = 0;
         *abort_flag = 0;
         fence_mbar_init();
@@ -524,22 +555,13 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
         float* const sref = reinterpret_cast<float*>(smem + C::OFF_REF);   // [NG][ROWS]
         float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
         volatile int* const flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG) + group * 2;
-        uint32_t all_phase = 0, group_phase = 0;
-        // Barriers of all warps with products and of a group, with the bounded wait.
-        auto sync = [&](uint32_t bar, uint32_t& phase) -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-            const bool ok = wait(bar, phase, abort_flag, P.err);
-            phase ^= 1;
-            return __all_sync(0xffffffffu, ok);
-        };
-        auto meet = [&]() { return sync(group_bar(NG), all_phase); };
-        auto meet_group = [&]() { return sync(group_bar(group), group_phase); };
+        auto meet_all = [&]() { meet(1, 32 * NW); };
+        auto meet_group = [&]() { meet(2 + group, 32 * GW); };
         const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
+        const float vscale = *P.scale_dev[1];
         uint32_t n = 0;     // tiles of the CTA so far
         uint32_t mine = 0;  // tiles of the group so far
-        bool ok = true;
-        while (ok && it.next(P, seqs, begin)) {
+        while (it.next(P, seqs, begin)) {
             const Span s = it.s;
             const int row0 = it.g * ROWS;
             if (threadIdx.x == 0) write_task(P, it, ranges);
@@ -553,8 +575,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 const int at = DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
                 *reinterpret_cast<uint4*>(sq + r * C::Q_ROW + at) = v;
             }
-            ok = meet();
-            if (!ok) break;
+            meet_all();
             float o[4][NT][4];              // places 8 gid + 2 i, + 1 of the slice; rows 2 t, 2 t + 1
             float mref[NT][2], l[NT][2];    // of rows 2 t, 2 t + 1
 #pragma unroll
@@ -573,9 +594,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
                 const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
-                ok = wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
+                __syncwarp();
                 const int key0 = tile_key(s, j);
                 const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
@@ -682,8 +702,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 put_p(ls);
                 // One barrier a tile: P is there, and nobody reads the other buffer, which
                 // the next tile writes, any more (its products are in front of it).
-                ok = meet_group();
-                if (!ok) break;
+                meet_group();
                 if (flag[mine & 1] == (int)mine + 1) {
                     // A reference moves: the tile's largest scores of all warps.
 #pragma unroll
@@ -696,8 +715,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
                             if (gid == 0) smax[warp * ROWS + nt * 8 + 2 * t + e] = m;
                         }
-                    ok = meet_group();
-                    if (!ok) break;
+                    meet_group();
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
@@ -723,8 +741,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                         }
                     }
                     put_p(ls);
-                    ok = meet_group();   // (also: the maxima have been read)
-                    if (!ok) break;
+                    meet_group();   // (also: the maxima have been read)
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -829,10 +846,10 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
                 ++mine;
             }
-            if (!ok) break;
 
             // ---------------------------------------------------------- end of the piece
-            // Sums of the rows' weights by warp, the groups' references.
+            // Sums of the rows' weights by warp, the groups' references; then each row's
+            // factors for the groups' O and what its sums are to be divided by.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -845,11 +862,34 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                         if (gwarp == 0) sref[group * ROWS + nt * 8 + 2 * t + e] = mref[nt][e];
                     }
                 }
-            // O in four rounds, a quarter of each lane's places each: the sources' shares
-            // go through shared memory and are added in order, in units of the largest
-            // reference.
             const int slot = cta * 2 + (it.first ? 0 : 1);
             const bool whole = it.whole();
+            meet_all();
+            if (threadIdx.x < ROWS) {
+                const int row = threadIdx.x;
+                float M = sref[row];
+#pragma unroll
+                for (int g = 1; g < NG; ++g) M = fmaxf(M, sref[g * ROWS + row]);
+                float sum = 0.f, f[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float mg = sref[g * ROWS + row];
+                    f[g] = mg == -INFINITY ? 0.f : ex2(mg - M);
+                    float lg = 0.f;
+#pragma unroll
+                    for (int x = 0; x < GW; ++x) lg += smax[(g * GW + x) * ROWS + row];
+                    sum = fmaf(f[g], lg, sum);
+                }
+                if (!whole && row0 + row < P.nq)
+                    *reinterpret_cast<float2*>(P.ws_ml + ((long long)slot * ROWS + row) * 2) =
+                        make_float2(M, sum);
+                // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
+                const float unit = !whole ? 1.f : sum == 0.f ? 0.f : vscale / sum;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) sref[g * ROWS + row] = f[g] * unit;
+            }
+            // O in four rounds, a quarter of each lane's places each: the sources' shares
+            // go through shared memory and are added in order.
 #pragma unroll 1
             for (int r = 0; r < 4; ++r) {
                 float* to = join + (group * C::SHARES + share) * ROWS * C::JOIN_ROW + slice * 16 +
@@ -860,21 +900,14 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int e = 0; e < 2; ++e)
                         *reinterpret_cast<float2*>(to + (nt * 8 + 2 * t + e) * C::JOIN_ROW) =
                             make_float2(o[0][nt][e], o[0][nt][e + 2]);
-                ok = meet();
-                if (!ok) break;
+                meet_all();
 #pragma unroll 1
                 for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
                     const int row = i / (DH / 8), at = i % (DH / 8);   // at: slice, gid
                     if (row0 + row >= P.nq) break;
-                    float M = sref[row];
-#pragma unroll
-                    for (int g = 1; g < NG; ++g) M = fmaxf(M, sref[g * ROWS + row]);
                     float2 a = make_float2(0.f, 0.f);
-                    float sum = 0.f;
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const float mg = sref[g * ROWS + row];
-                        const float f = mg == -INFINITY ? 0.f : ex2(mg - M);
                         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int x = 0; x < C::SHARES; ++x) {
@@ -883,30 +916,20 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                             v.x += y.x;
                             v.y += y.y;
                         }
-                        float lg = 0.f;
-#pragma unroll
-                        for (int x = 0; x < GW; ++x) lg += smax[(g * GW + x) * ROWS + row];
-                        sum = fmaf(f, lg, sum);
+                        const float f = sref[g * ROWS + row];
                         a.x = fmaf(f, v.x, a.x);
                         a.y = fmaf(f, v.y, a.y);
                     }
                     const int d = at * 8 + r * 2;
-                    if (whole) {
-                        // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
-                        const float inv = sum == 0.f ? 0.f : *P.scale_dev[1] / sum;
+                    if (whole)
                         *reinterpret_cast<uint32_t*>(
                             P.out + row_offset(P, it.b, it.h, row0 + row, DH) + d) =
-                            pack_half2(a.x * inv, a.y * inv);
-                    } else {
+                            pack_half2(a.x, a.y);
+                    else
                         *reinterpret_cast<float2*>(
                             P.ws_o + ((long long)slot * ROWS + row) * DH + d) = a;
-                        if (at == 0 && r == 0)
-                            *reinterpret_cast<float2*>(
-                                P.ws_ml + ((long long)slot * ROWS + row) * 2) = make_float2(M, sum);
-                    }
                 }
-                ok = meet();
-                if (!ok) break;
+                meet_all();
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
 #pragma unroll
@@ -942,7 +965,7 @@ struct Narrow {
     static constexpr int OFF_STARTS = OFF_ML + NW * 8 * 8;
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
-    static constexpr int OFF_ABORT = OFF_BARS + (2 * NG * STAGES + 1) * 8;
+    static constexpr int OFF_ABORT = OFF_BARS + 2 * NG * STAGES * 8;
     static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
     static constexpr int BYTES = OFF_RING + STAGES * STAGE;
     static_assert(BYTES <= 232448, "shared memory");
@@ -958,14 +981,12 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-    const uint32_t meet_bar = bars + 8 * (2 * NG * STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NG * STAGES; ++i) {
             mbar_init(bars + 8 * i, COPY_WARPS);
             mbar_init(bars + 8 * (NG * STAGES + i), C::GW);
         }
-        mbar_init(meet_bar, NW);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -988,18 +1009,11 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
         const int gid = lane >> 2, t = lane & 3;
         float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
         float* const sml = reinterpret_cast<float*>(smem + C::OFF_ML);
-        uint32_t phase = 0;
-        auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(meet_bar);
-            const bool ok = wait(meet_bar, phase, abort_flag, P.err);
-            phase ^= 1;
-            return __all_sync(0xffffffffu, ok);
-        };
+        auto meet_all = [&]() { meet(1, 32 * NW); };
         const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
+        const float vscale = *P.scale_dev[1];
         uint32_t n = 0;     // tiles of the CTA so far
-        bool ok = true;
-        while (ok && it.next(P, seqs, begin)) {
+        while (it.next(P, seqs, begin)) {
             const Span s = it.s;
             if (threadIdx.x == 0) write_task(P, it, ranges);
             // The lane's places of row gid: the products' B operands.
@@ -1027,9 +1041,8 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
             for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
                 const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
-                ok = wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
+                __syncwarp();
                 const int k0 = tile_key(s, j) + gwarp * 16 * KZ;
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE + gwarp * 16 * KZ * ROWB;
                 const uint8_t* vst = kst + TILE * ROWB;
@@ -1233,7 +1246,6 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
             }
-            if (!ok) break;
 
             // ---------------------------------------------------------- end of the piece
 #pragma unroll
@@ -1245,9 +1257,13 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                         make_float2(mref[e], l[e]);
             }
             // O in rounds of a word of each lane's places: the warps' sums go through shared
-            // memory and are added in order, in units of the largest reference.
+            // memory and are added in order, in units of the largest reference.  A thread
+            // has two places of a row.
             const int slot = blockIdx.x * 2 + (it.first ? 0 : 1);
             const bool whole = it.whole();
+            const int row = threadIdx.x >> 5, at = threadIdx.x & 31;
+            float f[NW];
+            __half* out = nullptr;
 #pragma unroll 1
             for (int r = 0; r < MT / 4; ++r) {
 #pragma unroll
@@ -1257,44 +1273,48 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                     to[0] = make_float4(o[0][e], o[0][e + 2], o[1][e], o[1][e + 2]);
                     to[1] = make_float4(o[2][e], o[2][e + 2], o[3][e], o[3][e + 2]);
                 }
-                ok = meet();
-                if (!ok) break;
-                // A thread's two places: row tid / 32, of gid (tid % 32) / 4.
-                const int row = threadIdx.x >> 5, at = threadIdx.x & 31;
+                meet_all();
                 if (row < P.nq) {
-                    float2 ml[NW];
-                    float M = -INFINITY;
+                    if (r == 0) {
+                        float2 ml[NW];
+                        float M = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < NW; ++x) {
-                        ml[x] = *reinterpret_cast<const float2*>(sml + (x * 8 + row) * 2);
-                        M = fmaxf(M, ml[x].x);
-                    }
-                    float2 a = make_float2(0.f, 0.f);
-                    float sum = 0.f;
+                        for (int x = 0; x < NW; ++x) {
+                            ml[x] = *reinterpret_cast<const float2*>(sml + (x * 8 + row) * 2);
+                            M = fmaxf(M, ml[x].x);
+                        }
+                        float sum = 0.f;
 #pragma unroll
-                    for (int x = 0; x < NW; ++x) {
-                        const float f = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - M);
-                        const float2 v = *reinterpret_cast<const float2*>(
-                            join + (x * 8 + row) * C::JOIN_ROW + at * 2);
-                        sum = fmaf(f, ml[x].y, sum);
-                        a.x = fmaf(f, v.x, a.x);
-                        a.y = fmaf(f, v.y, a.y);
-                    }
-                    const int d = (at >> 2) * (DH / 8) + r * 8 + (at & 3) * 2;
-                    if (whole) {
-                        // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
-                        const float inv = sum == 0.f ? 0.f : *P.scale_dev[1] / sum;
-                        *reinterpret_cast<uint32_t*>(P.out + row_offset(P, it.b, it.h, row, DH) + d) =
-                            pack_half2(a.x * inv, a.y * inv);
-                    } else {
-                        *reinterpret_cast<float2*>(P.ws_o + ((long long)slot * 8 + row) * DH + d) = a;
-                        if (at == 0 && r == 0)
+                        for (int x = 0; x < NW; ++x) {
+                            f[x] = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - M);
+                            sum = fmaf(f[x], ml[x].y, sum);
+                        }
+                        if (whole) {
+                            // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
+                            const float unit = sum == 0.f ? 0.f : vscale / sum;
+#pragma unroll
+                            for (int x = 0; x < NW; ++x) f[x] *= unit;
+                            out = P.out + row_offset(P, it.b, it.h, row, DH);
+                        } else if (at == 0) {
                             *reinterpret_cast<float2*>(P.ws_ml + ((long long)slot * 8 + row) * 2) =
                                 make_float2(M, sum);
+                        }
                     }
+                    float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < NW; ++x) {
+                        const float2 v = *reinterpret_cast<const float2*>(
+                            join + (x * 8 + row) * C::JOIN_ROW + at * 2);
+                        a.x = fmaf(f[x], v.x, a.x);
+                        a.y = fmaf(f[x], v.y, a.y);
+                    }
+                    const int d = (at >> 2) * (DH / 8) + r * 8 + (at & 3) * 2;
+                    if (whole)
+                        *reinterpret_cast<uint32_t*>(out + d) = pack_half2(a.x, a.y);
+                    else
+                        *reinterpret_cast<float2*>(P.ws_o + ((long long)slot * 8 + row) * DH + d) = a;
                 }
-                ok = meet();
-                if (!ok) break;
+                meet_all();
 #pragma unroll
                 for (int i = 0; i < MT - 4; ++i)
 #pragma unroll
@@ -1485,7 +1505,7 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
     P.scale = scale;
     // No more ranges than tiles.
     const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len + TILE - 1LL) / TILE);
-    if (tiles > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+    if (tiles > 0x1fffffffLL) return GQA_ERR_UNSUPPORTED;   // (with their LEADs below 2^31)
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
     if (P.G > MAX_RANGES) P.G = MAX_RANGES;
     P.by_unit = (long long)batch * Hkv * P.groups < P.G;
