@@ -43,7 +43,6 @@ namespace gqa {
 namespace paged4 {
 
 constexpr int TILE = 128;                  // keys of a tile
-constexpr int GW = 8;                      // warps of a group, 16 keys of a tile each
 constexpr int MAX_BATCH = 1024;
 constexpr float RESCALE_THRESHOLD = 8.0f;
 
@@ -101,7 +100,7 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
 // Ranges are equal in tiles and what a piece costs besides: LEAD tiles' time in front of
 // each unit's.  (Sixteen windows of 17 tiles: 22 us without, see below.)
 constexpr int LANES = 32;
-constexpr int LEAD = 3;
+constexpr int LEAD = 2;
 struct Seqs {
     const int* starts;         // [batch + 1], or null
     int start, tiles, ctx;     // of sequence `lane`; tiles with LEAD in front
@@ -457,34 +456,40 @@ __device__ __forceinline__ bool unseen(const Params& P, const Span& s, int key) 
 // DH: head size; NT: eights of packed rows.
 template <int DH, int NT>
 struct Config {
-    // Two groups of eight warps while a warp's sums leave room (four warps for each
-    // quarter of an SM hide the products' latencies: two took twice as long), one for
-    // more rows.  The warpgroup behind them copies.  Registers: what the launch gives
-    // (65536 over the threads, by eights) moved from the copies to the products.
-    static constexpr int NG = NT <= 3 ? 2 : 1;
+    // Two groups of four warps, each group on a tile of its own, so that one's products go
+    // on while the other's warps meet, each warp with 32 keys.  (Groups of eight warps
+    // with 16 keys and half the registers: 28 us instead of 26 for two rows over 200000
+    // tokens, 35 instead of 29 for four.)  The warpgroup behind them copies.  Registers:
+    // what the launch gives (65536 over the threads, by eights) moved from the copies to
+    // the products.
+    static constexpr int NG = 2;
+    static constexpr int GW = 4;
+    static constexpr int KZ = 8 / GW;              // sixteens of keys of a warp
     static constexpr int NW = GW * NG;
     static constexpr int THREADS = 32 * NW + 128;
-    static constexpr int REGS_PRODUCTS = NG == 2 ? 112 : 224;
-    static constexpr int REGS_COPIES = NG == 2 ? 32 : 56;
+    static constexpr int REGS_PRODUCTS = 224;
+    static constexpr int REGS_COPIES = 56;
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
 
     static constexpr int ROWB = fp4::row_bytes(DH);
     static constexpr int STAGE = 2 * TILE * ROWB;
     static constexpr int ROWS = 8 * NT;
-    // V: slices of 64 places, and the shares of a tile's keys that then occupy eight warps.
+    // V: slices of 64 places, and the shares of a tile's keys that then occupy a group.
     static constexpr int SLICES = DH / 64, SHARES = GW / SLICES;
     static constexpr int SOURCES = NG * SHARES;    // warps that sum the same places
     // Query rows: a lane's part of a row so that the eight lanes of a load's phase use
     // different banks (DH 256: quarters padded by 16 bytes; 128: rows).
     static constexpr int Q_ROW = DH == 256 ? 4 * 144 : 272;
     static constexpr int P_ROW = TILE * 2 + 16;    // P^T: rows of 128 keys, padded
+    static constexpr int P_BYTES = NG * ROWS * P_ROW;
     static constexpr int JOIN_ROW = DH / 4 + 4;    // floats of a row in one round of the join
 
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_P = OFF_Q + ROWS * Q_ROW;                    // [NG][2][ROWS]
-    static constexpr int OFF_JOIN = OFF_P + NG * 2 * ROWS * P_ROW;        // [SOURCES][ROWS]
-    static constexpr int OFF_MAX = OFF_JOIN + SOURCES * ROWS * JOIN_ROW * 4;   // [NW][ROWS]
+    static constexpr int OFF_P = OFF_Q + ROWS * Q_ROW;      // [NG][ROWS]
+    static constexpr int OFF_JOIN = OFF_P;                  // [SOURCES][ROWS], when P is done with
+    static constexpr int JOIN_BYTES = SOURCES * ROWS * JOIN_ROW * 4;
+    static constexpr int OFF_MAX = OFF_P + (P_BYTES > JOIN_BYTES ? P_BYTES : JOIN_BYTES);   // [NW][ROWS]
     static constexpr int OFF_REF = OFF_MAX + NW * ROWS * 4;               // [NG][ROWS]
     static constexpr int OFF_STARTS = OFF_REF + NG * ROWS * 4;
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
@@ -512,6 +517,7 @@ template <int DH, int NT>
 __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const Params P) {
     using C = Config<DH, NT>;
     constexpr int ROWB = C::ROWB, ROWS = C::ROWS, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
+    constexpr int GW = C::GW, KZ = C::KZ;
     extern __shared__ __align__(128) uint8_t smem[];
     int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
         const int gid = lane >> 2, t = lane & 3;
         const int slice = gwarp % C::SLICES, share = gwarp / C::SLICES;
         uint8_t* const sq = smem + C::OFF_Q;
-        uint8_t* const sp = smem + C::OFF_P + group * 2 * ROWS * C::P_ROW;
+        uint8_t* const pt = smem + C::OFF_P + group * ROWS * C::P_ROW;
         float* const smax = reinterpret_cast<float*>(smem + C::OFF_MAX);   // [NW][ROWS]
         float* const sref = reinterpret_cast<float*>(smem + C::OFF_REF);   // [NG][ROWS]
         float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
@@ -565,22 +571,33 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             const Span s = it.s;
             const int row0 = it.g * ROWS;
             if (threadIdx.x == 0) write_task(P, it, ranges);
-#pragma unroll 1
-            for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
-                const int r = i / (DH / 8), c = i % (DH / 8);
-                const uint4 v = row0 + r < P.nq
-                                    ? *reinterpret_cast<const uint4*>(
-                                          P.q + row_offset(P, it.b, it.h, row0 + r, DH) + c * 8)
-                                    : make_uint4(0, 0, 0, 0);
-                const int at = DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
-                *reinterpret_cast<uint4*>(sq + r * C::Q_ROW + at) = v;
+            // Q, all loads under way together.
+            {
+                constexpr int EACH = (ROWS * DH / 8 + 32 * NW - 1) / (32 * NW);
+                uint4 v[EACH];
+#pragma unroll
+                for (int x = 0; x < EACH; ++x) {
+                    const int i = threadIdx.x + x * 32 * NW, r = i / (DH / 8), c = i % (DH / 8);
+                    v[x] = r < ROWS && row0 + r < P.nq
+                               ? *reinterpret_cast<const uint4*>(
+                                     P.q + row_offset(P, it.b, it.h, row0 + r, DH) + c * 8)
+                               : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int x = 0; x < EACH; ++x) {
+                    const int i = threadIdx.x + x * 32 * NW, r = i / (DH / 8), c = i % (DH / 8);
+                    const int at = DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
+                    if (r < ROWS) *reinterpret_cast<uint4*>(sq + r * C::Q_ROW + at) = v[x];
+                }
             }
             meet_all();
+            if (gwarp == 0)
+                for (int i = lane; i < ROWS; i += 32) sref[group * ROWS + i] = -INFINITY;
+            meet_group();
             float o[4][NT][4];              // places 8 gid + 2 i, + 1 of the slice; rows 2 t, 2 t + 1
-            float mref[NT][2], l[NT][2];    // of rows 2 t, 2 t + 1
+            float l[NT][2];                 // of rows 2 t, 2 t + 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mref[nt][0] = mref[nt][1] = -INFINITY;
                 l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -600,27 +617,22 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
                 const uint8_t* vst = kst + TILE * ROWB;
-                uint8_t* const pt = sp + (mine & 1) * ROWS * C::P_ROW;
-                // ---- scores of keys key_of(gid) and key_of(gid + 8) of the warp's 16
-                float sc[NT][4];
-                {
-                    constexpr int CHAINS = NT == 1 ? 2 : 1;   // (sums side by side)
-                    float sd[CHAINS][NT][4];
+                // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
+                float sc[KZ][NT][4];
 #pragma unroll
-                    for (int x = 0; x < CHAINS; ++x)
+                for (int z = 0; z < KZ; ++z) {
+                    const int k0 = (gwarp * KZ + z) * 16;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) sd[x][nt][e] = 0.f;
-                    constexpr int KW = DH / 32;   // words of a lane and key
-                    constexpr int HALF = KW / 2;  // of one load
+                        for (int e = 0; e < 4; ++e) sc[z][nt][e] = 0.f;
+                    constexpr int HALF = DH / 64;   // words of a lane and key in one load
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         uint32_t w[2][HALF], u[2][HALF / 2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint8_t* row =
-                                kst + (gwarp * 16 + key_of<DH>(gid + 8 * e)) * ROWB;
+                            const uint8_t* row = kst + (k0 + key_of<DH>(gid + 8 * e)) * ROWB;
                             if constexpr (DH == 256) {
                                 const uint4 v =
                                     *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
@@ -653,34 +665,45 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                                     sq + (nt * 8 + gid) * C::Q_ROW +
                                     (DH == 256 ? t * 144 + x * 64 + i * 16
                                                : t * 32 + x * 128 + i * 16));
-                                mma16816(sd[0][nt], a[0], b[0], a[1], b[1], qv.x, qv.y);
-                                mma16816(sd[CHAINS - 1][nt], a[2], b[2], a[3], b[3], qv.z, qv.w);
+                                mma16816(sc[z][nt], a[0], b[0], a[1], b[1], qv.x, qv.y);
+                                mma16816(sc[z][nt], a[2], b[2], a[3], b[3], qv.z, qv.w);
                             }
                         }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[nt][e] = (CHAINS == 2 ? sd[0][nt][e] + sd[CHAINS - 1][nt][e]
-                                                     : sd[0][nt][e]) * sl2;
+                        for (int e = 0; e < 4; ++e) sc[z][nt][e] *= sl2;
                 }
                 if (edge) {
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!sees(P, row_pos(P, s, row0 + nt * 8 + 2 * t + (e & 1)),
+                                          key0 + (gwarp * KZ + z) * 16 +
+                                              key_of<DH>(gid + (e & 2) * 4)))
+                                    sc[z][nt][e] = -INFINITY;
+                }
+                // ---- P by the references as they stand
+                float mref[NT][2];   // the group's references of rows 2 t, 2 t + 1
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 m = *reinterpret_cast<const float2*>(sref + group * ROWS +
+                                                                      nt * 8 + 2 * t);
+                    mref[nt][0] = m.x;
+                    mref[nt][1] = m.y;
+                }
+                bool exceed = false;
+#pragma unroll
+                for (int z = 0; z < KZ; ++z)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (!sees(P, row_pos(P, s, row0 + nt * 8 + 2 * t + (e & 1)),
-                                      key0 + gwarp * 16 + key_of<DH>(gid + (e & 2) * 4)))
-                                sc[nt][e] = -INFINITY;
-                }
-                // ---- P by the references as they stand
-                bool exceed = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        exceed |= sc[nt][e] > mref[nt][e & 1] + RESCALE_THRESHOLD;
+                            exceed |= sc[z][nt][e] > mref[nt][e & 1] + RESCALE_THRESHOLD;
                 if (__any_sync(0xffffffffu, exceed) && lane == 0) flag[mine & 1] = (int)mine + 1;
                 // The P of a strip, transposed: keys 2 t, 2 t + 1 (and 8 more) of packed
                 // row gid.  Returns the rows' sums in ls.
@@ -689,19 +712,23 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int nt = 0; nt < NT; ++nt) {
                         const float m0 = mref[nt][0] == -INFINITY ? 0.f : mref[nt][0];
                         const float m1 = mref[nt][1] == -INFINITY ? 0.f : mref[nt][1];
-                        const float p0 = ex2(sc[nt][0] - m0), p1 = ex2(sc[nt][1] - m1);
-                        const float p2 = ex2(sc[nt][2] - m0), p3 = ex2(sc[nt][3] - m1);
-                        ls[nt][0] = p0 + p2;
-                        ls[nt][1] = p1 + p3;
-                        uint8_t* to = pt + (nt * 8 + gid) * C::P_ROW + (gwarp * 16 + 2 * t) * 2;
-                        *reinterpret_cast<uint32_t*>(to) = transpose8(pack_half2(p0, p1));
-                        *reinterpret_cast<uint32_t*>(to + 16) = transpose8(pack_half2(p2, p3));
+                        ls[nt][0] = ls[nt][1] = 0.f;
+#pragma unroll
+                        for (int z = 0; z < KZ; ++z) {
+                            const float p0 = ex2(sc[z][nt][0] - m0), p1 = ex2(sc[z][nt][1] - m1);
+                            const float p2 = ex2(sc[z][nt][2] - m0), p3 = ex2(sc[z][nt][3] - m1);
+                            ls[nt][0] += p0 + p2;
+                            ls[nt][1] += p1 + p3;
+                            uint8_t* to = pt + (nt * 8 + gid) * C::P_ROW +
+                                          ((gwarp * KZ + z) * 16 + 2 * t) * 2;
+                            *reinterpret_cast<uint32_t*>(to) = transpose8(pack_half2(p0, p1));
+                            *reinterpret_cast<uint32_t*>(to + 16) = transpose8(pack_half2(p2, p3));
+                        }
                     }
                 };
                 float ls[NT][2];
+                meet_group();   // the last tile's P has been read
                 put_p(ls);
-                // One barrier a tile: P is there, and nobody reads the other buffer, which
-                // the next tile writes, any more (its products are in front of it).
                 meet_group();
                 if (flag[mine & 1] == (int)mine + 1) {
                     // A reference moves: the tile's largest scores of all warps.
@@ -709,7 +736,10 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+                            float m = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+                            for (int z = 1; z < KZ; ++z)
+                                m = fmaxf(m, fmaxf(sc[z][nt][e], sc[z][nt][e + 2]));
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1)
                                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
@@ -732,6 +762,9 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                             }
                             l[nt][e] *= f[e];
                         }
+                        if (gwarp == 0 && gid == 0)
+                            *reinterpret_cast<float2*>(sref + group * ROWS + nt * 8 + 2 * t) =
+                                make_float2(mref[nt][0], mref[nt][1]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             o[i][nt][0] *= f[0];
@@ -848,7 +881,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
             }
 
             // ---------------------------------------------------------- end of the piece
-            // Sums of the rows' weights by warp, the groups' references; then each row's
+            // Sums of the rows' weights by warp; then, from them and the references, each row's
             // factors for the groups' O and what its sums are to be divided by.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -859,7 +892,6 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
                     if (gid == 0) {
                         smax[warp * ROWS + nt * 8 + 2 * t + e] = l[nt][e];
-                        if (gwarp == 0) sref[group * ROWS + nt * 8 + 2 * t + e] = mref[nt][e];
                     }
                 }
             const int slot = cta * 2 + (it.first ? 0 : 1);

@@ -187,10 +187,13 @@ __host__ __device__ inline int tiles_of(const Params& P, int t) {
     if constexpr (WIN) return win_tiles(P, t).n;
     else return kv_tiles(t, P.Q, P.KV, P.M_total, P.grp);
 }
-// Maps of the sinks alone (rows past them are zeros).
+// Maps of the sinks alone (rows past them are zeros), and where each pair's range begins:
+// its pair tile, and the iterations of that tile in front of the range.  (Counted from
+// the first tile by every thread, as the other kernels do, that took 10 us of 162.)
 template <bool WIN>
 struct SinkMaps {
     CUtensorMap k, v;
+    int tile[kMaxClusters], skip[kMaxClusters];
 };
 template <>
 struct SinkMaps<false> {};
@@ -216,9 +219,17 @@ struct SegIter {
             ++hd;
         }
     }
-    __device__ void init(const Params& P, int pair) {
+    __device__ void init(const Params& P, const SinkMaps<WIN>& at, int pair) {
         pos = pair_begin(P.total, P.G, pair);
         end = pair_begin(P.total, P.G, pair + 1);
+        if constexpr (WIN) {
+            t = at.tile[pair];
+            hd = MH ? P.ptiles.div(t) : 0;
+            lt = t - hd * P.num_ptiles;
+            cum = pos - at.skip[pair];
+            first = true;
+            return;
+        }
         t = 0;
         hd = 0;
         lt = 0;
@@ -545,7 +556,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     asm volatile("griddepcontrol.launch_dependents;");
 
     SegIter<MH, WIN> it;
-    it.init(P, pair);
+    it.init(P, tm_sink, pair);
     int pt, hd, jb, je, n;
     bool is_first;
 
@@ -1330,11 +1341,21 @@ static int launch(const void* q, const void* k, const void* v, const float* ksca
     }
     MergeTasks tasks;  // passed to the merge kernel by value
     find_cut_tiles<WIN>(P, tasks);
+    SinkMaps<WIN> ts;
+    if constexpr (WIN) {
+        long long cum = 0;
+        int t = 0;
+        for (int c = 0; c < P.G; ++c) {
+            const long long pos = pair_begin(P.total, P.G, c);
+            for (int n; cum + (n = tiles_of<WIN>(P, t % P.num_ptiles)) <= pos; ++t) cum += n;
+            ts.tile[c] = t;
+            ts.skip[c] = (int)(pos - cum);
+        }
+    }
 
     // E4M3 K / V are read by the converter warps through P.k8 / P.v8; their
     // kernels take the Q map in the K / V map arguments, unused.
     CUtensorMap tq, tk, tv;
-    SinkMaps<WIN> ts;
     // Keys of the sinks' maps: the sinks alone, or all where they reach the window.
     const uint64_t sink_keys = P.base > 0 && sinks > 0 ? (uint64_t)sinks : (uint64_t)KV;
     if (packed) {
