@@ -83,6 +83,10 @@ constexpr int COLS = BN / NWG;                // S columns per softmax thread
 constexpr int NSOFT = 128 * NWG;              // softmax threads per CTA
 constexpr int V_WARP = 2 + NSOFT / 32;
 constexpr int XCH_BYTES = 3 * NWG * BM * 4;  // part maxima [parity][part][row], sums [part][row]
+// Epilogue: a softmax warp's 32 rows x 64 bytes on their way to memory, rows padded by 16
+// bytes (eight rows' 16-byte units then use different banks).
+constexpr int OUT_ROW = 64 + 16;
+constexpr int OUT_BYTES = NSOFT / 32 * 32 * OUT_ROW;
 
 // S buffers follow O in tensor memory: two of 128 columns after a 256-column
 // O (DH = 256), three after a 128-column O (DH = 128).
@@ -118,7 +122,7 @@ struct Cfg {
     static constexpr int PV_WARP = DH == 128 ? V_WARP + 1 + NCONV : -1;
     static constexpr int NTHREADS = 32 * (V_WARP + 1 + NCONV + (DH == 128 ? 1 : 0));
     static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + Q_BYTES +
-                                      XCH_BYTES + NUM_BARS * 8 + 16;
+                                      XCH_BYTES + OUT_BYTES + NUM_BARS * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 constexpr uint32_t TMEM_COLS = 512;
@@ -501,14 +505,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
-    // Layout: fp16 ring | Q | exchange | barriers | tmem address.
+    // Layout: fp16 ring | Q | exchange | output rows | barriers | tmem address.
     const uint32_t s_ring = base;
     const uint32_t s_q = base + RING_BYTES;
-    const uint32_t s_bars = s_q + Q_BYTES + XCH_BYTES;
+    const uint32_t s_bars = s_q + Q_BYTES + XCH_BYTES + OUT_BYTES;
     const Bars<NRING> BR{s_bars};
     float* xch = reinterpret_cast<float*>(base_ptr + RING_BYTES + Q_BYTES);
     uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(base_ptr + RING_BYTES + Q_BYTES +
-                                                          XCH_BYTES + NUM_BARS * 8);
+                                                          XCH_BYTES + OUT_BYTES + NUM_BARS * 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_ptr + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -555,6 +559,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // The merge kernel may be scheduled now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;");
 
+    // A windowed call is short beside its own launch, which overlaps the kernel in front
+    // (152 -> 148 us): nothing of global memory is read or written before that is done.
+    if constexpr (WIN) asm volatile("griddepcontrol.wait;" ::: "memory");
     SegIter<MH, WIN> it;
     it.init(P, tm_sink, pair);
     int pt, hd, jb, je, n;
@@ -1055,9 +1062,30 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             float l_row = xl[row];
 #pragma unroll
             for (int h = 1; h < NWG; ++h) l_row += xl[h * BM + row];
+            // A thread has a row, and a warp's stores of rows apart touch 32 lines each
+            // (3.5 us for a tile of fp16, 6 us of fp32): 64 bytes of every row go through
+            // shared memory, and four lanes store a row's.
+            uint8_t* const mine = base_ptr + RING_BYTES + Q_BYTES + XCH_BYTES +
+                                  (warp - 2) * (32 * OUT_ROW);
+            const int m_row0 = m_row - lane;   // the warp's first row
+            auto turn = [&](const uint32_t* v, auto&& store) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint4*>(mine + lane * OUT_ROW + e * 16) =
+                        make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = (lane >> 2) + 8 * e;
+                    store(r, lane & 3,
+                          *reinterpret_cast<const uint4*>(mine + r * OUT_ROW + (lane & 3) * 16));
+                }
+                __syncwarp();
+            };
             if (jb == 0 && je == n) {
                 const float inv = (l_row > 0.f) ? vsc / l_row : 0.f;
-                uint4* dst = reinterpret_cast<uint4*>(P.out + (MH ? (size_t)hd * DH : 0) + (size_t)m_row * P.out_stride + OCOLS * hg);
+                __half* dst = P.out + (MH ? (size_t)hd * DH : 0) + (size_t)m_row0 * P.out_stride +
+                              OCOLS * hg;
 #pragma unroll 1
                 for (int c = 0; c < OCOLS / 32; ++c) {
                     uint32_t o[32];
@@ -1068,17 +1096,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int e = 0; e < 16; ++e)
                         hv[e] = pack_half2(__uint_as_float(o[2 * e]) * inv,
                                            __uint_as_float(o[2 * e + 1]) * inv);
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[c * 4 + e] = make_uint4(hv[4 * e], hv[4 * e + 1], hv[4 * e + 2],
-                                                        hv[4 * e + 3]);
-                    }
+                    turn(hv, [&](int r, int u, const uint4& v) {
+                        if (m_row0 + r < P.M_total)
+                            *reinterpret_cast<uint4*>(dst + (size_t)r * P.out_stride + c * 32 +
+                                                      u * 8) = v;
+                    });
                 }
             } else {
                 const int slot = is_first ? 0 : 1;
                 const size_t prow = ((size_t)pair * 2 + slot) * BM2 + BM * rank + row;
-                uint4* dst = reinterpret_cast<uint4*>(P.ws_o + prow * DH + OCOLS * hg);
+                float* dst = P.ws_o + (prow - lane) * DH + OCOLS * hg;
 #pragma unroll 1
                 for (int c = 0; c < OCOLS / 32; ++c) {
                     uint32_t o[32];
@@ -1090,8 +1117,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * vsc);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[c * 8 + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int h = 0; h < 2; ++h)
+                        turn(o + 16 * h, [&](int r, int u, const uint4& v) {
+                            *reinterpret_cast<uint4*>(dst + (size_t)r * DH + c * 32 + h * 16 +
+                                                      u * 4) = v;
+                        });
                 }
                 if (hg == 0) {
                     P.ws_ml[prow * 2 + 0] = m_ref;
@@ -1145,6 +1175,7 @@ prefill_merge_kernel(const Params P, const __grid_constant__ MergeTasks T) {
     const int hd = MH ? P.ptiles.div(t) : 0;        // head of tile-space index t
     const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int m_row = (t - hd * P.num_ptiles) * BM2 + r;
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (m_row >= P.M_total) return;
     const int d0 = (threadIdx.x & 31) * 8;
@@ -1236,19 +1267,22 @@ static int launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
     if (ensure_smem_limit(reinterpret_cast<const void*>(prefill_kernel<MH, DH, F8, WIN>),
                           C::SMEM_BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
-    prefill_kernel<MH, DH, F8, WIN>
-        <<<2 * P.G, C::NTHREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, ts, P);
-    if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * P.G);
+    cfg.blockDim = dim3(C::NTHREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = WIN ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, prefill_kernel<MH, DH, F8, WIN>, tq, tk, tv, ts, P) != cudaSuccess)
+        return GQA_ERR_CUDA;
     if (tasks.n > 0) {
-        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(tasks.n, BM2 / 8);
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, prefill_merge_kernel<MH, DH>, P, tasks) != cudaSuccess)
             return GQA_ERR_CUDA;
