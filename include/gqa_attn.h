@@ -192,13 +192,14 @@ int gqa_attn_paged_e4m3_batch(const void* q, const uint8_t* kcache, const uint8_
 
 /* The batched tails with a sliding window and first tokens that stay visible
  * ("sinks"): the row at position p sees the keys j <= p with j > p - window or
- * j < sinks; window >= 1, sinks >= 0.  Arguments, layouts and workspace of
+ * j < sinks; window >= 1, sinks >= 0.  Arguments and layouts of
  * gqa_attn_paged_e4m3_batch, any batch from 1 on, except: a context length may be
  * anything from 0 to max_ctx_len (others are clamped and flag
  * GQA_DEVERR_BAD_CTX_LEN), and a row that sees no key (a context shorter than
  * query_rows, or of no tokens) gets zeros.  Only tiles that some row sees are read
  * (table entries of other pages need not be valid), and keys that no row of a sequence
- * sees may hold any byte; one that a row sees must not be the E4M3 NaN code. */
+ * sees may hold any byte; one that a row sees must not be the E4M3 NaN code.  Limits,
+ * precision, division of the work and workspace as for gqa_attn_paged_fp4. */
 int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8_t* vcache,
                                const float* kscale, const float* vscale,
                                const int32_t* block_tables, int table_stride, int num_pages,
@@ -249,12 +250,12 @@ int gqa_attn_paged_e4m3_noalloc(const void* q, const uint8_t* kcache, const uint
  * entries of pages that no row sees are not read; others outside the cache read page 0
  * and flag GQA_DEVERR_BAD_PAGE_ID.  Keys that a row does not see have no effect on it,
  * whatever their bytes (NaN scales included).
- * 1 <= batch <= 1024; num_pages * page < 2^31; batch * Hkv * ceil(max_ctx_len / 128) <
- * 2^29 (GQA_ERR_UNSUPPORTED).  FP32 accumulation; cached values enter the
+ * 1 <= batch <= 1024; num_pages * page < 2^31; batch * Hkv * max_ctx_len < 2^35
+ * (GQA_ERR_UNSUPPORTED beyond).  FP32 accumulation; cached values enter the
  * products exactly, P rounded to fp16.  The visible tiles of all sequences and KV
  * heads are divided equally between the SMs on the device, and what is cut is joined
  * in a fixed order by a second kernel.  Workspace: gqa_workspace_bytes(
- * GQA_KIND_PAGED_FP4, query_rows, any, Hq, D), for any batch and context. */
+ * GQA_KIND_TAILS, query_rows, any, Hq, D), for any batch and context. */
 int gqa_attn_paged_fp4(const void* q, const uint8_t* kcache, const uint8_t* vcache,
                        const float* kscale, const float* vscale, const int32_t* block_tables,
                        int table_stride, int num_pages, int page, const int32_t* ctx_lens_dev,
@@ -475,7 +476,7 @@ int gqa_select_blocks(const void* q, const int8_t* index, const float* index_sca
 #define GQA_KIND_SPARSE 2
 #define GQA_KIND_PAGED_E4M3_BATCH 3   /* ctx_or_kv = number of sequences */
 #define GQA_KIND_SELECT_BLOCKS 4
-#define GQA_KIND_PAGED_FP4 5          /* ctx_or_kv unused */
+#define GQA_KIND_TAILS 5   /* 4-bit and windowed tails; ctx_or_kv unused */
 
 /* Bytes of workspace an entry point of `kind` needs for the given shape on
  * the current device (query_rows = Q or the tail/row count, ctx_or_kv = KV or

@@ -36,7 +36,7 @@ KIND_PAGED_E4M3 = 1
 KIND_SPARSE = 2
 KIND_PAGED_E4M3_BATCH = 3
 KIND_SELECT_BLOCKS = 4
-KIND_PAGED_FP4 = 5
+KIND_TAILS = 5
 DTYPE_F16 = 0
 DTYPE_BF16 = 1
 DEVERR_WAIT_TIMEOUT = 0x1
@@ -730,7 +730,7 @@ def paged_fp4(q, kcache, vcache, kscale, vscale, block_tables, ctx_lens_dev, max
     lib = load() if _lib is None else _lib
     idx = _device_of(q)
     kp, vp, pages = _fp4_pages(kcache, vcache, idx)
-    return _tails(lib.gqa_attn_paged_fp4, KIND_PAGED_FP4, q, idx, pages, (kp, vp), kscale, vscale,
+    return _tails(lib.gqa_attn_paged_fp4, KIND_TAILS, q, idx, pages, (kp, vp), kscale, vscale,
                   block_tables, ctx_lens_dev, max_ctx_len, scale, window, sinks, out, stream)
 
 
@@ -742,7 +742,7 @@ def paged_e4m3_window(q, kcache, vcache, kscale, vscale, block_tables, ctx_lens_
     lib = load() if _lib is None else _lib
     idx = _device_of(q)
     kp, vp, pages = _pages(kcache, vcache, torch.uint8, idx)
-    return _tails(lib.gqa_attn_paged_e4m3_window, KIND_PAGED_E4M3_BATCH, q, idx, pages, (kp, vp),
+    return _tails(lib.gqa_attn_paged_e4m3_window, KIND_TAILS, q, idx, pages, (kp, vp),
                   kscale, vscale, block_tables, ctx_lens_dev, max_ctx_len, scale, window, sinks,
                   out, stream)
 

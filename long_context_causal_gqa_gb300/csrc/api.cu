@@ -393,7 +393,7 @@ int gqa_attn_paged_e4m3_batch(const void* q, const uint8_t* kcache, const uint8_
     if ((long long)table_stride * page < (long long)max_ctx_len) return GQA_ERR_INVALID_ARG;
     return paged_e4m3_batch_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
                                    num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows,
-                                   Hq, Hkv, D, scale, 0, 0, out, stream);
+                                   Hq, Hkv, D, scale, out, stream);
 }
 
 int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8_t* vcache,
@@ -407,11 +407,9 @@ int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8
                                Hkv, D, scale, out);
     if (rc != GQA_OK) return rc;
     if (window < 1 || sinks < 0) return GQA_ERR_INVALID_ARG;
-    // (beyond the longest context both mean all of it)
-    return paged_e4m3_batch_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
-                                   num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows,
-                                   Hq, Hkv, D, scale, window < max_ctx_len ? window : max_ctx_len,
-                                   sinks < max_ctx_len ? sinks : max_ctx_len, out, stream);
+    return tails_launch(false, q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                        num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq, Hkv, D,
+                        scale, window, sinks, out, stream);
 }
 
 int gqa_attn_paged_e4m3_devctx(const void* q, const uint8_t* kcache, const uint8_t* vcache,
@@ -517,9 +515,9 @@ int gqa_attn_paged_fp4(const void* q, const uint8_t* kcache, const uint8_t* vcac
                                Hkv, D, scale, out);
     if (rc != GQA_OK) return rc;
     if (window < 0 || sinks < 0) return GQA_ERR_INVALID_ARG;
-    return paged_fp4_launch(q, kcache, vcache, kscale, vscale, block_tables, table_stride,
-                            num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq, Hkv,
-                            D, scale, window, sinks, out, stream);
+    return tails_launch(true, q, kcache, vcache, kscale, vscale, block_tables, table_stride,
+                        num_pages, page, ctx_lens_dev, max_ctx_len, batch, query_rows, Hq, Hkv, D,
+                        scale, window, sinks, out, stream);
 }
 
 int gqa_cache_read_e4m3(const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
@@ -599,9 +597,9 @@ size_t gqa_workspace_bytes(int kind, int query_rows, int ctx_or_kv, int Hq, int 
         if (query_rows > kMaxTailPackedRows || ctx_or_kv > kMaxTailBatch) return 0;
         return paged_e4m3_batch_workspace_bytes(query_rows * Hq, ctx_or_kv, di->num_sms, D);
     }
-    if (kind == GQA_KIND_PAGED_FP4) {
+    if (kind == GQA_KIND_TAILS) {
         if (query_rows > kMaxTailPackedRows) return 0;
-        return paged_fp4_workspace_bytes(query_rows * Hq, di->num_sms, D);
+        return tails_workspace_bytes(query_rows * Hq, di->num_sms, D);
     }
     if (ctx_or_kv < query_rows) return 0;
     switch (kind) {

@@ -119,8 +119,8 @@ int paged_e4m3_batch_launch(const void* q, const uint8_t* kcache, const uint8_t*
                             const float* kscale, const float* vscale,
                             const int32_t* block_tables, int table_stride, int num_pages,
                             int page, const int* ctx_lens_dev, int max_ctx_len, int batch,
-                            int R, int Hq, int Hkv, int Dh, float scale, int window, int sinks,
-                            void* out, cudaStream_t stream);
+                            int R, int Hq, int Hkv, int Dh, float scale, void* out,
+                            cudaStream_t stream);
 size_t paged_e4m3_batch_workspace_bytes(int nq, int batch, int num_sms, int Dh);
 
 // Same as paged_e4m3_launch, with the split partials in a static device array.
@@ -130,13 +130,14 @@ int paged_e4m3_noalloc_launch(const void* q, const uint8_t* kcache, const uint8_
                               int R, int Hq, int Hkv, int Dh, float scale, void* out,
                               cudaStream_t stream);
 
-// Tails over a 4-bit cache, one sequence or several, with a window (0: none).
-int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache,
-                     const float* kscale, const float* vscale, const int32_t* block_tables,
-                     int table_stride, int num_pages, int page, const int* ctx_lens_dev,
-                     int max_ctx_len, int batch, int R, int Hq, int Hkv, int Dh, float scale,
-                     int window, int sinks, void* out, cudaStream_t stream);
-size_t paged_fp4_workspace_bytes(int nq, int num_sms, int Dh);
+// Tails of a batch over a 4-bit cache (fp4) or an E4M3 one, with a window (0: none).
+int tails_launch(bool fp4, const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                 const float* kscale, const float* vscale, const int32_t* block_tables,
+                 int table_stride, int num_pages, int page, const int* ctx_lens_dev,
+                 int max_ctx_len, int batch, int R, int Hq, int Hkv, int Dh, float scale, int window,
+                 int sinks, void* out, cudaStream_t stream);
+// nq = packed rows of one KV head (at most query_rows * Hq).
+size_t tails_workspace_bytes(int nq, int num_sms, int Dh);
 
 // kcache / vcache: fp16 elements, or E4M3 codes with kscale / vscale (device
 // pointers to one fp32 each) when e4m3 is set.

@@ -95,7 +95,6 @@ struct Params {
     float* ws_ml;   // [G][nq][2]  (m in log2 units, l)
     __half* out;
     unsigned* err;
-    int window, sinks;   // windowed kernels only
 };
 
 // Element offset of packed row r of sequence seq in q / out.  Packed row r is
@@ -206,42 +205,12 @@ struct SplitOwner {
     int b, j, g, ctx;
     bool bad;
 };
-// (with a window, contexts shorter than the rows, or of no tokens, are contexts too:
-// rows that see no key get zeros)
-template <bool WIN>
 __device__ __forceinline__ int clamp_ctx(const Params& P, int c) {
-    const int least = WIN ? 0 : P.R;
-    return c < least ? least : (c > P.ctx_len ? P.ctx_len : c);
+    return c < P.R ? P.R : (c > P.ctx_len ? P.ctx_len : c);
 }
+__device__ __forceinline__ long long tiles_of(int ctx) { return (ctx + TILE - 1) / TILE; }
 
-// The tiles of a context that some row sees with a window: `sink` from its front,
-// then those from tile `first` to its end.
-struct Visible {
-    int lo;      // first key some row's window reaches
-    int first, sink;
-    int n;
-    __device__ int key(int j) const { return (j < sink ? j : first + j - sink) * TILE; }
-};
-__device__ __forceinline__ Visible visible_tiles(const Params& P, int ctx) {
-    Visible v;
-    const int past_first = ctx - P.R + 1;   // (the keys up to the first row's own)
-    v.lo = past_first > P.window ? past_first - P.window : 0;
-    v.first = v.lo / TILE;
-    v.sink = (min(P.sinks, v.first * TILE) + TILE - 1) / TILE;
-    v.n = ctx > 0 ? v.sink + (ctx + TILE - 1) / TILE - v.first : 0;
-    return v;
-}
-template <bool WIN>
-__device__ __forceinline__ long long tiles_of(const Params& P, int ctx) {
-    return WIN ? visible_tiles(P, ctx).n : (ctx + TILE - 1) / TILE;
-}
-// Spare splits of a sequence with `tiles` of `total` tiles.
-template <bool WIN>
-__device__ __forceinline__ int spare_splits(long long spare, long long tiles, long long total) {
-    return WIN && total == 0 ? 0 : (int)(spare * tiles / total);
-}
-
-template <bool BATCHED, bool WIN>
+template <bool BATCHED>
 __device__ SplitOwner split_owner(const Params& P, int split) {
     SplitOwner r;
     if (!BATCHED) {
@@ -249,13 +218,13 @@ __device__ SplitOwner split_owner(const Params& P, int split) {
         r.b = 0;
         r.j = split;
         r.g = P.G;
-        r.ctx = clamp_ctx<WIN>(P, raw);
+        r.ctx = clamp_ctx(P, raw);
         r.bad = raw != r.ctx;
         return r;
     }
     const int lane = threadIdx.x & 31;
     long long total = 0;
-    for (int i = lane; i < P.batch; i += 32) total += tiles_of<WIN>(P, clamp_ctx<WIN>(P, P.ctx_dev[i]));
+    for (int i = lane; i < P.batch; i += 32) total += tiles_of(clamp_ctx(P, P.ctx_dev[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const long long spare = P.G - P.batch;
@@ -265,9 +234,9 @@ __device__ SplitOwner split_owner(const Params& P, int split) {
         int ci = 0, gi = 0, bad = 0;
         if (i < P.batch) {
             const int raw = P.ctx_dev[i];
-            ci = clamp_ctx<WIN>(P, raw);
+            ci = clamp_ctx(P, raw);
             bad = raw != ci;
-            gi = 1 + spare_splits<WIN>(spare, tiles_of<WIN>(P, ci), total);
+            gi = 1 + (int)(spare * tiles_of(ci) / total);
         }
         int incl = gi;
 #pragma unroll
@@ -296,25 +265,22 @@ __device__ SplitOwner split_owner(const Params& P, int split) {
 }
 
 // First split and split count of sequence b (the merge's view of split_owner).
-template <bool WIN>
 __device__ void seq_splits(const Params& P, int b, int& first, int& count) {
-    if (!WIN && P.batch == 1) {
+    if (P.batch == 1) {
         first = 0;
         count = P.G;
         return;
     }
     const int lane = threadIdx.x & 31;
     long long total = 0;
-    for (int i = lane; i < P.batch; i += 32) total += tiles_of<WIN>(P, clamp_ctx<WIN>(P, P.ctx_dev[i]));
+    for (int i = lane; i < P.batch; i += 32) total += tiles_of(clamp_ctx(P, P.ctx_dev[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const long long spare = P.G - P.batch;
     int base = 0;
     for (int i0 = 0; i0 <= b; i0 += 32) {
         const int i = i0 + lane;
-        const int gi = i < P.batch ? 1 + spare_splits<WIN>(
-                                             spare, tiles_of<WIN>(P, clamp_ctx<WIN>(P, P.ctx_dev[i])),
-                                             total)
+        const int gi = i < P.batch ? 1 + (int)(spare * tiles_of(clamp_ctx(P, P.ctx_dev[i])) / total)
                                    : 0;
         int incl = gi;
 #pragma unroll
@@ -333,9 +299,7 @@ __device__ void seq_splits(const Params& P, int b, int& first, int& count) {
     first = count = 0;
 }
 
-// WIN: a sliding window and sinks (the splits are those of the visible tiles, and
-// two more edges are masked).
-template <int NP, int NWG, bool BATCHED, int DH, bool WIN>
+template <int NP, int NWG, bool BATCHED, int DH>
 __global__ void __launch_bounds__(threads_for(NWG), 1)
 paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const Params P) {
@@ -381,15 +345,11 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     // Context length: the launch's, or read on the device (the grid is then
     // sized for the largest context, P.ctx_len, and splits past the actual
     // context get no tiles); with several sequences, this CTA's sequence.
-    const SplitOwner own = split_owner<BATCHED, WIN>(P, split);
+    const SplitOwner own = split_owner<BATCHED>(P, split);
     if (own.b < 0) return;   // uniform: no sequence left for this CTA
     if (own.bad && own.j == 0 && threadIdx.x == 0) atomicOr(P.err, kErrBadCtxLen);
     const int ctx_len = own.ctx;
-    Visible vis_t{};
-    if constexpr (WIN) vis_t = visible_tiles(P, ctx_len);
-    const int n_tiles = WIN ? vis_t.n : (ctx_len + TILE - 1) / TILE;
-    // First key of tile t of the sequence's (visible) tiles.
-    auto tile_key = [&](int t) { return WIN ? vis_t.key(t) : t * TILE; };
+    const int n_tiles = (ctx_len + TILE - 1) / TILE;
     const int t_begin = (int)((long long)own.j * n_tiles / own.g);
     const int t_end = (int)((long long)(own.j + 1) * n_tiles / own.g);
     const int seq = own.b;
@@ -402,14 +362,6 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int pg_end = ntl > 0 ? min(((t_end * TILE - 1) >> lpage) + 1, n_logical) : 0;
     const int32_t* table = P.table + (size_t)seq * P.table_stride;
     auto load_chunk = [&](int k) -> int {
-        if constexpr (WIN) {
-            // Entry by entry of the visible tiles (a tile's pages, or its page).
-            const int lppt = page >= TILE ? 0 : 7 - lpage;
-            const int e = 32 * k + lane, t = t_begin + (e >> lppt);
-            if (t >= t_end) return 0;
-            const int pg = (tile_key(t) >> lpage) + (e & ((1 << lppt) - 1));
-            return pg < n_logical ? __ldg(table + pg) : 0;
-        }
         const int pg = pg_begin + 32 * k + lane;
         return pg < pg_end ? __ldg(table + pg) : 0;
     };
@@ -486,15 +438,15 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 int id = 0, npg = 0, y0 = 0;
                 if (jj < ntl) {
                     const int tile = t_begin + jj;
-                    const int lp0 = tile_key(tile) >> lpage;           // first logical page
-                    const int rel = WIN ? jj * ppt : lp0 - pg_begin;
+                    const int lp0 = (tile * TILE) >> lpage;            // first logical page
+                    const int rel = lp0 - pg_begin;
                     while ((rel >> 5) > cur_k) {
                         cur = nxt;
                         ++cur_k;
                         nxt = load_chunk(cur_k + 1);
                     }
                     npg = min(ppt, n_logical - lp0);
-                    y0 = tile_key(tile) & (page - 1);
+                    y0 = (tile * TILE) & (page - 1);
                     id = __shfl_sync(0xffffffffu, cur, (rel & 31) + (pp < ppt ? pp : 0));
                     if (lane < HALVES * npg && (id < 0 || id >= P.num_pages)) {
                         atomicOr(P.err, kErrBadPageId);
@@ -712,28 +664,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         s[c] = combine3(r1[c], r2[c], r3[c]) *
                                (kSl2InRegs ? sl2[kSl2InRegs ? c : 0] : sl2k * qs[c0 + c]);
                 }
-                const int key0 = tile_key(t_begin + jj);
-                const int key = key0 + k;
-                if constexpr (WIN) {
-                    if (key0 + TILE - 1 > lim_base ||
-                        (key0 < ctx_len - P.window && key0 + TILE - 1 >= P.sinks)) {
-                        // Packed row cg (position lim_base + cg / grp) sees the key iff
-                        // cg >= (key - lim_base) grp, and its window reaches it iff cg <
-                        // (key - lim_base + window) grp.
-                        const int need = max(key - lim_base, 0) * P.grp.d;
-                        const int past =
-                            key < P.sinks
-                                ? 0x7fffffff
-                                : min(max(key - lim_base + P.window, 0), P.R) * P.grp.d;
-#pragma unroll
-                        for (int c = 0; c < NH; ++c) {
-                            const int cg = c0 + c;
-                            const bool vis = (cg < P.nq) ? (cg >= need && cg < past)
-                                                         : (key < ctx_len);
-                            if (!vis) s[c] = -INFINITY;
-                        }
-                    }
-                } else if (key0 + TILE - 1 > lim_base) {
+                const int key = (t_begin + jj) * TILE + k;
+                if ((t_begin + jj) * TILE + TILE - 1 > lim_base) {
                     // Packed row cg (position cg / grp) sees the key iff
                     // cg / grp >= key - lim_base, i.e. cg >= (key - lim_base) grp.
                     const int need = (key - lim_base) * P.grp.d;
@@ -811,18 +743,13 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // held, possibly the E4M3 NaN code; zero their V rows so that
                 // P = 0 times V stays 0.  Each warpgroup clears its share of the
                 // row's 16-byte units (8 per half of d).
-                // (WIN: and keys in front of every row's window that are no sinks.)
-                const bool unseen = WIN ? key0 + TILE > ctx_len ||
-                                              (key0 < vis_t.lo && key0 + TILE > P.sinks)
-                                        : t_begin + jj == n_tiles - 1 &&
-                                              (ctx_len & (TILE - 1)) != 0;
-                if (unseen) {
+                if (t_begin + jj == n_tiles - 1 && (ctx_len & (TILE - 1)) != 0) {
                     const int vi = item_v(jj, ntl);
                     ok = mbar_wait(bar(B_RAW_FULL + vi % NRAW), (uint32_t)((vi / NRAW) & 1), abort_flag,
                                    P.err);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (key >= ctx_len || (WIN && key < vis_t.lo && key >= P.sinks)) {
+                    if (key >= ctx_len) {
                         uint8_t* st = gbase + L::OFF_RAW + (vi % NRAW) * RAW_STAGE + k * 128;
                         for (int u = hg * 8 * HALVES / NWG; u < (hg + 1) * 8 * HALVES / NWG; ++u)
                             *reinterpret_cast<uint4*>(st + (u >> 3) * (TILE * 128) + (u & 7) * 16) =
@@ -930,7 +857,6 @@ constexpr int MERGE_MAX_SPLITS = 1024;
 constexpr int MERGE_WARPS = 16;
 constexpr int MERGE_PF = 10;
 
-template <bool WIN>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) paged_merge_kernel(const Params P) {
     __shared__ float w_s[MERGE_MAX_SPLITS];
     __shared__ float4 red[MERGE_WARPS][32];
@@ -947,7 +873,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) paged_merge_kernel(const Par
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int S0 = 0, G = P.G;                    // this sequence's splits S0 .. S0 + G - 1
-    if (WIN || P.batch > 1) seq_splits<WIN>(P, seq, S0, G);
+    if (P.batch > 1) seq_splits(P, seq, S0, G);
     const float vs = *P.vscale;
     // One round of loads: the O partials of this warp's first MERGE_PF splits
     // and the (m, l) pairs of the splits threadIdx.x + 512 i.
@@ -1036,12 +962,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) paged_merge_kernel(const Par
     }
 }
 
-template <int NP, int NWG, bool BATCHED, int DH, bool WIN>
+template <int NP, int NWG, bool BATCHED, int DH>
 int launch_np_b(const CUtensorMap& tk, const CUtensorMap& tv, Params& P, cudaStream_t stream,
                 int device) {
     using L = Layout<NP, NWG, DH>;
     (void)device;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(paged_split_kernel<NP, NWG, BATCHED, DH, WIN>),
+    if (ensure_smem_limit(reinterpret_cast<const void*>(paged_split_kernel<NP, NWG, BATCHED, DH>),
                           L::SMEM) != GQA_OK)
         return GQA_ERR_CUDA;
     // Both kernels are programmatic dependents of the kernel before them.
@@ -1055,13 +981,13 @@ int launch_np_b(const CUtensorMap& tk, const CUtensorMap& tv, Params& P, cudaStr
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_split_kernel<NP, NWG, BATCHED, DH, WIN>, tk, tv, P) !=
+    if (cudaLaunchKernelEx(&cfg, paged_split_kernel<NP, NWG, BATCHED, DH>, tk, tv, P) !=
         cudaSuccess)
         return GQA_ERR_CUDA;
     cfg.gridDim = dim3(P.batch * P.nq, P.dh / 128);
     cfg.blockDim = dim3(MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<WIN>, P) != cudaSuccess) return GQA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel, P) != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
 }
 
@@ -1074,9 +1000,8 @@ int launch_np(const CUtensorMap& tk, const CUtensorMap& tv, Params& P, cudaStrea
     // One sequence (the common tail) or several (the batched entry point):
     // separate instantiations, so the single-sequence kernel carries none of
     // the batched bookkeeping.
-    if (P.window > 0) return launch_np_b<NP, NWG, true, DH, true>(tk, tv, P, stream, device);
-    return P.batch > 1 ? launch_np_b<NP, NWG, true, DH, false>(tk, tv, P, stream, device)
-                       : launch_np_b<NP, NWG, false, DH, false>(tk, tv, P, stream, device);
+    return P.batch > 1 ? launch_np_b<NP, NWG, true, DH>(tk, tv, P, stream, device)
+                       : launch_np_b<NP, NWG, false, DH>(tk, tv, P, stream, device);
 }
 
 template <int DH>
@@ -1161,7 +1086,6 @@ int paged_e4m3_launch(const void* q, const uint8_t* kcache, const uint8_t* vcach
     P.G = P.n_tiles < di->num_sms ? P.n_tiles : di->num_sms;
     if (P.G > MERGE_MAX_SPLITS) P.G = MERGE_MAX_SPLITS;
     P.scale = scale;
-    P.window = P.sinks = 0;
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
     void* ws;
@@ -1188,8 +1112,8 @@ int paged_e4m3_batch_launch(const void* q, const uint8_t* kcache, const uint8_t*
                             const float* kscale, const float* vscale,
                             const int32_t* block_tables, int table_stride, int num_pages,
                             int page, const int* ctx_lens_dev, int max_ctx_len, int batch,
-                            int R, int Hq, int Hkv, int Dh, float scale, int window,
-                            int sinks, void* out, cudaStream_t stream) {
+                            int R, int Hq, int Hkv, int Dh, float scale, void* out,
+                            cudaStream_t stream) {
     using namespace paged;
     const DeviceInfo* di = device_info();
     if (!di) return GQA_ERR_CUDA;
@@ -1214,15 +1138,6 @@ int paged_e4m3_batch_launch(const void* q, const uint8_t* kcache, const uint8_t*
     P.G = batch > di->num_sms ? batch : di->num_sms;
     if (P.G > MERGE_MAX_SPLITS) return GQA_ERR_UNSUPPORTED;
     P.scale = scale;
-    P.window = window;
-    P.sinks = sinks;
-    if (window > 0) {
-        // No more splits than the windows and sinks have tiles (the rows' windows
-        // cover window + R - 1 keys, which lie in one tile more than they fill).
-        const long long most = batch * (((long long)window + R - 2) / TILE + 2 +
-                                        ((long long)sinks + TILE - 1) / TILE);
-        if (most < P.G) P.G = (int)most;
-    }
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
     void* ws;
@@ -1306,7 +1221,6 @@ int paged_e4m3_noalloc_launch(const void* q, const uint8_t* kcache, const uint8_
     P.G = P.n_tiles < di->num_sms ? P.n_tiles : di->num_sms;
     if (P.G > kNoAllocMaxSplits) P.G = kNoAllocMaxSplits;
     P.scale = scale;
-    P.window = P.sinks = 0;
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
     if (P.nq > kNoAllocMaxRows || (size_t)P.G * P.nq * (Dh + 2) > kNoAllocFloats)

@@ -40,9 +40,8 @@
 #include "sm100.cuh"
 
 namespace gqa {
-namespace paged4 {
+namespace tails {
 
-constexpr int TILE = 128;                  // keys of a tile
 constexpr int MAX_BATCH = 1024;
 constexpr float RESCALE_THRESHOLD = 8.0f;
 
@@ -53,6 +52,7 @@ struct Params {
     const int32_t* tables;
     const int* ctx_lens;
     int table_stride, num_pages, page, log2_page, max_ctx, batch;
+    int ltile;                   // log2 of the keys of a tile
     int R, hq, hkv;
     FastDiv grp;                 // query heads of one KV head
     int nq;                      // packed rows of one KV head (R * grp)
@@ -82,9 +82,10 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
     s.ctx = min(max(raw, 0), P.max_ctx);
     const int first_row = s.ctx - P.R + 1;   // (keys up to the first row's own)
     s.lo = P.window > 0 && first_row > P.window ? first_row - P.window : 0;
-    s.first_tile = s.lo / TILE;
-    s.sink_tiles = (min(P.sinks, s.first_tile * TILE) + TILE - 1) / TILE;
-    s.tiles = s.ctx > 0 ? s.sink_tiles + (s.ctx + TILE - 1) / TILE - s.first_tile : 0;
+    s.first_tile = s.lo >> P.ltile;
+    const int sinks = min(P.sinks, s.first_tile << P.ltile);
+    s.sink_tiles = sinks > 0 ? ((sinks - 1) >> P.ltile) + 1 : 0;
+    s.tiles = s.ctx > 0 ? s.sink_tiles + ((s.ctx - 1) >> P.ltile) + 1 - s.first_tile : 0;
     return s;
 }
 
@@ -263,34 +264,14 @@ __device__ __forceinline__ void meet(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ int tile_key(const Span& s, int j) {
-    return (j < s.sink_tiles ? j : s.first_tile + j - s.sink_tiles) * TILE;
+__device__ __forceinline__ int tile_key(const Params& P, const Span& s, int j) {
+    return (j < s.sink_tiles ? j : s.first_tile + j - s.sink_tiles) << P.ltile;
 }
 
 // Element offset of packed row r of a KV head in q / out.
 __device__ __forceinline__ long long row_offset(const Params& P, int b, int h, int r, int dh) {
     const int pos = P.grp.div(r);
     return (((long long)b * P.R + pos) * P.hq + h * P.grp.d + (r - pos * P.grp.d)) * dh;
-}
-
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The 8 x 8 matrix of 16-bit values the warp holds, transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
-    return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
-}
-__device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
-    return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
 }
 
 // This CTA's range of the tiles.  Nothing of global memory is read or written before the
@@ -335,6 +316,155 @@ __device__ __forceinline__ void finish_empty(const Params& P, const Pieces& it, 
     }
 }
 
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The 8 x 8 matrix of 16-bit values the warp holds, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
+    return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+}
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
+    return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+}
+
+// What a tile of a cache looks like in shared memory, and how the products' fragments are
+// made of it.  A lane (gid, t) of a warp loads, of K, its share of the key gid: places
+// that need not be neighbours, as long as Q has the same order; of V, of four keys, the
+// places of gid.
+//   key_of(k): the key that stands at place k of the sixteen along the second product's K.
+//     Any order does if P has the same one.
+//   K::load(x), K::decode(i, h): load x of LOADS, then for each GROUPS eight places as four
+//     fp16 pairs; q_of(t, x, i): where Q has these eight, q_at(c) where its places 8 c
+//     go; q_place(t, x, i): which they are.
+//   pairs(a, b, lo, hi): eight places of two keys as (key a, key b) pairs, the even ones
+//     and the odd ones.
+template <bool F8, int DH>
+struct Rows;
+
+// 4-bit rows (fp4_rows.cuh), as they are in memory.
+template <int DH>
+struct Rows<false, DH> {
+    static constexpr int TILE = 128;
+    static constexpr int TILE_BYTES = TILE * fp4::row_bytes(DH);   // of K, or of V
+    static constexpr int ROWB = fp4::row_bytes(DH);
+    static constexpr int LOADS = 2, GROUPS = DH / 64;
+    // Queries: a lane's part of a row so that the eight lanes of a load's phase use
+    // different banks (DH 256: quarters padded by 16 bytes; 128: rows).
+    static constexpr int Q_ROW = DH == 256 ? 4 * 144 : 272;
+    // (Spreads the four keys that a quarter of a warp loads words of over the banks:
+    // rows are 36 or 18 words apart.)
+    static __device__ __forceinline__ int key_of(int k) {
+        return DH == 256 ? k : (k & 6) * 2 + (k & 1) + (k >> 3) * 2;
+    }
+    static __device__ __forceinline__ int q_at(int c) {
+        return DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
+    }
+    static __device__ __forceinline__ int q_of(int t, int x, int i) {
+        return DH == 256 ? t * 144 + x * 64 + i * 16 : t * 32 + x * 128 + i * 16;
+    }
+    static __device__ __forceinline__ int q_place(int t, int x, int i) {
+        return DH == 256 ? t * 64 + x * 32 + i * 8 : x * 64 + t * 16 + i * 8;
+    }
+    struct K {
+        uint32_t w[GROUPS], u[GROUPS / 2];
+        __device__ __forceinline__ void load(const uint8_t* tile, int key, int t, int x) {
+            const uint8_t* row = tile + key * ROWB;
+            if constexpr (DH == 256) {
+                const uint4 v = *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                const uint32_t c = fp4::scales2(
+                    *reinterpret_cast<const uint16_t*>(row + DH / 2 + t * 4 + x * 2));
+                u[0] = __byte_perm(c, 0, 0x1010);
+                u[1] = __byte_perm(c, 0, 0x3232);
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(row + t * 8 + x * 32);
+                w[0] = v.x, w[1] = v.y;
+                u[0] = fp4::scales2(row[DH / 2 + t + x * 4] * 0x101u);
+            }
+        }
+        __device__ __forceinline__ void decode(int i, uint32_t (&h)[4]) const {
+            fp4::decode8(w[i], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = fp4::mul2(h[e], u[i / 2]);
+        }
+    };
+    // (with the pair's scales u)
+    static __device__ __forceinline__ void pairs(uint32_t a, uint32_t b, uint32_t u,
+                                                 uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+        fp4::decode8(low_nibbles(a, b), lo);
+        fp4::decode8(high_nibbles(a, b), hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            lo[e] = fp4::mul2(lo[e], u);
+            hi[e] = fp4::mul2(hi[e], u);
+        }
+    }
+};
+
+// E4M3 rows, in halves of 128 bytes with the 128-byte swizzle: unit u (16 bytes) of row r
+// at (u ^ r % 8) * 16.
+template <int DH>
+struct Rows<true, DH> {
+    static constexpr int TILE = DH == 256 ? 64 : 128;   // (stages of 32 KB)
+    static constexpr int HALF_BYTES = TILE * 128, TILE_BYTES = TILE * DH;
+    static constexpr int LOADS = DH / 64, GROUPS = 2;
+    // (a lane's 64 bytes of each half padded by 16, a row by 64)
+    static constexpr int Q_ROW = DH / 128 * 4 * 80 + (DH == 256 ? 64 : 0);
+    static __device__ __forceinline__ int key_of(int k) { return k; }
+    static __device__ __forceinline__ int q_at(int c) { return c / 4 * 80 + c % 4 * 16; }
+    static __device__ __forceinline__ int q_of(int t, int x, int i) {
+        return ((x >> 1) * 4 + t) * 80 + (x & 1) * 32 + i * 16;
+    }
+    static __device__ __forceinline__ int q_place(int t, int x, int i) {
+        return (x >> 1) * 128 + t * 32 + (x & 1) * 16 + i * 8;
+    }
+    static __device__ __forceinline__ int at(int key, int half, int unit) {
+        return half * HALF_BYTES + key * 128 + ((unit ^ (key & 7)) << 4);
+    }
+    static __device__ __forceinline__ uint32_t two(uint32_t v) {   // codes of the low 16 bits
+        return fp4::scales2(v);
+    }
+    struct K {
+        uint32_t w[4];
+        __device__ __forceinline__ void load(const uint8_t* tile, int key, int t, int x) {
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + at(key, x >> 1, 2 * t + (x & 1)));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
+        __device__ __forceinline__ void decode(int i, uint32_t (&h)[4]) const {
+            h[0] = two(w[2 * i]);
+            h[1] = two(w[2 * i] >> 16);
+            h[2] = two(w[2 * i + 1]);
+            h[3] = two(w[2 * i + 1] >> 16);
+        }
+    };
+    // (four places of a word: lo[0], hi[0], lo[1], hi[1])
+    static __device__ __forceinline__ void pairs4(uint32_t a, uint32_t b, uint32_t* lo,
+                                                  uint32_t* hi) {
+        const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
+        lo[0] = two(x);
+        hi[0] = two(x >> 16);
+        lo[1] = two(y);
+        hi[1] = two(y >> 16);
+    }
+};
+
+// Tensor maps of an E4M3 cache, [num_pages * page, Hkv * DH] codes, K and V.
+template <bool F8>
+struct Maps {
+    CUtensorMap kv[2];
+};
+template <>
+struct Maps<false> {};
+
 // Tiles are dealt to the NG groups in turn, tile n to group n % NG as its tile i = n / NG.
 // Its data go to stage n % STAGES of the ring, its barriers are number
 // (n % NG) STAGES + i % STAGES of NG STAGES "full" and as many "empty" ones: a group's
@@ -355,17 +485,20 @@ __device__ __forceinline__ uint32_t tile_phase(uint32_t n) {
 // tile's time at the memory's rate; 62 us for 64 sequences of up to 8192 tokens).
 constexpr int COPY_WARPS = 4;
 
-template <int DH, int NG, int STAGES>
-__device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Seqs& seqs,
-                                           uint32_t ring, uint32_t bars, volatile int* abort_flag,
-                                           int warp) {
-    constexpr int ROWB = fp4::row_bytes(DH);
+template <bool F8, int DH, int NG, int STAGES>
+__device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps, Pieces& it,
+                                           const Seqs& seqs, uint32_t ring, uint32_t bars,
+                                           volatile int* abort_flag, int warp) {
+    using W = Rows<F8, DH>;
+    constexpr int HALVES = F8 ? DH / 128 : 1;     // copies of a page's rows of K (or V)
+    constexpr int BYTES = W::TILE_BYTES / W::TILE / HALVES;   // of a row in one copy
     const int lane = threadIdx.x & 31;
-    // Rows of a copy, copies of a tile's K (and V); this lane's is of K or V, page p.
-    const int rows = min(P.page, TILE), lppt = max(7 - P.log2_page, 0), ppt = 1 << lppt;
-    const int kv = warp & 1, p = lane * (COPY_WARPS / 2) + (warp >> 1);
-    const uint8_t* const cache = kv ? P.cache[1] : P.cache[0];
-    const uint32_t to = ring + kv * (TILE * ROWB) + p * rows * ROWB;
+    // Rows of a copy, pages of a tile; this lane's is of K or V, page p, half of D.
+    const int rows = min(P.page, W::TILE), lppt = max(P.ltile - P.log2_page, 0), ppt = 1 << lppt;
+    const int kv = warp & 1, number = lane * (COPY_WARPS / 2) + (warp >> 1);
+    const int p = number / HALVES, half = number % HALVES;
+    const uint32_t to =
+        ring + kv * W::TILE_BYTES + half * (W::TILE_BYTES / HALVES) + p * rows * BYTES;
     const int begin = it.pos;
     uint32_t n = 0;   // tiles so far
     bool ok = true;
@@ -376,7 +509,7 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
         auto entries = [&](int lot) {
             const int e = lot * 32 + lane, j = it.jb + (e >> lppt);
             if (j >= it.je) return 0;
-            const int lp = (tile_key(it.s, j) >> P.log2_page) + (e & (ppt - 1));
+            const int lp = (tile_key(P, it.s, j) >> P.log2_page) + (e & (ppt - 1));
             return lp < pages ? __ldg(table + lp) : 0;
         };
         int lot = 0, now = entries(0), next = entries(1), after = entries(2);
@@ -390,7 +523,7 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
                 after = entries(lot + 2);
             }
             int id = __shfl_sync(0xffffffffu, now, (e & 31) + (p & (ppt - 1)));
-            const int key0 = tile_key(it.s, j);
+            const int key0 = tile_key(P, it.s, j);
             const int copies = min(ppt, pages - (key0 >> P.log2_page));
             if (p < copies && (id < 0 || id >= P.num_pages)) {
                 atomicOr(P.err, kErrBadPageId);
@@ -403,14 +536,20 @@ __device__ __forceinline__ void copy_tiles(const Params& P, Pieces& it, const Se
                 if (n >= STAGES)
                     okw = wait(bars + 8 * NG * STAGES + tile_bar<NG, STAGES>(n - STAGES),
                                tile_phase<NG, STAGES>(n - STAGES), abort_flag, P.err);
-                if (okw) mbar_arrive_expect_tx(full, mine * rows * ROWB);
+                if (okw) mbar_arrive_expect_tx(full, mine * rows * BYTES);
             }
             ok = __shfl_sync(0xffffffffu, okw, 0);
             if (!ok) break;
             if (p < copies) {
-                const long long row =
-                    ((long long)id * P.hkv + it.h) * P.page + (key0 & (P.page - 1));
-                bulk_load(to + n % STAGES * (2 * TILE * ROWB), cache + row * ROWB, rows * ROWB, full);
+                const uint32_t dst = to + n % STAGES * (2 * W::TILE_BYTES);
+                if constexpr (F8) {
+                    tma_load_2d(dst, &maps.kv[kv], full, it.h * DH + half * 128,
+                                id * P.page + (key0 & (P.page - 1)));
+                } else {
+                    const long long row =
+                        ((long long)id * P.hkv + it.h) * P.page + (key0 & (P.page - 1));
+                    bulk_load(dst, (kv ? P.cache[1] : P.cache[0]) + row * BYTES, rows * BYTES, full);
+                }
             }
             ++n;
         }
@@ -453,18 +592,20 @@ __device__ __forceinline__ bool unseen(const Params& P, const Span& s, int key) 
     return key >= s.ctx || (key < s.lo && key >= P.sinks);
 }
 
-// DH: head size; NT: eights of packed rows.
-template <int DH, int NT>
+// F8: the cache is E4M3, else 4-bit; DH: head size; NT: eights of packed rows.
+template <bool F8, int DH, int NT>
 struct Config {
+    using W = Rows<F8, DH>;
+    static constexpr int TILE = W::TILE;
     // Two groups of four warps, each group on a tile of its own, so that one's products go
-    // on while the other's warps meet, each warp with 32 keys.  (Groups of eight warps
-    // with 16 keys and half the registers: 28 us instead of 26 for two rows over 200000
-    // tokens, 35 instead of 29 for four.)  The warpgroup behind them copies.  Registers:
-    // what the launch gives (65536 over the threads, by eights) moved from the copies to
-    // the products.
+    // on while the other's warps meet, each warp with 32 keys (16 of a tile of 64).
+    // (Groups of eight warps with 16 keys and half the registers: 28 us instead of 26 for
+    // two rows over 200000 4-bit tokens, 35 instead of 29 for four.)  The warpgroup behind
+    // them copies.  Registers: what the launch gives (65536 over the threads, by eights)
+    // moved from the copies to the products.
     static constexpr int NG = 2;
     static constexpr int GW = 4;
-    static constexpr int KZ = 8 / GW;              // sixteens of keys of a warp
+    static constexpr int KZ = TILE / 16 / GW;      // sixteens of keys of a warp
     static constexpr int NW = GW * NG;
     static constexpr int THREADS = 32 * NW + 128;
     static constexpr int REGS_PRODUCTS = 224;
@@ -472,21 +613,17 @@ struct Config {
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
 
-    static constexpr int ROWB = fp4::row_bytes(DH);
-    static constexpr int STAGE = 2 * TILE * ROWB;
+    static constexpr int STAGE = 2 * W::TILE_BYTES;
     static constexpr int ROWS = 8 * NT;
     // V: slices of 64 places, and the shares of a tile's keys that then occupy a group.
     static constexpr int SLICES = DH / 64, SHARES = GW / SLICES;
     static constexpr int SOURCES = NG * SHARES;    // warps that sum the same places
-    // Query rows: a lane's part of a row so that the eight lanes of a load's phase use
-    // different banks (DH 256: quarters padded by 16 bytes; 128: rows).
-    static constexpr int Q_ROW = DH == 256 ? 4 * 144 : 272;
-    static constexpr int P_ROW = TILE * 2 + 16;    // P^T: rows of 128 keys, padded
+    static constexpr int P_ROW = TILE * 2 + 16;    // P^T: rows of a tile's keys, padded
     static constexpr int P_BYTES = NG * ROWS * P_ROW;
     static constexpr int JOIN_ROW = DH / 4 + 4;    // floats of a row in one round of the join
 
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_P = OFF_Q + ROWS * Q_ROW;      // [NG][ROWS]
+    static constexpr int OFF_P = OFF_Q + ROWS * W::Q_ROW;   // [NG][ROWS]
     static constexpr int OFF_JOIN = OFF_P;                  // [SOURCES][ROWS], when P is done with
     static constexpr int JOIN_BYTES = SOURCES * ROWS * JOIN_ROW * 4;
     static constexpr int OFF_MAX = OFF_P + (P_BYTES > JOIN_BYTES ? P_BYTES : JOIN_BYTES);   // [NW][ROWS]
@@ -497,28 +634,30 @@ struct Config {
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
     static constexpr int OFF_FLAG = OFF_BARS + 2 * NG * MAX_STAGES * 8;   // [NG][2]
     static constexpr int OFF_ABORT = OFF_FLAG + NG * 2 * 4;
-    static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
-    // The bytes in flight set the copy rate: all that is left, up to 184 KB.
-    static constexpr int FIT = (232448 - OFF_RING) / STAGE;
-    static constexpr int STAGES = FIT < (DH == 256 ? 5 : 10) ? FIT : (DH == 256 ? 5 : 10);
-    static constexpr int BYTES = OFF_RING + STAGES * STAGE;
+    static constexpr int OFF_RING = (OFF_ABORT + 4 + 1023) / 1024 * 1024;
+    // The bytes in flight set the copy rate: all that is left, up to 192 KB.
+    static constexpr int MOST = 196608 / STAGE < MAX_STAGES ? 196608 / STAGE : MAX_STAGES;
+    static constexpr int FIT = (232448 - 1024 - OFF_RING) / STAGE;
+    static constexpr int STAGES = FIT < MOST ? FIT : MOST;
+    static constexpr int BYTES = 1024 + OFF_RING + STAGES * STAGE;   // (1024: its alignment)
     static_assert(STAGES >= 2 && BYTES <= 232448, "shared memory");
 };
 
-// The k-th place along the products' K of the 16 keys of a warp, for the values: which
-// key it is.  Any order does if P has the same one; these spread the four keys that a
-// quarter of a warp loads words of over the banks (rows 36 or 18 words apart).
-template <int DH>
-__device__ __forceinline__ int key_of(int k) {
-    return DH == 256 ? k : (k & 6) * 2 + (k & 1) + (k >> 3) * 2;
+// Dynamic shared memory from a multiple of 1024 on (the swizzle goes by the address).
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) {
+    return raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
 }
 
-template <int DH, int NT>
-__global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const Params P) {
-    using C = Config<DH, NT>;
-    constexpr int ROWB = C::ROWB, ROWS = C::ROWS, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
+template <bool F8, int DH, int NT>
+__global__ void __launch_bounds__(Config<F8, DH, NT>::THREADS, 1)
+split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
+    using C = Config<F8, DH, NT>;
+    using W = Rows<F8, DH>;
+    constexpr int TILE = C::TILE;
+    constexpr int ROWS = C::ROWS, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
     constexpr int GW = C::GW, KZ = C::KZ;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = aligned_smem(smem_raw);
     int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
@@ -543,8 +682,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
       Pieces it;
       begin_range(P, starts, totals, it, seqs);
       if (warp == NW) finish_empty(P, it, DH);
-      copy_tiles<DH, NG, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
-                                 warp - NW);
+      copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, smem_u32(smem) + C::OFF_RING, bars,
+                                     abort_flag, warp - NW);
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
@@ -586,8 +725,8 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
 #pragma unroll
                 for (int x = 0; x < EACH; ++x) {
                     const int i = threadIdx.x + x * 32 * NW, r = i / (DH / 8), c = i % (DH / 8);
-                    const int at = DH == 256 ? (c / 8) * 144 + (c % 8) * 16 : c * 16;
-                    if (r < ROWS) *reinterpret_cast<uint4*>(sq + r * C::Q_ROW + at) = v[x];
+                    if (r < ROWS)
+                        *reinterpret_cast<uint4*>(sq + r * W::Q_ROW + W::q_at(c)) = v[x];
                 }
             }
             meet_all();
@@ -613,10 +752,10 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
                 wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
                 __syncwarp();
-                const int key0 = tile_key(s, j);
+                const int key0 = tile_key(P, s, j);
                 const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
-                const uint8_t* vst = kst + TILE * ROWB;
+                const uint8_t* vst = kst + W::TILE_BYTES;
                 // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
                 float sc[KZ][NT][4];
 #pragma unroll
@@ -626,45 +765,20 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sc[z][nt][e] = 0.f;
-                    constexpr int HALF = DH / 64;   // words of a lane and key in one load
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t w[2][HALF], u[2][HALF / 2];
+                    for (int x = 0; x < W::LOADS; ++x) {
+                        typename W::K key[2];
+                        key[0].load(kst, k0 + W::key_of(gid), t, x);
+                        key[1].load(kst, k0 + W::key_of(gid + 8), t, x);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint8_t* row = kst + (k0 + key_of<DH>(gid + 8 * e)) * ROWB;
-                            if constexpr (DH == 256) {
-                                const uint4 v =
-                                    *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
-                                w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
-                                const uint32_t c = fp4::scales2(*reinterpret_cast<const uint16_t*>(
-                                    row + DH / 2 + t * 4 + x * 2));
-                                u[e][0] = __byte_perm(c, 0, 0x1010);
-                                u[e][1] = __byte_perm(c, 0, 0x3232);
-                            } else {
-                                // (places 16 t and 64 + 16 t)
-                                const uint2 v =
-                                    *reinterpret_cast<const uint2*>(row + t * 8 + x * 32);
-                                w[e][0] = v.x, w[e][1] = v.y;
-                                u[e][0] = fp4::scales2(row[DH / 2 + t + x * 4] * 0x101u);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < HALF; ++i) {
+                        for (int i = 0; i < W::GROUPS; ++i) {
                             uint32_t a[4], b[4];
-                            fp4::decode8(w[0][i], a);
-                            fp4::decode8(w[1][i], b);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                a[e] = fp4::mul2(a[e], u[0][i / 2]);
-                                b[e] = fp4::mul2(b[e], u[1][i / 2]);
-                            }
+                            key[0].decode(i, a);
+                            key[1].decode(i, b);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint4 qv = *reinterpret_cast<const uint4*>(
-                                    sq + (nt * 8 + gid) * C::Q_ROW +
-                                    (DH == 256 ? t * 144 + x * 64 + i * 16
-                                               : t * 32 + x * 128 + i * 16));
+                                    sq + (nt * 8 + gid) * W::Q_ROW + W::q_of(t, x, i));
                                 mma16816(sc[z][nt], a[0], b[0], a[1], b[1], qv.x, qv.y);
                                 mma16816(sc[z][nt], a[2], b[2], a[3], b[3], qv.z, qv.w);
                             }
@@ -684,7 +798,7 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                             for (int e = 0; e < 4; ++e)
                                 if (!sees(P, row_pos(P, s, row0 + nt * 8 + 2 * t + (e & 1)),
                                           key0 + (gwarp * KZ + z) * 16 +
-                                              key_of<DH>(gid + (e & 2) * 4)))
+                                              W::key_of(gid + (e & 2) * 4)))
                                     sc[z][nt][e] = -INFINITY;
                 }
                 // ---- P by the references as they stand
@@ -783,38 +897,40 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
                 }
                 // ---- O += V^T P^T over the share's keys, 16 at a time
                 constexpr int STEPS = TILE / 16 / C::SHARES;
-                const uint8_t* const vcol = vst + slice * 32 + gid * 4;
-                const uint32_t pick = (gid >> 1) | ((gid >> 1) + 4) << 4;
-                uint32_t c01[STEPS], c23[STEPS];   // scales of a step's pairs of keys
-#pragma unroll
-                for (int x = 0; x < STEPS; ++x) {
-                    uint32_t u[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        u[e] = *reinterpret_cast<const uint32_t*>(
-                            vst + ((share * STEPS + x) * 16 +
-                                   key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB +
-                            DH / 2 + slice * 4);
-                    c01[x] = __byte_perm(u[0], u[1], pick) & 0xffff;
-                    c23[x] = __byte_perm(u[2], u[3], pick) & 0xffff;
-                }
+                // 4-bit: scales of a step's pairs of keys.  Keys no row sees may hold anything:
+                // scales of zero, and E4M3 codes of zero.  NaN scales of keys that some rows
+                // see and others do not are zeros too (0 * NaN), and the rows that see them
+                // are made NaN below.
+                uint32_t c01[STEPS], c23[STEPS];
                 bool apart = false;
-                if (edge) {
-                    // Keys no row sees may hold anything: scales of zero.  NaN scales of
-                    // keys that some rows see and others do not are zeros too (0 * NaN), and
-                    // the rows that see them are made NaN below.
+                if constexpr (!F8) {
+                    const uint32_t pick = (gid >> 1) | ((gid >> 1) + 4) << 4;
 #pragma unroll
-                    for (int x = 0; x < STEPS; ++x)
+                    for (int x = 0; x < STEPS; ++x) {
+                        uint32_t u[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + (share * STEPS + x) * 16 +
-                                            key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
-                            uint32_t& c = e < 2 ? c01[x] : c23[x];
-                            const uint32_t in = 0x7fu << (e & 1) * 8;
-                            const bool none = unseen(P, s, key), nan = (c & in) == in;
-                            if (none || nan) c &= ~(0xffu << (e & 1) * 8);
-                            apart |= nan && !none;
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = *reinterpret_cast<const uint32_t*>(
+                                vst + ((share * STEPS + x) * 16 +
+                                       W::key_of(2 * t + (e & 1) + (e >> 1) * 8)) * W::ROWB +
+                                DH / 2 + slice * 4);
+                        c01[x] = __byte_perm(u[0], u[1], pick) & 0xffff;
+                        c23[x] = __byte_perm(u[2], u[3], pick) & 0xffff;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int x = 0; x < STEPS; ++x)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = key0 + (share * STEPS + x) * 16 +
+                                                W::key_of(2 * t + (e & 1) + (e >> 1) * 8);
+                                uint32_t& c = e < 2 ? c01[x] : c23[x];
+                                const uint32_t in = 0x7fu << (e & 1) * 8;
+                                const bool none = unseen(P, s, key), nan = (c & in) == in;
+                                if (none || nan) c &= ~(0xffu << (e & 1) * 8);
+                                apart |= nan && !none;
+                            }
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < STEPS; x += 2) {
@@ -832,36 +948,46 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int k0 = (share * STEPS + x + y) * 16;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = *reinterpret_cast<const uint32_t*>(
-                                vcol + (k0 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB);
-                        const uint32_t u01 = fp4::scales2(c01[x + y]), u23 = fp4::scales2(c23[x + y]);
                         uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
-                        fp4::decode8(low_nibbles(w[0], w[1]), lo0);
-                        fp4::decode8(high_nibbles(w[0], w[1]), hi0);
-                        fp4::decode8(low_nibbles(w[2], w[3]), lo1);
-                        fp4::decode8(high_nibbles(w[2], w[3]), hi1);
+                        if constexpr (F8) {
+                            uint2 w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t a0 = fp4::mul2(lo0[i], u01);
-                            const uint32_t a1 = fp4::mul2(hi0[i], u01);
-                            const uint32_t a2 = fp4::mul2(lo1[i], u23);
-                            const uint32_t a3 = fp4::mul2(hi1[i], u23);
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = k0 + 2 * t + (e & 1) + (e >> 1) * 8;
+                                w[e] = *reinterpret_cast<const uint2*>(
+                                    vst + W::at(key, slice >> 1, (slice & 1) * 4 + (gid >> 1)) +
+                                    (gid & 1) * 8);
+                                if (edge && unseen(P, s, key0 + key)) w[e] = make_uint2(0, 0);
+                            }
+                            W::pairs4(w[0].x, w[1].x, lo0, hi0);
+                            W::pairs4(w[0].y, w[1].y, lo0 + 2, hi0 + 2);
+                            W::pairs4(w[2].x, w[3].x, lo1, hi1);
+                            W::pairs4(w[2].y, w[3].y, lo1 + 2, hi1 + 2);
+                        } else {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = *reinterpret_cast<const uint32_t*>(
+                                    vst + (k0 + W::key_of(2 * t + (e & 1) + (e >> 1) * 8)) * W::ROWB +
+                                    slice * 32 + gid * 4);
+                            W::pairs(w[0], w[1], fp4::scales2(c01[x + y]), lo0, hi0);
+                            W::pairs(w[2], w[3], fp4::scales2(c23[x + y]), lo1, hi1);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816(o[i][nt], a0, a1, a2, a3, pf[nt][2 * y], pf[nt][2 * y + 1]);
-                        }
+                                mma16816(o[i][nt], lo0[i], hi0[i], lo1[i], hi1[i], pf[nt][2 * y],
+                                         pf[nt][2 * y + 1]);
                     }
                 }
-                if (__any_sync(0xffffffffu, apart)) {
+                if constexpr (!F8) if (__any_sync(0xffffffffu, apart)) {
                     // All places of a lane lie in one block of 16.
                     uint32_t poison = 0;
 #pragma unroll 1
                     for (int k = share * STEPS * 16; k < (share + 1) * STEPS * 16; ++k) {
                         const int key = key0 + k;
-                        if ((vst[k * ROWB + DH / 2 + slice * 4 + (gid >> 1)] & 0x7f) != 0x7f)
+                        if ((vst[k * W::ROWB + DH / 2 + slice * 4 + (gid >> 1)] & 0x7f) != 0x7f)
                             continue;
 #pragma unroll
                         for (int r = 0; r < 2 * NT; ++r)
@@ -977,19 +1103,19 @@ __global__ void __launch_bounds__(Config<DH, NT>::THREADS, 1) split_kernel(const
 // Up to eight packed rows: every warp by itself, 32 keys of a tile, all of D, with its own
 // references, until the end of a piece.  (P never leaves the warp, and nothing meets in
 // a tile; more rows' sums of all of D do not fit a warp's registers.)
-template <int DH>
+template <bool F8, int DH>
 struct Narrow {
-    static constexpr int NG = 2;           // tiles under way
-    static constexpr int KZ = 2;           // sixteens of keys of a warp
-    static constexpr int GW = 8 / KZ;      // warps of a tile
+    using W = Rows<F8, DH>;
+    static constexpr int NG = 2;                     // tiles under way
+    static constexpr int GW = 4;                     // warps of a tile
+    static constexpr int KZ = W::TILE / 16 / GW;     // sixteens of keys of a warp
     static constexpr int NW = NG * GW;
     static constexpr int THREADS = 32 * NW + 128;
     static constexpr int REGS_PRODUCTS = 224, REGS_COPIES = 56;
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
-    static constexpr int ROWB = fp4::row_bytes(DH);
-    static constexpr int STAGE = 2 * TILE * ROWB;
-    static constexpr int STAGES = DH == 256 ? 5 : 10;   // 184 KB
+    static constexpr int STAGE = 2 * W::TILE_BYTES;
+    static constexpr int STAGES = 196608 / STAGE;    // 184 or 192 KB
     // One round of the join: eight places of every gid, of all warps.
     static constexpr int JOIN_ROW = 64 + 4;
     static constexpr int OFF_JOIN = 0;                                   // [NW][8][JOIN_ROW]
@@ -998,17 +1124,20 @@ struct Narrow {
     static constexpr int OFF_TOTALS = OFF_STARTS + (MAX_BATCH + 1) * 4;
     static constexpr int OFF_BARS = (OFF_TOTALS + 8 * 4 + 7) / 8 * 8;
     static constexpr int OFF_ABORT = OFF_BARS + 2 * NG * STAGES * 8;
-    static constexpr int OFF_RING = (OFF_ABORT + 4 + 127) / 128 * 128;
-    static constexpr int BYTES = OFF_RING + STAGES * STAGE;
+    static constexpr int OFF_RING = (OFF_ABORT + 4 + 1023) / 1024 * 1024;
+    static constexpr int BYTES = 1024 + OFF_RING + STAGES * STAGE;   // (1024: its alignment)
     static_assert(BYTES <= 232448, "shared memory");
 };
 
-template <int DH>
-__global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Params P) {
-    using C = Narrow<DH>;
-    constexpr int ROWB = C::ROWB, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
+template <bool F8, int DH>
+__global__ void __launch_bounds__(Narrow<F8, DH>::THREADS, 1)
+narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
+    using C = Narrow<F8, DH>;
+    using W = Rows<F8, DH>;
+    constexpr int STAGES = C::STAGES, NG = C::NG, NW = C::NW;
     constexpr int MT = DH / 16, KZ = C::KZ;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = aligned_smem(smem_raw);
     int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
     int* totals = reinterpret_cast<int*>(smem + C::OFF_TOTALS);
     const uint32_t bars = smem_u32(smem + C::OFF_BARS);
@@ -1029,8 +1158,8 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
         Pieces it;
         begin_range(P, starts, totals, it, seqs);
         if (warp == NW) finish_empty(P, it, DH);
-        copy_tiles<DH, NG, STAGES>(P, it, seqs, smem_u32(smem) + C::OFF_RING, bars, abort_flag,
-                                   warp - NW);
+        copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, smem_u32(smem) + C::OFF_RING, bars,
+                                       abort_flag, warp - NW);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
         Seqs seqs;
@@ -1056,8 +1185,7 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
 #pragma unroll
                 for (int i = 0; i < DH / 32; ++i)
                     q[i] = there ? *reinterpret_cast<const uint4*>(
-                                       src + (DH == 256 ? t * 64 + i * 8
-                                                        : (i >> 1) * 64 + t * 16 + (i & 1) * 8))
+                                       src + W::q_place(t, i / W::GROUPS, i % W::GROUPS))
                                  : make_uint4(0, 0, 0, 0);
             }
             float o[MT][4];
@@ -1075,9 +1203,10 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
                 wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
                 __syncwarp();
-                const int k0 = tile_key(s, j) + gwarp * 16 * KZ;
-                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE + gwarp * 16 * KZ * ROWB;
-                const uint8_t* vst = kst + TILE * ROWB;
+                const int w0 = gwarp * 16 * KZ;   // the warp's first key of the tile
+                const int k0 = tile_key(P, s, j) + w0;
+                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
+                const uint8_t* vst = kst + W::TILE_BYTES;
                 const bool edge = has_edge(P, s, k0, 16 * KZ);
                 // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
                 float sc[KZ][2][4];
@@ -1087,45 +1216,22 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sc[z][x][e] = 0.f;
-                constexpr int HALF = DH / 64;   // words of a lane and key in one load
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t w[KZ][2][HALF], u[KZ][2][HALF / 2];
+                for (int x = 0; x < W::LOADS; ++x) {
+                    typename W::K key[KZ][2];
 #pragma unroll
                     for (int z = 0; z < KZ; ++z)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint8_t* row = kst + (z * 16 + key_of<DH>(gid + 8 * e)) * ROWB;
-                            if constexpr (DH == 256) {
-                                const uint4 v =
-                                    *reinterpret_cast<const uint4*>(row + t * 32 + x * 16);
-                                w[z][e][0] = v.x, w[z][e][1] = v.y;
-                                w[z][e][2] = v.z, w[z][e][3] = v.w;
-                                const uint32_t c = fp4::scales2(*reinterpret_cast<const uint16_t*>(
-                                    row + DH / 2 + t * 4 + x * 2));
-                                u[z][e][0] = __byte_perm(c, 0, 0x1010);
-                                u[z][e][1] = __byte_perm(c, 0, 0x3232);
-                            } else {
-                                // (places 16 t and 64 + 16 t)
-                                const uint2 v =
-                                    *reinterpret_cast<const uint2*>(row + t * 8 + x * 32);
-                                w[z][e][0] = v.x, w[z][e][1] = v.y;
-                                u[z][e][0] = fp4::scales2(row[DH / 2 + t + x * 4] * 0x101u);
-                            }
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            key[z][e].load(kst, w0 + z * 16 + W::key_of(gid + 8 * e), t, x);
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i)
+                    for (int i = 0; i < W::GROUPS; ++i)
 #pragma unroll
                         for (int z = 0; z < KZ; ++z) {
                             uint32_t a[4], b[4];
-                            fp4::decode8(w[z][0][i], a);
-                            fp4::decode8(w[z][1][i], b);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                a[e] = fp4::mul2(a[e], u[z][0][i / 2]);
-                                b[e] = fp4::mul2(b[e], u[z][1][i / 2]);
-                            }
-                            const uint4 qv = q[x * HALF + i];
+                            key[z][0].decode(i, a);
+                            key[z][1].decode(i, b);
+                            const uint4 qv = q[x * W::GROUPS + i];
                             mma16816(sc[z][0], a[0], b[0], a[1], b[1], qv.x, qv.y);
                             mma16816(sc[z][1], a[2], b[2], a[3], b[3], qv.z, qv.w);
                         }
@@ -1141,7 +1247,7 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (!sees(P, row_pos(P, s, 2 * t + (e & 1)),
-                                      k0 + z * 16 + key_of<DH>(gid + (e & 2) * 4)))
+                                      k0 + z * 16 + W::key_of(gid + (e & 2) * 4)))
                                 sv[z][e] = -INFINITY;
                 }
                 bool exceed = false;
@@ -1191,80 +1297,114 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                     }
                 }
                 // ---- O += V^T P^T
-                constexpr int VW = DH / 64;   // words of a lane and key
-                uint32_t c[KZ][4];            // a scale for each 16 values
-#pragma unroll
-                for (int z = 0; z < KZ; ++z)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint8_t* at =
-                            vst + (z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB +
-                            DH / 2 + gid * (DH / 128);
-                        if constexpr (DH == 256) c[z][e] = *reinterpret_cast<const uint16_t*>(at);
-                        else c[z][e] = *at;
-                    }
+                // Keys no row sees may hold anything: their codes, or 4-bit scales, are zeros.
+                // NaN scales of keys that some rows see and others do not are zeros too (0 *
+                // NaN), and the rows that see them are made NaN below.
                 bool apart = false;
-                if (edge) {
-                    // Keys no row sees may hold anything: scales of zero.  NaN scales of
-                    // keys that some rows see and others do not are zeros too (0 * NaN), and
-                    // the rows that see them are made NaN below.
+                if constexpr (F8) {
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z)
+#pragma unroll
+                        for (int h = 0; h < DH / 128; ++h) {
+                            uint4 w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = w0 + z * 16 + 2 * t + (e & 1) + (e >> 1) * 8;
+                                w[e] = *reinterpret_cast<const uint4*>(vst + W::at(key, h, gid));
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (unseen(P, s, k0 + z * 16 + 2 * t + (e & 1) + (e >> 1) * 8))
+                                        w[e] = make_uint4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                auto word = [&](const uint4& v) {
+                                    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+                                };
+                                uint32_t lo0[2], hi0[2], lo1[2], hi1[2];
+                                W::pairs4(word(w[0]), word(w[1]), lo0, hi0);
+                                W::pairs4(word(w[2]), word(w[3]), lo1, hi1);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    mma16816(o[h * 8 + 2 * i + e], lo0[e], hi0[e], lo1[e], hi1[e],
+                                             pf[z][0], pf[z][1]);
+                            }
+                        }
+                } else {
+                    constexpr int VW = DH / 64;   // words of a lane and key
+                    uint32_t c[KZ][4];            // a scale for each 16 values
 #pragma unroll
                     for (int z = 0; z < KZ; ++z)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int k = z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8);
-                            if (unseen(P, s, k0 + k)) c[z][e] = 0;
-#pragma unroll
-                            for (int y = 0; y < DH / 128; ++y)
-                                if ((c[z][e] >> 8 * y & 0x7f) == 0x7f) {
-                                    apart = true;
-                                    c[z][e] &= ~(0xffu << 8 * y);
-                                }
+                            const uint8_t* at =
+                                vst +
+                                (w0 + z * 16 + W::key_of(2 * t + (e & 1) + (e >> 1) * 8)) * W::ROWB +
+                                DH / 2 + gid * (DH / 128);
+                            if constexpr (DH == 256)
+                                c[z][e] = *reinterpret_cast<const uint16_t*>(at);
+                            else
+                                c[z][e] = *at;
                         }
-                }
+                    if (edge) {
 #pragma unroll
-                for (int z = 0; z < KZ; ++z) {
-                    uint32_t w[4][VW];
+                        for (int z = 0; z < KZ; ++z)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint8_t* row =
-                            vst + (z * 16 + key_of<DH>(2 * t + (e & 1) + (e >> 1) * 8)) * ROWB;
-                        if constexpr (DH == 256) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(row + gid * 16);
-                            w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2*>(row + gid * 8);
-                            w[e][0] = v.x, w[e][1] = v.y;
+                            for (int e = 0; e < 4; ++e) {
+                                const int k = z * 16 + W::key_of(2 * t + (e & 1) + (e >> 1) * 8);
+                                if (unseen(P, s, k0 + k)) c[z][e] = 0;
+#pragma unroll
+                                for (int y = 0; y < DH / 128; ++y)
+                                    if ((c[z][e] >> 8 * y & 0x7f) == 0x7f) {
+                                        apart = true;
+                                        c[z][e] &= ~(0xffu << 8 * y);
+                                    }
+                            }
+                    }
+#pragma unroll
+                    for (int z = 0; z < KZ; ++z) {
+                        uint32_t w[4][VW];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint8_t* row =
+                                vst +
+                                (w0 + z * 16 + W::key_of(2 * t + (e & 1) + (e >> 1) * 8)) * W::ROWB;
+                            if constexpr (DH == 256) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(row + gid * 16);
+                                w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2*>(row + gid * 8);
+                                w[e][0] = v.x, w[e][1] = v.y;
+                            }
+                        }
+                        // (words 2 i and 2 i + 1 share a scale)
+                        uint32_t u01[DH / 128], u23[DH / 128];
+#pragma unroll
+                        for (int y = 0; y < DH / 128; ++y) {
+                            u01[y] = fp4::scales2(__byte_perm(c[z][0], c[z][1], y ? 0x0051 : 0x0040));
+                            u23[y] = fp4::scales2(__byte_perm(c[z][2], c[z][3], y ? 0x0051 : 0x0040));
+                        }
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) {
+                            uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
+                            W::pairs(w[0][i], w[1][i], u01[i / 2], lo0, hi0);
+                            W::pairs(w[2][i], w[3][i], u23[i / 2], lo1, hi1);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mma16816(o[4 * i + e], lo0[e], hi0[e], lo1[e], hi1[e], pf[z][0],
+                                         pf[z][1]);
                         }
                     }
-                    // (words 2 i and 2 i + 1 share a scale)
-                    uint32_t u01[DH / 128], u23[DH / 128];
-#pragma unroll
-                    for (int y = 0; y < DH / 128; ++y) {
-                        u01[y] = fp4::scales2(__byte_perm(c[z][0], c[z][1], y ? 0x0051 : 0x0040));
-                        u23[y] = fp4::scales2(__byte_perm(c[z][2], c[z][3], y ? 0x0051 : 0x0040));
-                    }
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) {
-                        uint32_t lo0[4], hi0[4], lo1[4], hi1[4];
-                        fp4::decode8(low_nibbles(w[0][i], w[1][i]), lo0);
-                        fp4::decode8(high_nibbles(w[0][i], w[1][i]), hi0);
-                        fp4::decode8(low_nibbles(w[2][i], w[3][i]), lo1);
-                        fp4::decode8(high_nibbles(w[2][i], w[3][i]), hi1);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mma16816(o[4 * i + e], fp4::mul2(lo0[e], u01[i / 2]),
-                                     fp4::mul2(hi0[e], u01[i / 2]), fp4::mul2(lo1[e], u23[i / 2]),
-                                     fp4::mul2(hi1[e], u23[i / 2]), pf[z][0], pf[z][1]);
-                    }
                 }
-                if (__any_sync(0xffffffffu, apart)) {
+                if constexpr (!F8) if (__any_sync(0xffffffffu, apart)) {
                     uint32_t poison = 0;   // bits: block * 2 + row
 #pragma unroll 1
                     for (int k = 0; k < 16 * KZ; ++k)
 #pragma unroll
                         for (int y = 0; y < DH / 128; ++y)
-                            if ((vst[k * ROWB + DH / 2 + gid * (DH / 128) + y] & 0x7f) == 0x7f)
+                            if ((vst[(w0 + k) * W::ROWB + DH / 2 + gid * (DH / 128) + y] & 0x7f) == 0x7f)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
                                     if (sees(P, row_pos(P, s, 2 * t + e), k0 + k))
@@ -1340,7 +1480,9 @@ __global__ void __launch_bounds__(Narrow<DH>::THREADS, 1) narrow_kernel(const Pa
                         a.x = fmaf(f[x], v.x, a.x);
                         a.y = fmaf(f[x], v.y, a.y);
                     }
-                    const int d = (at >> 2) * (DH / 8) + r * 8 + (at & 3) * 2;
+                    const int d = (F8 ? (r >> 1) * 128 + (at >> 2) * 16 + (r & 1) * 8
+                                      : (at >> 2) * (DH / 8) + r * 8) +
+                                  (at & 3) * 2;
                     if (whole)
                         *reinterpret_cast<uint32_t*>(out + d) = pack_half2(a.x, a.y);
                     else
@@ -1446,13 +1588,14 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P)
     *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * ROWS + r, DH) + d0) = v;
 }
 
-template <int DH, int NT>
-int launch(const Params& P, cudaStream_t stream) {
+template <bool F8, int DH, int NT>
+int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     // (kernel and sizes of one eight of rows, or of more)
-    using C = typename std::conditional<NT == 1, Narrow<DH>, Config<DH, NT == 1 ? 2 : NT>>::type;
-    void (*kernel)(Params);
-    if constexpr (NT == 1) kernel = narrow_kernel<DH>;
-    else kernel = split_kernel<DH, NT>;
+    using C = typename std::conditional<NT == 1, Narrow<F8, DH>,
+                                        Config<F8, DH, NT == 1 ? 2 : NT>>::type;
+    void (*kernel)(Maps<F8>, Params);
+    if constexpr (NT == 1) kernel = narrow_kernel<F8, DH>;
+    else kernel = split_kernel<F8, DH, NT>;
     if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), C::BYTES) != GQA_OK)
         return GQA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
@@ -1465,7 +1608,7 @@ int launch(const Params& P, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, P) != cudaSuccess) return GQA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
     const int rows = P.nq < 8 * NT ? P.nq : 8 * NT;
     cfg.blockDim = dim3(MERGE_WARPS * 32);
@@ -1484,30 +1627,23 @@ int launch(const Params& P, cudaStream_t stream) {
 // Packed rows of a unit: all of a KV head's.
 int unit_rows(int nq) { return nq <= 32 ? (nq + 7) / 8 * 8 : 48; }
 
-template <int DH>
-int launch_rows(const Params& P, cudaStream_t stream) {
+template <bool F8, int DH>
+int launch_rows(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     switch (unit_rows(P.nq)) {
-        case 8: return launch<DH, 1>(P, stream);
-        case 16: return launch<DH, 2>(P, stream);
-        case 24: return launch<DH, 3>(P, stream);
-        case 32: return launch<DH, 4>(P, stream);
-        default: return launch<DH, 6>(P, stream);
+        case 8: return launch<F8, DH, 1>(maps, P, stream);
+        case 16: return launch<F8, DH, 2>(maps, P, stream);
+        case 24: return launch<F8, DH, 3>(maps, P, stream);
+        case 32: return launch<F8, DH, 4>(maps, P, stream);
+        default: return launch<F8, DH, 6>(maps, P, stream);
     }
 }
 
-}  // namespace paged4
-
-size_t paged_fp4_workspace_bytes(int nq, int num_sms, int Dh) {
-    return kWorkspaceCounterBytes +
-           (size_t)num_sms * (2 * paged4::unit_rows(nq < 48 ? nq : 48) * (Dh + 2) * sizeof(float) + sizeof(int4));
-}
-
-int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache,
-                     const float* kscale, const float* vscale, const int32_t* block_tables,
-                     int table_stride, int num_pages, int page, const int* ctx_lens_dev,
-                     int max_ctx_len, int batch, int R, int Hq, int Hkv, int Dh, float scale,
-                     int window, int sinks, void* out, cudaStream_t stream) {
-    using namespace paged4;
+template <bool F8>
+int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, const float* kscale,
+                 const float* vscale, const int32_t* block_tables, int table_stride, int num_pages,
+                 int page, const int* ctx_lens_dev, int max_ctx_len, int batch, int R, int Hq,
+                 int Hkv, int Dh, float scale, int window, int sinks, void* out,
+                 cudaStream_t stream) {
     const DeviceInfo* di = device_info();
     if (!di) return GQA_ERR_CUDA;
     Params P;
@@ -1522,6 +1658,8 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
     P.num_pages = num_pages;
     P.page = page;
     P.log2_page = __builtin_ctz((unsigned)page);
+    const int tile = Dh == 256 ? Rows<F8, 256>::TILE : Rows<F8, 128>::TILE;
+    P.ltile = __builtin_ctz((unsigned)tile);
     P.max_ctx = max_ctx_len;
     P.batch = batch;
     P.R = R;
@@ -1536,7 +1674,7 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
     P.sinks = P.window > 0 ? sinks : 0;
     P.scale = scale;
     // No more ranges than tiles.
-    const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len + TILE - 1LL) / TILE);
+    const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len - 1) / tile + 1);
     if (tiles > 0x1fffffffLL) return GQA_ERR_UNSUPPORTED;   // (with their LEADs below 2^31)
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
     if (P.G > MAX_RANGES) P.G = MAX_RANGES;
@@ -1546,12 +1684,38 @@ int paged_fp4_launch(const void* q, const uint8_t* kcache, const uint8_t* vcache
     void* ws;
     size_t ws_bytes;
     current_workspace(&ws, &ws_bytes);
-    if (!ws || ws_bytes < paged_fp4_workspace_bytes(P.nq, di->num_sms, Dh))
-        return GQA_ERR_WORKSPACE;
+    if (!ws || ws_bytes < tails_workspace_bytes(P.nq, di->num_sms, Dh)) return GQA_ERR_WORKSPACE;
     P.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWorkspaceCounterBytes);
     P.ws_ml = P.ws_o + (size_t)2 * P.G * rows * Dh;
     P.tasks = reinterpret_cast<int4*>(P.ws_ml + (size_t)2 * P.G * rows * 2);
-    return Dh == 256 ? launch_rows<256>(P, stream) : launch_rows<128>(P, stream);
+    Maps<F8> maps;
+    if constexpr (F8) {
+        const uint64_t keys = (uint64_t)num_pages * page, width = (uint64_t)Hkv * Dh;
+        const uint32_t box = page < tile ? page : tile;
+        if (!make_map_2d_u8(&maps.kv[0], kcache, keys, width, width, box, 128) ||
+            !make_map_2d_u8(&maps.kv[1], vcache, keys, width, width, box, 128))
+            return GQA_ERR_CUDA;
+    }
+    return Dh == 256 ? launch_rows<F8, 256>(maps, P, stream)
+                     : launch_rows<F8, 128>(maps, P, stream);
+}
+
+}  // namespace tails
+
+size_t tails_workspace_bytes(int nq, int num_sms, int Dh) {
+    return kWorkspaceCounterBytes +
+           (size_t)num_sms * (2 * tails::unit_rows(nq < 48 ? nq : 48) * (Dh + 2) * sizeof(float) +
+                              sizeof(int4));
+}
+
+int tails_launch(bool fp4, const void* q, const uint8_t* kcache, const uint8_t* vcache,
+                 const float* kscale, const float* vscale, const int32_t* block_tables,
+                 int table_stride, int num_pages, int page, const int* ctx_lens_dev,
+                 int max_ctx_len, int batch, int R, int Hq, int Hkv, int Dh, float scale, int window,
+                 int sinks, void* out, cudaStream_t stream) {
+    const auto fn = fp4 ? tails::launch_tails<false> : tails::launch_tails<true>;
+    return fn(q, kcache, vcache, kscale, vscale, block_tables, table_stride, num_pages, page,
+              ctx_lens_dev, max_ctx_len, batch, R, Hq, Hkv, Dh, scale, window, sinks, out, stream);
 }
 
 }  // namespace gqa

@@ -111,9 +111,9 @@ def test_cache_read_fp4_refuses(lib, kw, want):
 
 def test_workspace_bytes_refuse():
     lib = binding.load()
-    assert lib.gqa_workspace_bytes(binding.KIND_PAGED_FP4, 49, 1, 6, 256) == 0
-    assert lib.gqa_workspace_bytes(binding.KIND_PAGED_FP4, 0, 1, 6, 256) == 0
-    assert lib.gqa_workspace_bytes(binding.KIND_PAGED_FP4, 1, 1, 6, 64) == 0
+    assert lib.gqa_workspace_bytes(binding.KIND_TAILS, 49, 1, 6, 256) == 0
+    assert lib.gqa_workspace_bytes(binding.KIND_TAILS, 0, 1, 6, 256) == 0
+    assert lib.gqa_workspace_bytes(binding.KIND_TAILS, 1, 1, 6, 64) == 0
 
 
 def test_binding_refuses_cpu_tensors():
