@@ -91,17 +91,48 @@ __device__ __forceinline__ float max4_abs(Pair a, Pair b) {
     const float2 x = unpack(a), y = unpack(b);
     return max4_abs(x.x, x.y, y.x, y.y);
 }
-// Four values over their block's scale as E2M1 codes, the first in the lowest
-// nibble: round to nearest even, +-6 beyond the range; zeros for a scale of zero or
-// NaN.  (A true quotient: values and scales have few bits, so that many quotients lie
-// half way between two codes, where the product with a reciprocal may go either way.)
-__device__ __forceinline__ uint32_t to_e2m1x4(Pair a, Pair b, float s) {
-    const float2 x = unpack(a), y = unpack(b);
-    if (!(s > 0.f)) return 0;
-    return __nv_cvt_float2_to_fp4x2(make_float2(x.x / s, x.y / s), __NV_E2M1, cudaRoundNearest) |
-           (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(y.x / s, y.y / s), __NV_E2M1,
-                                              cudaRoundNearest)
-               << 8;
+// A block's scale and its reciprocal: {s, r}.
+//
+// A value's code is that of its true quotient with the scale: values and scales have
+// few bits, so that many quotients lie half way between two codes, where the product
+// with a reciprocal goes either way.  A division a value is most of the arithmetic,
+// though (8000 rows: 26.4 us, against 22.2).  So the product with the rounded
+// reciprocal is corrected by its remainder (Markstein's method): q0 = x r,
+// q = q0 + (x - q0 s) r with two fused operations.  The remainder is exact, so the
+// error is that of r times that of q0, 2^-47 of the quotient before q's own rounding:
+// a half-way quotient comes out exact.  It needs every product finite: blocks with an
+// infinity, a NaN or a magnitude from 2^100 on have r = 0, and divide.  (Products that
+// underflow belong to quotients that round to zero.)
+__device__ __forceinline__ float corrected_quotient(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+__device__ __forceinline__ float2 block_scale(float most, uint32_t* code) {
+    constexpr float kHuge = 0x1p100f;
+    const float sixth =
+        most < kHuge ? corrected_quotient(most, 6.f, 1.f / 6.f) : most / 6.f;
+    *code = __nv_cvt_float_to_fp8(sixth, __NV_SATFINITE, __NV_E4M3);
+    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)*code, __NV_E4M3);
+    const float s = __half2float(*reinterpret_cast<const __half*>(&hr));
+    return make_float2(s, s > 0.f && most < kHuge ? __frcp_rn(s) : 0.f);
+}
+// Four values over their block's scale as E2M1 codes, the first in the lowest nibble:
+// round to nearest even, +-6 beyond the range; zeros for a scale of zero or NaN.
+__device__ __forceinline__ uint32_t to_e2m1x4(Pair a, Pair b, float2 sr) {
+    const float s = sr.x;
+    float2 x, y;
+    if (sr.y > 0.f) {
+        const Pair r = pack(sr.y, sr.y), m = pack(-s, -s);
+        const Pair qa = mul2(a, r), qb = mul2(b, r);
+        x = unpack(fma2(fma2(qa, m, a), r, qa));
+        y = unpack(fma2(fma2(qb, m, b), r, qb));
+    } else {
+        if (!(s > 0.f)) return 0;
+        x = unpack(a), y = unpack(b);
+        x.x /= s, x.y /= s, y.x /= s, y.y /= s;
+    }
+    return __nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest) |
+           (uint32_t)__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest) << 8;
 }
 
 // cos and sin of position * frequency, as a fraction of a turn: frequency / (2 pi)
@@ -150,7 +181,8 @@ __device__ __forceinline__ float2 turn(int pos, float hi, float lo) {
 // 8000 rows of 6 + 1 + 1 heads of 256 into an E4M3 cache move 61 MB, 9.0 us at the
 // copy rate, and take 16.9 us (a plain copy of the same buffers, 11.7): between
 // the loads a head's chain of sum, shuffles and products is exposed, with 20
-// warps an SM to cover it; 8 rows take 2.8 us, most of it the launch.
+// warps an SM to cover it; 8 rows take 2.8 us, most of it the launch.  Into a 4-bit
+// cache, 60 MB, 20.5 us: its blocks' largest magnitudes cross lanes as well.
 //
 // A lane holds two runs of four values: in the rotated part both members of
 // four pairs, so no value crosses lanes.  Pairs (i, i + rot / 2): runs 4 l and
@@ -175,6 +207,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
     __shared__ __align__(16) float s_sin[UNIT][MAX_ROT_PAIRS];
     // FP4: the largest magnitude of every run of four values of a group's head.
     __shared__ __align__(16) float s_most[KIND == FP4 ? GROUPS : 1][UNIT][DH / 4];
+    __shared__ float2 s_block[KIND == FP4 ? GROUPS : 1][UNIT][DH / 16];   // its blocks' scales
     const int t0 = blockIdx.x * P.tile;
     const int nt = min(P.tile, P.rows.tokens - t0);
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -185,10 +218,14 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
     const int run0 = split ? lane * 4 : lane * 8;
     const int run1 = split ? P.pairs + lane * 4 : lane * 8 + 4;
     const int k0 = P.nq, v0 = k0 + P.hkv, heads = v0 + P.hkv;   // heads: q, then K, then V
-    // This group's heads.
+    // This group's heads: neighbours, which share their weights.  For a 4-bit cache every
+    // groups-th one: K's and V's heads cost more than q's there, and neighbours of them
+    // would fall to the same groups (8000 rows: 20.5 us, 22.2 with neighbours).
     const int groups = gridDim.y * GROUPS, per = (heads + groups - 1) / groups;
-    int head = (blockIdx.y * GROUPS + group) * per;
-    const int head_end = min(head + per, heads);
+    const int my_group = blockIdx.y * GROUPS + group;
+    const int head_step = KIND == FP4 ? groups : 1;
+    int head = KIND == FP4 ? my_group : my_group * per;
+    const int head_end = KIND == FP4 ? heads : min(head + per, heads);
 
     struct Place {
         int kind, in_kind;
@@ -248,7 +285,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
 
     int weights_of = -1;     // the kind w belongs to
     Pair w[4];
-    for (; head < head_end; ++head) {
+    for (; head < head_end; head += head_step) {
         const Place p = at_next;
         Pair x[UNIT][4];
 #pragma unroll
@@ -258,8 +295,8 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
             x[i][2] = unpack16<BF16>(next[i][1].x);
             x[i][3] = unpack16<BF16>(next[i][1].y);
         }
-        if (head + 1 < head_end) {
-            at_next = place(head + 1);
+        if (head + head_step < head_end) {
+            at_next = place(head + head_step);
             load(at_next, next);
         }
         const uint16_t* weight = p.kind < 2 ? P.weight[p.kind] : nullptr;
@@ -338,8 +375,13 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
         const float f = p.kind == 1 ? kinv : vinv;
         const Pair ff = pack(f, f);
         if constexpr (KIND == FP4) {
-            // A block of 16 is four runs of up to four lanes, which meet in shared memory.
-            __syncwarp(mates);
+            // A block of 16 is four runs of up to four lanes, which meet in shared memory;
+            // each lane takes the scales of two neighbouring blocks of one token.
+            auto row_of = [&](int i) {
+                return static_cast<uint8_t*>(cache) +
+                       (s_cache[i] + ((long long)p.in_kind << P.rows.log2_page)) *
+                           fp4::row_bytes(DH);
+            };
 #pragma unroll
             for (int i = 0; i < UNIT; ++i) {
 #pragma unroll
@@ -348,26 +390,28 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) write_kernel(const 
                 s_most[group][i][run1 / 4] = max4_abs(x[i][2], x[i][3]);
             }
             __syncwarp(mates);
+            {
+                static_assert(UNIT * DH / 16 == 2 * LANES, "two blocks a lane");
+                const int i = lane / (LANES / UNIT), block = lane % (LANES / UNIT) * 2;
+                const float4* m = reinterpret_cast<const float4*>(&s_most[group][i][block * 4]);
+                uint32_t codes[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    s_block[group][i][block + k] =
+                        block_scale(max4_abs(m[k].x, m[k].y, m[k].z, m[k].w), &codes[k]);
+                if (i < nt && s_cache[i] >= 0)
+                    *reinterpret_cast<uint16_t*>(row_of(i) + DH / 2 + block) =
+                        (uint16_t)(codes[0] | codes[1] << 8);
+            }
+            __syncwarp(mates);
 #pragma unroll
             for (int i = 0; i < UNIT; ++i) {
                 if (i >= nt || s_cache[i] < 0) continue;
-                uint8_t* row = static_cast<uint8_t*>(cache) +
-                               (s_cache[i] + ((long long)p.in_kind << P.rows.log2_page)) *
-                                   fp4::row_bytes(DH);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int run = k ? run1 : run0;
-                    const float4 m =
-                        *reinterpret_cast<const float4*>(&s_most[group][i][run / 16 * 4]);
-                    const float most = max4_abs(m.x, m.y, m.z, m.w);
-                    const __nv_fp8_storage_t code =
-                        __nv_cvt_float_to_fp8(most / 6.f, __NV_SATFINITE, __NV_E4M3);
-                    const __half_raw hr = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
-                    const float s = __half2float(*reinterpret_cast<const __half*>(&hr));
-                    *reinterpret_cast<uint16_t*>(row + run / 2) =
-                        (uint16_t)to_e2m1x4(x[i][2 * k], x[i][2 * k + 1], s);
-                    if (run % 16 == 0) row[DH / 2 + run / 16] = code;
-                }
+                uint8_t* row = row_of(i);
+                *reinterpret_cast<uint16_t*>(row + run0 / 2) =
+                    (uint16_t)to_e2m1x4(x[i][0], x[i][1], s_block[group][i][run0 / 16]);
+                *reinterpret_cast<uint16_t*>(row + run1 / 2) =
+                    (uint16_t)to_e2m1x4(x[i][2], x[i][3], s_block[group][i][run1 / 16]);
             }
             continue;
         }
