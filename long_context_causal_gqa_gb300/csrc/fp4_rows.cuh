@@ -25,7 +25,7 @@ __host__ __device__ constexpr int row_bytes(int d) { return d / 2 + d / 16; }
 
 // Eight codes (a word) as fp16 pairs: r[i] holds the two nibbles of byte i, the
 // low one in the low half.
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&r)[4]) {
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t* r) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"

@@ -212,3 +212,56 @@ def test_stream_and_graph(cuda_lib):
         for p, pg in zip((n - 2, n - 1), pages):
             assert torch.equal(kc[pg, :, p % 8], got[2][pg, :, p % 8])
     assert cuda_lib.device_error() == 0
+
+
+def test_quotients_half_way_and_far(cuda_lib):
+    """Values half way between two codes go to the even one; blocks beyond 2^100, where
+    the kernel divides, and blocks of tiny values give the formula's codes too."""
+    dev = torch.device("cuda")
+    g = torch.Generator().manual_seed(11)
+    T, D = 512, 128
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    # Blocks whose scale is m / 8 * 2^e and whose values are half-way points of it.
+    m = torch.randint(8, 16, (T, 1, D // 16, 1), generator=g) / 8
+    e = torch.randint(-6, 7, (T, 1, D // 16, 1), generator=g).float()
+    x = mids[torch.randint(0, 8, (T, 1, D // 16, 16), generator=g)]
+    x[..., 0] = 6.0
+    x = x * torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0) * m * 2.0 ** e
+    k = x.reshape(T, 1, D).bfloat16()
+    assert torch.equal(k.float(), x.reshape(T, 1, D))
+    v = torch.randn(T, 1, D, generator=g).bfloat16()
+    v[0::4] *= 2.0 ** 104
+    v[1::4] *= 2.0 ** -13
+    v[2::4] *= 2.0 ** -126
+    pages = T // 8
+    kc, vc = (torch.zeros(pages, 1, 8, 72, dtype=torch.uint8, device=dev) for _ in "kv")
+    one = torch.ones(1, device=dev)
+    table = torch.arange(pages, dtype=torch.int32, device=dev)[None].contiguous()
+    lens = torch.tensor([T], dtype=torch.int32, device=dev)
+    cuda_lib.cache_write_fp4(None, k.to(dev), v.to(dev), kc, vc, one, one, table, lens, T)
+    for cache, y in ((kc, k), (vc, v)):
+        want = ref.encode_rows(y.float().numpy()).reshape(cache.shape)
+        assert np.array_equal(cache.cpu().numpy(), want)
+    assert cuda_lib.device_error() == 0
+
+
+def test_read_into_odd_addresses(cuda_lib):
+    """Outputs 16 bytes past a 32-byte boundary: the same rows, and nothing beside them."""
+    dev = torch.device("cuda")
+    c = fp4_case(3, 3, 21, 60, 8, 2, 128)
+    tables, lens, starts = device_rows(c)
+    s = torch.tensor([0.37], device=dev)
+    caches = [x.to(dev) for x in c["caches"]]
+    args = (*caches, s, s, tables, lens, c["max_ctx"], c["tokens"])
+    zeros = [torch.full((c["tokens"], 2, 128), 7.0, dtype=torch.float16, device=dev) for _ in "kv"]
+    cuda_lib.cache_read_fp4(*args, row_starts=starts, k_out=zeros[0], v_out=zeros[1])
+    n = zeros[0].numel()
+    flat = [torch.full((n + 16,), 7.0, dtype=torch.float16, device=dev) for _ in "kv"]
+    for at in ((8, 8), (0, 8), (8, 0)):
+        outs = [f[a:a + n].view(zeros[0].shape) for f, a in zip(flat, at)]
+        cuda_lib.cache_read_fp4(*args, row_starts=starts, k_out=outs[0], v_out=outs[1])
+        for f, o, a, want in zip(flat, outs, at, zeros):
+            assert torch.equal(o, want)
+            assert (f[:a] == 7).all() and (f[a + n:] == 7).all()
+            f.fill_(7.0)
+    assert cuda_lib.device_error() == 0
