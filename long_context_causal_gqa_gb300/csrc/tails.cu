@@ -166,20 +166,22 @@ __device__ __forceinline__ void seqs_large(const Params& P, int* starts, int* to
     __syncthreads();
 }
 
-// G equal ranges over all tiles of all units (the first `more` one longer).
+// G equal ranges over all tiles of all units: range c begins at floor(c total / G).
 struct Ranges {
-    uint32_t each, more;
-    int G;
+    uint32_t each, more;   // total = each G + more
+    int G, total;
     __device__ Ranges(const Params& P, const Seqs& q) {
-        const int total = q.all * (P.hkv * P.groups);
+        total = q.all * (P.hkv * P.groups);
         G = min(P.G, total);
         each = G ? (uint32_t)total / (uint32_t)G : 0;
         more = total - each * G;
     }
-    __device__ int begin(int c) const { return c * each + min((uint32_t)c, more); }
-    __device__ int of(uint32_t pos) const {
-        const uint32_t front = more * (each + 1);
-        return pos < front ? pos / (each + 1) : more + (pos - front) / each;
+    __device__ int begin(int c) const { return c * each + c * more / (uint32_t)max(G, 1); }
+    __device__ int of(int pos) const {
+        int c = (int)((float)pos * ((float)G / (float)total));   // (or one beside it)
+        while (begin(c) > pos) --c;
+        while (begin(c + 1) <= pos) ++c;
+        return c;
     }
 };
 
@@ -194,18 +196,19 @@ struct Pieces {
     __device__ bool whole() const { return jb == 0 && je == n; }
     // Sets b, u, n, unit and s to the unit that holds position at.
     __device__ void find(const Params& P, const Seqs& q, int at) {
-        const int per = P.hkv * P.groups;
+        u = P.hkv * P.groups == 1 ? 0 : at / q.all;
+        const int in_u = at - u * q.all;
         int start, ctx;
         if (!q.starts) {
-            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start * per <= at));
+            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start <= in_u));
             start = __shfl_sync(0xffffffffu, q.start, b);
             n = __shfl_sync(0xffffffffu, q.tiles, b);
             ctx = __shfl_sync(0xffffffffu, q.ctx, b);
         } else {
-            int lo = 0, hi = P.batch;   // starts[lo] * per <= at < starts[hi] * per
+            int lo = 0, hi = P.batch;   // starts[lo] <= in_u < starts[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (q.starts[mid] * per <= at) lo = mid;
+                if (q.starts[mid] <= in_u) lo = mid;
                 else hi = mid;
             }
             b = lo;
@@ -214,8 +217,7 @@ struct Pieces {
             ctx = P.ctx_lens[b];
         }
         s = span_of(P, ctx);
-        u = per == 1 ? 0 : (at - start * per) / n;
-        unit = start * per + u * n;
+        unit = at - in_u + start;
         n -= LEAD;
     }
     // A boundary in or right behind a LEAD is the unit's beginning.
@@ -298,9 +300,9 @@ __device__ __forceinline__ Ranges begin_range(const Params& P, int* starts, int*
 
 // What has no tiles (one warp): rows of sequences without a key are zeros; no units of
 // theirs, and no cut unit for ranges that get no tiles.
-__device__ __forceinline__ void finish_empty(const Params& P, const Pieces& it, int dh) {
+__device__ __forceinline__ void finish_empty(const Params& P, bool idle, int dh) {
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
-    if (it.pos == it.end && !P.by_unit && lane == 0) P.tasks[cta] = make_int4(0, 0, 0, 0);
+    if (idle && !P.by_unit && lane == 0) P.tasks[cta] = make_int4(0, 0, 0, 0);
 #pragma unroll 1
     for (int b = cta; b < P.batch; b += gridDim.x) {
         const int raw = P.ctx_lens[b];
@@ -566,14 +568,30 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
 }
 
 // How a unit is joined, from the piece it begins with; a range whose last piece is no
-// cut unit's beginning has none to say.  (One thread.)
+// cut unit's beginning has none to say.
 __device__ __forceinline__ void write_task(const Params& P, const Pieces& it, const Ranges& ranges) {
     const int unit = it.b * (P.hkv * P.groups) + it.u, cta = blockIdx.x;
     const bool cut = it.jb == 0 && !it.whole();
-    if (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end))
+    if ((threadIdx.x & 31) == 0 && (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end)))
         P.tasks[P.by_unit ? unit : cta] =
             make_int4(unit, cta * 2 + (it.first ? 0 : 1),
                       cut ? ranges.of(it.unit + LEAD + it.n - 1) - cta + 1 : 0, 0);
+}
+
+// What the copy warps do: the first of them also what concerns the join.
+template <bool F8, int DH, int NG, int STAGES>
+__device__ __forceinline__ void bring(const Params& P, const Maps<F8>& maps, int* starts,
+                                      int* totals, uint32_t ring, uint32_t bars,
+                                      volatile int* abort_flag, int warp) {
+    Seqs seqs;
+    Pieces it;
+    const Ranges ranges = begin_range(P, starts, totals, it, seqs);
+    const int begin = it.pos;
+    copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, ring, bars, abort_flag, warp);
+    if (warp) return;
+    finish_empty(P, begin == it.end, DH);
+    it.pos = begin;
+    while (it.next(P, seqs, begin)) write_task(P, it, ranges);
 }
 
 // Position of packed row r of a KV head, and whether a row there sees a key.
@@ -677,19 +695,15 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
     const int cta = blockIdx.x;
 
     if (warp >= NW) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
-      Seqs seqs;
-      Pieces it;
-      begin_range(P, starts, totals, it, seqs);
-      if (warp == NW) finish_empty(P, it, DH);
-      copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, smem_u32(smem) + C::OFF_RING, bars,
-                                     abort_flag, warp - NW);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
+        bring<F8, DH, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
+                                  abort_flag, warp - NW);
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
         Seqs seqs;
         Pieces it;
-        const Ranges ranges = begin_range(P, starts, totals, it, seqs);
+        begin_range(P, starts, totals, it, seqs);
         const int begin = it.pos;
         const int group = warp / GW, gwarp = warp % GW;
         const int gid = lane >> 2, t = lane & 3;
@@ -709,7 +723,6 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         while (it.next(P, seqs, begin)) {
             const Span s = it.s;
             const int row0 = it.g * ROWS;
-            if (threadIdx.x == 0) write_task(P, it, ranges);
             // Q, all loads under way together.
             {
                 constexpr int EACH = (ROWS * DH / 8 + 32 * NW - 1) / (32 * NW);
@@ -747,7 +760,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
             const uint32_t n0 = n;   // the piece's first tile
             n += it.je - it.jb;
 #pragma unroll 1
-            for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
+            for (int j = it.jb + (int)((group + NG - n0 % NG) % NG); j < it.je; j += NG) {
                 const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
                 wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
@@ -1154,17 +1167,13 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
     __syncthreads();
     if (warp >= NW) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
-        Seqs seqs;
-        Pieces it;
-        begin_range(P, starts, totals, it, seqs);
-        if (warp == NW) finish_empty(P, it, DH);
-        copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, smem_u32(smem) + C::OFF_RING, bars,
-                                       abort_flag, warp - NW);
+        bring<F8, DH, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
+                                  abort_flag, warp - NW);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
         Seqs seqs;
         Pieces it;
-        const Ranges ranges = begin_range(P, starts, totals, it, seqs);
+        begin_range(P, starts, totals, it, seqs);
         const int begin = it.pos;
         const int group = warp / C::GW, gwarp = warp % C::GW;
         const int gid = lane >> 2, t = lane & 3;
@@ -1176,7 +1185,6 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         uint32_t n = 0;     // tiles of the CTA so far
         while (it.next(P, seqs, begin)) {
             const Span s = it.s;
-            if (threadIdx.x == 0) write_task(P, it, ranges);
             // The lane's places of row gid: the products' B operands.
             uint4 q[DH / 32];
             {
@@ -1198,7 +1206,7 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
             const uint32_t n0 = n;   // the piece's first tile
             n += it.je - it.jb;
 #pragma unroll 1
-            for (int j = it.jb + (int)((group - n0) % NG); j < it.je; j += NG) {
+            for (int j = it.jb + (int)((group + NG - n0 % NG) % NG); j < it.je; j += NG) {
                 const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
                 const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
                 wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
