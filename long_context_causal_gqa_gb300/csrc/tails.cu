@@ -472,14 +472,26 @@ struct Maps<false> {};
 // (n % NG) STAGES + i % STAGES of NG STAGES "full" and as many "empty" ones: a group's
 // own, so that it sees each of their phases (with a barrier for each stage a group would
 // skip the others' phases, and could not tell one it waits for from the one before).
+//
+// Counted on from tile to tile: the remainders' instructions were most of a copying
+// warp's time for a tile (740 cycles without any copy; @@).
 template <int NG, int STAGES>
-__device__ __forceinline__ uint32_t tile_bar(uint32_t n) {
-    return 8 * ((n % NG) * STAGES + n / NG % STAGES);
-}
-template <int NG, int STAGES>
-__device__ __forceinline__ uint32_t tile_phase(uint32_t n) {
-    return n / NG / STAGES & 1;
-}
+struct Turn {
+    uint32_t stage = 0, group = 0, slot = 0, phase = 0;
+    __device__ __forceinline__ uint32_t bar() const { return 8 * (group * STAGES + slot); }
+    __device__ __forceinline__ void next() {
+        if (++stage == STAGES) stage = 0;
+        if (++group == NG) {
+            group = 0;
+            if (++slot == STAGES) slot = 0, phase ^= 1;
+        }
+    }
+    // The group's next.
+    __device__ __forceinline__ void next_own() {
+        stage = stage + NG < STAGES ? stage + NG : stage + NG - STAGES;
+        if (++slot == STAGES) slot = 0, phase ^= 1;
+    }
+};
 
 // The copies (COPY_WARPS warps): the pages of each tile into the ring.  A bulk copy is an instruction of one lane at a
 // time, about 70 cycles each: the 16 copies of a tile of 16-token pages are shared out
@@ -502,7 +514,8 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
     const uint32_t to =
         ring + kv * W::TILE_BYTES + half * (W::TILE_BYTES / HALVES) + p * rows * BYTES;
     const int begin = it.pos;
-    uint32_t n = 0;   // tiles so far
+    Turn<NG, STAGES> at, old;   // the next tile, the oldest in the ring
+    uint32_t room = STAGES;     // stages that held none yet
     bool ok = true;
     while (ok && it.next(P, seqs, begin)) {
         const int pages = (it.s.ctx + P.page - 1) >> P.log2_page;
@@ -524,45 +537,48 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
                 next = after;
                 after = entries(lot + 2);
             }
+            // All that can be known before a stage is free.
             int id = __shfl_sync(0xffffffffu, now, (e & 31) + (p & (ppt - 1)));
-            const int key0 = tile_key(P, it.s, j);
-            const int copies = min(ppt, pages - (key0 >> P.log2_page));
-            if (p < copies && (id < 0 || id >= P.num_pages)) {
+            const int key0 = tile_key(P, it.s, j), in_page = key0 & (P.page - 1);
+            const bool mine = p < min(ppt, pages - (key0 >> P.log2_page));
+            if (mine && (id < 0 || id >= P.num_pages)) {
                 atomicOr(P.err, kErrBadPageId);
                 id = 0;
             }
-            const uint32_t mine = __popc(__ballot_sync(0xffffffffu, p < copies));
-            const uint32_t full = bars + tile_bar<NG, STAGES>(n);
-            int okw = 1;
-            if (lane == 0) {
-                if (n >= STAGES)
-                    okw = wait(bars + 8 * NG * STAGES + tile_bar<NG, STAGES>(n - STAGES),
-                               tile_phase<NG, STAGES>(n - STAGES), abort_flag, P.err);
-                if (okw) mbar_arrive_expect_tx(full, mine * rows * BYTES);
+            const uint32_t bytes =
+                __popc(__ballot_sync(0xffffffffu, mine)) * (rows * BYTES);
+            const uint8_t* src = nullptr;
+            if constexpr (!F8)
+                src = (kv ? P.cache[1] : P.cache[0]) +
+                      (((long long)id * P.hkv + it.h) * P.page + in_page) * BYTES;
+            const uint32_t full = bars + at.bar(), dst = to + at.stage * (2 * W::TILE_BYTES);
+            if (room) {
+                --room;
+            } else {
+                ok = wait(bars + 8 * NG * STAGES + old.bar(), old.phase, abort_flag, P.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                old.next();
             }
-            ok = __shfl_sync(0xffffffffu, okw, 0);
-            if (!ok) break;
-            if (p < copies) {
-                const uint32_t dst = to + n % STAGES * (2 * W::TILE_BYTES);
-                if constexpr (F8) {
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+            if (mine) {
+                if constexpr (F8)
                     tma_load_2d(dst, &maps.kv[kv], full, it.h * DH + half * 128,
-                                id * P.page + (key0 & (P.page - 1)));
-                } else {
-                    const long long row =
-                        ((long long)id * P.hkv + it.h) * P.page + (key0 & (P.page - 1));
-                    bulk_load(dst, (kv ? P.cache[1] : P.cache[0]) + row * BYTES, rows * BYTES, full);
-                }
+                                id * P.page + in_page);
+                else
+                    bulk_load(dst, src, rows * BYTES, full);
             }
-            ++n;
+            at.next();
         }
     }
     if (!ok && lane == 0) {
         // Unwind: every copy in flight lands before the CTA exits.
 #pragma unroll 1
-        for (uint32_t m = n > STAGES ? n - STAGES : 0; m < n; ++m) {
+        for (int i = 0; i < STAGES; ++i) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bars + tile_bar<NG, STAGES>(m), tile_phase<NG, STAGES>(m)))
+            while (!mbar_try_wait(bars + old.bar(), old.phase))
                 if (global_timer_ns() - t0 > 100000000ull) break;
+            old.next();
         }
     }
 }
@@ -719,6 +735,8 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
         const float vscale = *P.scale_dev[1];
         uint32_t n = 0;     // tiles of the CTA so far
+        Turn<NG, STAGES> at;
+        at.stage = at.group = group;
         uint32_t mine = 0;  // tiles of the group so far
         while (it.next(P, seqs, begin)) {
             const Span s = it.s;
@@ -761,13 +779,12 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
             n += it.je - it.jb;
 #pragma unroll 1
             for (int j = it.jb + (int)((group + NG - n0 % NG) % NG); j < it.je; j += NG) {
-                const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
-                const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
-                wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
+                const uint32_t full = bars + at.bar();
+                wait(full, at.phase, abort_flag, P.err);
                 __syncwarp();
                 const int key0 = tile_key(P, s, j);
                 const bool edge = has_edge(P, s, key0, TILE);
-                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
+                const uint8_t* kst = smem + C::OFF_RING + at.stage * C::STAGE;
                 const uint8_t* vst = kst + W::TILE_BYTES;
                 // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
                 float sc[KZ][NT][4];
@@ -1016,6 +1033,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
+                at.next_own();
                 ++mine;
             }
 
@@ -1183,6 +1201,8 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         const float sl2 = P.scale * *P.scale_dev[0] * 1.4426950408889634f;
         const float vscale = *P.scale_dev[1];
         uint32_t n = 0;     // tiles of the CTA so far
+        Turn<NG, STAGES> at;
+        at.stage = at.group = group;
         while (it.next(P, seqs, begin)) {
             const Span s = it.s;
             // The lane's places of row gid: the products' B operands.
@@ -1207,13 +1227,12 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
             n += it.je - it.jb;
 #pragma unroll 1
             for (int j = it.jb + (int)((group + NG - n0 % NG) % NG); j < it.je; j += NG) {
-                const uint32_t tile = n0 + (j - it.jb), st = tile % STAGES;
-                const uint32_t full = bars + tile_bar<NG, STAGES>(tile);
-                wait(full, tile_phase<NG, STAGES>(tile), abort_flag, P.err);
+                const uint32_t full = bars + at.bar();
+                wait(full, at.phase, abort_flag, P.err);
                 __syncwarp();
                 const int w0 = gwarp * 16 * KZ;   // the warp's first key of the tile
                 const int k0 = tile_key(P, s, j) + w0;
-                const uint8_t* kst = smem + C::OFF_RING + st * C::STAGE;
+                const uint8_t* kst = smem + C::OFF_RING + at.stage * C::STAGE;
                 const uint8_t* vst = kst + W::TILE_BYTES;
                 const bool edge = has_edge(P, s, k0, 16 * KZ);
                 // ---- scores of keys key_of(gid) and key_of(gid + 8) of each sixteen
@@ -1425,6 +1444,7 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + 8 * NG * STAGES);
+                at.next_own();
             }
 
             // ---------------------------------------------------------- end of the piece
@@ -1508,15 +1528,13 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 }
 
 // Joins the partials of the units that lie in several ranges.  A block of 16 warps
-// takes 128 places of D of one packed row where there are few units, of two rows where
-// there are many (most then have two or three pieces); a row's warps share its pieces
-// out and their sums are added in order.
+// takes 128 places of D of 16 / WPR packed rows; a row's WPR warps share its pieces out
+// and their sums are added in order.
 constexpr int MERGE_WARPS = 16;
-constexpr int MAX_RANGES = 256;   // 32 pieces a warp where eight share a row
 
-template <int DH, int NT, int WPR>   // WPR: warps of a row
-__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P) {
-    constexpr int ROWS = 8 * NT;
+template <int WPR>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P, int unit_rows,
+                                                                 int dh) {
     __shared__ float4 part[MERGE_WARPS][32];
     __shared__ float2 top[MERGE_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1529,46 +1547,57 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P)
     const int per = P.hkv * P.groups;
     const int b = task.x / per, u = task.x - b * per;
     const int h = u / P.groups, g = u - h * P.groups;
-    const bool there = r < ROWS && g * ROWS + r < P.nq;
+    const bool there = r < unit_rows && g * unit_rows + r < P.nq;
     const int d0 = blockIdx.z * 128 + lane * 4;
     const float vscale = *P.scale_dev[1];
     auto row_of = [&](int i) {
-        return (i == 0 ? (long long)task.y : (long long)(task.y / 2 + i) * 2) * ROWS + r;
+        return (i == 0 ? (long long)task.y : (long long)(task.y / 2 + i) * 2) * unit_rows + r;
     };
-    // The warp's pieces w, w + WPR, ...: references and sums, a lane each, and the first O
-    // in flight beside them.
-    constexpr int AHEAD = WPR == MERGE_WARPS ? 10 : 3;
-    const int mine = there && pieces > w ? (pieces - w + WPR - 1) / WPR : 0;
     const float* from = P.ws_o + d0;
-    float4 o[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (i < mine)
-            o[i] = __ldcg(reinterpret_cast<const float4*>(from + row_of(w + i * WPR) * DH));
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < mine) ml = __ldcg(reinterpret_cast<const float2*>(P.ws_ml + row_of(w + lane * WPR) * 2));
-    float m = ml.x;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    // Sums in units of the warp's own largest reference.
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-    float sum = f * ml.y;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int i, const float4& v) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        acc.x = fmaf(fi, v.x, acc.x);
-        acc.y = fmaf(fi, v.y, acc.y);
-        acc.z = fmaf(fi, v.z, acc.z);
-        acc.w = fmaf(fi, v.w, acc.w);
+    auto load = [&](int i) {
+        return __ldcg(reinterpret_cast<const float4*>(from + row_of(w + i * WPR) * dh));
     };
+    // The warp's pieces w, w + WPR, ..., 32 at a time: references and sums, a lane each, and
+    // the first O in flight beside them.
+    constexpr int AHEAD = WPR == MERGE_WARPS ? 10 : 4;
+    const int mine = there && pieces > w ? (pieces - w + WPR - 1) / WPR : 0;
+    float m = -INFINITY, sum = 0.f;   // of the pieces so far, in units of the largest reference
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int n = min(mine - i0, 32);
+        float4 o[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (i < mine) add(i, o[i]);
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < n) o[i] = load(i0 + i);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n)
+            ml = __ldcg(
+                reinterpret_cast<const float2*>(P.ws_ml + row_of(w + (i0 + lane) * WPR) * 2));
+        float mx = fmaxf(ml.x, m);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+        const float keep = m == -INFINITY ? 0.f : ex2(m - mx);
+        float part_sum = f * ml.y;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, x);
+        m = mx;
+        sum = fmaf(keep, sum, part_sum);
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+        auto add = [&](int i, const float4& v) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            acc.x = fmaf(fi, v.x, acc.x);
+            acc.y = fmaf(fi, v.y, acc.y);
+            acc.z = fmaf(fi, v.z, acc.z);
+            acc.w = fmaf(fi, v.w, acc.w);
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < n) add(i, o[i]);
 #pragma unroll 4
-    for (int i = AHEAD; i < mine; ++i)
-        add(i, __ldcg(reinterpret_cast<const float4*>(from + row_of(w + i * WPR) * DH)));
+        for (int i = AHEAD; i < n; ++i) add(i, load(i0 + i));
+    }
     part[warp][lane] = acc;
     if (lane == 0) top[warp] = make_float2(m, sum);
     __syncthreads();
@@ -1593,7 +1622,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P)
     uint2 v;
     v.x = pack_half2(acc.x * inv, acc.y * inv);
     v.y = pack_half2(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * ROWS + r, DH) + d0) = v;
+    *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * unit_rows + r, dh) + d0) = v;
 }
 
 template <bool F8, int DH, int NT>
@@ -1618,18 +1647,16 @@ int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, maps, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
-    const int rows = P.nq < 8 * NT ? P.nq : 8 * NT;
+    // A row's warps, by how many pieces a unit has.
+    const int units = P.batch * P.hkv * P.groups;
+    const int wpr = P.G >= 16 * units ? 16 : P.G >= 4 * units ? 4 : 2;
+    void (*const merge)(Params, int, int) =
+        wpr == 16 ? merge_kernel<16> : wpr == 4 ? merge_kernel<4> : merge_kernel<2>;
+    const int rows = P.nq < 8 * NT ? P.nq : 8 * NT, a_block = MERGE_WARPS / wpr;
+    cfg.gridDim = dim3(P.by_unit ? units : P.G, (rows + a_block - 1) / a_block, DH / 128);
     cfg.blockDim = dim3(MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
-    cudaError_t e;
-    if (P.by_unit) {
-        cfg.gridDim = dim3(P.batch * P.hkv * P.groups, rows, DH / 128);
-        e = cudaLaunchKernelEx(&cfg, merge_kernel<DH, NT, MERGE_WARPS>, P);
-    } else {
-        cfg.gridDim = dim3(P.G, (rows + 1) / 2, DH / 128);
-        e = cudaLaunchKernelEx(&cfg, merge_kernel<DH, NT, MERGE_WARPS / 2>, P);
-    }
-    return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, merge, P, 8 * NT, DH) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 // Packed rows of a unit: all of a KV head's.
@@ -1685,7 +1712,6 @@ int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, co
     const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len - 1) / tile + 1);
     if (tiles > 0x1fffffffLL) return GQA_ERR_UNSUPPORTED;   // (with their LEADs below 2^31)
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
-    if (P.G > MAX_RANGES) P.G = MAX_RANGES;
     P.by_unit = (long long)batch * Hkv * P.groups < P.G;
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
