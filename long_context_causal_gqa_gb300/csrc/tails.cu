@@ -349,13 +349,20 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
 //     go; q_place(t, x, i): which they are.
 //   pairs(a, b, lo, hi): eight places of two keys as (key a, key b) pairs, the even ones
 //     and the odd ones.
+//
+// A tile's keys: 128 (E4M3 rows of 256: 64, stages of 32 KB); from four eights of packed
+// rows on 64, whose scores take half the registers (@@).
 template <bool F8, int DH>
+__host__ __device__ constexpr int tile_keys(int nt) {
+    return (F8 && DH == 256) || nt >= 4 ? 64 : 128;
+}
+template <bool F8, int DH, int KEYS>
 struct Rows;
 
 // 4-bit rows (fp4_rows.cuh), as they are in memory.
-template <int DH>
-struct Rows<false, DH> {
-    static constexpr int TILE = 128;
+template <int DH, int KEYS>
+struct Rows<false, DH, KEYS> {
+    static constexpr int TILE = KEYS;
     static constexpr int TILE_BYTES = TILE * fp4::row_bytes(DH);   // of K, or of V
     static constexpr int ROWB = fp4::row_bytes(DH);
     static constexpr int LOADS = 2, GROUPS = DH / 64;
@@ -414,9 +421,9 @@ struct Rows<false, DH> {
 
 // E4M3 rows, in halves of 128 bytes with the 128-byte swizzle: unit u (16 bytes) of row r
 // at (u ^ r % 8) * 16.
-template <int DH>
-struct Rows<true, DH> {
-    static constexpr int TILE = DH == 256 ? 64 : 128;   // (stages of 32 KB)
+template <int DH, int KEYS>
+struct Rows<true, DH, KEYS> {
+    static constexpr int TILE = KEYS;
     static constexpr int HALF_BYTES = TILE * 128, TILE_BYTES = TILE * DH;
     static constexpr int LOADS = DH / 64, GROUPS = 2;
     // (a lane's 64 bytes of each half padded by 16, a row by 64)
@@ -499,11 +506,10 @@ struct Turn {
 // tile's time at the memory's rate; 62 us for 64 sequences of up to 8192 tokens).
 constexpr int COPY_WARPS = 4;
 
-template <bool F8, int DH, int NG, int STAGES>
+template <bool F8, int DH, typename W, int NG, int STAGES>
 __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps, Pieces& it,
                                            const Seqs& seqs, uint32_t ring, uint32_t bars,
                                            volatile int* abort_flag, int warp) {
-    using W = Rows<F8, DH>;
     constexpr int HALVES = F8 ? DH / 128 : 1;     // copies of a page's rows of K (or V)
     constexpr int BYTES = W::TILE_BYTES / W::TILE / HALVES;   // of a row in one copy
     const int lane = threadIdx.x & 31;
@@ -595,7 +601,7 @@ __device__ __forceinline__ void write_task(const Params& P, const Pieces& it, co
 }
 
 // What the copy warps do: the first of them also what concerns the join.
-template <bool F8, int DH, int NG, int STAGES>
+template <bool F8, int DH, typename W, int NG, int STAGES>
 __device__ __forceinline__ void bring(const Params& P, const Maps<F8>& maps, int* starts,
                                       int* totals, uint32_t ring, uint32_t bars,
                                       volatile int* abort_flag, int warp) {
@@ -603,7 +609,7 @@ __device__ __forceinline__ void bring(const Params& P, const Maps<F8>& maps, int
     Pieces it;
     const Ranges ranges = begin_range(P, starts, totals, it, seqs);
     const int begin = it.pos;
-    copy_tiles<F8, DH, NG, STAGES>(P, maps, it, seqs, ring, bars, abort_flag, warp);
+    copy_tiles<F8, DH, W, NG, STAGES>(P, maps, it, seqs, ring, bars, abort_flag, warp);
     if (warp) return;
     finish_empty(P, begin == it.end, DH);
     it.pos = begin;
@@ -629,7 +635,7 @@ __device__ __forceinline__ bool unseen(const Params& P, const Span& s, int key) 
 // F8: the cache is E4M3, else 4-bit; DH: head size; NT: eights of packed rows.
 template <bool F8, int DH, int NT>
 struct Config {
-    using W = Rows<F8, DH>;
+    using W = Rows<F8, DH, tile_keys<F8, DH>(NT)>;
     static constexpr int TILE = W::TILE;
     // Two groups of four warps, each group on a tile of its own, so that one's products go
     // on while the other's warps meet, each warp with 32 keys (16 of a tile of 64).
@@ -686,7 +692,7 @@ template <bool F8, int DH, int NT>
 __global__ void __launch_bounds__(Config<F8, DH, NT>::THREADS, 1)
 split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
     using C = Config<F8, DH, NT>;
-    using W = Rows<F8, DH>;
+    using W = typename C::W;
     constexpr int TILE = C::TILE;
     constexpr int ROWS = C::ROWS, STAGES = C::STAGES, NG = C::NG, NW = C::NW;
     constexpr int GW = C::GW, KZ = C::KZ;
@@ -712,7 +718,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 
     if (warp >= NW) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
-        bring<F8, DH, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
+        bring<F8, DH, W, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
                                   abort_flag, warp - NW);
     } else {
         // ------------------------------------------------------------ products
@@ -1136,7 +1142,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 // a tile; more rows' sums of all of D do not fit a warp's registers.)
 template <bool F8, int DH>
 struct Narrow {
-    using W = Rows<F8, DH>;
+    using W = Rows<F8, DH, tile_keys<F8, DH>(1)>;
     static constexpr int NG = 2;                     // tiles under way
     static constexpr int GW = 4;                     // warps of a tile
     static constexpr int KZ = W::TILE / 16 / GW;     // sixteens of keys of a warp
@@ -1164,7 +1170,7 @@ template <bool F8, int DH>
 __global__ void __launch_bounds__(Narrow<F8, DH>::THREADS, 1)
 narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
     using C = Narrow<F8, DH>;
-    using W = Rows<F8, DH>;
+    using W = typename C::W;
     constexpr int STAGES = C::STAGES, NG = C::NG, NW = C::NW;
     constexpr int MT = DH / 16, KZ = C::KZ;
     extern __shared__ uint8_t smem_raw[];
@@ -1185,7 +1191,7 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
     __syncthreads();
     if (warp >= NW) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPIES));
-        bring<F8, DH, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
+        bring<F8, DH, W, NG, STAGES>(P, maps, starts, totals, smem_u32(smem) + C::OFF_RING, bars,
                                   abort_flag, warp - NW);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_PRODUCTS));
@@ -1693,8 +1699,6 @@ int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, co
     P.num_pages = num_pages;
     P.page = page;
     P.log2_page = __builtin_ctz((unsigned)page);
-    const int tile = Dh == 256 ? Rows<F8, 256>::TILE : Rows<F8, 128>::TILE;
-    P.ltile = __builtin_ctz((unsigned)tile);
     P.max_ctx = max_ctx_len;
     P.batch = batch;
     P.R = R;
@@ -1703,6 +1707,8 @@ int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, co
     P.grp = make_fastdiv(Hq / Hkv);
     P.nq = R * (Hq / Hkv);
     const int rows = unit_rows(P.nq);
+    const int tile = Dh == 256 ? tile_keys<F8, 256>(rows / 8) : tile_keys<F8, 128>(rows / 8);
+    P.ltile = __builtin_ctz((unsigned)tile);
     P.groups = (P.nq + rows - 1) / rows;
     // A window that holds every context hides nothing.
     P.window = window >= max_ctx_len ? 0 : window;
