@@ -560,7 +560,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     asm volatile("griddepcontrol.launch_dependents;");
 
     // A windowed call is short beside its own launch, which overlaps the kernel in front
-    // (152 -> 148 us): nothing of global memory is read or written before that is done.
+    // (8000 rows of 40000, window 4096: 152 -> 148 us when it was added): nothing of global
+    // memory is read or written before that is done.
     if constexpr (WIN) asm volatile("griddepcontrol.wait;" ::: "memory");
     SegIter<MH, WIN> it;
     it.init(P, tm_sink, pair);

@@ -1,34 +1,48 @@
-// paged_fp4.cu -- causal GQA tails over a 4-bit paged cache (rows as in
-// fp4_rows.cuh), for a batch of sequences, with a sliding window and first tokens
-// that stay visible ("sinks").
+// tails.cu -- causal GQA tails of a batch over a 4-bit paged cache (rows as in
+// fp4_rows.cuh) or an E4M3 one, with a sliding window and first tokens that stay
+// visible ("sinks").
 //
 //   out = softmax_j(scale * q . k_j) v_j over the keys j of the sequence with
 //   j <= p and (no window, or j > p - window, or j < sinks), p the row's position.
 //
-// One pass over the visible tiles of 128 keys, with a running maximum and sum.
+// One pass over the visible tiles of 128 or 64 keys, with a running maximum and sum.
 //
-// * Work split.  The visible tiles of all (sequence, KV head, group of up to
-//   8 NT packed rows) units, one behind the other, are cut into one equal
-//   contiguous range per CTA, from the context lengths on the device.  A unit that
-//   lies in one range is finished there; a unit that is cut leaves (O, m, l)
-//   partials, at most two for a CTA, which a second kernel joins in range order.
-// * Copies.  One warp brings the pages of a tile (a page of one head is one
-//   contiguous run) into a ring of stages by bulk copies, table entries two tiles
-//   ahead.
-// * Products.  Groups of eight warps take a tile each, a warp 16 keys of it for the
-//   scores and a share of D and of the keys for the values, with P going through
-//   shared memory in between.  A warp decodes its codes from shared memory straight
-//   into the fragments of m16n8k16 products, keys (for K) or places of D (for V)
-//   along M, packed query rows along N, so eight rows waste nothing.  The order of the
-//   places within a product is free, so a lane loads whole words of one key: K's pairs
-//   are a byte's two nibbles, V's pairs are put together from two keys' nibbles.
+// * Work split.  The visible tiles of all (KV head, group of up to 48 packed rows,
+//   sequence) units, one behind the other in this order, are cut into one equal
+//   contiguous range per CTA, from the context lengths on the device.  (Sequences
+//   innermost: ranges of two heads then go over the same pages side by side, and what one
+//   reads beside its own 128 bytes of an E4M3 row the other finds in L2: 54 us instead of
+//   61 for 48 windows of 8192 tokens, two heads of 128.)  A unit that lies in one range is
+//   finished there; a unit that is cut leaves (O, m, l) partials, at most two for a CTA,
+//   which a second kernel joins in range order.
+// * Copies.  Four warps bring the pages of a tile into a ring of stages (192 KB: the bytes
+//   in flight set the copy rate), 4-bit pages by bulk copies (a page of one head is one
+//   contiguous run), E4M3 rows by tensor maps, table entries lots ahead.
+// * Products.  Two groups of four warps take a tile each.  A warp decodes its codes from
+//   shared memory straight into the fragments of m16n8k16 products, keys (for K) or
+//   places of D (for V) along M, packed query rows along N, so eight rows waste nothing.
+//   The order of the places within a product is free, so a lane loads whole words of one
+//   key: K's pairs are a byte's two nibbles, V's pairs are put together from two keys'.
 //   Nothing decoded goes through shared memory, which operands of tcgen05.mma would
 //   have to (four times the codes' bytes, written and read: more than shared memory can
 //   move while the codes arrive).
-// * Softmax.  A group's reference of a row moves only when a score passes it by more
-//   than 8 (log2 units), so P <= 256 in fp16.  A tile's P is computed with the
-//   reference as it stands, and only where some warp's scores passed it (flagged at the
-//   one barrier of a tile) is it moved, and P computed again.
+// * Softmax.  A reference of a row moves only when a score passes it by more than 8 (log2
+//   units), so P <= 256 in fp16.  More than eight packed rows: P goes through shared
+//   memory to the warps that hold the sums, computed with the group's reference as it
+//   stands, and only where some warp's scores passed it (flagged at the one barrier of a
+//   tile) is it moved, and P computed again.  Up to eight: a warp keeps all for itself.
+//
+// Replays behind one another, with the bytes that have to be read at the copy rate and a
+// plain reading kernel's time where it was measured: one row over 261888 4-bit tokens
+// 23.7 us (11.3; 18.1 by one call of the reading kernel against 26.8), 64 ragged contexts
+// of up to 8192 47 us (26.5; 34 against 54), eight rows over 128000 31 us (5.6), sixteen
+// windows of 2000 12.2 us (1.3), 48 E4M3 windows of 8192 44 us (29; 38.5 against 49).
+// Small calls are chains of latencies: lengths, table, first page, then the join's
+// record and partials (a window of 4096: 7.8 us, 7.2 of it without any product).  One
+// context's 64 x 1 tails are bound by decoding (49 us without the copies, 36 without the
+// products), windows of E4M3 rows by the copies (40 us without the products), eight
+// packed tails by the products (m16n8k16 takes 8.75 cycles of a quarter of an SM: under a
+// third of tcgen05's rate).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -99,7 +113,8 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
 // units and their LEADs are fewer than 2^31: the host sees to it.)
 //
 // Ranges are equal in tiles and what a piece costs besides: LEAD tiles' time in front of
-// each unit's.  (Sixteen windows of 17 tiles: 22 us without, see below.)
+// each unit's.  (Sixteen windows of 17 tiles: 16.4 us without, 12.2 with one or two, 13.1
+// with four; 64 contexts of up to 64 tiles 48.5, 47.6 with one, 47.1, 46.6 with four.)
 constexpr int LANES = 32;
 constexpr int LEAD = 2;
 struct Seqs {
@@ -351,7 +366,10 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
 //     and the odd ones.
 //
 // A tile's keys: 128 (E4M3 rows of 256: 64, stages of 32 KB); from four eights of packed
-// rows on 64, whose scores take half the registers (@@).
+// rows on 64, whose scores take half the registers.  (4-bit, heads of 256, 128 and 64
+// keys: eight rows of six heads over 128000 37.8 us and 31.2, five rows over 200000 34.0
+// and 31.9, four rows 28.3 and 28.6, sixteen windows of two 12.3 and 12.9; heads of 128,
+// sixteen contexts of four rows of four heads 34 and 39.)
 template <bool F8, int DH>
 __host__ __device__ constexpr int tile_keys(int nt) {
     return (F8 && DH == 256) || nt >= 4 ? 64 : 128;
@@ -481,7 +499,7 @@ struct Maps<false> {};
 // skip the others' phases, and could not tell one it waits for from the one before).
 //
 // Counted on from tile to tile: the remainders' instructions were most of a copying
-// warp's time for a tile (740 cycles without any copy; @@).
+// warp's time for a tile (sixteen contexts of four rows, heads of 128: 36 us, 34 so).
 template <int NG, int STAGES>
 struct Turn {
     uint32_t stage = 0, group = 0, slot = 0, phase = 0;
@@ -500,10 +518,11 @@ struct Turn {
     }
 };
 
-// The copies (COPY_WARPS warps): the pages of each tile into the ring.  A bulk copy is an instruction of one lane at a
-// time, about 70 cycles each: the 16 copies of a tile of 16-token pages are shared out
-// among four warps (one warp's took 1100 cycles a tile of head size 128, more than the
-// tile's time at the memory's rate; 62 us for 64 sequences of up to 8192 tokens).
+// The copies (COPY_WARPS warps): the pages of each tile into the ring.  A copy is an
+// instruction of one lane at a time, about 70 cycles each: the 16 copies of a tile of
+// 16-token pages are shared out among four warps (one warp's took 1100 cycles a tile of
+// head size 128, more than the tile's time at the memory's rate; 62 us instead of 50 for
+// 64 contexts of up to 8192 tokens).
 constexpr int COPY_WARPS = 4;
 
 template <bool F8, int DH, typename W, int NG, int STAGES>
@@ -1139,7 +1158,8 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 
 // Up to eight packed rows: every warp by itself, 32 keys of a tile, all of D, with its own
 // references, until the end of a piece.  (P never leaves the warp, and nothing meets in
-// a tile; more rows' sums of all of D do not fit a warp's registers.)
+// a tile; more rows' sums of all of D do not fit a warp's registers.  64 contexts of one
+// row, heads of 128: 47 us, 54 with the kernel above; one row over 261888 23.7 and 23.8.)
 template <bool F8, int DH>
 struct Narrow {
     using W = Rows<F8, DH, tile_keys<F8, DH>(1)>;
@@ -1535,7 +1555,9 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 
 // Joins the partials of the units that lie in several ranges.  A block of 16 warps
 // takes 128 places of D of 16 / WPR packed rows; a row's WPR warps share its pieces out
-// and their sums are added in order.
+// and their sums are added in order.  The whole calls with 16, 4 and 2 warps a row: one
+// unit in 152 pieces 23.7, 32.0 and 40.9 us; sixteen units in about ten each 15.5, 12.2
+// and 12.6; 96 units in two or three 60.4, 45.5 and 44.4.
 constexpr int MERGE_WARPS = 16;
 
 template <int WPR>
@@ -1633,7 +1655,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P,
 
 template <bool F8, int DH, int NT>
 int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
-    // (kernel and sizes of one eight of rows, or of more)
+    // (one eight of rows, or more)
     using C = typename std::conditional<NT == 1, Narrow<F8, DH>,
                                         Config<F8, DH, NT == 1 ? 2 : NT>>::type;
     void (*kernel)(Maps<F8>, Params);
