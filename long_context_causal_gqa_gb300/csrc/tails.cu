@@ -7,9 +7,9 @@
 //
 // One pass over the visible tiles of 128 or 64 keys, with a running maximum and sum.
 //
-// * Work split.  The visible tiles of all (KV head, group of up to 48 packed rows,
-//   sequence) units, one behind the other in this order, are cut into one equal
-//   contiguous range per CTA, from the context lengths on the device.  (Sequences
+// * Work split.  A KV head's rows of all query heads are packed, up to 48.  The visible
+//   tiles of all (KV head, sequence) units, one behind the other in this order, are cut
+//   into one equal contiguous range per CTA, from the context lengths on the device.  (Sequences
 //   innermost: ranges of two heads then go over the same pages side by side, and what one
 //   reads beside its own 128 bytes of an E4M3 row the other finds in L2: 54 us instead of
 //   61 for 48 windows of 8192 tokens, two heads of 128.)  A unit that lies in one range is
@@ -69,8 +69,7 @@ struct Params {
     int ltile;                   // log2 of the keys of a tile
     int R, hq, hkv;
     FastDiv grp;                 // query heads of one KV head
-    int nq;                      // packed rows of one KV head (R * grp)
-    int groups;                  // groups of 8 NT packed rows
+    int nq;                      // packed rows of one KV head (R * grp), at most 48
     int window, sinks;           // window 0: none
     float scale;
     int G;                       // ranges (CTAs)
@@ -186,7 +185,7 @@ struct Ranges {
     uint32_t each, more;   // total = each G + more
     int G, total;
     __device__ Ranges(const Params& P, const Seqs& q) {
-        total = q.all * (P.hkv * P.groups);
+        total = q.all * P.hkv;
         G = min(P.G, total);
         each = G ? (uint32_t)total / (uint32_t)G : 0;
         more = total - each * G;
@@ -203,27 +202,27 @@ struct Ranges {
 // Walks the pieces (unit, tiles [jb, je)) of one range.  (All lanes of a warp.)
 struct Pieces {
     int pos, end;     // LEADs counted
-    int b, u, h, g;   // sequence, unit within it, its KV head and group of packed rows
+    int b, h;         // sequence, KV head
     int jb, je, n;    // tiles of the piece, of the unit
     int unit;         // where the unit begins, its LEAD counted
     bool first;       // the range's first piece
     Span s;
     __device__ bool whole() const { return jb == 0 && je == n; }
-    // Sets b, u, n, unit and s to the unit that holds position at.
+    // Sets b, h, n, unit and s to the unit that holds position at.
     __device__ void find(const Params& P, const Seqs& q, int at) {
-        u = P.hkv * P.groups == 1 ? 0 : at / q.all;
-        const int in_u = at - u * q.all;
+        h = P.hkv == 1 ? 0 : at / q.all;
+        const int in_h = at - h * q.all;
         int start, ctx;
         if (!q.starts) {
-            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start <= in_u));
+            b = 31 - __clz(__ballot_sync(0xffffffffu, q.tiles > 0 && q.start <= in_h));
             start = __shfl_sync(0xffffffffu, q.start, b);
             n = __shfl_sync(0xffffffffu, q.tiles, b);
             ctx = __shfl_sync(0xffffffffu, q.ctx, b);
         } else {
-            int lo = 0, hi = P.batch;   // starts[lo] <= in_u < starts[hi]
+            int lo = 0, hi = P.batch;   // starts[lo] <= in_h < starts[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (q.starts[mid] <= in_u) lo = mid;
+                if (q.starts[mid] <= in_h) lo = mid;
                 else hi = mid;
             }
             b = lo;
@@ -232,7 +231,7 @@ struct Pieces {
             ctx = P.ctx_lens[b];
         }
         s = span_of(P, ctx);
-        unit = at - in_u + start;
+        unit = at - in_h + start;
         n -= LEAD;
     }
     // A boundary in or right behind a LEAD is the unit's beginning.
@@ -245,8 +244,6 @@ struct Pieces {
         if (pos >= end) return false;
         first = pos == begin;
         find(P, q, pos);
-        h = P.groups == 1 ? u : u / P.groups;
-        g = u - h * P.groups;
         jb = max(pos - unit - LEAD, 0);
         je = min(end - unit - LEAD, n);
         pos = je == n ? unit + LEAD + n : end;
@@ -306,7 +303,7 @@ __device__ __forceinline__ Ranges begin_range(const Params& P, int* starts, int*
     const Ranges ranges(P, seqs);
     it.pos = it.end = 0;
     if ((int)blockIdx.x < ranges.G) {
-        const int total = seqs.all * (P.hkv * P.groups);
+        const int total = seqs.all * P.hkv;
         it.pos = it.boundary(P, seqs, ranges.begin(blockIdx.x), total);
         it.end = it.boundary(P, seqs, ranges.begin(blockIdx.x + 1), total);
     }
@@ -328,8 +325,8 @@ __device__ __forceinline__ void finish_empty(const Params& P, bool idle, int dh)
         for (int i = lane; i < P.R * P.hq * dh / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         if (P.by_unit)
 #pragma unroll 1
-            for (int u = lane; u < P.hkv * P.groups; u += 32)
-                P.tasks[b * P.hkv * P.groups + u] = make_int4(0, 0, 0, 0);
+            for (int h = lane; h < P.hkv; h += 32)
+                P.tasks[b * P.hkv + h] = make_int4(0, 0, 0, 0);
     }
 }
 
@@ -611,7 +608,7 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
 // How a unit is joined, from the piece it begins with; a range whose last piece is no
 // cut unit's beginning has none to say.
 __device__ __forceinline__ void write_task(const Params& P, const Pieces& it, const Ranges& ranges) {
-    const int unit = it.b * (P.hkv * P.groups) + it.u, cta = blockIdx.x;
+    const int unit = it.b * P.hkv + it.h, cta = blockIdx.x;
     const bool cut = it.jb == 0 && !it.whole();
     if ((threadIdx.x & 31) == 0 && (cut || (P.by_unit ? it.jb == 0 : it.pos >= it.end)))
         P.tasks[P.by_unit ? unit : cta] =
@@ -765,7 +762,6 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         uint32_t mine = 0;  // tiles of the group so far
         while (it.next(P, seqs, begin)) {
             const Span s = it.s;
-            const int row0 = it.g * ROWS;
             // Q, all loads under way together.
             {
                 constexpr int EACH = (ROWS * DH / 8 + 32 * NW - 1) / (32 * NW);
@@ -773,9 +769,9 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 #pragma unroll
                 for (int x = 0; x < EACH; ++x) {
                     const int i = threadIdx.x + x * 32 * NW, r = i / (DH / 8), c = i % (DH / 8);
-                    v[x] = r < ROWS && row0 + r < P.nq
+                    v[x] = r < P.nq
                                ? *reinterpret_cast<const uint4*>(
-                                     P.q + row_offset(P, it.b, it.h, row0 + r, DH) + c * 8)
+                                     P.q + row_offset(P, it.b, it.h, r, DH) + c * 8)
                                : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
@@ -851,7 +847,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (!sees(P, row_pos(P, s, row0 + nt * 8 + 2 * t + (e & 1)),
+                                if (!sees(P, row_pos(P, s, nt * 8 + 2 * t + (e & 1)),
                                           key0 + (gwarp * KZ + z) * 16 +
                                               W::key_of(gid + (e & 2) * 4)))
                                     sc[z][nt][e] = -INFINITY;
@@ -1046,7 +1042,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                             continue;
 #pragma unroll
                         for (int r = 0; r < 2 * NT; ++r)
-                            if (sees(P, row_pos(P, s, row0 + (r >> 1) * 8 + 2 * t + (r & 1)), key))
+                            if (sees(P, row_pos(P, s, (r >> 1) * 8 + 2 * t + (r & 1)), key))
                                 poison |= 1u << r;
                     }
 #pragma unroll
@@ -1094,7 +1090,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                     for (int x = 0; x < GW; ++x) lg += smax[(g * GW + x) * ROWS + row];
                     sum = fmaf(f[g], lg, sum);
                 }
-                if (!whole && row0 + row < P.nq)
+                if (!whole && row < P.nq)
                     *reinterpret_cast<float2*>(P.ws_ml + ((long long)slot * ROWS + row) * 2) =
                         make_float2(M, sum);
                 // (a NaN sum is a NaN row, a sum of zero a row that sees nothing)
@@ -1118,7 +1114,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 #pragma unroll 1
                 for (int i = threadIdx.x; i < ROWS * DH / 8; i += 32 * NW) {
                     const int row = i / (DH / 8), at = i % (DH / 8);   // at: slice, gid
-                    if (row0 + row >= P.nq) break;
+                    if (row >= P.nq) break;
                     float2 a = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
@@ -1137,7 +1133,7 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                     const int d = at * 8 + r * 2;
                     if (whole)
                         *reinterpret_cast<uint32_t*>(
-                            P.out + row_offset(P, it.b, it.h, row0 + row, DH) + d) =
+                            P.out + row_offset(P, it.b, it.h, row, DH) + d) =
                             pack_half2(a.x, a.y);
                     else
                         *reinterpret_cast<float2*>(
@@ -1572,10 +1568,13 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P,
     const int4 task = __ldcg(P.tasks + blockIdx.x);
     const int pieces = task.z;
     if (pieces == 0) return;
-    const int per = P.hkv * P.groups;
-    const int b = task.x / per, u = task.x - b * per;
-    const int h = u / P.groups, g = u - h * P.groups;
-    const bool there = r < unit_rows && g * unit_rows + r < P.nq;
+    // (calls that overlap on one workspace spoil each other's records: nothing is read or
+    // written outside of what is this call's)
+    if (pieces < 0 || (unsigned)task.x >= (unsigned)(P.batch * P.hkv) || task.y < 0 ||
+        task.y / 2 + (long long)pieces > P.G)
+        return;
+    const int b = task.x / P.hkv, h = task.x - b * P.hkv;
+    const bool there = r < P.nq;
     const int d0 = blockIdx.z * 128 + lane * 4;
     const float vscale = *P.scale_dev[1];
     auto row_of = [&](int i) {
@@ -1650,7 +1649,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_kernel(const Params P,
     uint2 v;
     v.x = pack_half2(acc.x * inv, acc.y * inv);
     v.y = pack_half2(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, g * unit_rows + r, dh) + d0) = v;
+    *reinterpret_cast<uint2*>(P.out + row_offset(P, b, h, r, dh) + d0) = v;
 }
 
 template <bool F8, int DH, int NT>
@@ -1676,7 +1675,7 @@ int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     if (cudaLaunchKernelEx(&cfg, kernel, maps, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
     // A row's warps, by how many pieces a unit has.
-    const int units = P.batch * P.hkv * P.groups;
+    const int units = P.batch * P.hkv;
     const int wpr = P.G >= 16 * units ? 16 : P.G >= 4 * units ? 4 : 2;
     void (*const merge)(Params, int, int) =
         wpr == 16 ? merge_kernel<16> : wpr == 4 ? merge_kernel<4> : merge_kernel<2>;
@@ -1687,7 +1686,7 @@ int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, merge, P, 8 * NT, DH) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
-// Packed rows of a unit: all of a KV head's.
+// Packed rows of a unit: all of a KV head's, by eights.
 int unit_rows(int nq) { return nq <= 32 ? (nq + 7) / 8 * 8 : 48; }
 
 template <bool F8, int DH>
@@ -1731,16 +1730,15 @@ int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, co
     const int rows = unit_rows(P.nq);
     const int tile = Dh == 256 ? tile_keys<F8, 256>(rows / 8) : tile_keys<F8, 128>(rows / 8);
     P.ltile = __builtin_ctz((unsigned)tile);
-    P.groups = (P.nq + rows - 1) / rows;
     // A window that holds every context hides nothing.
     P.window = window >= max_ctx_len ? 0 : window;
     P.sinks = P.window > 0 ? sinks : 0;
     P.scale = scale;
     // No more ranges than tiles.
-    const long long tiles = (long long)batch * Hkv * P.groups * ((max_ctx_len - 1) / tile + 1);
+    const long long tiles = (long long)batch * Hkv * ((max_ctx_len - 1) / tile + 1);
     if (tiles > 0x1fffffffLL) return GQA_ERR_UNSUPPORTED;   // (with their LEADs below 2^31)
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
-    P.by_unit = (long long)batch * Hkv * P.groups < P.G;
+    P.by_unit = (long long)batch * Hkv < P.G;
     P.out = static_cast<__half*>(out);
     P.err = di->err_word;
     void* ws;

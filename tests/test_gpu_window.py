@@ -105,12 +105,10 @@ TAILS = [
 ]
 
 
-@pytest.mark.parametrize("fp4", [True, False])
-@pytest.mark.parametrize("case", TAILS)
+# (The E4M3 tails without a window are another entry point.)
+@pytest.mark.parametrize("case,fp4", [(c, f) for c in TAILS for f in (True, False) if f or c[6]])
 def test_tails(cuda_lib, case, fp4):
     R, Hq, Hkv, D, page, lens, window, sinks = case
-    if not fp4 and window == 0:
-        pytest.skip("the E4M3 tails without a window are another entry point")
     t = Tails(fp4, R, Hq, Hkv, D, page, lens, seed=R * 100 + len(lens) + window)
     scale = D ** -0.5
     args = t.args()
@@ -130,6 +128,28 @@ def test_many_sequences(cuda_lib, fp4):
     out = t.run(cuda_lib, 200, 3, 0.09)
     assert cuda_lib.device_error() == 0
     t.check(out, 200, 3, 0.09)
+
+
+@pytest.mark.parametrize("fp4", [True, False])
+@pytest.mark.parametrize("R,Hq,Hkv,D", [(2, 16, 2, 128), (3, 6, 1, 256), (4, 6, 1, 256)])
+def test_wide_rows_of_many_sequences(cuda_lib, fp4, R, Hq, Hkv, D):
+    """Two to four eights of packed rows, more sequences than a warp's lanes, cut anywhere."""
+    rnd = random.Random(R)
+    lens = [rnd.choice([0, 1, 2, 700, rnd.randint(1, 1500)]) for _ in range(70)]
+    t = Tails(fp4, R, Hq, Hkv, D, 16, lens, seed=R)
+    out = t.run(cuda_lib, 900, 5, 0.07)
+    assert cuda_lib.device_error() == 0
+    t.check(out, 900, 5, 0.07, only=range(0, 70, 3))
+
+
+@pytest.mark.parametrize("fp4", [True, False])
+def test_one_long_sequence_among_many(cuda_lib, fp4):
+    """Its unit is cut into almost all ranges, while most are whole: more pieces than the
+    join takes at a time."""
+    t = Tails(fp4, 1, 2, 1, 128, 16, [3] * 40 + [30000] + [3] * 39, seed=4)
+    out = t.run(cuda_lib, 29000, 2, 0.09)
+    assert cuda_lib.device_error() == 0
+    t.check(out, 29000, 2, 0.09)
 
 
 def test_most_sequences(cuda_lib):
@@ -435,4 +455,32 @@ def test_a_model_step_over_the_4_bit_cache(cuda_lib):
                                      scale=D ** -0.5, window=window, sinks=sinks)[0]
             for h, want, bound in plain(qd, n + i + 1, window or 0, sinks):
                 assert (np.abs(out[:, h].cpu().double().numpy() - want) <= bound).all()
+    assert cuda_lib.device_error() == 0
+
+
+@pytest.mark.parametrize("Hkv,D", [(1, 256), (3, 128)])
+def test_a_cache_beyond_32_bits(cuda_lib, Hkv, D):
+    """Pages on both sides of 2^32 bytes: written, read back and attended as in a small
+    cache."""
+    dev = torch.device("cuda")
+    g = torch.Generator().manual_seed(31)
+    page, n = 16, 120
+    a_page = Hkv * page * 9 * D // 16
+    pages = 2 ** 32 // a_page + 9
+    big = [torch.zeros(pages, Hkv, page, 9 * D // 16, dtype=torch.uint8, device=dev) for _ in "kv"]
+    small = [torch.zeros(8, Hkv, page, 9 * D // 16, dtype=torch.uint8, device=dev) for _ in "kv"]
+    k, v = (torch.randn(n, Hkv, D, generator=g).half().to(dev) for _ in "kv")
+    q = torch.randn(1, 2, 2 * Hkv, D, generator=g).half().to(dev)
+    s = torch.tensor([0.02], device=dev)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    got = []
+    for (kc, vc), ids in ((big, [pages - 1, 0, pages - 3, 1, pages - 2, 2 ** 32 // a_page, 5,
+                                2 ** 31 // a_page]),
+                          (small, range(8))):
+        table = torch.tensor([list(ids)], dtype=torch.int32, device=dev)
+        cuda_lib.cache_write_fp4(None, k, v, kc, vc, s, s, table, lens, n)
+        got.append(list(cuda_lib.cache_read_fp4(kc, vc, s, s, table, lens, n, n)) +
+                   [cuda_lib.paged_fp4(q, kc, vc, s, s, table, lens, n, window=w, sinks=3)
+                    for w in (None, 70)])
+    assert got[0][0].any() and all(torch.equal(a, b) for a, b in zip(*got))
     assert cuda_lib.device_error() == 0
