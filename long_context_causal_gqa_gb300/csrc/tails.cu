@@ -675,11 +675,11 @@ struct Config {
     static constexpr int SLICES = DH / 64, SHARES = GW / SLICES;
     static constexpr int SOURCES = NG * SHARES;    // warps that sum the same places
     static constexpr int P_ROW = TILE * 2 + 16;    // P^T: rows of a tile's keys, padded
-    static constexpr int P_BYTES = NG * ROWS * P_ROW;
+    static constexpr int P_BYTES = 2 * NG * ROWS * P_ROW;   // (of two tiles: see below)
     static constexpr int JOIN_ROW = DH / 4 + 4;    // floats of a row in one round of the join
 
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_P = OFF_Q + ROWS * W::Q_ROW;   // [NG][ROWS]
+    static constexpr int OFF_P = OFF_Q + ROWS * W::Q_ROW;   // [NG][2][ROWS]
     static constexpr int OFF_JOIN = OFF_P;                  // [SOURCES][ROWS], when P is done with
     static constexpr int JOIN_BYTES = SOURCES * ROWS * JOIN_ROW * 4;
     static constexpr int OFF_MAX = OFF_P + (P_BYTES > JOIN_BYTES ? P_BYTES : JOIN_BYTES);   // [NW][ROWS]
@@ -747,7 +747,6 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
         const int gid = lane >> 2, t = lane & 3;
         const int slice = gwarp % C::SLICES, share = gwarp / C::SLICES;
         uint8_t* const sq = smem + C::OFF_Q;
-        uint8_t* const pt = smem + C::OFF_P + group * ROWS * C::P_ROW;
         float* const smax = reinterpret_cast<float*>(smem + C::OFF_MAX);   // [NW][ROWS]
         float* const sref = reinterpret_cast<float*>(smem + C::OFF_REF);   // [NG][ROWS]
         float* const join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
@@ -803,6 +802,10 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                 const uint32_t full = bars + at.bar();
                 wait(full, at.phase, abort_flag, P.err);
                 __syncwarp();
+                // P of this tile and the last one lie side by side: a warp that is ahead writes
+                // beside what others still read, and one barrier a tile is enough.
+                uint8_t* const pt =
+                    smem + C::OFF_P + (group * 2 + (mine & 1)) * ROWS * C::P_ROW;
                 const int key0 = tile_key(P, s, j);
                 const bool edge = has_edge(P, s, key0, TILE);
                 const uint8_t* kst = smem + C::OFF_RING + at.stage * C::STAGE;
@@ -892,7 +895,6 @@ split_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
                     }
                 };
                 float ls[NT][2];
-                meet_group();   // the last tile's P has been read
                 put_p(ls);
                 meet_group();
                 if (flag[mine & 1] == (int)mine + 1) {
