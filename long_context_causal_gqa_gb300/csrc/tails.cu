@@ -35,7 +35,7 @@
 // Replays behind one another, with the bytes that have to be read at the copy rate and a
 // plain reading kernel's time where it was measured: one row over 261888 4-bit tokens
 // 23.7 us (11.3; 18.1 by one call of the reading kernel against 26.8), 64 ragged contexts
-// of up to 8192 47 us (26.5; 34 against 54), eight rows over 128000 31 us (5.6), sixteen
+// of up to 8192 47 us (26.5; 34 against 54), eight rows over 128000 30.9 us (5.6), sixteen
 // windows of 2000 12.2 us (1.3), 48 E4M3 windows of 8192 44 us (29; 38.5 against 49).
 // Small calls are chains of latencies: lengths, table, first page, then the join's
 // record and partials (a window of 4096: 7.8 us, 7.2 of it without any product).  One
