@@ -35,12 +35,11 @@
 // Replays behind one another, with the bytes that have to be read at the copy rate and a
 // plain reading kernel's time where it was measured: one row over 261888 4-bit tokens
 // 23.7 us (11.3; 18.1 by one call of the reading kernel against 26.8), 64 ragged contexts
-// of up to 8192 47 us (26.5; 34 against 54), eight rows over 128000 30.9 us (5.6), sixteen
+// of up to 8192 47 us (26.5; 34 against 52), eight rows over 128000 30.9 us (5.6), sixteen
 // windows of 2000 12.2 us (1.3), 48 E4M3 windows of 8192 44 us (29; 38.5 against 49).
 // Small calls are chains of latencies: lengths, table, first page, then the join's
-// record and partials (a window of 4096: 7.8 us, 7.2 of it without any product).  One
-// context's 64 x 1 tails are bound by decoding (49 us without the copies, 36 without the
-// products), windows of E4M3 rows by the copies (40 us without the products), eight
+// record and partials (a window of 4096: 7.8 us, 7.2 of it without any product).  The 64
+// contexts are bound by decoding (49 us without the copies, 36 without the products), windows of E4M3 rows by the copies (40 us without the products), eight
 // packed tails by the products (m16n8k16 takes 8.75 cycles of a quarter of an SM: under a
 // third of tcgen05's rate).
 #include <cuda_fp16.h>

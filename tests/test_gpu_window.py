@@ -484,3 +484,50 @@ def test_a_cache_beyond_32_bits(cuda_lib, Hkv, D):
                     for w in (None, 70)])
     assert got[0][0].any() and all(torch.equal(a, b) for a, b in zip(*got))
     assert cuda_lib.device_error() == 0
+
+
+def test_calls_that_overlap_their_launches(cuda_lib):
+    """Each call's launch overlaps the kernel in front, whose output it takes: a chain of all
+    operators gives the same bits with a wait after every call and without any."""
+    dev = torch.device("cuda")
+    g = torch.Generator().manual_seed(41)
+    n, page, D, Hq, Hkv, R = 1200, 16, 256, 6, 1, 2
+    pages = n // page
+    kv = torch.randn(n, 2 * Hkv, D, generator=g).half().to(dev)
+    k, v = kv[:, :Hkv].contiguous(), kv[:, Hkv:].contiguous()
+    s = torch.tensor([0.02], device=dev)
+    table = torch.randperm(pages, generator=g).int().to(dev).view(1, -1)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    first = torch.randn(R, Hq, D, generator=g).half().to(dev)
+
+    def chain(after):
+        caches = [torch.zeros(pages, Hkv, page, 9 * D // 16, dtype=torch.uint8, device=dev)
+                  for _ in "kv"]
+        codes = [torch.zeros(pages, page, Hkv, D, dtype=torch.uint8, device=dev) for _ in "kv"]
+        cuda_lib.cache_write_fp4(None, k, v, *caches, s, s, table, lens, n)
+        cuda_lib.cache_write_e4m3(None, k, v, *codes, s, s, table, lens, n)
+        x, seen = first, []
+        for i in range(12):
+            # The rows so far become queries and the last rows' keys of the next call.
+            x = cuda_lib.cache_write_fp4(x, x[:, :1], x[:, 1:2], *caches, s, s, table, lens, n)
+            after()
+            x = cuda_lib.paged_fp4(x[None], *caches, s, s, table, lens, n, window=[None, 300][i % 2],
+                                   sinks=i)[0]
+            after()
+            x = cuda_lib.paged_e4m3_window(x[None], *codes, s, s, table, lens, n, 500, sinks=3)[0]
+            after()
+            kd, vd = cuda_lib.cache_read_fp4(*caches, s, s, table, lens, n, n)
+            after()
+            x = cuda_lib.prefill_window(x, kd, vd, 400, sinks=i)
+            after()
+            x = cuda_lib.paged_e4m3(x, *codes, s, s, table[0], n)
+            after()
+            x = cuda_lib.prefill_window(x, kd, vd, 100) * 4
+            seen.append(x)
+        return torch.stack(seen)
+
+    want = chain(torch.cuda.synchronize)
+    assert torch.isfinite(want).all() and want.any()
+    for _ in range(5):
+        assert torch.equal(chain(lambda: None), want)
+    assert cuda_lib.device_error() == 0
