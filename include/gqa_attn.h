@@ -196,10 +196,11 @@ int gqa_attn_paged_e4m3_batch(const void* q, const uint8_t* kcache, const uint8_
  * gqa_attn_paged_e4m3_batch, any batch from 1 on, except: a context length may be
  * anything from 0 to max_ctx_len (others are clamped and flag
  * GQA_DEVERR_BAD_CTX_LEN), and a row that sees no key (a context shorter than
- * query_rows, or of no tokens) gets zeros.  Only tiles that some row sees are read
- * (table entries of other pages need not be valid), and keys that no row of a sequence
- * sees may hold any byte; one that a row sees must not be the E4M3 NaN code.  Limits,
- * precision, division of the work and workspace as for gqa_attn_paged_fp4. */
+ * query_rows, or of no tokens) gets zeros.  Block-table entries of pages that no row
+ * sees are not read, so pages may be given back as they leave the window.  Keys that no
+ * row of a sequence sees may hold any byte; one that a row sees must not be the E4M3 NaN
+ * code.  Limits, precision, division of the work and workspace as for
+ * gqa_attn_paged_fp4. */
 int gqa_attn_paged_e4m3_window(const void* q, const uint8_t* kcache, const uint8_t* vcache,
                                const float* kscale, const float* vscale,
                                const int32_t* block_tables, int table_stride, int num_pages,

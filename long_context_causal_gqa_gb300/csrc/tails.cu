@@ -539,14 +539,20 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
     uint32_t room = STAGES;     // stages that held none yet
     bool ok = true;
     while (ok && it.next(P, seqs, begin)) {
-        const int pages = (it.s.ctx + P.page - 1) >> P.log2_page;
         const int32_t* table = P.tables + (long long)it.b * P.table_stride;
+        // A copy's rows from `key` on hold a key that some row sees.  A tile that the
+        // sinks end in, or the window begins in, has pages without one, which may have been
+        // given back: their entries are not read, and their places in the stage keep what
+        // they held.  (The products' masks go by the key.)
+        auto seen = [&](int key) {
+            return key < it.s.ctx && (key < P.sinks || key + rows > it.s.lo);
+        };
         // Table entries 32 at a time, a lane each, three lots ahead of their use.
         auto entries = [&](int lot) {
             const int e = lot * 32 + lane, j = it.jb + (e >> lppt);
             if (j >= it.je) return 0;
-            const int lp = (tile_key(P, it.s, j) >> P.log2_page) + (e & (ppt - 1));
-            return lp < pages ? __ldg(table + lp) : 0;
+            const int key = tile_key(P, it.s, j) + (e & (ppt - 1)) * rows;
+            return seen(key) ? __ldg(table + (key >> P.log2_page)) : 0;
         };
         int lot = 0, now = entries(0), next = entries(1), after = entries(2);
 #pragma unroll 1
@@ -561,7 +567,7 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
             // All that can be known before a stage is free.
             int id = __shfl_sync(0xffffffffu, now, (e & 31) + (p & (ppt - 1)));
             const int key0 = tile_key(P, it.s, j), in_page = key0 & (P.page - 1);
-            const bool mine = p < min(ppt, pages - (key0 >> P.log2_page));
+            const bool mine = p < ppt && seen(key0 + p * rows);
             if (mine && (id < 0 || id >= P.num_pages)) {
                 atomicOr(P.err, kErrBadPageId);
                 id = 0;
