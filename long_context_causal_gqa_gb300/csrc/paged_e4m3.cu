@@ -358,12 +358,14 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int n_logical = (ctx_len + page - 1) >> lpage;
     // The producer's first two chunks of block-table entries (one per lane),
     // requested before the barrier set-up so that their DRAM latency overlaps it.
+    // (Ordinary loads: the kernel in front may write them while this one is resident
+    // already, so they are not read-only for its lifetime.)
     const int pg_begin = (t_begin * TILE) >> lpage;
     const int pg_end = ntl > 0 ? min(((t_end * TILE - 1) >> lpage) + 1, n_logical) : 0;
     const int32_t* table = P.table + (size_t)seq * P.table_stride;
     auto load_chunk = [&](int k) -> int {
         const int pg = pg_begin + 32 * k + lane;
-        return pg < pg_end ? __ldg(table + pg) : 0;
+        return pg < pg_end ? table[pg] : 0;
     };
     int cur = 0, nxt = 0;
     if (warp == 0) {

@@ -692,6 +692,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tile0 = wt.key(j, P.base);
                     if (j < wt.sink && P.base > 0) limit = P.sinks;
                 }
+                // (Ordinary loads, as the scales': with WIN the kernel in front may write them
+                // while this one is resident already.)
                 uint4 code[SLOTS][PASSES];
 #pragma unroll
                 for (int h = 0; h < SLOTS; ++h) {
@@ -703,8 +705,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int i = 0; i < PASSES; ++i) {
                         const int key = key0 + rbase + i * rpi;
                         code[h][i] = key < limit
-                                         ? __ldg(reinterpret_cast<const uint4*>(
-                                               codes + (size_t)key * P.kv_rs + kvh * DH + d0))
+                                         ? *reinterpret_cast<const uint4*>(
+                                               codes + (size_t)key * P.kv_rs + kvh * DH + d0)
                                          : make_uint4(0, 0, 0, 0);
                     }
                 }
@@ -911,8 +913,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t gbar = BR.group();
         uint32_t gphase = 0;
         // F8: the K scale joins the score scale; the V scale multiplies O.
-        const float sl2 = F8 ? P.scale_log2 * __ldg(P.kscale) : P.scale_log2;
-        const float vsc = F8 ? __ldg(P.vscale) : 1.0f;
+        const float sl2 = F8 ? P.scale_log2 * *P.kscale : P.scale_log2;
+        const float vsc = F8 ? *P.vscale : 1.0f;
         uint32_t g = 0;
         bool ok = true;
         while (ok && it.next(P, pt, hd, jb, je, n, is_first)) {

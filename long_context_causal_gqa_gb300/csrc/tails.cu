@@ -547,12 +547,14 @@ __device__ __forceinline__ void copy_tiles(const Params& P, const Maps<F8>& maps
         auto seen = [&](int key) {
             return key < it.s.ctx && (key < P.sinks || key + rows > it.s.lo);
         };
-        // Table entries 32 at a time, a lane each, three lots ahead of their use.
+        // Table entries 32 at a time, a lane each, three lots ahead of their use.  (Ordinary
+        // loads: the kernel in front may write them while this one is resident already, so
+        // they are not read-only for its lifetime.)
         auto entries = [&](int lot) {
             const int e = lot * 32 + lane, j = it.jb + (e >> lppt);
             if (j >= it.je) return 0;
             const int key = tile_key(P, it.s, j) + (e & (ppt - 1)) * rows;
-            return seen(key) ? __ldg(table + (key >> P.log2_page)) : 0;
+            return seen(key) ? table[key >> P.log2_page] : 0;
         };
         int lot = 0, now = entries(0), next = entries(1), after = entries(2);
 #pragma unroll 1
