@@ -587,8 +587,9 @@ int gqa_select_blocks(const void* q, const int8_t* index, const float* index_sca
 }
 
 size_t gqa_workspace_bytes(int kind, int query_rows, int ctx_or_kv, int Hq, int D) {
-    if ((D != kHeadDim && D != 128) || query_rows < 1 || ctx_or_kv < 1) return 0;
+    if ((D != kHeadDim && D != 128) || query_rows < 1) return 0;
     if (Hq < 1 || Hq > kMaxHeads) return 0;
+    if (kind != GQA_KIND_TAILS && ctx_or_kv < 1) return 0;   // (unused by the tails)
     const DeviceInfo* di = device_info();
     if (!di) return 0;
     // The tail's partials are sized for query_rows x Hq packed rows, enough
