@@ -314,6 +314,7 @@ int batch_check(const void* q, const void* kcache, const void* vcache, const flo
     if ((long long)max_ctx_len > (long long)num_pages * page ||
         (long long)max_ctx_len > (long long)table_stride * page)
         return GQA_ERR_INVALID_ARG;
+    if ((long long)batch * Hkv * max_ctx_len >= kMaxTailKeys) return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
 }
 

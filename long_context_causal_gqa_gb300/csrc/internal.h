@@ -27,6 +27,9 @@ inline bool page_ok(int page) { return page >= 8 && page <= 256 && (page & (page
 // Most sequences one batched tail launch takes (its merge reads at most 1024
 // split partials per packed row).
 constexpr int kMaxTailBatch = 1024;
+// batch x KV heads x max_ctx_len of the 4-bit and the windowed tails stays below this:
+// their tiles are counted in 32 bits.
+constexpr long long kMaxTailKeys = 1LL << 35;
 
 struct DeviceInfo {
     int device;

@@ -108,7 +108,8 @@ __device__ __forceinline__ Span span_of(const Params& P, int raw) {
 
 // Where each sequence's tiles begin among all.  Up to 32 sequences: lane i of every
 // warp holds sequence i, nothing is shared.  More: in shared memory.  (All tiles of all
-// units and their LEADs are fewer than 2^31: the host sees to it.)
+// units and their LEADs are fewer than 2^30: kMaxTailKeys / 64, and three for each of the
+// at most 2^16 units.)
 //
 // Ranges are equal in tiles and what a piece costs besides: LEAD tiles' time in front of
 // each unit's.  (Sixteen windows of 17 tiles: 16.4 us without, 12.2 with one or two, 13.1
@@ -1745,7 +1746,6 @@ int launch_tails(const void* q, const uint8_t* kcache, const uint8_t* vcache, co
     P.scale = scale;
     // No more ranges than tiles.
     const long long tiles = (long long)batch * Hkv * ((max_ctx_len - 1) / tile + 1);
-    if (tiles > 0x1fffffffLL) return GQA_ERR_UNSUPPORTED;   // (with their LEADs below 2^31)
     P.G = (int)(tiles < di->num_sms ? tiles : di->num_sms);
     P.by_unit = (long long)batch * Hkv < P.G;
     P.out = static_cast<__half*>(out);
