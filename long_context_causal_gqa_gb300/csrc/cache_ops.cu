@@ -441,7 +441,7 @@ struct ReadParams {
     const uint8_t* cache[2];   // K, V
     const float* scale[2];     // E4M3 dequantisation scales (null: rows as they are)
     uint8_t* out[2];
-    int row_bytes;             // cached bytes of one token of K (or V)
+    int row_bytes;             // cached bytes of one token of K (or V); unused by read_fp4_kernel
     FastDiv chunks;            // pieces of one token's K (or V)
     int tile;                  // tokens per CTA
 };
@@ -862,7 +862,6 @@ int cache_read_fp4_launch(const CacheRows& r, const void* kcache, const void* vc
     P.scale[1] = vscale;
     P.out[0] = static_cast<uint8_t*>(k_out);
     P.out[1] = static_cast<uint8_t*>(v_out);
-    P.row_bytes = fp4::row_bytes(D);
     P.chunks = make_fastdiv(Hkv * D / 16);
     P.tile = r.tokens <= 2048 ? 8 : 32;
     const int grid = (r.tokens - 1) / P.tile + 1;

@@ -919,7 +919,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool ok = true;
         while (ok && it.next(P, pt, hd, jb, je, n, is_first)) {
             const int m_row = pt * BM2 + BM * (int)rank + row;
-            const bool valid = m_row < P.M_total;
             const int lim = P.KV - P.Q + P.grp.div(m_row);      // last visible key
             const int first_lim = P.KV - P.Q + P.grp.div(pt * BM2 + BM * (int)rank);
             const int j_mask = (first_lim + 1) / BN;

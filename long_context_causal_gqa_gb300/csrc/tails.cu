@@ -1689,8 +1689,8 @@ int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     const int wpr = P.G >= 16 * units ? 16 : P.G >= 4 * units ? 4 : 2;
     void (*const merge)(Params, int, int) =
         wpr == 16 ? merge_kernel<16> : wpr == 4 ? merge_kernel<4> : merge_kernel<2>;
-    const int rows = P.nq < 8 * NT ? P.nq : 8 * NT, a_block = MERGE_WARPS / wpr;
-    cfg.gridDim = dim3(P.by_unit ? units : P.G, (rows + a_block - 1) / a_block, DH / 128);
+    const int a_block = MERGE_WARPS / wpr;
+    cfg.gridDim = dim3(P.by_unit ? units : P.G, (P.nq + a_block - 1) / a_block, DH / 128);
     cfg.blockDim = dim3(MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, merge, P, 8 * NT, DH) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
