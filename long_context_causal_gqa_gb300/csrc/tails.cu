@@ -15,17 +15,18 @@
 //   61 for 48 windows of 8192 tokens, two heads of 128.)  A unit that lies in one range is
 //   finished there; a unit that is cut leaves (O, m, l) partials, at most two for a CTA,
 //   which a second kernel joins in range order.
-// * Copies.  Four warps bring the pages of a tile into a ring of stages (192 KB: the bytes
-//   in flight set the copy rate), 4-bit pages by bulk copies (a page of one head is one
-//   contiguous run), E4M3 rows by tensor maps, table entries lots ahead.
+// * Copies.  Four warps bring the pages of a tile that some row sees into a ring of stages
+//   (up to 192 KB: the bytes in flight set the copy rate), 4-bit pages by bulk copies (a
+//   page of one head is one contiguous run), E4M3 rows by tensor maps, table entries lots
+//   ahead.
 // * Products.  Two groups of four warps take a tile each.  A warp decodes its codes from
 //   shared memory straight into the fragments of m16n8k16 products, keys (for K) or
 //   places of D (for V) along M, packed query rows along N, so eight rows waste nothing.
 //   The order of the places within a product is free, so a lane loads whole words of one
 //   key: K's pairs are a byte's two nibbles, V's pairs are put together from two keys'.
-//   Nothing decoded goes through shared memory, which operands of tcgen05.mma would
-//   have to (four times the codes' bytes, written and read: more than shared memory can
-//   move while the codes arrive).
+//   Nothing decoded goes through shared memory.  (For tcgen05.mma V would have to, or be
+//   turned: its places of D would lie along M, and codes arrive by key.  Keys along M could
+//   be decoded into tensor memory, a key a lane, and the scores taken there; not built.)
 // * Softmax.  A reference of a row moves only when a score passes it by more than 8 (log2
 //   units), so P <= 256 in fp16.  More than eight packed rows: P goes through shared
 //   memory to the warps that hold the sums, computed with the group's reference as it
@@ -34,14 +35,17 @@
 //
 // Replays behind one another, with the bytes that have to be read at the copy rate and a
 // plain reading kernel's time where it was measured: one row over 261888 4-bit tokens
-// 23.7 us (11.3; 18.1 by one call of the reading kernel against 26.8), 64 ragged contexts
-// of up to 8192 47 us (26.5; 34 against 52), eight rows over 128000 30.9 us (5.6), sixteen
-// windows of 2000 12.2 us (1.3), 48 E4M3 windows of 8192 44 us (29; 38.5 against 49).
+// 24.1 us (11.3; 18.1 by one call of the reading kernel against 26.8), 64 ragged contexts
+// of up to 8192 46.4 us (26.5; 34 against 52), eight rows over 128000 30.8 us (5.6), sixteen
+// windows of 2000 11.9 us (1.3), 48 E4M3 windows of 8192 43.6 us (29; 38.5 against 49).
 // Small calls are chains of latencies: lengths, table, first page, then the join's
-// record and partials (a window of 4096: 7.8 us, 7.2 of it without any product).  The 64
-// contexts are bound by decoding (49 us without the copies, 36 without the products), windows of E4M3 rows by the copies (40 us without the products), eight
-// packed tails by the products (m16n8k16 takes 8.75 cycles of a quarter of an SM: under a
-// third of tcgen05's rate).
+// record and partials (a window of 4096: 7.5 us, 7.2 of it without any product).  The 64
+// contexts are bound by decoding (49 us without the copies, 36 without the products),
+// windows of E4M3 rows by the copies (40 us without the products), eight packed tails by
+// the products (m16n8k16 takes 8.75 cycles of a quarter of an SM: under a third of
+// tcgen05's rate): eight rows of six heads over 261888 tokens take 48.4 us in 4 bits and
+// 50.4 in E4M3 with a window of all but one, where paged_e4m3.cu's tcgen05 kernel takes
+// 38.1 without a window.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -365,8 +369,14 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t a, uint32_t b) {
 // A tile's keys: 128 (E4M3 rows of 256: 64, stages of 32 KB); from four eights of packed
 // rows on 64, whose scores take half the registers.  (4-bit, heads of 256, 128 and 64
 // keys: eight rows of six heads over 128000 37.8 us and 31.2, five rows over 200000 34.0
-// and 31.9, four rows 28.3 and 28.6, sixteen windows of two 12.3 and 12.9; heads of 128,
-// sixteen contexts of four rows of four heads 34 and 39.)
+// and 31.9, four rows 28.3 and 28.6, sixteen windows of two 12.3 and 12.9.  Heads of 128,
+// two eights: sixteen contexts of four rows of four heads 34 and 39.  Heads of 128 from four
+// eights on, where neither is the better one for all: 32 packed rows, 4-bit, sixteen
+// windows of 2000 13.6 and 11.9, one context of 128000 18.0 and 18.6, of 261888 26.4 and
+// 28.7, sixteen contexts of 8000 18.2 and 19.4; E4M3, a window of 100000 17.2 and 17.0,
+// sixteen of 4096 13.9 and 15.4; 48 packed rows, 4-bit, sixteen windows of 2000 18.8 and
+// 15.0, one context of 128000 23.9 and 22.1, sixteen of 8000 25.2 and 24.2; E4M3, a window of
+// 100000 23.3 and 21.8, sixteen of 4096 19.5 and 21.9.)
 template <bool F8, int DH>
 __host__ __device__ constexpr int tile_keys(int nt) {
     return (F8 && DH == 256) || nt >= 4 ? 64 : 128;
@@ -1178,7 +1188,7 @@ struct Narrow {
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(32 * NW * REGS_PRODUCTS + 128 * REGS_COPIES <= THREADS * REGS_LAUNCH, "registers");
     static constexpr int STAGE = 2 * W::TILE_BYTES;
-    static constexpr int STAGES = 196608 / STAGE;    // 184 or 192 KB
+    static constexpr int STAGES = 196608 / STAGE;    // 180 KB (4-bit) or 192 KB (E4M3)
     // One round of the join: eight places of every gid, of all warps.
     static constexpr int JOIN_ROW = 64 + 4;
     static constexpr int OFF_JOIN = 0;                                   // [NW][8][JOIN_ROW]
@@ -1563,7 +1573,10 @@ narrow_kernel(const __grid_constant__ Maps<F8> maps, const Params P) {
 // takes 128 places of D of 16 / WPR packed rows; a row's WPR warps share its pieces out
 // and their sums are added in order.  The whole calls with 16, 4 and 2 warps a row: one
 // unit in 152 pieces 23.7, 32.0 and 40.9 us; sixteen units in about ten each 15.5, 12.2
-// and 12.6; 96 units in two or three 60.4, 45.5 and 44.4.
+// and 12.6; 96 units in two or three 60.4, 45.5 and 44.4.  The choice goes by the batch, for
+// the lengths are known on the device alone: among 63 sequences of no tokens one of 128000
+// is joined by two warps a row (one 4-bit row 29.5 us, 18.0 alone; eight rows 47.3 and
+// 31.4).
 constexpr int MERGE_WARPS = 16;
 
 template <int WPR>
@@ -1684,7 +1697,7 @@ int launch(const Maps<F8>& maps, const Params& P, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, maps, P) != cudaSuccess) return GQA_ERR_CUDA;
     if (P.G == 1) return GQA_OK;   // nothing is cut
-    // A row's warps, by how many pieces a unit has.
+    // A row's warps, by how many pieces a unit has if all are of one length.
     const int units = P.batch * P.hkv;
     const int wpr = P.G >= 16 * units ? 16 : P.G >= 4 * units ? 4 : 2;
     void (*const merge)(Params, int, int) =
